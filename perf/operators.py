@@ -198,7 +198,7 @@ def prepare(case, seed):
         if case["bits"] == 8:
             s["m"].zero_()
             s["v"].zero_()
-            s["values"] = [(s["m"][a:a + k], s["v"][a:a + k]) for a, k in zip(starts, sizes)]
+            s["values"] = optim.StateValues(s["opt"], [(s["m"][a:a + k], s["v"][a:a + k]) for a, k in zip(starts, sizes)])
     return s
 
 
@@ -361,7 +361,7 @@ def run(state):
     if op == "adamw":
         s["opt"].step(grad_scale=s["scale"])
         if s["case"]["bits"] == 8:  # the states as the numbers they stand for
-            s["opt"].state_values(s["values"])
+            s["values"]()
         return _adamw_outputs(s)
     from deformable_convolution_gb300 import binding as B
     if op == "fwd":

@@ -26,7 +26,13 @@ EXPORTED_SYMBOLS = (
     "dc_kernel_times", "deform_conv_offsets", "deform_conv_margin_histogram", "dc_suggest_margin",
     "deform_conv_bwd_after_fwd", "deform_conv_fwd_sampled_gemm", "dc_relu_fwd", "dc_relu_bwd",
     "dc_col_layout", "dc_sample_tile", "dc_selftest_wait_timeout", "dc_test_fail_launches",
+    "dc_group_norm_workspace_size", "dc_group_norm_fwd", "dc_group_norm_bwd",
+    "dc_adamw_step", "dc_adamw_state_values", "dc_grad_norm_workspace_size", "dc_grad_norm",
 )
+DC_NCHW, DC_NHWC = 0, 1
+DC_ACT_NONE, DC_ACT_RELU, DC_ACT_SILU, DC_ACT_GELU = range(4)
+DC_STATE_F32, DC_STATE_Q8 = 0, 1
+STATE_BLOCK = 256  # elements of an 8-bit state that share a scale
 DC_COL_PLANE_MAJOR, DC_COL_PIXEL_MAJOR = 0, 1
 MARGIN_BINS = 64
 NOALLOC_SCRATCH_BYTES = 32 << 20
@@ -38,6 +44,27 @@ class DcProblem(ctypes.Structure):
         "n", "c_in", "h", "w", "c_out", "kh", "kw", "stride_h", "stride_w",
         "pad_h", "pad_w", "dil_h", "dil_w", "offset_groups", "dtype", "halo_margin", "out_relu",
         "in_relu")]
+
+
+class DcNormProblem(ctypes.Structure):
+    """Mirror of ``dc_norm_problem``."""
+    _fields_ = [(name, ctypes.c_int) for name in (
+        "n", "c", "h", "w", "groups", "dtype", "layout", "act")] + \
+        [("eps", ctypes.c_float), ("grad_dtype", ctypes.c_int)]
+
+
+class DcAdamwTensor(ctypes.Structure):
+    """Mirror of ``dc_adamw_tensor``."""
+    _fields_ = [(name, ctypes.c_void_p) for name in (
+        "param", "master", "grad", "m", "v", "m_scale", "v_scale")] + \
+        [("count", ctypes.c_longlong), ("param_dtype", ctypes.c_int),
+         ("grad_dtype", ctypes.c_int), ("state", ctypes.c_int), ("weight_decay", ctypes.c_float)]
+
+
+class DcAdamwHyper(ctypes.Structure):
+    """Mirror of ``dc_adamw_hyper``."""
+    _fields_ = [(name, ctypes.c_double) for name in ("lr", "beta1", "beta2", "eps")] + \
+        [("step", ctypes.c_longlong)]
 
 
 class DcError(RuntimeError):
@@ -101,6 +128,22 @@ def lib() -> ctypes.CDLL:
         L.dc_relu_fwd.restype = i
         L.dc_relu_bwd.argtypes = [vp, vp, vp, sz, i, vp]
         L.dc_relu_bwd.restype = i
+        pn, pt = ctypes.POINTER(DcNormProblem), ctypes.POINTER(DcAdamwTensor)
+        ph, pv = ctypes.POINTER(DcAdamwHyper), ctypes.POINTER(vp)
+        L.dc_group_norm_workspace_size.argtypes = [pn, i, ctypes.POINTER(sz)]
+        L.dc_group_norm_workspace_size.restype = i
+        L.dc_group_norm_fwd.argtypes = [pn, vp, vp, vp, vp, vp, vp, vp, sz, vp]
+        L.dc_group_norm_fwd.restype = i
+        L.dc_group_norm_bwd.argtypes = [pn, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, sz, vp]
+        L.dc_group_norm_bwd.restype = i
+        L.dc_adamw_step.argtypes = [pt, i, ph, vp, vp, vp]
+        L.dc_adamw_step.restype = i
+        L.dc_adamw_state_values.argtypes = [pt, i, pv, pv, vp]
+        L.dc_adamw_state_values.restype = i
+        L.dc_grad_norm_workspace_size.argtypes = [i, ctypes.POINTER(sz)]
+        L.dc_grad_norm_workspace_size.restype = i
+        L.dc_grad_norm.argtypes = [pt, i, ctypes.c_float, vp, vp, vp, sz, vp]
+        L.dc_grad_norm.restype = i
         L.dc_launch_count.argtypes = []
         L.dc_launch_count.restype = ctypes.c_ulonglong
         _configured = True
@@ -415,6 +458,175 @@ def dc_relu_bwd(act, grad_out, grad_in, stream=None):
                              _dc_dtype(act), _stream(stream)), "dc_relu_bwd")
 
 
+# ---------------------------------------------------------------- group norm
+
+@dataclass(frozen=True)
+class NormProblem:
+    """Group norm with an activation over [n, c, h, w] (DC_NCHW) or
+    [n, h, w, c] (DC_NHWC) tensors; a torch channels-last tensor ``t`` is
+    ``t.permute(0, 2, 3, 1)`` here.  grad_dtype: grad_y's type, DC_F32 (a
+    deformable layer's grad_x) or ``dtype``."""
+    n: int
+    c: int
+    h: int
+    w: int
+    groups: int
+    dtype: int = DC_F32
+    layout: int = DC_NCHW
+    act: int = DC_ACT_NONE
+    eps: float = 1e-5
+    grad_dtype: int = DC_F32
+
+    def c_struct(self) -> DcNormProblem:
+        return DcNormProblem(self.n, self.c, self.h, self.w, self.groups, self.dtype, self.layout,
+                             self.act, self.eps, self.grad_dtype)
+
+    @property
+    def torch_dtype(self):
+        return _TORCH_DTYPE[self.dtype]
+
+    @property
+    def shape(self):
+        """Of x, y, grad_y and grad_x."""
+        if self.layout == DC_NHWC:
+            return (self.n, self.h, self.w, self.c)
+        return (self.n, self.c, self.h, self.w)
+
+    @property
+    def stat_shape(self):
+        """Of mean and rstd."""
+        return (self.n, self.groups)
+
+
+def dc_group_norm_workspace_size(p: NormProblem, backward: bool) -> int:
+    out = ctypes.c_size_t(0)
+    st = p.c_struct()
+    _check(lib().dc_group_norm_workspace_size(ctypes.byref(st), 1 if backward else 0,
+                                              ctypes.byref(out)), "dc_group_norm_workspace_size")
+    return int(out.value)
+
+
+def _ws(ws):
+    """(pointer, bytes) of a workspace that may be None."""
+    if ws is None:
+        return None, 0
+    return _ptr(ws, "ws", dtype=torch.uint8), ws.numel()
+
+
+def dc_group_norm_fwd(p: NormProblem, x, gamma, beta, y, mean=None, rstd=None, ws=None,
+                      stream=None):
+    """y = act(group norm of x); mean and rstd [n, groups] for the backward.
+    gamma, beta: float32 [c] or None; y may be x."""
+    dt, f32, sh, ss = p.torch_dtype, torch.float32, p.shape, p.stat_shape
+    st = p.c_struct()
+    ws_ptr, ws_bytes = _ws(ws)
+    _check(lib().dc_group_norm_fwd(
+        ctypes.byref(st), _ptr(x, "x", sh, dt), _ptr(gamma, "gamma", (p.c,), f32, True),
+        _ptr(beta, "beta", (p.c,), f32, True), _ptr(y, "y", sh, dt),
+        _ptr(mean, "mean", ss, f32, True), _ptr(rstd, "rstd", ss, f32, True),
+        ws_ptr, ws_bytes, _stream(stream)), "dc_group_norm_fwd")
+
+
+def dc_group_norm_bwd(p: NormProblem, x, gamma, beta, mean, rstd, grad_y, grad_x,
+                      grad_gamma=None, grad_beta=None, ws=None, stream=None):
+    """grad_x (x's dtype; may be grad_y where the types agree), grad_gamma and
+    grad_beta (float32 [c] or None) from grad_y in ``p.grad_dtype``."""
+    dt, f32, sh, ss = p.torch_dtype, torch.float32, p.shape, p.stat_shape
+    st = p.c_struct()
+    ws_ptr, ws_bytes = _ws(ws)
+    _check(lib().dc_group_norm_bwd(
+        ctypes.byref(st), _ptr(x, "x", sh, dt), _ptr(gamma, "gamma", (p.c,), f32, True),
+        _ptr(beta, "beta", (p.c,), f32, True), _ptr(mean, "mean", ss, f32),
+        _ptr(rstd, "rstd", ss, f32), _ptr(grad_y, "grad_y", sh, _TORCH_DTYPE[p.grad_dtype]),
+        _ptr(grad_x, "grad_x", sh, dt), _ptr(grad_gamma, "grad_gamma", (p.c,), f32, True),
+        _ptr(grad_beta, "grad_beta", (p.c,), f32, True), ws_ptr, ws_bytes, _stream(stream)),
+        "dc_group_norm_bwd")
+
+
+# ---------------------------------------------------------------- AdamW
+
+def adamw_tensors(entries):
+    """A host array of ``dc_adamw_tensor`` from dicts of tensors: param, grad
+    (required for a step), m, v, and optionally master, m_scale, v_scale,
+    weight_decay.  8-bit states are an int8 m and a uint8 v.  The array holds
+    plain pointers: the caller keeps the tensors."""
+    out = (DcAdamwTensor * max(len(entries), 1))()
+    for t, q in zip(out, entries):
+        count = q["grad"].numel()
+        shape = tuple(q["grad"].shape)
+        t.count = count
+        t.grad = _addr(q["grad"], "grad", shape)
+        t.grad_dtype = _dc_dtype(q["grad"])
+        if q.get("param") is None:
+            continue
+        t.param, t.param_dtype = _addr(q["param"], "param", shape), _dc_dtype(q["param"])
+        t.master = _addr(q.get("master"), "master", shape, torch.float32)
+        eight = q["m"].dtype == torch.int8
+        t.state = DC_STATE_Q8 if eight else DC_STATE_F32
+        t.m = _addr(q["m"], "m", shape, torch.int8 if eight else torch.float32)
+        t.v = _addr(q["v"], "v", shape, torch.uint8 if eight else torch.float32)
+        if eight:
+            blocks = (-(-count // STATE_BLOCK),)
+            t.m_scale = _addr(q["m_scale"], "m_scale", blocks, torch.float32)
+            t.v_scale = _addr(q["v_scale"], "v_scale", blocks, torch.float32)
+        t.weight_decay = q.get("weight_decay", 0.0)
+    return out
+
+
+def _addr(t, name, shape=None, dtype=None):
+    p = _ptr(t, name, shape, dtype, True)
+    return None if p is None else p.value
+
+
+def dc_adamw_step(tensors, count: int, hyper: DcAdamwHyper, grad_scale=None, schedule=None,
+                  stream=None):
+    """One AdamW step over ``tensors`` (``adamw_tensors``).  grad_scale: a
+    float32 device scalar or None; schedule: float32 [3] {lr, 1 - beta1^step,
+    1 - beta2^step} on the device or None."""
+    if grad_scale is not None and grad_scale.numel() != 1:
+        raise ValueError("grad_scale must hold one value")
+    _check(lib().dc_adamw_step(
+        tensors, count, ctypes.byref(hyper), _ptr(grad_scale, "grad_scale", None, torch.float32, True),
+        _ptr(schedule, "schedule", (3,), torch.float32, True), _stream(stream)), "dc_adamw_step")
+
+
+def pointers(tensors, name, shapes, dtype):
+    """A host array of the tensors' device pointers (None: a null pointer),
+    each checked against its shape.  The caller keeps the tensors."""
+    a = (ctypes.c_void_p * max(len(tensors), 1))()
+    for k, (t, shape) in enumerate(zip(tensors, shapes)):
+        a[k] = _addr(t, f"{name}[{k}]", shape, dtype)
+    return a
+
+
+def dc_adamw_state_values(tensors, count: int, m, v, stream=None):
+    """The states as float32 values: m[i] and v[i] (``pointers``, either may be
+    None) receive tensor i's."""
+    _check(lib().dc_adamw_state_values(tensors, count, m, v, _stream(stream)),
+           "dc_adamw_state_values")
+
+
+def dc_grad_norm_workspace_size(count: int) -> int:
+    out = ctypes.c_size_t(0)
+    _check(lib().dc_grad_norm_workspace_size(count, ctypes.byref(out)),
+           "dc_grad_norm_workspace_size")
+    return int(out.value)
+
+
+def dc_grad_norm(tensors, count: int, max_norm: float, norm=None, scale=None, ws=None,
+                 stream=None):
+    """norm: the gradients' global 2-norm; scale: the factor that clips it to
+    max_norm (float32 device scalars or None)."""
+    for t, name in ((norm, "norm"), (scale, "scale")):
+        if t is not None and t.numel() != 1:
+            raise ValueError(f"{name} must hold one value")
+    ws_ptr, ws_bytes = _ws(ws)
+    _check(lib().dc_grad_norm(
+        tensors, count, float(max_norm), _ptr(norm, "norm", None, torch.float32, True),
+        _ptr(scale, "scale", None, torch.float32, True), ws_ptr, ws_bytes, _stream(stream)),
+        "dc_grad_norm")
+
+
 # ---------------------------------------------------------------- conveniences
 # Allocate outputs with torch (device memory is PyTorch's job) and call the ABI.
 
@@ -449,4 +661,31 @@ def backward(p: Problem, x, w_off, w, offset, grad_y, ws=None, stream=None):
         ws = workspace(p, True, dev)
     deform_conv_bwd(p, x, w_off, w, offset, grad_y, out["grad_x"], out["grad_w_off"],
                     out["grad_b_off"], out["grad_w"], out["grad_offset"], ws, stream)
+    return out
+
+
+def norm_workspace(p: NormProblem, backward: bool, device="cuda"):
+    return torch.empty(max(dc_group_norm_workspace_size(p, backward), 1), dtype=torch.uint8,
+                       device=device)
+
+
+def group_norm(p: NormProblem, x, gamma=None, beta=None, ws=None, stream=None):
+    """Returns (y, mean, rstd)."""
+    y = torch.empty(p.shape, dtype=p.torch_dtype, device=x.device)
+    mean, rstd = (torch.empty(p.stat_shape, dtype=torch.float32, device=x.device) for _ in range(2))
+    if ws is None:
+        ws = norm_workspace(p, False, x.device)
+    dc_group_norm_fwd(p, x, gamma, beta, y, mean, rstd, ws, stream)
+    return y, mean, rstd
+
+
+def group_norm_backward(p: NormProblem, x, gamma, beta, mean, rstd, grad_y, ws=None, stream=None):
+    """Returns dict(grad_x, grad_gamma, grad_beta)."""
+    out = dict(grad_x=torch.empty(p.shape, dtype=p.torch_dtype, device=x.device),
+               grad_gamma=torch.empty(p.c, dtype=torch.float32, device=x.device),
+               grad_beta=torch.empty(p.c, dtype=torch.float32, device=x.device))
+    if ws is None:
+        ws = norm_workspace(p, True, x.device)
+    dc_group_norm_bwd(p, x, gamma, beta, mean, rstd, grad_y, out["grad_x"], out["grad_gamma"],
+                      out["grad_beta"], ws, stream)
     return out

@@ -10,6 +10,8 @@
 // accumulates the offset gradient and replays the deformed map; K4 runs the
 // offset convolution's backward; a second GEMM gives the main weights'
 // gradient from the replayed map.
+#include <float.h>
+#include <math.h>
 #include <stdint.h>
 #include <string.h>
 
@@ -742,6 +744,239 @@ const char* dc_build_info(void) {
 #define DC_STR2(x) #x
 #define DC_STR(x) DC_STR2(x)
          DC_STR(__CUDACC_VER_MAJOR__) "." DC_STR(__CUDACC_VER_MINOR__);
+}
+
+}  // extern "C"
+
+namespace dc {
+namespace {
+
+dc_status make_norm(const dc_norm_problem* p, NormArgs* a) {
+  if (!p) return DC_ERR_INVALID_ARG;
+  if (p->n < 0 || p->c <= 0 || p->h <= 0 || p->w <= 0 || p->groups <= 0 || p->c % p->groups != 0)
+    return DC_ERR_INVALID_ARG;
+  if (p->dtype != DC_F32 && p->dtype != DC_BF16) return DC_ERR_INVALID_ARG;
+  if (p->grad_dtype != DC_F32 && p->grad_dtype != p->dtype) return DC_ERR_INVALID_ARG;
+  if (p->layout != DC_NCHW && p->layout != DC_NHWC) return DC_ERR_INVALID_ARG;
+  if (p->act != DC_ACT_NONE && p->act != DC_ACT_RELU && p->act != DC_ACT_SILU &&
+      p->act != DC_ACT_GELU)
+    return DC_ERR_INVALID_ARG;
+  if (!(p->eps >= 0.f) || p->eps > FLT_MAX) return DC_ERR_INVALID_ARG;
+  const long long hw = (long long)p->h * p->w;
+  if (hw > 1LL << 30 || p->c > 1 << 20 || (long long)p->n * p->c > INT_MAX ||
+      (double)p->n * p->c * (double)hw > (double)(1LL << 40))
+    return DC_ERR_UNSUPPORTED;
+  a->n = p->n;
+  a->c = p->c;
+  a->groups = p->groups;
+  a->cpg = p->c / p->groups;
+  a->hw = (int)hw;
+  a->nhwc = p->layout == DC_NHWC;
+  a->act = p->act;
+  a->eps = p->eps;
+  a->dt = p->dtype;
+  a->gdt = p->grad_dtype;
+  return norm_supported(*a) ? DC_OK : DC_ERR_UNSUPPORTED;
+}
+
+dc_status run(const char* name, cudaStream_t s, cudaError_t (*launch)(const NormArgs&, cudaStream_t),
+              const NormArgs& a) {
+  return cuda_status(timed(name, s, [&] { return launch(a, s); }));
+}
+
+bool aligned_to(const void* p, size_t n) { return ((uintptr_t)p & (n - 1)) == 0; }
+
+// A tensor of the AdamW calls; grad_only: what the gradient norm reads of it.
+dc_status check_tensor(const dc_adamw_tensor& t, bool grad_only) {
+  if (t.count < 0) return DC_ERR_INVALID_ARG;
+  if (t.grad_dtype != DC_F32 && t.grad_dtype != DC_BF16) return DC_ERR_INVALID_ARG;
+  if (t.count && !t.grad) return DC_ERR_INVALID_ARG;
+  if (!aligned_to(t.grad, elt_size(t.grad_dtype))) return DC_ERR_UNSUPPORTED;
+  if (grad_only) return DC_OK;
+  if (t.param_dtype != DC_F32 && t.param_dtype != DC_BF16) return DC_ERR_INVALID_ARG;
+  if (t.master && t.param_dtype != DC_BF16) return DC_ERR_INVALID_ARG;
+  if (t.state != DC_STATE_F32 && t.state != DC_STATE_Q8) return DC_ERR_INVALID_ARG;
+  if (!(t.weight_decay >= 0.f) || t.weight_decay > FLT_MAX) return DC_ERR_INVALID_ARG;
+  if (t.count && (!t.param || !t.m || !t.v)) return DC_ERR_INVALID_ARG;
+  if (t.count && t.state == DC_STATE_Q8 && (!t.m_scale || !t.v_scale)) return DC_ERR_INVALID_ARG;
+  const size_t st = t.state == DC_STATE_Q8 ? 1 : 4;
+  if (!aligned_to(t.param, elt_size(t.param_dtype)) || !aligned_to(t.master, 4) ||
+      !aligned_to(t.m, st) || !aligned_to(t.v, st))
+    return DC_ERR_UNSUPPORTED;
+  if (t.state == DC_STATE_Q8 && (!aligned_to(t.m_scale, 4) || !aligned_to(t.v_scale, 4)))
+    return DC_ERR_UNSUPPORTED;
+  return DC_OK;
+}
+
+// The state values are read: state, count, m, v and the scales.
+dc_status check_state(const dc_adamw_tensor& t) {
+  if (t.count < 0) return DC_ERR_INVALID_ARG;
+  if (t.state != DC_STATE_F32 && t.state != DC_STATE_Q8) return DC_ERR_INVALID_ARG;
+  if (t.count && (!t.m || !t.v)) return DC_ERR_INVALID_ARG;
+  const bool q8 = t.state == DC_STATE_Q8;
+  if (t.count && q8 && (!t.m_scale || !t.v_scale)) return DC_ERR_INVALID_ARG;
+  const size_t st = q8 ? 1 : 4;
+  if (!aligned_to(t.m, st) || !aligned_to(t.v, st)) return DC_ERR_UNSUPPORTED;
+  if (q8 && (!aligned_to(t.m_scale, 4) || !aligned_to(t.v_scale, 4))) return DC_ERR_UNSUPPORTED;
+  return DC_OK;
+}
+
+}  // namespace
+}  // namespace dc
+
+extern "C" {
+
+dc_status dc_group_norm_workspace_size(const dc_norm_problem* prob, int backward, size_t* bytes) {
+  if (!bytes) return DC_ERR_INVALID_ARG;
+  NormArgs a{};
+  const dc_status st = make_norm(prob, &a);
+  if (st != DC_OK) return st;
+  *bytes = norm_workspace_bytes(a, backward != 0);
+  return DC_OK;
+}
+
+dc_status dc_group_norm_fwd(const dc_norm_problem* prob, const void* x, const float* gamma,
+                            const float* beta, void* y, float* mean, float* rstd, void* ws,
+                            size_t ws_bytes, void* stream) {
+  NormArgs a{};
+  dc_status st = make_norm(prob, &a);
+  if (st != DC_OK) return st;
+  if (a.n == 0) return DC_OK;
+  if (!x || !y) return DC_ERR_INVALID_ARG;
+  const void* ptrs[] = {x, gamma, beta, y, mean, rstd, ws};
+  for (const void* p : ptrs)
+    if (p && !aligned16(p)) return DC_ERR_UNSUPPORTED;
+  const size_t need = norm_workspace_bytes(a, false);
+  if (need && (!ws || ws_bytes < need)) return DC_ERR_WORKSPACE;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  a.x = x;
+  a.gamma = gamma;
+  a.beta = beta;
+  a.y = y;
+  a.mean = mean;
+  a.rstd = rstd;
+  a.ws = static_cast<char*>(ws);
+  if ((st = run("norm_stats", s, launch_norm_stats, a)) != DC_OK) return st;
+  if ((st = run("norm_merge", s, launch_norm_merge, a)) != DC_OK) return st;
+  return run("norm_apply", s, launch_norm_apply, a);
+}
+
+dc_status dc_group_norm_bwd(const dc_norm_problem* prob, const void* x, const float* gamma,
+                            const float* beta, const float* mean, const float* rstd,
+                            const void* grad_y, void* grad_x, float* grad_gamma,
+                            float* grad_beta, void* ws, size_t ws_bytes, void* stream) {
+  NormArgs a{};
+  dc_status st = make_norm(prob, &a);
+  if (st != DC_OK) return st;
+  if (a.n && (!x || !mean || !rstd || !grad_y || !grad_x)) return DC_ERR_INVALID_ARG;
+  const void* ptrs[] = {x, gamma, beta, mean, rstd, grad_y, grad_x, grad_gamma, grad_beta, ws};
+  for (const void* p : ptrs)
+    if (p && !aligned16(p)) return DC_ERR_UNSUPPORTED;
+  const size_t need = norm_workspace_bytes(a, true);
+  if (need && (!ws || ws_bytes < need)) return DC_ERR_WORKSPACE;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  a.x = x;
+  a.gamma = gamma;
+  a.beta = beta;
+  a.mean = const_cast<float*>(mean);
+  a.rstd = const_cast<float*>(rstd);
+  a.gy = grad_y;
+  a.gx = grad_x;
+  a.ggamma = grad_gamma;
+  a.gbeta = grad_beta;
+  a.ws = static_cast<char*>(ws);
+  if (a.n) {
+    if ((st = run("norm_sums", s, launch_norm_sums, a)) != DC_OK) return st;
+    if ((st = run("norm_merge_bwd", s, launch_norm_merge_bwd, a)) != DC_OK) return st;
+    if ((st = run("norm_apply_bwd", s, launch_norm_apply_bwd, a)) != DC_OK) return st;
+  }
+  if (!grad_gamma && !grad_beta) return DC_OK;
+  return run("norm_params", s, launch_norm_params, a);
+}
+
+dc_status dc_adamw_step(const dc_adamw_tensor* tensors, int count, const dc_adamw_hyper* hyper,
+                        const float* grad_scale, const float* schedule, void* stream) {
+  if (count < 0 || (count && !tensors) || !hyper) return DC_ERR_INVALID_ARG;
+  const double lr = hyper->lr, b1 = hyper->beta1, b2 = hyper->beta2, eps = hyper->eps;
+  if (!(lr >= 0) || lr > FLT_MAX || !(b1 >= 0 && b1 < 1) || !(b2 >= 0 && b2 < 1) || !(eps >= 0) ||
+      eps > FLT_MAX || hyper->step < 1)
+    return DC_ERR_INVALID_ARG;
+  if (!aligned_to(grad_scale, 4) || !aligned_to(schedule, 4)) return DC_ERR_UNSUPPORTED;
+  for (int i = 0; i < count; ++i) {
+    const dc_status st = check_tensor(tensors[i], false);
+    if (st != DC_OK) return st;
+  }
+  AdamScalars h{};
+  h.lr = (float)lr;
+  h.b1 = (float)b1;
+  h.omb1 = (float)(1.0 - b1);
+  h.b2 = (float)b2;
+  h.omb2 = (float)(1.0 - b2);
+  h.eps = (float)eps;
+  h.root2 = (float)(1.0 / sqrt(1.0 - pow(b2, (double)hyper->step)));
+  h.step = (float)(lr / (1.0 - pow(b1, (double)hyper->step)));
+  h.grad_scale = grad_scale;
+  h.schedule = schedule;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  for (int i = 0; i < count; i += kAdamTensors) {
+    const int k = count - i < kAdamTensors ? count - i : kAdamTensors;
+    const dc_status st =
+        cuda_status(timed("adamw", s, [&] { return launch_adamw(tensors + i, k, h, s); }));
+    if (st != DC_OK) return st;
+  }
+  return DC_OK;
+}
+
+dc_status dc_adamw_state_values(const dc_adamw_tensor* tensors, int count, float* const* m,
+                                float* const* v, void* stream) {
+  if (count < 0 || (count && !tensors)) return DC_ERR_INVALID_ARG;
+  for (int i = 0; i < count; ++i) {
+    const dc_status st = check_state(tensors[i]);
+    if (st != DC_OK) return st;
+    if ((m && !aligned_to(m[i], 4)) || (v && !aligned_to(v[i], 4))) return DC_ERR_UNSUPPORTED;
+  }
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  for (int i = 0; i < count; i += kAdamTensors) {
+    const int k = count - i < kAdamTensors ? count - i : kAdamTensors;
+    const dc_status st = cuda_status(timed("adamw_values", s, [&] {
+      return launch_adamw_values(tensors + i, k, m ? m + i : nullptr, v ? v + i : nullptr, s);
+    }));
+    if (st != DC_OK) return st;
+  }
+  return DC_OK;
+}
+
+dc_status dc_grad_norm_workspace_size(int count, size_t* bytes) {
+  if (count < 0 || !bytes) return DC_ERR_INVALID_ARG;
+  *bytes = (size_t)ceil_div_ll(count, kAdamTensors) * kNormParts * sizeof(float);
+  return DC_OK;
+}
+
+dc_status dc_grad_norm(const dc_adamw_tensor* tensors, int count, float max_norm, float* norm,
+                       float* scale, void* ws, size_t ws_bytes, void* stream) {
+  if (count < 0 || (count && !tensors) || !(max_norm > 0.f)) return DC_ERR_INVALID_ARG;
+  for (int i = 0; i < count; ++i) {
+    const dc_status st = check_tensor(tensors[i], true);
+    if (st != DC_OK) return st;
+  }
+  if (!aligned_to(norm, 4) || !aligned_to(scale, 4) || (ws && !aligned16(ws)))
+    return DC_ERR_UNSUPPORTED;
+  size_t need = 0;
+  dc_grad_norm_workspace_size(count, &need);
+  if (need && (!ws || ws_bytes < need)) return DC_ERR_WORKSPACE;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  float* part = static_cast<float*>(ws);
+  long long parts = 0;
+  for (int i = 0; i < count; i += kAdamTensors) {
+    const int k = count - i < kAdamTensors ? count - i : kAdamTensors;
+    const dc_status st = cuda_status(
+        timed("grad_squares", s, [&] { return launch_grad_squares(tensors + i, k, part + parts, s); }));
+    if (st != DC_OK) return st;
+    parts += kNormParts;
+  }
+  return cuda_status(timed("grad_norm", s, [&] {
+    return launch_grad_norm(part, parts, max_norm, norm, scale, s);
+  }));
 }
 
 }  // extern "C"

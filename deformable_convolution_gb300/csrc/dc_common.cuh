@@ -346,4 +346,55 @@ cudaError_t launch_relu_fwd(const void* y, void* out, long long count, dc_dtype 
 cudaError_t launch_relu_bwd(const void* act, const float* gout, void* gin, long long count,
                             dc_dtype dt, cudaStream_t s);
 
+// ---------------------------------------------------------------- training step
+// Group norm with an activation (group_norm.cu).
+struct NormArgs {
+  int n, c, groups, cpg;  // cpg: channels of a group
+  int hw;
+  bool nhwc;
+  int act;
+  float eps;
+  dc_dtype dt, gdt;
+  const void* x;
+  const float* gamma;  // null: ones
+  const float* beta;   // null: zeros
+  void* y;
+  float* mean;  // [n][groups]
+  float* rstd;
+  const void* gy;
+  void* gx;
+  float* ggamma;  // may be null
+  float* gbeta;
+  char* ws;
+};
+bool norm_supported(const NormArgs& a);  // grids and indices in range
+// Workspace bytes of the forward or backward pass.
+size_t norm_workspace_bytes(const NormArgs& a, bool backward);
+// One launch each; the ABI layer runs them in order.
+cudaError_t launch_norm_stats(const NormArgs& a, cudaStream_t s);        // per-channel statistics of parts
+cudaError_t launch_norm_merge(const NormArgs& a, cudaStream_t s);        // mean and rstd of every group
+cudaError_t launch_norm_apply(const NormArgs& a, cudaStream_t s);        // y
+cudaError_t launch_norm_sums(const NormArgs& a, cudaStream_t s);         // per-channel gradient sums of parts
+cudaError_t launch_norm_merge_bwd(const NormArgs& a, cudaStream_t s);    // of images and groups
+cudaError_t launch_norm_apply_bwd(const NormArgs& a, cudaStream_t s);    // grad_x
+cudaError_t launch_norm_params(const NormArgs& a, cudaStream_t s);       // grad_gamma, grad_beta
+
+// AdamW and the gradient norm (adamw.cu).
+struct AdamScalars {
+  float lr, b1, omb1, b2, omb2, eps;
+  float root2;  // 1 / sqrt(1 - beta2^step)
+  float step;   // lr / (1 - beta1^step)
+  const float* grad_scale;  // may be null
+  const float* schedule;    // may be null
+};
+// tensors: checked by the ABI layer; at most kAdamTensors (a launch's table).
+constexpr int kAdamTensors = 400;
+cudaError_t launch_adamw(const dc_adamw_tensor* t, int count, const AdamScalars& h, cudaStream_t s);
+cudaError_t launch_adamw_values(const dc_adamw_tensor* t, int count, float* const* m,
+                                float* const* v, cudaStream_t s);
+constexpr int kNormParts = 608;  // partial sums of one gradient-norm launch
+cudaError_t launch_grad_squares(const dc_adamw_tensor* t, int count, float* part, cudaStream_t s);
+cudaError_t launch_grad_norm(const float* part, long long parts, float max_norm, float* norm,
+                             float* scale, cudaStream_t s);
+
 }  // namespace dc

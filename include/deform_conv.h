@@ -307,6 +307,150 @@ dc_status dc_relu_fwd(const void* y, void* out, size_t count, dc_dtype dtype, vo
 dc_status dc_relu_bwd(const void* act, const float* grad_out, void* grad_in, size_t count,
                       dc_dtype dtype, void* stream);
 
+/* ---------------------------------------------------------------- training step
+ * The operators around the layers in a training step: group norm with an
+ * activation between layers, the global gradient norm with its clip factor,
+ * and AdamW over all parameters at once.  The explainer page trains networks
+ * of deformable layers ("Why it works / Fixing the slowest stage lifts the
+ * whole layer": training time of a fully deformable ResNet) and leaves these
+ * parts of the step to the framework. */
+
+typedef enum { DC_NCHW = 0, DC_NHWC = 1 } dc_layout;
+typedef enum { DC_ACT_NONE = 0, DC_ACT_RELU = 1, DC_ACT_SILU = 2, DC_ACT_GELU = 3 } dc_act;
+
+/* Group norm followed by an activation.  The c channels form `groups` equal
+ * groups of consecutive channels; each group of each image is normalised over
+ * its m = (c / groups) * h * w values x:
+ *   mean = sum(x) / m, var = sum((x - mean)^2) / m, rstd = 1 / sqrt(var + eps),
+ *   xh = (x - mean) * rstd, z = xh * gamma[channel] + beta[channel], y = act(z)
+ * with act(z) = z, max(z, 0) (NaN kept), z / (1 + exp(-z)) or
+ * z * (1 + erf(z / sqrt 2)) / 2.
+ * x, y, grad_x: dense [n][c][h][w] (DC_NCHW, what the deformable layer takes
+ * and gives) or [n][h][w][c] (DC_NHWC), in `dtype`.  grad_y: the same layout
+ * in grad_dtype: DC_F32 (a deformable layer's grad_x) or `dtype`.
+ * n may be 0 (an empty batch); h * w is at most 2^30. */
+typedef struct {
+  int n, c, h, w, groups;
+  dc_dtype dtype;
+  dc_layout layout;
+  dc_act act;
+  float eps; /* >= 0, finite */
+  dc_dtype grad_dtype;
+} dc_norm_problem;
+
+/* Bytes of workspace the forward (backward = 0) or backward call needs; may
+ * be 0.  Errors: DC_ERR_INVALID_ARG for NULL bytes or a bad problem (a size
+ * below 1 other than n, c % groups != 0, an unknown enum, a bad eps, a
+ * grad_dtype that is neither DC_F32 nor dtype); DC_ERR_UNSUPPORTED for h * w
+ * over 2^30, c over 2^20, n * c over 2^31 - 1 or more than 2^40 elements. */
+dc_status dc_group_norm_workspace_size(const dc_norm_problem* prob, int backward, size_t* bytes);
+
+/* Forward.
+ *   gamma, beta  [c] float32, NULL = ones / zeros
+ *   mean, rstd   [n][groups] float32, written; NULL = not returned (the
+ *                backward needs them)
+ *   y            may be x itself
+ * All arithmetic is float32; a bf16 y is rounded to nearest even.  The sums
+ * run in a fixed order: the same inputs give the same bits. */
+dc_status dc_group_norm_fwd(const dc_norm_problem* prob, const void* x, const float* gamma,
+                            const float* beta, void* y, float* mean, float* rstd, void* ws,
+                            size_t ws_bytes, void* stream);
+
+/* Backward, for the gradient grad_y of y:
+ *   dz = grad_y * act'(z) (act'(z) = z > 0 for the ReLU),
+ *   s1 = sum(gamma * dz) / m, s2 = sum(gamma * dz * xh) / m over a group,
+ *   grad_x = rstd * (gamma * dz - s1 - xh * s2),
+ *   grad_gamma[channel] = sum(dz * xh), grad_beta[channel] = sum(dz)
+ * over images and pixels.
+ *   x, gamma, beta  as in the forward; mean, rstd: the forward's
+ *   grad_x          `dtype`; may be grad_y itself where the types agree
+ *   grad_gamma, grad_beta  [c] float32, overwritten, NULL = not returned
+ * The sums run in a fixed order.  Errors of both calls: DC_ERR_INVALID_ARG
+ * for a bad problem or a NULL required pointer (x, y, mean, rstd, grad_y and
+ * grad_x of an empty batch may be NULL), DC_ERR_UNSUPPORTED for a pointer
+ * that is not 16-byte aligned, DC_ERR_WORKSPACE for a short workspace. */
+dc_status dc_group_norm_bwd(const dc_norm_problem* prob, const void* x, const float* gamma,
+                            const float* beta, const float* mean, const float* rstd,
+                            const void* grad_y, void* grad_x, float* grad_gamma,
+                            float* grad_beta, void* ws, size_t ws_bytes, void* stream);
+
+/* Optimiser state: float32, or 8 bits with a float32 scale for each block of
+ * DC_STATE_BLOCK consecutive elements of a tensor (the last block may be
+ * short).  The 8-bit code is a square law, so that its steps are finest in
+ * proportion to the value's square root:
+ *   m: signed char q in [-127, 127], value s * |t| * t with t = q / 127 and s
+ *      the block's largest |m|; q = round(127 * sqrt(|m| / s)) with m's sign;
+ *   v: kept as its root r = sqrt(v): unsigned char q in [0, 255], value
+ *      (s * t^2)^2 with t = q / 255 and s the block's largest r;
+ *      q = round(255 * sqrt(r / s)), but at least 1 where v > 0, so that a
+ *      small v never becomes 0 and its update never runs away.
+ * A block whose s is below 2^-126 is stored as zeros. */
+#define DC_STATE_BLOCK 256
+typedef enum { DC_STATE_F32 = 0, DC_STATE_Q8 = 1 } dc_state;
+
+/* One parameter tensor.  Pointers need only their element's alignment;
+ * tensors must not overlap.  count 0 is allowed. */
+typedef struct {
+  void* param;        /* [count] param_dtype, updated */
+  float* master;      /* NULL, or the float32 parameter a bf16 `param` is a rounded copy of:
+                         the update is made on `master` and rounded into `param` */
+  const void* grad;   /* [count] grad_dtype */
+  void* m;            /* first moment:  [count] float, or signed char (DC_STATE_Q8) */
+  void* v;            /* second moment: [count] float, or unsigned char */
+  float* m_scale;     /* DC_STATE_Q8: [ceil(count / DC_STATE_BLOCK)] each; else ignored */
+  float* v_scale;
+  long long count;
+  dc_dtype param_dtype, grad_dtype;
+  dc_state state;
+  float weight_decay; /* >= 0, finite */
+} dc_adamw_tensor;
+
+/* beta1, beta2 in [0, 1); lr, eps >= 0; step: this step's number, from 1. */
+typedef struct {
+  double lr, beta1, beta2, eps;
+  long long step;
+} dc_adamw_hyper;
+
+/* One AdamW step (decoupled weight decay) over `count` tensors:
+ *   g = grad * *grad_scale
+ *   m = m * beta1 + g * (1 - beta1);  v = v * beta2 + g * g * (1 - beta2)
+ *   p = p * (1 - lr * weight_decay)
+ *       - (m / (sqrt(v) / sqrt(1 - beta2^step) + eps)) * (lr / (1 - beta1^step))
+ * in float32, every operation rounded by itself; 8-bit states are decoded
+ * first and encoded last, the update uses the values before encoding.
+ *   tensors     host array, read before the call returns
+ *   grad_scale  device float, NULL = 1 (dc_grad_norm's scale).  If it is not
+ *               finite the step is skipped: nothing is changed.
+ *   schedule    device float[3] {lr, 1 - beta1^step, 1 - beta2^step} that
+ *               take the place of hyper's, NULL = hyper's (for steps replayed
+ *               from a CUDA graph, whose arguments are fixed)
+ * A bf16 param without a master is updated from its rounded value and rounded
+ * to nearest even.  A gradient that is not finite makes its element's state
+ * and parameter so, or its whole block's state where that is in 8 bits.
+ * Any number of tensors (one launch per 400).  Errors: DC_ERR_INVALID_ARG for
+ * NULL pointers, negative counts or hyper-parameters out of range,
+ * DC_ERR_UNSUPPORTED for a pointer without its element's alignment. */
+dc_status dc_adamw_step(const dc_adamw_tensor* tensors, int count, const dc_adamw_hyper* hyper,
+                        const float* grad_scale, const float* schedule, void* stream);
+
+/* The states as float32 values: m[i] and v[i] (host arrays of device
+ * pointers, either may be NULL, as may any entry) receive tensor i's. */
+dc_status dc_adamw_state_values(const dc_adamw_tensor* tensors, int count, float* const* m,
+                                float* const* v, void* stream);
+
+/* Global gradient norm over all tensors (only grad, grad_dtype and count are
+ * read): *norm = sqrt(sum of squares), and the factor that clips it to
+ * max_norm: *scale = min(1, max_norm / (*norm + 1e-6)); a norm that is not
+ * finite gives a NaN scale (a step that dc_adamw_step skips).
+ *   norm, scale  device floats, overwritten; either may be NULL
+ *   max_norm     > 0; infinity gives scale 1 for every finite norm
+ * Squares are summed in float32 in a fixed order (a gradient above 1.8e19 in
+ * magnitude overflows to an infinite norm).  ws: dc_grad_norm_workspace_size
+ * bytes, 16-byte aligned. */
+dc_status dc_grad_norm_workspace_size(int count, size_t* bytes);
+dc_status dc_grad_norm(const dc_adamw_tensor* tensors, int count, float max_norm, float* norm,
+                       float* scale, void* ws, size_t ws_bytes, void* stream);
+
 /* Static description of a status code. */
 const char* dc_status_string(dc_status status);
 

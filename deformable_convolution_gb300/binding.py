@@ -9,6 +9,7 @@ from __future__ import annotations
 
 import ctypes
 from dataclasses import dataclass
+from functools import cached_property
 
 import torch
 
@@ -458,6 +459,26 @@ def dc_relu_bwd(act, grad_out, grad_in, stream=None):
                              _dc_dtype(act), _stream(stream)), "dc_relu_bwd")
 
 
+def _arg(t, name, shape, dtype, optional=False):
+    """As ``_ptr``, a plain address: one pass over the usual case, ``_ptr`` for
+    what is missing or wrong (these calls are short: a check of a tensor costs
+    as much as a kernel's launch)."""
+    if t.__class__ in _TENSORS and t.dtype is dtype and t.shape == shape and t.is_cuda and \
+            t.is_contiguous():
+        return t.data_ptr()
+    p = _ptr(t, name, shape, dtype, optional)
+    return None if p is None else p.value
+
+
+_TENSORS = (torch.Tensor, torch.nn.Parameter)
+
+
+def _raw_stream(stream):
+    if stream is not None:
+        return stream.cuda_stream
+    return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
+
+
 # ---------------------------------------------------------------- group norm
 
 @dataclass(frozen=True)
@@ -481,28 +502,36 @@ class NormProblem:
         return DcNormProblem(self.n, self.c, self.h, self.w, self.groups, self.dtype, self.layout,
                              self.act, self.eps, self.grad_dtype)
 
-    @property
+    @cached_property
+    def _as_parameter_(self):
+        return ctypes.byref(self.c_struct())
+
+    @cached_property
     def torch_dtype(self):
         return _TORCH_DTYPE[self.dtype]
 
-    @property
+    @cached_property
     def shape(self):
         """Of x, y, grad_y and grad_x."""
         if self.layout == DC_NHWC:
             return (self.n, self.h, self.w, self.c)
         return (self.n, self.c, self.h, self.w)
 
-    @property
+    @cached_property
     def stat_shape(self):
         """Of mean and rstd."""
         return (self.n, self.groups)
 
+    @cached_property
+    def channel_shape(self):
+        """Of gamma, beta and their gradients."""
+        return (self.c,)
+
 
 def dc_group_norm_workspace_size(p: NormProblem, backward: bool) -> int:
     out = ctypes.c_size_t(0)
-    st = p.c_struct()
-    _check(lib().dc_group_norm_workspace_size(ctypes.byref(st), 1 if backward else 0,
-                                              ctypes.byref(out)), "dc_group_norm_workspace_size")
+    _check(lib().dc_group_norm_workspace_size(p, 1 if backward else 0, ctypes.byref(out)),
+           "dc_group_norm_workspace_size")
     return int(out.value)
 
 
@@ -510,37 +539,38 @@ def _ws(ws):
     """(pointer, bytes) of a workspace that may be None."""
     if ws is None:
         return None, 0
-    return _ptr(ws, "ws", dtype=torch.uint8), ws.numel()
+    return _arg(ws, "ws", ws.shape, torch.uint8), ws.numel()
 
 
 def dc_group_norm_fwd(p: NormProblem, x, gamma, beta, y, mean=None, rstd=None, ws=None,
                       stream=None):
     """y = act(group norm of x); mean and rstd [n, groups] for the backward.
     gamma, beta: float32 [c] or None; y may be x."""
-    dt, f32, sh, ss = p.torch_dtype, torch.float32, p.shape, p.stat_shape
-    st = p.c_struct()
+    dt, f32, sh, ss, cs = p.torch_dtype, torch.float32, p.shape, p.stat_shape, p.channel_shape
     ws_ptr, ws_bytes = _ws(ws)
-    _check(lib().dc_group_norm_fwd(
-        ctypes.byref(st), _ptr(x, "x", sh, dt), _ptr(gamma, "gamma", (p.c,), f32, True),
-        _ptr(beta, "beta", (p.c,), f32, True), _ptr(y, "y", sh, dt),
-        _ptr(mean, "mean", ss, f32, True), _ptr(rstd, "rstd", ss, f32, True),
-        ws_ptr, ws_bytes, _stream(stream)), "dc_group_norm_fwd")
+    status = lib().dc_group_norm_fwd(
+        p, _arg(x, "x", sh, dt), _arg(gamma, "gamma", cs, f32, True),
+        _arg(beta, "beta", cs, f32, True), _arg(y, "y", sh, dt),
+        _arg(mean, "mean", ss, f32, True), _arg(rstd, "rstd", ss, f32, True),
+        ws_ptr, ws_bytes, _raw_stream(stream))
+    if status:
+        raise DcError(status, "dc_group_norm_fwd")
 
 
 def dc_group_norm_bwd(p: NormProblem, x, gamma, beta, mean, rstd, grad_y, grad_x,
                       grad_gamma=None, grad_beta=None, ws=None, stream=None):
     """grad_x (x's dtype; may be grad_y where the types agree), grad_gamma and
     grad_beta (float32 [c] or None) from grad_y in ``p.grad_dtype``."""
-    dt, f32, sh, ss = p.torch_dtype, torch.float32, p.shape, p.stat_shape
-    st = p.c_struct()
+    dt, f32, sh, ss, cs = p.torch_dtype, torch.float32, p.shape, p.stat_shape, p.channel_shape
     ws_ptr, ws_bytes = _ws(ws)
-    _check(lib().dc_group_norm_bwd(
-        ctypes.byref(st), _ptr(x, "x", sh, dt), _ptr(gamma, "gamma", (p.c,), f32, True),
-        _ptr(beta, "beta", (p.c,), f32, True), _ptr(mean, "mean", ss, f32),
-        _ptr(rstd, "rstd", ss, f32), _ptr(grad_y, "grad_y", sh, _TORCH_DTYPE[p.grad_dtype]),
-        _ptr(grad_x, "grad_x", sh, dt), _ptr(grad_gamma, "grad_gamma", (p.c,), f32, True),
-        _ptr(grad_beta, "grad_beta", (p.c,), f32, True), ws_ptr, ws_bytes, _stream(stream)),
-        "dc_group_norm_bwd")
+    status = lib().dc_group_norm_bwd(
+        p, _arg(x, "x", sh, dt), _arg(gamma, "gamma", cs, f32, True),
+        _arg(beta, "beta", cs, f32, True), _arg(mean, "mean", ss, f32),
+        _arg(rstd, "rstd", ss, f32), _arg(grad_y, "grad_y", sh, _TORCH_DTYPE[p.grad_dtype]),
+        _arg(grad_x, "grad_x", sh, dt), _arg(grad_gamma, "grad_gamma", cs, f32, True),
+        _arg(grad_beta, "grad_beta", cs, f32, True), ws_ptr, ws_bytes, _raw_stream(stream))
+    if status:
+        raise DcError(status, "dc_group_norm_bwd")
 
 
 # ---------------------------------------------------------------- AdamW
@@ -583,11 +613,21 @@ def dc_adamw_step(tensors, count: int, hyper: DcAdamwHyper, grad_scale=None, sch
     """One AdamW step over ``tensors`` (``adamw_tensors``).  grad_scale: a
     float32 device scalar or None; schedule: float32 [3] {lr, 1 - beta1^step,
     1 - beta2^step} on the device or None."""
-    if grad_scale is not None and grad_scale.numel() != 1:
-        raise ValueError("grad_scale must hold one value")
-    _check(lib().dc_adamw_step(
-        tensors, count, ctypes.byref(hyper), _ptr(grad_scale, "grad_scale", None, torch.float32, True),
-        _ptr(schedule, "schedule", (3,), torch.float32, True), _stream(stream)), "dc_adamw_step")
+    status = lib().dc_adamw_step(
+        tensors, count, hyper, _scalar(grad_scale, "grad_scale"),
+        None if schedule is None else _arg(schedule, "schedule", (3,), torch.float32),
+        _raw_stream(stream))
+    if status:
+        raise DcError(status, "dc_adamw_step")
+
+
+def _scalar(t, name):
+    """The address of a one-element float32 device tensor, None for None."""
+    if t is None:
+        return None
+    if t.numel() != 1:
+        raise ValueError(f"{name} must hold one value")
+    return _arg(t, name, t.shape, torch.float32)
 
 
 def pointers(tensors, name, shapes, dtype):
@@ -602,8 +642,9 @@ def pointers(tensors, name, shapes, dtype):
 def dc_adamw_state_values(tensors, count: int, m, v, stream=None):
     """The states as float32 values: m[i] and v[i] (``pointers``, either may be
     None) receive tensor i's."""
-    _check(lib().dc_adamw_state_values(tensors, count, m, v, _stream(stream)),
-           "dc_adamw_state_values")
+    status = lib().dc_adamw_state_values(tensors, count, m, v, _raw_stream(stream))
+    if status:
+        raise DcError(status, "dc_adamw_state_values")
 
 
 def dc_grad_norm_workspace_size(count: int) -> int:
@@ -617,14 +658,11 @@ def dc_grad_norm(tensors, count: int, max_norm: float, norm=None, scale=None, ws
                  stream=None):
     """norm: the gradients' global 2-norm; scale: the factor that clips it to
     max_norm (float32 device scalars or None)."""
-    for t, name in ((norm, "norm"), (scale, "scale")):
-        if t is not None and t.numel() != 1:
-            raise ValueError(f"{name} must hold one value")
     ws_ptr, ws_bytes = _ws(ws)
-    _check(lib().dc_grad_norm(
-        tensors, count, float(max_norm), _ptr(norm, "norm", None, torch.float32, True),
-        _ptr(scale, "scale", None, torch.float32, True), ws_ptr, ws_bytes, _stream(stream)),
-        "dc_grad_norm")
+    status = lib().dc_grad_norm(tensors, count, max_norm, _scalar(norm, "norm"),
+                                _scalar(scale, "scale"), ws_ptr, ws_bytes, _raw_stream(stream))
+    if status:
+        raise DcError(status, "dc_grad_norm")
 
 
 # ---------------------------------------------------------------- conveniences

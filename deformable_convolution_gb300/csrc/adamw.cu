@@ -30,6 +30,8 @@ struct Entry {
   float *m_scale, *v_scale;
   long long count;
   float decay;
+  unsigned char lead;  // elements by which the first chunk starts ahead of the tensor
+  bool vec;            // runs of four elements from `lead` ahead are aligned in every array
   bool p16, g16, q8;
 };
 template <int N>
@@ -83,108 +85,354 @@ __device__ __forceinline__ unsigned char encode_v(float v, float root, float inv
   return (unsigned char)(v > 0.f && q < 1 && inv > 0.f ? 1 : q);
 }
 
+// ---------------------------------------------------------------- element access
+// A lane's eight elements of a warp's block of 256: two runs of four
+// consecutive ones (VEC: every array 16-byte aligned for float, 8 for bf16,
+// 4 for codes), or every 32nd one.  A warp's access is whole 128-byte lines
+// either way; the runs take a quarter of the instructions.
+
+template <bool VEC>
+__device__ __forceinline__ int place(int lane, int k) {
+  return VEC ? (k >> 2) * 128 + lane * 4 + (k & 3) : lane + 32 * k;
+}
+
+template <bool VEC>
+__device__ __forceinline__ void load8(const float* p, int lane, float* f) {
+  if (VEC) {
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const float4 v = *reinterpret_cast<const float4*>(p + h * 128 + lane * 4);
+      f[4 * h] = v.x, f[4 * h + 1] = v.y, f[4 * h + 2] = v.z, f[4 * h + 3] = v.w;
+    }
+  } else {
+#pragma unroll
+    for (int k = 0; k < kPer; ++k) f[k] = p[lane + 32 * k];
+  }
+}
+template <bool VEC>
+__device__ __forceinline__ void load8(const __nv_bfloat16* p, int lane, float* f) {
+  if (VEC) {
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const uint2 v = *reinterpret_cast<const uint2*>(p + h * 128 + lane * 4);
+      f[4 * h] = __uint_as_float(v.x << 16), f[4 * h + 1] = __uint_as_float(v.x & 0xffff0000u);
+      f[4 * h + 2] = __uint_as_float(v.y << 16), f[4 * h + 3] = __uint_as_float(v.y & 0xffff0000u);
+    }
+  } else {
+#pragma unroll
+    for (int k = 0; k < kPer; ++k) f[k] = to_f(p[lane + 32 * k]);
+  }
+}
+template <bool VEC, typename C>
+__device__ __forceinline__ void load8(const C* p, int lane, C* c) {
+  if (VEC) {
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const uint32_t v = *reinterpret_cast<const uint32_t*>(p + h * 128 + lane * 4);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) c[4 * h + e] = (C)(v >> (8 * e));
+    }
+  } else {
+#pragma unroll
+    for (int k = 0; k < kPer; ++k) c[k] = p[lane + 32 * k];
+  }
+}
+
+template <bool VEC>
+__device__ __forceinline__ void store8(float* p, int lane, const float* f) {
+  if (VEC) {
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+      *reinterpret_cast<float4*>(p + h * 128 + lane * 4) =
+          make_float4(f[4 * h], f[4 * h + 1], f[4 * h + 2], f[4 * h + 3]);
+  } else {
+#pragma unroll
+    for (int k = 0; k < kPer; ++k) p[lane + 32 * k] = f[k];
+  }
+}
+template <bool VEC>
+__device__ __forceinline__ void store8(__nv_bfloat16* p, int lane, const float* f) {
+  if (VEC) {
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const __nv_bfloat162 a = __floats2bfloat162_rn(f[4 * h], f[4 * h + 1]);
+      const __nv_bfloat162 b = __floats2bfloat162_rn(f[4 * h + 2], f[4 * h + 3]);
+      *reinterpret_cast<uint2*>(p + h * 128 + lane * 4) =
+          make_uint2(*reinterpret_cast<const uint32_t*>(&a), *reinterpret_cast<const uint32_t*>(&b));
+    }
+  } else {
+#pragma unroll
+    for (int k = 0; k < kPer; ++k) p[lane + 32 * k] = __float2bfloat16_rn(f[k]);
+  }
+}
+template <bool VEC, typename C>
+__device__ __forceinline__ void store8(C* p, int lane, const C* c) {
+  if (VEC) {
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      uint32_t v = 0;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) v |= (uint32_t)(unsigned char)c[4 * h + e] << (8 * e);
+      *reinterpret_cast<uint32_t*>(p + h * 128 + lane * 4) = v;
+    }
+  } else {
+#pragma unroll
+    for (int k = 0; k < kPer; ++k) p[lane + 32 * k] = c[k];
+  }
+}
+
+// ---------------------------------------------------------------- the step
+
+// The step's numbers, read once by each thread (gs and the schedule's from
+// device memory, behind the first block's loads).
+struct Step {
+  float gs, lr, root2, step;
+  bool scaled;
+};
+__device__ __forceinline__ Step make_step(const AdamScalars& h) {
+  Step st{1.f, h.lr, h.root2, h.step, h.grad_scale != nullptr};
+  if (h.grad_scale) st.gs = *h.grad_scale;
+  if (h.schedule) {
+    st.lr = h.schedule[0];
+    st.step = __fdiv_rn(st.lr, h.schedule[1]);
+    st.root2 = __frcp_rn(__fsqrt_rn(h.schedule[2]));
+  }
+  return st;
+}
+
+// One element: p, m, v in, out with r = sqrt(v).
+__device__ __forceinline__ void update(const AdamScalars& h, const Step& st, float keep, float g,
+                                       float& p, float& m, float& v, float& r) {
+  if (st.scaled) g = __fmul_rn(g, st.gs);
+  m = __fadd_rn(__fmul_rn(m, h.b1), __fmul_rn(g, h.omb1));
+  v = __fadd_rn(__fmul_rn(v, h.b2), __fmul_rn(__fmul_rn(g, g), h.omb2));
+  r = __fsqrt_rn(v);
+  const float u = __fdiv_rn(m, __fadd_rn(__fmul_rn(r, st.root2), h.eps));
+  p = __fsub_rn(__fmul_rn(p, keep), __fmul_rn(u, st.step));
+}
+
+__device__ __forceinline__ float abs_max(float a, float b) {
+  return __uint_as_float(umax(__float_as_uint(a), __float_as_uint(fabsf(b))));
+}
+
+// The block's new scales (stored by lane 0) and their reciprocals.
+__device__ __forceinline__ void new_scales(const Entry& t, long long blk, int lane,
+                                           const float* m, const float* r, float* inv_m,
+                                           float* inv_v) {
+  float mt = 0.f, rt = 0.f;
+#pragma unroll
+  for (int k = 0; k < kPer; ++k) {
+    mt = abs_max(mt, m[k]);
+    rt = abs_max(rt, r[k]);
+  }
+  float ms, vs;
+  block_scale(warp_max(mt), &ms, inv_m);
+  block_scale(warp_max(rt), &vs, inv_v);
+  if (lane == 0) t.m_scale[blk] = ms, t.v_scale[blk] = vs;
+}
+
+// A whole block of 256 elements from `base`.  PARAM: 0 float, 1 bf16 with a
+// master, 2 bf16 alone.
+template <int PARAM, bool G16, bool Q8, bool VEC>
+__device__ __forceinline__ void whole_block(const Entry& t, long long base, int lane,
+                                            const AdamScalars& h, const Step& st) {
+  float p[kPer], g[kPer], m[kPer], v[kPer], r[kPer];
+  signed char cm[kPer];
+  unsigned char cv[kPer];
+  const long long blk = base / DC_STATE_BLOCK;
+  float ms = 0.f, vs = 0.f;
+  if (G16)
+    load8<VEC>(static_cast<const __nv_bfloat16*>(t.grad) + base, lane, g);
+  else
+    load8<VEC>(static_cast<const float*>(t.grad) + base, lane, g);
+  if (Q8) {
+    load8<VEC>(static_cast<const signed char*>(t.m) + base, lane, cm);
+    load8<VEC>(static_cast<const unsigned char*>(t.v) + base, lane, cv);
+    ms = t.m_scale[blk], vs = t.v_scale[blk];
+  } else {
+    load8<VEC>(static_cast<const float*>(t.m) + base, lane, m);
+    load8<VEC>(static_cast<const float*>(t.v) + base, lane, v);
+  }
+  if (PARAM == 1)
+    load8<VEC>(t.master + base, lane, p);
+  else if (PARAM == 2)
+    load8<VEC>(static_cast<const __nv_bfloat16*>(t.param) + base, lane, p);
+  else
+    load8<VEC>(static_cast<const float*>(t.param) + base, lane, p);
+  if (!isfinite(st.gs)) return;
+  const float keep = __fsub_rn(1.f, __fmul_rn(st.lr, t.decay));
+#pragma unroll
+  for (int k = 0; k < kPer; ++k) {
+    if (Q8) {
+      m[k] = decode_m(cm[k], ms);
+      v[k] = decode_root(cv[k], vs);
+      v[k] = __fmul_rn(v[k], v[k]);
+    }
+    update(h, st, keep, g[k], p[k], m[k], v[k], r[k]);
+  }
+  if (PARAM == 0)
+    store8<VEC>(static_cast<float*>(t.param) + base, lane, p);
+  else
+    store8<VEC>(static_cast<__nv_bfloat16*>(t.param) + base, lane, p);
+  if (PARAM == 1) store8<VEC>(t.master + base, lane, p);
+  if (Q8) {
+    float inv_m, inv_v;
+    new_scales(t, blk, lane, m, r, &inv_m, &inv_v);
+#pragma unroll
+    for (int k = 0; k < kPer; ++k) {
+      cm[k] = encode_m(m[k], inv_m);
+      cv[k] = encode_v(v[k], r[k], inv_v);
+    }
+    store8<VEC>(static_cast<signed char*>(t.m) + base, lane, cm);
+    store8<VEC>(static_cast<unsigned char*>(t.v) + base, lane, cv);
+  } else {
+    store8<VEC>(static_cast<float*>(t.m) + base, lane, m);
+    store8<VEC>(static_cast<float*>(t.v) + base, lane, v);
+  }
+}
+
+// A block that hangs over an end of its tensor (base < 0 where the tensor's
+// start is not on the vectors' grid), any kind.
+__device__ __noinline__ void part_block(const Entry& t, long long base, int lane,
+                                        const AdamScalars& h, const Step& st) {
+  if (!isfinite(st.gs)) return;
+  const long long blk = base / DC_STATE_BLOCK;
+  float ms = 0.f, vs = 0.f, m[kPer], r[kPer], v[kPer];
+  if (t.q8) ms = t.m_scale[blk], vs = t.v_scale[blk];
+  const float keep = __fsub_rn(1.f, __fmul_rn(st.lr, t.decay));
+#pragma unroll
+  for (int k = 0; k < kPer; ++k) {
+    const long long i = base + lane + 32 * k;
+    m[k] = v[k] = r[k] = 0.f;
+    if (i < 0 || i >= t.count) continue;
+    const float g = t.g16 ? to_f(static_cast<const __nv_bfloat16*>(t.grad)[i])
+                          : static_cast<const float*>(t.grad)[i];
+    float p = t.master ? t.master[i]
+              : t.p16  ? to_f(static_cast<const __nv_bfloat16*>(t.param)[i])
+                       : static_cast<const float*>(t.param)[i];
+    if (t.q8) {
+      m[k] = decode_m(static_cast<const signed char*>(t.m)[i], ms);
+      v[k] = decode_root(static_cast<const unsigned char*>(t.v)[i], vs);
+      v[k] = __fmul_rn(v[k], v[k]);
+    } else {
+      m[k] = static_cast<const float*>(t.m)[i];
+      v[k] = static_cast<const float*>(t.v)[i];
+    }
+    update(h, st, keep, g, p, m[k], v[k], r[k]);
+    if (t.master) t.master[i] = p;
+    if (t.p16)
+      static_cast<__nv_bfloat16*>(t.param)[i] = __float2bfloat16_rn(p);
+    else
+      static_cast<float*>(t.param)[i] = p;
+    if (!t.q8) {
+      static_cast<float*>(t.m)[i] = m[k];
+      static_cast<float*>(t.v)[i] = v[k];
+    }
+  }
+  if (!t.q8) return;
+  __syncwarp();  // every lane has read the old scales
+  float inv_m, inv_v;
+  new_scales(t, blk, lane, m, r, &inv_m, &inv_v);
+#pragma unroll
+  for (int k = 0; k < kPer; ++k) {
+    const long long i = base + lane + 32 * k;
+    if (i >= t.count) continue;
+    static_cast<signed char*>(t.m)[i] = encode_m(m[k], inv_m);
+    static_cast<unsigned char*>(t.v)[i] = encode_v(v[k], r[k], inv_v);
+  }
+}
+
+template <bool G16, bool Q8, bool VEC>
+__device__ __forceinline__ void by_param(const Entry& t, long long base, int lane,
+                                         const AdamScalars& h, const Step& st) {
+  if (!t.p16)
+    whole_block<0, G16, Q8, VEC>(t, base, lane, h, st);
+  else if (t.master)
+    whole_block<1, G16, Q8, VEC>(t, base, lane, h, st);
+  else
+    whole_block<2, G16, Q8, VEC>(t, base, lane, h, st);
+}
+
 template <typename TB>
 __global__ void __launch_bounds__(kThreads)
     adamw_kernel(const __grid_constant__ TB tb, const __grid_constant__ AdamScalars h) {
   pdl_wait();
-  const float gs = h.grad_scale ? *h.grad_scale : 1.f;
-  float lr = h.lr, root2 = h.root2, step = h.step;
-  if (h.schedule) {
-    lr = h.schedule[0];
-    step = __fdiv_rn(lr, h.schedule[1]);
-    root2 = __frcp_rn(__fsqrt_rn(h.schedule[2]));
-  }
+  const Step st = make_step(h);
   const unsigned chunks = tb.first[tb.count];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  if (isfinite(gs))
-    for (unsigned c = blockIdx.x; c < chunks; c += gridDim.x) {
-      const Entry& t = tb.t[find(tb, c)];
-      const long long base =
-          (long long)(c - tb.first[&t - tb.t]) * kChunk + warp * DC_STATE_BLOCK;
-      const long long left = t.count - base;
-      if (left <= 0) continue;
-      const float keep = __fsub_rn(1.f, __fmul_rn(lr, t.decay));
-      float p[kPer], g[kPer], m[kPer], r[kPer], v[kPer];
-      const long long blk = base / DC_STATE_BLOCK;
-      float ms = 0.f, vs = 0.f;
-      if (t.q8) ms = t.m_scale[blk], vs = t.v_scale[blk];
-#pragma unroll
-      for (int k = 0; k < kPer; ++k) {
-        const long long i = base + lane + 32 * k;
-        p[k] = g[k] = m[k] = v[k] = 0.f;
-        if (lane + 32 * k >= left) continue;
-        g[k] = t.g16 ? to_f(static_cast<const __nv_bfloat16*>(t.grad)[i])
-                     : static_cast<const float*>(t.grad)[i];
-        p[k] = t.master ? t.master[i]
-               : t.p16  ? to_f(static_cast<const __nv_bfloat16*>(t.param)[i])
-                        : static_cast<const float*>(t.param)[i];
-        if (t.q8) {
-          m[k] = decode_m(static_cast<const signed char*>(t.m)[i], ms);
-          v[k] = decode_root(static_cast<const unsigned char*>(t.v)[i], vs);
-          v[k] = __fmul_rn(v[k], v[k]);
-        } else {
-          m[k] = static_cast<const float*>(t.m)[i];
-          v[k] = static_cast<const float*>(t.v)[i];
-        }
-      }
-      float mtop = 0.f, rtop = 0.f;
-#pragma unroll
-      for (int k = 0; k < kPer; ++k) {
-        if (h.grad_scale) g[k] = __fmul_rn(g[k], gs);
-        m[k] = __fadd_rn(__fmul_rn(m[k], h.b1), __fmul_rn(g[k], h.omb1));
-        v[k] = __fadd_rn(__fmul_rn(v[k], h.b2), __fmul_rn(__fmul_rn(g[k], g[k]), h.omb2));
-        r[k] = __fsqrt_rn(v[k]);
-        const float u = __fdiv_rn(m[k], __fadd_rn(__fmul_rn(r[k], root2), h.eps));
-        p[k] = __fsub_rn(__fmul_rn(p[k], keep), __fmul_rn(u, step));
-        mtop = __uint_as_float(umax(__float_as_uint(mtop), __float_as_uint(fabsf(m[k]))));
-        rtop = __uint_as_float(umax(__float_as_uint(rtop), __float_as_uint(r[k])));
-      }
-      float inv_m = 0.f, inv_v = 0.f;
-      if (t.q8) {
-        block_scale(warp_max(mtop), &ms, &inv_m);
-        block_scale(warp_max(rtop), &vs, &inv_v);
-        if (lane == 0) t.m_scale[blk] = ms, t.v_scale[blk] = vs;
-      }
-#pragma unroll
-      for (int k = 0; k < kPer; ++k) {
-        const long long i = base + lane + 32 * k;
-        if (lane + 32 * k >= left) continue;
-        if (t.master) t.master[i] = p[k];
-        if (t.p16)
-          static_cast<__nv_bfloat16*>(t.param)[i] = __float2bfloat16_rn(p[k]);
-        else
-          static_cast<float*>(t.param)[i] = p[k];
-        if (t.q8) {
-          static_cast<signed char*>(t.m)[i] = encode_m(m[k], inv_m);
-          static_cast<unsigned char*>(t.v)[i] = encode_v(v[k], r[k], inv_v);
-        } else {
-          static_cast<float*>(t.m)[i] = m[k];
-          static_cast<float*>(t.v)[i] = v[k];
-        }
-      }
+  for (unsigned c = blockIdx.x; c < chunks; c += gridDim.x) {
+    const int ti = find(tb, c);
+    const Entry& t = tb.t[ti];
+    const long long base =
+        (long long)(c - tb.first[ti]) * kChunk + warp * DC_STATE_BLOCK - t.lead;
+    if (base >= t.count) continue;
+    if (base < 0 || base + DC_STATE_BLOCK > t.count) {
+      part_block(t, base, lane, h, st);
+      continue;
     }
+    switch ((t.g16 ? 4 : 0) | (t.q8 ? 2 : 0) | (t.vec ? 1 : 0)) {
+      case 0: by_param<false, false, false>(t, base, lane, h, st); break;
+      case 1: by_param<false, false, true>(t, base, lane, h, st); break;
+      case 2: by_param<false, true, false>(t, base, lane, h, st); break;
+      case 3: by_param<false, true, true>(t, base, lane, h, st); break;
+      case 4: by_param<true, false, false>(t, base, lane, h, st); break;
+      case 5: by_param<true, false, true>(t, base, lane, h, st); break;
+      case 6: by_param<true, true, false>(t, base, lane, h, st); break;
+      case 7: by_param<true, true, true>(t, base, lane, h, st); break;
+    }
+  }
   pdl_release();
 }
 
 // The states as float32: Entry::param receives m, Entry::master v (either null).
+template <bool Q8, bool VEC>
+__device__ __forceinline__ void whole_values(const Entry& t, long long base, int lane) {
+  float* mo = static_cast<float*>(t.param);
+  float m[kPer], v[kPer];
+  if (Q8) {
+    signed char cm[kPer];
+    unsigned char cv[kPer];
+    load8<VEC>(static_cast<const signed char*>(t.m) + base, lane, cm);
+    load8<VEC>(static_cast<const unsigned char*>(t.v) + base, lane, cv);
+    const float ms = t.m_scale[base / DC_STATE_BLOCK], vs = t.v_scale[base / DC_STATE_BLOCK];
+#pragma unroll
+    for (int k = 0; k < kPer; ++k) {
+      m[k] = decode_m(cm[k], ms);
+      v[k] = decode_root(cv[k], vs);
+      v[k] = __fmul_rn(v[k], v[k]);
+    }
+  } else {
+    load8<VEC>(static_cast<const float*>(t.m) + base, lane, m);
+    load8<VEC>(static_cast<const float*>(t.v) + base, lane, v);
+  }
+  if (mo) store8<VEC>(mo + base, lane, m);
+  if (t.master) store8<VEC>(t.master + base, lane, v);
+}
+
 template <typename TB>
 __global__ void __launch_bounds__(kThreads) values_kernel(const __grid_constant__ TB tb) {
   pdl_wait();
   const unsigned chunks = tb.first[tb.count];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   for (unsigned c = blockIdx.x; c < chunks; c += gridDim.x) {
-    const Entry& t = tb.t[find(tb, c)];
-    const long long base = (long long)(c - tb.first[&t - tb.t]) * kChunk + warp * DC_STATE_BLOCK;
-    const long long blk = base / DC_STATE_BLOCK;
-    const long long left = t.count - base;
-    if (left <= 0) continue;
+    const int ti = find(tb, c);
+    const Entry& t = tb.t[ti];
+    const long long base =
+        (long long)(c - tb.first[ti]) * kChunk + warp * DC_STATE_BLOCK - t.lead;
+    if (base >= t.count) continue;
+    if (base >= 0 && base + DC_STATE_BLOCK <= t.count) {
+      if (t.q8)
+        t.vec ? whole_values<true, true>(t, base, lane) : whole_values<true, false>(t, base, lane);
+      else
+        t.vec ? whole_values<false, true>(t, base, lane) : whole_values<false, false>(t, base, lane);
+      continue;
+    }
     float* mo = static_cast<float*>(t.param);
     float ms = 0.f, vs = 0.f;
-    if (t.q8) ms = t.m_scale[blk], vs = t.v_scale[blk];
-#pragma unroll
+    if (t.q8) ms = t.m_scale[base / DC_STATE_BLOCK], vs = t.v_scale[base / DC_STATE_BLOCK];
     for (int k = 0; k < kPer; ++k) {
       const long long i = base + lane + 32 * k;
-      if (lane + 32 * k >= left) continue;
+      if (i < 0 || i >= t.count) continue;
       if (t.q8) {
         const float root = decode_root(static_cast<const unsigned char*>(t.v)[i], vs);
         if (mo) mo[i] = decode_m(static_cast<const signed char*>(t.m)[i], ms);
@@ -210,27 +458,45 @@ __device__ __forceinline__ float block_sum(float v) {
   return v;
 }
 
-// part[block] = sum of squares of the block's chunks.
+// part[block] = sum of squares of the block's chunks (eight running sums a
+// thread: the loads do not wait for one another).
 template <typename TB>
 __global__ void __launch_bounds__(kThreads)
     squares_kernel(const __grid_constant__ TB tb, float* part) {
   pdl_wait();
   const unsigned chunks = tb.first[tb.count];
-  float sum = 0.f;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  float sum[kPer] = {};
   for (unsigned c = blockIdx.x; c < chunks; c += gridDim.x) {
-    const Entry& t = tb.t[find(tb, c)];
-    const long long base = (long long)(c - tb.first[&t - tb.t]) * kChunk + threadIdx.x;
+    const int ti = find(tb, c);
+    const Entry& t = tb.t[ti];
+    const long long base =
+        (long long)(c - tb.first[ti]) * kChunk + warp * DC_STATE_BLOCK - t.lead;
+    if (base >= t.count) continue;
+    float g[kPer];
+    if (base >= 0 && base + DC_STATE_BLOCK <= t.count) {
+      if (t.g16) {
+        const __nv_bfloat16* p = static_cast<const __nv_bfloat16*>(t.grad) + base;
+        t.vec ? load8<true>(p, lane, g) : load8<false>(p, lane, g);
+      } else {
+        const float* p = static_cast<const float*>(t.grad) + base;
+        t.vec ? load8<true>(p, lane, g) : load8<false>(p, lane, g);
+      }
+    } else {
 #pragma unroll
-    for (int k = 0; k < kPer; ++k) {
-      const long long i = base + kThreads * k;
-      if (i >= t.count) continue;
-      const float g = t.g16 ? to_f(static_cast<const __nv_bfloat16*>(t.grad)[i])
-                            : static_cast<const float*>(t.grad)[i];
-      sum = fmaf(g, g, sum);
+      for (int k = 0; k < kPer; ++k) {
+        const long long i = base + lane + 32 * k;
+        g[k] = i < 0 || i >= t.count ? 0.f
+               : t.g16               ? to_f(static_cast<const __nv_bfloat16*>(t.grad)[i])
+                                     : static_cast<const float*>(t.grad)[i];
+      }
     }
+#pragma unroll
+    for (int k = 0; k < kPer; ++k) sum[k] = fmaf(g[k], g[k], sum[k]);
   }
-  sum = block_sum(sum);
-  if (threadIdx.x == 0) part[blockIdx.x] = sum;
+  const float all = block_sum(((sum[0] + sum[1]) + (sum[2] + sum[3])) +
+                              ((sum[4] + sum[5]) + (sum[6] + sum[7])));
+  if (threadIdx.x == 0) part[blockIdx.x] = all;
   pdl_release();
 }
 
@@ -276,20 +542,59 @@ cudaError_t launch(K kern, unsigned grid, int threads, cudaStream_t s, const A&.
   return e;
 }
 
-// The tensors of one launch; false if their chunks do not fit in 32 bits.
+// Elements from an address back to the last boundary of four of them.
+int lead_of(const void* p, int size) { return (int)((uintptr_t)p / size % 4); }
+
+// lead and vec of a tensor whose arrays are the given ones (null: not read):
+// arrays that all sit the same distance past a boundary of four elements are
+// read from there; 8-bit blocks start with the tensor, so they need it at 0.
+struct Array {
+  const void* p;
+  int size;
+};
 template <int N>
-bool fill(Table<N>* tb, const dc_adamw_tensor* t, int count) {
+void set_grid(Entry* e, const Array (&arrays)[N]) {
+  int lead = -1;
+  bool same = true;
+  for (const Array& a : arrays) {
+    if (!a.p) continue;
+    const int l = lead_of(a.p, a.size);
+    if (lead < 0) lead = l;
+    same &= l == lead;
+  }
+  e->vec = same && (!e->q8 || lead <= 0);
+  e->lead = (unsigned char)(e->vec && lead > 0 ? lead : 0);
+}
+
+enum class Use { kStep, kValues, kGrad };
+
+// The tensors of one launch; false if their chunks do not fit in 32 bits.
+// Values go to m[i] and v[i].
+template <int N>
+bool fill(Table<N>* tb, const dc_adamw_tensor* t, int count, Use use, float* const* m,
+          float* const* v) {
   unsigned long long at = 0;
   tb->count = count;
   for (int i = 0; i < count; ++i) {
+    Entry& e = tb->t[i];
+    e = Entry{t[i].param, t[i].master, t[i].grad, t[i].m, t[i].v, t[i].m_scale, t[i].v_scale,
+              t[i].count, t[i].weight_decay};
+    e.p16 = t[i].param_dtype == DC_BF16;
+    e.g16 = t[i].grad_dtype == DC_BF16;
+    e.q8 = use != Use::kGrad && t[i].state == DC_STATE_Q8;
+    const int st = e.q8 ? 1 : 4, gr = e.g16 ? 2 : 4;
+    if (use == Use::kValues) {
+      e.param = m ? m[i] : nullptr;
+      e.master = v ? v[i] : nullptr;
+      set_grid(&e, {{e.m, st}, {e.v, st}, {e.param, 4}, {e.master, 4}});
+    } else if (use == Use::kGrad) {
+      set_grid(&e, {{e.grad, gr}});
+    } else {
+      set_grid(&e, {{e.param, e.p16 ? 2 : 4}, {e.master, 4}, {e.grad, gr}, {e.m, st}, {e.v, st}});
+    }
     tb->first[i] = (unsigned)at;
-    at += (unsigned long long)ceil_div_ll(t[i].count, kChunk);
-    if (at > UINT_MAX) return false;
-    tb->t[i] = Entry{t[i].param,   t[i].master,  t[i].grad,
-                     t[i].m,       t[i].v,       t[i].m_scale,
-                     t[i].v_scale, t[i].count,   t[i].weight_decay,
-                     t[i].param_dtype == DC_BF16, t[i].grad_dtype == DC_BF16,
-                     t[i].state == DC_STATE_Q8};
+    if (e.count) at += (unsigned long long)ceil_div_ll(e.count + e.lead, kChunk);
+    if (at > UINT_MAX / 2) return false;
   }
   tb->first[count] = (unsigned)at;
   return true;
@@ -299,13 +604,14 @@ constexpr int kFew = 40;  // a table that fits in the first 4 KB of a launch's a
 
 // f(table) with a table of the tensors, a small one where they are few.
 template <typename F>
-cudaError_t with_table(const dc_adamw_tensor* t, int count, F&& f) {
+cudaError_t with_table(const dc_adamw_tensor* t, int count, Use use, float* const* m,
+                       float* const* v, F&& f) {
   if (count <= kFew) {
     Table<kFew> tb;
-    return fill(&tb, t, count) ? f(tb) : cudaErrorInvalidValue;
+    return fill(&tb, t, count, use, m, v) ? f(tb) : cudaErrorInvalidValue;
   }
   Table<kAdamTensors> tb;
-  return fill(&tb, t, count) ? f(tb) : cudaErrorInvalidValue;
+  return fill(&tb, t, count, use, m, v) ? f(tb) : cudaErrorInvalidValue;
 }
 
 unsigned grid_of(unsigned chunks, int per_sm) {
@@ -318,7 +624,7 @@ unsigned grid_of(unsigned chunks, int per_sm) {
 
 cudaError_t launch_adamw(const dc_adamw_tensor* t, int count, const AdamScalars& h,
                          cudaStream_t s) {
-  return with_table(t, count, [&](const auto& tb) {
+  return with_table(t, count, Use::kStep, nullptr, nullptr, [&](const auto& tb) {
     const unsigned grid = grid_of(tb.first[tb.count], 8);
     if (!grid) return cudaSuccess;
     return launch(adamw_kernel<std::decay_t<decltype(tb)>>, grid, kThreads, s, tb, h);
@@ -327,11 +633,7 @@ cudaError_t launch_adamw(const dc_adamw_tensor* t, int count, const AdamScalars&
 
 cudaError_t launch_adamw_values(const dc_adamw_tensor* t, int count, float* const* m,
                                 float* const* v, cudaStream_t s) {
-  return with_table(t, count, [&](auto& tb) {
-    for (int i = 0; i < count; ++i) {
-      tb.t[i].param = m ? m[i] : nullptr;
-      tb.t[i].master = v ? v[i] : nullptr;
-    }
+  return with_table(t, count, Use::kValues, m, v, [&](const auto& tb) {
     const unsigned grid = grid_of(tb.first[tb.count], 8);
     if (!grid) return cudaSuccess;
     return launch(values_kernel<std::decay_t<decltype(tb)>>, grid, kThreads, s, tb);
@@ -341,7 +643,7 @@ cudaError_t launch_adamw_values(const dc_adamw_tensor* t, int count, float* cons
 // part: kNormParts floats, all written.
 cudaError_t launch_grad_squares(const dc_adamw_tensor* t, int count, float* part,
                                 cudaStream_t s) {
-  return with_table(t, count, [&](const auto& tb) {
+  return with_table(t, count, Use::kGrad, nullptr, nullptr, [&](const auto& tb) {
     return launch(squares_kernel<std::decay_t<decltype(tb)>>, (unsigned)kNormParts, kThreads, s,
                   tb, part);
   });

@@ -388,7 +388,7 @@ struct AdamScalars {
   const float* schedule;    // may be null
 };
 // tensors: checked by the ABI layer; at most kAdamTensors (a launch's table).
-constexpr int kAdamTensors = 400;
+constexpr int kAdamTensors = 384;
 cudaError_t launch_adamw(const dc_adamw_tensor* t, int count, const AdamScalars& h, cudaStream_t s);
 cudaError_t launch_adamw_values(const dc_adamw_tensor* t, int count, float* const* m,
                                 float* const* v, cudaStream_t s);

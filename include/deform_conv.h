@@ -427,7 +427,7 @@ typedef struct {
  * A bf16 param without a master is updated from its rounded value and rounded
  * to nearest even.  A gradient that is not finite makes its element's state
  * and parameter so, or its whole block's state where that is in 8 bits.
- * Any number of tensors (one launch per 400).  Errors: DC_ERR_INVALID_ARG for
+ * Any number of tensors (one launch per 384).  Errors: DC_ERR_INVALID_ARG for
  * NULL pointers, negative counts or hyper-parameters out of range,
  * DC_ERR_UNSUPPORTED for a pointer without its element's alignment. */
 dc_status dc_adamw_step(const dc_adamw_tensor* tensors, int count, const dc_adamw_hyper* hyper,

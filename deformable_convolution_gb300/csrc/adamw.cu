@@ -68,21 +68,36 @@ __device__ __forceinline__ void block_scale(float top, float* scale, float* inv)
   *inv = *scale > 0.f ? __frcp_rn(*scale) : 0.f;
 }
 
-__device__ __forceinline__ float decode_m(signed char q, float s) {
-  const float t = __fmul_rn((float)q, 1.f / 127.f);
+// Codes to floats and back without the conversion instructions (a sixteenth of
+// the multiplier's rate): a small integer added to 1.5 * 2^23 sits in the low
+// bits of the sum, rounded to nearest even by the addition itself.
+constexpr float kMagic = 12582912.f;  // 1.5 * 2^23
+// byte e of a word of four codes, as float
+__device__ __forceinline__ float code_u(uint32_t w, int e) {
+  return __fadd_rn(__uint_as_float(__byte_perm(w, 0x4b400000u, 0x7650 | e)), -kMagic);
+}
+// signed codes: w with every byte's top bit flipped
+__device__ __forceinline__ float code_s(uint32_t w, int e) {
+  return __fadd_rn(__uint_as_float(__byte_perm(w, 0x4b400000u, 0x7650 | e)), -(kMagic + 128.f));
+}
+
+__device__ __forceinline__ float decode_m(float q, float s) {
+  const float t = __fmul_rn(q, 1.f / 127.f);
   return __fmul_rn(__fmul_rn(t, fabsf(t)), s);
 }
-__device__ __forceinline__ float decode_root(unsigned char q, float s) {
-  const float t = __fmul_rn((float)q, 1.f / 255.f);
+__device__ __forceinline__ float decode_root(float q, float s) {
+  const float t = __fmul_rn(q, 1.f / 255.f);
   return __fmul_rn(__fmul_rn(t, t), s);
 }
-__device__ __forceinline__ signed char encode_m(float m, float inv) {
-  const int q = __float2int_rn(__fmul_rn(__fsqrt_rn(__fmul_rn(fabsf(m), inv)), 127.f));
-  return (signed char)(m < 0.f ? -q : q);
+// The code is the low byte.
+__device__ __forceinline__ uint32_t encode_m(float m, float inv) {
+  const float q = __fmul_rn(__fsqrt_rn(__fmul_rn(fabsf(m), inv)), 127.f);
+  return __float_as_uint(__fadd_rn(copysignf(q, m), kMagic));
 }
-__device__ __forceinline__ unsigned char encode_v(float v, float root, float inv) {
-  const int q = __float2int_rn(__fmul_rn(__fsqrt_rn(__fmul_rn(root, inv)), 255.f));
-  return (unsigned char)(v > 0.f && q < 1 && inv > 0.f ? 1 : q);
+// low: 1, or 0 in a block that counts as zero
+__device__ __forceinline__ uint32_t encode_v(float v, float root, float inv, float low) {
+  const float q = __fmul_rn(__fsqrt_rn(__fmul_rn(root, inv)), 255.f);
+  return __float_as_uint(__fadd_rn(fmaxf(q, v > 0.f ? low : 0.f), kMagic));
 }
 
 // ---------------------------------------------------------------- element access
@@ -123,18 +138,18 @@ __device__ __forceinline__ void load8(const __nv_bfloat16* p, int lane, float* f
     for (int k = 0; k < kPer; ++k) f[k] = to_f(p[lane + 32 * k]);
   }
 }
-template <bool VEC, typename C>
-__device__ __forceinline__ void load8(const C* p, int lane, C* c) {
-  if (VEC) {
+// codes: four to a word
+template <bool VEC>
+__device__ __forceinline__ void load8(const unsigned char* p, int lane, uint32_t* w) {
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const uint32_t v = *reinterpret_cast<const uint32_t*>(p + h * 128 + lane * 4);
+  for (int h = 0; h < 2; ++h) {
+    if (VEC) {
+      w[h] = *reinterpret_cast<const uint32_t*>(p + h * 128 + lane * 4);
+    } else {
+      w[h] = 0;
 #pragma unroll
-      for (int e = 0; e < 4; ++e) c[4 * h + e] = (C)(v >> (8 * e));
+      for (int e = 0; e < 4; ++e) w[h] |= (uint32_t)p[lane + 32 * (4 * h + e)] << (8 * e);
     }
-  } else {
-#pragma unroll
-    for (int k = 0; k < kPer; ++k) c[k] = p[lane + 32 * k];
   }
 }
 
@@ -165,19 +180,18 @@ __device__ __forceinline__ void store8(__nv_bfloat16* p, int lane, const float* 
     for (int k = 0; k < kPer; ++k) p[lane + 32 * k] = __float2bfloat16_rn(f[k]);
   }
 }
-template <bool VEC, typename C>
-__device__ __forceinline__ void store8(C* p, int lane, const C* c) {
+// codes in the low bytes of q
+template <bool VEC>
+__device__ __forceinline__ void store8(unsigned char* p, int lane, const uint32_t* q) {
   if (VEC) {
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      uint32_t v = 0;
-#pragma unroll
-      for (int e = 0; e < 4; ++e) v |= (uint32_t)(unsigned char)c[4 * h + e] << (8 * e);
-      *reinterpret_cast<uint32_t*>(p + h * 128 + lane * 4) = v;
-    }
+    for (int h = 0; h < 2; ++h)
+      *reinterpret_cast<uint32_t*>(p + h * 128 + lane * 4) =
+          __byte_perm(__byte_perm(q[4 * h], q[4 * h + 1], 0x0040),
+                      __byte_perm(q[4 * h + 2], q[4 * h + 3], 0x0040), 0x5410);
   } else {
 #pragma unroll
-    for (int k = 0; k < kPer; ++k) p[lane + 32 * k] = c[k];
+    for (int k = 0; k < kPer; ++k) p[lane + 32 * k] = (unsigned char)q[k];
   }
 }
 
@@ -237,8 +251,7 @@ template <int PARAM, bool G16, bool Q8, bool VEC>
 __device__ __forceinline__ void whole_block(const Entry& t, long long base, int lane,
                                             const AdamScalars& h, const Step& st) {
   float p[kPer], g[kPer], m[kPer], v[kPer], r[kPer];
-  signed char cm[kPer];
-  unsigned char cv[kPer];
+  uint32_t cm[2], cv[2];
   const long long blk = base / DC_STATE_BLOCK;
   float ms = 0.f, vs = 0.f;
   if (G16)
@@ -246,7 +259,7 @@ __device__ __forceinline__ void whole_block(const Entry& t, long long base, int 
   else
     load8<VEC>(static_cast<const float*>(t.grad) + base, lane, g);
   if (Q8) {
-    load8<VEC>(static_cast<const signed char*>(t.m) + base, lane, cm);
+    load8<VEC>(static_cast<const unsigned char*>(t.m) + base, lane, cm);
     load8<VEC>(static_cast<const unsigned char*>(t.v) + base, lane, cv);
     ms = t.m_scale[blk], vs = t.v_scale[blk];
   } else {
@@ -264,8 +277,8 @@ __device__ __forceinline__ void whole_block(const Entry& t, long long base, int 
 #pragma unroll
   for (int k = 0; k < kPer; ++k) {
     if (Q8) {
-      m[k] = decode_m(cm[k], ms);
-      v[k] = decode_root(cv[k], vs);
+      m[k] = decode_m(code_s(cm[k >> 2] ^ 0x80808080u, k & 3), ms);
+      v[k] = decode_root(code_u(cv[k >> 2], k & 3), vs);
       v[k] = __fmul_rn(v[k], v[k]);
     }
     update(h, st, keep, g[k], p[k], m[k], v[k], r[k]);
@@ -278,13 +291,15 @@ __device__ __forceinline__ void whole_block(const Entry& t, long long base, int 
   if (Q8) {
     float inv_m, inv_v;
     new_scales(t, blk, lane, m, r, &inv_m, &inv_v);
+    const float low = inv_v > 0.f ? 1.f : 0.f;
+    uint32_t qm[kPer], qv[kPer];
 #pragma unroll
     for (int k = 0; k < kPer; ++k) {
-      cm[k] = encode_m(m[k], inv_m);
-      cv[k] = encode_v(v[k], r[k], inv_v);
+      qm[k] = encode_m(m[k], inv_m);
+      qv[k] = encode_v(v[k], r[k], inv_v, low);
     }
-    store8<VEC>(static_cast<signed char*>(t.m) + base, lane, cm);
-    store8<VEC>(static_cast<unsigned char*>(t.v) + base, lane, cv);
+    store8<VEC>(static_cast<unsigned char*>(t.m) + base, lane, qm);
+    store8<VEC>(static_cast<unsigned char*>(t.v) + base, lane, qv);
   } else {
     store8<VEC>(static_cast<float*>(t.m) + base, lane, m);
     store8<VEC>(static_cast<float*>(t.v) + base, lane, v);
@@ -311,8 +326,8 @@ __device__ __noinline__ void part_block(const Entry& t, long long base, int lane
               : t.p16  ? to_f(static_cast<const __nv_bfloat16*>(t.param)[i])
                        : static_cast<const float*>(t.param)[i];
     if (t.q8) {
-      m[k] = decode_m(static_cast<const signed char*>(t.m)[i], ms);
-      v[k] = decode_root(static_cast<const unsigned char*>(t.v)[i], vs);
+      m[k] = decode_m((float)static_cast<const signed char*>(t.m)[i], ms);
+      v[k] = decode_root((float)static_cast<const unsigned char*>(t.v)[i], vs);
       v[k] = __fmul_rn(v[k], v[k]);
     } else {
       m[k] = static_cast<const float*>(t.m)[i];
@@ -337,8 +352,9 @@ __device__ __noinline__ void part_block(const Entry& t, long long base, int lane
   for (int k = 0; k < kPer; ++k) {
     const long long i = base + lane + 32 * k;
     if (i >= t.count) continue;
-    static_cast<signed char*>(t.m)[i] = encode_m(m[k], inv_m);
-    static_cast<unsigned char*>(t.v)[i] = encode_v(v[k], r[k], inv_v);
+    static_cast<unsigned char*>(t.m)[i] = (unsigned char)encode_m(m[k], inv_m);
+    static_cast<unsigned char*>(t.v)[i] =
+        (unsigned char)encode_v(v[k], r[k], inv_v, inv_v > 0.f ? 1.f : 0.f);
   }
 }
 
@@ -390,15 +406,14 @@ __device__ __forceinline__ void whole_values(const Entry& t, long long base, int
   float* mo = static_cast<float*>(t.param);
   float m[kPer], v[kPer];
   if (Q8) {
-    signed char cm[kPer];
-    unsigned char cv[kPer];
-    load8<VEC>(static_cast<const signed char*>(t.m) + base, lane, cm);
+    uint32_t cm[2], cv[2];
+    load8<VEC>(static_cast<const unsigned char*>(t.m) + base, lane, cm);
     load8<VEC>(static_cast<const unsigned char*>(t.v) + base, lane, cv);
     const float ms = t.m_scale[base / DC_STATE_BLOCK], vs = t.v_scale[base / DC_STATE_BLOCK];
 #pragma unroll
     for (int k = 0; k < kPer; ++k) {
-      m[k] = decode_m(cm[k], ms);
-      v[k] = decode_root(cv[k], vs);
+      m[k] = decode_m(code_s(cm[k >> 2] ^ 0x80808080u, k & 3), ms);
+      v[k] = decode_root(code_u(cv[k >> 2], k & 3), vs);
       v[k] = __fmul_rn(v[k], v[k]);
     }
   } else {
@@ -434,8 +449,8 @@ __global__ void __launch_bounds__(kThreads) values_kernel(const __grid_constant_
       const long long i = base + lane + 32 * k;
       if (i < 0 || i >= t.count) continue;
       if (t.q8) {
-        const float root = decode_root(static_cast<const unsigned char*>(t.v)[i], vs);
-        if (mo) mo[i] = decode_m(static_cast<const signed char*>(t.m)[i], ms);
+        const float root = decode_root((float)static_cast<const unsigned char*>(t.v)[i], vs);
+        if (mo) mo[i] = decode_m((float)static_cast<const signed char*>(t.m)[i], ms);
         if (t.master) t.master[i] = __fmul_rn(root, root);
       } else {
         if (mo) mo[i] = static_cast<const float*>(t.m)[i];
@@ -458,9 +473,9 @@ __device__ __forceinline__ float block_sum(float v) {
   return v;
 }
 
-// part[block] = sum of squares of the block's chunks (eight running sums a
-// thread: the loads do not wait for one another).
-template <typename TB>
+// part[block] = sum of squares of the block's chunks.  A chunk is B batches of
+// kChunk elements whose loads are all under way before the first is used.
+template <int B, typename TB>
 __global__ void __launch_bounds__(kThreads)
     squares_kernel(const __grid_constant__ TB tb, float* part) {
   pdl_wait();
@@ -471,28 +486,55 @@ __global__ void __launch_bounds__(kThreads)
     const int ti = find(tb, c);
     const Entry& t = tb.t[ti];
     const long long base =
-        (long long)(c - tb.first[ti]) * kChunk + warp * DC_STATE_BLOCK - t.lead;
-    if (base >= t.count) continue;
-    float g[kPer];
-    if (base >= 0 && base + DC_STATE_BLOCK <= t.count) {
+        (long long)(c - tb.first[ti]) * (B * kChunk) + warp * DC_STATE_BLOCK - t.lead;
+    if (t.vec && base >= 0 && base + (B - 1) * kChunk + DC_STATE_BLOCK <= t.count) {
       if (t.g16) {
         const __nv_bfloat16* p = static_cast<const __nv_bfloat16*>(t.grad) + base;
-        t.vec ? load8<true>(p, lane, g) : load8<false>(p, lane, g);
+        uint2 w[2 * B];
+#pragma unroll
+        for (int b = 0; b < 2 * B; ++b)
+          w[b] = *reinterpret_cast<const uint2*>(p + (b >> 1) * kChunk + (b & 1) * 128 + lane * 4);
+#pragma unroll
+        for (int b = 0; b < 2 * B; ++b) {
+          const float f[4] = {__uint_as_float(w[b].x << 16), __uint_as_float(w[b].x & 0xffff0000u),
+                              __uint_as_float(w[b].y << 16), __uint_as_float(w[b].y & 0xffff0000u)};
+#pragma unroll
+          for (int e = 0; e < 4; ++e) sum[4 * (b & 1) + e] = fmaf(f[e], f[e], sum[4 * (b & 1) + e]);
+        }
       } else {
         const float* p = static_cast<const float*>(t.grad) + base;
-        t.vec ? load8<true>(p, lane, g) : load8<false>(p, lane, g);
-      }
-    } else {
+        float f[B][kPer];
 #pragma unroll
-      for (int k = 0; k < kPer; ++k) {
-        const long long i = base + lane + 32 * k;
-        g[k] = i < 0 || i >= t.count ? 0.f
-               : t.g16               ? to_f(static_cast<const __nv_bfloat16*>(t.grad)[i])
-                                     : static_cast<const float*>(t.grad)[i];
+        for (int b = 0; b < B; ++b) load8<true>(p + b * kChunk, lane, f[b]);
+#pragma unroll
+        for (int b = 0; b < B; ++b)
+#pragma unroll
+          for (int k = 0; k < kPer; ++k) sum[k] = fmaf(f[b][k], f[b][k], sum[k]);
       }
+      continue;
     }
+    // a chunk over an end of its tensor: by batches, whole ones as above
+#pragma unroll 1
+    for (int b = 0; b < B; ++b) {
+      const long long at = base + b * kChunk;
+      float f[kPer];
+      if (t.vec && at >= 0 && at + DC_STATE_BLOCK <= t.count) {
+        if (t.g16)
+          load8<true>(static_cast<const __nv_bfloat16*>(t.grad) + at, lane, f);
+        else
+          load8<true>(static_cast<const float*>(t.grad) + at, lane, f);
+      } else {
 #pragma unroll
-    for (int k = 0; k < kPer; ++k) sum[k] = fmaf(g[k], g[k], sum[k]);
+        for (int k = 0; k < kPer; ++k) {
+          const long long i = at + lane + 32 * k;
+          f[k] = i < 0 || i >= t.count ? 0.f
+                 : t.g16               ? to_f(static_cast<const __nv_bfloat16*>(t.grad)[i])
+                                       : static_cast<const float*>(t.grad)[i];
+        }
+      }
+#pragma unroll
+      for (int k = 0; k < kPer; ++k) sum[k] = fmaf(f[k], f[k], sum[k]);
+    }
   }
   const float all = block_sum(((sum[0] + sum[1]) + (sum[2] + sum[3])) +
                               ((sum[4] + sum[5]) + (sum[6] + sum[7])));
@@ -547,7 +589,7 @@ int lead_of(const void* p, int size) { return (int)((uintptr_t)p / size % 4); }
 
 // lead and vec of a tensor whose arrays are the given ones (null: not read):
 // arrays that all sit the same distance past a boundary of four elements are
-// read from there; 8-bit blocks start with the tensor, so they need it at 0.
+// read from there (vec); 8-bit blocks start with the tensor, so they need it at 0.
 struct Array {
   const void* p;
   int size;
@@ -571,8 +613,8 @@ enum class Use { kStep, kValues, kGrad };
 // The tensors of one launch; false if their chunks do not fit in 32 bits.
 // Values go to m[i] and v[i].
 template <int N>
-bool fill(Table<N>* tb, const dc_adamw_tensor* t, int count, Use use, float* const* m,
-          float* const* v) {
+bool fill(Table<N>* tb, const dc_adamw_tensor* t, int count, int chunk, Use use,
+          float* const* m, float* const* v) {
   unsigned long long at = 0;
   tb->count = count;
   for (int i = 0; i < count; ++i) {
@@ -593,7 +635,7 @@ bool fill(Table<N>* tb, const dc_adamw_tensor* t, int count, Use use, float* con
       set_grid(&e, {{e.param, e.p16 ? 2 : 4}, {e.master, 4}, {e.grad, gr}, {e.m, st}, {e.v, st}});
     }
     tb->first[i] = (unsigned)at;
-    if (e.count) at += (unsigned long long)ceil_div_ll(e.count + e.lead, kChunk);
+    if (e.count) at += (unsigned long long)ceil_div_ll(e.count + e.lead, chunk);
     if (at > UINT_MAX / 2) return false;
   }
   tb->first[count] = (unsigned)at;
@@ -604,14 +646,14 @@ constexpr int kFew = 40;  // a table that fits in the first 4 KB of a launch's a
 
 // f(table) with a table of the tensors, a small one where they are few.
 template <typename F>
-cudaError_t with_table(const dc_adamw_tensor* t, int count, Use use, float* const* m,
+cudaError_t with_table(const dc_adamw_tensor* t, int count, int chunk, Use use, float* const* m,
                        float* const* v, F&& f) {
   if (count <= kFew) {
     Table<kFew> tb;
-    return fill(&tb, t, count, use, m, v) ? f(tb) : cudaErrorInvalidValue;
+    return fill(&tb, t, count, chunk, use, m, v) ? f(tb) : cudaErrorInvalidValue;
   }
   Table<kAdamTensors> tb;
-  return fill(&tb, t, count, use, m, v) ? f(tb) : cudaErrorInvalidValue;
+  return fill(&tb, t, count, chunk, use, m, v) ? f(tb) : cudaErrorInvalidValue;
 }
 
 unsigned grid_of(unsigned chunks, int per_sm) {
@@ -624,7 +666,7 @@ unsigned grid_of(unsigned chunks, int per_sm) {
 
 cudaError_t launch_adamw(const dc_adamw_tensor* t, int count, const AdamScalars& h,
                          cudaStream_t s) {
-  return with_table(t, count, Use::kStep, nullptr, nullptr, [&](const auto& tb) {
+  return with_table(t, count, kChunk, Use::kStep, nullptr, nullptr, [&](const auto& tb) {
     const unsigned grid = grid_of(tb.first[tb.count], 8);
     if (!grid) return cudaSuccess;
     return launch(adamw_kernel<std::decay_t<decltype(tb)>>, grid, kThreads, s, tb, h);
@@ -633,19 +675,26 @@ cudaError_t launch_adamw(const dc_adamw_tensor* t, int count, const AdamScalars&
 
 cudaError_t launch_adamw_values(const dc_adamw_tensor* t, int count, float* const* m,
                                 float* const* v, cudaStream_t s) {
-  return with_table(t, count, Use::kValues, m, v, [&](const auto& tb) {
+  return with_table(t, count, kChunk, Use::kValues, m, v, [&](const auto& tb) {
     const unsigned grid = grid_of(tb.first[tb.count], 8);
     if (!grid) return cudaSuccess;
     return launch(values_kernel<std::decay_t<decltype(tb)>>, grid, kThreads, s, tb);
   });
 }
 
-// part: kNormParts floats, all written.
+// part: kNormParts floats, all written.  Chunks of four batches keep enough
+// loads in flight; few elements are spread over the blocks one batch at a time.
 cudaError_t launch_grad_squares(const dc_adamw_tensor* t, int count, float* part,
                                 cudaStream_t s) {
-  return with_table(t, count, Use::kGrad, nullptr, nullptr, [&](const auto& tb) {
-    return launch(squares_kernel<std::decay_t<decltype(tb)>>, (unsigned)kNormParts, kThreads, s,
-                  tb, part);
+  long long total = 0;
+  for (int i = 0; i < count; ++i) total += t[i].count;
+  const bool large = total > 4LL * kNormParts * kChunk;
+  return with_table(t, count, large ? 4 * kChunk : kChunk, Use::kGrad, nullptr, nullptr,
+                    [&](const auto& tb) {
+    using TB = std::decay_t<decltype(tb)>;
+    if (large)
+      return launch(squares_kernel<4, TB>, (unsigned)kNormParts, kThreads, s, tb, part);
+    return launch(squares_kernel<1, TB>, (unsigned)kNormParts, kThreads, s, tb, part);
   });
 }
 

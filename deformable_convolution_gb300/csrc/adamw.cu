@@ -7,9 +7,9 @@
 // consecutive elements; a chunk lies in one tensor, and holds whole blocks of
 // the 8-bit states, one to a warp.
 //
-// Every operation is rounded by itself (no contraction): an 8-bit code is a
-// rounded number, and a last-bit difference ahead of it would show as a whole
-// step of the code.
+// Every operation ahead of an 8-bit code is rounded by itself (no contraction):
+// a code is a rounded number, and a last-bit difference ahead of it would show
+// as a whole step.
 #include <float.h>
 
 #include "dc_common.cuh"
@@ -72,13 +72,10 @@ __device__ __forceinline__ void block_scale(float top, float* scale, float* inv)
 // the multiplier's rate): a small integer added to 1.5 * 2^23 sits in the low
 // bits of the sum, rounded to nearest even by the addition itself.
 constexpr float kMagic = 12582912.f;  // 1.5 * 2^23
-// byte e of a word of four codes, as float
-__device__ __forceinline__ float code_u(uint32_t w, int e) {
-  return __fadd_rn(__uint_as_float(__byte_perm(w, 0x4b400000u, 0x7650 | e)), -kMagic);
-}
-// signed codes: w with every byte's top bit flipped
-__device__ __forceinline__ float code_s(uint32_t w, int e) {
-  return __fadd_rn(__uint_as_float(__byte_perm(w, 0x4b400000u, 0x7650 | e)), -(kMagic + 128.f));
+// byte e of a word of four codes, as the float 1.5 * 2^23 + byte (for signed
+// codes the word's bytes come with their top bits flipped, 128 more)
+__device__ __forceinline__ float code_bits(uint32_t w, int e) {
+  return __uint_as_float(__byte_perm(w, 0x4b400000u, 0x7650 | e));
 }
 
 __device__ __forceinline__ float decode_m(float q, float s) {
@@ -89,15 +86,54 @@ __device__ __forceinline__ float decode_root(float q, float s) {
   const float t = __fmul_rn(q, 1.f / 255.f);
   return __fmul_rn(__fmul_rn(t, t), s);
 }
-// The code is the low byte.
-__device__ __forceinline__ uint32_t encode_m(float m, float inv) {
-  const float q = __fmul_rn(__fsqrt_rn(__fmul_rn(fabsf(m), inv)), 127.f);
-  return __float_as_uint(__fadd_rn(copysignf(q, m), kMagic));
+// The codes before rounding, from the root of m (or of r = sqrt(v)) over s.
+__device__ __forceinline__ float level_m(float root, float m) {
+  return copysignf(__fmul_rn(root, 127.f), m);
 }
-// low: 1, or 0 in a block that counts as zero
-__device__ __forceinline__ uint32_t encode_v(float v, float root, float inv, float low) {
-  const float q = __fmul_rn(__fsqrt_rn(__fmul_rn(root, inv)), 255.f);
-  return __float_as_uint(__fadd_rn(fmaxf(q, v > 0.f ? low : 0.f), kMagic));
+// At least `low` (1, or 0 in a block that counts as zero) where r > 0: a root
+// of a float32 is 0 or at least 2^-75.
+__device__ __forceinline__ float level_v(float root, float r, float low) {
+  return fmaxf(__fmul_rn(root, 255.f), fminf(r * 0x1p127f, low));
+}
+
+// Two floats in one instruction.  A product that goes into a packed sum may be
+// contracted with it: where that would matter the sum is taken apart.
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+  float2 d;
+  asm("{.reg .b64 ra, rb, rd;\n mov.b64 ra, {%2,%3};\n mov.b64 rb, {%4,%5};\n"
+      " mul.rn.f32x2 rd, ra, rb;\n mov.b64 {%0,%1}, rd;}"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return d;
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+  float2 d;
+  asm("{.reg .b64 ra, rb, rd;\n mov.b64 ra, {%2,%3};\n mov.b64 rb, {%4,%5};\n"
+      " add.rn.f32x2 rd, ra, rb;\n mov.b64 {%0,%1}, rd;}"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return d;
+}
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+  float2 d;
+  asm("{.reg .b64 ra, rb, rc, rd;\n mov.b64 ra, {%2,%3};\n mov.b64 rb, {%4,%5};\n"
+      " mov.b64 rc, {%6,%7};\n fma.rn.f32x2 rd, ra, rb, rc;\n mov.b64 {%0,%1}, rd;}"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+  return d;
+}
+__device__ __forceinline__ float2 both(float a) { return make_float2(a, a); }
+
+// One instruction each; a subnormal argument counts as 0.
+__device__ __forceinline__ float sqrt_approx(float x) {
+  float y;
+  asm("sqrt.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ float rcp_approx(float x) {
+  float y;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
 }
 
 // ---------------------------------------------------------------- element access
@@ -198,13 +234,12 @@ __device__ __forceinline__ void store8(unsigned char* p, int lane, const uint32_
 // ---------------------------------------------------------------- the step
 
 // The step's numbers, read once by each thread (gs and the schedule's from
-// device memory, behind the first block's loads).
+// device memory).
 struct Step {
   float gs, lr, root2, step;
-  bool scaled;
 };
 __device__ __forceinline__ Step make_step(const AdamScalars& h) {
-  Step st{1.f, h.lr, h.root2, h.step, h.grad_scale != nullptr};
+  Step st{1.f, h.lr, h.root2, h.step};
   if (h.grad_scale) st.gs = *h.grad_scale;
   if (h.schedule) {
     st.lr = h.schedule[0];
@@ -214,19 +249,26 @@ __device__ __forceinline__ Step make_step(const AdamScalars& h) {
   return st;
 }
 
-// One element: p, m, v in, out with r = sqrt(v).
-__device__ __forceinline__ void update(const AdamScalars& h, const Step& st, float keep, float g,
-                                       float& p, float& m, float& v, float& r) {
-  if (st.scaled) g = __fmul_rn(g, st.gs);
-  m = __fadd_rn(__fmul_rn(m, h.b1), __fmul_rn(g, h.omb1));
-  v = __fadd_rn(__fmul_rn(v, h.b2), __fmul_rn(__fmul_rn(g, g), h.omb2));
-  r = __fsqrt_rn(v);
-  const float u = __fdiv_rn(m, __fadd_rn(__fmul_rn(r, st.root2), h.eps));
-  p = __fsub_rn(__fmul_rn(p, keep), __fmul_rn(u, st.step));
+// Two elements: p, m, v in, out with r = sqrt(v).  The quotient (2 units in
+// the last place) and the sum it goes into feed no code and need not be
+// separately rounded ones.
+__device__ __forceinline__ void update2(const AdamScalars& h, const Step& st, float keep, float2 g,
+                                        float2& p, float2& m, float2& v, float2& r) {
+  g = mul2(g, both(st.gs));
+  const float2 mo = mul2(m, both(h.b1)), mg = mul2(g, both(h.omb1));
+  const float2 vo = mul2(v, both(h.b2)), vg = mul2(mul2(g, g), both(h.omb2));
+  m = make_float2(__fadd_rn(mo.x, mg.x), __fadd_rn(mo.y, mg.y));
+  v = make_float2(__fadd_rn(vo.x, vg.x), __fadd_rn(vo.y, vg.y));
+  r = make_float2(__fsqrt_rn(v.x), __fsqrt_rn(v.y));
+  const float2 d = add2(mul2(r, both(st.root2)), both(h.eps));
+  const float2 u = mul2(m, make_float2(rcp_approx(d.x), rcp_approx(d.y)));
+  p = fma2(u, both(-st.step), mul2(p, both(keep)));
 }
 
-__device__ __forceinline__ float abs_max(float a, float b) {
-  return __uint_as_float(umax(__float_as_uint(a), __float_as_uint(fabsf(b))));
+__device__ __forceinline__ float abs_max(float a, float b, float c) {  // NaN stays
+  float d;
+  asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(fabsf(b)), "f"(fabsf(c)));
+  return d;
 }
 
 // The block's new scales (stored by lane 0) and their reciprocals.
@@ -235,14 +277,73 @@ __device__ __forceinline__ void new_scales(const Entry& t, long long blk, int la
                                            float* inv_v) {
   float mt = 0.f, rt = 0.f;
 #pragma unroll
-  for (int k = 0; k < kPer; ++k) {
-    mt = abs_max(mt, m[k]);
-    rt = abs_max(rt, r[k]);
+  for (int k = 0; k < kPer; k += 2) {
+    mt = abs_max(mt, m[k], m[k + 1]);
+    rt = abs_max(rt, r[k], r[k + 1]);
   }
   float ms, vs;
   block_scale(warp_max(mt), &ms, inv_m);
   block_scale(warp_max(rt), &vs, inv_v);
   if (lane == 0) t.m_scale[blk] = ms, t.v_scale[blk] = vs;
+}
+
+__device__ __forceinline__ float max3(float a, float b, float c) {  // NaN is passed over
+  float d;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
+}
+
+// A lane's codes, exactly the rounded ones: levels from the approximate
+// root decide (its error is below 2^-22 of at most 255), unless one of the
+// lane's is within 2.5e-4 of half way between two codes.
+__device__ __forceinline__ void encode8(const float* m, const float* r, float inv_m, float inv_v,
+                                        uint32_t* qm, uint32_t* qv) {
+  const float low = inv_v > 0.f ? 1.f : 0.f;
+  float off = 0.f;
+#pragma unroll
+  for (int k = 0; k < kPer; k += 2) {
+    const float2 am = mul2(make_float2(m[k], m[k + 1]), both(inv_m));
+    const float2 av = mul2(make_float2(r[k], r[k + 1]), both(inv_v));
+    const float2 lm = make_float2(level_m(sqrt_approx(fabsf(am.x)), m[k]),
+                                  level_m(sqrt_approx(fabsf(am.y)), m[k + 1]));
+    const float2 lv = make_float2(level_v(sqrt_approx(av.x), r[k], low),
+                                  level_v(sqrt_approx(av.y), r[k + 1], low));
+    const float2 cm = add2(lm, both(kMagic)), cv = add2(lv, both(kMagic));
+    const float2 dm = fma2(both(-1.f), add2(cm, both(-kMagic)), lm);
+    const float2 dv = fma2(both(-1.f), add2(cv, both(-kMagic)), lv);
+    off = max3(off, fabsf(dm.x), fabsf(dm.y));
+    off = max3(off, fabsf(dv.x), fabsf(dv.y));
+    qm[k] = __float_as_uint(cm.x), qm[k + 1] = __float_as_uint(cm.y);
+    qv[k] = __float_as_uint(cv.x), qv[k + 1] = __float_as_uint(cv.y);
+  }
+  if (off > 0.5f - 2.5e-4f) {
+#pragma unroll
+    for (int k = 0; k < kPer; ++k) {
+      const float lm = level_m(__fsqrt_rn(__fmul_rn(fabsf(m[k]), inv_m)), m[k]);
+      const float lv = level_v(__fsqrt_rn(__fmul_rn(r[k], inv_v)), r[k], low);
+      qm[k] = __float_as_uint(__fadd_rn(lm, kMagic));
+      qv[k] = __float_as_uint(__fadd_rn(lv, kMagic));
+    }
+  }
+}
+
+// decode: the lane's m and v from its two words of codes each.
+__device__ __forceinline__ void decode8(const uint32_t* cm, const uint32_t* cv, float ms, float vs,
+                                        float* m, float* v) {
+#pragma unroll
+  for (int k = 0; k < kPer; k += 2) {
+    const uint32_t wm = cm[k >> 2] ^ 0x80808080u, wv = cv[k >> 2];
+    const int e = k & 3;
+    float2 t = mul2(add2(make_float2(code_bits(wm, e), code_bits(wm, e + 1)), both(-(kMagic + 128.f))),
+                    both(1.f / 127.f));
+    t = mul2(make_float2(__fmul_rn(t.x, fabsf(t.x)), __fmul_rn(t.y, fabsf(t.y))), both(ms));
+    m[k] = t.x, m[k + 1] = t.y;
+    t = mul2(add2(make_float2(code_bits(wv, e), code_bits(wv, e + 1)), both(-kMagic)),
+             both(1.f / 255.f));
+    t = mul2(mul2(t, t), both(vs));
+    t = mul2(t, t);
+    v[k] = t.x, v[k + 1] = t.y;
+  }
 }
 
 // A whole block of 256 elements from `base`.  PARAM: 0 float, 1 bf16 with a
@@ -274,14 +375,14 @@ __device__ __forceinline__ void whole_block(const Entry& t, long long base, int 
     load8<VEC>(static_cast<const float*>(t.param) + base, lane, p);
   if (!isfinite(st.gs)) return;
   const float keep = __fsub_rn(1.f, __fmul_rn(st.lr, t.decay));
+  if (Q8) decode8(cm, cv, ms, vs, m, v);
 #pragma unroll
-  for (int k = 0; k < kPer; ++k) {
-    if (Q8) {
-      m[k] = decode_m(code_s(cm[k >> 2] ^ 0x80808080u, k & 3), ms);
-      v[k] = decode_root(code_u(cv[k >> 2], k & 3), vs);
-      v[k] = __fmul_rn(v[k], v[k]);
-    }
-    update(h, st, keep, g[k], p[k], m[k], v[k], r[k]);
+  for (int k = 0; k < kPer; k += 2) {
+    float2 p2 = make_float2(p[k], p[k + 1]), m2 = make_float2(m[k], m[k + 1]);
+    float2 v2 = make_float2(v[k], v[k + 1]), r2;
+    update2(h, st, keep, make_float2(g[k], g[k + 1]), p2, m2, v2, r2);
+    p[k] = p2.x, p[k + 1] = p2.y, m[k] = m2.x, m[k + 1] = m2.y;
+    v[k] = v2.x, v[k + 1] = v2.y, r[k] = r2.x, r[k + 1] = r2.y;
   }
   if (PARAM == 0)
     store8<VEC>(static_cast<float*>(t.param) + base, lane, p);
@@ -291,13 +392,8 @@ __device__ __forceinline__ void whole_block(const Entry& t, long long base, int 
   if (Q8) {
     float inv_m, inv_v;
     new_scales(t, blk, lane, m, r, &inv_m, &inv_v);
-    const float low = inv_v > 0.f ? 1.f : 0.f;
     uint32_t qm[kPer], qv[kPer];
-#pragma unroll
-    for (int k = 0; k < kPer; ++k) {
-      qm[k] = encode_m(m[k], inv_m);
-      qv[k] = encode_v(v[k], r[k], inv_v, low);
-    }
+    encode8(m, r, inv_m, inv_v, qm, qv);
     store8<VEC>(static_cast<unsigned char*>(t.m) + base, lane, qm);
     store8<VEC>(static_cast<unsigned char*>(t.v) + base, lane, qv);
   } else {
@@ -333,7 +429,9 @@ __device__ __noinline__ void part_block(const Entry& t, long long base, int lane
       m[k] = static_cast<const float*>(t.m)[i];
       v[k] = static_cast<const float*>(t.v)[i];
     }
-    update(h, st, keep, g, p, m[k], v[k], r[k]);
+    float2 p2 = both(p), m2 = both(m[k]), v2 = both(v[k]), r2;
+    update2(h, st, keep, both(g), p2, m2, v2, r2);
+    p = p2.x, m[k] = m2.x, v[k] = v2.x, r[k] = r2.x;
     if (t.master) t.master[i] = p;
     if (t.p16)
       static_cast<__nv_bfloat16*>(t.param)[i] = __float2bfloat16_rn(p);
@@ -348,13 +446,14 @@ __device__ __noinline__ void part_block(const Entry& t, long long base, int lane
   __syncwarp();  // every lane has read the old scales
   float inv_m, inv_v;
   new_scales(t, blk, lane, m, r, &inv_m, &inv_v);
+  uint32_t qm[kPer], qv[kPer];
+  encode8(m, r, inv_m, inv_v, qm, qv);
 #pragma unroll
   for (int k = 0; k < kPer; ++k) {
     const long long i = base + lane + 32 * k;
     if (i >= t.count) continue;
-    static_cast<unsigned char*>(t.m)[i] = (unsigned char)encode_m(m[k], inv_m);
-    static_cast<unsigned char*>(t.v)[i] =
-        (unsigned char)encode_v(v[k], r[k], inv_v, inv_v > 0.f ? 1.f : 0.f);
+    static_cast<unsigned char*>(t.m)[i] = (unsigned char)qm[k];
+    static_cast<unsigned char*>(t.v)[i] = (unsigned char)qv[k];
   }
 }
 
@@ -370,7 +469,7 @@ __device__ __forceinline__ void by_param(const Entry& t, long long base, int lan
 }
 
 template <typename TB>
-__global__ void __launch_bounds__(kThreads)
+__global__ void __launch_bounds__(kThreads, 4)
     adamw_kernel(const __grid_constant__ TB tb, const __grid_constant__ AdamScalars h) {
   pdl_wait();
   const Step st = make_step(h);
@@ -410,12 +509,7 @@ __device__ __forceinline__ void whole_values(const Entry& t, long long base, int
     load8<VEC>(static_cast<const unsigned char*>(t.m) + base, lane, cm);
     load8<VEC>(static_cast<const unsigned char*>(t.v) + base, lane, cv);
     const float ms = t.m_scale[base / DC_STATE_BLOCK], vs = t.v_scale[base / DC_STATE_BLOCK];
-#pragma unroll
-    for (int k = 0; k < kPer; ++k) {
-      m[k] = decode_m(code_s(cm[k >> 2] ^ 0x80808080u, k & 3), ms);
-      v[k] = decode_root(code_u(cv[k >> 2], k & 3), vs);
-      v[k] = __fmul_rn(v[k], v[k]);
-    }
+    decode8(cm, cv, ms, vs, m, v);
   } else {
     load8<VEC>(static_cast<const float*>(t.m) + base, lane, m);
     load8<VEC>(static_cast<const float*>(t.v) + base, lane, v);

@@ -912,7 +912,7 @@ dc_status dc_adamw_step(const dc_adamw_tensor* tensors, int count, const dc_adam
   h.omb1 = (float)(1.0 - b1);
   h.b2 = (float)b2;
   h.omb2 = (float)(1.0 - b2);
-  h.eps = (float)eps;
+  h.eps = eps > 0 && eps < FLT_MIN ? FLT_MIN : (float)eps;  // not subnormal: the kernel's reciprocal flushes
   h.root2 = (float)(1.0 / sqrt(1.0 - pow(b2, (double)hyper->step)));
   h.step = (float)(lr / (1.0 - pow(b1, (double)hyper->step)));
   h.grad_scale = grad_scale;

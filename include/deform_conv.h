@@ -405,7 +405,8 @@ typedef struct {
   float weight_decay; /* >= 0, finite */
 } dc_adamw_tensor;
 
-/* beta1, beta2 in [0, 1); lr, eps >= 0; step: this step's number, from 1. */
+/* beta1, beta2 in [0, 1); lr, eps >= 0 (an eps between 0 and 2^-126 counts as
+ * 2^-126); step: this step's number, from 1. */
 typedef struct {
   double lr, beta1, beta2, eps;
   long long step;
@@ -416,8 +417,9 @@ typedef struct {
  *   m = m * beta1 + g * (1 - beta1);  v = v * beta2 + g * g * (1 - beta2)
  *   p = p * (1 - lr * weight_decay)
  *       - (m / (sqrt(v) / sqrt(1 - beta2^step) + eps)) * (lr / (1 - beta1^step))
- * in float32, every operation rounded by itself; 8-bit states are decoded
- * first and encoded last, the update uses the values before encoding.
+ * in float32; m and v with every operation rounded by itself, p with a
+ * quotient good to 2 units in its last place.  8-bit states are decoded first
+ * and encoded last, the update uses the values before encoding.
  *   tensors     host array, read before the call returns
  *   grad_scale  device float, NULL = 1 (dc_grad_norm's scale).  If it is not
  *               finite the step is skipped: nothing is changed.

@@ -856,6 +856,7 @@ dc_status dc_group_norm_fwd(const dc_norm_problem* prob, const void* x, const fl
   a.mean = mean;
   a.rstd = rstd;
   a.ws = static_cast<char*>(ws);
+  if (norm_one_launch(a, false)) return run("norm_fwd", s, launch_norm_fwd, a);
   if ((st = run("norm_stats", s, launch_norm_stats, a)) != DC_OK) return st;
   if ((st = run("norm_merge", s, launch_norm_merge, a)) != DC_OK) return st;
   return run("norm_apply", s, launch_norm_apply, a);
@@ -885,7 +886,9 @@ dc_status dc_group_norm_bwd(const dc_norm_problem* prob, const void* x, const fl
   a.ggamma = grad_gamma;
   a.gbeta = grad_beta;
   a.ws = static_cast<char*>(ws);
-  if (a.n) {
+  if (a.n && norm_one_launch(a, true)) {
+    if ((st = run("norm_bwd", s, launch_norm_bwd, a)) != DC_OK) return st;
+  } else if (a.n) {
     if ((st = run("norm_sums", s, launch_norm_sums, a)) != DC_OK) return st;
     if ((st = run("norm_merge_bwd", s, launch_norm_merge_bwd, a)) != DC_OK) return st;
     if ((st = run("norm_apply_bwd", s, launch_norm_apply_bwd, a)) != DC_OK) return st;

@@ -370,6 +370,11 @@ struct NormArgs {
 bool norm_supported(const NormArgs& a);  // grids and indices in range
 // Workspace bytes of the forward or backward pass.
 size_t norm_workspace_bytes(const NormArgs& a, bool backward);
+// Whether the pass runs as one launch (launch_norm_fwd; launch_norm_bwd, then
+// launch_norm_params), or in steps.
+bool norm_one_launch(const NormArgs& a, bool backward);
+cudaError_t launch_norm_fwd(const NormArgs& a, cudaStream_t s);
+cudaError_t launch_norm_bwd(const NormArgs& a, cudaStream_t s);
 // One launch each; the ABI layer runs them in order.
 cudaError_t launch_norm_stats(const NormArgs& a, cudaStream_t s);        // per-channel statistics of parts
 cudaError_t launch_norm_merge(const NormArgs& a, cudaStream_t s);        // mean and rstd of every group

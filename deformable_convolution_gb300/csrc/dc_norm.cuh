@@ -1,0 +1,382 @@
+// Group norm with an activation: what its translation units share (tilings,
+// vector access, activations, statistics, cluster and launch helpers).
+//
+// Statistics.  A thread keeps (count, mean, M2) of what it has read, M2 the
+// sum of squared distances from its own mean: a batch of vectors is averaged
+// first and its squared distances summed second, and two such triples merge
+// exactly,
+//   d = mb - ma, m = ma + d nb / (na + nb), M2 = M2a + M2b + d^2 na nb / (na + nb),
+// so no sum of squares about a far-off origin is ever formed (a large mean
+// over a small spread costs no digits).
+#pragma once
+
+#include "dc_common.cuh"
+
+namespace dc {
+
+
+// Two floats in one instruction.
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+  float2 d;
+  asm("{.reg .b64 ra, rb, rd;\n mov.b64 ra, {%2,%3};\n mov.b64 rb, {%4,%5};\n"
+      " mul.rn.f32x2 rd, ra, rb;\n mov.b64 {%0,%1}, rd;}"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return d;
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+  float2 d;
+  asm("{.reg .b64 ra, rb, rd;\n mov.b64 ra, {%2,%3};\n mov.b64 rb, {%4,%5};\n"
+      " add.rn.f32x2 rd, ra, rb;\n mov.b64 {%0,%1}, rd;}"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return d;
+}
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+  float2 d;
+  asm("{.reg .b64 ra, rb, rc, rd;\n mov.b64 ra, {%2,%3};\n mov.b64 rb, {%4,%5};\n"
+      " mov.b64 rc, {%6,%7};\n fma.rn.f32x2 rd, ra, rb, rc;\n mov.b64 {%0,%1}, rd;}"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+  return d;
+}
+__device__ __forceinline__ float2 both(float a) { return make_float2(a, a); }
+
+// V floats as pairs; V = 1 leaves the second of its pair unused.
+template <int V>
+struct Pairs {
+  static constexpr int n = (V + 1) / 2;
+  float2 p[n];
+  __device__ __forceinline__ float& operator[](int e) { return e & 1 ? p[e >> 1].y : p[e >> 1].x; }
+  __device__ __forceinline__ float operator[](int e) const {
+    return e & 1 ? p[e >> 1].y : p[e >> 1].x;
+  }
+};
+
+template <typename T>
+struct VecOf {
+  static constexpr int n = 16 / sizeof(T);
+};
+
+// V elements at p (aligned to V * sizeof(T) bytes) as floats.
+template <typename T, int V>
+__device__ __forceinline__ void load_vec(const T* p, float* f) {
+  if constexpr (V * sizeof(T) == 32) {
+    load_vec<T, V / 2>(p, f);
+    load_vec<T, V / 2>(p + V / 2, f + V / 2);
+  } else if constexpr (sizeof(T) == 4) {
+    if constexpr (V == 4) {
+      const float4 v = *reinterpret_cast<const float4*>(p);
+      f[0] = v.x, f[1] = v.y, f[2] = v.z, f[3] = v.w;
+    } else {
+#pragma unroll
+      for (int e = 0; e < V; ++e) f[e] = p[e];
+    }
+  } else if constexpr (V == 1) {
+    f[0] = to_f(p[0]);
+  } else {
+    uint32_t w[V / 2];
+    if constexpr (V == 8) {
+      const uint4 v = *reinterpret_cast<const uint4*>(p);
+      w[0] = v.x, w[1] = v.y, w[2] = v.z, w[3] = v.w;
+    } else {
+      static_assert(V == 4);
+      const uint2 v = *reinterpret_cast<const uint2*>(p);
+      w[0] = v.x, w[1] = v.y;
+    }
+#pragma unroll
+    for (int e = 0; e < V / 2; ++e) {
+      f[2 * e] = __uint_as_float(w[e] << 16);
+      f[2 * e + 1] = __uint_as_float(w[e] & 0xffff0000u);
+    }
+  }
+}
+
+template <typename T, int V>
+__device__ __forceinline__ void store_vec(T* p, const float* f) {
+  if constexpr (sizeof(T) == 4) {
+    if constexpr (V == 4) {
+      *reinterpret_cast<float4*>(p) = make_float4(f[0], f[1], f[2], f[3]);
+    } else {
+#pragma unroll
+      for (int e = 0; e < V; ++e) p[e] = f[e];
+    }
+  } else if constexpr (V == 1) {
+    p[0] = __float2bfloat16_rn(f[0]);
+  } else {
+    uint32_t w[V / 2];
+#pragma unroll
+    for (int e = 0; e < V / 2; ++e) {
+      __nv_bfloat162 b = __floats2bfloat162_rn(f[2 * e], f[2 * e + 1]);
+      w[e] = *reinterpret_cast<uint32_t*>(&b);
+    }
+    if constexpr (V == 8)
+      *reinterpret_cast<uint4*>(p) = make_uint4(w[0], w[1], w[2], w[3]);
+    else
+      *reinterpret_cast<uint2*>(p) = make_uint2(w[0], w[1]);
+  }
+}
+
+template <typename T, int V>
+__device__ __forceinline__ void load_vec(const T* p, Pairs<V>& f) {
+  float t[V];
+  load_vec<T, V>(p, t);
+#pragma unroll
+  for (int e = 0; e < V; ++e) f[e] = t[e];
+  if (V == 1) f.p[0].y = 0.f;
+}
+template <typename T, int V>
+__device__ __forceinline__ void store_vec(T* p, const Pairs<V>& f) {
+  float t[V];
+#pragma unroll
+  for (int e = 0; e < V; ++e) t[e] = f[e];
+  store_vec<T, V>(p, t);
+}
+
+// The elements [lo, hi) of a vector whose ends lie outside the row.
+template <typename T, int V>
+__device__ __forceinline__ void load_part(const T* p, int lo, int hi, float* f) {
+#pragma unroll
+  for (int e = 0; e < V; ++e) f[e] = e >= lo && e < hi ? to_f(p[e]) : 0.f;
+}
+template <typename T, int V>
+__device__ __forceinline__ void store_part(T* p, int lo, int hi, const float* f) {
+#pragma unroll
+  for (int e = 0; e < V; ++e)
+    if (e >= lo && e < hi) p[e] = from_f<T>(f[e]);
+}
+
+// One instruction each, subnormal numbers as 0.
+__device__ __forceinline__ float exp2_approx(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ float rcp_approx(float x) {
+  float y;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ float sigmoid(float z) {
+  return rcp_approx(1.f + exp2_approx(-1.4426950408889634f * z));
+}
+
+// The normal distribution's Phi(z), and e = exp(-z^2 / 2): Abramowitz and
+// Stegun's rational approximation 7.1.26 of erf (absolute error 1.5e-7, two
+// and a half units of float32 at 1) at |z| / sqrt 2; it needs e anyway, as
+// the slope does.
+__device__ __forceinline__ float normal_cdf(float z, float* e) {
+  const float x = fabsf(z) * 0.70710678118654752f;
+  const float t = rcp_approx(fmaf(0.3275911f, x, 1.f));
+  *e = exp2_approx(z * z * -0.72134752044448170f);
+  float q = fmaf(1.061405429f, t, -1.453152027f);
+  q = fmaf(q, t, 1.421413741f);
+  q = fmaf(q, t, -0.284496736f);
+  q = fmaf(q, t, 0.254829592f);
+  const float half = 0.5f * (q * t) * *e;  // Phi(-|z|)
+  return z < 0.f ? half : 1.f - half;
+}
+
+// Activations by kind: 0 max(z, floor), the floor 0 for the ReLU and -inf for
+// none (NaN is kept); 1 SiLU; 2 GELU.
+template <int ACT>
+__device__ __forceinline__ float act_fwd(float z, float floor) {
+  if (ACT == 1) return z * sigmoid(z);
+  if (ACT == 2) {
+    float e;
+    return z * normal_cdf(z, &e);
+  }
+  float y;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(y) : "f"(z), "f"(floor));
+  return y;
+}
+
+// d * act'(z); the ReLU's closed side passes nothing, whatever d is.
+template <int ACT>
+__device__ __forceinline__ float act_bwd(float z, float d, float floor) {
+  if (ACT == 1) {
+    const float sg = sigmoid(z);
+    return d * fmaf(z * sg, 1.f - sg, sg);
+  }
+  if (ACT == 2) {
+    float e;
+    const float cdf = normal_cdf(z, &e);
+    return d * fmaf(z * 0.39894228040143268f, e, cdf);
+  }
+  return z > floor ? d : 0.f;
+}
+
+// ---------------------------------------------------------------- the tiling
+// NCHW: a row is one channel of one image, hw consecutive elements; `lpr`
+// lanes of a warp walk a row's 16-byte vectors (the first and last may hang
+// over the row's ends), a warp takes 32 / lpr rows, and a long row is cut into
+// `parts` segments of `seg` vectors.
+// NHWC: a thread keeps one vector of v channels and walks pixels; a block
+// takes cb such columns and `seg` pixels of an image.
+struct Tiling {
+  int parts, seg;
+  int lpr;             // NCHW
+  int v, cols, cb, rl;  // NHWC: vector width, vectors of a pixel, of a block, pixel lanes
+};
+
+struct Shape {
+  int n, c, groups, cpg, hw;
+  float floor;  // of activation kind 0
+  float eps;
+  Tiling t;
+};
+
+// One launch for a pass: a cluster of blocks holds a unit in shared memory from
+// its statistics to its results.
+// NCHW: a unit is a group of an image; its rows are cut into tasks as above,
+// dealt over the warps of the cluster's blocks in `rounds`.
+struct RowTeam {
+  int cluster, warps, units;  // blocks of a unit, warps of a unit in a block, units of a block
+  int tasks, rounds;          // of a unit, of a warp
+  int held, slots;            // rounds kept in shared memory, vectors of a lane in a round
+  // whole-vector rows, forward: the unit's vectors in one run, `span` of them
+  // to a block (0: by tasks); held and slots count a thread's vectors
+  int span, step_c, step_v;   // threads of a unit in a block, as channels and vectors
+};
+// NHWC: a unit is a slice of whole groups, `cb` vectors wide, of an image; a
+// thread keeps one of its columns and walks pixels, `rl` threads to a column.
+struct ColTeam {
+  int cluster, slices, width;  // blocks of a unit, units of an image, channels of a unit
+  int cb, rl, ng;              // ng: groups of a unit
+  int span;                    // pixels of a block
+  int held, slots;             // pixels of a thread: kept in shared memory, all
+};
+constexpr int kTeam = 512;       // most threads of a block
+constexpr int kMaxCluster = 16;
+constexpr int kMaxGroups = 64;   // of a unit (NHWC)
+
+// How a call runs: as one launch of teams, or in the three-launch form.
+struct NormPlan {
+  Shape s;
+  bool team;
+  RowTeam row;
+  ColTeam col;
+  unsigned blocks;
+  int threads;
+  size_t smem;
+  int parts;  // rows of channel sums an image leaves (backward)
+};
+cudaError_t launch_team_nchw(const NormPlan& p, const NormArgs& a, bool backward, cudaStream_t s);
+cudaError_t launch_team_nhwc(const NormPlan& p, const NormArgs& a, bool backward, cudaStream_t s);
+
+__host__ __device__ inline int row_vectors(int hw, int mis, int vec) {
+  return (mis + hw + vec - 1) / vec;
+}
+
+__device__ __forceinline__ void merge(float& n, float& mean, float& m2, float nb, float mb,
+                                      float m2b) {
+  if (nb == 0.f) return;
+  const float t = n + nb, d = mb - mean, w = __fdividef(nb, t);
+  mean += d * w;
+  m2 += m2b + d * d * n * w;
+  n = t;
+}
+
+// Sum over the lpr lanes that share a row (lpr a power of two), in every lane.
+__device__ __forceinline__ float row_sum(float v, int lpr) {
+  for (int o = lpr >> 1; o; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  return v;
+}
+
+__device__ __forceinline__ float warp_sum(float v) { return row_sum(v, 32); }
+
+// ---------------------------------------------------------------- clusters
+
+__device__ __forceinline__ void cluster_arrive() {
+  asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void cluster_wait() {
+  asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+// This block's place in its cluster, and the cluster's in the grid (a launch
+// without clusters counts as clusters of one).
+__device__ __forceinline__ int cluster_rank() {
+  int r;
+  asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+  return r;
+}
+__device__ __forceinline__ int cluster_id() {
+  int r;
+  asm("mov.u32 %0, %%clusterid.x;" : "=r"(r));
+  return r;
+}
+// *p of the cluster's block `rank` = v
+__device__ __forceinline__ void store_cluster(float* p, int rank, float v) {
+  uint32_t to;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;"
+               : "=r"(to)
+               : "r"((uint32_t)__cvta_generic_to_shared(p)), "r"(rank));
+  asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(to), "f"(v) : "memory");
+}
+
+// Asynchronous copy of BYTES (4, 8 or 16) to shared memory; of 16, only the
+// first `bytes` are read and the rest becomes zero.
+template <int BYTES>
+__device__ __forceinline__ void copy_async(void* to, const void* from, int bytes = BYTES) {
+  const uint32_t dst = (uint32_t)__cvta_generic_to_shared(to);
+  if (BYTES == 16)
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(from), "r"(bytes)
+                 : "memory");
+  else
+    asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(dst), "l"(from), "n"(BYTES)
+                 : "memory");
+}
+__device__ __forceinline__ void copy_wait() { asm volatile("cp.async.wait_all;" ::: "memory"); }
+
+template <typename K, typename... A>
+cudaError_t launch_team(K kern, const NormPlan& p, int cluster, cudaStream_t s, A... args) {
+  cudaError_t e = cudaSuccess;
+  if (cluster > 8)
+    e = cudaFuncSetAttribute(kern, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+  if (e == cudaSuccess && p.smem > 24 * 1024)  // (beside up to 18 KB of static arrays)
+    e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)p.smem);
+  if (e != cudaSuccess) return e;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(p.blocks);
+  cfg.blockDim = dim3((unsigned)p.threads);
+  cfg.dynamicSmemBytes = p.smem;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = (unsigned)cluster;
+  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = cluster > 1 ? 2 : 1;
+  e = cudaLaunchKernelEx(&cfg, kern, args...);
+  note_launches(1);
+  return e;
+}
+
+template <int N>
+struct Int {
+  static constexpr int value = N;
+};
+template <typename F>
+cudaError_t by_dtype(dc_dtype dt, F&& f) {
+  return dt == DC_BF16 ? f(__nv_bfloat16{}) : f(float{});
+}
+// f(x's type, grad_y's type)
+template <typename F>
+cudaError_t by_dtypes(const NormArgs& a, F&& f) {
+  if (a.dt == DC_F32) return f(float{}, float{});
+  return a.gdt == DC_F32 ? f(__nv_bfloat16{}, float{}) : f(__nv_bfloat16{}, __nv_bfloat16{});
+}
+template <typename F>
+cudaError_t by_act(int act, F&& f) {
+  return act == DC_ACT_SILU ? f(Int<1>{}) : act == DC_ACT_GELU ? f(Int<2>{}) : f(Int<0>{});
+}
+template <typename T, typename F>
+cudaError_t by_width(int v, F&& f) {
+  if (v == VecOf<T>::n) return f(Int<VecOf<T>::n>{});
+  if (sizeof(T) == 2 && v == 4) return f(Int<4>{});
+  return f(Int<1>{});
+}
+
+}  // namespace dc

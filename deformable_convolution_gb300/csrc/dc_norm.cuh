@@ -10,6 +10,8 @@
 // over a small spread costs no digits).
 #pragma once
 
+#include <type_traits>
+
 #include "dc_common.cuh"
 
 namespace dc {
@@ -117,20 +119,43 @@ __device__ __forceinline__ void store_vec(T* p, const float* f) {
   }
 }
 
+// V packed elements to pairs.
+template <typename T, int V>
+__device__ __forceinline__ void unpack(const uint32_t* u, Pairs<V>& f) {
+#pragma unroll
+  for (int e = 0; e < Pairs<V>::n; ++e) {
+    if (sizeof(T) == 4)
+      f.p[e] = make_float2(__uint_as_float(u[V == 1 ? 0 : 2 * e]),
+                           V == 1 ? 0.f : __uint_as_float(u[V == 1 ? 0 : 2 * e + 1]));
+    else
+      f.p[e] = make_float2(__uint_as_float(u[e] << 16),
+                           V == 1 ? 0.f : __uint_as_float(u[e] & 0xffff0000u));
+  }
+}
+
 template <typename T, int V>
 __device__ __forceinline__ void load_vec(const T* p, Pairs<V>& f) {
-  float t[V];
-  load_vec<T, V>(p, t);
+  constexpr int kBytes = V * sizeof(T);
+  uint32_t u[(kBytes + 3) / 4];
+  if constexpr (kBytes >= 16) {
 #pragma unroll
-  for (int e = 0; e < V; ++e) f[e] = t[e];
-  if (V == 1) f.p[0].y = 0.f;
+    for (int i = 0; i < kBytes / 16; ++i) {
+      const uint4 v = reinterpret_cast<const uint4*>(p)[i];
+      u[4 * i] = v.x, u[4 * i + 1] = v.y, u[4 * i + 2] = v.z, u[4 * i + 3] = v.w;
+    }
+  } else if constexpr (kBytes == 8) {
+    const uint2 v = *reinterpret_cast<const uint2*>(p);
+    u[0] = v.x, u[1] = v.y;
+  } else if constexpr (kBytes == 4) {
+    u[0] = *reinterpret_cast<const uint32_t*>(p);
+  } else {
+    u[0] = *reinterpret_cast<const unsigned short*>(p);
+  }
+  unpack<T, V>(u, f);
 }
 template <typename T, int V>
 __device__ __forceinline__ void store_vec(T* p, const Pairs<V>& f) {
-  float t[V];
-#pragma unroll
-  for (int e = 0; e < V; ++e) t[e] = f[e];
-  store_vec<T, V>(p, t);
+  store_vec<T, V>(p, reinterpret_cast<const float*>(f.p));
 }
 
 // The elements [lo, hi) of a vector whose ends lie outside the row.
@@ -157,53 +182,70 @@ __device__ __forceinline__ float rcp_approx(float x) {
   asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
-__device__ __forceinline__ float sigmoid(float z) {
-  return rcp_approx(1.f + exp2_approx(-1.4426950408889634f * z));
+// 1 / (1 + exp(-z))
+__device__ __forceinline__ float2 sigmoid2(float2 z) {
+  const float2 t = mul2(z, both(-1.4426950408889634f));
+  const float2 u = add2(make_float2(exp2_approx(t.x), exp2_approx(t.y)), both(1.f));
+  return make_float2(rcp_approx(u.x), rcp_approx(u.y));
 }
 
 // The normal distribution's Phi(z), and e = exp(-z^2 / 2): Abramowitz and
 // Stegun's rational approximation 7.1.26 of erf (absolute error 1.5e-7, two
 // and a half units of float32 at 1) at |z| / sqrt 2; it needs e anyway, as
 // the slope does.
-__device__ __forceinline__ float normal_cdf(float z, float* e) {
-  const float x = fabsf(z) * 0.70710678118654752f;
-  const float t = rcp_approx(fmaf(0.3275911f, x, 1.f));
-  *e = exp2_approx(z * z * -0.72134752044448170f);
-  float q = fmaf(1.061405429f, t, -1.453152027f);
-  q = fmaf(q, t, 1.421413741f);
-  q = fmaf(q, t, -0.284496736f);
-  q = fmaf(q, t, 0.254829592f);
-  const float half = 0.5f * (q * t) * *e;  // Phi(-|z|)
-  return z < 0.f ? half : 1.f - half;
+__device__ __forceinline__ float2 normal_cdf2(float2 z, float2* e) {
+  const float2 a = make_float2(fabsf(z.x), fabsf(z.y));
+  const float2 u = fma2(a, both(0.3275911f * 0.70710678118654752f), both(1.f));
+  const float2 t = make_float2(rcp_approx(u.x), rcp_approx(u.y));
+  const float2 s = mul2(mul2(z, z), both(-0.72134752044448170f));
+  *e = make_float2(exp2_approx(s.x), exp2_approx(s.y));
+  float2 q = fma2(both(0.5f * 1.061405429f), t, both(0.5f * -1.453152027f));
+  q = fma2(q, t, both(0.5f * 1.421413741f));
+  q = fma2(q, t, both(0.5f * -0.284496736f));
+  q = fma2(q, t, both(0.5f * 0.254829592f));
+  q = mul2(mul2(q, t), *e);  // Phi(-|z|)
+  const float2 c = add2(both(1.f), make_float2(-q.x, -q.y));
+  return make_float2(z.x < 0.f ? q.x : c.x, z.y < 0.f ? q.y : c.y);
 }
 
 // Activations by kind: 0 max(z, floor), the floor 0 for the ReLU and -inf for
 // none (NaN is kept); 1 SiLU; 2 GELU.
 template <int ACT>
-__device__ __forceinline__ float act_fwd(float z, float floor) {
-  if (ACT == 1) return z * sigmoid(z);
+__device__ __forceinline__ float2 act_fwd2(float2 z, float floor) {
+  if (ACT == 1) return mul2(z, sigmoid2(z));
   if (ACT == 2) {
-    float e;
-    return z * normal_cdf(z, &e);
+    float2 e;
+    const float2 c = normal_cdf2(z, &e);
+    return mul2(z, c);
   }
-  float y;
-  asm("max.NaN.f32 %0, %1, %2;" : "=f"(y) : "f"(z), "f"(floor));
+  float2 y;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(y.x) : "f"(z.x), "f"(floor));
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(y.y) : "f"(z.y), "f"(floor));
   return y;
+}
+template <int ACT>
+__device__ __forceinline__ float act_fwd(float z, float floor) {
+  return act_fwd2<ACT>(both(z), floor).x;
 }
 
 // d * act'(z); the ReLU's closed side passes nothing, whatever d is.
 template <int ACT>
-__device__ __forceinline__ float act_bwd(float z, float d, float floor) {
+__device__ __forceinline__ float2 act_bwd2(float2 z, float2 d, float floor) {
   if (ACT == 1) {
-    const float sg = sigmoid(z);
-    return d * fmaf(z * sg, 1.f - sg, sg);
+    const float2 sg = sigmoid2(z);
+    const float2 r = add2(both(1.f), make_float2(-sg.x, -sg.y));
+    return mul2(d, fma2(mul2(z, sg), r, sg));
   }
   if (ACT == 2) {
-    float e;
-    const float cdf = normal_cdf(z, &e);
-    return d * fmaf(z * 0.39894228040143268f, e, cdf);
+    float2 e;
+    const float2 cdf = normal_cdf2(z, &e);
+    return mul2(d, fma2(mul2(z, both(0.39894228040143268f)), e, cdf));
   }
-  return z > floor ? d : 0.f;
+  return make_float2(z.x > floor ? d.x : 0.f, z.y > floor ? d.y : 0.f);
+}
+template <int ACT>
+__device__ __forceinline__ float act_bwd(float z, float d, float floor) {
+  return act_bwd2<ACT>(both(z), both(d), floor).x;
 }
 
 // ---------------------------------------------------------------- the tiling
@@ -245,10 +287,15 @@ struct ColTeam {
   int cb, rl, ng;              // ng: groups of a unit
   int span;                    // pixels of a block
   int held, slots;             // pixels of a thread: kept in shared memory, all
+  int rows;                    // of the backward's table of channel sums
 };
 constexpr int kTeam = 512;       // most threads of a block
 constexpr int kMaxCluster = 16;
 constexpr int kMaxGroups = 64;   // of a unit (NHWC)
+
+// Whether the backward keeps dz, in float32, where it held grad_y: where the
+// slope costs more than a wider slot (SiLU, GELU), or the slot is that wide.
+constexpr bool keep_dz(bool grad_f32, int act_kind) { return grad_f32 || act_kind != 0; }
 
 // How a call runs: as one launch of teams, or in the three-launch form.
 struct NormPlan {
@@ -333,7 +380,7 @@ cudaError_t launch_team(K kern, const NormPlan& p, int cluster, cudaStream_t s, 
   cudaError_t e = cudaSuccess;
   if (cluster > 8)
     e = cudaFuncSetAttribute(kern, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
-  if (e == cudaSuccess && p.smem > 24 * 1024)  // (beside up to 18 KB of static arrays)
+  if (e == cudaSuccess && p.smem > 40 * 1024)  // (beside up to 6 KB of static arrays)
     e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)p.smem);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};

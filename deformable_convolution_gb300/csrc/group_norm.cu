@@ -23,7 +23,8 @@ Tiling make_tiling(const NormArgs& a) {
     t.seg = (int)ceil_div_ll(vr, t.parts);
     t.parts = (int)ceil_div_ll(vr, t.seg);
   } else {
-    t.v = a.c % vec == 0 ? vec : a.dt == DC_BF16 && a.c % 4 == 0 ? 4 : 1;
+    // 16 bytes, or 8 where only that much is of one group (or divides c)
+    t.v = a.c % vec == 0 && (vec == 4 || a.cpg % 8 != 4) ? vec : a.c % 4 == 0 ? 4 : 1;
     t.cols = a.c / t.v;
     t.cb = t.cols < 32 ? t.cols : 32;
     t.rl = kThreads / t.cb;
@@ -568,8 +569,9 @@ NormPlan make_plan(const NormArgs& a, bool backward) {
   p.parts = 1;
   if (a.n == 0) return p;
   const int vec = a.dt == DC_BF16 ? 8 : 4, elt = a.dt == DC_BF16 ? 2 : 4;
-  // 16-byte pieces of a vector of x, and of one of grad_y
-  const int planes = 1 + (backward ? (a.gdt == DC_F32 && a.dt == DC_BF16 ? 2 : 1) : 0);
+  const bool keep = keep_dz(a.gdt == DC_F32, a.act == DC_ACT_SILU || a.act == DC_ACT_GELU);
+  // 16-byte pieces of a held vector of x, and of one of grad_y
+  const int planes = 1 + (backward ? (keep && a.dt == DC_BF16 ? 2 : 1) : 0);
   const long long groups = (long long)a.n * a.groups;
   if (!a.nhwc) {
     Tiling t{};
@@ -640,7 +642,7 @@ NormPlan make_plan(const NormArgs& a, bool backward) {
   const long long base = (long long)a.cpg / gcd(a.cpg, v) * v;
   if (base / v > 256) return p;
   const int slices_most = (int)(a.c / base);
-  const int held_bytes = v * (elt + (backward ? (a.gdt == DC_F32 ? 4 : 2) : 0));  // of a pixel's column
+  const int held_bytes = v * (elt + (backward ? (keep ? 4 : 2) : 0));  // of a pixel's column
   ColTeam& c = p.col;
   // the narrowest slice of 128 bytes a pixel, or of 64 where that leaves few
   // blocks or does not fit in a cluster
@@ -671,8 +673,9 @@ NormPlan make_plan(const NormArgs& a, bool backward) {
   const bool copies = v * elt >= 4;  // (an asynchronous copy moves 4 bytes at least)
   c.held = !copies ? 0 : slot * c.slots <= kBlockBytes ? c.slots : (int)(kBlockBytes / slot);
   if (c.held < c.slots && units * c.cluster < kSms) return p;
-  p.smem = (size_t)(slot * c.held);
-  if (backward) p.smem += (size_t)(32 % c.cb ? c.rl : p.threads / 32) * c.width * sizeof(float2);
+  c.rows = 32 % c.cb ? c.rl : p.threads / 32;
+  p.smem = (size_t)(slot * c.held) + (size_t)c.cluster * c.ng * (backward ? 2 : 3) * sizeof(float);
+  if (backward) p.smem += (size_t)c.rows * c.width * sizeof(float2);
   p.team = true;
   p.blocks = (unsigned)(units * c.cluster);
   p.parts = c.cluster;

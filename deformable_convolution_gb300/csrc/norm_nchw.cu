@@ -41,52 +41,50 @@ struct UnitTask {
   __device__ __forceinline__ int hi(int v) const { return EVEN || v != last ? VEC : tail; }
 };
 
-// A vector of VEC elements as it lies in memory: one or two 16-byte pieces.
+// 16-byte pieces of a vector of VEC elements.
 template <typename T, int VEC>
-struct Raw {
-  static constexpr int n = VEC * sizeof(T) / 16;
-  uint4 w[n];
-  __device__ __forceinline__ void unpack(Pairs<VEC>& f) const {
-    const uint32_t* u = reinterpret_cast<const uint32_t*>(w);
-#pragma unroll
-    for (int e = 0; e < VEC / 2; ++e)
-      f.p[e] = sizeof(T) == 4
-                   ? make_float2(__uint_as_float(u[2 * e]), __uint_as_float(u[2 * e + 1]))
-                   : make_float2(__uint_as_float(u[e] << 16), __uint_as_float(u[e] & 0xffff0000u));
-  }
-};
+constexpr int kPieces = VEC * sizeof(T) / 16;
 
-// Starts the copies of a task's vectors to this thread's slots.
+// A held vector: its pieces lie blockDim.x apart.
+template <typename T, int VEC>
+__device__ __forceinline__ void take(const uint4* slot, Pairs<VEC>& f) {
+  uint32_t u[4 * kPieces<T, VEC>];
+#pragma unroll
+  for (int i = 0; i < kPieces<T, VEC>; ++i) {
+    const uint4 v = slot[i * blockDim.x];
+    u[4 * i] = v.x, u[4 * i + 1] = v.y, u[4 * i + 2] = v.z, u[4 * i + 3] = v.w;
+  }
+  unpack<T, VEC>(u, f);
+}
+
+// Starts the copies of a task's vectors to this thread's slots, `stride` apart.
 template <typename T, int VEC, bool EVEN>
 __device__ __forceinline__ void hold_task(const Shape& s, const UnitTask<VEC, EVEN>& k, const T* x,
-                                          uint4* slot) {
+                                          uint4* slot, int stride) {
+  const T* p = x + k.off + (long long)k.v0 * VEC;
   for (int v = k.v0; v < k.v1; v += s.t.lpr) {
-    const T* p = x + k.off + (long long)v * VEC;
-    const int bytes = EVEN ? VEC * (int)sizeof(T) : k.hi(v) * (int)sizeof(T);
+    const int bytes = k.hi(v) * (int)sizeof(T);
 #pragma unroll
-    for (int i = 0; i < Raw<T, VEC>::n; ++i) {
+    for (int i = 0; i < kPieces<T, VEC>; ++i) {
       // (a piece past the row's end is skipped; its slot is not used)
       const int b = min(16, bytes - 16 * i);
       if (EVEN || b > 0)
-        copy_async<16>(slot, reinterpret_cast<const char*>(p) + 16 * i, EVEN ? 16 : b);
-      slot += blockDim.x;
+        copy_async<16>(slot + i * blockDim.x, reinterpret_cast<const char*>(p) + 16 * i,
+                       EVEN ? 16 : b);
     }
+    slot += stride;
+    p += s.t.lpr * VEC;
   }
 }
 
-// Vector v of a task, from this thread's slot or from memory; what lies
-// outside the row is 0.
-template <typename T, int VEC, bool EVEN>
-__device__ __forceinline__ void fetch(const UnitTask<VEC, EVEN>& k, int v, const T* x, bool held,
+// Vector v of a task at p, held or from memory; what lies outside the row is 0.
+template <typename T, int VEC, bool EVEN, bool HELD>
+__device__ __forceinline__ void fetch(const UnitTask<VEC, EVEN>& k, int v, const T* p,
                                       const uint4* slot, Pairs<VEC>& f) {
-  const T* p = x + k.off + (long long)v * VEC;
   const int lo = k.lo(v), hi = k.hi(v);
   const bool full = EVEN || (lo == 0 && hi == VEC);
-  if (held) {
-    Raw<T, VEC> r;
-#pragma unroll
-    for (int i = 0; i < Raw<T, VEC>::n; ++i) r.w[i] = slot[i * blockDim.x];
-    r.unpack(f);
+  if (HELD) {
+    take<T, VEC>(slot, f);
     if (!full) {
 #pragma unroll
       for (int e = 0; e < VEC; ++e)
@@ -103,18 +101,13 @@ __device__ __forceinline__ void fetch(const UnitTask<VEC, EVEN>& k, int v, const
 }
 
 template <typename T, int VEC, bool EVEN>
-__device__ __forceinline__ void put(const UnitTask<VEC, EVEN>& k, int v, T* y,
+__device__ __forceinline__ void put(const UnitTask<VEC, EVEN>& k, int v, T* p,
                                     const Pairs<VEC>& f) {
-  T* p = y + k.off + (long long)v * VEC;
   const int lo = k.lo(v), hi = k.hi(v);
-  if (EVEN || (lo == 0 && hi == VEC)) {
+  if (EVEN || (lo == 0 && hi == VEC))
     store_vec<T, VEC>(p, f);
-  } else {
-    float t[VEC];
-#pragma unroll
-    for (int e = 0; e < VEC; ++e) t[e] = f[e];
-    store_part<T, VEC>(p, lo, hi, t);
-  }
+  else
+    store_part<T, VEC>(p, lo, hi, reinterpret_cast<const float*>(f.p));
 }
 
 // This thread's place: block `rank` of the cluster, warp w of the unit's.
@@ -182,6 +175,84 @@ __device__ __forceinline__ float2 unit_stats(const Shape& s, const RowTeam& tm, 
 
 constexpr int kBatch = 4;
 
+// A lane's (n, mean, m2) merged with those of B vectors, cnt elements; get(b, f)
+// fetches vector b, fix(b, f, m) sets to m what of it does not count.
+template <int VEC, int B, typename GET, typename FIX>
+__device__ __forceinline__ void add_batch(int most, int cnt, float& n, float& mean, float& m2,
+                                          GET&& get, FIX&& fix) {
+  Pairs<VEC> f[B];
+  float2 sum = both(0.f), q = both(0.f);
+#pragma unroll
+  for (int b = 0; b < B; ++b) {
+    if (b >= most) continue;
+    get(b, f[b]);
+#pragma unroll
+    for (int e = 0; e < VEC / 2; ++e) sum = add2(sum, f[b].p[e]);
+  }
+  const float mb = (sum.x + sum.y) * rcp_approx((float)cnt);
+#pragma unroll
+  for (int b = 0; b < B; ++b) {
+    if (b >= most) continue;
+    fix(b, f[b], mb);
+#pragma unroll
+    for (int e = 0; e < VEC / 2; ++e) {
+      const float2 d = add2(f[b].p[e], both(-mb));
+      q = fma2(d, d, q);
+    }
+  }
+  merge(n, mean, m2, (float)cnt, mb, q.x + q.y);
+}
+
+// The statistics of one task.
+template <typename T, int VEC, bool EVEN, bool HELD>
+__device__ __forceinline__ void task_stats(const Shape& s, const UnitTask<VEC, EVEN>& k, const T* x,
+                                           const uint4* slot, float& n, float& mean, float& m2) {
+  const T* p = x + k.off + (long long)k.v0 * VEC;
+  const int lpr = s.t.lpr;
+  for (int v0 = k.v0; v0 < k.v1; v0 += kBatch * lpr) {
+    const int most = (k.v1 - v0 + lpr - 1) / lpr;
+    int cnt = 0;
+#pragma unroll
+    for (int b = 0; b < kBatch; ++b)
+      if (b < most) cnt += k.hi(v0 + b * lpr) - k.lo(v0 + b * lpr);
+    add_batch<VEC, kBatch>(
+        most, cnt, n, mean, m2,
+        [&](int b, Pairs<VEC>& f) {
+          fetch<T, VEC, EVEN, HELD>(k, v0 + b * lpr, p + b * lpr * VEC, slot + b * blockDim.x, f);
+        },
+        [&](int b, Pairs<VEC>& f, float m) {
+          if (EVEN) return;
+          const int lo = k.lo(v0 + b * lpr), hi = k.hi(v0 + b * lpr);
+          if (hi - lo < VEC) {
+#pragma unroll
+            for (int e = 0; e < VEC; ++e)
+              if (e < lo || e >= hi) f[e] = m;
+          }
+        });
+    slot += kBatch * blockDim.x;
+    p += kBatch * lpr * VEC;
+  }
+}
+
+template <typename T, int VEC, bool EVEN, bool HELD, int ACT>
+__device__ __forceinline__ void task_apply(const Shape& s, const UnitTask<VEC, EVEN>& k, const T* x,
+                                           T* y, const uint4* slot, float mu, float a, float b) {
+  const T* p = x + k.off + (long long)k.v0 * VEC;
+  T* to = y + k.off + (long long)k.v0 * VEC;
+#pragma unroll 2
+  for (int v = k.v0; v < k.v1; v += s.t.lpr) {
+    Pairs<VEC> f;
+    fetch<T, VEC, EVEN, HELD>(k, v, p, slot, f);
+#pragma unroll
+    for (int e = 0; e < VEC / 2; ++e)
+      f.p[e] = act_fwd2<ACT>(fma2(add2(f.p[e], both(-mu)), both(a), both(b)), s.floor);
+    put<T, VEC, EVEN>(k, v, to, f);
+    slot += blockDim.x;
+    p += s.t.lpr * VEC;
+    to += s.t.lpr * VEC;
+  }
+}
+
 template <typename T, bool EVEN, int ACT>
 __global__ void __launch_bounds__(kTeam, 2)
     fwd_nchw(Shape s, RowTeam tm, const T* x, const float* gamma, const float* beta, T* y,
@@ -200,47 +271,15 @@ __global__ void __launch_bounds__(kTeam, 2)
     return r == 0 ? first : Task(s, pl.unit, pl.ch0, pl.task(tm, r), tasks);
   };
   uint4* mine = hold + threadIdx.x;
-  for (int r = 0; r < tm.held; ++r) hold_task<T, VEC, EVEN>(s, task(r), x, mine + r * pitch);
+  for (int r = 0; r < tm.held; ++r)
+    hold_task<T, VEC, EVEN>(s, task(r), x, mine + r * pitch, blockDim.x);
   // what is not held first: its loads go on behind the copies
   float n = 0.f, mean = 0.f, m2 = 0.f;
-  for (int r = tm.rounds - 1; r >= 0; --r) {
-    const Task k = task(r);
-    const bool held = r < tm.held;
-    const uint4* slot = mine + r * pitch;
-    if (r == tm.held - 1) copy_wait();
-    for (int v0 = k.v0; v0 < k.v1; v0 += kBatch * s.t.lpr) {
-      Pairs<VEC> f[kBatch];
-      float2 sum = both(0.f), q = both(0.f);
-      int cnt = 0;
-#pragma unroll
-      for (int b = 0; b < kBatch; ++b) {
-        const int v = v0 + b * s.t.lpr;
-        if (v >= k.v1) continue;
-        fetch<T, VEC, EVEN>(k, v, x, held, slot + b * blockDim.x, f[b]);
-        cnt += k.hi(v) - k.lo(v);
-#pragma unroll
-        for (int e = 0; e < VEC / 2; ++e) sum = add2(sum, f[b].p[e]);
-      }
-      const float mb = (sum.x + sum.y) * rcp_approx((float)cnt);
-#pragma unroll
-      for (int b = 0; b < kBatch; ++b) {
-        const int v = v0 + b * s.t.lpr;
-        if (v >= k.v1) continue;
-        if (!EVEN && k.hi(v) - k.lo(v) < VEC) {
-#pragma unroll
-          for (int e = 0; e < VEC; ++e)
-            if (e < k.lo(v) || e >= k.hi(v)) f[b][e] = mb;  // adds nothing below
-        }
-#pragma unroll
-        for (int e = 0; e < VEC / 2; ++e) {
-          const float2 d = add2(f[b].p[e], both(-mb));
-          q = fma2(d, d, q);
-        }
-      }
-      merge(n, mean, m2, (float)cnt, mb, q.x + q.y);
-      slot += kBatch * blockDim.x;
-    }
-  }
+  for (int r = tm.rounds - 1; r >= tm.held; --r)
+    task_stats<T, VEC, EVEN, false>(s, task(r), x, mine, n, mean, m2);
+  copy_wait();
+  for (int r = 0; r < tm.held; ++r)
+    task_stats<T, VEC, EVEN, true>(s, task(r), x, mine + r * pitch, n, mean, m2);
   const float2 st = unit_stats(s, tm, pl, sm, n, mean, m2);
   if (!pl.here) return;
   if (pl.rank == 0 && pl.w == 0 && (threadIdx.x & 31) == 0) {
@@ -249,20 +288,11 @@ __global__ void __launch_bounds__(kTeam, 2)
   }
   for (int r = 0; r < tm.rounds; ++r) {
     const Task k = task(r);
-    const bool held = r < tm.held;
-    const uint4* slot = mine + r * pitch;
     const float a = st.y * (gamma ? gamma[k.ch] : 1.f), b = beta ? beta[k.ch] : 0.f;
-#pragma unroll 2
-    for (int v = k.v0; v < k.v1; v += s.t.lpr) {
-      Pairs<VEC> f;
-      fetch<T, VEC, EVEN>(k, v, x, held, slot, f);
-#pragma unroll
-      for (int e = 0; e < VEC / 2; ++e) f.p[e] = fma2(add2(f.p[e], both(-st.x)), both(a), both(b));
-#pragma unroll
-      for (int e = 0; e < VEC; ++e) f[e] = act_fwd<ACT>(f[e], s.floor);
-      put<T, VEC, EVEN>(k, v, y, f);
-      slot += blockDim.x;
-    }
+    if (r < tm.held)
+      task_apply<T, VEC, EVEN, true, ACT>(s, k, x, y, mine + r * pitch, st.x, a, b);
+    else
+      task_apply<T, VEC, EVEN, false, ACT>(s, k, x, y, mine, st.x, a, b);
   }
 }
 
@@ -281,82 +311,143 @@ __global__ void __launch_bounds__(kTeam, 2)
   pdl_release();
   const Place pl(s, tm);
   const int threads = 32 * tm.warps, tid = threadIdx.x - pl.u * threads;
-  const int vr = s.hw / VEC;
-  const long long first = (long long)pl.unit * s.cpg * s.hw;
+  const int vr = s.hw / VEC, step = threads * VEC;
   const int begin = pl.rank * tm.span + tid;
-  int end = s.cpg * vr;  // (a unit of over 2^30 vectors does not come here)
+  int end = s.cpg * vr;  // (a unit of 2^30 vectors or more does not come here)
   if (end > (pl.rank + 1) * tm.span) end = (pl.rank + 1) * tm.span;
   if (!pl.here) end = 0;
-  x += first;
-  y += first;
+  const int mine_n = begin < end ? (end - begin + threads - 1) / threads : 0;  // vectors
+  const int held = mine_n < tm.held ? mine_n : tm.held;
+  const long long off = (long long)pl.unit * s.cpg * s.hw + (long long)begin * VEC;
   uint4* mine = hold + threadIdx.x;
   {
+    const T* p = x + off;
     uint4* slot = mine;
-    for (int i = 0, v = begin; i < tm.held && v < end; ++i, v += threads, slot += blockDim.x)
-      copy_async<16>(slot, x + (long long)v * VEC);
+    for (int i = 0; i < held; ++i, p += step, slot += blockDim.x) copy_async<16>(slot, p);
   }
   float n = 0.f, mean = 0.f, m2 = 0.f;
-  auto batches = [&](int i0, int i1) {
-    for (int i = i0; i < i1; i += kBatch) {
-      const int v0 = begin + i * threads;
-      if (v0 >= end) break;
-      Pairs<VEC> f[kBatch];
-      float2 sum = both(0.f), q = both(0.f);
-      int cnt = 0;
-#pragma unroll
-      for (int b = 0; b < kBatch; ++b) {
-        const int v = v0 + b * threads;
-        if (i + b >= i1 || v >= end) continue;
-        Raw<T, VEC> r;
-        r.w[0] = i + b < tm.held ? mine[(i + b) * blockDim.x]
-                                 : *reinterpret_cast<const uint4*>(x + (long long)v * VEC);
-        r.unpack(f[b]);
-        cnt += VEC;
-#pragma unroll
-        for (int e = 0; e < VEC / 2; ++e) sum = add2(sum, f[b].p[e]);
-      }
-      const float mb = (sum.x + sum.y) * rcp_approx((float)cnt);
-#pragma unroll
-      for (int b = 0; b < kBatch; ++b) {
-        if (i + b >= i1 || v0 + b * threads >= end) continue;
-#pragma unroll
-        for (int e = 0; e < VEC / 2; ++e) {
-          const float2 d = add2(f[b].p[e], both(-mb));
-          q = fma2(d, d, q);
-        }
-      }
-      merge(n, mean, m2, (float)cnt, mb, q.x + q.y);
-    }
-  };
-  batches(tm.held, tm.slots);  // what is not held, behind the copies
+  auto keep = [](int, Pairs<VEC>&, float) {};
+  // what is not held first: its loads go on behind the copies
+  for (int i = held; i < mine_n; i += kBatch) {
+    const int most = min(mine_n - i, kBatch);
+    add_batch<VEC, kBatch>(
+        most, most * VEC, n, mean, m2,
+        [&](int b, Pairs<VEC>& f) { load_vec<T, VEC>(x + off + (long long)(i + b) * step, f); },
+        keep);
+  }
   copy_wait();
-  batches(0, tm.held);
+  {
+    const uint4* slot = mine;
+    auto get = [&](int b, Pairs<VEC>& f) { take<T, VEC>(slot + b * blockDim.x, f); };
+    int i = 0;
+    for (; i + kBatch <= held; i += kBatch, slot += kBatch * blockDim.x)
+      add_batch<VEC, kBatch>(kBatch, kBatch * VEC, n, mean, m2, get, keep);
+    if (i < held) add_batch<VEC, kBatch>(held - i, (held - i) * VEC, n, mean, m2, get, keep);
+  }
   const float2 st = unit_stats(s, tm, pl, sm, n, mean, m2);
   if (!pl.here) return;
   if (pl.rank == 0 && tid == 0) {
     if (mean_out) mean_out[pl.unit] = st.x;
     if (rstd_out) rstd_out[pl.unit] = st.y;
   }
-  // vector `begin + i * threads` lies in channel c, `at` vectors from its start
+  // vector i of this thread lies in channel c, `at` vectors from its start
   int c = begin / vr, at = begin - c * vr;
   const float* gm = gamma ? gamma + pl.ch0 : nullptr;
   const float* bt = beta ? beta + pl.ch0 : nullptr;
-#pragma unroll 2
-  for (int i = 0, v = begin; v < end; ++i, v += threads) {
+  const T* p = x + off;
+  T* to = y + off;
+  auto apply = [&](Pairs<VEC>& f) {
     const float a = st.y * (gm ? gm[c] : 1.f), b = bt ? bt[c] : 0.f;
-    Raw<T, VEC> r;
-    r.w[0] = i < tm.held ? mine[i * blockDim.x]
-                         : *reinterpret_cast<const uint4*>(x + (long long)v * VEC);
-    Pairs<VEC> f;
-    r.unpack(f);
 #pragma unroll
-    for (int e = 0; e < VEC / 2; ++e) f.p[e] = fma2(add2(f.p[e], both(-st.x)), both(a), both(b));
-#pragma unroll
-    for (int e = 0; e < VEC; ++e) f[e] = act_fwd<ACT>(f[e], s.floor);
-    store_vec<T, VEC>(y + (long long)v * VEC, f);
+    for (int e = 0; e < VEC / 2; ++e)
+      f.p[e] = act_fwd2<ACT>(fma2(add2(f.p[e], both(-st.x)), both(a), both(b)), s.floor);
+    store_vec<T, VEC>(to, f);
+    to += step;
     c += tm.step_c;
     at += tm.step_v;
     if (at >= vr) at -= vr, ++c;
+  };
+#pragma unroll 2
+  for (int i = 0; i < held; ++i) {
+    Pairs<VEC> f;
+    take<T, VEC>(mine + i * blockDim.x, f);
+    apply(f);
+  }
+  p += (long long)held * step;
+  for (int i = held; i < mine_n; ++i, p += step) {
+    Pairs<VEC> f;
+    load_vec<T, VEC>(p, f);
+    apply(f);
+  }
+}
+
+// A task's sums of dz and dz * xh.  KEEP: dz takes grad_y's place in the slot
+// (in float32), so that the results need the activation's slope no more.
+template <typename T, typename TG, int VEC, bool EVEN, bool HELD, bool KEEP, int ACT>
+__device__ __forceinline__ void task_sums(const Shape& s, const UnitTask<VEC, EVEN>& k, const T* x,
+                                          const TG* gy, const uint4* slot, uint4* slot_g,
+                                          int stride_g, float mu, float rs, float g, float b,
+                                          float2& sa, float2& sb) {
+  const long long off = k.off + (long long)k.v0 * VEC;
+  const T* p = x + off;
+  const TG* pg = gy + off;
+#pragma unroll 2
+  for (int v = k.v0; v < k.v1; v += s.t.lpr) {
+    Pairs<VEC> f, d;  // (0 outside the row: dz is 0 there)
+    fetch<T, VEC, EVEN, HELD>(k, v, p, slot, f);
+    fetch<TG, VEC, EVEN, HELD>(k, v, pg, slot_g, d);
+#pragma unroll
+    for (int e = 0; e < VEC / 2; ++e) {
+      const float2 xh = mul2(add2(f.p[e], both(-mu)), both(rs));
+      d.p[e] = act_bwd2<ACT>(fma2(xh, both(g), both(b)), d.p[e], s.floor);
+      sa = add2(sa, d.p[e]);
+      sb = fma2(d.p[e], xh, sb);
+    }
+    if (HELD && KEEP) {
+#pragma unroll
+      for (int i = 0; i < VEC / 4; ++i)
+        *reinterpret_cast<float4*>(slot_g + i * blockDim.x) = make_float4(
+            d.p[2 * i].x, d.p[2 * i].y, d.p[2 * i + 1].x, d.p[2 * i + 1].y);
+    }
+    slot += blockDim.x;
+    slot_g += stride_g;
+    p += s.t.lpr * VEC;
+    pg += s.t.lpr * VEC;
+  }
+}
+
+// grad_x = dz * gr - s1 - xh * s2 (gr = gamma * rstd; s1, s2 times rstd)
+template <typename T, typename TG, int VEC, bool EVEN, bool HELD, bool KEEP, int ACT>
+__device__ __forceinline__ void task_grads(const Shape& s, const UnitTask<VEC, EVEN>& k, const T* x,
+                                           const TG* gy, T* gx, const uint4* slot,
+                                           const uint4* slot_g, int stride_g, float mu, float rs,
+                                           float g, float b, float s1, float s2) {
+  const long long off = k.off + (long long)k.v0 * VEC;
+  const T* p = x + off;
+  const TG* pg = gy + off;
+  T* to = gx + off;
+  const float gr = g * rs;
+#pragma unroll 2
+  for (int v = k.v0; v < k.v1; v += s.t.lpr) {
+    Pairs<VEC> f, d;
+    fetch<T, VEC, EVEN, HELD>(k, v, p, slot, f);
+    if (HELD && KEEP)
+      take<float, VEC>(slot_g, d);
+    else
+      fetch<TG, VEC, EVEN, HELD>(k, v, pg, slot_g, d);
+#pragma unroll
+    for (int e = 0; e < VEC / 2; ++e) {
+      const float2 xh = mul2(add2(f.p[e], both(-mu)), both(rs));
+      if (!(HELD && KEEP))
+        d.p[e] = act_bwd2<ACT>(fma2(xh, both(g), both(b)), d.p[e], s.floor);
+      f.p[e] = fma2(xh, both(-s2), fma2(d.p[e], both(gr), both(-s1)));
+    }
+    put<T, VEC, EVEN>(k, v, to, f);
+    slot += blockDim.x;
+    slot_g += stride_g;
+    p += s.t.lpr * VEC;
+    pg += s.t.lpr * VEC;
+    to += s.t.lpr * VEC;
   }
 }
 
@@ -367,7 +458,8 @@ __global__ void __launch_bounds__(kTeam, 2)
     bwd_nchw(Shape s, RowTeam tm, const T* x, const TG* gy, const float* gamma, const float* beta,
              const float* mean, const float* rstd, T* gx, float2* part) {
   constexpr int VEC = VecOf<T>::n;
-  constexpr int kX = Raw<T, VEC>::n, kG = Raw<TG, VEC>::n;
+  constexpr bool KEEP = keep_dz(sizeof(TG) == 4, ACT);
+  constexpr int kG = KEEP ? VEC / 4 : kPieces<TG, VEC>;  // pieces of a slot of grad_y
   extern __shared__ uint4 hold[];
   __shared__ float sm[2][256];
   if (tm.cluster > 1) cluster_arrive();
@@ -375,45 +467,33 @@ __global__ void __launch_bounds__(kTeam, 2)
   pdl_release();
   const Place pl(s, tm);
   const int tasks = pl.here ? tm.tasks : 0, pitch = tm.slots * blockDim.x;
+  const int stride_g = kG * blockDim.x;
   using Task = UnitTask<VEC, EVEN>;
   const Task first(s, pl.unit, pl.ch0, pl.task(tm, 0), tasks);
   auto task = [&](int r) {
     return r == 0 ? first : Task(s, pl.unit, pl.ch0, pl.task(tm, r), tasks);
   };
   uint4* mine = hold + threadIdx.x;
-  uint4* mine_g = mine + (size_t)tm.held * pitch * kX;
+  uint4* mine_g = mine + (size_t)tm.held * pitch;
   for (int r = 0; r < tm.held; ++r) {
     const Task k = task(r);
-    hold_task<T, VEC, EVEN>(s, k, x, mine + r * pitch * kX);
-    hold_task<TG, VEC, EVEN>(s, k, gy, mine_g + r * pitch * kG);
+    hold_task<T, VEC, EVEN>(s, k, x, mine + r * pitch, blockDim.x);
+    hold_task<TG, VEC, EVEN>(s, k, gy, mine_g + r * pitch * kG, stride_g);
   }
   const float mu = pl.here ? mean[pl.unit] : 0.f, rs = pl.here ? rstd[pl.unit] : 0.f;
   float val[2] = {0.f, 0.f};
   for (int r = tm.rounds - 1; r >= 0; --r) {
     const Task k = task(r);
-    const bool held = r < tm.held;
-    const uint4* slot = mine + r * pitch * kX;
-    const uint4* slot_g = mine_g + r * pitch * kG;
     if (r == tm.held - 1) copy_wait();
     const float g = gamma ? gamma[k.ch] : 1.f, b = beta ? beta[k.ch] : 0.f;
     float2 sa = both(0.f), sb = both(0.f);
-#pragma unroll 2
-    for (int v = k.v0; v < k.v1; v += s.t.lpr) {
-      Pairs<VEC> f, d;  // (0 outside the row: dz is 0 there)
-      fetch<T, VEC, EVEN>(k, v, x, held, slot, f);
-      fetch<TG, VEC, EVEN>(k, v, gy, held, slot_g, d);
-#pragma unroll
-      for (int e = 0; e < VEC / 2; ++e) {
-        const float2 xh = mul2(add2(f.p[e], both(-mu)), both(rs));
-        const float2 z = fma2(xh, both(g), both(b));
-        const float2 dz = make_float2(act_bwd<ACT>(z.x, d.p[e].x, s.floor),
-                                      act_bwd<ACT>(z.y, d.p[e].y, s.floor));
-        sa = add2(sa, dz);
-        sb = fma2(dz, xh, sb);
-      }
-      slot += kX * blockDim.x;
-      slot_g += kG * blockDim.x;
-    }
+    if (r < tm.held)
+      task_sums<T, TG, VEC, EVEN, true, KEEP, ACT>(s, k, x, gy, mine + r * pitch,
+                                                   mine_g + r * pitch * kG, stride_g, mu, rs, g, b,
+                                                   sa, sb);
+    else
+      task_sums<T, TG, VEC, EVEN, false, KEEP, ACT>(s, k, x, gy, mine, mine_g, stride_g, mu, rs, g,
+                                                    b, sa, sb);
     const float ra = row_sum(sa.x + sa.y, s.t.lpr), rb = row_sum(sb.x + sb.y, s.t.lpr);
     if (k.live && (threadIdx.x & (s.t.lpr - 1)) == 0) {
       part[(long long)k.part * s.n * s.c + k.row] = make_float2(ra, rb);
@@ -434,28 +514,14 @@ __global__ void __launch_bounds__(kTeam, 2)
   if (!pl.here) return;
   for (int r = 0; r < tm.rounds; ++r) {
     const Task k = task(r);
-    const bool held = r < tm.held;
-    const uint4* slot = mine + r * pitch * kX;
-    const uint4* slot_g = mine_g + r * pitch * kG;
     const float g = gamma ? gamma[k.ch] : 1.f, b = beta ? beta[k.ch] : 0.f;
-    const float gr = g * rs;
-#pragma unroll 2
-    for (int v = k.v0; v < k.v1; v += s.t.lpr) {
-      Pairs<VEC> f, d;
-      fetch<T, VEC, EVEN>(k, v, x, held, slot, f);
-      fetch<TG, VEC, EVEN>(k, v, gy, held, slot_g, d);
-#pragma unroll
-      for (int e = 0; e < VEC / 2; ++e) {
-        const float2 xh = mul2(add2(f.p[e], both(-mu)), both(rs));
-        const float2 z = fma2(xh, both(g), both(b));
-        const float2 dz = make_float2(act_bwd<ACT>(z.x, d.p[e].x, s.floor),
-                                      act_bwd<ACT>(z.y, d.p[e].y, s.floor));
-        f.p[e] = fma2(xh, both(-s2), fma2(dz, both(gr), both(-s1)));
-      }
-      put<T, VEC, EVEN>(k, v, gx, f);
-      slot += kX * blockDim.x;
-      slot_g += kG * blockDim.x;
-    }
+    if (r < tm.held)
+      task_grads<T, TG, VEC, EVEN, true, KEEP, ACT>(s, k, x, gy, gx, mine + r * pitch,
+                                                    mine_g + r * pitch * kG, stride_g, mu, rs, g,
+                                                    b, s1, s2);
+    else
+      task_grads<T, TG, VEC, EVEN, false, KEEP, ACT>(s, k, x, gy, gx, mine, mine_g, stride_g, mu,
+                                                     rs, g, b, s1, s2);
   }
 }
 

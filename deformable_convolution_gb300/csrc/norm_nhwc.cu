@@ -32,125 +32,156 @@ struct UnitCol {
   }
 };
 
-// A thread's held pixels: slot i at i * blockDim.x.
+// Held vectors: slot i of a thread is P pieces of kUnit bytes, blockDim.x
+// pieces apart; V elements of T take the first of them.
 template <typename T, int V>
-struct __align__(V * sizeof(T) >= 16 ? 16 : V * sizeof(T)) Cell {
-  T e[V];
-};
+constexpr int kUnit = V * sizeof(T) >= 16 ? 16 : V * sizeof(T);
+template <typename T, int V>
+constexpr int kPieces = V * sizeof(T) / kUnit<T, V>;
 
 template <typename T, int V>
-__device__ __forceinline__ void hold_col(const Shape& s, const ColTeam& tm, const UnitCol<V>& k,
-                                         const T* x, Cell<T, V>* slot) {
+__device__ __forceinline__ void take(const char* slot, Pairs<V>& f) {
   constexpr int kBytes = V * sizeof(T);
-  if constexpr (kBytes >= 4) {
-    int p = k.p0;
-    for (int i = 0; i < tm.held && p < k.p1; ++i, p += tm.rl, slot += blockDim.x) {
-      const T* from = x + k.base + (long long)p * s.c;
-      if constexpr (kBytes > 16) {
-        copy_async<16>(slot, from);
-        copy_async<16>(reinterpret_cast<char*>(slot) + 16, from + V / 2);
-      } else {
-        copy_async<kBytes>(slot, from);
-      }
+  if constexpr (kBytes <= 16) {
+    load_vec<T, V>(reinterpret_cast<const T*>(slot), f);
+  } else {
+    uint32_t u[kBytes / 4];
+#pragma unroll
+    for (int i = 0; i < kBytes / 16; ++i) {
+      const uint4 v = *reinterpret_cast<const uint4*>(slot + i * 16 * blockDim.x);
+      u[4 * i] = v.x, u[4 * i + 1] = v.y, u[4 * i + 2] = v.z, u[4 * i + 3] = v.w;
+    }
+    unpack<T, V>(u, f);
+  }
+}
+// f in float32 over a slot of as many bytes
+template <int V>
+__device__ __forceinline__ void leave(char* slot, const Pairs<V>& f) {
+  const float* e = reinterpret_cast<const float*>(f.p);
+  if constexpr (V >= 4) {
+#pragma unroll
+    for (int i = 0; i < V / 4; ++i)
+      *reinterpret_cast<float4*>(slot + i * 16 * blockDim.x) =
+          make_float4(e[4 * i], e[4 * i + 1], e[4 * i + 2], e[4 * i + 3]);
+  } else {
+    *reinterpret_cast<float*>(slot) = e[0];
+  }
+}
+
+// Starts the copies of a thread's first `count` pixels to its slots.
+template <typename T, int V>
+__device__ __forceinline__ void hold_col(const T* p, long long step, int count, char* slot,
+                                         int stride) {
+  constexpr int kBytes = V * sizeof(T);
+  if constexpr (kBytes >= 4) {  // (an asynchronous copy moves 4 bytes at least)
+    for (int i = 0; i < count; ++i, p += step, slot += stride) {
+      copy_async<kUnit<T, V>>(slot, p);
+      if constexpr (kBytes > 16) copy_async<16>(slot + 16 * blockDim.x, p + V / 2);
     }
   }
 }
 
-template <typename T, int V>
-__device__ __forceinline__ void fetch(const Shape& s, const ColTeam& tm, const UnitCol<V>& k, int i,
-                                      int p, const T* x, const Cell<T, V>* slot, Pairs<V>& f) {
-  if (i < tm.held)
-    load_vec<T, V>(slot[(size_t)i * blockDim.x].e, f);
-  else
-    load_vec<T, V>(x + k.base + (long long)p * s.c, f);
+constexpr int kBatch = 4;
+
+// A thread's (n, mean, m2), a triple for each channel of its vector or (ONE)
+// for all of them, merged with those of `most` <= kBatch pixels; get(b, f)
+// fetches pixel b.
+template <int V, bool ONE, typename M, typename GET>
+__device__ __forceinline__ void add_batch(int most, float& n, M& mean, M& m2, GET&& get) {
+  constexpr int P = Pairs<V>::n, EP = ONE ? 1 : P;
+  Pairs<V> f[kBatch];
+  float2 sum[EP], q[EP];
+#pragma unroll
+  for (int e = 0; e < EP; ++e) sum[e] = q[e] = both(0.f);
+#pragma unroll
+  for (int b = 0; b < kBatch; ++b) {
+    if (b >= most) continue;
+    get(b, f[b]);
+#pragma unroll
+    for (int e = 0; e < P; ++e) sum[ONE ? 0 : e] = add2(sum[ONE ? 0 : e], f[b].p[e]);
+  }
+  const float cnt = (float)(ONE ? most * V : most), t = n + cnt;
+  const float w = rcp_approx(cnt), wn = cnt * rcp_approx(t), c = n * wn;
+#pragma unroll
+  for (int e = 0; e < EP; ++e)  // the means
+    sum[e] = ONE ? both((sum[e].x + sum[e].y) * w) : mul2(sum[e], both(w));
+#pragma unroll
+  for (int b = 0; b < kBatch; ++b) {
+    if (b >= most) continue;
+#pragma unroll
+    for (int e = 0; e < P; ++e) {
+      const float2 m = sum[ONE ? 0 : e];
+      float2 d = add2(f[b].p[e], make_float2(-m.x, -m.y));
+      if (V == 1) d.y = 0.f;
+      q[ONE ? 0 : e] = fma2(d, d, q[ONE ? 0 : e]);
+    }
+  }
+#pragma unroll
+  for (int e = 0; e < EP; ++e) {
+    if (ONE) q[e].x += q[e].y;
+    const float2 d = add2(sum[e], make_float2(-mean.p[e].x, -mean.p[e].y));
+    mean.p[e] = fma2(d, both(wn), mean.p[e]);
+    m2.p[e] = add2(m2.p[e], fma2(mul2(d, d), both(c), q[e]));
+  }
+  n = t;
 }
 
 // ONE: a vector's channels are all of one group; else channels are kept apart
-// until the block's are merged.
+// until the block's are merged.  Dynamic shared memory: the slots, then the
+// blocks' triples of the unit's groups, [3][cluster][ng].
 template <typename T, int V, bool ONE, int ACT>
-__global__ void __launch_bounds__(kTeam, 2)
+__global__ void __launch_bounds__(kTeam, ONE || V < 8 ? 2 : 1)
     fwd_nhwc(Shape s, ColTeam tm, const T* x, const float* gamma, const float* beta, T* y,
              float* mean_out, float* rstd_out) {
-  constexpr int E = ONE ? 1 : V;
-  constexpr int kBatch = 4;
+  constexpr int P = Pairs<V>::n, E = ONE ? 1 : V, EP = ONE ? 1 : P;
   extern __shared__ uint4 hold[];
   __shared__ float2 ent[kTeam];
   __shared__ float cnts[kTeam];
-  __shared__ float sn[kMaxCluster * kMaxGroups], sm[kMaxCluster * kMaxGroups],
-      sq[kMaxCluster * kMaxGroups];
   const bool many = tm.cluster > 1;
   if (many) cluster_arrive();
   pdl_wait();
   pdl_release();
   const UnitCol<V> k(s, tm);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, warps = blockDim.x >> 5;
-  Cell<T, V>* mine = reinterpret_cast<Cell<T, V>*>(hold) + threadIdx.x;
-  hold_col<T, V>(s, tm, k, x, mine);
-  constexpr int P = Pairs<V>::n;
-  constexpr int EP = ONE ? 1 : P;  // pairs of sums
+  const int stride = kPieces<T, V> * kUnit<T, V> * blockDim.x;
+  char* mine = reinterpret_cast<char*>(hold) + threadIdx.x * kUnit<T, V>;
+  float* sn = reinterpret_cast<float*>(reinterpret_cast<char*>(hold) + (size_t)tm.held * stride);
+  float* sm = sn + tm.cluster * tm.ng;
+  float* sq = sm + tm.cluster * tm.ng;
+  const int count = k.p1 > k.p0 ? (k.p1 - k.p0 + tm.rl - 1) / tm.rl : 0;  // this thread's pixels
+  const int held = count < tm.held ? count : tm.held;
+  const long long step = (long long)tm.rl * s.c;
+  const T* px = x + k.base + (long long)k.p0 * s.c;
+  hold_col<T, V>(px, step, held, mine, stride);
   float n = 0.f;
   Pairs<2 * EP> mean, m2;  // ONE: the first of a pair alone
 #pragma unroll
   for (int e = 0; e < EP; ++e) mean.p[e] = m2.p[e] = both(0.f);
-  auto batches = [&](int i0, int i1) {
-    for (int i = i0; i < i1; i += kBatch) {
-      const int p = k.p0 + i * tm.rl;
-      if (p >= k.p1) break;
-      Pairs<V> f[kBatch];
-      float2 sum[EP], q[EP];
-#pragma unroll
-      for (int e = 0; e < EP; ++e) sum[e] = q[e] = both(0.f);
-      float cnt = 0.f;
-#pragma unroll
-      for (int b = 0; b < kBatch; ++b) {
-        if (i + b >= i1 || p + b * tm.rl >= k.p1) continue;
-        fetch<T, V>(s, tm, k, i + b, p + b * tm.rl, x, mine, f[b]);
-        cnt += ONE ? (float)V : 1.f;
-#pragma unroll
-        for (int e = 0; e < P; ++e) sum[ONE ? 0 : e] = add2(sum[ONE ? 0 : e], f[b].p[e]);
-      }
-      const float w = rcp_approx(cnt), t = n + cnt, wn = cnt * rcp_approx(t), c = n * wn;
-#pragma unroll
-      for (int e = 0; e < EP; ++e)  // the means
-        sum[e] = ONE ? both((sum[e].x + sum[e].y) * w) : mul2(sum[e], both(w));
-#pragma unroll
-      for (int b = 0; b < kBatch; ++b) {
-        if (i + b >= i1 || p + b * tm.rl >= k.p1) continue;
-#pragma unroll
-        for (int e = 0; e < P; ++e) {
-          const float2 m = sum[ONE ? 0 : e];
-          float2 d = add2(f[b].p[e], make_float2(-m.x, -m.y));
-          if (V == 1) d.y = 0.f;
-          q[ONE ? 0 : e] = fma2(d, d, q[ONE ? 0 : e]);
-        }
-      }
-#pragma unroll
-      for (int e = 0; e < EP; ++e) {
-        if (ONE) q[e].x += q[e].y;
-        const float2 d = add2(sum[e], make_float2(-mean.p[e].x, -mean.p[e].y));
-        mean.p[e] = fma2(d, both(wn), mean.p[e]);
-        m2.p[e] = add2(m2.p[e], fma2(mul2(d, d), both(c), q[e]));
-      }
-      n = t;
-    }
-  };
   // what is not held first: its loads go on behind the copies
-  batches(tm.held, tm.slots);
+  for (int i = held; i < count; i += kBatch)
+    add_batch<V, ONE>(min(count - i, kBatch), n, mean, m2,
+                      [&](int b, Pairs<V>& f) { load_vec<T, V>(px + (i + b) * step, f); });
   copy_wait();
-  batches(0, tm.held);
+  {
+    const char* slot = mine;
+    auto get = [&](int b, Pairs<V>& f) { take<T, V>(slot + b * stride, f); };
+    int i = 0;
+    for (; i + kBatch <= held; i += kBatch, slot += kBatch * stride)
+      add_batch<V, ONE>(kBatch, n, mean, m2, get);
+    if (i < held) add_batch<V, ONE>(held - i, n, mean, m2, get);
+  }
   // the block's groups, a warp each: entries of every pixel lane, channel by
   // channel of the vector where those are apart
   const int cols = ONE ? s.cpg / V : tm.cb;  // columns of a group (all, where they mix)
-  float gn = 0.f, gm = 0.f, gq = 0.f;        // of group `warp`, then warp + warps, ...: see below
   cnts[threadIdx.x] = n;
   if (many) cluster_wait();
   for (int g0 = 0; g0 < tm.ng; g0 += warps) {
     const int g = g0 + warp;
-    gn = gm = gq = 0.f;
+    float gn = 0.f, gm = 0.f, gq = 0.f;
 #pragma unroll 1
     for (int e = 0; e < E; ++e) {
       __syncthreads();
-      float a = mean[0], b = m2[0];
+      float a = mean.p[0].x, b = m2.p[0].x;
 #pragma unroll
       for (int j = 1; j < E; ++j)
         if (j == e) a = mean[j], b = m2[j];
@@ -160,7 +191,7 @@ __global__ void __launch_bounds__(kTeam, 2)
       const int entries = cols * tm.rl;
       float ln = 0.f, lm = 0.f, lq = 0.f;
       for (int i = lane; i < entries; i += 32) {
-        const int l = i / cols, j = i - l * cols;
+        const int l = cols == 1 ? i : i / cols, j = i - l * cols;
         const int th = l * tm.cb + (ONE ? g * cols + j : j);
         if (!ONE && (j * V + e) / s.cpg != g) continue;
         const float2 v = ent[th];
@@ -189,21 +220,22 @@ __global__ void __launch_bounds__(kTeam, 2)
   } else {
     __syncthreads();
   }
-  for (int g = threadIdx.x; g < tm.ng; g += blockDim.x) {
+  // a group's blocks, a lane each
+  for (int g = warp; g < tm.ng; g += warps) {
     const float total = (float)s.hw * (float)s.cpg;
-    float sum = 0.f, q = 0.f;
-    for (int j = 0; j < tm.cluster; ++j) sum = fmaf(sn[j * tm.ng + g], sm[j * tm.ng + g], sum);
-    const float mu = sum / total;
-    for (int j = 0; j < tm.cluster; ++j) {
-      const float d = sm[j * tm.ng + g] - mu;
-      if (sn[j * tm.ng + g] > 0.f) q += fmaf(sn[j * tm.ng + g] * d, d, sq[j * tm.ng + g]);
-    }
-    const float rs = 1.f / sqrtf(q / total + s.eps);
-    ent[g] = make_float2(mu, rs);
-    if (k.rank == 0) {
-      const long long at = (long long)k.img * s.groups + k.slice * tm.ng + g;
-      if (mean_out) mean_out[at] = mu;
-      if (rstd_out) rstd_out[at] = rs;
+    const int at = lane * tm.ng + g;
+    const bool in = lane < tm.cluster && sn[at] > 0.f;
+    const float mu = warp_sum(in ? sn[at] * sm[at] : 0.f) / total;
+    const float d = in ? sm[at] - mu : 0.f;
+    const float var = warp_sum(in ? fmaf(sn[at] * d, d, sq[at]) : 0.f) / total;
+    const float rs = 1.f / sqrtf(var + s.eps);
+    if (lane == 0) {
+      ent[g] = make_float2(mu, rs);
+      if (k.rank == 0) {
+        const long long to = (long long)k.img * s.groups + k.slice * tm.ng + g;
+        if (mean_out) mean_out[to] = mu;
+        if (rstd_out) rstd_out[to] = rs;
+      }
     }
   }
   __syncthreads();
@@ -213,50 +245,66 @@ __global__ void __launch_bounds__(kTeam, 2)
   if (V == 1) a.p[0] = b.p[0] = mu.p[0] = both(0.f);
 #pragma unroll
   for (int e = 0; e < V; ++e) {
-    const float2 st = ent[(k.col * V + e) / s.cpg];
+    const float2 st = ent[(k.col * V + (ONE ? 0 : e)) / s.cpg];
     mu[ONE ? 0 : e] = -st.x;
     a[e] = st.y * (gamma ? gamma[k.ch + e] : 1.f);
     b[e] = beta ? beta[k.ch + e] : 0.f;
   }
-#pragma unroll 2
-  for (int i = 0, p = k.p0; p < k.p1; ++i, p += tm.rl) {
-    Pairs<V> f;
-    fetch<T, V>(s, tm, k, i, p, x, mine, f);
+  T* to = y + k.base + (long long)k.p0 * s.c;
+  auto apply = [&](Pairs<V>& f) {
 #pragma unroll
     for (int e = 0; e < P; ++e)
-      f.p[e] = fma2(add2(f.p[e], ONE ? both(mu[0]) : mu.p[ONE ? 0 : e]), a.p[e], b.p[e]);
-#pragma unroll
-    for (int e = 0; e < V; ++e) f[e] = act_fwd<ACT>(f[e], s.floor);
-    store_vec<T, V>(y + k.base + (long long)p * s.c, f);
+      f.p[e] = act_fwd2<ACT>(fma2(add2(f.p[e], ONE ? both(mu[0]) : mu.p[ONE ? 0 : e]), a.p[e],
+                                  b.p[e]), s.floor);
+    store_vec<T, V>(to, f);
+    to += step;
+  };
+  const char* slot = mine;
+#pragma unroll 2
+  for (int i = 0; i < held; ++i, slot += stride) {
+    Pairs<V> f;
+    take<T, V>(slot, f);
+    apply(f);
+  }
+  px += held * step;
+  for (int i = held; i < count; ++i, px += step) {
+    Pairs<V> f;
+    load_vec<T, V>(px, f);
+    apply(f);
   }
 }
 
 // part[rank][image * c + channel]: the sums of dz and dz * xh over a block's
-// pixels.
+// pixels.  Dynamic shared memory: the slots of x, of grad_y, a table of channel
+// sums, then the blocks' sums of the unit's groups, [2][cluster][ng].
 template <typename T, typename TG, int V, bool ONE, int ACT>
-__global__ void __launch_bounds__(kTeam, 2)
+__global__ void __launch_bounds__(kTeam, ONE || V < 8 ? 2 : 1)
     bwd_nhwc(Shape s, ColTeam tm, const T* x, const TG* gy, const float* gamma, const float* beta,
              const float* mean, const float* rstd, T* gx, float2* part) {
+  constexpr int P = Pairs<V>::n;
+  constexpr bool KEEP = keep_dz(sizeof(TG) == 4, ACT);
+  using SG = std::conditional_t<KEEP, float, TG>;  // what a slot of grad_y has room for
   extern __shared__ uint4 hold[];
   __shared__ float2 ps[kTeam];
-  __shared__ float sa[kMaxCluster * kMaxGroups], sb[kMaxCluster * kMaxGroups];
   const bool many = tm.cluster > 1;
   if (many) cluster_arrive();
   pdl_wait();
   pdl_release();
   const UnitCol<V> k(s, tm);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, warps = blockDim.x >> 5;
-  Cell<T, V>* mine = reinterpret_cast<Cell<T, V>*>(hold) + threadIdx.x;
-  Cell<TG, V>* mine_g =
-      reinterpret_cast<Cell<TG, V>*>(reinterpret_cast<Cell<T, V>*>(hold) +
-                                     (size_t)tm.held * blockDim.x) + threadIdx.x;
-  float2* tab = reinterpret_cast<float2*>(reinterpret_cast<char*>(hold) +
-                                          (size_t)tm.held * blockDim.x * V *
-                                              (sizeof(T) + sizeof(TG)));
-  hold_col<T, V>(s, tm, k, x, mine);
-  hold_col<TG, V>(s, tm, k, gy, mine_g);
+  const int stride = V * sizeof(T) * blockDim.x, stride_g = V * sizeof(SG) * blockDim.x;
+  char* mine = reinterpret_cast<char*>(hold) + threadIdx.x * kUnit<T, V>;
+  char* held_g = reinterpret_cast<char*>(hold) + (size_t)tm.held * stride;
+  char* mine_g = held_g + threadIdx.x * kUnit<SG, V>;
+  float2* tab = reinterpret_cast<float2*>(held_g + (size_t)tm.held * stride_g);
+  float* sa = reinterpret_cast<float*>(tab + tm.rows * tm.width);
+  float* sb = sa + tm.cluster * tm.ng;
+  const int count = k.p1 > k.p0 ? (k.p1 - k.p0 + tm.rl - 1) / tm.rl : 0;
+  const int held = count < tm.held ? count : tm.held;
+  const long long step = (long long)tm.rl * s.c, off = k.base + (long long)k.p0 * s.c;
+  hold_col<T, V>(x + off, step, held, mine, stride);
+  hold_col<TG, V>(gy + off, step, held, mine_g, stride_g);
   const long long g0 = (long long)k.img * s.groups + k.slice * tm.ng;
-  constexpr int P = Pairs<V>::n;
   Pairs<ONE ? 1 : V> mu, rs;  // minus the mean
   Pairs<V> g, b, s1, s2;
 #pragma unroll
@@ -266,53 +314,66 @@ __global__ void __launch_bounds__(kTeam, 2)
   if (k.live) {
 #pragma unroll
     for (int e = 0; e < V; ++e) {
-      const long long at = g0 + (k.col * V + e) / s.cpg;
-      if (!ONE || e == 0) mu[ONE ? 0 : e] = -mean[at], rs[ONE ? 0 : e] = rstd[at];
+      if (!ONE || e == 0) {
+        const long long at = g0 + (k.col * V + e) / s.cpg;
+        mu[ONE ? 0 : e] = -mean[at], rs[ONE ? 0 : e] = rstd[at];
+      }
       g[e] = gamma ? gamma[k.ch + e] : 1.f;
       b[e] = beta ? beta[k.ch + e] : 0.f;
     }
   }
-  // the pair e of xh, and of dz in place of grad_y
-  auto grads = [&](const Pairs<V>& f, Pairs<V>& d, int e) {
-    const float2 m = ONE ? both(mu[0]) : mu.p[ONE ? 0 : e], r = ONE ? both(rs[0]) : rs.p[ONE ? 0 : e];
-    const float2 xh = mul2(add2(f.p[e], m), r);
-    const float2 z = fma2(xh, g.p[e], b.p[e]);
-    d.p[e] = make_float2(act_bwd<ACT>(z.x, d.p[e].x, s.floor),
-                         V == 1 ? 0.f : act_bwd<ACT>(z.y, d.p[e].y, s.floor));
-    return xh;
+  auto xhat = [&](const Pairs<V>& f, int e) {
+    const float2 m = ONE ? both(mu[0]) : mu.p[ONE ? 0 : e];
+    return mul2(add2(f.p[e], m), ONE ? both(rs[0]) : rs.p[ONE ? 0 : e]);
   };
-  auto sums = [&](int i0, int i1) {
-#pragma unroll 2
-    for (int i = i0; i < i1; ++i) {
-      const int p = k.p0 + i * tm.rl;
-      if (p >= k.p1) break;
-      Pairs<V> f, d;
-      fetch<T, V>(s, tm, k, i, p, x, mine, f);
-      fetch<TG, V>(s, tm, k, i, p, gy, mine_g, d);
+  // dz in place of grad_y
+  auto slope = [&](const float2 xh, Pairs<V>& d, int e) {
+    d.p[e] = act_bwd2<ACT>(fma2(xh, g.p[e], b.p[e]), d.p[e], s.floor);
+    if (V == 1) d.p[e].y = 0.f;
+  };
+  auto sums = [&](const Pairs<V>& f, Pairs<V>& d) {
 #pragma unroll
-      for (int e = 0; e < P; ++e) {
-        const float2 xh = grads(f, d, e);
-        s1.p[e] = add2(s1.p[e], d.p[e]);
-        s2.p[e] = fma2(d.p[e], xh, s2.p[e]);
-      }
+    for (int e = 0; e < P; ++e) {
+      const float2 xh = xhat(f, e);
+      slope(xh, d, e);
+      s1.p[e] = add2(s1.p[e], d.p[e]);
+      s2.p[e] = fma2(d.p[e], xh, s2.p[e]);
     }
   };
-  sums(tm.held, tm.slots);
+  // what is not held first: its loads go on behind the copies
+#pragma unroll 2
+  for (int i = held; i < count; ++i) {
+    Pairs<V> f, d;
+    load_vec<T, V>(x + off + i * step, f);
+    load_vec<TG, V>(gy + off + i * step, d);
+    sums(f, d);
+  }
   copy_wait();
-  sums(0, tm.held);
+  {
+    const char* slot = mine;
+    char* slot_g = mine_g;
+#pragma unroll 2
+    for (int i = 0; i < held; ++i, slot += stride, slot_g += stride_g) {
+      Pairs<V> f, d;
+      take<T, V>(slot, f);
+      take<TG, V>(slot_g, d);
+      sums(f, d);
+      if (KEEP) leave<V>(slot_g, d);
+    }
+  }
   // the block's sum of each channel: pixel lanes of a warp first (where a warp
-  // holds whole pixels), then `rows` rows of the table by `lanes` threads a
-  // channel, then by one
-  int rows = tm.rl, row = k.lane;
+  // holds whole pixels), then the table's rows by `lanes` threads a channel,
+  // then by one
+  int row = k.lane;
   bool put = k.live;
   if (32 % tm.cb == 0) {
+    for (int o = 16; o >= tm.cb; o >>= 1) {
 #pragma unroll
-    for (int e = 0; e < V; ++e)
-      for (int o = 16; o >= tm.cb; o >>= 1) {
+      for (int e = 0; e < V; ++e) {
         s1[e] += __shfl_xor_sync(0xffffffffu, s1[e], o);
         s2[e] += __shfl_xor_sync(0xffffffffu, s2[e], o);
       }
-    rows = warps;
+    }
     row = warp;
     put = lane < tm.cb;
   }
@@ -325,7 +386,7 @@ __global__ void __launch_bounds__(kTeam, 2)
   for (int i = threadIdx.x; i < lanes * tm.width; i += blockDim.x) {
     const int l0 = i / tm.width, c = i - l0 * tm.width;
     float2 t = make_float2(0.f, 0.f);
-    for (int l = l0; l < rows; l += lanes) {
+    for (int l = l0; l < tm.rows; l += lanes) {
       const float2 v = tab[l * tm.width + c];
       t.x += v.x;
       t.y += v.y;
@@ -376,14 +437,12 @@ __global__ void __launch_bounds__(kTeam, 2)
   } else {
     __syncthreads();
   }
-  for (int q = threadIdx.x; q < tm.ng; q += blockDim.x) {
+  for (int q = warp; q < tm.ng; q += warps) {  // a group's blocks, a lane each
     const float total = (float)s.hw * (float)s.cpg;
-    float a1 = 0.f, b1 = 0.f;
-    for (int j = 0; j < tm.cluster; ++j) {
-      a1 += sa[j * tm.ng + q];
-      b1 += sb[j * tm.ng + q];
-    }
-    ps[q] = make_float2(a1 / total, b1 / total);
+    const bool in = lane < tm.cluster;
+    const float a1 = warp_sum(in ? sa[lane * tm.ng + q] : 0.f);
+    const float b1 = warp_sum(in ? sb[lane * tm.ng + q] : 0.f);
+    if (lane == 0) ps[q] = make_float2(a1 / total, b1 / total);
   }
   __syncthreads();
   if (!k.live) return;
@@ -396,20 +455,33 @@ __global__ void __launch_bounds__(kTeam, 2)
     k1[e] = -rs[e] * v.x;
     k2[e] = -rs[e] * v.y;
   }
-#pragma unroll 2
-  for (int i = 0, p = k.p0; p < k.p1; ++i, p += tm.rl) {
-    Pairs<V> f, d;
-    fetch<T, V>(s, tm, k, i, p, x, mine, f);
-    fetch<TG, V>(s, tm, k, i, p, gy, mine_g, d);
+  T* to = gx + off;
+  auto result = [&](Pairs<V>& f, Pairs<V>& d, bool is_dz) {
 #pragma unroll
     for (int e = 0; e < P; ++e) {
-      const float2 xh = grads(f, d, e);
-      const float2 r = ONE ? both(rs[0]) : rs.p[ONE ? 0 : e];
-      const float2 c1 = ONE ? both(k1[0]) : k1.p[ONE ? 0 : e];
-      const float2 c2 = ONE ? both(k2[0]) : k2.p[ONE ? 0 : e];
-      f.p[e] = fma2(xh, c2, fma2(d.p[e], mul2(g.p[e], r), c1));
+      const float2 xh = xhat(f, e);
+      if (!is_dz) slope(xh, d, e);
+      const float2 gr = mul2(g.p[e], ONE ? both(rs[0]) : rs.p[ONE ? 0 : e]);
+      f.p[e] = fma2(xh, ONE ? both(k2[0]) : k2.p[ONE ? 0 : e],
+                    fma2(d.p[e], gr, ONE ? both(k1[0]) : k1.p[ONE ? 0 : e]));
     }
-    store_vec<T, V>(gx + k.base + (long long)p * s.c, f);
+    store_vec<T, V>(to, f);
+    to += step;
+  };
+  const char* slot = mine;
+  const char* slot_g = mine_g;
+#pragma unroll 2
+  for (int i = 0; i < held; ++i, slot += stride, slot_g += stride_g) {
+    Pairs<V> f, d;
+    take<T, V>(slot, f);
+    take<SG, V>(slot_g, d);
+    result(f, d, KEEP);
+  }
+  for (int i = held; i < count; ++i) {
+    Pairs<V> f, d;
+    load_vec<T, V>(x + off + i * step, f);
+    load_vec<TG, V>(gy + off + i * step, d);
+    result(f, d, false);
   }
 }
 

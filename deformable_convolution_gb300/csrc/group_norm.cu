@@ -545,13 +545,19 @@ constexpr int kSms = 152;
 
 int gcd(int a, int b) { return b ? gcd(b, a % b) : a; }
 
-constexpr int kBlockBytes = 92 * 1024;  // of a unit in a block: two blocks to an SM
-constexpr int kLeastBytes = 16 * 1024;   // not split further to make more blocks
+constexpr int kBlockBytes = 92 * 1024;  // most of a unit in a block: two blocks to an SM
+constexpr int kFourBytes = 50 * 1024;   // four blocks to an SM
+constexpr int kLeastBytes = 16 * 1024;  // not split further to make more blocks
 
 // Blocks of a unit of `bytes`: enough that it fits, and that every SM gets two,
-// as long as a block keeps work worth its launch.
-int cluster_of(double bytes, long long units) {
+// as long as a block keeps work worth its launch.  The backward, whose blocks
+// compute for longer, overlaps better as four to an SM where the cluster stays
+// small (stack's 256 units of 150 KB: 15.6 us as three blocks of 50 KB, 18.6
+// as two of 75).
+int cluster_of(double bytes, long long units, bool backward) {
   long long k = (long long)ceil(bytes / kBlockBytes), most = (long long)(bytes / kLeastBytes);
+  const long long four = (long long)ceil(bytes / kFourBytes);
+  if (backward && four <= 8) k = four;
   long long spread = ceil_div_ll(2 * kSms, units);
   if (spread > most) spread = most;
   if (k < spread) k = spread;
@@ -581,7 +587,7 @@ NormPlan make_plan(const NormArgs& a, bool backward) {
     const long long blks = ceil_div_ll(a.cpg, 32 / t.lpr);
     const double bytes = (double)a.cpg * vr * 16 * planes;
     RowTeam& r = p.row;
-    r.cluster = cluster_of(bytes, groups);
+    r.cluster = cluster_of(bytes, groups, backward);
     const long long run = (long long)a.cpg * vr;
     if (!backward && a.hw % vec == 0 && run < 1 << 30) {
       r.span = (int)ceil_div_ll(run, r.cluster);
@@ -654,7 +660,7 @@ NormPlan make_plan(const NormArgs& a, bool backward) {
     c.slices = a.c / c.width;
     c.cb = c.width / v;
     c.ng = c.width / a.cpg;
-    c.cluster = cluster_of((double)a.hw * c.cb * held_bytes, (long long)a.n * c.slices);
+    c.cluster = cluster_of((double)a.hw * c.cb * held_bytes, (long long)a.n * c.slices, backward);
     if ((long long)a.n * c.slices * c.cluster >= 2 * kSms &&
         (double)a.hw * c.cb * held_bytes <= (double)kMaxCluster * kBlockBytes)
       break;

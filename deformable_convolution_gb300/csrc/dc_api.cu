@@ -779,9 +779,24 @@ dc_status make_norm(const dc_norm_problem* p, NormArgs* a) {
   return norm_supported(*a) ? DC_OK : DC_ERR_UNSUPPORTED;
 }
 
-dc_status run(const char* name, cudaStream_t s, cudaError_t (*launch)(const NormArgs&, cudaStream_t),
-              const NormArgs& a) {
-  return cuda_status(timed(name, s, [&] { return launch(a, s); }));
+// A pass's launches, in order.
+dc_status run_norm(const NormArgs& a, bool backward, cudaStream_t s) {
+  const NormTurns t = norm_turns(a, backward);
+  if (t.one)
+    return cuda_status(timed(backward ? "norm_bwd" : "norm_fwd", s,
+                             [&] { return launch_norm(a, backward, s); }));
+  for (int i = 0; i < a.n; i += t.images) {
+    const int count = a.n - i < t.images ? a.n - i : t.images;
+    for (int second = 0; second < 2; ++second) {
+      const char* name = backward ? (second ? "norm_grads" : "norm_sums")
+                                  : (second ? "norm_apply" : "norm_stats");
+      const dc_status st = cuda_status(timed(name, s, [&] {
+        return launch_norm_two(a, backward, second != 0, i, count, s);
+      }));
+      if (st != DC_OK) return st;
+    }
+  }
+  return DC_OK;
 }
 
 bool aligned_to(const void* p, size_t n) { return ((uintptr_t)p & (n - 1)) == 0; }
@@ -856,10 +871,7 @@ dc_status dc_group_norm_fwd(const dc_norm_problem* prob, const void* x, const fl
   a.mean = mean;
   a.rstd = rstd;
   a.ws = static_cast<char*>(ws);
-  if (norm_one_launch(a, false)) return run("norm_fwd", s, launch_norm_fwd, a);
-  if ((st = run("norm_stats", s, launch_norm_stats, a)) != DC_OK) return st;
-  if ((st = run("norm_merge", s, launch_norm_merge, a)) != DC_OK) return st;
-  return run("norm_apply", s, launch_norm_apply, a);
+  return run_norm(a, false, s);
 }
 
 dc_status dc_group_norm_bwd(const dc_norm_problem* prob, const void* x, const float* gamma,
@@ -886,15 +898,9 @@ dc_status dc_group_norm_bwd(const dc_norm_problem* prob, const void* x, const fl
   a.ggamma = grad_gamma;
   a.gbeta = grad_beta;
   a.ws = static_cast<char*>(ws);
-  if (a.n && norm_one_launch(a, true)) {
-    if ((st = run("norm_bwd", s, launch_norm_bwd, a)) != DC_OK) return st;
-  } else if (a.n) {
-    if ((st = run("norm_sums", s, launch_norm_sums, a)) != DC_OK) return st;
-    if ((st = run("norm_merge_bwd", s, launch_norm_merge_bwd, a)) != DC_OK) return st;
-    if ((st = run("norm_apply_bwd", s, launch_norm_apply_bwd, a)) != DC_OK) return st;
-  }
+  if (a.n && (st = run_norm(a, true, s)) != DC_OK) return st;
   if (!grad_gamma && !grad_beta) return DC_OK;
-  return run("norm_params", s, launch_norm_params, a);
+  return cuda_status(timed("norm_params", s, [&] { return launch_norm_params(a, s); }));
 }
 
 dc_status dc_adamw_step(const dc_adamw_tensor* tensors, int count, const dc_adamw_hyper* hyper,

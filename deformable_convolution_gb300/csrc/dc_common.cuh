@@ -370,19 +370,18 @@ struct NormArgs {
 bool norm_supported(const NormArgs& a);  // grids and indices in range
 // Workspace bytes of the forward or backward pass.
 size_t norm_workspace_bytes(const NormArgs& a, bool backward);
-// Whether the pass runs as one launch (launch_norm_fwd; launch_norm_bwd, then
-// launch_norm_params), or in steps.
-bool norm_one_launch(const NormArgs& a, bool backward);
-cudaError_t launch_norm_fwd(const NormArgs& a, cudaStream_t s);
-cudaError_t launch_norm_bwd(const NormArgs& a, cudaStream_t s);
-// One launch each; the ABI layer runs them in order.
-cudaError_t launch_norm_stats(const NormArgs& a, cudaStream_t s);        // per-channel statistics of parts
-cudaError_t launch_norm_merge(const NormArgs& a, cudaStream_t s);        // mean and rstd of every group
-cudaError_t launch_norm_apply(const NormArgs& a, cudaStream_t s);        // y
-cudaError_t launch_norm_sums(const NormArgs& a, cudaStream_t s);         // per-channel gradient sums of parts
-cudaError_t launch_norm_merge_bwd(const NormArgs& a, cudaStream_t s);    // of images and groups
-cudaError_t launch_norm_apply_bwd(const NormArgs& a, cudaStream_t s);    // grad_x
-cudaError_t launch_norm_params(const NormArgs& a, cudaStream_t s);       // grad_gamma, grad_beta
+// How a pass runs: as one launch (launch_norm), or as two (launch_norm_two, the
+// second reading again what the first left in L2) for `images` images at a
+// time.  The backward ends with launch_norm_params (grad_gamma, grad_beta).
+struct NormTurns {
+  bool one;
+  int images;
+};
+NormTurns norm_turns(const NormArgs& a, bool backward);
+cudaError_t launch_norm(const NormArgs& a, bool backward, cudaStream_t s);
+cudaError_t launch_norm_two(const NormArgs& a, bool backward, bool second, int img0, int count,
+                            cudaStream_t s);
+cudaError_t launch_norm_params(const NormArgs& a, cudaStream_t s);
 
 // AdamW and the gradient norm (adamw.cu).
 struct AdamScalars {

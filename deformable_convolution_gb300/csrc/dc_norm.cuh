@@ -253,63 +253,72 @@ __device__ __forceinline__ float act_bwd(float z, float d, float floor) {
 // lanes of a warp walk a row's 16-byte vectors (the first and last may hang
 // over the row's ends), a warp takes 32 / lpr rows, and a long row is cut into
 // `parts` segments of `seg` vectors.
-// NHWC: a thread keeps one vector of v channels and walks pixels; a block
-// takes cb such columns and `seg` pixels of an image.
-struct Tiling {
-  int parts, seg;
-  int lpr;             // NCHW
-  int v, cols, cb, rl;  // NHWC: vector width, vectors of a pixel, of a block, pixel lanes
-};
-
 struct Shape {
   int n, c, groups, cpg, hw;
   float floor;  // of activation kind 0
   float eps;
-  Tiling t;
+  int v;                // NHWC: channels of a thread's vector
+  int parts, seg, lpr;  // NCHW
 };
 
-// One launch for a pass: a cluster of blocks holds a unit in shared memory from
-// its statistics to its results.
+// How the blocks share the work.  A unit has `blocks` of them: a cluster that
+// holds the unit in shared memory from its statistics to its results (one
+// launch for a pass), or blocks that leave their statistics in memory for a
+// second launch, which reads the unit again (from L2, where it fits there).
 // NCHW: a unit is a group of an image; its rows are cut into tasks as above,
-// dealt over the warps of the cluster's blocks in `rounds`.
+// dealt over the warps of the unit's blocks in `rounds`.
 struct RowTeam {
-  int cluster, warps, units;  // blocks of a unit, warps of a unit in a block, units of a block
-  int tasks, rounds;          // of a unit, of a warp
-  int held, slots;            // rounds kept in shared memory, vectors of a lane in a round
+  int blocks, warps, units;  // of a unit, of a unit in a block, units of a block
+  int tasks, rounds;         // of a unit, of a warp
+  int held;                  // rounds kept in shared memory
   // whole-vector rows, forward: the unit's vectors in one run, `span` of them
-  // to a block (0: by tasks); held and slots count a thread's vectors
-  int span, step_c, step_v;   // threads of a unit in a block, as channels and vectors
+  // to a block (0: by tasks); held counts a thread's vectors
+  int span, step_c, step_v;  // threads of a unit in a block, as channels and vectors
 };
-// NHWC: a unit is a slice of whole groups, `cb` vectors wide, of an image; a
-// thread keeps one of its columns and walks pixels, `rl` threads to a column.
+// NHWC: a unit is a slice of channels, `cb` vectors wide, of an image (whole
+// groups, in a cluster); a thread keeps one of its columns and walks pixels,
+// `rl` threads to a column.
 struct ColTeam {
-  int cluster, slices, width;  // blocks of a unit, units of an image, channels of a unit
-  int cb, rl, ng;              // ng: groups of a unit
-  int span;                    // pixels of a block
-  int held, slots;             // pixels of a thread: kept in shared memory, all
-  int rows;                    // of the backward's table of channel sums
+  int blocks, slices, width;  // blocks of a unit, units of an image, channels of a unit
+  int cb, rl, ng;             // ng: groups of a unit (cluster)
+  int span;                   // pixels of a block
+  int held;                   // pixels of a thread kept in shared memory
+  int rows;                   // of the backward's table of channel sums
+  int shares;                 // most slices that share a group (two launches)
 };
-constexpr int kTeam = 512;       // most threads of a block
+constexpr int kTeam = 512;       // most threads of a cluster's block
+constexpr int kTwo = 256;        // threads of a block of two launches
 constexpr int kMaxCluster = 16;
-constexpr int kMaxGroups = 64;   // of a unit (NHWC)
+constexpr int kMaxGroups = 64;   // of a unit (NHWC, in a cluster)
 
 // Whether the backward keeps dz, in float32, where it held grad_y: where the
 // slope costs more than a wider slot (SiLU, GELU), or the slot is that wide.
 constexpr bool keep_dz(bool grad_f32, int act_kind) { return grad_f32 || act_kind != 0; }
 
-// How a call runs: as one launch of teams, or in the three-launch form.
 struct NormPlan {
   Shape s;
-  bool team;
+  bool cluster;  // one launch; else two
   RowTeam row;
   ColTeam col;
-  unsigned blocks;
+  unsigned blocks;  // of a launch (two launches: of `images` images)
   int threads;
   size_t smem;
-  int parts;  // rows of channel sums an image leaves (backward)
+  int parts;   // rows of channel sums that an image leaves (backward)
+  int images;  // two launches: at a time, so that the second finds them in L2
 };
-cudaError_t launch_team_nchw(const NormPlan& p, const NormArgs& a, bool backward, cudaStream_t s);
-cudaError_t launch_team_nhwc(const NormPlan& p, const NormArgs& a, bool backward, cudaStream_t s);
+// The forward, or the backward up to the channels' sums.  Two launches: the
+// first (second = false) or the second of images [img0, img0 + count).
+cudaError_t launch_nchw(const NormPlan& p, const NormArgs& a, bool backward, cudaStream_t s);
+cudaError_t launch_nhwc(const NormPlan& p, const NormArgs& a, bool backward, cudaStream_t s);
+cudaError_t launch_two_nchw(const NormPlan& p, const NormArgs& a, bool backward, bool second,
+                            int img0, int count, cudaStream_t s);
+cudaError_t launch_two_nhwc(const NormPlan& p, const NormArgs& a, bool backward, bool second,
+                            int img0, int count, cudaStream_t s);
+// Workspace of the two launches: the channels' sums (backward), then an entry
+// for each group of an image, block of it and slice that shares it.
+inline size_t norm_part_bytes(const NormPlan& p, const NormArgs& a, bool backward) {
+  return backward ? ((size_t)p.parts * a.n * a.c * sizeof(float2) + 255) / 256 * 256 : 0;
+}
 
 __host__ __device__ inline int row_vectors(int hw, int mis, int vec) {
   return (mis + hw + vec - 1) / vec;
@@ -399,6 +408,29 @@ cudaError_t launch_team(K kern, const NormPlan& p, int cluster, cudaStream_t s, 
   e = cudaLaunchKernelEx(&cfg, kern, args...);
   note_launches(1);
   return e;
+}
+
+// A launch without a cluster (programmatic, as all of this library's).
+template <typename K, typename... A>
+cudaError_t launch_smem(K kern, unsigned blocks, int threads, size_t smem, cudaStream_t s,
+                        A... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(blocks);
+  cfg.blockDim = dim3((unsigned)threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, kern, args...);
+  note_launches(1);
+  return e;
+}
+template <typename K, typename... A>
+cudaError_t launch_plain(K kern, unsigned blocks, int threads, cudaStream_t s, A... args) {
+  return launch_smem(kern, blocks, threads, 0, s, args...);
 }
 
 template <int N>

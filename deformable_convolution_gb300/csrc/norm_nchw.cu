@@ -20,18 +20,18 @@ struct UnitTask {
   int ch, part, mis, v0, v1, last, tail;  // tail: elements of the row in its vector `last`
   bool live;
   __device__ __forceinline__ UnitTask(const Shape& s, unsigned unit, int ch0, int t, int tasks) {
-    const int lane = threadIdx.x & 31, per = 32 / s.t.lpr;
-    const int blk = s.t.parts == 1 ? t : t / s.t.parts;
-    part = t - blk * s.t.parts;
-    const int local = blk * per + lane / s.t.lpr;
+    const int lane = threadIdx.x & 31, per = 32 / s.lpr;
+    const int blk = s.parts == 1 ? t : t / s.parts;
+    part = t - blk * s.parts;
+    const int local = blk * per + lane / s.lpr;
     live = t < tasks && local < s.cpg;
     row = (long long)unit * s.cpg + (live ? local : 0);
     ch = ch0 + (live ? local : 0);
     const long long first = row * s.hw;
     mis = EVEN ? 0 : (int)first & (VEC - 1);
     off = first - mis;
-    v0 = part * s.t.seg + (lane & (s.t.lpr - 1));
-    const int end = part * s.t.seg + s.t.seg, vr = row_vectors(s.hw, mis, VEC);
+    v0 = part * s.seg + (lane & (s.lpr - 1));
+    const int end = part * s.seg + s.seg, vr = row_vectors(s.hw, mis, VEC);
     v1 = !live ? v0 : end < vr ? end : vr;
     last = vr - 1;
     tail = s.hw + mis - last * VEC;
@@ -45,46 +45,55 @@ struct UnitTask {
 template <typename T, int VEC>
 constexpr int kPieces = VEC * sizeof(T) / 16;
 
-// A held vector: its pieces lie blockDim.x apart.
+// A held vector: its pieces lie `plane` apart.
 template <typename T, int VEC>
-__device__ __forceinline__ void take(const uint4* slot, Pairs<VEC>& f) {
+__device__ __forceinline__ void take(const uint4* slot, int plane, Pairs<VEC>& f) {
   uint32_t u[4 * kPieces<T, VEC>];
 #pragma unroll
   for (int i = 0; i < kPieces<T, VEC>; ++i) {
-    const uint4 v = slot[i * blockDim.x];
+    const uint4 v = slot[i * plane];
     u[4 * i] = v.x, u[4 * i + 1] = v.y, u[4 * i + 2] = v.z, u[4 * i + 3] = v.w;
   }
   unpack<T, VEC>(u, f);
 }
 
-// Starts the copies of a task's vectors to this thread's slots, `stride` apart.
+// Held vectors: a warp's segments one after the other, a round after the other,
+// in planes of 16-byte pieces.  The lane's first slot of a round:
+__device__ __forceinline__ int first_slot(const Shape& s) {
+  const int lane = threadIdx.x & 31, per = 32 / s.lpr;
+  return ((threadIdx.x >> 5) * per + lane / s.lpr) * s.seg + (lane & (s.lpr - 1));
+}
+__device__ __forceinline__ int round_slots(const Shape& s) {
+  return (blockDim.x >> 5) * (32 / s.lpr) * s.seg;
+}
+
+// Starts the copies of a task's vectors to this thread's slots.
 template <typename T, int VEC, bool EVEN>
 __device__ __forceinline__ void hold_task(const Shape& s, const UnitTask<VEC, EVEN>& k, const T* x,
-                                          uint4* slot, int stride) {
+                                          uint4* slot, int plane) {
   const T* p = x + k.off + (long long)k.v0 * VEC;
-  for (int v = k.v0; v < k.v1; v += s.t.lpr) {
+  for (int v = k.v0; v < k.v1; v += s.lpr) {
     const int bytes = k.hi(v) * (int)sizeof(T);
 #pragma unroll
     for (int i = 0; i < kPieces<T, VEC>; ++i) {
       // (a piece past the row's end is skipped; its slot is not used)
       const int b = min(16, bytes - 16 * i);
       if (EVEN || b > 0)
-        copy_async<16>(slot + i * blockDim.x, reinterpret_cast<const char*>(p) + 16 * i,
-                       EVEN ? 16 : b);
+        copy_async<16>(slot + i * plane, reinterpret_cast<const char*>(p) + 16 * i, EVEN ? 16 : b);
     }
-    slot += stride;
-    p += s.t.lpr * VEC;
+    slot += s.lpr;
+    p += s.lpr * VEC;
   }
 }
 
 // Vector v of a task at p, held or from memory; what lies outside the row is 0.
 template <typename T, int VEC, bool EVEN, bool HELD>
 __device__ __forceinline__ void fetch(const UnitTask<VEC, EVEN>& k, int v, const T* p,
-                                      const uint4* slot, Pairs<VEC>& f) {
+                                      const uint4* slot, int plane, Pairs<VEC>& f) {
   const int lo = k.lo(v), hi = k.hi(v);
   const bool full = EVEN || (lo == 0 && hi == VEC);
   if (HELD) {
-    take<T, VEC>(slot, f);
+    take<T, VEC>(slot, plane, f);
     if (!full) {
 #pragma unroll
       for (int e = 0; e < VEC; ++e)
@@ -115,6 +124,7 @@ struct Place {
   int rank, u, w, team, ch0;  // ch0: the unit's first channel
   unsigned unit;
   bool here;
+  __device__ __forceinline__ Place() {}
   __device__ __forceinline__ Place(const Shape& s, const RowTeam& tm) {
     const int warp = threadIdx.x >> 5;
     rank = cluster_rank();
@@ -124,7 +134,7 @@ struct Place {
     here = unit < (unsigned)s.n * s.groups;
     if (!here) unit = 0;
     ch0 = (int)(unit % (unsigned)s.groups) * s.cpg;
-    team = tm.cluster * tm.warps;
+    team = tm.blocks * tm.warps;
   }
   __device__ __forceinline__ int task(const RowTeam& tm, int r) const {
     return rank * tm.warps + w + r * team;
@@ -137,9 +147,9 @@ template <int N>
 __device__ __forceinline__ const float* share(const RowTeam& tm, const Place& pl,
                                               float (&sm)[N][256], const float (&val)[N]) {
   const int lane = threadIdx.x & 31, at = pl.rank * tm.warps + pl.w;
-  if (tm.cluster > 1) {
+  if (tm.blocks > 1) {
     cluster_wait();  // every block of the cluster runs
-    if (lane < tm.cluster)
+    if (lane < tm.blocks)
 #pragma unroll
       for (int i = 0; i < N; ++i) store_cluster(&sm[i][at], lane, val[i]);
     cluster_arrive();
@@ -208,7 +218,7 @@ template <typename T, int VEC, bool EVEN, bool HELD>
 __device__ __forceinline__ void task_stats(const Shape& s, const UnitTask<VEC, EVEN>& k, const T* x,
                                            const uint4* slot, float& n, float& mean, float& m2) {
   const T* p = x + k.off + (long long)k.v0 * VEC;
-  const int lpr = s.t.lpr;
+  const int lpr = s.lpr;
   for (int v0 = k.v0; v0 < k.v1; v0 += kBatch * lpr) {
     const int most = (k.v1 - v0 + lpr - 1) / lpr;
     int cnt = 0;
@@ -218,7 +228,7 @@ __device__ __forceinline__ void task_stats(const Shape& s, const UnitTask<VEC, E
     add_batch<VEC, kBatch>(
         most, cnt, n, mean, m2,
         [&](int b, Pairs<VEC>& f) {
-          fetch<T, VEC, EVEN, HELD>(k, v0 + b * lpr, p + b * lpr * VEC, slot + b * blockDim.x, f);
+          fetch<T, VEC, EVEN, HELD>(k, v0 + b * lpr, p + b * lpr * VEC, slot + b * lpr, 0, f);
         },
         [&](int b, Pairs<VEC>& f, float m) {
           if (EVEN) return;
@@ -229,7 +239,7 @@ __device__ __forceinline__ void task_stats(const Shape& s, const UnitTask<VEC, E
               if (e < lo || e >= hi) f[e] = m;
           }
         });
-    slot += kBatch * blockDim.x;
+    slot += kBatch * lpr;
     p += kBatch * lpr * VEC;
   }
 }
@@ -237,19 +247,28 @@ __device__ __forceinline__ void task_stats(const Shape& s, const UnitTask<VEC, E
 template <typename T, int VEC, bool EVEN, bool HELD, int ACT>
 __device__ __forceinline__ void task_apply(const Shape& s, const UnitTask<VEC, EVEN>& k, const T* x,
                                            T* y, const uint4* slot, float mu, float a, float b) {
+  constexpr int B = HELD ? 1 : 4;  // (loads ahead of the stores, which may be in place)
   const T* p = x + k.off + (long long)k.v0 * VEC;
   T* to = y + k.off + (long long)k.v0 * VEC;
-#pragma unroll 2
-  for (int v = k.v0; v < k.v1; v += s.t.lpr) {
-    Pairs<VEC> f;
-    fetch<T, VEC, EVEN, HELD>(k, v, p, slot, f);
+  const int lpr = s.lpr;
+#pragma unroll(HELD ? 2 : 1)
+  for (int v0 = k.v0; v0 < k.v1; v0 += B * lpr) {
+    Pairs<VEC> f[B];
 #pragma unroll
-    for (int e = 0; e < VEC / 2; ++e)
-      f.p[e] = act_fwd2<ACT>(fma2(add2(f.p[e], both(-mu)), both(a), both(b)), s.floor);
-    put<T, VEC, EVEN>(k, v, to, f);
-    slot += blockDim.x;
-    p += s.t.lpr * VEC;
-    to += s.t.lpr * VEC;
+    for (int i = 0; i < B; ++i)
+      if (v0 + i * lpr < k.v1)
+        fetch<T, VEC, EVEN, HELD>(k, v0 + i * lpr, p + i * lpr * VEC, slot + i * lpr, 0, f[i]);
+#pragma unroll
+    for (int i = 0; i < B; ++i) {
+      if (v0 + i * lpr >= k.v1) break;
+#pragma unroll
+      for (int e = 0; e < VEC / 2; ++e)
+        f[i].p[e] = act_fwd2<ACT>(fma2(add2(f[i].p[e], both(-mu)), both(a), both(b)), s.floor);
+      put<T, VEC, EVEN>(k, v0 + i * lpr, to + i * lpr * VEC, f[i]);
+    }
+    slot += B * lpr;
+    p += B * lpr * VEC;
+    to += B * lpr * VEC;
   }
 }
 
@@ -260,19 +279,19 @@ __global__ void __launch_bounds__(kTeam, 2)
   constexpr int VEC = VecOf<T>::n;
   extern __shared__ uint4 hold[];
   __shared__ float sm[3][256];
-  if (tm.cluster > 1) cluster_arrive();
+  if (tm.blocks > 1) cluster_arrive();
   pdl_wait();
   pdl_release();
   const Place pl(s, tm);
-  const int tasks = pl.here ? tm.tasks : 0, pitch = tm.slots * blockDim.x;
+  const int tasks = pl.here ? tm.tasks : 0, pitch = round_slots(s);
   using Task = UnitTask<VEC, EVEN>;
   const Task first(s, pl.unit, pl.ch0, pl.task(tm, 0), tasks);
   auto task = [&](int r) {
     return r == 0 ? first : Task(s, pl.unit, pl.ch0, pl.task(tm, r), tasks);
   };
-  uint4* mine = hold + threadIdx.x;
+  uint4* mine = hold + first_slot(s);
   for (int r = 0; r < tm.held; ++r)
-    hold_task<T, VEC, EVEN>(s, task(r), x, mine + r * pitch, blockDim.x);
+    hold_task<T, VEC, EVEN>(s, task(r), x, mine + r * pitch, 0);
   // what is not held first: its loads go on behind the copies
   float n = 0.f, mean = 0.f, m2 = 0.f;
   for (int r = tm.rounds - 1; r >= tm.held; --r)
@@ -306,7 +325,7 @@ __global__ void __launch_bounds__(kTeam, 2)
   constexpr int VEC = VecOf<T>::n;
   extern __shared__ uint4 hold[];
   __shared__ float sm[3][256];
-  if (tm.cluster > 1) cluster_arrive();
+  if (tm.blocks > 1) cluster_arrive();
   pdl_wait();
   pdl_release();
   const Place pl(s, tm);
@@ -338,7 +357,7 @@ __global__ void __launch_bounds__(kTeam, 2)
   copy_wait();
   {
     const uint4* slot = mine;
-    auto get = [&](int b, Pairs<VEC>& f) { take<T, VEC>(slot + b * blockDim.x, f); };
+    auto get = [&](int b, Pairs<VEC>& f) { take<T, VEC>(slot + b * blockDim.x, 0, f); };
     int i = 0;
     for (; i + kBatch <= held; i += kBatch, slot += kBatch * blockDim.x)
       add_batch<VEC, kBatch>(kBatch, kBatch * VEC, n, mean, m2, get, keep);
@@ -370,7 +389,7 @@ __global__ void __launch_bounds__(kTeam, 2)
 #pragma unroll 2
   for (int i = 0; i < held; ++i) {
     Pairs<VEC> f;
-    take<T, VEC>(mine + i * blockDim.x, f);
+    take<T, VEC>(mine + i * blockDim.x, 0, f);
     apply(f);
   }
   p += (long long)held * step;
@@ -386,16 +405,16 @@ __global__ void __launch_bounds__(kTeam, 2)
 template <typename T, typename TG, int VEC, bool EVEN, bool HELD, bool KEEP, int ACT>
 __device__ __forceinline__ void task_sums(const Shape& s, const UnitTask<VEC, EVEN>& k, const T* x,
                                           const TG* gy, const uint4* slot, uint4* slot_g,
-                                          int stride_g, float mu, float rs, float g, float b,
+                                          int plane, float mu, float rs, float g, float b,
                                           float2& sa, float2& sb) {
   const long long off = k.off + (long long)k.v0 * VEC;
   const T* p = x + off;
   const TG* pg = gy + off;
 #pragma unroll 2
-  for (int v = k.v0; v < k.v1; v += s.t.lpr) {
+  for (int v = k.v0; v < k.v1; v += s.lpr) {
     Pairs<VEC> f, d;  // (0 outside the row: dz is 0 there)
-    fetch<T, VEC, EVEN, HELD>(k, v, p, slot, f);
-    fetch<TG, VEC, EVEN, HELD>(k, v, pg, slot_g, d);
+    fetch<T, VEC, EVEN, HELD>(k, v, p, slot, plane, f);
+    fetch<TG, VEC, EVEN, HELD>(k, v, pg, slot_g, plane, d);
 #pragma unroll
     for (int e = 0; e < VEC / 2; ++e) {
       const float2 xh = mul2(add2(f.p[e], both(-mu)), both(rs));
@@ -406,13 +425,13 @@ __device__ __forceinline__ void task_sums(const Shape& s, const UnitTask<VEC, EV
     if (HELD && KEEP) {
 #pragma unroll
       for (int i = 0; i < VEC / 4; ++i)
-        *reinterpret_cast<float4*>(slot_g + i * blockDim.x) = make_float4(
+        *reinterpret_cast<float4*>(slot_g + i * plane) = make_float4(
             d.p[2 * i].x, d.p[2 * i].y, d.p[2 * i + 1].x, d.p[2 * i + 1].y);
     }
-    slot += blockDim.x;
-    slot_g += stride_g;
-    p += s.t.lpr * VEC;
-    pg += s.t.lpr * VEC;
+    slot += s.lpr;
+    slot_g += s.lpr;
+    p += s.lpr * VEC;
+    pg += s.lpr * VEC;
   }
 }
 
@@ -420,34 +439,46 @@ __device__ __forceinline__ void task_sums(const Shape& s, const UnitTask<VEC, EV
 template <typename T, typename TG, int VEC, bool EVEN, bool HELD, bool KEEP, int ACT>
 __device__ __forceinline__ void task_grads(const Shape& s, const UnitTask<VEC, EVEN>& k, const T* x,
                                            const TG* gy, T* gx, const uint4* slot,
-                                           const uint4* slot_g, int stride_g, float mu, float rs,
+                                           const uint4* slot_g, int plane, float mu, float rs,
                                            float g, float b, float s1, float s2) {
   const long long off = k.off + (long long)k.v0 * VEC;
   const T* p = x + off;
   const TG* pg = gy + off;
   T* to = gx + off;
   const float gr = g * rs;
-#pragma unroll 2
-  for (int v = k.v0; v < k.v1; v += s.t.lpr) {
-    Pairs<VEC> f, d;
-    fetch<T, VEC, EVEN, HELD>(k, v, p, slot, f);
-    if (HELD && KEEP)
-      take<float, VEC>(slot_g, d);
-    else
-      fetch<TG, VEC, EVEN, HELD>(k, v, pg, slot_g, d);
+  constexpr int B = HELD ? 1 : 2;  // (loads ahead of the stores, which may be in place)
+  const int lpr = s.lpr;
+#pragma unroll(HELD ? 2 : 1)
+  for (int v0 = k.v0; v0 < k.v1; v0 += B * lpr) {
+    Pairs<VEC> f[B], d[B];
 #pragma unroll
-    for (int e = 0; e < VEC / 2; ++e) {
-      const float2 xh = mul2(add2(f.p[e], both(-mu)), both(rs));
-      if (!(HELD && KEEP))
-        d.p[e] = act_bwd2<ACT>(fma2(xh, both(g), both(b)), d.p[e], s.floor);
-      f.p[e] = fma2(xh, both(-s2), fma2(d.p[e], both(gr), both(-s1)));
+    for (int i = 0; i < B; ++i) {
+      const int v = v0 + i * lpr;
+      if (v >= k.v1) break;
+      fetch<T, VEC, EVEN, HELD>(k, v, p + i * lpr * VEC, slot + i * lpr, plane, f[i]);
+      if (HELD && KEEP)
+        take<float, VEC>(slot_g + i * lpr, plane, d[i]);
+      else
+        fetch<TG, VEC, EVEN, HELD>(k, v, pg + i * lpr * VEC, slot_g + i * lpr, plane, d[i]);
     }
-    put<T, VEC, EVEN>(k, v, to, f);
-    slot += blockDim.x;
-    slot_g += stride_g;
-    p += s.t.lpr * VEC;
-    pg += s.t.lpr * VEC;
-    to += s.t.lpr * VEC;
+#pragma unroll
+    for (int i = 0; i < B; ++i) {
+      const int v = v0 + i * lpr;
+      if (v >= k.v1) break;
+#pragma unroll
+      for (int e = 0; e < VEC / 2; ++e) {
+        const float2 xh = mul2(add2(f[i].p[e], both(-mu)), both(rs));
+        if (!(HELD && KEEP))
+          d[i].p[e] = act_bwd2<ACT>(fma2(xh, both(g), both(b)), d[i].p[e], s.floor);
+        f[i].p[e] = fma2(xh, both(-s2), fma2(d[i].p[e], both(gr), both(-s1)));
+      }
+      put<T, VEC, EVEN>(k, v, to + i * lpr * VEC, f[i]);
+    }
+    slot += B * lpr;
+    slot_g += B * lpr;
+    p += B * lpr * VEC;
+    pg += B * lpr * VEC;
+    to += B * lpr * VEC;
   }
 }
 
@@ -462,23 +493,22 @@ __global__ void __launch_bounds__(kTeam, 2)
   constexpr int kG = KEEP ? VEC / 4 : kPieces<TG, VEC>;  // pieces of a slot of grad_y
   extern __shared__ uint4 hold[];
   __shared__ float sm[2][256];
-  if (tm.cluster > 1) cluster_arrive();
+  if (tm.blocks > 1) cluster_arrive();
   pdl_wait();
   pdl_release();
   const Place pl(s, tm);
-  const int tasks = pl.here ? tm.tasks : 0, pitch = tm.slots * blockDim.x;
-  const int stride_g = kG * blockDim.x;
+  const int tasks = pl.here ? tm.tasks : 0, pitch = round_slots(s);
   using Task = UnitTask<VEC, EVEN>;
   const Task first(s, pl.unit, pl.ch0, pl.task(tm, 0), tasks);
   auto task = [&](int r) {
     return r == 0 ? first : Task(s, pl.unit, pl.ch0, pl.task(tm, r), tasks);
   };
-  uint4* mine = hold + threadIdx.x;
+  uint4* mine = hold + first_slot(s);
   uint4* mine_g = mine + (size_t)tm.held * pitch;
   for (int r = 0; r < tm.held; ++r) {
     const Task k = task(r);
-    hold_task<T, VEC, EVEN>(s, k, x, mine + r * pitch, blockDim.x);
-    hold_task<TG, VEC, EVEN>(s, k, gy, mine_g + r * pitch * kG, stride_g);
+    hold_task<T, VEC, EVEN>(s, k, x, mine + r * pitch, pitch);
+    hold_task<TG, VEC, EVEN>(s, k, gy, mine_g + r * pitch * kG, pitch);
   }
   const float mu = pl.here ? mean[pl.unit] : 0.f, rs = pl.here ? rstd[pl.unit] : 0.f;
   float val[2] = {0.f, 0.f};
@@ -489,13 +519,13 @@ __global__ void __launch_bounds__(kTeam, 2)
     float2 sa = both(0.f), sb = both(0.f);
     if (r < tm.held)
       task_sums<T, TG, VEC, EVEN, true, KEEP, ACT>(s, k, x, gy, mine + r * pitch,
-                                                   mine_g + r * pitch * kG, stride_g, mu, rs, g, b,
+                                                   mine_g + r * pitch * kG, pitch, mu, rs, g, b,
                                                    sa, sb);
     else
-      task_sums<T, TG, VEC, EVEN, false, KEEP, ACT>(s, k, x, gy, mine, mine_g, stride_g, mu, rs, g,
+      task_sums<T, TG, VEC, EVEN, false, KEEP, ACT>(s, k, x, gy, mine, mine_g, pitch, mu, rs, g,
                                                     b, sa, sb);
-    const float ra = row_sum(sa.x + sa.y, s.t.lpr), rb = row_sum(sb.x + sb.y, s.t.lpr);
-    if (k.live && (threadIdx.x & (s.t.lpr - 1)) == 0) {
+    const float ra = row_sum(sa.x + sa.y, s.lpr), rb = row_sum(sb.x + sb.y, s.lpr);
+    if (k.live && (threadIdx.x & (s.lpr - 1)) == 0) {
       part[(long long)k.part * s.n * s.c + k.row] = make_float2(ra, rb);
       val[0] = fmaf(g, ra, val[0]);
       val[1] = fmaf(g, rb, val[1]);
@@ -517,17 +547,194 @@ __global__ void __launch_bounds__(kTeam, 2)
     const float g = gamma ? gamma[k.ch] : 1.f, b = beta ? beta[k.ch] : 0.f;
     if (r < tm.held)
       task_grads<T, TG, VEC, EVEN, true, KEEP, ACT>(s, k, x, gy, gx, mine + r * pitch,
-                                                    mine_g + r * pitch * kG, stride_g, mu, rs, g,
+                                                    mine_g + r * pitch * kG, pitch, mu, rs, g,
                                                     b, s1, s2);
     else
-      task_grads<T, TG, VEC, EVEN, false, KEEP, ACT>(s, k, x, gy, gx, mine, mine_g, stride_g, mu,
+      task_grads<T, TG, VEC, EVEN, false, KEEP, ACT>(s, k, x, gy, gx, mine, mine_g, pitch, mu,
                                                      rs, g, b, s1, s2);
+  }
+}
+
+// ---------------------------------------------------------------- two launches
+
+// This thread's place where a unit's blocks are no cluster.
+__device__ __forceinline__ Place loose_place(const Shape& s, const RowTeam& tm, unsigned unit0) {
+  Place pl;
+  const unsigned id = blockIdx.x / (unsigned)tm.blocks;
+  pl.rank = (int)(blockIdx.x - id * tm.blocks);
+  pl.u = 0;
+  pl.w = threadIdx.x >> 5;
+  pl.unit = unit0 + id;
+  pl.here = true;
+  pl.ch0 = (int)(pl.unit % (unsigned)s.groups) * s.cpg;
+  pl.team = tm.blocks * tm.warps;
+  return pl;
+}
+
+// entry[unit * blocks + rank] = (count, mean, M2) of a block's share.
+template <typename T, bool EVEN>
+__global__ void __launch_bounds__(kTwo)
+    stats_nchw(Shape s, RowTeam tm, unsigned unit0, const T* x, float4* entry) {
+  constexpr int VEC = VecOf<T>::n;
+  __shared__ float sm[3][kTwo / 32];
+  pdl_wait();
+  pdl_release();
+  const Place pl = loose_place(s, tm, unit0);
+  float n = 0.f, mean = 0.f, m2 = 0.f;
+  if (EVEN) {
+    const int begin = pl.rank * tm.span + threadIdx.x;
+    const int end = min(s.cpg * (s.hw / VEC), (pl.rank + 1) * tm.span);
+    const T* p = x + (long long)pl.unit * s.cpg * s.hw + (long long)begin * VEC;
+    const int count = begin < end ? (end - begin + kTwo - 1) / kTwo : 0;
+    auto get = [&](int b, Pairs<VEC>& f) { load_vec<T, VEC>(p + b * kTwo * VEC, f); };
+    auto keep = [](int, Pairs<VEC>&, float) {};
+    int i = 0;
+    for (; i + kBatch <= count; i += kBatch, p += kBatch * kTwo * VEC)
+      add_batch<VEC, kBatch>(kBatch, kBatch * VEC, n, mean, m2, get, keep);
+    if (i < count) add_batch<VEC, kBatch>(count - i, (count - i) * VEC, n, mean, m2, get, keep);
+  } else {
+    for (int r = 0; r < tm.rounds; ++r)
+      task_stats<T, VEC, EVEN, false>(
+          s, UnitTask<VEC, EVEN>(s, pl.unit, pl.ch0, pl.task(tm, r), tm.tasks), x, nullptr, n,
+          mean, m2);
+  }
+  const float wn = warp_sum(n), wm = warp_sum(n * mean) / fmaxf(wn, 1.f);
+  const float wq = warp_sum(n > 0.f ? fmaf(n * (mean - wm), mean - wm, m2) : 0.f);
+  if ((threadIdx.x & 31) == 0) sm[0][pl.w] = wn, sm[1][pl.w] = wm, sm[2][pl.w] = wq;
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    n = mean = m2 = 0.f;
+    for (int w = 0; w < kTwo / 32; ++w) merge(n, mean, m2, sm[0][w], sm[1][w], sm[2][w]);
+    entry[(size_t)pl.unit * tm.blocks + pl.rank] = make_float4(n, mean, m2, 0.f);
+  }
+}
+
+template <typename T, bool EVEN, int ACT>
+__global__ void __launch_bounds__(kTwo)
+    apply_nchw(Shape s, RowTeam tm, unsigned unit0, const T* x, const float* gamma,
+               const float* beta, const float4* entry, T* y, float* mean_out, float* rstd_out) {
+  constexpr int VEC = VecOf<T>::n;
+  pdl_wait();
+  pdl_release();
+  const Place pl = loose_place(s, tm, unit0);
+  const int lane = threadIdx.x & 31;
+  const float4* mine = entry + (size_t)pl.unit * tm.blocks;
+  float n = 0.f, mean = 0.f, m2 = 0.f;
+  for (int i = lane; i < tm.blocks; i += 32) {
+    const float4 v = mine[i];
+    merge(n, mean, m2, v.x, v.y, v.z);
+  }
+  const float total = (float)s.hw * (float)s.cpg;
+  const float mu = warp_sum(n * mean) / total;
+  const float var = warp_sum(n > 0.f ? fmaf(n * (mean - mu), mean - mu, m2) : 0.f) / total;
+  const float rs = 1.f / sqrtf(var + s.eps);
+  if (pl.rank == 0 && threadIdx.x == 0) {
+    if (mean_out) mean_out[pl.unit] = mu;
+    if (rstd_out) rstd_out[pl.unit] = rs;
+  }
+  if (EVEN) {
+    const int vr = s.hw / VEC, begin = pl.rank * tm.span + threadIdx.x;
+    const int end = min(s.cpg * vr, (pl.rank + 1) * tm.span);
+    const long long off = (long long)pl.unit * s.cpg * s.hw + (long long)begin * VEC;
+    const T* p = x + off;
+    T* to = y + off;
+    int c = begin / vr, at = begin - c * vr;
+    for (int v0 = begin; v0 < end; v0 += kBatch * kTwo) {
+      Pairs<VEC> f[kBatch];  // (loads ahead of the stores, which may be in place)
+#pragma unroll
+      for (int i = 0; i < kBatch; ++i)
+        if (v0 + i * kTwo < end) load_vec<T, VEC>(p + i * kTwo * VEC, f[i]);
+#pragma unroll
+      for (int i = 0; i < kBatch; ++i) {
+        if (v0 + i * kTwo >= end) break;
+        const float a = rs * (gamma ? gamma[pl.ch0 + c] : 1.f), b = beta ? beta[pl.ch0 + c] : 0.f;
+#pragma unroll
+        for (int e = 0; e < VEC / 2; ++e)
+          f[i].p[e] = act_fwd2<ACT>(fma2(add2(f[i].p[e], both(-mu)), both(a), both(b)), s.floor);
+        store_vec<T, VEC>(to + i * kTwo * VEC, f[i]);
+        c += tm.step_c;
+        at += tm.step_v;
+        if (at >= vr) at -= vr, ++c;
+      }
+      p += kBatch * kTwo * VEC;
+      to += kBatch * kTwo * VEC;
+    }
+    return;
+  }
+  for (int r = 0; r < tm.rounds; ++r) {
+    const UnitTask<VEC, EVEN> k(s, pl.unit, pl.ch0, pl.task(tm, r), tm.tasks);
+    task_apply<T, VEC, EVEN, false, ACT>(s, k, x, y, nullptr, mu, rs * (gamma ? gamma[k.ch] : 1.f),
+                                         beta ? beta[k.ch] : 0.f);
+  }
+}
+
+// part as above; entry[unit * blocks + rank] = the block's sums of gamma dz and
+// gamma dz xh.
+template <typename T, typename TG, bool EVEN, int ACT>
+__global__ void __launch_bounds__(kTwo)
+    sums_nchw(Shape s, RowTeam tm, unsigned unit0, const T* x, const TG* gy, const float* gamma,
+              const float* beta, const float* mean, const float* rstd, float2* part,
+              float2* entry) {
+  constexpr int VEC = VecOf<T>::n;
+  __shared__ float2 sm[kTwo / 32];
+  pdl_wait();
+  pdl_release();
+  const Place pl = loose_place(s, tm, unit0);
+  const float mu = mean[pl.unit], rs = rstd[pl.unit];
+  float ga = 0.f, gb = 0.f;
+  for (int r = 0; r < tm.rounds; ++r) {
+    const UnitTask<VEC, EVEN> k(s, pl.unit, pl.ch0, pl.task(tm, r), tm.tasks);
+    const float g = gamma ? gamma[k.ch] : 1.f, b = beta ? beta[k.ch] : 0.f;
+    float2 sa = both(0.f), sb = both(0.f);
+    task_sums<T, TG, VEC, EVEN, false, false, ACT>(s, k, x, gy, nullptr, nullptr, 0, mu, rs, g, b,
+                                                   sa, sb);
+    const float ra = row_sum(sa.x + sa.y, s.lpr), rb = row_sum(sb.x + sb.y, s.lpr);
+    if (k.live && (threadIdx.x & (s.lpr - 1)) == 0) {
+      part[(long long)k.part * s.n * s.c + k.row] = make_float2(ra, rb);
+      ga = fmaf(g, ra, ga);
+      gb = fmaf(g, rb, gb);
+    }
+  }
+  ga = warp_sum(ga);
+  gb = warp_sum(gb);
+  if ((threadIdx.x & 31) == 0) sm[pl.w] = make_float2(ga, gb);
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    for (int w = 1; w < kTwo / 32; ++w) ga += sm[w].x, gb += sm[w].y;
+    entry[(size_t)pl.unit * tm.blocks + pl.rank] = make_float2(ga, gb);
+  }
+}
+
+template <typename T, typename TG, bool EVEN, int ACT>
+__global__ void __launch_bounds__(kTwo)
+    grads_nchw(Shape s, RowTeam tm, unsigned unit0, const T* x, const TG* gy, const float* gamma,
+               const float* beta, const float* mean, const float* rstd, const float2* entry,
+               T* gx) {
+  constexpr int VEC = VecOf<T>::n;
+  pdl_wait();
+  pdl_release();
+  const Place pl = loose_place(s, tm, unit0);
+  const float mu = mean[pl.unit], rs = rstd[pl.unit];
+  const float2* e = entry + (size_t)pl.unit * tm.blocks;
+  float ga = 0.f, gb = 0.f;
+  for (int i = threadIdx.x & 31; i < tm.blocks; i += 32) {
+    const float2 v = e[i];
+    ga += v.x;
+    gb += v.y;
+  }
+  const float total = (float)s.hw * (float)s.cpg;
+  const float s1 = rs * (warp_sum(ga) / total), s2 = rs * (warp_sum(gb) / total);
+  for (int r = 0; r < tm.rounds; ++r) {
+    const UnitTask<VEC, EVEN> k(s, pl.unit, pl.ch0, pl.task(tm, r), tm.tasks);
+    task_grads<T, TG, VEC, EVEN, false, false, ACT>(s, k, x, gy, gx, nullptr, nullptr, 0, mu, rs,
+                                                    gamma ? gamma[k.ch] : 1.f,
+                                                    beta ? beta[k.ch] : 0.f, s1, s2);
   }
 }
 
 }  // namespace
 
-cudaError_t launch_team_nchw(const NormPlan& p, const NormArgs& a, bool backward,
+cudaError_t launch_nchw(const NormPlan& p, const NormArgs& a, bool backward,
                              cudaStream_t st) {
   if (!backward)
     return by_dtype(a.dt, [&](auto t) {
@@ -535,7 +742,7 @@ cudaError_t launch_team_nchw(const NormPlan& p, const NormArgs& a, bool backward
       return by_act(a.act, [&](auto act) {
         constexpr int ACT = decltype(act)::value;
         auto go = [&](auto kern) {
-          return launch_team(kern, p, p.row.cluster, st, p.s, p.row, static_cast<const T*>(a.x),
+          return launch_team(kern, p, p.row.blocks, st, p.s, p.row, static_cast<const T*>(a.x),
                              a.gamma, a.beta, static_cast<T*>(a.y), a.mean, a.rstd);
         };
         if (p.row.span) return go(fwd_flat<T, ACT>);
@@ -548,12 +755,57 @@ cudaError_t launch_team_nchw(const NormPlan& p, const NormArgs& a, bool backward
     return by_act(a.act, [&](auto act) {
       constexpr int ACT = decltype(act)::value;
       auto go = [&](auto kern) {
-        return launch_team(kern, p, p.row.cluster, st, p.s, p.row, static_cast<const T*>(a.x),
+        return launch_team(kern, p, p.row.blocks, st, p.s, p.row, static_cast<const T*>(a.x),
                            static_cast<const TG*>(a.gy), a.gamma, a.beta,
                            static_cast<const float*>(a.mean), static_cast<const float*>(a.rstd),
                            static_cast<T*>(a.gx), reinterpret_cast<float2*>(a.ws));
       };
       return a.hw % VecOf<T>::n ? go(bwd_nchw<T, TG, false, ACT>) : go(bwd_nchw<T, TG, true, ACT>);
+    });
+  });
+}
+
+cudaError_t launch_two_nchw(const NormPlan& p, const NormArgs& a, bool backward, bool second,
+                            int img0, int count, cudaStream_t st) {
+  const unsigned unit0 = (unsigned)img0 * a.groups;
+  const unsigned grid = (unsigned)count * a.groups * p.row.blocks;
+  char* entry = a.ws + norm_part_bytes(p, a, backward);
+  if (!backward)
+    return by_dtype(a.dt, [&](auto t) {
+      using T = decltype(t);
+      const T* x = static_cast<const T*>(a.x);
+      float4* e = reinterpret_cast<float4*>(entry);
+      auto by_even = [&](auto even) {
+        constexpr bool EVEN = decltype(even)::value != 0;
+        if (!second)
+          return launch_plain(stats_nchw<T, EVEN>, grid, kTwo, st, p.s, p.row, unit0, x, e);
+        return by_act(a.act, [&](auto act) {
+          return launch_plain(apply_nchw<T, EVEN, decltype(act)::value>, grid, kTwo, st, p.s,
+                              p.row, unit0, x, a.gamma, a.beta, static_cast<const float4*>(e),
+                              static_cast<T*>(a.y), a.mean, a.rstd);
+        });
+      };
+      return a.hw % VecOf<T>::n ? by_even(Int<0>{}) : by_even(Int<1>{});
+    });
+  return by_dtypes(a, [&](auto t, auto g) {
+    using T = decltype(t);
+    using TG = decltype(g);
+    const T* x = static_cast<const T*>(a.x);
+    const TG* gy = static_cast<const TG*>(a.gy);
+    const float *mean = a.mean, *rstd = a.rstd;
+    float2* e = reinterpret_cast<float2*>(entry);
+    return by_act(a.act, [&](auto act) {
+      constexpr int ACT = decltype(act)::value;
+      auto by_even = [&](auto even) {
+        constexpr bool EVEN = decltype(even)::value != 0;
+        if (!second)
+          return launch_plain(sums_nchw<T, TG, EVEN, ACT>, grid, kTwo, st, p.s, p.row, unit0, x,
+                              gy, a.gamma, a.beta, mean, rstd, reinterpret_cast<float2*>(a.ws), e);
+        return launch_plain(grads_nchw<T, TG, EVEN, ACT>, grid, kTwo, st, p.s, p.row, unit0, x, gy,
+                            a.gamma, a.beta, mean, rstd, static_cast<const float2*>(e),
+                            static_cast<T*>(a.gx));
+      };
+      return a.hw % VecOf<T>::n ? by_even(Int<0>{}) : by_even(Int<1>{});
     });
   });
 }

@@ -137,7 +137,7 @@ __global__ void __launch_bounds__(kTeam, ONE || V < 8 ? 2 : 1)
   extern __shared__ uint4 hold[];
   __shared__ float2 ent[kTeam];
   __shared__ float cnts[kTeam];
-  const bool many = tm.cluster > 1;
+  const bool many = tm.blocks > 1;
   if (many) cluster_arrive();
   pdl_wait();
   pdl_release();
@@ -146,8 +146,8 @@ __global__ void __launch_bounds__(kTeam, ONE || V < 8 ? 2 : 1)
   const int stride = kPieces<T, V> * kUnit<T, V> * blockDim.x;
   char* mine = reinterpret_cast<char*>(hold) + threadIdx.x * kUnit<T, V>;
   float* sn = reinterpret_cast<float*>(reinterpret_cast<char*>(hold) + (size_t)tm.held * stride);
-  float* sm = sn + tm.cluster * tm.ng;
-  float* sq = sm + tm.cluster * tm.ng;
+  float* sm = sn + tm.blocks * tm.ng;
+  float* sq = sm + tm.blocks * tm.ng;
   const int count = k.p1 > k.p0 ? (k.p1 - k.p0 + tm.rl - 1) / tm.rl : 0;  // this thread's pixels
   const int held = count < tm.held ? count : tm.held;
   const long long step = (long long)tm.rl * s.c;
@@ -205,7 +205,7 @@ __global__ void __launch_bounds__(kTeam, ONE || V < 8 ? 2 : 1)
     if (g >= tm.ng) continue;
     const int at = k.rank * tm.ng + g;
     if (many) {
-      if (lane < tm.cluster) {
+      if (lane < tm.blocks) {
         store_cluster(&sn[at], lane, gn);
         store_cluster(&sm[at], lane, gm);
         store_cluster(&sq[at], lane, gq);
@@ -224,7 +224,7 @@ __global__ void __launch_bounds__(kTeam, ONE || V < 8 ? 2 : 1)
   for (int g = warp; g < tm.ng; g += warps) {
     const float total = (float)s.hw * (float)s.cpg;
     const int at = lane * tm.ng + g;
-    const bool in = lane < tm.cluster && sn[at] > 0.f;
+    const bool in = lane < tm.blocks && sn[at] > 0.f;
     const float mu = warp_sum(in ? sn[at] * sm[at] : 0.f) / total;
     const float d = in ? sm[at] - mu : 0.f;
     const float var = warp_sum(in ? fmaf(sn[at] * d, d, sq[at]) : 0.f) / total;
@@ -286,7 +286,7 @@ __global__ void __launch_bounds__(kTeam, ONE || V < 8 ? 2 : 1)
   using SG = std::conditional_t<KEEP, float, TG>;  // what a slot of grad_y has room for
   extern __shared__ uint4 hold[];
   __shared__ float2 ps[kTeam];
-  const bool many = tm.cluster > 1;
+  const bool many = tm.blocks > 1;
   if (many) cluster_arrive();
   pdl_wait();
   pdl_release();
@@ -298,7 +298,7 @@ __global__ void __launch_bounds__(kTeam, ONE || V < 8 ? 2 : 1)
   char* mine_g = held_g + threadIdx.x * kUnit<SG, V>;
   float2* tab = reinterpret_cast<float2*>(held_g + (size_t)tm.held * stride_g);
   float* sa = reinterpret_cast<float*>(tab + tm.rows * tm.width);
-  float* sb = sa + tm.cluster * tm.ng;
+  float* sb = sa + tm.blocks * tm.ng;
   const int count = k.p1 > k.p0 ? (k.p1 - k.p0 + tm.rl - 1) / tm.rl : 0;
   const int held = count < tm.held ? count : tm.held;
   const long long step = (long long)tm.rl * s.c, off = k.base + (long long)k.p0 * s.c;
@@ -423,7 +423,7 @@ __global__ void __launch_bounds__(kTeam, ONE || V < 8 ? 2 : 1)
     b1 = warp_sum(b1);
     const int at = k.rank * tm.ng + q;
     if (many) {
-      if (lane < tm.cluster) {
+      if (lane < tm.blocks) {
         store_cluster(&sa[at], lane, a1);
         store_cluster(&sb[at], lane, b1);
       }
@@ -439,7 +439,7 @@ __global__ void __launch_bounds__(kTeam, ONE || V < 8 ? 2 : 1)
   }
   for (int q = warp; q < tm.ng; q += warps) {  // a group's blocks, a lane each
     const float total = (float)s.hw * (float)s.cpg;
-    const bool in = lane < tm.cluster;
+    const bool in = lane < tm.blocks;
     const float a1 = warp_sum(in ? sa[lane * tm.ng + q] : 0.f);
     const float b1 = warp_sum(in ? sb[lane * tm.ng + q] : 0.f);
     if (lane == 0) ps[q] = make_float2(a1 / total, b1 / total);
@@ -485,9 +485,370 @@ __global__ void __launch_bounds__(kTeam, ONE || V < 8 ? 2 : 1)
   }
 }
 
+// ---------------------------------------------------------------- two launches
+
+// A block's slice of channels and share of pixels; neighbouring blocks take
+// neighbouring slices of the same pixels.
+template <int V>
+struct Loose {
+  long long base;  // of the image's first pixel, plus this column's channel
+  int img, rank, slice, c0, cols, col, ch, lane, p0, count, g0, ng;  // groups [g0, g0 + ng)
+  bool live;
+  __device__ __forceinline__ Loose(const Shape& s, const ColTeam& tm, int img0) {
+    const unsigned id = blockIdx.x / (unsigned)tm.slices;
+    slice = (int)(blockIdx.x - id * tm.slices);
+    const unsigned i = id / (unsigned)tm.blocks;
+    rank = (int)(id - i * tm.blocks);
+    img = img0 + (int)i;
+    c0 = slice * tm.width;
+    cols = min(tm.cb, (s.c - c0) / V);
+    lane = threadIdx.x / tm.cb;
+    col = threadIdx.x - lane * tm.cb;
+    live = lane < tm.rl && col < cols;
+    ch = c0 + col * V;
+    base = (long long)img * s.hw * s.c + ch;
+    const long long first = (long long)rank * tm.span + lane;
+    const long long end = min((long long)s.hw, (long long)(rank + 1) * tm.span);
+    p0 = (int)first;
+    count = live && first < end ? (int)((end - first + tm.rl - 1) / tm.rl) : 0;
+    g0 = c0 / s.cpg;
+    ng = (c0 + cols * V - 1) / s.cpg - g0 + 1;
+  }
+  // entry of group g (of the image) from this block: a group's entries are
+  // [block][slice that shares it]
+  __device__ __forceinline__ size_t entry(const Shape& s, const ColTeam& tm, int g) const {
+    return (((size_t)img * s.groups + g) * tm.blocks + rank) * tm.shares +
+           (slice - g * s.cpg / tm.width);
+  }
+};
+
+// f(group's index in the block, lane, lanes) for the block's groups, `lanes`
+// neighbouring threads each; f runs in whole warps.
+template <typename F>
+__device__ __forceinline__ void each_group(int ng, F&& f) {
+  int lanes = 1;
+  while (lanes < 32 && 2 * lanes * ng <= kTwo) lanes *= 2;
+  for (int g = threadIdx.x / lanes; g - (int)threadIdx.x / lanes < ng; g += kTwo / lanes)
+    f(g, threadIdx.x & (lanes - 1), lanes);
+}
+
+// entry = (count, mean, M2) of a group's share of a block.
+template <typename T, int V, bool ONE>
+__global__ void __launch_bounds__(kTwo)
+    stats_nhwc(Shape s, ColTeam tm, int img0, const T* x, float4* entry) {
+  constexpr int P = Pairs<V>::n, E = ONE ? 1 : V, EP = ONE ? 1 : P;
+  __shared__ float2 ent[kTwo];
+  __shared__ float cnts[kTwo];
+  pdl_wait();
+  pdl_release();
+  const Loose<V> k(s, tm, img0);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const long long step = (long long)tm.rl * s.c;
+  const T* px = x + k.base + (long long)k.p0 * s.c;
+  float n = 0.f;
+  Pairs<2 * EP> mean, m2;
+#pragma unroll
+  for (int e = 0; e < EP; ++e) mean.p[e] = m2.p[e] = both(0.f);
+  auto get = [&](int b, Pairs<V>& f) { load_vec<T, V>(px + b * step, f); };
+  int i = 0;
+  for (; i + kBatch <= k.count; i += kBatch, px += kBatch * step)
+    add_batch<V, ONE>(kBatch, n, mean, m2, get);
+  if (i < k.count) add_batch<V, ONE>(k.count - i, n, mean, m2, get);
+  cnts[threadIdx.x] = n;
+  for (int q0 = 0; q0 < k.ng; q0 += kTwo / 32) {
+    const int g = k.g0 + q0 + warp;
+    const bool in = q0 + warp < k.ng;
+    // the group's columns in this block (all, where groups mix in a vector)
+    const int j0 = ONE ? max(0, g * s.cpg - k.c0) / V : 0;
+    const int j1 = ONE ? min(k.cols, ((g + 1) * s.cpg - k.c0) / V) : k.cols;
+    const int cols = max(j1 - j0, 1);
+    float gn = 0.f, gm = 0.f, gq = 0.f;
+#pragma unroll 1
+    for (int e = 0; e < E; ++e) {
+      __syncthreads();
+      float a = mean.p[0].x, b = m2.p[0].x;
+#pragma unroll
+      for (int j = 1; j < E; ++j)
+        if (j == e) a = mean[j], b = m2[j];
+      ent[threadIdx.x] = make_float2(a, b);
+      __syncthreads();
+      if (!in) continue;
+      float ln = 0.f, lm = 0.f, lq = 0.f;
+      for (int q = lane; q < cols * tm.rl; q += 32) {
+        const int l = cols == 1 ? q : q / cols, j = j0 + q - l * cols;
+        if (!ONE && (k.c0 + j * V + e) / s.cpg != g) continue;
+        const int th = l * tm.cb + j;
+        const float2 v = ent[th];
+        merge(ln, lm, lq, cnts[th], v.x, v.y);
+      }
+      const float c = warp_sum(ln);
+      const float m = warp_sum(ln * lm) / fmaxf(c, 1.f);
+      const float q = warp_sum(ln > 0.f ? fmaf(ln * (lm - m), lm - m, lq) : 0.f);
+      merge(gn, gm, gq, c, m, q);
+    }
+    if (in && lane == 0) entry[k.entry(s, tm, g)] = make_float4(gn, gm, gq, 0.f);
+  }
+}
+
+// The entries [first, first + count) of a group: its blocks', and in each the
+// slices' that share it.
+__device__ __forceinline__ size_t group_entry(const Shape& s, const ColTeam& tm, int img, int g,
+                                              int i, int shared) {
+  const int b = shared == 1 ? i : i / shared;
+  return (((size_t)img * s.groups + g) * tm.blocks + b) * tm.shares + (i - b * shared);
+}
+__device__ __forceinline__ int group_shared(const Shape& s, const ColTeam& tm, int g) {
+  return ((g + 1) * s.cpg - 1) / tm.width - g * s.cpg / tm.width + 1;
+}
+
+template <typename T, int V, bool ONE, int ACT>
+__global__ void __launch_bounds__(kTwo)
+    apply_nhwc(Shape s, ColTeam tm, int img0, const T* x, const float* gamma, const float* beta,
+               const float4* entry, T* y, float* mean_out, float* rstd_out) {
+  constexpr int P = Pairs<V>::n;
+  __shared__ float2 ent[kTwo];
+  pdl_wait();
+  pdl_release();
+  const Loose<V> k(s, tm, img0);
+  const float total = (float)s.hw * (float)s.cpg;
+  each_group(k.ng, [&](int q, int lane, int lanes) {
+    float n = 0.f, mean = 0.f, m2 = 0.f;
+    const int g = k.g0 + q;
+    if (q < k.ng) {
+      const int shared = group_shared(s, tm, g);
+#pragma unroll 4
+      for (int i = lane; i < tm.blocks * shared; i += lanes) {
+        const float4 v = entry[group_entry(s, tm, k.img, g, i, shared)];
+        merge(n, mean, m2, v.x, v.y, v.z);
+      }
+    }
+    const float mu = row_sum(n * mean, lanes) / total;
+    const float var = row_sum(n > 0.f ? fmaf(n * (mean - mu), mean - mu, m2) : 0.f, lanes) / total;
+    if (q < k.ng && lane == 0) {
+      const float rs = 1.f / sqrtf(var + s.eps);
+      ent[q] = make_float2(mu, rs);
+      if (k.rank == 0 && g * s.cpg / tm.width == k.slice) {
+        const long long to = (long long)k.img * s.groups + g;
+        if (mean_out) mean_out[to] = mu;
+        if (rstd_out) rstd_out[to] = rs;
+      }
+    }
+  });
+  __syncthreads();
+  if (!k.live) return;
+  Pairs<ONE ? 1 : V> mu;  // minus the mean
+  Pairs<V> a, b;
+  if (V == 1) a.p[0] = b.p[0] = mu.p[0] = both(0.f);
+#pragma unroll
+  for (int e = 0; e < V; ++e) {
+    const float2 st = ent[(k.ch + (ONE ? 0 : e)) / s.cpg - k.g0];
+    mu[ONE ? 0 : e] = -st.x;
+    a[e] = st.y * (gamma ? gamma[k.ch + e] : 1.f);
+    b[e] = beta ? beta[k.ch + e] : 0.f;
+  }
+  const long long step = (long long)tm.rl * s.c;
+  const T* px = x + k.base + (long long)k.p0 * s.c;
+  T* to = y + k.base + (long long)k.p0 * s.c;
+  auto pixels = [&](int most) {  // (loads ahead of the stores, which may be in place)
+    Pairs<V> f[kBatch];
+#pragma unroll
+    for (int i = 0; i < kBatch; ++i)
+      if (i < most) load_vec<T, V>(px + i * step, f[i]);
+#pragma unroll
+    for (int i = 0; i < kBatch; ++i) {
+      if (i >= most) break;
+#pragma unroll
+      for (int e = 0; e < P; ++e)
+        f[i].p[e] = act_fwd2<ACT>(fma2(add2(f[i].p[e], ONE ? both(mu[0]) : mu.p[ONE ? 0 : e]),
+                                       a.p[e], b.p[e]), s.floor);
+      store_vec<T, V>(to + i * step, f[i]);
+    }
+    px += kBatch * step;
+    to += kBatch * step;
+  };
+  int i = 0;
+  for (; i + kBatch <= k.count; i += kBatch) pixels(kBatch);
+  if (i < k.count) pixels(k.count - i);
+}
+
+// part[rank][image * c + channel] as above; entry = a block's sums of gamma dz
+// and gamma dz xh over a group's share.  Dynamic shared memory: the table.
+template <typename T, typename TG, int V, bool ONE, int ACT>
+__global__ void __launch_bounds__(kTwo)
+    sums_nhwc(Shape s, ColTeam tm, int img0, const T* x, const TG* gy, const float* gamma,
+              const float* beta, const float* mean, const float* rstd, float2* part,
+              float2* entry) {
+  constexpr int P = Pairs<V>::n;
+  extern __shared__ float2 tab[];
+  pdl_wait();
+  pdl_release();
+  const Loose<V> k(s, tm, img0);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  Pairs<ONE ? 1 : V> mu, rs;  // minus the mean
+  Pairs<V> g, b, s1, s2;
+#pragma unroll
+  for (int e = 0; e < P; ++e) g.p[e] = b.p[e] = s1.p[e] = s2.p[e] = both(0.f);
+#pragma unroll
+  for (int e = 0; e < (ONE ? 1 : P); ++e) mu.p[e] = rs.p[e] = both(0.f);
+  if (k.live) {
+#pragma unroll
+    for (int e = 0; e < V; ++e) {
+      if (!ONE || e == 0) {
+        const long long at = (long long)k.img * s.groups + (k.ch + e) / s.cpg;
+        mu[ONE ? 0 : e] = -mean[at], rs[ONE ? 0 : e] = rstd[at];
+      }
+      g[e] = gamma ? gamma[k.ch + e] : 1.f;
+      b[e] = beta ? beta[k.ch + e] : 0.f;
+    }
+  }
+  const long long step = (long long)tm.rl * s.c, off = k.base + (long long)k.p0 * s.c;
+  const T* px = x + off;
+  const TG* pg = gy + off;
+#pragma unroll 2
+  for (int i = 0; i < k.count; ++i) {
+    Pairs<V> f, d;
+    load_vec<T, V>(px, f);
+    load_vec<TG, V>(pg, d);
+#pragma unroll
+    for (int e = 0; e < P; ++e) {
+      const float2 xh = mul2(add2(f.p[e], ONE ? both(mu[0]) : mu.p[ONE ? 0 : e]),
+                             ONE ? both(rs[0]) : rs.p[ONE ? 0 : e]);
+      float2 dz = act_bwd2<ACT>(fma2(xh, g.p[e], b.p[e]), d.p[e], s.floor);
+      if (V == 1) dz.y = 0.f;
+      s1.p[e] = add2(s1.p[e], dz);
+      s2.p[e] = fma2(dz, xh, s2.p[e]);
+    }
+    px += step;
+    pg += step;
+  }
+  int row = k.lane;
+  bool put = k.live;
+  if (32 % tm.cb == 0) {
+    for (int o = 16; o >= tm.cb; o >>= 1) {
+#pragma unroll
+      for (int e = 0; e < V; ++e) {
+        s1[e] += __shfl_xor_sync(0xffffffffu, s1[e], o);
+        s2[e] += __shfl_xor_sync(0xffffffffu, s2[e], o);
+      }
+    }
+    row = warp;
+    put = lane < tm.cb && k.col < k.cols;
+  }
+  if (put) {
+#pragma unroll
+    for (int e = 0; e < V; ++e) tab[row * tm.width + k.col * V + e] = make_float2(s1[e], s2[e]);
+  }
+  __syncthreads();
+  const int width = k.cols * V;
+  for (int c = threadIdx.x; c < width; c += kTwo) {
+    float2 t = tab[c];
+    for (int l = 1; l < tm.rows; ++l) {
+      const float2 v = tab[l * tm.width + c];
+      t.x += v.x;
+      t.y += v.y;
+    }
+    part[((long long)k.rank * s.n + k.img) * s.c + k.c0 + c] = t;
+    const float gm = gamma ? gamma[k.c0 + c] : 1.f;
+    tab[c] = make_float2(gm * t.x, gm * t.y);
+  }
+  __syncthreads();
+  for (int q = warp; q < k.ng; q += kTwo / 32) {
+    const int gr = k.g0 + q;
+    const int c1 = min(width, (gr + 1) * s.cpg - k.c0);
+    float a1 = 0.f, b1 = 0.f;
+    for (int c = max(0, gr * s.cpg - k.c0) + lane; c < c1; c += 32) {
+      a1 += tab[c].x;
+      b1 += tab[c].y;
+    }
+    a1 = warp_sum(a1);
+    b1 = warp_sum(b1);
+    if (lane == 0) entry[k.entry(s, tm, gr)] = make_float2(a1, b1);
+  }
+}
+
+template <typename T, typename TG, int V, bool ONE, int ACT>
+__global__ void __launch_bounds__(kTwo)
+    grads_nhwc(Shape s, ColTeam tm, int img0, const T* x, const TG* gy, const float* gamma,
+               const float* beta, const float* mean, const float* rstd, const float2* entry,
+               T* gx) {
+  constexpr int P = Pairs<V>::n;
+  __shared__ float2 ent[kTwo];
+  pdl_wait();
+  pdl_release();
+  const Loose<V> k(s, tm, img0);
+  const float total = (float)s.hw * (float)s.cpg;
+  each_group(k.ng, [&](int q, int lane, int lanes) {
+    float a1 = 0.f, b1 = 0.f;
+    const int g = k.g0 + q;
+    if (q < k.ng) {
+      const int shared = group_shared(s, tm, g);
+#pragma unroll 4
+      for (int i = lane; i < tm.blocks * shared; i += lanes) {
+        const float2 v = entry[group_entry(s, tm, k.img, g, i, shared)];
+        a1 += v.x;
+        b1 += v.y;
+      }
+    }
+    a1 = row_sum(a1, lanes);
+    b1 = row_sum(b1, lanes);
+    if (q < k.ng && lane == 0) ent[q] = make_float2(a1 / total, b1 / total);
+  });
+  __syncthreads();
+  if (!k.live) return;
+  // grad_x = dz * (gamma * rstd) - rstd * s1 - xh * (rstd * s2)
+  Pairs<ONE ? 1 : V> mu, rs, k1, k2;
+  Pairs<V> g, b;
+  if (V == 1) {
+    mu.p[0] = rs.p[0] = k1.p[0] = k2.p[0] = both(0.f);
+    g.p[0] = b.p[0] = both(0.f);
+  }
+#pragma unroll
+  for (int e = 0; e < V; ++e) {
+    if (!ONE || e == 0) {
+      const int gr = (k.ch + e) / s.cpg;
+      const long long at = (long long)k.img * s.groups + gr;
+      const float2 v = ent[gr - k.g0];
+      mu[ONE ? 0 : e] = -mean[at], rs[ONE ? 0 : e] = rstd[at];
+      k1[ONE ? 0 : e] = -rstd[at] * v.x, k2[ONE ? 0 : e] = -rstd[at] * v.y;
+    }
+    g[e] = gamma ? gamma[k.ch + e] : 1.f;
+    b[e] = beta ? beta[k.ch + e] : 0.f;
+  }
+  const long long step = (long long)tm.rl * s.c, off = k.base + (long long)k.p0 * s.c;
+  const T* px = x + off;
+  const TG* pg = gy + off;
+  T* to = gx + off;
+  constexpr int B = 2;  // (loads ahead of the stores, which may be in place)
+  for (int i0 = 0; i0 < k.count; i0 += B) {
+    Pairs<V> f[B], d[B];
+#pragma unroll
+    for (int i = 0; i < B; ++i) {
+      if (i0 + i >= k.count) break;
+      load_vec<T, V>(px + i * step, f[i]);
+      load_vec<TG, V>(pg + i * step, d[i]);
+    }
+#pragma unroll
+    for (int i = 0; i < B; ++i) {
+      if (i0 + i >= k.count) break;
+#pragma unroll
+      for (int e = 0; e < P; ++e) {
+        const float2 r = ONE ? both(rs[0]) : rs.p[ONE ? 0 : e];
+        const float2 xh = mul2(add2(f[i].p[e], ONE ? both(mu[0]) : mu.p[ONE ? 0 : e]), r);
+        const float2 dz = act_bwd2<ACT>(fma2(xh, g.p[e], b.p[e]), d[i].p[e], s.floor);
+        f[i].p[e] = fma2(xh, ONE ? both(k2[0]) : k2.p[ONE ? 0 : e],
+                         fma2(dz, mul2(g.p[e], r), ONE ? both(k1[0]) : k1.p[ONE ? 0 : e]));
+      }
+      store_vec<T, V>(to + i * step, f[i]);
+    }
+    px += B * step;
+    pg += B * step;
+    to += B * step;
+  }
+}
+
 }  // namespace
 
-cudaError_t launch_team_nhwc(const NormPlan& p, const NormArgs& a, bool backward,
+cudaError_t launch_nhwc(const NormPlan& p, const NormArgs& a, bool backward,
                              cudaStream_t st) {
   const int cpg = p.s.cpg;
   if (!backward)
@@ -495,10 +856,10 @@ cudaError_t launch_team_nhwc(const NormPlan& p, const NormArgs& a, bool backward
       using T = decltype(t);
       return by_act(a.act, [&](auto act) {
         constexpr int ACT = decltype(act)::value;
-        return by_width<T>(p.s.t.v, [&](auto w) {
+        return by_width<T>(p.s.v, [&](auto w) {
           constexpr int V = decltype(w)::value;
           auto go = [&](auto kern) {
-            return launch_team(kern, p, p.col.cluster, st, p.s, p.col, static_cast<const T*>(a.x),
+            return launch_team(kern, p, p.col.blocks, st, p.s, p.col, static_cast<const T*>(a.x),
                                a.gamma, a.beta, static_cast<T*>(a.y), a.mean, a.rstd);
           };
           return cpg % V ? go(fwd_nhwc<T, V, false, ACT>) : go(fwd_nhwc<T, V, true, ACT>);
@@ -510,15 +871,66 @@ cudaError_t launch_team_nhwc(const NormPlan& p, const NormArgs& a, bool backward
     using TG = decltype(g);
     return by_act(a.act, [&](auto act) {
       constexpr int ACT = decltype(act)::value;
-      return by_width<T>(p.s.t.v, [&](auto w) {
+      return by_width<T>(p.s.v, [&](auto w) {
         constexpr int V = decltype(w)::value;
         auto go = [&](auto kern) {
-          return launch_team(kern, p, p.col.cluster, st, p.s, p.col, static_cast<const T*>(a.x),
+          return launch_team(kern, p, p.col.blocks, st, p.s, p.col, static_cast<const T*>(a.x),
                              static_cast<const TG*>(a.gy), a.gamma, a.beta,
                              static_cast<const float*>(a.mean), static_cast<const float*>(a.rstd),
                              static_cast<T*>(a.gx), reinterpret_cast<float2*>(a.ws));
         };
         return cpg % V ? go(bwd_nhwc<T, TG, V, false, ACT>) : go(bwd_nhwc<T, TG, V, true, ACT>);
+      });
+    });
+  });
+}
+
+cudaError_t launch_two_nhwc(const NormPlan& p, const NormArgs& a, bool backward, bool second,
+                            int img0, int count, cudaStream_t st) {
+  const unsigned grid = (unsigned)count * p.col.blocks * p.col.slices;
+  char* entry = a.ws + norm_part_bytes(p, a, backward);
+  if (!backward)
+    return by_dtype(a.dt, [&](auto t) {
+      using T = decltype(t);
+      const T* x = static_cast<const T*>(a.x);
+      float4* e = reinterpret_cast<float4*>(entry);
+      return by_width<T>(p.s.v, [&](auto w) {
+        constexpr int V = decltype(w)::value;
+        auto by_one = [&](auto one) {
+          constexpr bool ONE = decltype(one)::value != 0;
+          if (!second)
+            return launch_plain(stats_nhwc<T, V, ONE>, grid, kTwo, st, p.s, p.col, img0, x, e);
+          return by_act(a.act, [&](auto act) {
+            return launch_plain(apply_nhwc<T, V, ONE, decltype(act)::value>, grid, kTwo, st, p.s,
+                                p.col, img0, x, a.gamma, a.beta, static_cast<const float4*>(e),
+                                static_cast<T*>(a.y), a.mean, a.rstd);
+          });
+        };
+        return p.s.cpg % V ? by_one(Int<0>{}) : by_one(Int<1>{});
+      });
+    });
+  return by_dtypes(a, [&](auto t, auto g) {
+    using T = decltype(t);
+    using TG = decltype(g);
+    const T* x = static_cast<const T*>(a.x);
+    const TG* gy = static_cast<const TG*>(a.gy);
+    const float *mean = a.mean, *rstd = a.rstd;
+    float2* e = reinterpret_cast<float2*>(entry);
+    return by_act(a.act, [&](auto act) {
+      constexpr int ACT = decltype(act)::value;
+      return by_width<T>(p.s.v, [&](auto w) {
+        constexpr int V = decltype(w)::value;
+        auto by_one = [&](auto one) {
+          constexpr bool ONE = decltype(one)::value != 0;
+          if (!second)
+            return launch_smem(sums_nhwc<T, TG, V, ONE, ACT>, grid, kTwo, p.smem, st, p.s, p.col, img0,
+                               x, gy, a.gamma, a.beta, mean, rstd,
+                               reinterpret_cast<float2*>(a.ws), e);
+          return launch_plain(grads_nhwc<T, TG, V, ONE, ACT>, grid, kTwo, st, p.s, p.col, img0, x,
+                              gy, a.gamma, a.beta, mean, rstd, static_cast<const float2*>(e),
+                              static_cast<T*>(a.gx));
+        };
+        return p.s.cpg % V ? by_one(Int<0>{}) : by_one(Int<1>{});
       });
     });
   });

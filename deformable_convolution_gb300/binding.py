@@ -74,80 +74,81 @@ class DcError(RuntimeError):
         super().__init__(f"{what}: {status_string(status)}")
 
 
-_configured = False
+_configured = None  # the library, once its functions' types are set
 
 
 def lib() -> ctypes.CDLL:
     global _configured
+    if _configured is not None:
+        return _configured
     L = _native.load()
-    if not _configured:
-        vp, sz, i = ctypes.c_void_p, ctypes.c_size_t, ctypes.c_int
-        pp = ctypes.POINTER(DcProblem)
-        L.dc_out_h.argtypes = [pp]
-        L.dc_out_h.restype = i
-        L.dc_out_w.argtypes = [pp]
-        L.dc_out_w.restype = i
-        L.deform_conv_workspace_size.argtypes = [pp, i, ctypes.POINTER(sz)]
-        L.deform_conv_workspace_size.restype = i
-        L.deform_conv_fwd.argtypes = [pp, vp, vp, vp, vp, vp, vp, vp, vp, vp, sz, vp]
-        L.deform_conv_fwd.restype = i
-        L.deform_conv_bwd.argtypes = [pp, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, sz, vp]
-        L.deform_conv_bwd.restype = i
-        L.deform_conv_bwd_after_fwd.argtypes = [pp, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, sz, vp]
-        L.deform_conv_bwd_after_fwd.restype = i
-        L.deform_conv_sample.argtypes = [pp, vp, vp, vp, vp, vp, vp, vp, vp, vp, sz, vp]
-        L.deform_conv_sample.restype = i
-        L.dc_col_layout.argtypes = [pp]
-        L.dc_col_layout.restype = i
-        L.dc_sample_tile.argtypes = [pp, ctypes.POINTER(i), ctypes.POINTER(i)]
-        L.dc_sample_tile.restype = i
-        L.deform_conv_offsets.argtypes = [pp, vp, vp, vp, vp, vp, vp, sz, vp]
-        L.deform_conv_offsets.restype = i
-        L.deform_conv_fwd_sampled_gemm.argtypes = [pp, vp, vp, vp, vp, vp, vp, vp, vp]
-        L.deform_conv_fwd_sampled_gemm.restype = i
-        L.deform_conv_margin_histogram.argtypes = [pp, vp, vp, vp]
-        L.deform_conv_margin_histogram.restype = i
-        L.dc_suggest_margin.argtypes = [pp, ctypes.POINTER(ctypes.c_ulonglong), ctypes.c_double, i]
-        L.dc_suggest_margin.restype = i
-        L.dc_status_string.argtypes = [i]
-        L.dc_status_string.restype = ctypes.c_char_p
-        L.dc_build_info.argtypes = []
-        L.dc_build_info.restype = ctypes.c_char_p
-        L.deform_conv_fwd_noalloc.argtypes = [pp, vp, vp, vp, vp, vp, vp, vp, vp, vp]
-        L.deform_conv_fwd_noalloc.restype = i
-        L.dc_kernel_timing.argtypes = [i]
-        L.dc_kernel_timing.restype = None
-        L.dc_kernel_times.argtypes = [ctypes.POINTER(ctypes.c_char_p), ctypes.POINTER(ctypes.c_float), i]
-        L.dc_kernel_times.restype = i
-        L.dc_device_error.argtypes = [i]
-        L.dc_device_error.restype = i
-        L.dc_selftest_wait_timeout.argtypes = [ctypes.c_uint, vp]
-        L.dc_selftest_wait_timeout.restype = i
-        L.dc_test_fail_launches.argtypes = [i]
-        L.dc_test_fail_launches.restype = i
-        L.dc_relu_fwd.argtypes = [vp, vp, sz, i, vp]
-        L.dc_relu_fwd.restype = i
-        L.dc_relu_bwd.argtypes = [vp, vp, vp, sz, i, vp]
-        L.dc_relu_bwd.restype = i
-        pn, pt = ctypes.POINTER(DcNormProblem), ctypes.POINTER(DcAdamwTensor)
-        ph, pv = ctypes.POINTER(DcAdamwHyper), ctypes.POINTER(vp)
-        L.dc_group_norm_workspace_size.argtypes = [pn, i, ctypes.POINTER(sz)]
-        L.dc_group_norm_workspace_size.restype = i
-        L.dc_group_norm_fwd.argtypes = [pn, vp, vp, vp, vp, vp, vp, vp, sz, vp]
-        L.dc_group_norm_fwd.restype = i
-        L.dc_group_norm_bwd.argtypes = [pn, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, sz, vp]
-        L.dc_group_norm_bwd.restype = i
-        L.dc_adamw_step.argtypes = [pt, i, ph, vp, vp, vp]
-        L.dc_adamw_step.restype = i
-        L.dc_adamw_state_values.argtypes = [pt, i, pv, pv, vp]
-        L.dc_adamw_state_values.restype = i
-        L.dc_grad_norm_workspace_size.argtypes = [i, ctypes.POINTER(sz)]
-        L.dc_grad_norm_workspace_size.restype = i
-        L.dc_grad_norm.argtypes = [pt, i, ctypes.c_float, vp, vp, vp, sz, vp]
-        L.dc_grad_norm.restype = i
-        L.dc_launch_count.argtypes = []
-        L.dc_launch_count.restype = ctypes.c_ulonglong
-        _configured = True
+    vp, sz, i = ctypes.c_void_p, ctypes.c_size_t, ctypes.c_int
+    pp = ctypes.POINTER(DcProblem)
+    L.dc_out_h.argtypes = [pp]
+    L.dc_out_h.restype = i
+    L.dc_out_w.argtypes = [pp]
+    L.dc_out_w.restype = i
+    L.deform_conv_workspace_size.argtypes = [pp, i, ctypes.POINTER(sz)]
+    L.deform_conv_workspace_size.restype = i
+    L.deform_conv_fwd.argtypes = [pp, vp, vp, vp, vp, vp, vp, vp, vp, vp, sz, vp]
+    L.deform_conv_fwd.restype = i
+    L.deform_conv_bwd.argtypes = [pp, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, sz, vp]
+    L.deform_conv_bwd.restype = i
+    L.deform_conv_bwd_after_fwd.argtypes = [pp, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, sz, vp]
+    L.deform_conv_bwd_after_fwd.restype = i
+    L.deform_conv_sample.argtypes = [pp, vp, vp, vp, vp, vp, vp, vp, vp, vp, sz, vp]
+    L.deform_conv_sample.restype = i
+    L.dc_col_layout.argtypes = [pp]
+    L.dc_col_layout.restype = i
+    L.dc_sample_tile.argtypes = [pp, ctypes.POINTER(i), ctypes.POINTER(i)]
+    L.dc_sample_tile.restype = i
+    L.deform_conv_offsets.argtypes = [pp, vp, vp, vp, vp, vp, vp, sz, vp]
+    L.deform_conv_offsets.restype = i
+    L.deform_conv_fwd_sampled_gemm.argtypes = [pp, vp, vp, vp, vp, vp, vp, vp, vp]
+    L.deform_conv_fwd_sampled_gemm.restype = i
+    L.deform_conv_margin_histogram.argtypes = [pp, vp, vp, vp]
+    L.deform_conv_margin_histogram.restype = i
+    L.dc_suggest_margin.argtypes = [pp, ctypes.POINTER(ctypes.c_ulonglong), ctypes.c_double, i]
+    L.dc_suggest_margin.restype = i
+    L.dc_status_string.argtypes = [i]
+    L.dc_status_string.restype = ctypes.c_char_p
+    L.dc_build_info.argtypes = []
+    L.dc_build_info.restype = ctypes.c_char_p
+    L.deform_conv_fwd_noalloc.argtypes = [pp, vp, vp, vp, vp, vp, vp, vp, vp, vp]
+    L.deform_conv_fwd_noalloc.restype = i
+    L.dc_kernel_timing.argtypes = [i]
+    L.dc_kernel_timing.restype = None
+    L.dc_kernel_times.argtypes = [ctypes.POINTER(ctypes.c_char_p), ctypes.POINTER(ctypes.c_float), i]
+    L.dc_kernel_times.restype = i
+    L.dc_device_error.argtypes = [i]
+    L.dc_device_error.restype = i
+    L.dc_selftest_wait_timeout.argtypes = [ctypes.c_uint, vp]
+    L.dc_selftest_wait_timeout.restype = i
+    L.dc_test_fail_launches.argtypes = [i]
+    L.dc_test_fail_launches.restype = i
+    L.dc_relu_fwd.argtypes = [vp, vp, sz, i, vp]
+    L.dc_relu_fwd.restype = i
+    L.dc_relu_bwd.argtypes = [vp, vp, vp, sz, i, vp]
+    L.dc_relu_bwd.restype = i
+    pn, pt = ctypes.POINTER(DcNormProblem), ctypes.POINTER(DcAdamwTensor)
+    ph, pv = ctypes.POINTER(DcAdamwHyper), ctypes.POINTER(vp)
+    L.dc_group_norm_workspace_size.argtypes = [pn, i, ctypes.POINTER(sz)]
+    L.dc_group_norm_workspace_size.restype = i
+    L.dc_group_norm_fwd.argtypes = [pn, vp, vp, vp, vp, vp, vp, vp, sz, vp]
+    L.dc_group_norm_fwd.restype = i
+    L.dc_group_norm_bwd.argtypes = [pn, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, sz, vp]
+    L.dc_group_norm_bwd.restype = i
+    L.dc_adamw_step.argtypes = [pt, i, ph, vp, vp, vp]
+    L.dc_adamw_step.restype = i
+    L.dc_adamw_state_values.argtypes = [pt, i, pv, pv, vp]
+    L.dc_adamw_state_values.restype = i
+    L.dc_grad_norm_workspace_size.argtypes = [i, ctypes.POINTER(sz)]
+    L.dc_grad_norm_workspace_size.restype = i
+    L.dc_grad_norm.argtypes = [pt, i, ctypes.c_float, vp, vp, vp, sz, vp]
+    L.dc_grad_norm.restype = i
+    L.dc_launch_count.argtypes = []
+    L.dc_launch_count.restype = ctypes.c_ulonglong
+    _configured = L
     return L
 
 

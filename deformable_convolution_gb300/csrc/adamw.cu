@@ -472,6 +472,7 @@ template <typename TB>
 __global__ void __launch_bounds__(kThreads, 4)
     adamw_kernel(const __grid_constant__ TB tb, const __grid_constant__ AdamScalars h) {
   pdl_wait();
+  pdl_release();
   const Step st = make_step(h);
   const unsigned chunks = tb.first[tb.count];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -496,7 +497,6 @@ __global__ void __launch_bounds__(kThreads, 4)
       case 7: by_param<true, true, true>(t, base, lane, h, st); break;
     }
   }
-  pdl_release();
 }
 
 // The states as float32: Entry::param receives m, Entry::master v (either null).
@@ -521,6 +521,7 @@ __device__ __forceinline__ void whole_values(const Entry& t, long long base, int
 template <typename TB>
 __global__ void __launch_bounds__(kThreads) values_kernel(const __grid_constant__ TB tb) {
   pdl_wait();
+  pdl_release();
   const unsigned chunks = tb.first[tb.count];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   for (unsigned c = blockIdx.x; c < chunks; c += gridDim.x) {
@@ -552,7 +553,6 @@ __global__ void __launch_bounds__(kThreads) values_kernel(const __grid_constant_
       }
     }
   }
-  pdl_release();
 }
 
 // Sum over the block in a fixed order, in thread 0.
@@ -567,79 +567,82 @@ __device__ __forceinline__ float block_sum(float v) {
   return v;
 }
 
-// part[block] = sum of squares of the block's chunks.  A chunk is B batches of
-// kChunk elements whose loads are all under way before the first is used.
+// part[block] = sum of squares of the block's chunks.  A chunk is B vectors of
+// 16 bytes for every thread, all under way before the first is used; chunks
+// start `lead` elements ahead of their tensor, on a boundary of 16 bytes.
+template <typename T, int B>
+__device__ __forceinline__ void add_squares(const Entry& t, long long chunk, float (&sum)[8]) {
+  constexpr int V = 16 / sizeof(T);
+  const T* grad = static_cast<const T*>(t.grad);
+  const long long base = chunk * (B * kThreads * V) - t.lead + threadIdx.x * V;
+  uint4 w[B];
+  if ((chunk > 0 || t.lead == 0) && base - threadIdx.x * V + B * kThreads * V <= t.count) {
+#pragma unroll
+    for (int b = 0; b < B; ++b)
+      w[b] = *reinterpret_cast<const uint4*>(grad + base + b * kThreads * V);
+  } else {  // an end of the tensor lies in the chunk
+#pragma unroll
+    for (int b = 0; b < B; ++b) {
+      const long long at = base + b * kThreads * V;
+      w[b] = make_uint4(0u, 0u, 0u, 0u);
+      if (at >= 0 && at + V <= t.count) {
+        w[b] = *reinterpret_cast<const uint4*>(grad + at);
+      } else {
+        uint32_t* u = reinterpret_cast<uint32_t*>(&w[b]);
+#pragma unroll
+        for (int e = 0; e < V; ++e) {
+          if (at + e < 0 || at + e >= t.count) continue;
+          if (sizeof(T) == 4)
+            u[e] = reinterpret_cast<const uint32_t*>(grad)[at + e];
+          else
+            u[e >> 1] |= (uint32_t) reinterpret_cast<const unsigned short*>(grad)[at + e]
+                         << (16 * (e & 1));
+        }
+      }
+    }
+  }
+#pragma unroll
+  for (int b = 0; b < B; ++b) {
+    const uint32_t* u = reinterpret_cast<const uint32_t*>(&w[b]);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      if (sizeof(T) == 4) {
+        const float f = __uint_as_float(u[e]);
+        sum[e + 4 * (b & 1)] = fmaf(f, f, sum[e + 4 * (b & 1)]);
+      } else {
+        const float lo = __uint_as_float(u[e] << 16), hi = __uint_as_float(u[e] & 0xffff0000u);
+        sum[e] = fmaf(lo, lo, sum[e]);
+        sum[4 + e] = fmaf(hi, hi, sum[4 + e]);
+      }
+    }
+  }
+}
+
 template <int B, typename TB>
 __global__ void __launch_bounds__(kThreads)
     squares_kernel(const __grid_constant__ TB tb, float* part) {
   pdl_wait();
+  pdl_release();
   const unsigned chunks = tb.first[tb.count];
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  float sum[kPer] = {};
+  float sum[8] = {};
   for (unsigned c = blockIdx.x; c < chunks; c += gridDim.x) {
     const int ti = find(tb, c);
     const Entry& t = tb.t[ti];
-    const long long base =
-        (long long)(c - tb.first[ti]) * (B * kChunk) + warp * DC_STATE_BLOCK - t.lead;
-    if (t.vec && base >= 0 && base + (B - 1) * kChunk + DC_STATE_BLOCK <= t.count) {
-      if (t.g16) {
-        const __nv_bfloat16* p = static_cast<const __nv_bfloat16*>(t.grad) + base;
-        uint2 w[2 * B];
-#pragma unroll
-        for (int b = 0; b < 2 * B; ++b)
-          w[b] = *reinterpret_cast<const uint2*>(p + (b >> 1) * kChunk + (b & 1) * 128 + lane * 4);
-#pragma unroll
-        for (int b = 0; b < 2 * B; ++b) {
-          const float f[4] = {__uint_as_float(w[b].x << 16), __uint_as_float(w[b].x & 0xffff0000u),
-                              __uint_as_float(w[b].y << 16), __uint_as_float(w[b].y & 0xffff0000u)};
-#pragma unroll
-          for (int e = 0; e < 4; ++e) sum[4 * (b & 1) + e] = fmaf(f[e], f[e], sum[4 * (b & 1) + e]);
-        }
-      } else {
-        const float* p = static_cast<const float*>(t.grad) + base;
-        float f[B][kPer];
-#pragma unroll
-        for (int b = 0; b < B; ++b) load8<true>(p + b * kChunk, lane, f[b]);
-#pragma unroll
-        for (int b = 0; b < B; ++b)
-#pragma unroll
-          for (int k = 0; k < kPer; ++k) sum[k] = fmaf(f[b][k], f[b][k], sum[k]);
-      }
-      continue;
-    }
-    // a chunk over an end of its tensor: by batches, whole ones as above
-#pragma unroll 1
-    for (int b = 0; b < B; ++b) {
-      const long long at = base + b * kChunk;
-      float f[kPer];
-      if (t.vec && at >= 0 && at + DC_STATE_BLOCK <= t.count) {
-        if (t.g16)
-          load8<true>(static_cast<const __nv_bfloat16*>(t.grad) + at, lane, f);
-        else
-          load8<true>(static_cast<const float*>(t.grad) + at, lane, f);
-      } else {
-#pragma unroll
-        for (int k = 0; k < kPer; ++k) {
-          const long long i = at + lane + 32 * k;
-          f[k] = i < 0 || i >= t.count ? 0.f
-                 : t.g16               ? to_f(static_cast<const __nv_bfloat16*>(t.grad)[i])
-                                       : static_cast<const float*>(t.grad)[i];
-        }
-      }
-#pragma unroll
-      for (int k = 0; k < kPer; ++k) sum[k] = fmaf(f[k], f[k], sum[k]);
-    }
+    if (t.g16)
+      add_squares<__nv_bfloat16, B>(t, c - tb.first[ti], sum);
+    else
+      add_squares<float, B>(t, c - tb.first[ti], sum);
   }
   const float all = block_sum(((sum[0] + sum[1]) + (sum[2] + sum[3])) +
                               ((sum[4] + sum[5]) + (sum[6] + sum[7])));
   if (threadIdx.x == 0) part[blockIdx.x] = all;
-  pdl_release();
 }
 
 __global__ void __launch_bounds__(1024)
     grad_norm_kernel(const float* part, long long parts, float max_norm, float* norm,
                      float* scale) {
   pdl_wait();
+  pdl_release();
   float sum = 0.f;
   for (long long i = threadIdx.x; i < parts; i += 1024) sum += part[i];
   sum = block_sum(sum);
@@ -651,7 +654,6 @@ __global__ void __launch_bounds__(1024)
       *scale = isfinite(n) ? fminf(r, 1.f) : __uint_as_float(0x7fc00000u);
     }
   }
-  pdl_release();
 }
 
 int sm_count() {
@@ -705,7 +707,8 @@ void set_grid(Entry* e, const Array (&arrays)[N]) {
 enum class Use { kStep, kValues, kGrad };
 
 // The tensors of one launch; false if their chunks do not fit in 32 bits.
-// Values go to m[i] and v[i].
+// chunk: elements of one, or (kGrad) its 16-byte vectors.  Values go to m[i]
+// and v[i].
 template <int N>
 bool fill(Table<N>* tb, const dc_adamw_tensor* t, int count, int chunk, Use use,
           float* const* m, float* const* v) {
@@ -724,12 +727,14 @@ bool fill(Table<N>* tb, const dc_adamw_tensor* t, int count, int chunk, Use use,
       e.master = v ? v[i] : nullptr;
       set_grid(&e, {{e.m, st}, {e.v, st}, {e.param, 4}, {e.master, 4}});
     } else if (use == Use::kGrad) {
-      set_grid(&e, {{e.grad, gr}});
+      e.lead = (unsigned char)((uintptr_t)e.grad % 16 / gr);
     } else {
       set_grid(&e, {{e.param, e.p16 ? 2 : 4}, {e.master, 4}, {e.grad, gr}, {e.m, st}, {e.v, st}});
     }
     tb->first[i] = (unsigned)at;
-    if (e.count) at += (unsigned long long)ceil_div_ll(e.count + e.lead, chunk);
+    if (e.count)
+      at += (unsigned long long)ceil_div_ll(e.count + e.lead,
+                                            use == Use::kGrad ? chunk * 16 / gr : chunk);
     if (at > UINT_MAX / 2) return false;
   }
   tb->first[count] = (unsigned)at;
@@ -776,19 +781,19 @@ cudaError_t launch_adamw_values(const dc_adamw_tensor* t, int count, float* cons
   });
 }
 
-// part: kNormParts floats, all written.  Chunks of four batches keep enough
-// loads in flight; few elements are spread over the blocks one batch at a time.
+// part: kNormParts floats, all written.  Eight vectors a thread keep enough
+// loads in flight; few elements are spread over the blocks two at a time.
 cudaError_t launch_grad_squares(const dc_adamw_tensor* t, int count, float* part,
                                 cudaStream_t s) {
-  long long total = 0;
-  for (int i = 0; i < count; ++i) total += t[i].count;
-  const bool large = total > 4LL * kNormParts * kChunk;
-  return with_table(t, count, large ? 4 * kChunk : kChunk, Use::kGrad, nullptr, nullptr,
+  double bytes = 0;
+  for (int i = 0; i < count; ++i) bytes += (double)t[i].count * (t[i].grad_dtype == DC_BF16 ? 2 : 4);
+  const bool large = bytes > 8.0 * kThreads * 16 * kNormParts;
+  return with_table(t, count, (large ? 8 : 2) * kThreads, Use::kGrad, nullptr, nullptr,
                     [&](const auto& tb) {
     using TB = std::decay_t<decltype(tb)>;
     if (large)
-      return launch(squares_kernel<4, TB>, (unsigned)kNormParts, kThreads, s, tb, part);
-    return launch(squares_kernel<1, TB>, (unsigned)kNormParts, kThreads, s, tb, part);
+      return launch(squares_kernel<8, TB>, (unsigned)kNormParts, kThreads, s, tb, part);
+    return launch(squares_kernel<2, TB>, (unsigned)kNormParts, kThreads, s, tb, part);
   });
 }
 

@@ -396,7 +396,7 @@ constexpr int kAdamTensors = 384;
 cudaError_t launch_adamw(const dc_adamw_tensor* t, int count, const AdamScalars& h, cudaStream_t s);
 cudaError_t launch_adamw_values(const dc_adamw_tensor* t, int count, float* const* m,
                                 float* const* v, cudaStream_t s);
-constexpr int kNormParts = 1216;  // 8 blocks on each of 152 SMs: partial sums of one gradient-norm launch
+constexpr int kNormParts = 760;  // 5 blocks on each of 152 SMs: partial sums of one gradient-norm launch
 cudaError_t launch_grad_squares(const dc_adamw_tensor* t, int count, float* part, cudaStream_t s);
 cudaError_t launch_grad_norm(const float* part, long long parts, float max_norm, float* norm,
                              float* scale, cudaStream_t s);

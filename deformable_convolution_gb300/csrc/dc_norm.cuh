@@ -182,6 +182,17 @@ __device__ __forceinline__ float rcp_approx(float x) {
   asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
+// sum / n by the approximate reciprocal w of n and the remainder: exact where
+// the quotient is a float (a constant's mean is the constant).
+__device__ __forceinline__ float quotient(float sum, float n, float w) {
+  const float m = sum * w;
+  return fmaf(fmaf(-m, n, sum), w, m);
+}
+__device__ __forceinline__ float2 quotient2(float2 sum, float n, float w) {
+  const float2 m = mul2(sum, both(w));
+  return fma2(fma2(make_float2(-m.x, -m.y), both(n), sum), both(w), m);
+}
+
 // 1 / (1 + exp(-z))
 __device__ __forceinline__ float2 sigmoid2(float2 z) {
   const float2 t = mul2(z, both(-1.4426950408889634f));
@@ -327,7 +338,7 @@ __host__ __device__ inline int row_vectors(int hw, int mis, int vec) {
 __device__ __forceinline__ void merge(float& n, float& mean, float& m2, float nb, float mb,
                                       float m2b) {
   if (nb == 0.f) return;
-  const float t = n + nb, d = mb - mean, w = __fdividef(nb, t);
+  const float t = n + nb, d = mb - mean, w = quotient(nb, t, rcp_approx(t));
   mean += d * w;
   m2 += m2b + d * d * n * w;
   n = t;

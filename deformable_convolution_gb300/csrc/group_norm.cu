@@ -134,6 +134,11 @@ bool plan_rows(const NormArgs& a, bool backward, int planes, NormPlan* p) {
   return true;
 }
 
+// The forward's table of channel statistics and its partial triples.
+size_t stats_table(const ColTeam& c, int threads) {
+  return ((size_t)c.rows * c.width + 1) / 2 * 2 * sizeof(float2) + (size_t)threads * sizeof(float4);
+}
+
 bool plan_cols(const NormArgs& a, bool backward, bool keep, NormPlan* p) {
   ColTeam& c = p->col;
   const int v = p->s.v, elt = a.dt == DC_BF16 ? 2 : 4;
@@ -168,8 +173,12 @@ bool plan_cols(const NormArgs& a, bool backward, bool keep, NormPlan* p) {
   const long long slot = (long long)p->threads * held_bytes;
   c.held = slot * slots <= kBlockBytes ? slots : (int)(kBlockBytes / slot);
   c.rows = 32 % c.cb ? c.rl : p->threads / 32;
-  p->smem = (size_t)(slot * c.held) + (size_t)c.blocks * c.ng * (backward ? 2 : 3) * sizeof(float);
-  if (backward) p->smem += (size_t)c.rows * c.width * sizeof(float2);
+  p->smem = (size_t)(slot * c.held) +
+            (size_t)(c.blocks * c.ng * (backward ? 2 : 3) + 3) / 4 * 4 * sizeof(float);
+  if (backward)
+    p->smem += (size_t)c.rows * c.width * sizeof(float2);
+  else if (a.cpg % v)
+    p->smem += stats_table(c, p->threads);
   p->blocks = (unsigned)(units * c.blocks);
   p->parts = c.blocks;
   return true;
@@ -225,7 +234,10 @@ void plan_two(const NormArgs& a, bool backward, int planes, NormPlan* p) {
   c.span = (int)ceil_div_ll(a.hw, c.blocks);
   c.shares = c.slices == 1 ? 1 : (a.cpg + c.width - 2) / c.width + 1;
   c.rows = 32 % c.cb ? c.rl : kTwo / 32;
-  p->smem = (size_t)c.rows * c.width * sizeof(float2);
+  if (backward)
+    p->smem = (size_t)c.rows * c.width * sizeof(float2);
+  else if (a.cpg % s.v)
+    p->smem = stats_table(c, kTwo);
   p->parts = c.blocks;
 }
 

@@ -199,7 +199,7 @@ __device__ __forceinline__ void add_batch(int most, int cnt, float& n, float& me
 #pragma unroll
     for (int e = 0; e < VEC / 2; ++e) sum = add2(sum, f[b].p[e]);
   }
-  const float mb = (sum.x + sum.y) * rcp_approx((float)cnt);
+  const float mb = quotient(sum.x + sum.y, (float)cnt, rcp_approx((float)cnt));
 #pragma unroll
   for (int b = 0; b < B; ++b) {
     if (b >= most) continue;

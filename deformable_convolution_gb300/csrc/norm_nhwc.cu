@@ -101,10 +101,10 @@ __device__ __forceinline__ void add_batch(int most, float& n, M& mean, M& m2, GE
     for (int e = 0; e < P; ++e) sum[ONE ? 0 : e] = add2(sum[ONE ? 0 : e], f[b].p[e]);
   }
   const float cnt = (float)(ONE ? most * V : most), t = n + cnt;
-  const float w = rcp_approx(cnt), wn = cnt * rcp_approx(t), c = n * wn;
+  const float w = rcp_approx(cnt), wn = quotient(cnt, t, rcp_approx(t)), c = n * wn;
 #pragma unroll
   for (int e = 0; e < EP; ++e)  // the means
-    sum[e] = ONE ? both((sum[e].x + sum[e].y) * w) : mul2(sum[e], both(w));
+    sum[e] = ONE ? both(quotient(sum[e].x + sum[e].y, cnt, w)) : quotient2(sum[e], cnt, w);
 #pragma unroll
   for (int b = 0; b < kBatch; ++b) {
     if (b >= most) continue;
@@ -126,17 +126,104 @@ __device__ __forceinline__ void add_batch(int most, float& n, M& mean, M& m2, GE
   n = t;
 }
 
+// The block's triples of its channels, where a vector's channels are of several
+// groups: tab[rows][width] holds the pixel lanes' (mean, M2) (or, where a warp
+// holds whole pixels, the warps'), cnt[row] their counts; merged by `lanes`
+// threads a channel, then by one, into tab[0 .. width) and *n (the count).
+template <int V, typename M>
+__device__ __forceinline__ void channel_stats(int cb, int rl, int rows, int cols, int lane_px,
+                                              int col, bool live, float n, M mean, M m2,
+                                              float2* tab, float* cnt, float4* ps, float* total) {
+  constexpr int P = Pairs<V>::n;
+  const int width = cb * V, lane = threadIdx.x & 31;
+  int row = lane_px;
+  bool put = live;
+  if (32 % cb == 0) {
+    float c = n;
+    for (int o = 16; o >= cb; o >>= 1) c += __shfl_xor_sync(0xffffffffu, c, o);
+    const float w = rcp_approx(fmaxf(c, 1.f));
+    Pairs<2 * P> m;
+#pragma unroll
+    for (int e = 0; e < P; ++e) m.p[e] = mul2(mean.p[e], both(n));
+    for (int o = 16; o >= cb; o >>= 1)
+#pragma unroll
+      for (int e = 0; e < V; ++e) m[e] += __shfl_xor_sync(0xffffffffu, m[e], o);
+#pragma unroll
+    for (int e = 0; e < P; ++e) {
+      m.p[e] = quotient2(m.p[e], fmaxf(c, 1.f), w);
+      const float2 d = add2(mean.p[e], make_float2(-m.p[e].x, -m.p[e].y));
+      if (n > 0.f) m2.p[e] = fma2(mul2(d, d), both(n), m2.p[e]);
+    }
+    for (int o = 16; o >= cb; o >>= 1)
+#pragma unroll
+      for (int e = 0; e < V; ++e) m2[e] += __shfl_xor_sync(0xffffffffu, m2[e], o);
+#pragma unroll
+    for (int e = 0; e < P; ++e) mean.p[e] = m.p[e];
+    n = c;
+    row = threadIdx.x >> 5;
+    put = lane < cb && col < cols;
+  }
+  if (put) {
+#pragma unroll
+    for (int e = 0; e < V; ++e) tab[row * width + col * V + e] = make_float2(mean[e], m2[e]);
+    if (col == 0) cnt[row] = n;
+  }
+  __syncthreads();
+  const int used = cols * V;
+  const int lanes = (int)blockDim.x > used ? min((int)blockDim.x / used, rows) : 1;
+  for (int i = threadIdx.x; i < lanes * used; i += blockDim.x) {
+    const int l0 = i / used, c = i - l0 * used;
+    float tn = 0.f, tm = 0.f, tq = 0.f;
+    for (int l = l0; l < rows; l += lanes) {
+      const float2 v = tab[l * width + c];
+      merge(tn, tm, tq, cnt[l], v.x, v.y);
+    }
+    if (lanes > 1) {
+      ps[i] = make_float4(tn, tm, tq, 0.f);
+    } else {
+      tab[c] = make_float2(tm, tq);  // (row 0's own entry: read above by this thread alone)
+      if (c == 0) *total = tn;
+    }
+  }
+  __syncthreads();
+  if (lanes > 1) {
+    for (int c = threadIdx.x; c < used; c += blockDim.x) {
+      float tn = 0.f, tm = 0.f, tq = 0.f;
+      for (int l = 0; l < lanes; ++l) {
+        const float4 v = ps[l * used + c];
+        merge(tn, tm, tq, v.x, v.y, v.z);
+      }
+      tab[c] = make_float2(tm, tq);
+      if (c == 0) *total = tn;
+    }
+    __syncthreads();
+  }
+}
+
+// f(group, lane, lanes) for the groups [0, ng) of a block, `lanes` neighbouring
+// threads each, no more than 32 and no more than `most` is of use to; f runs in
+// whole warps (and for groups at or past ng).
+template <typename F>
+__device__ __forceinline__ void each_group(int ng, int most, F&& f) {
+  int lanes = 1;
+  while (lanes < 32 && lanes < most && 2 * lanes * ng <= (int)blockDim.x) lanes *= 2;
+  const int first = threadIdx.x / lanes;
+  for (int g = first; g - first < ng; g += blockDim.x / lanes)
+    f(g, (int)threadIdx.x & (lanes - 1), lanes);
+}
+
 // ONE: a vector's channels are all of one group; else channels are kept apart
-// until the block's are merged.  Dynamic shared memory: the slots, then the
-// blocks' triples of the unit's groups, [3][cluster][ng].
+// until the block's are merged.  Dynamic shared memory: the slots, the blocks'
+// triples of the unit's groups, [3][cluster][ng], then (not ONE) the table of
+// channel_stats and its partial triples.
 template <typename T, int V, bool ONE, int ACT>
 __global__ void __launch_bounds__(kTeam, ONE || V < 8 ? 2 : 1)
     fwd_nhwc(Shape s, ColTeam tm, const T* x, const float* gamma, const float* beta, T* y,
              float* mean_out, float* rstd_out) {
-  constexpr int P = Pairs<V>::n, E = ONE ? 1 : V, EP = ONE ? 1 : P;
+  constexpr int P = Pairs<V>::n, EP = ONE ? 1 : P;
   extern __shared__ uint4 hold[];
   __shared__ float2 ent[kTeam];
-  __shared__ float cnts[kTeam];
+  __shared__ float cnts[kTeam + 1];
   const bool many = tm.blocks > 1;
   if (many) cluster_arrive();
   pdl_wait();
@@ -170,49 +257,57 @@ __global__ void __launch_bounds__(kTeam, ONE || V < 8 ? 2 : 1)
       add_batch<V, ONE>(kBatch, n, mean, m2, get);
     if (i < held) add_batch<V, ONE>(held - i, n, mean, m2, get);
   }
-  // the block's groups, a warp each: entries of every pixel lane, channel by
-  // channel of the vector where those are apart
-  const int cols = ONE ? s.cpg / V : tm.cb;  // columns of a group (all, where they mix)
-  cnts[threadIdx.x] = n;
-  if (many) cluster_wait();
-  for (int g0 = 0; g0 < tm.ng; g0 += warps) {
-    const int g = g0 + warp;
-    float gn = 0.f, gm = 0.f, gq = 0.f;
-#pragma unroll 1
-    for (int e = 0; e < E; ++e) {
-      __syncthreads();
-      float a = mean.p[0].x, b = m2.p[0].x;
-#pragma unroll
-      for (int j = 1; j < E; ++j)
-        if (j == e) a = mean[j], b = m2[j];
-      ent[threadIdx.x] = make_float2(a, b);
-      __syncthreads();
-      if (g >= tm.ng) continue;
-      const int entries = cols * tm.rl;
+  // the block's groups, to every block of the cluster
+  auto send = [&](int g, int lane_g, int lanes, float gn, float gm, float gq) {
+    const int at = k.rank * tm.ng + g;
+    if (many) {
+      for (int j = lane_g; j < tm.blocks; j += lanes) {
+        store_cluster(&sn[at], j, gn);
+        store_cluster(&sm[at], j, gm);
+        store_cluster(&sq[at], j, gq);
+      }
+    } else if (lane_g == 0) {
+      sn[at] = gn, sm[at] = gm, sq[at] = gq;
+    }
+  };
+  if constexpr (ONE) {
+    ent[threadIdx.x] = make_float2(mean.p[0].x, m2.p[0].x);
+    cnts[threadIdx.x] = n;
+    __syncthreads();
+    if (many) cluster_wait();
+    // a warp each: entries of every pixel lane and column
+    const int cols = s.cpg / V;
+    for (int g = warp; g < tm.ng; g += warps) {
       float ln = 0.f, lm = 0.f, lq = 0.f;
-      for (int i = lane; i < entries; i += 32) {
-        const int l = cols == 1 ? i : i / cols, j = i - l * cols;
-        const int th = l * tm.cb + (ONE ? g * cols + j : j);
-        if (!ONE && (j * V + e) / s.cpg != g) continue;
+      for (int i = lane; i < cols * tm.rl; i += 32) {
+        const int l = cols == 1 ? i : i / cols, th = l * tm.cb + g * cols + i - l * cols;
         const float2 v = ent[th];
         merge(ln, lm, lq, cnts[th], v.x, v.y);
       }
       const float c = warp_sum(ln);
       const float m = warp_sum(ln * lm) / fmaxf(c, 1.f);
       const float q = warp_sum(ln > 0.f ? fmaf(ln * (lm - m), lm - m, lq) : 0.f);
-      merge(gn, gm, gq, c, m, q);
+      send(g, lane, 32, c, m, q);
     }
-    if (g >= tm.ng) continue;
-    const int at = k.rank * tm.ng + g;
-    if (many) {
-      if (lane < tm.blocks) {
-        store_cluster(&sn[at], lane, gn);
-        store_cluster(&sm[at], lane, gm);
-        store_cluster(&sq[at], lane, gq);
-      }
-    } else if (lane == 0) {
-      sn[at] = gn, sm[at] = gm, sq[at] = gq;
-    }
+  } else {
+    float2* tab = reinterpret_cast<float2*>(sn + (3 * tm.blocks * tm.ng + 3) / 4 * 4);
+    float4* ps = reinterpret_cast<float4*>(tab + ((tm.rows * tm.width + 1) & ~1));
+    channel_stats<V>(tm.cb, tm.rl, tm.rows, tm.cb, k.lane, k.col, k.live, n, mean, m2, tab, cnts,
+                     ps, &cnts[kTeam]);
+    if (many) cluster_wait();
+    const float cn = cnts[kTeam];
+    each_group(tm.ng, s.cpg, [&](int g, int lane_g, int lanes) {
+      float ln = 0.f, lm = 0.f, lq = 0.f;
+      if (g < tm.ng)
+        for (int i = lane_g; i < s.cpg; i += lanes) {
+          const float2 v = tab[g * s.cpg + i];
+          merge(ln, lm, lq, cn, v.x, v.y);
+        }
+      const float c = row_sum(ln, lanes);
+      const float m = row_sum(ln * lm, lanes) / fmaxf(c, 1.f);
+      const float q = row_sum(ln > 0.f ? fmaf(ln * (lm - m), lm - m, lq) : 0.f, lanes);
+      if (g < tm.ng) send(g, lane_g, lanes, c, m, q);
+    });
   }
   if (many) {
     cluster_arrive();
@@ -522,23 +617,14 @@ struct Loose {
   }
 };
 
-// f(group's index in the block, lane, lanes) for the block's groups, `lanes`
-// neighbouring threads each; f runs in whole warps.
-template <typename F>
-__device__ __forceinline__ void each_group(int ng, F&& f) {
-  int lanes = 1;
-  while (lanes < 32 && 2 * lanes * ng <= kTwo) lanes *= 2;
-  for (int g = threadIdx.x / lanes; g - (int)threadIdx.x / lanes < ng; g += kTwo / lanes)
-    f(g, threadIdx.x & (lanes - 1), lanes);
-}
-
 // entry = (count, mean, M2) of a group's share of a block.
 template <typename T, int V, bool ONE>
 __global__ void __launch_bounds__(kTwo)
     stats_nhwc(Shape s, ColTeam tm, int img0, const T* x, float4* entry) {
-  constexpr int P = Pairs<V>::n, E = ONE ? 1 : V, EP = ONE ? 1 : P;
+  constexpr int P = Pairs<V>::n, EP = ONE ? 1 : P;
+  extern __shared__ float2 tab[];  // (not ONE) of channel_stats, and its partial triples
   __shared__ float2 ent[kTwo];
-  __shared__ float cnts[kTwo];
+  __shared__ float cnts[kTwo + 1];
   pdl_wait();
   pdl_release();
   const Loose<V> k(s, tm, img0);
@@ -554,39 +640,44 @@ __global__ void __launch_bounds__(kTwo)
   for (; i + kBatch <= k.count; i += kBatch, px += kBatch * step)
     add_batch<V, ONE>(kBatch, n, mean, m2, get);
   if (i < k.count) add_batch<V, ONE>(k.count - i, n, mean, m2, get);
-  cnts[threadIdx.x] = n;
-  for (int q0 = 0; q0 < k.ng; q0 += kTwo / 32) {
-    const int g = k.g0 + q0 + warp;
-    const bool in = q0 + warp < k.ng;
-    // the group's columns in this block (all, where groups mix in a vector)
-    const int j0 = ONE ? max(0, g * s.cpg - k.c0) / V : 0;
-    const int j1 = ONE ? min(k.cols, ((g + 1) * s.cpg - k.c0) / V) : k.cols;
-    const int cols = max(j1 - j0, 1);
-    float gn = 0.f, gm = 0.f, gq = 0.f;
-#pragma unroll 1
-    for (int e = 0; e < E; ++e) {
-      __syncthreads();
-      float a = mean.p[0].x, b = m2.p[0].x;
-#pragma unroll
-      for (int j = 1; j < E; ++j)
-        if (j == e) a = mean[j], b = m2[j];
-      ent[threadIdx.x] = make_float2(a, b);
-      __syncthreads();
-      if (!in) continue;
+  if constexpr (ONE) {
+    ent[threadIdx.x] = make_float2(mean.p[0].x, m2.p[0].x);
+    cnts[threadIdx.x] = n;
+    __syncthreads();
+    for (int q = warp; q < k.ng; q += kTwo / 32) {
+      const int g = k.g0 + q;  // its columns in this block
+      const int j0 = max(0, g * s.cpg - k.c0) / V;
+      const int cols = min(k.cols, ((g + 1) * s.cpg - k.c0) / V) - j0;
       float ln = 0.f, lm = 0.f, lq = 0.f;
-      for (int q = lane; q < cols * tm.rl; q += 32) {
-        const int l = cols == 1 ? q : q / cols, j = j0 + q - l * cols;
-        if (!ONE && (k.c0 + j * V + e) / s.cpg != g) continue;
-        const int th = l * tm.cb + j;
+      for (int i = lane; i < cols * tm.rl; i += 32) {
+        const int l = cols == 1 ? i : i / cols, th = l * tm.cb + j0 + i - l * cols;
         const float2 v = ent[th];
         merge(ln, lm, lq, cnts[th], v.x, v.y);
       }
       const float c = warp_sum(ln);
       const float m = warp_sum(ln * lm) / fmaxf(c, 1.f);
-      const float q = warp_sum(ln > 0.f ? fmaf(ln * (lm - m), lm - m, lq) : 0.f);
-      merge(gn, gm, gq, c, m, q);
+      const float t = warp_sum(ln > 0.f ? fmaf(ln * (lm - m), lm - m, lq) : 0.f);
+      if (lane == 0) entry[k.entry(s, tm, g)] = make_float4(c, m, t, 0.f);
     }
-    if (in && lane == 0) entry[k.entry(s, tm, g)] = make_float4(gn, gm, gq, 0.f);
+  } else {
+    float4* ps = reinterpret_cast<float4*>(tab + ((tm.rows * tm.width + 1) & ~1));
+    channel_stats<V>(tm.cb, tm.rl, tm.rows, k.cols, k.lane, k.col, k.live, n, mean, m2, tab, cnts,
+                     ps, &cnts[kTwo]);
+    const float cn = cnts[kTwo];
+    const int used = k.cols * V;
+    each_group(k.ng, s.cpg, [&](int q, int lane_g, int lanes) {
+      const int g = k.g0 + q, c1 = min(used, (g + 1) * s.cpg - k.c0);
+      float ln = 0.f, lm = 0.f, lq = 0.f;
+      if (q < k.ng)
+        for (int c = max(0, g * s.cpg - k.c0) + lane_g; c < c1; c += lanes) {
+          const float2 v = tab[c];
+          merge(ln, lm, lq, cn, v.x, v.y);
+        }
+      const float c = row_sum(ln, lanes);
+      const float m = row_sum(ln * lm, lanes) / fmaxf(c, 1.f);
+      const float t = row_sum(ln > 0.f ? fmaf(ln * (lm - m), lm - m, lq) : 0.f, lanes);
+      if (q < k.ng && lane_g == 0) entry[k.entry(s, tm, g)] = make_float4(c, m, t, 0.f);
+    });
   }
 }
 
@@ -611,7 +702,7 @@ __global__ void __launch_bounds__(kTwo)
   pdl_release();
   const Loose<V> k(s, tm, img0);
   const float total = (float)s.hw * (float)s.cpg;
-  each_group(k.ng, [&](int q, int lane, int lanes) {
+  each_group(k.ng, 32, [&](int q, int lane, int lanes) {
     float n = 0.f, mean = 0.f, m2 = 0.f;
     const int g = k.g0 + q;
     if (q < k.ng) {
@@ -777,7 +868,7 @@ __global__ void __launch_bounds__(kTwo)
   pdl_release();
   const Loose<V> k(s, tm, img0);
   const float total = (float)s.hw * (float)s.cpg;
-  each_group(k.ng, [&](int q, int lane, int lanes) {
+  each_group(k.ng, 32, [&](int q, int lane, int lanes) {
     float a1 = 0.f, b1 = 0.f;
     const int g = k.g0 + q;
     if (q < k.ng) {
@@ -899,7 +990,7 @@ cudaError_t launch_two_nhwc(const NormPlan& p, const NormArgs& a, bool backward,
         auto by_one = [&](auto one) {
           constexpr bool ONE = decltype(one)::value != 0;
           if (!second)
-            return launch_plain(stats_nhwc<T, V, ONE>, grid, kTwo, st, p.s, p.col, img0, x, e);
+            return launch_smem(stats_nhwc<T, V, ONE>, grid, kTwo, p.smem, st, p.s, p.col, img0, x, e);
           return by_act(a.act, [&](auto act) {
             return launch_plain(apply_nhwc<T, V, ONE, decltype(act)::value>, grid, kTwo, st, p.s,
                                 p.col, img0, x, a.gamma, a.beta, static_cast<const float4*>(e),

@@ -338,7 +338,7 @@ __host__ __device__ inline int row_vectors(int hw, int mis, int vec) {
 __device__ __forceinline__ void merge(float& n, float& mean, float& m2, float nb, float mb,
                                       float m2b) {
   if (nb == 0.f) return;
-  const float t = n + nb, d = mb - mean, w = quotient(nb, t, rcp_approx(t));
+  const float t = n + nb, d = mb - mean, w = n > 0.f ? nb * rcp_approx(t) : 1.f;
   mean += d * w;
   m2 += m2b + d * d * n * w;
   n = t;

@@ -277,7 +277,7 @@ __global__ void __launch_bounds__(kTeam, 2)
     fwd_nchw(Shape s, RowTeam tm, const T* x, const float* gamma, const float* beta, T* y,
              float* mean_out, float* rstd_out) {
   constexpr int VEC = VecOf<T>::n;
-  extern __shared__ uint4 hold[];
+  extern __shared__ __align__(128) uint4 hold[];
   __shared__ float sm[3][256];
   if (tm.blocks > 1) cluster_arrive();
   pdl_wait();
@@ -323,7 +323,7 @@ __global__ void __launch_bounds__(kTeam, 2)
     fwd_flat(Shape s, RowTeam tm, const T* x, const float* gamma, const float* beta, T* y,
              float* mean_out, float* rstd_out) {
   constexpr int VEC = VecOf<T>::n;
-  extern __shared__ uint4 hold[];
+  extern __shared__ __align__(128) uint4 hold[];
   __shared__ float sm[3][256];
   if (tm.blocks > 1) cluster_arrive();
   pdl_wait();
@@ -491,7 +491,7 @@ __global__ void __launch_bounds__(kTeam, 2)
   constexpr int VEC = VecOf<T>::n;
   constexpr bool KEEP = keep_dz(sizeof(TG) == 4, ACT);
   constexpr int kG = KEEP ? VEC / 4 : kPieces<TG, VEC>;  // pieces of a slot of grad_y
-  extern __shared__ uint4 hold[];
+  extern __shared__ __align__(128) uint4 hold[];
   __shared__ float sm[2][256];
   if (tm.blocks > 1) cluster_arrive();
   pdl_wait();

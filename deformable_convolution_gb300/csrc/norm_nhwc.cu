@@ -101,7 +101,7 @@ __device__ __forceinline__ void add_batch(int most, float& n, M& mean, M& m2, GE
     for (int e = 0; e < P; ++e) sum[ONE ? 0 : e] = add2(sum[ONE ? 0 : e], f[b].p[e]);
   }
   const float cnt = (float)(ONE ? most * V : most), t = n + cnt;
-  const float w = rcp_approx(cnt), wn = quotient(cnt, t, rcp_approx(t)), c = n * wn;
+  const float w = rcp_approx(cnt), wn = n > 0.f ? cnt * rcp_approx(t) : 1.f, c = n * wn;
 #pragma unroll
   for (int e = 0; e < EP; ++e)  // the means
     sum[e] = ONE ? both(quotient(sum[e].x + sum[e].y, cnt, w)) : quotient2(sum[e], cnt, w);
@@ -221,9 +221,10 @@ __global__ void __launch_bounds__(kTeam, ONE || V < 8 ? 2 : 1)
     fwd_nhwc(Shape s, ColTeam tm, const T* x, const float* gamma, const float* beta, T* y,
              float* mean_out, float* rstd_out) {
   constexpr int P = Pairs<V>::n, EP = ONE ? 1 : P;
-  extern __shared__ uint4 hold[];
+  extern __shared__ __align__(128) uint4 hold[];
   __shared__ float2 ent[kTeam];
-  __shared__ float cnts[kTeam + 1];
+  __shared__ float cnts[kTeam];
+  __shared__ float total_n;
   const bool many = tm.blocks > 1;
   if (many) cluster_arrive();
   pdl_wait();
@@ -293,9 +294,9 @@ __global__ void __launch_bounds__(kTeam, ONE || V < 8 ? 2 : 1)
     float2* tab = reinterpret_cast<float2*>(sn + (3 * tm.blocks * tm.ng + 3) / 4 * 4);
     float4* ps = reinterpret_cast<float4*>(tab + ((tm.rows * tm.width + 1) & ~1));
     channel_stats<V>(tm.cb, tm.rl, tm.rows, tm.cb, k.lane, k.col, k.live, n, mean, m2, tab, cnts,
-                     ps, &cnts[kTeam]);
+                     ps, &total_n);
     if (many) cluster_wait();
-    const float cn = cnts[kTeam];
+    const float cn = total_n;
     each_group(tm.ng, s.cpg, [&](int g, int lane_g, int lanes) {
       float ln = 0.f, lm = 0.f, lq = 0.f;
       if (g < tm.ng)
@@ -379,7 +380,7 @@ __global__ void __launch_bounds__(kTeam, ONE || V < 8 ? 2 : 1)
   constexpr int P = Pairs<V>::n;
   constexpr bool KEEP = keep_dz(sizeof(TG) == 4, ACT);
   using SG = std::conditional_t<KEEP, float, TG>;  // what a slot of grad_y has room for
-  extern __shared__ uint4 hold[];
+  extern __shared__ __align__(128) uint4 hold[];
   __shared__ float2 ps[kTeam];
   const bool many = tm.blocks > 1;
   if (many) cluster_arrive();
@@ -624,7 +625,8 @@ __global__ void __launch_bounds__(kTwo)
   constexpr int P = Pairs<V>::n, EP = ONE ? 1 : P;
   extern __shared__ float2 tab[];  // (not ONE) of channel_stats, and its partial triples
   __shared__ float2 ent[kTwo];
-  __shared__ float cnts[kTwo + 1];
+  __shared__ float cnts[kTwo];
+  __shared__ float total_n;
   pdl_wait();
   pdl_release();
   const Loose<V> k(s, tm, img0);
@@ -662,8 +664,8 @@ __global__ void __launch_bounds__(kTwo)
   } else {
     float4* ps = reinterpret_cast<float4*>(tab + ((tm.rows * tm.width + 1) & ~1));
     channel_stats<V>(tm.cb, tm.rl, tm.rows, k.cols, k.lane, k.col, k.live, n, mean, m2, tab, cnts,
-                     ps, &cnts[kTwo]);
-    const float cn = cnts[kTwo];
+                     ps, &total_n);
+    const float cn = total_n;
     const int used = k.cols * V;
     each_group(k.ng, s.cpg, [&](int q, int lane_g, int lanes) {
       const int g = k.g0 + q, c1 = min(used, (g + 1) * s.cpg - k.c0);

@@ -270,7 +270,22 @@ struct Shape {
   float eps;
   int v;                // NHWC: channels of a thread's vector
   int parts, seg, lpr;  // NCHW
+  // reciprocals: of a unit's values, cpg, parts and the columns of a block
+  // (a block runs its few hundred instructions of preparation once: a
+  // division in full is one part in twenty of them)
+  float inv_total, inv_cpg, inv_parts, inv_cb;
 };
+
+// a / b for 0 <= a < 2^20 by the rounded reciprocal of b: (a + 1/2) / b is at
+// least 1 / (2 b) from a whole number, the product's error below a / b * 2^-22.
+__device__ __forceinline__ int quick_div(int a, float inv) {
+  return (int)(((float)a + 0.5f) * inv);
+}
+
+// The mean of a unit from its sum.
+__device__ __forceinline__ float unit_mean(const Shape& s, float sum) {
+  return quotient(sum, (float)s.hw * (float)s.cpg, s.inv_total);
+}
 
 // How the blocks share the work.  A unit has `blocks` of them: a cluster that
 // holds the unit in shared memory from its statistics to its results (one
@@ -346,6 +361,11 @@ __device__ __forceinline__ void merge(float& n, float& mean, float& m2, float nb
 
 // Sum over the lpr lanes that share a row (lpr a power of two), in every lane.
 __device__ __forceinline__ float row_sum(float v, int lpr) {
+  if (lpr == 32) {
+#pragma unroll
+    for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+    return v;
+  }
   for (int o = lpr >> 1; o; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
   return v;
 }
@@ -393,7 +413,24 @@ __device__ __forceinline__ void copy_async(void* to, const void* from, int bytes
     asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(dst), "l"(from), "n"(BYTES)
                  : "memory");
 }
-__device__ __forceinline__ void copy_wait() { asm volatile("cp.async.wait_all;" ::: "memory"); }
+// Copies are grouped as they are started, and a thread waits until no more
+// than `open` of its groups are (or 7), so that it works on the first of its
+// vectors while the others arrive.
+__device__ __forceinline__ void copy_group() {
+  asm volatile("cp.async.commit_group;" ::: "memory");
+}
+__device__ __forceinline__ void copy_wait(int open) {
+  switch (open < 7 ? open : 7) {
+    case 0: asm volatile("cp.async.wait_group 0;" ::: "memory"); break;
+    case 1: asm volatile("cp.async.wait_group 1;" ::: "memory"); break;
+    case 2: asm volatile("cp.async.wait_group 2;" ::: "memory"); break;
+    case 3: asm volatile("cp.async.wait_group 3;" ::: "memory"); break;
+    case 4: asm volatile("cp.async.wait_group 4;" ::: "memory"); break;
+    case 5: asm volatile("cp.async.wait_group 5;" ::: "memory"); break;
+    case 6: asm volatile("cp.async.wait_group 6;" ::: "memory"); break;
+    default: asm volatile("cp.async.wait_group 7;" ::: "memory"); break;
+  }
+}
 
 template <typename K, typename... A>
 cudaError_t launch_team(K kern, const NormPlan& p, int cluster, cudaStream_t s, A... args) {

@@ -241,6 +241,14 @@ void plan_two(const NormArgs& a, bool backward, int planes, NormPlan* p) {
   p->parts = c.blocks;
 }
 
+void set_reciprocals(const NormArgs& a, NormPlan* p) {
+  Shape& s = p->s;
+  s.inv_total = (float)(1.0 / ((double)a.hw * a.cpg));
+  s.inv_cpg = 1.f / a.cpg;
+  s.inv_parts = s.parts ? 1.f / s.parts : 0.f;
+  s.inv_cb = p->col.cb ? 1.f / p->col.cb : 0.f;
+}
+
 NormPlan make_plan(const NormArgs& a, bool backward) {
   NormPlan p{};
   p.s = make_shape(a);
@@ -255,6 +263,7 @@ NormPlan make_plan(const NormArgs& a, bool backward) {
     p.s = make_shape(a);
     plan_two(a, backward, planes, &p);
   }
+  set_reciprocals(a, &p);
   return p;
 }
 

@@ -21,9 +21,9 @@ struct UnitTask {
   bool live;
   __device__ __forceinline__ UnitTask(const Shape& s, unsigned unit, int ch0, int t, int tasks) {
     const int lane = threadIdx.x & 31, per = 32 / s.lpr;
-    const int blk = s.parts == 1 ? t : t / s.parts;
+    const int blk = tasks < 1 << 20 ? quick_div(t, s.inv_parts) : t / s.parts;
     part = t - blk * s.parts;
-    const int local = blk * per + lane / s.lpr;
+    const int local = blk * per + (s.lpr == 32 ? 0 : lane / s.lpr);
     live = t < tasks && local < s.cpg;
     row = (long long)unit * s.cpg + (live ? local : 0);
     ch = ch0 + (live ? local : 0);
@@ -61,28 +61,24 @@ __device__ __forceinline__ void take(const uint4* slot, int plane, Pairs<VEC>& f
 // in planes of 16-byte pieces.  The lane's first slot of a round:
 __device__ __forceinline__ int first_slot(const Shape& s) {
   const int lane = threadIdx.x & 31, per = 32 / s.lpr;
-  return ((threadIdx.x >> 5) * per + lane / s.lpr) * s.seg + (lane & (s.lpr - 1));
+  return ((threadIdx.x >> 5) * per + (s.lpr == 32 ? 0 : lane / s.lpr)) * s.seg +
+         (lane & (s.lpr - 1));
 }
 __device__ __forceinline__ int round_slots(const Shape& s) {
   return (blockDim.x >> 5) * (32 / s.lpr) * s.seg;
 }
 
-// Starts the copies of a task's vectors to this thread's slots.
+// Starts the copy of vector v of a task, at p.
 template <typename T, int VEC, bool EVEN>
-__device__ __forceinline__ void hold_task(const Shape& s, const UnitTask<VEC, EVEN>& k, const T* x,
-                                          uint4* slot, int plane) {
-  const T* p = x + k.off + (long long)k.v0 * VEC;
-  for (int v = k.v0; v < k.v1; v += s.lpr) {
-    const int bytes = k.hi(v) * (int)sizeof(T);
+__device__ __forceinline__ void hold(const UnitTask<VEC, EVEN>& k, int v, const T* p, uint4* slot,
+                                     int plane) {
+  const int bytes = k.hi(v) * (int)sizeof(T);
 #pragma unroll
-    for (int i = 0; i < kPieces<T, VEC>; ++i) {
-      // (a piece past the row's end is skipped; its slot is not used)
-      const int b = min(16, bytes - 16 * i);
-      if (EVEN || b > 0)
-        copy_async<16>(slot + i * plane, reinterpret_cast<const char*>(p) + 16 * i, EVEN ? 16 : b);
-    }
-    slot += s.lpr;
-    p += s.lpr * VEC;
+  for (int i = 0; i < kPieces<T, VEC>; ++i) {
+    // (a piece past the row's end is skipped; its slot is not used)
+    const int b = min(16, bytes - 16 * i);
+    if (EVEN || b > 0)
+      copy_async<16>(slot + i * plane, reinterpret_cast<const char*>(p) + 16 * i, EVEN ? 16 : b);
   }
 }
 
@@ -168,19 +164,18 @@ __device__ __forceinline__ float2 unit_stats(const Shape& s, const RowTeam& tm, 
                                              float (&sm)[3][256], float n, float mean, float m2) {
   float val[3];
   val[0] = warp_sum(n);
-  val[1] = warp_sum(n * mean) / fmaxf(val[0], 1.f);
+  val[1] = quotient(warp_sum(n * mean), fmaxf(val[0], 1.f), rcp_approx(fmaxf(val[0], 1.f)));
   val[2] = warp_sum(n > 0.f ? fmaf(n * (mean - val[1]), mean - val[1], m2) : 0.f);
   const float* sn = share<3>(tm, pl, sm, val);
   const int lane = threadIdx.x & 31;
   float sum = 0.f, q = 0.f;
   for (int i = lane; i < pl.team; i += 32) sum = fmaf(sn[i], sn[256 + i], sum);
-  const float total = (float)s.hw * (float)s.cpg;
-  const float mu = warp_sum(sum) / total;
+  const float mu = unit_mean(s, warp_sum(sum));
   for (int i = lane; i < pl.team; i += 32) {
     const float d = sn[256 + i] - mu;
     if (sn[i] > 0.f) q += fmaf(sn[i] * d, d, sn[512 + i]);
   }
-  return make_float2(mu, 1.f / sqrtf(warp_sum(q) / total + s.eps));
+  return make_float2(mu, rsqrtf(warp_sum(q) * s.inv_total + s.eps));
 }
 
 constexpr int kBatch = 4;
@@ -213,14 +208,16 @@ __device__ __forceinline__ void add_batch(int most, int cnt, float& n, float& me
   merge(n, mean, m2, (float)cnt, mb, q.x + q.y);
 }
 
-// The statistics of one task.
+// The statistics of one task (held: `open` groups of copies are under way).
 template <typename T, int VEC, bool EVEN, bool HELD>
 __device__ __forceinline__ void task_stats(const Shape& s, const UnitTask<VEC, EVEN>& k, const T* x,
-                                           const uint4* slot, float& n, float& mean, float& m2) {
+                                           const uint4* slot, int& open, float& n, float& mean,
+                                           float& m2) {
   const T* p = x + k.off + (long long)k.v0 * VEC;
   const int lpr = s.lpr;
   for (int v0 = k.v0; v0 < k.v1; v0 += kBatch * lpr) {
     const int most = (k.v1 - v0 + lpr - 1) / lpr;
+    if (HELD) copy_wait(--open);
     int cnt = 0;
 #pragma unroll
     for (int b = 0; b < kBatch; ++b)
@@ -277,7 +274,7 @@ __global__ void __launch_bounds__(kTeam, 2)
     fwd_nchw(Shape s, RowTeam tm, const T* x, const float* gamma, const float* beta, T* y,
              float* mean_out, float* rstd_out) {
   constexpr int VEC = VecOf<T>::n;
-  extern __shared__ __align__(128) uint4 hold[];
+  extern __shared__ __align__(128) uint4 slots[];
   __shared__ float sm[3][256];
   if (tm.blocks > 1) cluster_arrive();
   pdl_wait();
@@ -289,16 +286,27 @@ __global__ void __launch_bounds__(kTeam, 2)
   auto task = [&](int r) {
     return r == 0 ? first : Task(s, pl.unit, pl.ch0, pl.task(tm, r), tasks);
   };
-  uint4* mine = hold + first_slot(s);
-  for (int r = 0; r < tm.held; ++r)
-    hold_task<T, VEC, EVEN>(s, task(r), x, mine + r * pitch, 0);
+  uint4* mine = slots + first_slot(s);
+  int open = 0;  // groups of copies under way: of kBatch vectors, or the task's last
+  for (int r = 0; r < tm.held; ++r) {
+    const Task k = task(r);
+    const T* p = x + k.off + (long long)k.v0 * VEC;
+    uint4* slot = mine + r * pitch;
+    for (int v0 = k.v0; v0 < k.v1; v0 += kBatch * s.lpr, ++open) {
+      for (int v = v0; v < k.v1 && v < v0 + kBatch * s.lpr; v += s.lpr) {
+        hold<T, VEC, EVEN>(k, v, p, slot, 0);
+        slot += s.lpr;
+        p += s.lpr * VEC;
+      }
+      copy_group();
+    }
+  }
   // what is not held first: its loads go on behind the copies
   float n = 0.f, mean = 0.f, m2 = 0.f;
   for (int r = tm.rounds - 1; r >= tm.held; --r)
-    task_stats<T, VEC, EVEN, false>(s, task(r), x, mine, n, mean, m2);
-  copy_wait();
+    task_stats<T, VEC, EVEN, false>(s, task(r), x, mine, open, n, mean, m2);
   for (int r = 0; r < tm.held; ++r)
-    task_stats<T, VEC, EVEN, true>(s, task(r), x, mine + r * pitch, n, mean, m2);
+    task_stats<T, VEC, EVEN, true>(s, task(r), x, mine + r * pitch, open, n, mean, m2);
   const float2 st = unit_stats(s, tm, pl, sm, n, mean, m2);
   if (!pl.here) return;
   if (pl.rank == 0 && pl.w == 0 && (threadIdx.x & 31) == 0) {
@@ -323,7 +331,7 @@ __global__ void __launch_bounds__(kTeam, 2)
     fwd_flat(Shape s, RowTeam tm, const T* x, const float* gamma, const float* beta, T* y,
              float* mean_out, float* rstd_out) {
   constexpr int VEC = VecOf<T>::n;
-  extern __shared__ __align__(128) uint4 hold[];
+  extern __shared__ __align__(128) uint4 slots[];
   __shared__ float sm[3][256];
   if (tm.blocks > 1) cluster_arrive();
   pdl_wait();
@@ -338,11 +346,14 @@ __global__ void __launch_bounds__(kTeam, 2)
   const int mine_n = begin < end ? (end - begin + threads - 1) / threads : 0;  // vectors
   const int held = mine_n < tm.held ? mine_n : tm.held;
   const long long off = (long long)pl.unit * s.cpg * s.hw + (long long)begin * VEC;
-  uint4* mine = hold + threadIdx.x;
+  uint4* mine = slots + threadIdx.x;
   {
     const T* p = x + off;
     uint4* slot = mine;
-    for (int i = 0; i < held; ++i, p += step, slot += blockDim.x) copy_async<16>(slot, p);
+    for (int i = 0; i < held; ++i, p += step, slot += blockDim.x) {
+      copy_async<16>(slot, p);
+      if (i % kBatch == kBatch - 1 || i == held - 1) copy_group();
+    }
   }
   float n = 0.f, mean = 0.f, m2 = 0.f;
   auto keep = [](int, Pairs<VEC>&, float) {};
@@ -354,14 +365,18 @@ __global__ void __launch_bounds__(kTeam, 2)
         [&](int b, Pairs<VEC>& f) { load_vec<T, VEC>(x + off + (long long)(i + b) * step, f); },
         keep);
   }
-  copy_wait();
   {
     const uint4* slot = mine;
     auto get = [&](int b, Pairs<VEC>& f) { take<T, VEC>(slot + b * blockDim.x, 0, f); };
-    int i = 0;
-    for (; i + kBatch <= held; i += kBatch, slot += kBatch * blockDim.x)
+    int i = 0, open = (held + kBatch - 1) / kBatch;
+    for (; i + kBatch <= held; i += kBatch, slot += kBatch * blockDim.x) {
+      copy_wait(--open);
       add_batch<VEC, kBatch>(kBatch, kBatch * VEC, n, mean, m2, get, keep);
-    if (i < held) add_batch<VEC, kBatch>(held - i, (held - i) * VEC, n, mean, m2, get, keep);
+    }
+    if (i < held) {
+      copy_wait(0);
+      add_batch<VEC, kBatch>(held - i, (held - i) * VEC, n, mean, m2, get, keep);
+    }
   }
   const float2 st = unit_stats(s, tm, pl, sm, n, mean, m2);
   if (!pl.here) return;
@@ -400,18 +415,18 @@ __global__ void __launch_bounds__(kTeam, 2)
   }
 }
 
-// A task's sums of dz and dz * xh.  KEEP: dz takes grad_y's place in the slot
+// A task's sums of dz and dz * xh (held: `open` groups of copies are under
+// way).  KEEP: dz takes grad_y's place in the slot
 // (in float32), so that the results need the activation's slope no more.
 template <typename T, typename TG, int VEC, bool EVEN, bool HELD, bool KEEP, int ACT>
 __device__ __forceinline__ void task_sums(const Shape& s, const UnitTask<VEC, EVEN>& k, const T* x,
                                           const TG* gy, const uint4* slot, uint4* slot_g,
-                                          int plane, float mu, float rs, float g, float b,
-                                          float2& sa, float2& sb) {
+                                          int plane, int& open, float mu, float rs, float g,
+                                          float b, float2& sa, float2& sb) {
   const long long off = k.off + (long long)k.v0 * VEC;
   const T* p = x + off;
   const TG* pg = gy + off;
-#pragma unroll 2
-  for (int v = k.v0; v < k.v1; v += s.lpr) {
+  auto vector = [&](int v) {
     Pairs<VEC> f, d;  // (0 outside the row: dz is 0 there)
     fetch<T, VEC, EVEN, HELD>(k, v, p, slot, plane, f);
     fetch<TG, VEC, EVEN, HELD>(k, v, pg, slot_g, plane, d);
@@ -432,6 +447,11 @@ __device__ __forceinline__ void task_sums(const Shape& s, const UnitTask<VEC, EV
     slot_g += s.lpr;
     p += s.lpr * VEC;
     pg += s.lpr * VEC;
+  };
+  for (int v = k.v0; v < k.v1; v += 2 * s.lpr) {
+    if (HELD) copy_wait(--open);
+    vector(v);
+    if (v + s.lpr < k.v1) vector(v + s.lpr);
   }
 }
 
@@ -491,7 +511,7 @@ __global__ void __launch_bounds__(kTeam, 2)
   constexpr int VEC = VecOf<T>::n;
   constexpr bool KEEP = keep_dz(sizeof(TG) == 4, ACT);
   constexpr int kG = KEEP ? VEC / 4 : kPieces<TG, VEC>;  // pieces of a slot of grad_y
-  extern __shared__ __align__(128) uint4 hold[];
+  extern __shared__ __align__(128) uint4 slots[];
   __shared__ float sm[2][256];
   if (tm.blocks > 1) cluster_arrive();
   pdl_wait();
@@ -503,27 +523,45 @@ __global__ void __launch_bounds__(kTeam, 2)
   auto task = [&](int r) {
     return r == 0 ? first : Task(s, pl.unit, pl.ch0, pl.task(tm, r), tasks);
   };
-  uint4* mine = hold + first_slot(s);
+  uint4* mine = slots + first_slot(s);
   uint4* mine_g = mine + (size_t)tm.held * pitch;
+  int open = 0;  // groups of copies under way: of two vectors, or the task's last
   for (int r = 0; r < tm.held; ++r) {
     const Task k = task(r);
-    hold_task<T, VEC, EVEN>(s, k, x, mine + r * pitch, pitch);
-    hold_task<TG, VEC, EVEN>(s, k, gy, mine_g + r * pitch * kG, pitch);
+    const long long off = k.off + (long long)k.v0 * VEC;
+    const T* p = x + off;
+    const TG* pg = gy + off;
+    uint4* slot = mine + r * pitch;
+    uint4* slot_g = mine_g + r * pitch * kG;
+    for (int v0 = k.v0; v0 < k.v1; v0 += 2 * s.lpr, ++open) {
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        if (v0 + i * s.lpr >= k.v1) break;
+        hold<T, VEC, EVEN>(k, v0 + i * s.lpr, p, slot, pitch);
+        hold<TG, VEC, EVEN>(k, v0 + i * s.lpr, pg, slot_g, pitch);
+        slot += s.lpr;
+        slot_g += s.lpr;
+        p += s.lpr * VEC;
+        pg += s.lpr * VEC;
+      }
+      copy_group();
+    }
   }
   const float mu = pl.here ? mean[pl.unit] : 0.f, rs = pl.here ? rstd[pl.unit] : 0.f;
   float val[2] = {0.f, 0.f};
-  for (int r = tm.rounds - 1; r >= 0; --r) {
+  // (what is not held first: its loads go on behind the copies)
+  for (int q = 0; q < tm.rounds; ++q) {
+    const int r = q < tm.rounds - tm.held ? tm.held + q : q - (tm.rounds - tm.held);
     const Task k = task(r);
-    if (r == tm.held - 1) copy_wait();
     const float g = gamma ? gamma[k.ch] : 1.f, b = beta ? beta[k.ch] : 0.f;
     float2 sa = both(0.f), sb = both(0.f);
     if (r < tm.held)
       task_sums<T, TG, VEC, EVEN, true, KEEP, ACT>(s, k, x, gy, mine + r * pitch,
-                                                   mine_g + r * pitch * kG, pitch, mu, rs, g, b,
+                                                   mine_g + r * pitch * kG, pitch, open, mu, rs, g, b,
                                                    sa, sb);
     else
-      task_sums<T, TG, VEC, EVEN, false, KEEP, ACT>(s, k, x, gy, mine, mine_g, pitch, mu, rs, g,
-                                                    b, sa, sb);
+      task_sums<T, TG, VEC, EVEN, false, KEEP, ACT>(s, k, x, gy, mine, mine_g, pitch, open, mu, rs,
+                                                    g, b, sa, sb);
     const float ra = row_sum(sa.x + sa.y, s.lpr), rb = row_sum(sb.x + sb.y, s.lpr);
     if (k.live && (threadIdx.x & (s.lpr - 1)) == 0) {
       part[(long long)k.part * s.n * s.c + k.row] = make_float2(ra, rb);
@@ -539,8 +577,7 @@ __global__ void __launch_bounds__(kTeam, 2)
     ga += se[i];
     gb += se[256 + i];
   }
-  const float total = (float)s.hw * (float)s.cpg;
-  const float s1 = rs * (warp_sum(ga) / total), s2 = rs * (warp_sum(gb) / total);
+  const float s1 = rs * (warp_sum(ga) * s.inv_total), s2 = rs * (warp_sum(gb) * s.inv_total);
   if (!pl.here) return;
   for (int r = 0; r < tm.rounds; ++r) {
     const Task k = task(r);
@@ -593,10 +630,11 @@ __global__ void __launch_bounds__(kTwo)
       add_batch<VEC, kBatch>(kBatch, kBatch * VEC, n, mean, m2, get, keep);
     if (i < count) add_batch<VEC, kBatch>(count - i, (count - i) * VEC, n, mean, m2, get, keep);
   } else {
+    int none = 0;
     for (int r = 0; r < tm.rounds; ++r)
       task_stats<T, VEC, EVEN, false>(
-          s, UnitTask<VEC, EVEN>(s, pl.unit, pl.ch0, pl.task(tm, r), tm.tasks), x, nullptr, n,
-          mean, m2);
+          s, UnitTask<VEC, EVEN>(s, pl.unit, pl.ch0, pl.task(tm, r), tm.tasks), x, nullptr, none,
+          n, mean, m2);
   }
   const float wn = warp_sum(n), wm = warp_sum(n * mean) / fmaxf(wn, 1.f);
   const float wq = warp_sum(n > 0.f ? fmaf(n * (mean - wm), mean - wm, m2) : 0.f);
@@ -624,10 +662,9 @@ __global__ void __launch_bounds__(kTwo)
     const float4 v = mine[i];
     merge(n, mean, m2, v.x, v.y, v.z);
   }
-  const float total = (float)s.hw * (float)s.cpg;
-  const float mu = warp_sum(n * mean) / total;
-  const float var = warp_sum(n > 0.f ? fmaf(n * (mean - mu), mean - mu, m2) : 0.f) / total;
-  const float rs = 1.f / sqrtf(var + s.eps);
+  const float mu = unit_mean(s, warp_sum(n * mean));
+  const float var = warp_sum(n > 0.f ? fmaf(n * (mean - mu), mean - mu, m2) : 0.f) * s.inv_total;
+  const float rs = rsqrtf(var + s.eps);
   if (pl.rank == 0 && threadIdx.x == 0) {
     if (mean_out) mean_out[pl.unit] = mu;
     if (rstd_out) rstd_out[pl.unit] = rs;
@@ -682,12 +719,13 @@ __global__ void __launch_bounds__(kTwo)
   const Place pl = loose_place(s, tm, unit0);
   const float mu = mean[pl.unit], rs = rstd[pl.unit];
   float ga = 0.f, gb = 0.f;
+  int none = 0;
   for (int r = 0; r < tm.rounds; ++r) {
     const UnitTask<VEC, EVEN> k(s, pl.unit, pl.ch0, pl.task(tm, r), tm.tasks);
     const float g = gamma ? gamma[k.ch] : 1.f, b = beta ? beta[k.ch] : 0.f;
     float2 sa = both(0.f), sb = both(0.f);
-    task_sums<T, TG, VEC, EVEN, false, false, ACT>(s, k, x, gy, nullptr, nullptr, 0, mu, rs, g, b,
-                                                   sa, sb);
+    task_sums<T, TG, VEC, EVEN, false, false, ACT>(s, k, x, gy, nullptr, nullptr, 0, none, mu, rs,
+                                                   g, b, sa, sb);
     const float ra = row_sum(sa.x + sa.y, s.lpr), rb = row_sum(sb.x + sb.y, s.lpr);
     if (k.live && (threadIdx.x & (s.lpr - 1)) == 0) {
       part[(long long)k.part * s.n * s.c + k.row] = make_float2(ra, rb);
@@ -722,8 +760,7 @@ __global__ void __launch_bounds__(kTwo)
     ga += v.x;
     gb += v.y;
   }
-  const float total = (float)s.hw * (float)s.cpg;
-  const float s1 = rs * (warp_sum(ga) / total), s2 = rs * (warp_sum(gb) / total);
+  const float s1 = rs * (warp_sum(ga) * s.inv_total), s2 = rs * (warp_sum(gb) * s.inv_total);
   for (int r = 0; r < tm.rounds; ++r) {
     const UnitTask<VEC, EVEN> k(s, pl.unit, pl.ch0, pl.task(tm, r), tm.tasks);
     task_grads<T, TG, VEC, EVEN, false, false, ACT>(s, k, x, gy, gx, nullptr, nullptr, 0, mu, rs,

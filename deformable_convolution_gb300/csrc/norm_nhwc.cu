@@ -20,7 +20,7 @@ struct UnitCol {
     rank = cluster_rank();
     img = id / tm.slices;
     slice = id - img * tm.slices;
-    lane = threadIdx.x / tm.cb;
+    lane = quick_div(threadIdx.x, s.inv_cb);
     col = threadIdx.x - lane * tm.cb;
     live = lane < tm.rl;
     ch = slice * tm.width + col * V;
@@ -68,16 +68,13 @@ __device__ __forceinline__ void leave(char* slot, const Pairs<V>& f) {
   }
 }
 
-// Starts the copies of a thread's first `count` pixels to its slots.
+// Starts the copy of a vector to a slot.
 template <typename T, int V>
-__device__ __forceinline__ void hold_col(const T* p, long long step, int count, char* slot,
-                                         int stride) {
+__device__ __forceinline__ void hold(const T* p, char* slot) {
   constexpr int kBytes = V * sizeof(T);
   if constexpr (kBytes >= 4) {  // (an asynchronous copy moves 4 bytes at least)
-    for (int i = 0; i < count; ++i, p += step, slot += stride) {
-      copy_async<kUnit<T, V>>(slot, p);
-      if constexpr (kBytes > 16) copy_async<16>(slot + 16 * blockDim.x, p + V / 2);
-    }
+    copy_async<kUnit<T, V>>(slot, p);
+    if constexpr (kBytes > 16) copy_async<16>(slot + 16 * blockDim.x, p + V / 2);
   }
 }
 
@@ -221,7 +218,7 @@ __global__ void __launch_bounds__(kTeam, ONE || V < 8 ? 2 : 1)
     fwd_nhwc(Shape s, ColTeam tm, const T* x, const float* gamma, const float* beta, T* y,
              float* mean_out, float* rstd_out) {
   constexpr int P = Pairs<V>::n, EP = ONE ? 1 : P;
-  extern __shared__ __align__(128) uint4 hold[];
+  extern __shared__ __align__(128) uint4 slots[];
   __shared__ float2 ent[kTeam];
   __shared__ float cnts[kTeam];
   __shared__ float total_n;
@@ -232,15 +229,22 @@ __global__ void __launch_bounds__(kTeam, ONE || V < 8 ? 2 : 1)
   const UnitCol<V> k(s, tm);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, warps = blockDim.x >> 5;
   const int stride = kPieces<T, V> * kUnit<T, V> * blockDim.x;
-  char* mine = reinterpret_cast<char*>(hold) + threadIdx.x * kUnit<T, V>;
-  float* sn = reinterpret_cast<float*>(reinterpret_cast<char*>(hold) + (size_t)tm.held * stride);
+  char* mine = reinterpret_cast<char*>(slots) + threadIdx.x * kUnit<T, V>;
+  float* sn = reinterpret_cast<float*>(reinterpret_cast<char*>(slots) + (size_t)tm.held * stride);
   float* sm = sn + tm.blocks * tm.ng;
   float* sq = sm + tm.blocks * tm.ng;
   const int count = k.p1 > k.p0 ? (k.p1 - k.p0 + tm.rl - 1) / tm.rl : 0;  // this thread's pixels
   const int held = count < tm.held ? count : tm.held;
   const long long step = (long long)tm.rl * s.c;
   const T* px = x + k.base + (long long)k.p0 * s.c;
-  hold_col<T, V>(px, step, held, mine, stride);
+  {
+    const T* p = px;
+    char* slot = mine;
+    for (int i = 0; i < held; ++i, p += step, slot += stride) {
+      hold<T, V>(p, slot);
+      if (i % kBatch == kBatch - 1 || i == held - 1) copy_group();
+    }
+  }
   float n = 0.f;
   Pairs<2 * EP> mean, m2;  // ONE: the first of a pair alone
 #pragma unroll
@@ -249,14 +253,18 @@ __global__ void __launch_bounds__(kTeam, ONE || V < 8 ? 2 : 1)
   for (int i = held; i < count; i += kBatch)
     add_batch<V, ONE>(min(count - i, kBatch), n, mean, m2,
                       [&](int b, Pairs<V>& f) { load_vec<T, V>(px + (i + b) * step, f); });
-  copy_wait();
   {
     const char* slot = mine;
     auto get = [&](int b, Pairs<V>& f) { take<T, V>(slot + b * stride, f); };
-    int i = 0;
-    for (; i + kBatch <= held; i += kBatch, slot += kBatch * stride)
+    int i = 0, open = (held + kBatch - 1) / kBatch;
+    for (; i + kBatch <= held; i += kBatch, slot += kBatch * stride) {
+      copy_wait(--open);
       add_batch<V, ONE>(kBatch, n, mean, m2, get);
-    if (i < held) add_batch<V, ONE>(held - i, n, mean, m2, get);
+    }
+    if (i < held) {
+      copy_wait(0);
+      add_batch<V, ONE>(held - i, n, mean, m2, get);
+    }
   }
   // the block's groups, to every block of the cluster
   auto send = [&](int g, int lane_g, int lanes, float gn, float gm, float gq) {
@@ -318,13 +326,12 @@ __global__ void __launch_bounds__(kTeam, ONE || V < 8 ? 2 : 1)
   }
   // a group's blocks, a lane each
   for (int g = warp; g < tm.ng; g += warps) {
-    const float total = (float)s.hw * (float)s.cpg;
     const int at = lane * tm.ng + g;
     const bool in = lane < tm.blocks && sn[at] > 0.f;
-    const float mu = warp_sum(in ? sn[at] * sm[at] : 0.f) / total;
+    const float mu = unit_mean(s, warp_sum(in ? sn[at] * sm[at] : 0.f));
     const float d = in ? sm[at] - mu : 0.f;
-    const float var = warp_sum(in ? fmaf(sn[at] * d, d, sq[at]) : 0.f) / total;
-    const float rs = 1.f / sqrtf(var + s.eps);
+    const float var = warp_sum(in ? fmaf(sn[at] * d, d, sq[at]) : 0.f) * s.inv_total;
+    const float rs = rsqrtf(var + s.eps);
     if (lane == 0) {
       ent[g] = make_float2(mu, rs);
       if (k.rank == 0) {
@@ -341,7 +348,7 @@ __global__ void __launch_bounds__(kTeam, ONE || V < 8 ? 2 : 1)
   if (V == 1) a.p[0] = b.p[0] = mu.p[0] = both(0.f);
 #pragma unroll
   for (int e = 0; e < V; ++e) {
-    const float2 st = ent[(k.col * V + (ONE ? 0 : e)) / s.cpg];
+    const float2 st = ent[quick_div(k.col * V + (ONE ? 0 : e), s.inv_cpg)];
     mu[ONE ? 0 : e] = -st.x;
     a[e] = st.y * (gamma ? gamma[k.ch + e] : 1.f);
     b[e] = beta ? beta[k.ch + e] : 0.f;
@@ -380,7 +387,7 @@ __global__ void __launch_bounds__(kTeam, ONE || V < 8 ? 2 : 1)
   constexpr int P = Pairs<V>::n;
   constexpr bool KEEP = keep_dz(sizeof(TG) == 4, ACT);
   using SG = std::conditional_t<KEEP, float, TG>;  // what a slot of grad_y has room for
-  extern __shared__ __align__(128) uint4 hold[];
+  extern __shared__ __align__(128) uint4 slots[];
   __shared__ float2 ps[kTeam];
   const bool many = tm.blocks > 1;
   if (many) cluster_arrive();
@@ -389,8 +396,8 @@ __global__ void __launch_bounds__(kTeam, ONE || V < 8 ? 2 : 1)
   const UnitCol<V> k(s, tm);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, warps = blockDim.x >> 5;
   const int stride = V * sizeof(T) * blockDim.x, stride_g = V * sizeof(SG) * blockDim.x;
-  char* mine = reinterpret_cast<char*>(hold) + threadIdx.x * kUnit<T, V>;
-  char* held_g = reinterpret_cast<char*>(hold) + (size_t)tm.held * stride;
+  char* mine = reinterpret_cast<char*>(slots) + threadIdx.x * kUnit<T, V>;
+  char* held_g = reinterpret_cast<char*>(slots) + (size_t)tm.held * stride;
   char* mine_g = held_g + threadIdx.x * kUnit<SG, V>;
   float2* tab = reinterpret_cast<float2*>(held_g + (size_t)tm.held * stride_g);
   float* sa = reinterpret_cast<float*>(tab + tm.rows * tm.width);
@@ -398,8 +405,17 @@ __global__ void __launch_bounds__(kTeam, ONE || V < 8 ? 2 : 1)
   const int count = k.p1 > k.p0 ? (k.p1 - k.p0 + tm.rl - 1) / tm.rl : 0;
   const int held = count < tm.held ? count : tm.held;
   const long long step = (long long)tm.rl * s.c, off = k.base + (long long)k.p0 * s.c;
-  hold_col<T, V>(x + off, step, held, mine, stride);
-  hold_col<TG, V>(gy + off, step, held, mine_g, stride_g);
+  {
+    const T* p = x + off;
+    const TG* pg = gy + off;
+    char *slot = mine, *slot_g = mine_g;
+    for (int i = 0; i < held; ++i) {
+      hold<T, V>(p, slot);
+      hold<TG, V>(pg, slot_g);
+      if ((i & 1) || i == held - 1) copy_group();
+      p += step, pg += step, slot += stride, slot_g += stride_g;
+    }
+  }
   const long long g0 = (long long)k.img * s.groups + k.slice * tm.ng;
   Pairs<ONE ? 1 : V> mu, rs;  // minus the mean
   Pairs<V> g, b, s1, s2;
@@ -411,7 +427,7 @@ __global__ void __launch_bounds__(kTeam, ONE || V < 8 ? 2 : 1)
 #pragma unroll
     for (int e = 0; e < V; ++e) {
       if (!ONE || e == 0) {
-        const long long at = g0 + (k.col * V + e) / s.cpg;
+        const long long at = g0 + quick_div(k.col * V + e, s.inv_cpg);
         mu[ONE ? 0 : e] = -mean[at], rs[ONE ? 0 : e] = rstd[at];
       }
       g[e] = gamma ? gamma[k.ch + e] : 1.f;
@@ -444,17 +460,26 @@ __global__ void __launch_bounds__(kTeam, ONE || V < 8 ? 2 : 1)
     load_vec<TG, V>(gy + off + i * step, d);
     sums(f, d);
   }
-  copy_wait();
   {
     const char* slot = mine;
     char* slot_g = mine_g;
-#pragma unroll 2
-    for (int i = 0; i < held; ++i, slot += stride, slot_g += stride_g) {
+    auto pixel = [&] {
       Pairs<V> f, d;
       take<T, V>(slot, f);
       take<TG, V>(slot_g, d);
       sums(f, d);
       if (KEEP) leave<V>(slot_g, d);
+      slot += stride, slot_g += stride_g;
+    };
+    int open = (held + 1) / 2;
+    for (int i = 0; i + 2 <= held; i += 2) {
+      copy_wait(--open);
+      pixel();
+      pixel();
+    }
+    if (held & 1) {
+      copy_wait(0);
+      pixel();
     }
   }
   // the block's sum of each channel: pixel lanes of a warp first (where a warp
@@ -534,11 +559,10 @@ __global__ void __launch_bounds__(kTeam, ONE || V < 8 ? 2 : 1)
     __syncthreads();
   }
   for (int q = warp; q < tm.ng; q += warps) {  // a group's blocks, a lane each
-    const float total = (float)s.hw * (float)s.cpg;
     const bool in = lane < tm.blocks;
     const float a1 = warp_sum(in ? sa[lane * tm.ng + q] : 0.f);
     const float b1 = warp_sum(in ? sb[lane * tm.ng + q] : 0.f);
-    if (lane == 0) ps[q] = make_float2(a1 / total, b1 / total);
+    if (lane == 0) ps[q] = make_float2(a1 * s.inv_total, b1 * s.inv_total);
   }
   __syncthreads();
   if (!k.live) return;
@@ -547,7 +571,7 @@ __global__ void __launch_bounds__(kTeam, ONE || V < 8 ? 2 : 1)
   if (V == 1) k1.p[0] = k2.p[0] = both(0.f);
 #pragma unroll
   for (int e = 0; e < (ONE ? 1 : V); ++e) {
-    const float2 v = ps[(k.col * V + e) / s.cpg];
+    const float2 v = ps[quick_div(k.col * V + e, s.inv_cpg)];
     k1[e] = -rs[e] * v.x;
     k2[e] = -rs[e] * v.y;
   }
@@ -598,7 +622,7 @@ struct Loose {
     img = img0 + (int)i;
     c0 = slice * tm.width;
     cols = min(tm.cb, (s.c - c0) / V);
-    lane = threadIdx.x / tm.cb;
+    lane = quick_div(threadIdx.x, s.inv_cb);
     col = threadIdx.x - lane * tm.cb;
     live = lane < tm.rl && col < cols;
     ch = c0 + col * V;
@@ -703,7 +727,6 @@ __global__ void __launch_bounds__(kTwo)
   pdl_wait();
   pdl_release();
   const Loose<V> k(s, tm, img0);
-  const float total = (float)s.hw * (float)s.cpg;
   each_group(k.ng, 32, [&](int q, int lane, int lanes) {
     float n = 0.f, mean = 0.f, m2 = 0.f;
     const int g = k.g0 + q;
@@ -715,10 +738,11 @@ __global__ void __launch_bounds__(kTwo)
         merge(n, mean, m2, v.x, v.y, v.z);
       }
     }
-    const float mu = row_sum(n * mean, lanes) / total;
-    const float var = row_sum(n > 0.f ? fmaf(n * (mean - mu), mean - mu, m2) : 0.f, lanes) / total;
+    const float mu = unit_mean(s, row_sum(n * mean, lanes));
+    const float var =
+        row_sum(n > 0.f ? fmaf(n * (mean - mu), mean - mu, m2) : 0.f, lanes) * s.inv_total;
     if (q < k.ng && lane == 0) {
-      const float rs = 1.f / sqrtf(var + s.eps);
+      const float rs = rsqrtf(var + s.eps);
       ent[q] = make_float2(mu, rs);
       if (k.rank == 0 && g * s.cpg / tm.width == k.slice) {
         const long long to = (long long)k.img * s.groups + g;
@@ -734,7 +758,7 @@ __global__ void __launch_bounds__(kTwo)
   if (V == 1) a.p[0] = b.p[0] = mu.p[0] = both(0.f);
 #pragma unroll
   for (int e = 0; e < V; ++e) {
-    const float2 st = ent[(k.ch + (ONE ? 0 : e)) / s.cpg - k.g0];
+    const float2 st = ent[quick_div(k.ch + (ONE ? 0 : e), s.inv_cpg) - k.g0];
     mu[ONE ? 0 : e] = -st.x;
     a[e] = st.y * (gamma ? gamma[k.ch + e] : 1.f);
     b[e] = beta ? beta[k.ch + e] : 0.f;
@@ -787,7 +811,7 @@ __global__ void __launch_bounds__(kTwo)
 #pragma unroll
     for (int e = 0; e < V; ++e) {
       if (!ONE || e == 0) {
-        const long long at = (long long)k.img * s.groups + (k.ch + e) / s.cpg;
+        const long long at = (long long)k.img * s.groups + quick_div(k.ch + e, s.inv_cpg);
         mu[ONE ? 0 : e] = -mean[at], rs[ONE ? 0 : e] = rstd[at];
       }
       g[e] = gamma ? gamma[k.ch + e] : 1.f;
@@ -869,7 +893,6 @@ __global__ void __launch_bounds__(kTwo)
   pdl_wait();
   pdl_release();
   const Loose<V> k(s, tm, img0);
-  const float total = (float)s.hw * (float)s.cpg;
   each_group(k.ng, 32, [&](int q, int lane, int lanes) {
     float a1 = 0.f, b1 = 0.f;
     const int g = k.g0 + q;
@@ -884,7 +907,7 @@ __global__ void __launch_bounds__(kTwo)
     }
     a1 = row_sum(a1, lanes);
     b1 = row_sum(b1, lanes);
-    if (q < k.ng && lane == 0) ent[q] = make_float2(a1 / total, b1 / total);
+    if (q < k.ng && lane == 0) ent[q] = make_float2(a1 * s.inv_total, b1 * s.inv_total);
   });
   __syncthreads();
   if (!k.live) return;
@@ -898,7 +921,7 @@ __global__ void __launch_bounds__(kTwo)
 #pragma unroll
   for (int e = 0; e < V; ++e) {
     if (!ONE || e == 0) {
-      const int gr = (k.ch + e) / s.cpg;
+      const int gr = quick_div(k.ch + e, s.inv_cpg);
       const long long at = (long long)k.img * s.groups + gr;
       const float2 v = ent[gr - k.g0];
       mu[ONE ? 0 : e] = -mean[at], rs[ONE ? 0 : e] = rstd[at];

@@ -432,6 +432,32 @@ __device__ __forceinline__ void copy_wait(int open) {
   }
 }
 
+// A thread's stream of `count` items through slots of its own: start(i, slot)
+// starts the copies of item i, work(i, most, slot) works on items [i, i + most)
+// in the slots from `slot` on.  kRing batches of B items: two arrive while one
+// is worked on, and the copies go to the batch whose work is done.
+constexpr int kRing = 3;
+template <int B, typename START, typename WORK>
+__device__ __forceinline__ void through_ring(int count, START&& start, WORK&& work) {
+  int next = 0, put = 0, at = 0;
+  auto batch = [&] {
+#pragma unroll
+    for (int b = 0; b < B; ++b)
+      if (next + b < count) start(next + b, put + b);
+    copy_group();
+    next += B;
+    put = put == (kRing - 1) * B ? 0 : put + B;
+  };
+#pragma unroll
+  for (int r = 0; r < kRing - 1; ++r) batch();
+  for (int i = 0; i < count; i += B) {
+    batch();
+    asm volatile("cp.async.wait_group %0;" ::"n"(kRing - 1) : "memory");
+    work(i, min(count - i, B), at);
+    at = at == (kRing - 1) * B ? 0 : at + B;
+  }
+}
+
 template <typename K, typename... A>
 cudaError_t launch_team(K kern, const NormPlan& p, int cluster, cudaStream_t s, A... args) {
   cudaError_t e = cudaSuccess;
@@ -463,6 +489,11 @@ template <typename K, typename... A>
 cudaError_t launch_smem(K kern, unsigned blocks, int threads, size_t smem, cudaStream_t s,
                         A... args) {
   cudaLaunchConfig_t cfg = {};
+  if (smem > 40 * 1024) {
+    const cudaError_t e =
+        cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    if (e != cudaSuccess) return e;
+  }
   cfg.gridDim = dim3(blocks);
   cfg.blockDim = dim3((unsigned)threads);
   cfg.dynamicSmemBytes = smem;

@@ -147,8 +147,10 @@ bool plan_cols(const NormArgs& a, bool backward, bool keep, NormPlan* p) {
   const int slices_most = (int)(a.c / base);
   const int held_bytes = v * (elt + (backward ? (keep ? 4 : 2) : 0));  // of a pixel's column
   // the narrowest slice of 128 bytes a pixel, or of 64 where that leaves few
-  // blocks or does not fit in a cluster, or of 32 where that does not fit
-  for (int bytes = 128; bytes >= 32; bytes /= 2) {
+  // blocks or does not fit in a cluster (32 bytes, one sector of a line, took
+  // 32 us on the forward of 2 x 150 x 250 x 256 where two launches take 28, and
+  // 170 on the backward of 16 x 112 x 112 x 256 where they take 114)
+  for (int bytes = 128; bytes >= 64; bytes /= 2) {
     int m = 1;
     while (m < slices_most && (m * base * elt < bytes || slices_most % m)) ++m;
     while (m > 1 && (m * base / v > 256 || m * base / a.cpg > kMaxGroups || slices_most % m)) --m;
@@ -181,15 +183,25 @@ bool plan_cols(const NormArgs& a, bool backward, bool keep, NormPlan* p) {
     p->smem += stats_table(c, p->threads);
   p->blocks = (unsigned)(units * c.blocks);
   p->parts = c.blocks;
-  return true;
+  // A backward block reads nothing while it works on what it holds, so where
+  // the blocks are more than run at once, of units that take three blocks or
+  // more, two launches are faster: us of a bf16 SiLU backward on h x w x 256,
+  // clusters / two launches: 4 x 56 x 56 (224 blocks) 12 / 18.5, 8 x 56 x 56
+  // (448) 24 / 24, 16 x 56 x 56 (896) 46 / 31, 64 x 28 x 28 39 / 33, but with
+  // units of one block, 512 x 14 x 14, 59 / 76.  Not so of float32 (16 x 56 x 56
+  // 46 / 50), nor of ReLU's float32 gradients (64 x 28 x 28 41 / 56).
+  const bool two_byte =
+      elt == 2 && (a.gdt != DC_F32 || a.act == DC_ACT_SILU || a.act == DC_ACT_GELU);
+  return !(backward && two_byte && c.blocks > 2 && p->blocks > 3 * kSms);
 }
 
-constexpr double kImagesBytes = 64e6;   // of a pass's inputs, left in L2 between two launches
-constexpr int kTwoBlocks = 4 * kSms;    // blocks of a launch, where that leaves each enough
+constexpr double kImagesBytes = 96e6;   // of a pass's inputs, left in L2 between two launches
 
-// Two launches: blocks of a unit, `vectors` of it in all.
-int loose_blocks(long long units, double vectors) {
-  long long k = ceil_div_ll(kTwoBlocks, units);
+// Two launches: blocks of a unit, `vectors` of it in all, as many as an SM runs
+// at once (`per_sm`: a third more of them wait for a whole turn; 61 us became
+// 80 on the forward of 2 x 200 x 336 x 256).
+int loose_blocks(long long units, double vectors, int per_sm) {
+  long long k = per_sm * kSms / units;
   const long long most = (long long)(vectors / (8 * kTwo));
   if (k > most) k = most;
   return (int)(k < 1 ? 1 : k);
@@ -208,7 +220,7 @@ void plan_two(const NormArgs& a, bool backward, int planes, NormPlan* p) {
     RowTeam& r = p->row;
     const int vr = row_vectors(a.hw, a.hw % vec ? vec - 1 : 0, vec);
     const long long units = (long long)p->images * a.groups, run = (long long)a.cpg * vr;
-    r.blocks = loose_blocks(units, (double)run);
+    r.blocks = loose_blocks(units, (double)run, 4);
     if (ceil_div_ll(run, r.blocks) > 1 << 30) r.blocks = (int)ceil_div_ll(run, 1 << 30);
     r.units = 1;
     r.warps = kTwo / 32;
@@ -230,14 +242,17 @@ void plan_two(const NormArgs& a, bool backward, int planes, NormPlan* p) {
   c.slices = (int)ceil_div_ll(cols, c.cb);
   c.width = c.cb * s.v;
   c.rl = kTwo / c.cb;
-  c.blocks = loose_blocks((long long)p->images * c.slices, (double)a.hw * c.cb);
+  c.blocks = loose_blocks((long long)p->images * c.slices, (double)a.hw * c.cb, 3);
   c.span = (int)ceil_div_ll(a.hw, c.blocks);
   c.shares = c.slices == 1 ? 1 : (a.cpg + c.width - 2) / c.width + 1;
   c.rows = 32 % c.cb ? c.rl : kTwo / 32;
-  if (backward)
-    p->smem = (size_t)c.rows * c.width * sizeof(float2);
-  else if (a.cpg % s.v)
-    p->smem = stats_table(c, kTwo);
+  // the ring's slots, and in their place after them the tables
+  const size_t gelt = a.gdt == DC_F32 ? 4 : 2;
+  const size_t ring = backward ? (size_t)kRing * 2 * s.v * (elt + gelt) * kTwo
+                               : (size_t)kRing * 4 * s.v * elt * kTwo;
+  const size_t table = backward ? (size_t)c.rows * c.width * sizeof(float2)
+                                : a.cpg % s.v ? stats_table(c, kTwo) : 0;
+  p->smem = ring > table ? ring : table;
   p->parts = c.blocks;
 }
 

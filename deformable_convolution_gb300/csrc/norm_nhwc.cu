@@ -607,6 +607,10 @@ __global__ void __launch_bounds__(kTeam, ONE || V < 8 ? 2 : 1)
 
 // ---------------------------------------------------------------- two launches
 
+// Whether a vector can be copied asynchronously (4 bytes at least).
+template <typename T, int V>
+constexpr bool kStreams = V * sizeof(T) >= 4;
+
 // A block's slice of channels and share of pixels; neighbouring blocks take
 // neighbouring slices of the same pixels.
 template <int V>
@@ -647,7 +651,9 @@ template <typename T, int V, bool ONE>
 __global__ void __launch_bounds__(kTwo)
     stats_nhwc(Shape s, ColTeam tm, int img0, const T* x, float4* entry) {
   constexpr int P = Pairs<V>::n, EP = ONE ? 1 : P;
-  extern __shared__ float2 tab[];  // (not ONE) of channel_stats, and its partial triples
+  // the ring's slots; then (not ONE) the table of channel_stats and its partial triples
+  extern __shared__ __align__(128) uint4 slots[];
+  float2* tab = reinterpret_cast<float2*>(slots);
   __shared__ float2 ent[kTwo];
   __shared__ float cnts[kTwo];
   __shared__ float total_n;
@@ -661,11 +667,29 @@ __global__ void __launch_bounds__(kTwo)
   Pairs<2 * EP> mean, m2;
 #pragma unroll
   for (int e = 0; e < EP; ++e) mean.p[e] = m2.p[e] = both(0.f);
-  auto get = [&](int b, Pairs<V>& f) { load_vec<T, V>(px + b * step, f); };
-  int i = 0;
-  for (; i + kBatch <= k.count; i += kBatch, px += kBatch * step)
-    add_batch<V, ONE>(kBatch, n, mean, m2, get);
-  if (i < k.count) add_batch<V, ONE>(k.count - i, n, mean, m2, get);
+  if constexpr (kStreams<T, V>) {
+    char* mine = reinterpret_cast<char*>(slots) + threadIdx.x * kUnit<T, V>;
+    constexpr int stride = V * sizeof(T) * kTwo;
+    through_ring<kBatch>(
+        k.count,
+        [&](int, int slot) {
+          hold<T, V>(px, mine + slot * stride);
+          px += step;
+        },
+        [&](int, int most, int slot) {
+          const char* from = mine + slot * stride;
+          auto get = [&](int b, Pairs<V>& f) { take<T, V>(from + b * stride, f); };
+          if (most == kBatch)
+            add_batch<V, ONE>(kBatch, n, mean, m2, get);
+          else
+            add_batch<V, ONE>(most, n, mean, m2, get);
+        });
+    __syncthreads();  // (the table takes the slots' place)
+  } else {
+    auto get = [&](int b, Pairs<V>& f) { load_vec<T, V>(px + b * step, f); };
+    for (int i = 0; i < k.count; i += kBatch, px += kBatch * step)
+      add_batch<V, ONE>(min(k.count - i, kBatch), n, mean, m2, get);
+  }
   if constexpr (ONE) {
     ent[threadIdx.x] = make_float2(mean.p[0].x, m2.p[0].x);
     cnts[threadIdx.x] = n;
@@ -723,6 +747,7 @@ __global__ void __launch_bounds__(kTwo)
     apply_nhwc(Shape s, ColTeam tm, int img0, const T* x, const float* gamma, const float* beta,
                const float4* entry, T* y, float* mean_out, float* rstd_out) {
   constexpr int P = Pairs<V>::n;
+  extern __shared__ __align__(128) uint4 slots[];
   __shared__ float2 ent[kTwo];
   pdl_wait();
   pdl_release();
@@ -766,11 +791,12 @@ __global__ void __launch_bounds__(kTwo)
   const long long step = (long long)tm.rl * s.c;
   const T* px = x + k.base + (long long)k.p0 * s.c;
   T* to = y + k.base + (long long)k.p0 * s.c;
-  auto pixels = [&](int most) {  // (loads ahead of the stores, which may be in place)
+  // (an item's copy is done before its store, which may be in place)
+  auto pixels = [&](int most, auto&& get) {
     Pairs<V> f[kBatch];
 #pragma unroll
     for (int i = 0; i < kBatch; ++i)
-      if (i < most) load_vec<T, V>(px + i * step, f[i]);
+      if (i < most) get(i, f[i]);
 #pragma unroll
     for (int i = 0; i < kBatch; ++i) {
       if (i >= most) break;
@@ -780,23 +806,38 @@ __global__ void __launch_bounds__(kTwo)
                                        a.p[e], b.p[e]), s.floor);
       store_vec<T, V>(to + i * step, f[i]);
     }
-    px += kBatch * step;
     to += kBatch * step;
   };
-  int i = 0;
-  for (; i + kBatch <= k.count; i += kBatch) pixels(kBatch);
-  if (i < k.count) pixels(k.count - i);
+  if constexpr (kStreams<T, V>) {
+    char* mine = reinterpret_cast<char*>(slots) + threadIdx.x * kUnit<T, V>;
+    constexpr int stride = V * sizeof(T) * kTwo;
+    through_ring<kBatch>(
+        k.count,
+        [&](int, int slot) {
+          hold<T, V>(px, mine + slot * stride);
+          px += step;
+        },
+        [&](int, int most, int slot) {
+          const char* from = mine + slot * stride;
+          pixels(most, [&](int i, Pairs<V>& f) { take<T, V>(from + i * stride, f); });
+        });
+  } else {
+    for (int i = 0; i < k.count; i += kBatch, px += kBatch * step)
+      pixels(min(k.count - i, kBatch),
+             [&](int j, Pairs<V>& f) { load_vec<T, V>(px + j * step, f); });
+  }
 }
 
 // part[rank][image * c + channel] as above; entry = a block's sums of gamma dz
-// and gamma dz xh over a group's share.  Dynamic shared memory: the table.
+// and gamma dz xh over a group's share.
 template <typename T, typename TG, int V, bool ONE, int ACT>
 __global__ void __launch_bounds__(kTwo)
     sums_nhwc(Shape s, ColTeam tm, int img0, const T* x, const TG* gy, const float* gamma,
               const float* beta, const float* mean, const float* rstd, float2* part,
               float2* entry) {
   constexpr int P = Pairs<V>::n;
-  extern __shared__ float2 tab[];
+  extern __shared__ __align__(128) uint4 slots[];  // the ring's; then the table
+  float2* tab = reinterpret_cast<float2*>(slots);
   pdl_wait();
   pdl_release();
   const Loose<V> k(s, tm, img0);
@@ -821,11 +862,7 @@ __global__ void __launch_bounds__(kTwo)
   const long long step = (long long)tm.rl * s.c, off = k.base + (long long)k.p0 * s.c;
   const T* px = x + off;
   const TG* pg = gy + off;
-#pragma unroll 2
-  for (int i = 0; i < k.count; ++i) {
-    Pairs<V> f, d;
-    load_vec<T, V>(px, f);
-    load_vec<TG, V>(pg, d);
+  auto pixel = [&](const Pairs<V>& f, const Pairs<V>& d) {
 #pragma unroll
     for (int e = 0; e < P; ++e) {
       const float2 xh = mul2(add2(f.p[e], ONE ? both(mu[0]) : mu.p[ONE ? 0 : e]),
@@ -835,8 +872,38 @@ __global__ void __launch_bounds__(kTwo)
       s1.p[e] = add2(s1.p[e], dz);
       s2.p[e] = fma2(dz, xh, s2.p[e]);
     }
-    px += step;
-    pg += step;
+  };
+  if constexpr (kStreams<T, V> && kStreams<TG, V>) {
+    char* mine = reinterpret_cast<char*>(slots) + threadIdx.x * kUnit<T, V>;
+    char* mine_g = reinterpret_cast<char*>(slots) + kRing * 2 * V * sizeof(T) * kTwo +
+                   threadIdx.x * kUnit<TG, V>;
+    constexpr int stride = V * sizeof(T) * kTwo, stride_g = V * sizeof(TG) * kTwo;
+    through_ring<2>(
+        k.count,
+        [&](int, int slot) {
+          hold<T, V>(px, mine + slot * stride);
+          hold<TG, V>(pg, mine_g + slot * stride_g);
+          px += step;
+          pg += step;
+        },
+        [&](int, int most, int slot) {
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            if (i >= most) break;
+            Pairs<V> f, d;
+            take<T, V>(mine + (slot + i) * stride, f);
+            take<TG, V>(mine_g + (slot + i) * stride_g, d);
+            pixel(f, d);
+          }
+        });
+    __syncthreads();  // (the table takes the slots' place)
+  } else {
+    for (int i = 0; i < k.count; ++i, px += step, pg += step) {
+      Pairs<V> f, d;
+      load_vec<T, V>(px, f);
+      load_vec<TG, V>(pg, d);
+      pixel(f, d);
+    }
   }
   int row = k.lane;
   bool put = k.live;
@@ -883,12 +950,16 @@ __global__ void __launch_bounds__(kTwo)
   }
 }
 
+// Three blocks to an SM, as the grid is made for, are 80 registers a thread;
+// the other activations' float32 gradients would spill there and have no bound,
+// which is 0 (2 x 200 x 336 x 256: ReLU 144 -> 123 us, but SiLU 128 -> 147).
 template <typename T, typename TG, int V, bool ONE, int ACT>
-__global__ void __launch_bounds__(kTwo)
+__global__ void __launch_bounds__(kTwo, ONE && (ACT == 0 || sizeof(TG) == 2) ? 3 : 0)
     grads_nhwc(Shape s, ColTeam tm, int img0, const T* x, const TG* gy, const float* gamma,
                const float* beta, const float* mean, const float* rstd, const float2* entry,
                T* gx) {
   constexpr int P = Pairs<V>::n;
+  extern __shared__ __align__(128) uint4 slots[];
   __shared__ float2 ent[kTwo];
   pdl_wait();
   pdl_release();
@@ -934,18 +1005,16 @@ __global__ void __launch_bounds__(kTwo)
   const T* px = x + off;
   const TG* pg = gy + off;
   T* to = gx + off;
-  constexpr int B = 2;  // (loads ahead of the stores, which may be in place)
-  for (int i0 = 0; i0 < k.count; i0 += B) {
+  constexpr int B = 2;
+  // (an item's copies are done before its store, which may be in place)
+  auto pixels = [&](int most, auto&& get) {
     Pairs<V> f[B], d[B];
 #pragma unroll
-    for (int i = 0; i < B; ++i) {
-      if (i0 + i >= k.count) break;
-      load_vec<T, V>(px + i * step, f[i]);
-      load_vec<TG, V>(pg + i * step, d[i]);
-    }
+    for (int i = 0; i < B; ++i)
+      if (i < most) get(i, f[i], d[i]);
 #pragma unroll
     for (int i = 0; i < B; ++i) {
-      if (i0 + i >= k.count) break;
+      if (i >= most) break;
 #pragma unroll
       for (int e = 0; e < P; ++e) {
         const float2 r = ONE ? both(rs[0]) : rs.p[ONE ? 0 : e];
@@ -956,9 +1025,33 @@ __global__ void __launch_bounds__(kTwo)
       }
       store_vec<T, V>(to + i * step, f[i]);
     }
-    px += B * step;
-    pg += B * step;
     to += B * step;
+  };
+  if constexpr (kStreams<T, V> && kStreams<TG, V>) {
+    char* mine = reinterpret_cast<char*>(slots) + threadIdx.x * kUnit<T, V>;
+    char* mine_g = reinterpret_cast<char*>(slots) + kRing * 2 * V * sizeof(T) * kTwo +
+                   threadIdx.x * kUnit<TG, V>;
+    constexpr int stride = V * sizeof(T) * kTwo, stride_g = V * sizeof(TG) * kTwo;
+    through_ring<B>(
+        k.count,
+        [&](int, int slot) {
+          hold<T, V>(px, mine + slot * stride);
+          hold<TG, V>(pg, mine_g + slot * stride_g);
+          px += step;
+          pg += step;
+        },
+        [&](int, int most, int slot) {
+          pixels(most, [&](int i, Pairs<V>& f, Pairs<V>& d) {
+            take<T, V>(mine + (slot + i) * stride, f);
+            take<TG, V>(mine_g + (slot + i) * stride_g, d);
+          });
+        });
+  } else {
+    for (int i = 0; i < k.count; i += B, px += B * step, pg += B * step)
+      pixels(min(k.count - i, B), [&](int j, Pairs<V>& f, Pairs<V>& d) {
+        load_vec<T, V>(px + j * step, f);
+        load_vec<TG, V>(pg + j * step, d);
+      });
   }
 }
 
@@ -1017,8 +1110,8 @@ cudaError_t launch_two_nhwc(const NormPlan& p, const NormArgs& a, bool backward,
           if (!second)
             return launch_smem(stats_nhwc<T, V, ONE>, grid, kTwo, p.smem, st, p.s, p.col, img0, x, e);
           return by_act(a.act, [&](auto act) {
-            return launch_plain(apply_nhwc<T, V, ONE, decltype(act)::value>, grid, kTwo, st, p.s,
-                                p.col, img0, x, a.gamma, a.beta, static_cast<const float4*>(e),
+            return launch_smem(apply_nhwc<T, V, ONE, decltype(act)::value>, grid, kTwo, p.smem, st,
+                               p.s, p.col, img0, x, a.gamma, a.beta, static_cast<const float4*>(e),
                                 static_cast<T*>(a.y), a.mean, a.rstd);
           });
         };
@@ -1042,8 +1135,8 @@ cudaError_t launch_two_nhwc(const NormPlan& p, const NormArgs& a, bool backward,
             return launch_smem(sums_nhwc<T, TG, V, ONE, ACT>, grid, kTwo, p.smem, st, p.s, p.col, img0,
                                x, gy, a.gamma, a.beta, mean, rstd,
                                reinterpret_cast<float2*>(a.ws), e);
-          return launch_plain(grads_nhwc<T, TG, V, ONE, ACT>, grid, kTwo, st, p.s, p.col, img0, x,
-                              gy, a.gamma, a.beta, mean, rstd, static_cast<const float2*>(e),
+          return launch_smem(grads_nhwc<T, TG, V, ONE, ACT>, grid, kTwo, p.smem, st, p.s, p.col, img0,
+                             x, gy, a.gamma, a.beta, mean, rstd, static_cast<const float2*>(e),
                               static_cast<T*>(a.gx));
         };
         return p.s.cpg % V ? by_one(Int<0>{}) : by_one(Int<1>{});

@@ -403,10 +403,15 @@ __device__ __forceinline__ void store_cluster(float* p, int rank, float v) {
 
 // Asynchronous copy of BYTES (4, 8 or 16) to shared memory; of 16, only the
 // first `bytes` are read and the rest becomes zero.
-template <int BYTES>
+// TWICE: the other half of a 32-byte sector is copied too, so the sector stays
+// in L1 (past it, the sector comes from L2 for each half).
+template <int BYTES, bool TWICE = false>
 __device__ __forceinline__ void copy_async(void* to, const void* from, int bytes = BYTES) {
   const uint32_t dst = (uint32_t)__cvta_generic_to_shared(to);
-  if (BYTES == 16)
+  if (BYTES == 16 && TWICE)
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(from), "r"(bytes)
+                 : "memory");
+  else if (BYTES == 16)
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(from), "r"(bytes)
                  : "memory");
   else

@@ -39,8 +39,15 @@ __global__ void __launch_bounds__(1024)
 
 // ---------------------------------------------------------------- the plan
 
+// A call is one launch of clusters that hold their units on the chip, or, for
+// units over kMaxCluster * kBlockBytes (and where plan_cols says so), two
+// launches that read their inputs twice.  us of clusters / two launches:
+// forward 32 x 256 x 56 x 56 bf16 ReLU 24.0 / 27.5, 16 x 100 x 168 x 256 SiLU
+// 69 / 75, backward 8 x 256 x 56 x 56 with a float32 gradient 22.1 / 23.5.
 constexpr int kSms = 152;
-constexpr int kBlockBytes = 92 * 1024;  // most of a unit in a cluster's block: two blocks to an SM
+// Most of a unit in a cluster's block: two blocks to an SM (50 KB, four to an
+// SM: 20.3 instead of 18.4 us on that backward).
+constexpr int kBlockBytes = 92 * 1024;
 constexpr int kLeastBytes = 16 * 1024;  // not split further to make more blocks
 
 int gcd(int a, int b) { return b ? gcd(b, a % b) : a; }
@@ -131,7 +138,15 @@ bool plan_rows(const NormArgs& a, bool backward, int planes, NormPlan* p) {
     p->parts = s.parts;
   }
   p->blocks = (unsigned)(ceil_div_ll(groups, r.units) * r.blocks);
-  return true;
+  // As in plan_cols, but with less to gain: us of a bf16 SiLU backward on
+  // h x w x 256, clusters / two launches: 8 x 56 x 56 (512 blocks) 20 / 21,
+  // 16 x 56 x 56 (1024) 37 / 27, 4 x 112 x 112 41 / 27, 16 x 112 x 112
+  // 135 / 127; but with units of one block (64 x 28 x 28) 28 / 34, with rows of
+  // a vector a lane (64 x 14 x 14 x 1024 in 8 groups) 70 / 78, and for
+  // 16 x 112 x 112 under ReLU 93 / 104, GELU 140 / 165 (its slope is worked out
+  // twice), with float32 gradients 160 / 191.
+  return !(backward && a.dt == DC_BF16 && a.gdt == DC_BF16 && a.act == DC_ACT_SILU &&
+           r.blocks > 1 && vr >= 256 && p->blocks > 4 * kSms);
 }
 
 // The forward's table of channel statistics and its partial triples.
@@ -188,18 +203,24 @@ bool plan_cols(const NormArgs& a, bool backward, bool keep, NormPlan* p) {
   // more, two launches are faster: us of a bf16 SiLU backward on h x w x 256,
   // clusters / two launches: 4 x 56 x 56 (224 blocks) 12 / 18.5, 8 x 56 x 56
   // (448) 24 / 24, 16 x 56 x 56 (896) 46 / 31, 64 x 28 x 28 39 / 33, but with
-  // units of one block, 512 x 14 x 14, 59 / 76.  Not so of float32 (16 x 56 x 56
-  // 46 / 50), nor of ReLU's float32 gradients (64 x 28 x 28 41 / 56).
-  const bool two_byte =
-      elt == 2 && (a.gdt != DC_F32 || a.act == DC_ACT_SILU || a.act == DC_ACT_GELU);
-  return !(backward && two_byte && c.blocks > 2 && p->blocks > 3 * kSms);
+  // units of one block, 512 x 14 x 14, 59 / 76, and of float32 tensors 46 / 50
+  // on 16 x 56 x 56.  Float32 gradients of bf16 tensors gain where units are
+  // large (SiLU and GELU; 16 x 56 x 56 57 / 48 and 58 / 53, but 64 x 28 x 28
+  // 46 / 51 and 49 / 56) and a vector's channels are one group's (10 channels a
+  // group of 320: 70 / 94).
+  const bool slope = a.act == DC_ACT_SILU || a.act == DC_ACT_GELU;
+  const bool gains = a.gdt == DC_BF16 ? c.blocks > 2 : slope && c.blocks > 4 && a.cpg % v == 0;
+  return !(backward && a.dt == DC_BF16 && gains && p->blocks > 3 * kSms);
 }
 
-constexpr double kImagesBytes = 96e6;   // of a pass's inputs, left in L2 between two launches
+// Of a pass's inputs, left in L2 (129 MB) between two launches: 64 MB, which
+// makes a turn of every image, took 61 us where 96 MB take 43 (forward on
+// 2 x 200 x 336 x 256 bf16).
+constexpr double kImagesBytes = 96e6;
 
 // Two launches: blocks of a unit, `vectors` of it in all, as many as an SM runs
-// at once (`per_sm`: a third more of them wait for a whole turn; 61 us became
-// 80 on the forward of 2 x 200 x 336 x 256).
+// at once (`per_sm`; a third more of them wait for a whole turn, 43 us become
+// 51 on the forward of 2 x 200 x 336 x 256).
 int loose_blocks(long long units, double vectors, int per_sm) {
   long long k = per_sm * kSms / units;
   const long long most = (long long)(vectors / (8 * kTwo));
@@ -210,7 +231,8 @@ int loose_blocks(long long units, double vectors, int per_sm) {
 void plan_two(const NormArgs& a, bool backward, int planes, NormPlan* p) {
   Shape& s = p->s;
   const int vec = a.dt == DC_BF16 ? 8 : 4, elt = a.dt == DC_BF16 ? 2 : 4;
-  const double image = (double)a.c * a.hw * (elt + (backward ? (a.gdt == DC_F32 ? 4 : 2) : 0));
+  const int gelt = a.gdt == DC_F32 ? 4 : 2;
+  const double image = (double)a.c * a.hw * (elt + (backward ? gelt : 0));
   const double images = kImagesBytes / image;
   p->images = images < 1 ? 1 : images >= a.n ? a.n : (int)images;
   // as many at a time in every turn
@@ -233,6 +255,8 @@ void plan_two(const NormArgs& a, bool backward, int planes, NormPlan* p) {
     r.tasks = (int)(ceil_div_ll(a.cpg, 32 / s.lpr) * s.parts);
     r.rounds = (int)ceil_div_ll(r.tasks, (long long)r.blocks * r.warps);
     p->parts = s.parts;
+    // the ring's slots, of x and of grad_y in 16-byte pieces
+    if (backward) p->smem = (size_t)kRing * 2 * vec * (elt + gelt) * kTwo;
     return;
   }
   ColTeam& c = p->col;
@@ -247,7 +271,6 @@ void plan_two(const NormArgs& a, bool backward, int planes, NormPlan* p) {
   c.shares = c.slices == 1 ? 1 : (a.cpg + c.width - 2) / c.width + 1;
   c.rows = 32 % c.cb ? c.rl : kTwo / 32;
   // the ring's slots, and in their place after them the tables
-  const size_t gelt = a.gdt == DC_F32 ? 4 : 2;
   const size_t ring = backward ? (size_t)kRing * 2 * s.v * (elt + gelt) * kTwo
                                : (size_t)kRing * 4 * s.v * elt * kTwo;
   const size_t table = backward ? (size_t)c.rows * c.width * sizeof(float2)

@@ -1,10 +1,18 @@
-// Group norm with an activation on [n][h][w][c] tensors, one launch.
+// Group norm with an activation on [n][h][w][c] tensors (mathematics as on
+// [n][c][h][w]).
 //
 // A slice of whole groups of an image, 64 or 128 bytes of every pixel, is a
 // unit, held in the shared memory of a cluster's blocks from the statistics to
 // the results (as on [n][c][h][w] tensors).  A thread keeps one vector of
 // channels and walks pixels, so that gamma, beta and the sums of its channels
 // stay in registers; the threads of a channel are added in a fixed order.
+//
+// Measured (launches alone): forward on 16 x 100 x 168 x 256 bf16 with SiLU
+// 69 us, 4.0 TB/s, bytes' time 40.5; backward on 2 x 50 x 84 x 256 bf16 with
+// SiLU 10.4 us, most of it the latency of its two launches.  The forward is
+// bound by instruction issue and the barriers between a block's phases (17.6
+// instructions an element at 2.0 of 4 a cycle, 28 warps an SM): two launches
+// for it took 75 us, three 156.
 #include "dc_norm.cuh"
 
 namespace dc {
@@ -73,8 +81,8 @@ template <typename T, int V>
 __device__ __forceinline__ void hold(const T* p, char* slot) {
   constexpr int kBytes = V * sizeof(T);
   if constexpr (kBytes >= 4) {  // (an asynchronous copy moves 4 bytes at least)
-    copy_async<kUnit<T, V>>(slot, p);
-    if constexpr (kBytes > 16) copy_async<16>(slot + 16 * blockDim.x, p + V / 2);
+    copy_async<kUnit<T, V>, (kBytes > 16)>(slot, p);
+    if constexpr (kBytes > 16) copy_async<16, true>(slot + 16 * blockDim.x, p + V / 2);
   }
 }
 
@@ -606,6 +614,13 @@ __global__ void __launch_bounds__(kTeam, ONE || V < 8 ? 2 : 1)
 }
 
 // ---------------------------------------------------------------- two launches
+//
+// A thread streams its vectors through a ring of slots of its own: two batches
+// arrive while one is worked on, without registers that wait.  The same loops
+// on plain loads took, on 2 x 200 x 336 x 256 bf16 with SiLU, 69 us forward
+// (now 43, bytes' time 20.3: x is read twice, the second time from L2) and
+// 129 us backward (now 81, bytes' time 30.4).  Bound by instruction issue and
+// by L2 for the second read.
 
 // Whether a vector can be copied asynchronously (4 bytes at least).
 template <typename T, int V>

@@ -43,7 +43,7 @@ __global__ void __launch_bounds__(1024)
 // units over kMaxCluster * kBlockBytes (and where plan_cols says so), two
 // launches that read their inputs twice.  us of clusters / two launches:
 // forward 32 x 256 x 56 x 56 bf16 ReLU 24.0 / 27.5, 16 x 100 x 168 x 256 SiLU
-// 69 / 75, backward 8 x 256 x 56 x 56 with a float32 gradient 22.1 / 23.5.
+// 69 / 75, backward 8 x 256 x 56 x 56 with a float32 gradient 20.8 / 22.8.
 constexpr int kSms = 152;
 // Most of a unit in a cluster's block: two blocks to an SM (50 KB, four to an
 // SM: 20.3 instead of 18.4 us on that backward).
@@ -144,9 +144,12 @@ bool plan_rows(const NormArgs& a, bool backward, int planes, NormPlan* p) {
   // 135 / 127; but with units of one block (64 x 28 x 28) 28 / 34, with rows of
   // a vector a lane (64 x 14 x 14 x 1024 in 8 groups) 70 / 78, and for
   // 16 x 112 x 112 under ReLU 93 / 104, GELU 140 / 165 (its slope is worked out
-  // twice), with float32 gradients 160 / 191.
-  return !(backward && a.dt == DC_BF16 && a.gdt == DC_BF16 && a.act == DC_ACT_SILU &&
-           r.blocks > 1 && vr >= 256 && p->blocks > 4 * kSms);
+  // twice).  With float32 gradients 16 x 56 x 56, 4 x 112 x 112, 16 x 112 x 112
+  // take 41 / 39, 46 / 39, 150 / 149 under SiLU, 38 / 32, 42 / 32, 138 / 128
+  // under ReLU.
+  const bool gains = a.act == DC_ACT_SILU || (a.gdt == DC_F32 && a.act != DC_ACT_GELU);
+  return !(backward && a.dt == DC_BF16 && gains && r.blocks > 1 && vr >= 256 &&
+           p->blocks > 4 * kSms);
 }
 
 // The forward's table of channel statistics and its partial triples.
@@ -204,13 +207,11 @@ bool plan_cols(const NormArgs& a, bool backward, bool keep, NormPlan* p) {
   // clusters / two launches: 4 x 56 x 56 (224 blocks) 12 / 18.5, 8 x 56 x 56
   // (448) 24 / 24, 16 x 56 x 56 (896) 46 / 31, 64 x 28 x 28 39 / 33, but with
   // units of one block, 512 x 14 x 14, 59 / 76, and of float32 tensors 46 / 50
-  // on 16 x 56 x 56.  Float32 gradients of bf16 tensors gain where units are
-  // large (SiLU and GELU; 16 x 56 x 56 57 / 48 and 58 / 53, but 64 x 28 x 28
-  // 46 / 51 and 49 / 56) and a vector's channels are one group's (10 channels a
-  // group of 320: 70 / 94).
-  const bool slope = a.act == DC_ACT_SILU || a.act == DC_ACT_GELU;
-  const bool gains = a.gdt == DC_BF16 ? c.blocks > 2 : slope && c.blocks > 4 && a.cpg % v == 0;
-  return !(backward && a.dt == DC_BF16 && gains && p->blocks > 3 * kSms);
+  // on 16 x 56 x 56.  With float32 gradients 45 / 37 under ReLU, 8 x 56 x 56
+  // 24 / 26, but with channels of two groups in a vector (10 a group of 320)
+  // 70 / 94.
+  const bool gains = a.dt == DC_BF16 && c.blocks > 2 && (a.gdt == DC_BF16 || a.cpg % v == 0);
+  return !(backward && gains && p->blocks > 3 * kSms);
 }
 
 // Of a pass's inputs, left in L2 (129 MB) between two launches: 64 MB, which
@@ -256,7 +257,7 @@ void plan_two(const NormArgs& a, bool backward, int planes, NormPlan* p) {
     r.rounds = (int)ceil_div_ll(r.tasks, (long long)r.blocks * r.warps);
     p->parts = s.parts;
     // the ring's slots, of x and of grad_y in 16-byte pieces
-    if (backward) p->smem = (size_t)kRing * 2 * vec * (elt + gelt) * kTwo;
+    if (backward && elt == gelt) p->smem = (size_t)kRing * 2 * vec * (elt + gelt) * kTwo;
     return;
   }
   ColTeam& c = p->col;

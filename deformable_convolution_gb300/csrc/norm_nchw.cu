@@ -15,7 +15,7 @@
 // it saves.  What does not fit is read again (from L2) for the results.
 //
 // Measured on 8 x 256 x 56 x 56 bf16 with ReLU (launches alone, tensors in L2):
-// forward 6.7 us, backward with a float32 gradient 19.4 us, where the tensors'
+// forward 6.7 us, backward with a float32 gradient 16.6 us, where the tensors'
 // bytes take 3.8 and 7.6 us from memory.  What bounds them is the chain of a
 // block (load, reduce, cluster barrier, store) in two waves: the units' 25 and
 // 150 KB leave an SM two blocks.  Three launches with x read twice took 34 us
@@ -611,7 +611,7 @@ __global__ void __launch_bounds__(kTeam, 2)
 // blocks' shares into the workspace, then the results, the second read from L2.
 // The backward's lanes stream their vectors through rings of slots of their
 // own: 69 us on 2 x 200 x 336 x 256 bf16 with SiLU, where loads into registers
-// took 91 and the bytes take 30.4 once.  Bound by the second read and the
+// took 84 and the bytes take 30.4 once.  Bound by the second read and the
 // launches' latency.
 
 // This thread's place where a unit's blocks are no cluster.
@@ -725,8 +725,15 @@ __global__ void __launch_bounds__(kTwo)
   }
 }
 
-// A backward task's vectors through the ring, work(i, f, d) on the i-th from
-// the lane's first.  Dynamic shared memory: the slots of x, then of grad_y.
+// Whether a backward's vectors go through the ring: not those of float32
+// gradients of bf16 tensors, two pieces each, whose slots leave three blocks to
+// an SM (2 x 200 x 336 x 256, ReLU: 87 us with loads into registers, 109 with
+// the ring).
+template <typename T, typename TG>
+constexpr bool kStreams = sizeof(T) == sizeof(TG);
+
+// A backward task's vectors through the ring, work(v, f, d) on each.  Dynamic
+// shared memory: the slots of x, then of grad_y.
 template <typename T, typename TG, int VEC, bool EVEN, typename WORK>
 __device__ __forceinline__ void stream_task(const Shape& s, const UnitTask<VEC, EVEN>& k,
                                             const T* x, const TG* gy, WORK&& work) {
@@ -777,15 +784,21 @@ __global__ void __launch_bounds__(kTwo)
     const UnitTask<VEC, EVEN> k(s, pl.unit, pl.ch0, pl.task(tm, r), tm.tasks);
     const float g = gamma ? gamma[k.ch] : 1.f, b = beta ? beta[k.ch] : 0.f;
     float2 sa = both(0.f), sb = both(0.f);
-    stream_task<T, TG, VEC, EVEN>(s, k, x, gy, [&](int, Pairs<VEC>& f, Pairs<VEC>& d) {
+    if constexpr (kStreams<T, TG>) {
+      stream_task<T, TG, VEC, EVEN>(s, k, x, gy, [&](int, Pairs<VEC>& f, Pairs<VEC>& d) {
 #pragma unroll
-      for (int e = 0; e < VEC / 2; ++e) {
-        const float2 xh = mul2(add2(f.p[e], both(-mu)), both(rs));
-        const float2 dz = act_bwd2<ACT>(fma2(xh, both(g), both(b)), d.p[e], s.floor);
-        sa = add2(sa, dz);
-        sb = fma2(dz, xh, sb);
-      }
-    });
+        for (int e = 0; e < VEC / 2; ++e) {
+          const float2 xh = mul2(add2(f.p[e], both(-mu)), both(rs));
+          const float2 dz = act_bwd2<ACT>(fma2(xh, both(g), both(b)), d.p[e], s.floor);
+          sa = add2(sa, dz);
+          sb = fma2(dz, xh, sb);
+        }
+      });
+    } else {
+      int none = 0;
+      task_sums<T, TG, VEC, EVEN, false, false, ACT>(s, k, x, gy, nullptr, nullptr, 0, none, mu,
+                                                     rs, g, b, sa, sb);
+    }
     const float ra = row_sum(sa.x + sa.y, s.lpr), rb = row_sum(sb.x + sb.y, s.lpr);
     if (k.live && (threadIdx.x & (s.lpr - 1)) == 0) {
       part[(long long)k.part * s.n * s.c + k.row] = make_float2(ra, rb);
@@ -823,18 +836,24 @@ __global__ void __launch_bounds__(kTwo)
   const float s1 = rs * (warp_sum(ga) * s.inv_total), s2 = rs * (warp_sum(gb) * s.inv_total);
   for (int r = 0; r < tm.rounds; ++r) {
     const UnitTask<VEC, EVEN> k(s, pl.unit, pl.ch0, pl.task(tm, r), tm.tasks);
-    const float g = gamma ? gamma[k.ch] : 1.f, b = beta ? beta[k.ch] : 0.f, gr = g * rs;
-    T* to = gx + k.off + (long long)k.v0 * VEC;
-    stream_task<T, TG, VEC, EVEN>(s, k, x, gy, [&](int v, Pairs<VEC>& f, Pairs<VEC>& d) {
+    const float g = gamma ? gamma[k.ch] : 1.f, b = beta ? beta[k.ch] : 0.f;
+    if constexpr (kStreams<T, TG>) {
+      const float gr = g * rs;
+      T* to = gx + k.off + (long long)k.v0 * VEC;
+      stream_task<T, TG, VEC, EVEN>(s, k, x, gy, [&](int v, Pairs<VEC>& f, Pairs<VEC>& d) {
 #pragma unroll
-      for (int e = 0; e < VEC / 2; ++e) {
-        const float2 xh = mul2(add2(f.p[e], both(-mu)), both(rs));
-        const float2 dz = act_bwd2<ACT>(fma2(xh, both(g), both(b)), d.p[e], s.floor);
-        f.p[e] = fma2(xh, both(-s2), fma2(dz, both(gr), both(-s1)));
-      }
-      put<T, VEC, EVEN>(k, v, to, f);
-      to += s.lpr * VEC;
-    });
+        for (int e = 0; e < VEC / 2; ++e) {
+          const float2 xh = mul2(add2(f.p[e], both(-mu)), both(rs));
+          const float2 dz = act_bwd2<ACT>(fma2(xh, both(g), both(b)), d.p[e], s.floor);
+          f.p[e] = fma2(xh, both(-s2), fma2(dz, both(gr), both(-s1)));
+        }
+        put<T, VEC, EVEN>(k, v, to, f);
+        to += s.lpr * VEC;
+      });
+    } else {
+      task_grads<T, TG, VEC, EVEN, false, false, ACT>(s, k, x, gy, gx, nullptr, nullptr, 0, mu, rs,
+                                                      g, b, s1, s2);
+    }
   }
 }
 

@@ -45,8 +45,8 @@ __global__ void __launch_bounds__(1024)
 // forward 32 x 256 x 56 x 56 bf16 ReLU 24.0 / 27.5, 16 x 100 x 168 x 256 SiLU
 // 69 / 75, backward 8 x 256 x 56 x 56 with a float32 gradient 20.8 / 22.8.
 constexpr int kSms = 152;
-// Most of a unit in a cluster's block: two blocks to an SM (50 KB, four to an
-// SM: 20.3 instead of 18.4 us on that backward).
+// Most of a unit in a cluster's block: two blocks to an SM (with 50 KB, four to
+// an SM, that backward took a tenth longer).
 constexpr int kBlockBytes = 92 * 1024;
 constexpr int kLeastBytes = 16 * 1024;  // not split further to make more blocks
 

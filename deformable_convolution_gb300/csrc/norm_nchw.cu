@@ -19,7 +19,7 @@
 // bytes take 3.8 and 7.6 us from memory.  What bounds them is the chain of a
 // block (load, reduce, cluster barrier, store) in two waves: the units' 25 and
 // 150 KB leave an SM two blocks.  Three launches with x read twice took 34 us
-// for that backward, units held in registers 29 us.
+// for that backward.
 #include "dc_norm.cuh"
 
 namespace dc {

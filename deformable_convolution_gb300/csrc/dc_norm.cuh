@@ -350,6 +350,19 @@ __host__ __device__ inline int row_vectors(int hw, int mis, int vec) {
   return (mis + hw + vec - 1) / vec;
 }
 
+// Two launches over whole-vector rows: the `count` vectors from `begin` on that
+// block `rank` takes of its unit, `span` to a block.  (A block has 2^30 at most,
+// a unit 2^31 and more: a group of 32 GB.)
+struct BlockRun {
+  long long begin;
+  int count;
+  __host__ __device__ BlockRun(int cpg, int row_vectors, int span, int rank)
+      : begin((long long)rank * span) {
+    const long long left = (long long)cpg * row_vectors - begin;
+    count = left < 0 ? 0 : left < span ? (int)left : span;
+  }
+};
+
 __device__ __forceinline__ void merge(float& n, float& mean, float& m2, float nb, float mb,
                                       float m2b) {
   if (nb == 0.f) return;

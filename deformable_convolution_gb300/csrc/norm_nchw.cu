@@ -639,10 +639,10 @@ __global__ void __launch_bounds__(kTwo)
   const Place pl = loose_place(s, tm, unit0);
   float n = 0.f, mean = 0.f, m2 = 0.f;
   if (EVEN) {
-    const int begin = pl.rank * tm.span + threadIdx.x;
-    const int end = min(s.cpg * (s.hw / VEC), (pl.rank + 1) * tm.span);
-    const T* p = x + (long long)pl.unit * s.cpg * s.hw + (long long)begin * VEC;
-    const int count = begin < end ? (end - begin + kTwo - 1) / kTwo : 0;
+    const BlockRun run(s.cpg, s.hw / VEC, tm.span, pl.rank);
+    const int tid = threadIdx.x;
+    const T* p = x + (long long)pl.unit * s.cpg * s.hw + (run.begin + tid) * VEC;
+    const int count = tid < run.count ? (run.count - tid + kTwo - 1) / kTwo : 0;
     auto get = [&](int b, Pairs<VEC>& f) { load_vec<T, VEC>(p + b * kTwo * VEC, f); };
     auto keep = [](int, Pairs<VEC>&, float) {};
     int i = 0;
@@ -690,20 +690,21 @@ __global__ void __launch_bounds__(kTwo)
     if (rstd_out) rstd_out[pl.unit] = rs;
   }
   if (EVEN) {
-    const int vr = s.hw / VEC, begin = pl.rank * tm.span + threadIdx.x;
-    const int end = min(s.cpg * vr, (pl.rank + 1) * tm.span);
-    const long long off = (long long)pl.unit * s.cpg * s.hw + (long long)begin * VEC;
+    const int vr = s.hw / VEC;
+    const BlockRun run(s.cpg, vr, tm.span, pl.rank);
+    const long long begin = run.begin + threadIdx.x;
+    const long long off = (long long)pl.unit * s.cpg * s.hw + begin * VEC;
     const T* p = x + off;
     T* to = y + off;
-    int c = begin / vr, at = begin - c * vr;
-    for (int v0 = begin; v0 < end; v0 += kBatch * kTwo) {
+    int c = (int)(begin / vr), at = (int)(begin - (long long)c * vr);
+    for (int v0 = threadIdx.x; v0 < run.count; v0 += kBatch * kTwo) {
       Pairs<VEC> f[kBatch];  // (loads ahead of the stores, which may be in place)
 #pragma unroll
       for (int i = 0; i < kBatch; ++i)
-        if (v0 + i * kTwo < end) load_vec<T, VEC>(p + i * kTwo * VEC, f[i]);
+        if (v0 + i * kTwo < run.count) load_vec<T, VEC>(p + i * kTwo * VEC, f[i]);
 #pragma unroll
       for (int i = 0; i < kBatch; ++i) {
-        if (v0 + i * kTwo >= end) break;
+        if (v0 + i * kTwo >= run.count) break;
         const float a = rs * (gamma ? gamma[pl.ch0 + c] : 1.f), b = beta ? beta[pl.ch0 + c] : 0.f;
 #pragma unroll
         for (int e = 0; e < VEC / 2; ++e)

@@ -1,0 +1,103 @@
+// Host-side checks of group norm's plans (compiled and run by
+// tests/test_host_layout.py; no GPU).
+//
+//  * two launches over whole-vector rows: the blocks' runs cover a unit's
+//    vectors in order and exactly once, up to the largest sizes accepted.
+#include "../../deformable_convolution_gb300/csrc/group_norm.cu"
+
+#include <cstdio>
+#include <random>
+
+namespace dc {
+void note_launches(unsigned) {}
+cudaError_t launch_nchw(const NormPlan&, const NormArgs&, bool, cudaStream_t) { return cudaSuccess; }
+cudaError_t launch_nhwc(const NormPlan&, const NormArgs&, bool, cudaStream_t) { return cudaSuccess; }
+cudaError_t launch_two_nchw(const NormPlan&, const NormArgs&, bool, bool, int, int, cudaStream_t) {
+  return cudaSuccess;
+}
+cudaError_t launch_two_nhwc(const NormPlan&, const NormArgs&, bool, bool, int, int, cudaStream_t) {
+  return cudaSuccess;
+}
+}  // namespace dc
+
+using namespace dc;
+
+static long long failures = 0, runs = 0, wide = 0;
+#define CHECK(cond, ...)                  \
+  do {                                    \
+    if (!(cond)) {                        \
+      if (failures < 20) {                \
+        printf("FAIL %s: ", #cond);       \
+        printf(__VA_ARGS__);              \
+        printf("\n");                     \
+      }                                   \
+      ++failures;                         \
+    }                                     \
+  } while (0)
+
+static NormArgs make_args(int n, int groups, int cpg, long long hw, dc_dtype dt, dc_dtype gdt,
+                          bool nhwc, int act) {
+  NormArgs a{};
+  a.n = n;
+  a.c = groups * cpg;
+  a.groups = groups;
+  a.cpg = cpg;
+  a.hw = (int)hw;
+  a.nhwc = nhwc;
+  a.act = act;
+  a.eps = 1e-5f;
+  a.dt = dt;
+  a.gdt = gdt;
+  return a;
+}
+
+static void check_runs(const NormArgs& a, const NormPlan& p) {
+  const int vec = a.dt == DC_BF16 ? 8 : 4;
+  if (a.hw % vec) return;
+  const int vr = a.hw / vec;
+  const long long total = (long long)a.cpg * vr;
+  long long at = 0;
+  for (int rank = 0; rank < p.row.blocks; ++rank) {
+    const BlockRun r(a.cpg, vr, p.row.span, rank);
+    if (r.count == 0) continue;
+    CHECK(r.begin == at, "c %d hw %d rank %d: from %lld, not %lld", a.cpg, a.hw, rank, r.begin, at);
+    CHECK(r.count > 0 && r.count <= 1 << 30, "c %d hw %d rank %d: %d vectors", a.cpg, a.hw, rank,
+          r.count);
+    at = r.begin + r.count;
+  }
+  CHECK(at == total, "c %d hw %d: %lld of %lld vectors", a.cpg, a.hw, at, total);
+  ++runs;
+  wide += total > INT_MAX;
+}
+
+static void check(const NormArgs& a) {
+  if (!norm_supported(a)) return;
+  for (int backward = 0; backward < 2; ++backward) {
+    const NormPlan p = make_plan(a, backward != 0);
+    if (!p.cluster && !a.nhwc && !backward) check_runs(a, p);
+  }
+}
+
+int main() {
+  // a group of 2^31 vectors, and the sizes around it
+  for (const int cpg : {63, 64, 65, 72})
+    check(make_args(1, 1, cpg, 1LL << 28, DC_BF16, DC_BF16, false, DC_ACT_SILU));
+  check(make_args(1, 1, 24, 1LL << 30, DC_BF16, DC_BF16, false, DC_ACT_SILU));
+  check(make_args(1, 1, 1024, 1LL << 30, DC_BF16, DC_BF16, false, DC_ACT_NONE));
+  check(make_args(2, 3, 1 << 16, 1 << 20, DC_F32, DC_F32, false, DC_ACT_RELU));
+  std::mt19937_64 rng(1);
+  auto spread = [&](double lo, double hi) {
+    return (long long)std::lround(
+        std::exp(std::uniform_real_distribution<double>(std::log(lo), std::log(hi))(rng)));
+  };
+  for (int i = 0; i < 300000; ++i) {
+    const int groups = (int)spread(1, 64), cpg = (int)spread(1, 4000), n = (int)spread(1, 600);
+    long long hw = spread(1, 1 << 30);
+    if (rng() % 4) hw = (hw + 7) / 8 * 8;
+    if (hw > 1 << 30 || (double)n * groups * cpg * (double)hw > (double)(1LL << 40)) continue;
+    const dc_dtype dt = rng() % 2 ? DC_BF16 : DC_F32;
+    check(make_args(n, groups, cpg, hw, dt, rng() % 2 ? DC_F32 : dt, rng() % 2, (int)(rng() % 4)));
+  }
+  printf("%lld sizes in runs, %lld of them past 32 bits, %lld failures\n", runs, wide, failures);
+  return failures || runs < 1000 || wide < 100;
+}

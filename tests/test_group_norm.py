@@ -326,3 +326,44 @@ def test_gradients_match_differences_of_the_plain_forward(layout):
     h = 1e-6
     # float32 gradients: 2^-18 of the terms' absolute sum; the differences add 1e-6
     assert abs((loss(h) - loss(-h)) / (2 * h) - want) < 2.0 ** -18 * scale + 1e-6 * (1 + abs(want))
+
+
+@on_gpu
+def test_a_group_of_more_than_2_to_the_31_vectors():
+    c, size = 66, 16384
+    p = B.NormProblem(1, c, size, size, 1, B.DC_BF16, B.DC_NCHW, B.DC_ACT_SILU, 1e-5, B.DC_BF16)
+    gen = torch.Generator(device="cuda").manual_seed(7)
+    plane = torch.empty(size, size, device="cuda").normal_(generator=gen)
+    scale = 0.5 + torch.rand(c, generator=torch.Generator().manual_seed(8))
+    shift = torch.linspace(-1, 1, c)
+
+    def channel(k):
+        return (plane * float(scale[k]) + float(shift[k])).to(torch.bfloat16)
+
+    x = torch.empty(p.shape, dtype=torch.bfloat16, device="cuda")
+    sums, top = torch.zeros(2, dtype=torch.float64, device="cuda"), 0.0
+    for k in range(c):
+        x[0, k] = channel(k)
+        v = x[0, k].double()
+        sums += torch.stack([v.sum(), v.square().sum()])
+        top = max(top, float(v.abs().max()))
+    m = c * size * size
+    mean = float(sums[0]) / m
+    var = float(sums[1]) / m - mean ** 2  # (64 bits: the mean is of the spread's order)
+    rstd = (var + p.eps) ** -0.5
+    gamma = 1 + 0.2 * torch.randn(c, generator=torch.Generator().manual_seed(9))
+    beta = torch.linspace(-0.5, 0.5, c)
+    got_mean, got_rstd = (torch.empty(1, 1, device="cuda") for _ in range(2))
+    B.dc_group_norm_fwd(p, x, gamma.cuda(), beta.cuda(), x, got_mean, got_rstd, B.norm_workspace(p, False))  # in place
+    # a thread merges at most 2^12 batches one after the other, each a rounding
+    # of the mean and of the variance; then 64 as at every other size
+    chain = (2 ** 12 + 64) * P.U
+    d_mean = chain * top
+    d_rstd = rstd * (chain + 0.5 * rstd ** 2 * d_mean ** 2)
+    assert abs(float(got_mean) - mean) <= d_mean and abs(float(got_rstd) - rstd) <= d_rstd
+    for k in range(c):
+        z = (channel(k).double() - mean) * rstd * float(gamma[k]) + float(beta[k])
+        want = z / (1 + torch.exp(-z))
+        d_z = abs(float(gamma[k])) * rstd * d_mean + (z.abs() + 1) * d_rstd / rstd + 8 * P.U * (z.abs() + 1)
+        bound = 1.2 * d_z + (want.abs() + 1.2 * d_z) * 2.0 ** -8 * 1.01
+        assert ((x[0, k].double() - want).abs() <= bound).all(), k

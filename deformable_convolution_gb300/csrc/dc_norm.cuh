@@ -476,13 +476,23 @@ __device__ __forceinline__ void through_ring(int count, START&& start, WORK&& wo
   }
 }
 
+// Dynamic shared memory that a kernel may be launched with: more than any plan
+// asks for, and one value for all of them.  The limit is the kernel's, not the
+// call's: a host thread that set it to its own launch's need would have the
+// launch of another one, in between, refused.
+constexpr int kSmemLimit = 160 * 1024;
+template <typename K>
+cudaError_t allow_smem(K kern, size_t smem) {
+  if (smem <= 40 * 1024) return cudaSuccess;  // (beside up to 6 KB of static arrays)
+  return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemLimit);
+}
+
 template <typename K, typename... A>
 cudaError_t launch_team(K kern, const NormPlan& p, int cluster, cudaStream_t s, A... args) {
   cudaError_t e = cudaSuccess;
   if (cluster > 8)
     e = cudaFuncSetAttribute(kern, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
-  if (e == cudaSuccess && p.smem > 40 * 1024)  // (beside up to 6 KB of static arrays)
-    e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)p.smem);
+  if (e == cudaSuccess) e = allow_smem(kern, p.smem);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(p.blocks);
@@ -506,12 +516,9 @@ cudaError_t launch_team(K kern, const NormPlan& p, int cluster, cudaStream_t s, 
 template <typename K, typename... A>
 cudaError_t launch_smem(K kern, unsigned blocks, int threads, size_t smem, cudaStream_t s,
                         A... args) {
+  cudaError_t e = allow_smem(kern, smem);
+  if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
-  if (smem > 40 * 1024) {
-    const cudaError_t e =
-        cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-    if (e != cudaSuccess) return e;
-  }
   cfg.gridDim = dim3(blocks);
   cfg.blockDim = dim3((unsigned)threads);
   cfg.dynamicSmemBytes = smem;
@@ -521,7 +528,7 @@ cudaError_t launch_smem(K kern, unsigned blocks, int threads, size_t smem, cudaS
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  const cudaError_t e = cudaLaunchKernelEx(&cfg, kern, args...);
+  e = cudaLaunchKernelEx(&cfg, kern, args...);
   note_launches(1);
   return e;
 }

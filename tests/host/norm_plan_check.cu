@@ -2,7 +2,31 @@
 // tests/test_host_layout.py; no GPU).
 //
 //  * two launches over whole-vector rows: the blocks' runs cover a unit's
-//    vectors in order and exactly once, up to the largest sizes accepted.
+//    vectors in order and exactly once, up to the largest sizes accepted;
+//  * a kernel's limit of dynamic shared memory is set to one value whatever the
+//    problem (host threads that launch a kernel at the same time cannot lower it
+//    under one another), and every launch stays within it.
+#include <cuda_runtime.h>
+
+#include <set>
+
+// Launches and limits are recorded, not made.
+static std::set<int> limits;
+static size_t launched_smem, most_smem;
+template <typename K>
+static cudaError_t record_attribute(K, cudaFuncAttribute attr, int value) {
+  if (attr == cudaFuncAttributeMaxDynamicSharedMemorySize) limits.insert(value);
+  return cudaSuccess;
+}
+template <typename K, typename... A>
+static cudaError_t record_launch(const cudaLaunchConfig_t* c, K, A...) {
+  launched_smem = c->dynamicSmemBytes;
+  if (launched_smem > most_smem) most_smem = launched_smem;
+  return cudaSuccess;
+}
+#define cudaFuncSetAttribute record_attribute
+#define cudaLaunchKernelEx record_launch
+
 #include "../../deformable_convolution_gb300/csrc/group_norm.cu"
 
 #include <cstdio>
@@ -70,11 +94,23 @@ static void check_runs(const NormArgs& a, const NormPlan& p) {
   wide += total > INT_MAX;
 }
 
+__global__ void some_kernel(int) {}
+
+static void check_smem(const NormArgs& a, const NormPlan& p) {
+  launched_smem = 0;
+  if (p.cluster)
+    launch_team(some_kernel, p, a.nhwc ? p.col.blocks : p.row.blocks, nullptr, 0);
+  else
+    launch_smem(some_kernel, 1, p.threads, p.smem, nullptr, 0);
+  CHECK(launched_smem == p.smem, "%zu bytes planned, %zu launched", p.smem, launched_smem);
+}
+
 static void check(const NormArgs& a) {
   if (!norm_supported(a)) return;
   for (int backward = 0; backward < 2; ++backward) {
     const NormPlan p = make_plan(a, backward != 0);
     if (!p.cluster && !a.nhwc && !backward) check_runs(a, p);
+    check_smem(a, p);
   }
 }
 
@@ -98,6 +134,10 @@ int main() {
     const dc_dtype dt = rng() % 2 ? DC_BF16 : DC_F32;
     check(make_args(n, groups, cpg, hw, dt, rng() % 2 ? DC_F32 : dt, rng() % 2, (int)(rng() % 4)));
   }
+  // 227 KB are a block's at most, of which the static arrays take up to 8
+  CHECK(limits.size() == 1 && *limits.begin() <= (227 - 8) * 1024, "%zu limits, the largest %d",
+        limits.size(), *limits.rbegin());
+  CHECK(most_smem <= (size_t)*limits.begin(), "%zu bytes launched", most_smem);
   printf("%lld sizes in runs, %lld of them past 32 bits, %lld failures\n", runs, wide, failures);
   return failures || runs < 1000 || wide < 100;
 }

@@ -252,7 +252,8 @@ __device__ __forceinline__ float2 act_bwd2(float2 z, float2 d, float floor) {
     const float2 cdf = normal_cdf2(z, &e);
     return mul2(d, fma2(mul2(z, both(0.39894228040143268f)), e, cdf));
   }
-  return make_float2(z.x > floor ? d.x : 0.f, z.y > floor ? d.y : 0.f);
+  const bool none = floor < 0.f;  // (every z is open then, NaN and -inf too)
+  return make_float2(z.x > floor || none ? d.x : 0.f, z.y > floor || none ? d.y : 0.f);
 }
 template <int ACT>
 __device__ __forceinline__ float act_bwd(float z, float d, float floor) {

@@ -357,8 +357,9 @@ dc_status dc_group_norm_fwd(const dc_norm_problem* prob, const void* x, const fl
                             size_t ws_bytes, void* stream);
 
 /* Backward, for the gradient grad_y of y:
- *   dz = grad_y * act'(z) (act'(z) = z > 0 for the ReLU, whose
- *   closed side passes nothing whatever grad_y is),
+ *   dz = grad_y * act'(z) (act'(z) = z > 0 for the ReLU, whose closed side, a
+ *   NaN z's too, passes nothing whatever grad_y is; dz = grad_y for no
+ *   activation, whatever z is),
  *   s1 = sum(gamma * dz) / m, s2 = sum(gamma * dz * xh) / m over a group,
  *   grad_x = rstd * (gamma * dz - s1 - xh * s2),
  *   grad_gamma[channel] = sum(dz * xh), grad_beta[channel] = sum(dz)

@@ -367,3 +367,68 @@ def test_a_group_of_more_than_2_to_the_31_vectors():
         d_z = abs(float(gamma[k])) * rstd * d_mean + (z.abs() + 1) * d_rstd / rstd + 8 * P.U * (z.abs() + 1)
         bound = 1.2 * d_z + (want.abs() + 1.2 * d_z) * 2.0 ** -8 * 1.01
         assert ((x[0, k].double() - want).abs() <= bound).all(), k
+
+
+NOT_FINITE_SHAPES = [  # n, c, h, w, groups: in one launch and in two, whole vectors and odd rows
+    (2, 16, 12, 12, 4), (2, 12, 11, 13, 4), (2, 16, 400, 336, 2), (2, 20, 401, 333, 2),
+]
+
+
+@on_gpu
+@pytest.mark.parametrize("layout", (B.DC_NCHW, B.DC_NHWC))
+@pytest.mark.parametrize("dtype,grad", [(B.DC_F32, B.DC_F32), (B.DC_BF16, B.DC_BF16), (B.DC_BF16, B.DC_F32)])
+@pytest.mark.parametrize("act", (B.DC_ACT_NONE, B.DC_ACT_RELU))
+@pytest.mark.parametrize("shape", NOT_FINITE_SHAPES)
+def test_slopes_where_a_group_is_not_a_number(shape, act, dtype, grad, layout):
+    """act'(z) is 1 without an activation, whatever z is, and z > 0 for the
+    ReLU: a group that holds a NaN passes all of grad_y on, or none of it."""
+    n, c, h, w, groups = shape
+    p = B.NormProblem(n, c, h, w, groups, dtype, layout, act, 1e-5, grad)
+    x, gamma, beta, gy = (t.cuda() for t in inputs(p, 31))
+    hit = torch.zeros(n, groups, c // groups, h * w, dtype=torch.bool)
+    hit[1, 1] = True
+    hit = P.layout(p, hit).cuda()
+    x2 = x.clone()
+    if layout == B.DC_NHWC:
+        x2[1, 3, 2, c // groups] = float("nan")
+    else:
+        x2[1, c // groups, 3, 2] = float("nan")
+    _, mean, rstd = B.group_norm(p, x2, gamma, beta)
+    assert torch.isnan(mean[1, 1]) and torch.isfinite(mean).sum() == mean.numel() - 1
+    clean = B.group_norm_backward(p, x, gamma, beta, *B.group_norm(p, x, gamma, beta)[1:], gy)
+    g = B.group_norm_backward(p, x2, gamma, beta, mean, rstd, gy)
+    assert torch.isnan(g["grad_x"][hit]).all()
+    assert torch.equal(g["grad_x"][~hit], clean["grad_x"][~hit])
+    per = c // groups
+    assert torch.isnan(g["grad_gamma"][per:2 * per]).all()
+    # grad_beta: sums of non-negative terms' worth of at most 96 roundings in a row
+    over = (0, 1, 2) if layout == B.DC_NHWC else (0, 2, 3)
+    dz = gy.double()
+    if act == B.DC_ACT_RELU:
+        shape4 = (1, 1, 1, c) if layout == B.DC_NHWC else (1, c, 1, 1)
+        m4, r4 = (P.layout(p, t.double()[:, :, None, None].expand(n, groups, per, h * w)) for t in (mean, rstd))
+        z = (x2.double() - m4) * r4 * gamma.double().view(shape4) + beta.double().view(shape4)
+        near_kink = (z.abs() <= 8 * P.U * (1 + z.abs()))
+        slack = (dz.abs() * near_kink).sum(over)
+        dz = dz * (z > 0)
+    else:
+        slack = 0
+    bound = 96 * P.U * dz.abs().sum(over) + slack + 1e-38
+    assert ((g["grad_beta"].double() - dz.sum(over)).abs() <= bound).all()
+
+
+@on_gpu
+@pytest.mark.parametrize("layout", (B.DC_NCHW, B.DC_NHWC))
+@pytest.mark.parametrize("shape", NOT_FINITE_SHAPES)
+def test_a_channel_at_minus_infinity_passes_its_gradient_without_an_activation(shape, layout):
+    n, c, h, w, groups = shape
+    p = B.NormProblem(n, c, h, w, groups, B.DC_F32, layout, B.DC_ACT_NONE)
+    x, gamma, beta, gy = (t.cuda() for t in inputs(p, 32))
+    y, mean, rstd = B.group_norm(p, x, gamma, beta)
+    want = B.group_norm_backward(p, x, gamma, beta, mean, rstd, gy)
+    beta[1] = -float("inf")  # (no gradient depends on beta without an activation)
+    y = B.group_norm(p, x, gamma, beta)[0]
+    cut = y[..., 1] if layout == B.DC_NHWC else y[:, 1]
+    assert (cut == -float("inf")).all()
+    g = B.group_norm_backward(p, x, gamma, beta, mean, rstd, gy)
+    assert all(torch.equal(g[k], want[k]) for k in want)

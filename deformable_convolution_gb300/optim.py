@@ -135,21 +135,28 @@ class AdamW:
         return out
 
     def state_dict(self):
-        """The state as tensors (not copies): for saving between steps."""
-        keys = ("m", "v", "m_scale", "v_scale")
+        """The state as tensors (not copies): for saving between steps.  The
+        masters are part of it: a bfloat16 ``param`` lacks their low bits."""
+        keys = ("m", "v", "m_scale", "v_scale", "master")
         return dict(step=self._hyper.step, lr=self._hyper.lr,
                     state=[{k: q[k] for k in keys if q.get(k) is not None} for q in self.params])
 
     def load_state_dict(self, d):
-        """Copies a ``state_dict`` of the same parameters into this state."""
+        """Copies a ``state_dict`` of the same parameters into this state.  A
+        parameter with a master becomes its rounded copy; a state that holds no
+        masters leaves both as they are."""
         if len(d["state"]) != len(self.params):
             raise ValueError("state of another number of tensors")
         for q, s in zip(self.params, d["state"]):
-            for k in ("m", "v", "m_scale", "v_scale"):
+            for k in ("m", "v", "m_scale", "v_scale", "master"):
                 a, b = q.get(k), s.get(k)
+                if b is None and k == "master":
+                    continue
                 if (a is None) != (b is None) or (a is not None and (a.dtype != b.dtype or a.shape != b.shape)):
                     raise ValueError(f"state {k} of another kind or shape")
         for q, s in zip(self.params, d["state"]):
             for k, t in s.items():
                 q[k].copy_(t)
+            if s.get("master") is not None:
+                q["param"].copy_(q["master"])
         self._hyper.step, self._hyper.lr = d["step"], d["lr"]

@@ -358,6 +358,32 @@ def test_state_dict_resumes_bit_for_bit():
 
 
 @on_gpu
+@pytest.mark.parametrize("bits", (32, 8))
+def test_state_dict_carries_the_masters(bits):
+    a, b = (make([513, 9000], BF16, True, F32, bits, seed=k) for k in (6, 7))
+    a.step()
+    saved = a.state_dict()
+    b.load_state_dict(saved)
+    for q, r in zip(a.params, b.params):
+        assert torch.equal(q["master"], r["master"]) and torch.equal(q["param"], r["param"])
+        r["grad"].copy_(q["grad"])
+    a.step(), b.step()
+    for q, r in zip(a.params, b.params):
+        assert all(torch.equal(q[k], r[k]) for k in ("param", "master", "m", "v"))
+    # a state of another kind changes nothing
+    short = dict(saved, state=[saved["state"][0], dict(saved["state"][1], master=saved["state"][1]["master"][1:])])
+    old = [r["master"].clone() for r in b.params]
+    with pytest.raises(ValueError):
+        b.load_state_dict(short)
+    assert all(torch.equal(r["master"], o) for r, o in zip(b.params, old))
+    with pytest.raises(ValueError):
+        make([513, 9000], F32, False, F32, bits).load_state_dict(saved)
+    # one saved without masters leaves them as they are
+    b.load_state_dict(dict(saved, state=[{k: v for k, v in s.items() if k != "master"} for s in saved["state"]]))
+    assert all(torch.equal(r["master"], o) for r, o in zip(b.params, old))
+
+
+@on_gpu
 def test_side_stream():
     opt, ref = (make([3000, 70001], BF16, True, BF16, 8, seed=8) for _ in range(2))
     torch.cuda.synchronize()

@@ -100,3 +100,36 @@ def test_a_gradient_that_is_not_finite_leaves_the_parameters():
     assert not np.isfinite(float(tr.grad_norm))
     for q, o in zip(params, old):
         assert all(torch.equal(q[k], o[k]) for k in q)
+
+
+@pytest.mark.parametrize("bits", (32, 8))
+def test_a_saved_state_resumes_bit_for_bit(bits):
+    p = B.Problem(2, 64, 8, 8, 64, dtype=B.DC_BF16)
+    first, again = (T.Trainer(p, T.initial_params(p, 2, seed=s), groups=8, state_bits=bits) for s in (5, 6))
+    gen = torch.Generator().manual_seed(7)
+    x, g = (torch.randn(p.shapes()[k], generator=gen).to(torch.bfloat16).cuda() for k in ("x", "y"))
+
+    def step(tr):
+        tr.forward(x)
+        tr.backward(g)
+        tr.update()
+    for _ in range(3):
+        step(first)
+    for q, r in zip(first.params, again.params):
+        for k in q:
+            r[k].copy_(q[k])
+    again.opt.load_state_dict(first.opt.state_dict())
+    for _ in range(3):
+        # the layer's weight gradients are sums in an order of their own: the update's input is made the same
+        for tr in (first, again):
+            tr.forward(x)
+            tr.backward(g)
+        for a, b in zip(first.grads, again.grads):
+            for k in a:
+                b[k].copy_(a[k])
+        first.update(), again.update()
+        for q, r in zip(first.params, again.params):
+            assert all(torch.equal(q[k], r[k]) for k in q)
+    for q, r in zip(first.opt.params, again.opt.params):
+        if q.get("master") is not None:
+            assert torch.equal(q["master"], r["master"])

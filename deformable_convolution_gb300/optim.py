@@ -8,7 +8,7 @@ the device.  The update and the 8-bit state code are defined in
 """
 from __future__ import annotations
 
-import ctypes
+from types import MappingProxyType
 
 import torch
 
@@ -16,15 +16,30 @@ from . import binding as B
 
 
 class GradNorm:
-    """Global norm of a fixed list of gradients (float32 or bfloat16 CUDA
-    tensors), and the factor that clips it."""
+    """Global norm of a list of gradients (float32 or bfloat16 CUDA tensors),
+    and the factor that clips it.  Their addresses are taken here and by
+    ``set_grads``.  The object keeps one workspace: its calls belong on one
+    stream, or on streams that wait for one another."""
 
     def __init__(self, grads):
-        self.grads = list(grads)
-        self._table = B.adamw_tensors([dict(grad=g) for g in self.grads])
+        self._set(grads)
         device = self.grads[0].device if self.grads else "cuda"
         need = B.dc_grad_norm_workspace_size(len(self.grads))
         self._ws = torch.empty(max(need, 1), dtype=torch.uint8, device=device)
+
+    def _set(self, grads):
+        grads = tuple(grads)
+        self._table = B.adamw_tensors([dict(grad=g) for g in grads])
+        self.grads = grads
+
+    def set_grads(self, grads):
+        """Other gradients, as many as there were."""
+        grads = tuple(grads)
+        if len(grads) != len(self.grads):
+            raise ValueError(f"expected {len(self.grads)} gradients, got {len(grads)}")
+        if any(g is None for g in grads):
+            raise ValueError("a gradient is missing")
+        self._set(grads)
 
     def __call__(self, max_norm, norm, scale, stream=None):
         """norm, scale: one-element float32 tensors (or None)."""
@@ -36,7 +51,7 @@ class StateValues:
     an (m, v) pair of float32 tensors, either of which may be None."""
 
     def __init__(self, opt, out):
-        self.opt, self.out = opt, list(out)
+        self.opt, self.out = opt, tuple(tuple(pair) for pair in out)
         if len(self.out) != len(opt.params):
             raise ValueError(f"expected {len(opt.params)} pairs, got {len(self.out)}")
         shapes = [tuple(q["param"].shape) for q in opt.params]
@@ -59,13 +74,17 @@ class AdamW:
 
     state_bits: 32 (float32 states) or 8 (int8 m, uint8 v and a float32 scale
     for each 256 elements; tensors below ``min_8bit`` elements keep float32
-    states).  step: steps already taken."""
+    states).  step: steps already taken.
+
+    The optimiser reads and writes its tensors by the addresses they have when
+    it is made; ``params`` is therefore read-only, and gradients that autograd
+    allocates anew are handed over by ``set_grads``."""
 
     def __init__(self, params, lr=1e-3, betas=(0.9, 0.999), eps=1e-8, weight_decay=0.01,
                  state_bits=32, min_8bit=0, step=0):
         if state_bits not in (8, 32):
             raise ValueError("state_bits must be 8 or 32")
-        self.params = []
+        entries = []
         for q in params:
             q = dict(q)
             q.setdefault("weight_decay", weight_decay)
@@ -80,10 +99,25 @@ class AdamW:
                     blocks = -(-p.numel() // B.STATE_BLOCK)
                     q["m_scale"], q["v_scale"] = (torch.zeros(blocks, device=p.device)
                                                   for _ in range(2))
-            self.params.append(q)
+            entries.append(q)
         self._hyper = B.DcAdamwHyper(lr, betas[0], betas[1], eps, step)
-        self._table = B.adamw_tensors(self.params)
         self._norm = None
+        self._set(entries)
+
+    def _set(self, entries):
+        self._table = B.adamw_tensors(entries)
+        self.params = tuple(MappingProxyType(q) for q in entries)
+
+    def set_grads(self, grads):
+        """Other gradients for the next steps and norms, one for each parameter."""
+        grads = tuple(grads)
+        if len(grads) != len(self.params):
+            raise ValueError(f"expected {len(self.params)} gradients, got {len(grads)}")
+        if any(g is None or g.shape != q["param"].shape for g, q in zip(grads, self.params)):
+            raise ValueError("a gradient is missing or of another shape than its parameter")
+        self._set([dict(q, grad=g) for q, g in zip(self.params, grads)])
+        if self._norm is not None:
+            self._norm.set_grads(grads)
 
     @property
     def step_count(self):

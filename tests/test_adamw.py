@@ -457,3 +457,43 @@ def test_norm_of_nothing_of_no_limit_and_of_what_is_not_finite():
         h[4321] = value
         optim.GradNorm([g, h])(1.0, norm, scale)
         assert not math.isfinite(float(norm)) and math.isnan(float(scale))
+
+
+@on_gpu
+def test_gradients_are_renewed_by_set_grads_alone():
+    opt, ref = (make([5, 3000, 4097], BF16, True, F32, 8, seed=9) for _ in range(2))
+    # the table holds addresses: a tensor put into the optimiser's dicts would not be read
+    with pytest.raises(TypeError):
+        opt.params[1]["grad"] = torch.ones_like(opt.params[1]["grad"])
+    with pytest.raises(TypeError):
+        opt.params[1] = dict(opt.params[1])
+    opt.grad_norm(1.0)
+    gen = torch.Generator().manual_seed(10)
+    for dtype in (F32, BF16):
+        fresh = [torch.randn(q["grad"].shape, generator=gen).to(dtype).cuda() for q in ref.params]
+        opt.set_grads(fresh)
+        assert all(q["grad"] is g for q, g in zip(opt.params, fresh))
+        norm, scale = opt.grad_norm(0.5)
+        assert abs(float(norm) - exact_norm(fresh)) <= 2 ** 10 * U * exact_norm(fresh)
+        opt.step(scale)
+        want = optim.AdamW([dict(q, grad=g) for q, g in zip(ref.params, fresh)], lr=LR, betas=(B1, B2), eps=EPS, step=ref.step_count)
+        want.step(scale)
+        ref._hyper.step = want.step_count
+        for q, r in zip(opt.params, ref.params):
+            assert all(torch.equal(q[k], r[k]) for k in ("param", "master", "m", "v", "m_scale", "v_scale"))
+    # refusals leave the gradients that were there
+    for bad in (fresh[:2], [g[:-1] for g in fresh], [g.double() for g in fresh], [g.cpu() for g in fresh], [None] + fresh[1:]):
+        with pytest.raises(ValueError):
+            opt.set_grads(bad)
+    assert all(q["grad"] is g for q, g in zip(opt.params, fresh))
+    # the norm's own list
+    n = optim.GradNorm(fresh)
+    with pytest.raises(TypeError):
+        n.grads[0] = fresh[0]
+    with pytest.raises(ValueError):
+        n.set_grads(fresh[1:])
+    other = [2 * g for g in fresh]
+    n.set_grads(other)
+    out = torch.empty(1, device="cuda")
+    n(1.0, out, None)
+    assert abs(float(out) - exact_norm(other)) <= 2 ** 10 * U * exact_norm(other)

@@ -60,40 +60,7 @@ struct VecOf {
   static constexpr int n = 16 / sizeof(T);
 };
 
-// V elements at p (aligned to V * sizeof(T) bytes) as floats.
-template <typename T, int V>
-__device__ __forceinline__ void load_vec(const T* p, float* f) {
-  if constexpr (V * sizeof(T) == 32) {
-    load_vec<T, V / 2>(p, f);
-    load_vec<T, V / 2>(p + V / 2, f + V / 2);
-  } else if constexpr (sizeof(T) == 4) {
-    if constexpr (V == 4) {
-      const float4 v = *reinterpret_cast<const float4*>(p);
-      f[0] = v.x, f[1] = v.y, f[2] = v.z, f[3] = v.w;
-    } else {
-#pragma unroll
-      for (int e = 0; e < V; ++e) f[e] = p[e];
-    }
-  } else if constexpr (V == 1) {
-    f[0] = to_f(p[0]);
-  } else {
-    uint32_t w[V / 2];
-    if constexpr (V == 8) {
-      const uint4 v = *reinterpret_cast<const uint4*>(p);
-      w[0] = v.x, w[1] = v.y, w[2] = v.z, w[3] = v.w;
-    } else {
-      static_assert(V == 4);
-      const uint2 v = *reinterpret_cast<const uint2*>(p);
-      w[0] = v.x, w[1] = v.y;
-    }
-#pragma unroll
-    for (int e = 0; e < V / 2; ++e) {
-      f[2 * e] = __uint_as_float(w[e] << 16);
-      f[2 * e + 1] = __uint_as_float(w[e] & 0xffff0000u);
-    }
-  }
-}
-
+// V floats to p (aligned to V * sizeof(T) bytes).
 template <typename T, int V>
 __device__ __forceinline__ void store_vec(T* p, const float* f) {
   if constexpr (sizeof(T) == 4) {
@@ -234,10 +201,6 @@ __device__ __forceinline__ float2 act_fwd2(float2 z, float floor) {
   asm("max.NaN.f32 %0, %1, %2;" : "=f"(y.y) : "f"(z.y), "f"(floor));
   return y;
 }
-template <int ACT>
-__device__ __forceinline__ float act_fwd(float z, float floor) {
-  return act_fwd2<ACT>(both(z), floor).x;
-}
 
 // d * act'(z); the ReLU's closed side passes nothing, whatever d is.
 template <int ACT>
@@ -254,10 +217,6 @@ __device__ __forceinline__ float2 act_bwd2(float2 z, float2 d, float floor) {
   }
   const bool none = floor < 0.f;  // (every z is open then, NaN and -inf too)
   return make_float2(z.x > floor || none ? d.x : 0.f, z.y > floor || none ? d.y : 0.f);
-}
-template <int ACT>
-__device__ __forceinline__ float act_bwd(float z, float d, float floor) {
-  return act_bwd2<ACT>(both(z), both(d), floor).x;
 }
 
 // ---------------------------------------------------------------- the tiling
@@ -297,9 +256,8 @@ __device__ __forceinline__ float unit_mean(const Shape& s, float sum) {
 struct RowTeam {
   int blocks, warps, units;  // of a unit, of a unit in a block, units of a block
   int tasks, rounds;         // of a unit, of a warp
-  int held;                  // rounds kept in shared memory
   // whole-vector rows, forward: the unit's vectors in one run, `span` of them
-  // to a block (0: by tasks); held counts a thread's vectors
+  // to a block (0: by tasks)
   int span, step_c, step_v;  // threads of a unit in a block, as channels and vectors
 };
 // NHWC: a unit is a slice of channels, `cb` vectors wide, of an image (whole

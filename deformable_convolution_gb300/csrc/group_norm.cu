@@ -105,9 +105,8 @@ bool plan_rows(const NormArgs& a, bool backward, int planes, NormPlan* p) {
     const int threads = 32 * r.warps;
     r.step_c = threads / vr;
     r.step_v = threads % vr;
-    r.held = (int)ceil_div_ll(r.span, threads);
     p->threads = threads * r.units;
-    p->smem = (size_t)16 * p->threads * r.held;
+    p->smem = (size_t)16 * p->threads * ceil_div_ll(r.span, threads);
   } else {
     const int per = 32 / s.lpr;
     const long long blks = ceil_div_ll(a.cpg, per), run = (long long)a.cpg * vr;
@@ -133,7 +132,6 @@ bool plan_rows(const NormArgs& a, bool backward, int planes, NormPlan* p) {
     if (r.blocks == 1)
       while (r.units * r.warps < 4 && groups / (2 * r.units) >= 4 * kSms) r.units *= 2;
     p->threads = 32 * r.warps * r.units;
-    r.held = r.rounds;
     p->smem = (size_t)r.rounds * r.units * r.warps * per * s.seg * 16 * planes;
     p->parts = s.parts;
   }

@@ -12,7 +12,7 @@
 // registers wait for the loads, and no barrier stands between a copy and its
 // use.  The loops over the vectors stay rolled: a block runs its code once,
 // and a body unrolled over the vectors costs more in instruction fetches than
-// it saves.  What does not fit is read again (from L2) for the results.
+// it saves.  A unit that no cluster holds goes to two launches (below).
 //
 // Measured on 8 x 256 x 56 x 56 bf16 with ReLU (launches alone, tensors in L2):
 // forward 6.7 us, backward with a float32 gradient 16.6 us, where the tensors'
@@ -282,11 +282,13 @@ __device__ __forceinline__ void task_apply(const Shape& s, const UnitTask<VEC, E
   }
 }
 
-template <typename T, bool EVEN, int ACT>
+// Rows that are no whole vectors.
+template <typename T, int ACT>
 __global__ void __launch_bounds__(kTeam, 2)
     fwd_nchw(Shape s, RowTeam tm, const T* x, const float* gamma, const float* beta, T* y,
              float* mean_out, float* rstd_out) {
   constexpr int VEC = VecOf<T>::n;
+  constexpr bool EVEN = false;
   extern __shared__ __align__(128) uint4 slots[];
   __shared__ float sm[3][256];
   if (tm.blocks > 1) cluster_arrive();
@@ -301,7 +303,7 @@ __global__ void __launch_bounds__(kTeam, 2)
   };
   uint4* mine = slots + first_slot(s);
   int open = 0;  // groups of copies under way: of kBatch vectors, or the task's last
-  for (int r = 0; r < tm.held; ++r) {
+  for (int r = 0; r < tm.rounds; ++r) {
     const Task k = task(r);
     const T* p = x + k.off + (long long)k.v0 * VEC;
     uint4* slot = mine + r * pitch;
@@ -314,11 +316,8 @@ __global__ void __launch_bounds__(kTeam, 2)
       copy_group();
     }
   }
-  // what is not held first: its loads go on behind the copies
   float n = 0.f, mean = 0.f, m2 = 0.f;
-  for (int r = tm.rounds - 1; r >= tm.held; --r)
-    task_stats<T, VEC, EVEN, false>(s, task(r), x, mine, open, n, mean, m2);
-  for (int r = 0; r < tm.held; ++r)
+  for (int r = 0; r < tm.rounds; ++r)
     task_stats<T, VEC, EVEN, true>(s, task(r), x, mine + r * pitch, open, n, mean, m2);
   const float2 st = unit_stats(s, tm, pl, sm, n, mean, m2);
   if (!pl.here) return;
@@ -329,10 +328,7 @@ __global__ void __launch_bounds__(kTeam, 2)
   for (int r = 0; r < tm.rounds; ++r) {
     const Task k = task(r);
     const float a = st.y * (gamma ? gamma[k.ch] : 1.f), b = beta ? beta[k.ch] : 0.f;
-    if (r < tm.held)
-      task_apply<T, VEC, EVEN, true, ACT>(s, k, x, y, mine + r * pitch, st.x, a, b);
-    else
-      task_apply<T, VEC, EVEN, false, ACT>(s, k, x, y, mine, st.x, a, b);
+    task_apply<T, VEC, EVEN, true, ACT>(s, k, x, y, mine + r * pitch, st.x, a, b);
   }
 }
 
@@ -356,8 +352,7 @@ __global__ void __launch_bounds__(kTeam, 2)
   int end = s.cpg * vr;  // (a unit of 2^30 vectors or more does not come here)
   if (end > (pl.rank + 1) * tm.span) end = (pl.rank + 1) * tm.span;
   if (!pl.here) end = 0;
-  const int mine_n = begin < end ? (end - begin + threads - 1) / threads : 0;  // vectors
-  const int held = mine_n < tm.held ? mine_n : tm.held;
+  const int held = begin < end ? (end - begin + threads - 1) / threads : 0;  // vectors
   const long long off = (long long)pl.unit * s.cpg * s.hw + (long long)begin * VEC;
   uint4* mine = slots + threadIdx.x;
   {
@@ -368,16 +363,10 @@ __global__ void __launch_bounds__(kTeam, 2)
       if (i % kBatch == kBatch - 1 || i == held - 1) copy_group();
     }
   }
+  // vector i of this thread lies in channel c, `at` vectors from its start
+  int c = begin / vr, at = begin - c * vr;
   float n = 0.f, mean = 0.f, m2 = 0.f;
   auto keep = [](int, Pairs<VEC>&, float) {};
-  // what is not held first: its loads go on behind the copies
-  for (int i = held; i < mine_n; i += kBatch) {
-    const int most = min(mine_n - i, kBatch);
-    add_batch<VEC, kBatch>(
-        most, most * VEC, n, mean, m2,
-        [&](int b, Pairs<VEC>& f) { load_vec<T, VEC>(x + off + (long long)(i + b) * step, f); },
-        keep);
-  }
   {
     const uint4* slot = mine;
     auto get = [&](int b, Pairs<VEC>& f) { take<T, VEC>(slot + b * blockDim.x, 0, f); };
@@ -397,11 +386,8 @@ __global__ void __launch_bounds__(kTeam, 2)
     if (mean_out) mean_out[pl.unit] = st.x;
     if (rstd_out) rstd_out[pl.unit] = st.y;
   }
-  // vector i of this thread lies in channel c, `at` vectors from its start
-  int c = begin / vr, at = begin - c * vr;
   const float* gm = gamma ? gamma + pl.ch0 : nullptr;
   const float* bt = beta ? beta + pl.ch0 : nullptr;
-  const T* p = x + off;
   T* to = y + off;
   auto apply = [&](Pairs<VEC>& f) {
     const float a = st.y * (gm ? gm[c] : 1.f), b = bt ? bt[c] : 0.f;
@@ -414,16 +400,10 @@ __global__ void __launch_bounds__(kTeam, 2)
     at += tm.step_v;
     if (at >= vr) at -= vr, ++c;
   };
-#pragma unroll 2
+#pragma unroll 4
   for (int i = 0; i < held; ++i) {
     Pairs<VEC> f;
     take<T, VEC>(mine + i * blockDim.x, 0, f);
-    apply(f);
-  }
-  p += (long long)held * step;
-  for (int i = held; i < mine_n; ++i, p += step) {
-    Pairs<VEC> f;
-    load_vec<T, VEC>(p, f);
     apply(f);
   }
 }
@@ -537,9 +517,9 @@ __global__ void __launch_bounds__(kTeam, 2)
     return r == 0 ? first : Task(s, pl.unit, pl.ch0, pl.task(tm, r), tasks);
   };
   uint4* mine = slots + first_slot(s);
-  uint4* mine_g = mine + (size_t)tm.held * pitch;
+  uint4* mine_g = mine + (size_t)tm.rounds * pitch;
   int open = 0;  // groups of copies under way: of two vectors, or the task's last
-  for (int r = 0; r < tm.held; ++r) {
+  for (int r = 0; r < tm.rounds; ++r) {
     const Task k = task(r);
     const long long off = k.off + (long long)k.v0 * VEC;
     const T* p = x + off;
@@ -562,19 +542,13 @@ __global__ void __launch_bounds__(kTeam, 2)
   }
   const float mu = pl.here ? mean[pl.unit] : 0.f, rs = pl.here ? rstd[pl.unit] : 0.f;
   float val[2] = {0.f, 0.f};
-  // (what is not held first: its loads go on behind the copies)
-  for (int q = 0; q < tm.rounds; ++q) {
-    const int r = q < tm.rounds - tm.held ? tm.held + q : q - (tm.rounds - tm.held);
+  for (int r = 0; r < tm.rounds; ++r) {
     const Task k = task(r);
     const float g = gamma ? gamma[k.ch] : 1.f, b = beta ? beta[k.ch] : 0.f;
     float2 sa = both(0.f), sb = both(0.f);
-    if (r < tm.held)
-      task_sums<T, TG, VEC, EVEN, true, KEEP, ACT>(s, k, x, gy, mine + r * pitch,
-                                                   mine_g + r * pitch * kG, pitch, open, mu, rs, g, b,
-                                                   sa, sb);
-    else
-      task_sums<T, TG, VEC, EVEN, false, KEEP, ACT>(s, k, x, gy, mine, mine_g, pitch, open, mu, rs,
-                                                    g, b, sa, sb);
+    task_sums<T, TG, VEC, EVEN, true, KEEP, ACT>(s, k, x, gy, mine + r * pitch,
+                                                 mine_g + r * pitch * kG, pitch, open, mu, rs, g, b,
+                                                 sa, sb);
     const float ra = row_sum(sa.x + sa.y, s.lpr), rb = row_sum(sb.x + sb.y, s.lpr);
     if (k.live && (threadIdx.x & (s.lpr - 1)) == 0) {
       part[(long long)k.part * s.n * s.c + k.row] = make_float2(ra, rb);
@@ -595,13 +569,9 @@ __global__ void __launch_bounds__(kTeam, 2)
   for (int r = 0; r < tm.rounds; ++r) {
     const Task k = task(r);
     const float g = gamma ? gamma[k.ch] : 1.f, b = beta ? beta[k.ch] : 0.f;
-    if (r < tm.held)
-      task_grads<T, TG, VEC, EVEN, true, KEEP, ACT>(s, k, x, gy, gx, mine + r * pitch,
-                                                    mine_g + r * pitch * kG, pitch, mu, rs, g,
-                                                    b, s1, s2);
-    else
-      task_grads<T, TG, VEC, EVEN, false, KEEP, ACT>(s, k, x, gy, gx, mine, mine_g, pitch, mu,
-                                                     rs, g, b, s1, s2);
+    task_grads<T, TG, VEC, EVEN, true, KEEP, ACT>(s, k, x, gy, gx, mine + r * pitch,
+                                                  mine_g + r * pitch * kG, pitch, mu, rs, g, b, s1,
+                                                  s2);
   }
 }
 
@@ -638,7 +608,7 @@ __global__ void __launch_bounds__(kTwo)
   pdl_release();
   const Place pl = loose_place(s, tm, unit0);
   float n = 0.f, mean = 0.f, m2 = 0.f;
-  if (EVEN) {
+  if constexpr (EVEN) {
     const BlockRun run(s.cpg, s.hw / VEC, tm.span, pl.rank);
     const int tid = threadIdx.x;
     const T* p = x + (long long)pl.unit * s.cpg * s.hw + (run.begin + tid) * VEC;
@@ -689,7 +659,7 @@ __global__ void __launch_bounds__(kTwo)
     if (mean_out) mean_out[pl.unit] = mu;
     if (rstd_out) rstd_out[pl.unit] = rs;
   }
-  if (EVEN) {
+  if constexpr (EVEN) {
     const int vr = s.hw / VEC;
     const BlockRun run(s.cpg, vr, tm.span, pl.rank);
     const long long begin = run.begin + threadIdx.x;
@@ -717,12 +687,13 @@ __global__ void __launch_bounds__(kTwo)
       p += kBatch * kTwo * VEC;
       to += kBatch * kTwo * VEC;
     }
-    return;
-  }
-  for (int r = 0; r < tm.rounds; ++r) {
-    const UnitTask<VEC, EVEN> k(s, pl.unit, pl.ch0, pl.task(tm, r), tm.tasks);
-    task_apply<T, VEC, EVEN, false, ACT>(s, k, x, y, nullptr, mu, rs * (gamma ? gamma[k.ch] : 1.f),
-                                         beta ? beta[k.ch] : 0.f);
+  } else {
+    for (int r = 0; r < tm.rounds; ++r) {
+      const UnitTask<VEC, EVEN> k(s, pl.unit, pl.ch0, pl.task(tm, r), tm.tasks);
+      task_apply<T, VEC, EVEN, false, ACT>(s, k, x, y, nullptr, mu,
+                                           rs * (gamma ? gamma[k.ch] : 1.f),
+                                           beta ? beta[k.ch] : 0.f);
+    }
   }
 }
 
@@ -871,8 +842,7 @@ cudaError_t launch_nchw(const NormPlan& p, const NormArgs& a, bool backward,
           return launch_team(kern, p, p.row.blocks, st, p.s, p.row, static_cast<const T*>(a.x),
                              a.gamma, a.beta, static_cast<T*>(a.y), a.mean, a.rstd);
         };
-        if (p.row.span) return go(fwd_flat<T, ACT>);
-        return a.hw % VecOf<T>::n ? go(fwd_nchw<T, false, ACT>) : go(fwd_nchw<T, true, ACT>);
+        return a.hw % VecOf<T>::n ? go(fwd_nchw<T, ACT>) : go(fwd_flat<T, ACT>);
       });
     });
   return by_dtypes(a, [&](auto t, auto g) {

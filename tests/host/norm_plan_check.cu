@@ -5,7 +5,9 @@
 //    vectors in order and exactly once, up to the largest sizes accepted;
 //  * a kernel's limit of dynamic shared memory is set to one value whatever the
 //    problem (host threads that launch a kernel at the same time cannot lower it
-//    under one another), and every launch stays within it.
+//    under one another), and every launch stays within it;
+//  * a cluster's blocks on [n][c][h][w] have a slot for every vector they take,
+//    and take all of their unit's.
 #include <cuda_runtime.h>
 
 #include <set>
@@ -46,7 +48,7 @@ cudaError_t launch_two_nhwc(const NormPlan&, const NormArgs&, bool, bool, int, i
 
 using namespace dc;
 
-static long long failures = 0, runs = 0, wide = 0;
+static long long failures = 0, runs = 0, wide = 0, held = 0;
 #define CHECK(cond, ...)                  \
   do {                                    \
     if (!(cond)) {                        \
@@ -105,11 +107,34 @@ static void check_smem(const NormArgs& a, const NormPlan& p) {
   CHECK(launched_smem == p.smem, "%zu bytes planned, %zu launched", p.smem, launched_smem);
 }
 
+static void check_slots(const NormArgs& a, const NormPlan& p, bool backward) {
+  const RowTeam& r = p.row;
+  const int vec = a.dt == DC_BF16 ? 8 : 4, threads = 32 * r.warps;
+  const bool wide = keep_dz(a.gdt == DC_F32, a.act == DC_ACT_SILU || a.act == DC_ACT_GELU);
+  const int planes = 1 + (backward ? (wide && a.dt == DC_BF16 ? 2 : 1) : 0);
+  const long long slots = (long long)p.smem / 16 / planes;
+  CHECK(p.threads == threads * r.units && p.threads <= kTeam, "%d threads", p.threads);
+  CHECK((r.span != 0) == (!backward && a.hw % vec == 0), "hw %d: span %d", a.hw, r.span);
+  if (r.span) {
+    CHECK((long long)r.span * r.blocks >= (long long)a.cpg * (a.hw / vec), "span %d", r.span);
+    CHECK(ceil_div_ll(r.span, threads) * p.threads <= slots, "hw %d: %lld slots", a.hw, slots);
+  } else {
+    const int per = 32 / p.s.lpr, vr = row_vectors(a.hw, a.hw % vec ? vec - 1 : 0, vec);
+    CHECK((long long)p.s.seg * p.s.parts >= vr, "hw %d: segments", a.hw);
+    CHECK((long long)r.rounds * r.blocks * r.warps >= r.tasks &&
+              (long long)r.tasks * per >= (long long)a.cpg * p.s.parts, "hw %d: %d tasks", a.hw, r.tasks);
+    CHECK((long long)r.rounds * r.warps * r.units * per * p.s.seg <= slots, "hw %d: %lld slots",
+          a.hw, slots);
+  }
+  ++held;
+}
+
 static void check(const NormArgs& a) {
   if (!norm_supported(a)) return;
   for (int backward = 0; backward < 2; ++backward) {
     const NormPlan p = make_plan(a, backward != 0);
     if (!p.cluster && !a.nhwc && !backward) check_runs(a, p);
+    if (p.cluster && !a.nhwc) check_slots(a, p, backward != 0);
     check_smem(a, p);
   }
 }
@@ -138,6 +163,7 @@ int main() {
   CHECK(limits.size() == 1 && *limits.begin() <= (227 - 8) * 1024, "%zu limits, the largest %d",
         limits.size(), *limits.rbegin());
   CHECK(most_smem <= (size_t)*limits.begin(), "%zu bytes launched", most_smem);
-  printf("%lld sizes in runs, %lld of them past 32 bits, %lld failures\n", runs, wide, failures);
-  return failures || runs < 1000 || wide < 100;
+  printf("%lld sizes in runs, %lld of them past 32 bits, %lld held by clusters, %lld failures\n", runs,
+         wide, held, failures);
+  return failures || runs < 1000 || wide < 100 || held < 1000;
 }

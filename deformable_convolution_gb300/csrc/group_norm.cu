@@ -40,10 +40,11 @@ __global__ void __launch_bounds__(1024)
 // ---------------------------------------------------------------- the plan
 
 // A call is one launch of clusters that hold their units on the chip, or, for
-// units over kMaxCluster * kBlockBytes (and where plan_cols says so), two
-// launches that read their inputs twice.  us of clusters / two launches:
-// forward 32 x 256 x 56 x 56 bf16 ReLU 24.0 / 27.5, 16 x 100 x 168 x 256 SiLU
-// 69 / 75, backward 8 x 256 x 56 x 56 with a float32 gradient 20.8 / 22.8.
+// units over kMaxCluster * kBlockBytes (and where plan_rows or plan_cols says
+// so), two launches that read their inputs twice.  us of clusters / two
+// launches, inputs out of L2: forward 32 x 256 x 56 x 56 bf16 ReLU 23.5 / 27.4,
+// 16 x 100 x 168 x 256 SiLU 69 / 74, backward 8 x 256 x 56 x 56 ReLU with a
+// float32 gradient 19.6 / 23.3.
 constexpr int kSms = 152;
 // Most of a unit in a cluster's block: two blocks to an SM (with 50 KB, four to
 // an SM, that backward took a tenth longer).
@@ -85,7 +86,18 @@ Shape make_shape(const NormArgs& a) {
   return s;
 }
 
-// A cluster that holds the unit; false where it does not fit one.
+// Of a pass's inputs, left in L2 (129 MB) between two launches: 64 MB, which
+// makes a turn of every image, took 61 us where 96 MB take 43 (forward on
+// 2 x 200 x 336 x 256 bf16).
+constexpr double kImagesBytes = 96e6;
+// What a pass reads of an image.
+double image_bytes(const NormArgs& a, bool backward) {
+  const int elt = a.dt == DC_BF16 ? 2 : 4, gelt = a.gdt == DC_F32 ? 4 : 2;
+  return (double)a.c * a.hw * (elt + (backward ? gelt : 0));
+}
+
+// A cluster that holds the unit; false where it does not fit one, or where two
+// launches are faster.
 bool plan_rows(const NormArgs& a, bool backward, int planes, NormPlan* p) {
   Shape& s = p->s;
   RowTeam& r = p->row;
@@ -137,15 +149,20 @@ bool plan_rows(const NormArgs& a, bool backward, int planes, NormPlan* p) {
   }
   p->blocks = (unsigned)(ceil_div_ll(groups, r.units) * r.blocks);
   // As in plan_cols, but with less to gain: us of a bf16 SiLU backward on
-  // h x w x 256, clusters / two launches: 8 x 56 x 56 (512 blocks) 20 / 21,
-  // 16 x 56 x 56 (1024) 37 / 27, 4 x 112 x 112 41 / 27, 16 x 112 x 112
-  // 135 / 127; but with units of one block (64 x 28 x 28) 28 / 34, with rows of
-  // a vector a lane (64 x 14 x 14 x 1024 in 8 groups) 70 / 78, and for
-  // 16 x 112 x 112 under ReLU 93 / 104, GELU 140 / 165 (its slope is worked out
-  // twice).  With float32 gradients 16 x 56 x 56, 4 x 112 x 112, 16 x 112 x 112
-  // take 41 / 39, 46 / 39, 150 / 149 under SiLU, 38 / 32, 42 / 32, 138 / 128
-  // under ReLU.
-  const bool gains = a.act == DC_ACT_SILU || (a.gdt == DC_F32 && a.act != DC_ACT_GELU);
+  // h x w x 256, clusters / two launches: 8 x 56 x 56 (512 blocks) 19 / 21,
+  // 16 x 56 x 56 (1024) 36 / 27, 24 x 56 x 56 47 / 39, 48 x 56 x 56 84 / 77,
+  // 4 x 112 x 112 39 / 27, 16 x 112 x 112 126 / 127; but with units of one block
+  // (64 x 28 x 28) 26 / 34, with rows of a vector a lane (64 x 14 x 14 x 1024 in
+  // 8 groups) 60 / 78.  ReLU gains where all is one turn and loses in several
+  // (18 x 56 x 56 27 / 25, 4 x 112 x 112 29 / 24, 24 x 56 x 56 32 / 35,
+  // 16 x 112 x 112 87 / 104) and stays with clusters, as does GELU, whose slope
+  // is worked out twice (131 / 164).  With float32 gradients one turn under
+  // SiLU, ReLU: 12 x 56 x 56 30 / 35, 28 / 28; 16 x 56 x 56 38 / 39, 35 / 32;
+  // 4 x 112 x 112 42 / 39, 38 / 32; several, which read past L2 through
+  // registers: 20 x 56 x 56 44 / 66, 41 / 50; 48 x 56 x 56 88 / 113, 81 / 97;
+  // 16 x 112 x 112 134 / 149, 121 / 128; 32 x 64 x 64 x 320 95 / 192, 87 / 141.
+  const bool gains = a.gdt == DC_F32 ? a.act != DC_ACT_GELU && image_bytes(a, true) * a.n <= kImagesBytes
+                                     : a.act == DC_ACT_SILU;
   return !(backward && a.dt == DC_BF16 && gains && r.blocks > 1 && vr >= 256 &&
            p->blocks > 4 * kSms);
 }
@@ -212,11 +229,6 @@ bool plan_cols(const NormArgs& a, bool backward, bool keep, NormPlan* p) {
   return !(backward && gains && p->blocks > 3 * kSms);
 }
 
-// Of a pass's inputs, left in L2 (129 MB) between two launches: 64 MB, which
-// makes a turn of every image, took 61 us where 96 MB take 43 (forward on
-// 2 x 200 x 336 x 256 bf16).
-constexpr double kImagesBytes = 96e6;
-
 // Two launches: blocks of a unit, `vectors` of it in all, as many as an SM runs
 // at once (`per_sm`; a third more of them wait for a whole turn, 43 us become
 // 51 on the forward of 2 x 200 x 336 x 256).
@@ -231,8 +243,7 @@ void plan_two(const NormArgs& a, bool backward, int planes, NormPlan* p) {
   Shape& s = p->s;
   const int vec = a.dt == DC_BF16 ? 8 : 4, elt = a.dt == DC_BF16 ? 2 : 4;
   const int gelt = a.gdt == DC_F32 ? 4 : 2;
-  const double image = (double)a.c * a.hw * (elt + (backward ? gelt : 0));
-  const double images = kImagesBytes / image;
+  const double images = kImagesBytes / image_bytes(a, backward);
   p->images = images < 1 ? 1 : images >= a.n ? a.n : (int)images;
   // as many at a time in every turn
   p->images = (int)ceil_div_ll(a.n, ceil_div_ll(a.n, p->images));

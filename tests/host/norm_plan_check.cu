@@ -146,6 +146,13 @@ int main() {
   check(make_args(1, 1, 24, 1LL << 30, DC_BF16, DC_BF16, false, DC_ACT_SILU));
   check(make_args(1, 1, 1024, 1LL << 30, DC_BF16, DC_BF16, false, DC_ACT_NONE));
   check(make_args(2, 3, 1 << 16, 1 << 20, DC_F32, DC_F32, false, DC_ACT_RELU));
+  // a bf16 backward with a float32 gradient reads its inputs twice only where
+  // L2 holds all of them
+  for (const int n : {16, 18, 20, 48})
+    for (const int act : {DC_ACT_RELU, DC_ACT_SILU}) {
+      const NormArgs a = make_args(n, 32, 8, 56 * 56, DC_BF16, DC_F32, false, act);
+      CHECK(make_plan(a, true).cluster == (n > 19), "%d images", n);
+    }
   std::mt19937_64 rng(1);
   auto spread = [&](double lo, double hi) {
     return (long long)std::lround(

@@ -168,9 +168,12 @@ __device__ __forceinline__ float2 sigmoid2(float2 z) {
 }
 
 // The normal distribution's Phi(z), and e = exp(-z^2 / 2): Abramowitz and
-// Stegun's rational approximation 7.1.26 of erf (absolute error 1.5e-7, two
-// and a half units of float32 at 1) at |z| / sqrt 2; it needs e anyway, as
-// the slope does.
+// Stegun's rational approximation 7.1.26 of erf (absolute error 1.5e-7) at
+// |z| / sqrt 2; it needs e anyway, as the slope does.  z Phi(z) measured on
+// 2^19 values in [-9, 9], largest error over a range of z against that of
+// 0.5 z (1 + erf) in float32: [-5, -4] 5.9e-8 / 1.2e-7, [-4, -2] 2.1e-7 /
+// 2.6e-7, [-2, -1] 1.5e-7 / 1.8e-7, [-1, 1] 1.5e-7 / 1.4e-7, [2, 9] 4.2e-7 /
+// 4.7e-7; the slope 3e-7 anywhere.
 __device__ __forceinline__ float2 normal_cdf2(float2 z, float2* e) {
   const float2 a = make_float2(fabsf(z.x), fabsf(z.y));
   const float2 u = fma2(a, both(0.3275911f * 0.70710678118654752f), both(1.f));

@@ -432,3 +432,19 @@ def test_a_channel_at_minus_infinity_passes_its_gradient_without_an_activation(s
     assert (cut == -float("inf")).all()
     g = B.group_norm_backward(p, x, gamma, beta, mean, rstd, gy)
     assert all(torch.equal(g[k], want[k]) for k in want)
+
+
+@on_gpu
+@pytest.mark.parametrize("layout", (B.DC_NCHW, B.DC_NHWC))
+@pytest.mark.parametrize("value", (float("nan"), float("inf"), -float("inf")))
+@pytest.mark.parametrize("shape", NOT_FINITE_SHAPES)
+def test_statistics_of_a_group_that_is_not_finite_are_nan(shape, value, layout):
+    n, c, h, w, groups = shape
+    p = B.NormProblem(n, c, h, w, groups, B.DC_F32, layout, B.DC_ACT_RELU)
+    x = inputs(p, 33)[0].cuda()
+    x.view(-1)[0] = value  # of the first image's first group
+    y, mean, rstd = B.group_norm(p, x)
+    bad = torch.zeros(n, groups, dtype=torch.bool, device="cuda")
+    bad[0, 0] = True
+    assert torch.equal(torch.isnan(mean), bad) and torch.equal(torch.isnan(rstd), bad)
+    assert int(torch.isnan(y).sum()) == y.numel() // (n * groups)

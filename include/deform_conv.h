@@ -351,9 +351,10 @@ dc_status dc_group_norm_workspace_size(const dc_norm_problem* prob, int backward
  *                backward needs them)
  *   y            may be x itself
  * All arithmetic is float32; a bf16 y is rounded to nearest even.  A value
- * that is not finite makes its group's mean, rstd and y NaN.  GELU's largest error as measured, beside that of z: 2.5e-7 for z
- * below 2 (6e-8 below -4, 2.3e-9 below -5) and 1.6e-7 * y above; 3e-7 in its
- * slope.  The sums run in a fixed order: the same inputs give the same bits. */
+ * that is not finite makes its group's mean, rstd and y NaN.  GELU's largest
+ * error as measured, beside that of z: 2.5e-7 for z below 2 (6e-8 below -4,
+ * 2.3e-9 below -5) and 1.6e-7 * y above; 3e-7 in its slope.  The sums run in a
+ * fixed order: the same inputs give the same bits. */
 dc_status dc_group_norm_fwd(const dc_norm_problem* prob, const void* x, const float* gamma,
                             const float* beta, void* y, float* mean, float* rstd, void* ws,
                             size_t ws_bytes, void* stream);

@@ -29,10 +29,16 @@ EXPORTED_SYMBOLS = (
     "dc_col_layout", "dc_sample_tile", "dc_selftest_wait_timeout", "dc_test_fail_launches",
     "dc_group_norm_workspace_size", "dc_group_norm_fwd", "dc_group_norm_bwd",
     "dc_adamw_step", "dc_adamw_state_values", "dc_grad_norm_workspace_size", "dc_grad_norm",
+    "dc_fp8_sizes", "dc_fp8_quantize", "dc_fp8_values", "dc_fp8_matmul_workspace_size",
+    "dc_fp8_matmul", "dc_orthogonalize_workspace_size", "dc_orthogonalize",
+    "dc_muon_workspace_size", "dc_muon_step",
 )
 DC_NCHW, DC_NHWC = 0, 1
 DC_ACT_NONE, DC_ACT_RELU, DC_ACT_SILU, DC_ACT_GELU = range(4)
 DC_STATE_F32, DC_STATE_Q8 = 0, 1
+DC_E4M3, DC_E5M2 = 0, 1
+DC_ORTHO_16, DC_ORTHO_32 = 0, 1
+FP8_BLOCK = 128    # values that share a scale
 STATE_BLOCK = 256  # elements of an 8-bit state that share a scale
 DC_COL_PLANE_MAJOR, DC_COL_PIXEL_MAJOR = 0, 1
 MARGIN_BINS = 64
@@ -66,6 +72,36 @@ class DcAdamwHyper(ctypes.Structure):
     """Mirror of ``dc_adamw_hyper``."""
     _fields_ = [(name, ctypes.c_double) for name in ("lr", "beta1", "beta2", "eps")] + \
         [("step", ctypes.c_longlong)]
+
+
+class DcFp8Problem(ctypes.Structure):
+    """Mirror of ``dc_fp8_problem``."""
+    _fields_ = [(name, ctypes.c_int) for name in ("batch", "rows", "cols", "dtype", "format", "square")]
+
+
+class DcFp8Product(ctypes.Structure):
+    """Mirror of ``dc_fp8_product``."""
+    _fields_ = [(name, ctypes.c_int) for name in (
+        "batch", "m", "n", "k", "a_format", "b_format", "a_shared", "b_shared", "sum", "out")]
+
+
+class DcMatrix(ctypes.Structure):
+    """Mirror of ``dc_matrix``."""
+    _fields_ = [("in_", ctypes.c_void_p), ("out", ctypes.c_void_p)] + \
+        [(name, ctypes.c_int) for name in ("rows", "cols", "in_dtype", "out_dtype")]
+
+
+class DcMuonTensor(ctypes.Structure):
+    """Mirror of ``dc_muon_tensor``."""
+    _fields_ = [(name, ctypes.c_void_p) for name in ("param", "master", "grad", "m")] + \
+        [(name, ctypes.c_int) for name in ("rows", "cols", "param_dtype", "grad_dtype")] + \
+        [("weight_decay", ctypes.c_float), ("rate", ctypes.c_float)]
+
+
+class DcMuonHyper(ctypes.Structure):
+    """Mirror of ``dc_muon_hyper``."""
+    _fields_ = [("lr", ctypes.c_double), ("momentum", ctypes.c_double)] + \
+        [(name, ctypes.c_int) for name in ("nesterov", "steps", "precision")]
 
 
 class DcError(RuntimeError):
@@ -146,6 +182,17 @@ def lib() -> ctypes.CDLL:
     L.dc_grad_norm_workspace_size.restype = i
     L.dc_grad_norm.argtypes = [pt, i, ctypes.c_float, vp, vp, vp, sz, vp]
     L.dc_grad_norm.restype = i
+    pq, pm = ctypes.POINTER(DcFp8Problem), ctypes.POINTER(DcFp8Product)
+    po, pw, ps = ctypes.POINTER(DcMatrix), ctypes.POINTER(DcMuonTensor), ctypes.POINTER(sz)
+    for name, types in dict(
+            dc_fp8_sizes=[pq, i, ps, ps], dc_fp8_quantize=[pq, vp, vp, vp, vp, vp, vp],
+            dc_fp8_values=[pq, i, vp, vp, vp, vp], dc_fp8_matmul_workspace_size=[pm, ps],
+            dc_fp8_matmul=[pm, vp, vp, vp, vp, vp, vp, sz, vp],
+            dc_orthogonalize_workspace_size=[po, i, ps],
+            dc_orthogonalize=[po, i, i, i, vp, sz, vp], dc_muon_workspace_size=[pw, i, ps],
+            dc_muon_step=[pw, i, ctypes.POINTER(DcMuonHyper), vp, vp, vp, sz, vp]).items():
+        f = getattr(L, name)
+        f.argtypes, f.restype = types, i
     L.dc_launch_count.argtypes = []
     L.dc_launch_count.restype = ctypes.c_ulonglong
     _configured = L
@@ -664,6 +711,222 @@ def dc_grad_norm(tensors, count: int, max_norm: float, norm=None, scale=None, ws
                                 _scalar(scale, "scale"), ws_ptr, ws_bytes, _raw_stream(stream))
     if status:
         raise DcError(status, "dc_grad_norm")
+
+
+# ---------------------------------------------------------------- matrices in 8 bits
+
+@dataclass(frozen=True)
+class Fp8Problem:
+    """``batch`` matrices [rows, cols] of ``dtype`` values to be held as 8-bit
+    codes with a scale for each run of 128 columns (square: for each block of
+    128 x 128).  Codes are uint8 tensors [batch, rows, cols rounded up to 128],
+    scales flat uint8 tensors."""
+    batch: int
+    rows: int
+    cols: int
+    dtype: int = DC_BF16
+    format: int = DC_E4M3
+    square: int = 0
+
+    @cached_property
+    def _as_parameter_(self):
+        return ctypes.byref(DcFp8Problem(self.batch, self.rows, self.cols, self.dtype, self.format,
+                                         self.square))
+
+    @cached_property
+    def torch_dtype(self):
+        return _TORCH_DTYPE[self.dtype]
+
+    @cached_property
+    def shape(self):
+        """Of x."""
+        return (self.batch, self.rows, self.cols)
+
+    def _shapes(self, transposed):
+        r, c = (self.cols, self.rows) if transposed else (self.rows, self.cols)
+        nbytes = dc_fp8_sizes(self, transposed)
+        return (self.batch, r, -(-c // FP8_BLOCK) * FP8_BLOCK), (nbytes[1],)
+
+    @cached_property
+    def shapes(self):
+        """Of codes and scales."""
+        return self._shapes(False)
+
+    @cached_property
+    def shapes_t(self):
+        """Of the transposes' codes and scales."""
+        return self._shapes(True)
+
+
+@dataclass(frozen=True)
+class Fp8Product:
+    """D[i] = A[i] B[i]^T for matrices in 8 bits, A[i] [m, k], B[i] [n, k]
+    (``Fp8Problem``s with cols = k); a_shared, b_shared: one matrix for all i;
+    sum: D is the sum over i.  out: D's type."""
+    batch: int
+    m: int
+    n: int
+    k: int
+    a_format: int = DC_E4M3
+    b_format: int = DC_E4M3
+    a_shared: int = 0
+    b_shared: int = 0
+    sum: int = 0
+    out: int = DC_BF16
+
+    @cached_property
+    def _as_parameter_(self):
+        return ctypes.byref(DcFp8Product(self.batch, self.m, self.n, self.k, self.a_format,
+                                         self.b_format, self.a_shared, self.b_shared, self.sum,
+                                         self.out))
+
+    @cached_property
+    def torch_dtype(self):
+        return _TORCH_DTYPE[self.out]
+
+    @cached_property
+    def shape(self):
+        """Of D."""
+        return (self.m, self.n) if self.sum else (self.batch, self.m, self.n)
+
+    def _operand(self, shared, rows):
+        p = Fp8Problem(1 if shared else self.batch, rows, max(self.k, 1))
+        return p.shapes
+
+    @cached_property
+    def a_shapes(self):
+        """Of A's codes and scales."""
+        return self._operand(self.a_shared, self.m)
+
+    @cached_property
+    def b_shapes(self):
+        return self._operand(self.b_shared, self.n)
+
+
+def dc_fp8_sizes(p: Fp8Problem, transposed: bool):
+    """(bytes of codes, bytes of scales)."""
+    codes, scales = ctypes.c_size_t(0), ctypes.c_size_t(0)
+    _check(lib().dc_fp8_sizes(p, 1 if transposed else 0, ctypes.byref(codes), ctypes.byref(scales)),
+           "dc_fp8_sizes")
+    return int(codes.value), int(scales.value)
+
+
+def _codes(codes, scales, shapes, name, optional=False):
+    return (_arg(codes, name, shapes[0], torch.uint8, optional),
+            _arg(scales, f"{name}'s scales", shapes[1], torch.uint8, optional))
+
+
+def dc_fp8_quantize(p: Fp8Problem, x, codes=None, scales=None, codes_t=None, scales_t=None,
+                    stream=None):
+    """x's codes and scales and, from the same read, its transposes'; either
+    pair may be None."""
+    status = lib().dc_fp8_quantize(
+        p, _arg(x, "x", p.shape, p.torch_dtype), *_codes(codes, scales, p.shapes, "codes", True),
+        *_codes(codes_t, scales_t, p.shapes_t, "codes_t", True), _raw_stream(stream))
+    if status:
+        raise DcError(status, "dc_fp8_quantize")
+
+
+def dc_fp8_values(p: Fp8Problem, codes, scales, out, transposed=False, stream=None):
+    """out: the float32 values that codes stand for (transposed: codes_t's)."""
+    shape = (p.batch, p.cols, p.rows) if transposed else p.shape
+    status = lib().dc_fp8_values(
+        p, 1 if transposed else 0,
+        *_codes(codes, scales, p.shapes_t if transposed else p.shapes, "codes"),
+        _arg(out, "out", shape, torch.float32), _raw_stream(stream))
+    if status:
+        raise DcError(status, "dc_fp8_values")
+
+
+def dc_fp8_matmul_workspace_size(p: Fp8Product) -> int:
+    out = ctypes.c_size_t(0)
+    _check(lib().dc_fp8_matmul_workspace_size(p, ctypes.byref(out)), "dc_fp8_matmul_workspace_size")
+    return int(out.value)
+
+
+def dc_fp8_matmul(p: Fp8Product, a, a_scales, b, b_scales, d, ws=None, stream=None):
+    """d[i] = a[i] b[i]^T (their sum over i where ``p.sum``)."""
+    ws_ptr, ws_bytes = _ws(ws)
+    status = lib().dc_fp8_matmul(
+        p, *_codes(a, a_scales, p.a_shapes, "a"), *_codes(b, b_scales, p.b_shapes, "b"),
+        _arg(d, "d", p.shape, p.torch_dtype), ws_ptr, ws_bytes, _raw_stream(stream))
+    if status:
+        raise DcError(status, "dc_fp8_matmul")
+
+
+# ---------------------------------------------------------------- Muon
+
+def _matrix_shape(t, name):
+    """A weight as a matrix: its first dimension by all others."""
+    if t.dim() < 2:
+        raise ValueError(f"{name} must have two dimensions or more")
+    rows = t.shape[0]
+    return rows, (t.numel() // rows if rows else 0)
+
+
+def matrices(ins, outs):
+    """A host array of ``dc_matrix`` from input and output tensors of equal
+    shapes (the first dimension by all others).  The array holds plain
+    pointers: the caller keeps the tensors."""
+    if len(ins) != len(outs):
+        raise ValueError(f"{len(ins)} inputs and {len(outs)} outputs")
+    table = (DcMatrix * max(len(ins), 1))()
+    for k, (t, a, b) in enumerate(zip(table, ins, outs)):
+        t.rows, t.cols = _matrix_shape(a, f"in[{k}]")
+        t.in_, t.in_dtype = _addr(a, f"in[{k}]"), _dc_dtype(a)
+        t.out, t.out_dtype = _addr(b, f"out[{k}]", tuple(a.shape)), _dc_dtype(b)
+    return table
+
+
+def muon_tensors(entries):
+    """A host array of ``dc_muon_tensor`` from dicts of tensors: param, grad, m,
+    and optionally master, weight_decay, rate.  The array holds plain pointers:
+    the caller keeps the tensors."""
+    table = (DcMuonTensor * max(len(entries), 1))()
+    for t, q in zip(table, entries):
+        shape = tuple(q["param"].shape)
+        t.rows, t.cols = _matrix_shape(q["param"], "param")
+        t.param, t.param_dtype = _addr(q["param"], "param"), _dc_dtype(q["param"])
+        t.master = _addr(q.get("master"), "master", shape, torch.float32)
+        if q.get("grad") is None:
+            raise ValueError("grad is required")
+        t.grad, t.grad_dtype = _addr(q["grad"], "grad", shape), _dc_dtype(q["grad"])
+        t.m = _addr(q["m"], "m", shape, torch.float32)
+        t.weight_decay, t.rate = q.get("weight_decay", 0.0), q.get("rate", 1.0)
+    return table
+
+
+def dc_orthogonalize_workspace_size(table, count: int) -> int:
+    out = ctypes.c_size_t(0)
+    _check(lib().dc_orthogonalize_workspace_size(table, count, ctypes.byref(out)),
+           "dc_orthogonalize_workspace_size")
+    return int(out.value)
+
+
+def dc_orthogonalize(table, count: int, steps: int, precision: int, ws=None, stream=None):
+    """Orthogonalises the matrices of ``table`` (``matrices``)."""
+    ws_ptr, ws_bytes = _ws(ws)
+    status = lib().dc_orthogonalize(table, count, steps, precision, ws_ptr, ws_bytes,
+                                    _raw_stream(stream))
+    if status:
+        raise DcError(status, "dc_orthogonalize")
+
+
+def dc_muon_workspace_size(table, count: int) -> int:
+    out = ctypes.c_size_t(0)
+    _check(lib().dc_muon_workspace_size(table, count, ctypes.byref(out)), "dc_muon_workspace_size")
+    return int(out.value)
+
+
+def dc_muon_step(table, count: int, hyper: DcMuonHyper, grad_scale=None, lr=None, ws=None,
+                 stream=None):
+    """One Muon step over ``table`` (``muon_tensors``).  grad_scale, lr: float32
+    device scalars or None."""
+    ws_ptr, ws_bytes = _ws(ws)
+    status = lib().dc_muon_step(table, count, hyper, _scalar(grad_scale, "grad_scale"),
+                                _scalar(lr, "lr"), ws_ptr, ws_bytes, _raw_stream(stream))
+    if status:
+        raise DcError(status, "dc_muon_step")
 
 
 # ---------------------------------------------------------------- conveniences

@@ -19,6 +19,8 @@
 #include <mutex>
 
 #include "dc_common.cuh"
+#include "fp8.cuh"
+#include "muon.cuh"
 
 namespace dc {
 
@@ -986,6 +988,308 @@ dc_status dc_grad_norm(const dc_adamw_tensor* tensors, int count, float max_norm
   return cuda_status(timed("grad_norm", s, [&] {
     return launch_grad_norm(part, parts, max_norm, norm, scale, s);
   }));
+}
+
+}  // extern "C"
+
+// ---------------------------------------------------------------- matrices of a training step
+
+namespace dc {
+namespace {
+
+constexpr int kFp8MaxSide = 1 << 24, kFp8MaxBatch = 65535;
+
+bool dtype_known(dc_dtype d) { return d == DC_F32 || d == DC_BF16; }
+bool fp8_known(dc_fp8 f) { return f == DC_E4M3 || f == DC_E5M2; }
+
+dc_status check_fp8(const dc_fp8_problem* p) {
+  if (!p || p->batch < 0 || p->rows <= 0 || p->cols <= 0 || !dtype_known(p->dtype) ||
+      !fp8_known(p->format) || (p->square != 0 && p->square != 1))
+    return DC_ERR_INVALID_ARG;
+  if (p->rows > kFp8MaxSide || p->cols > kFp8MaxSide || p->batch > kFp8MaxBatch ||
+      (long long)p->rows * p->cols > (1LL << 40) / (p->batch ? p->batch : 1))
+    return DC_ERR_UNSUPPORTED;
+  return DC_OK;
+}
+
+dc_status check_product(const dc_fp8_product* p) {
+  if (!p || p->batch < 0 || p->m <= 0 || p->n <= 0 || p->k < 0 || !fp8_known(p->a_format) ||
+      !fp8_known(p->b_format) || !dtype_known(p->out))
+    return DC_ERR_INVALID_ARG;
+  for (int flag : {p->a_shared, p->b_shared, p->sum})
+    if (flag != 0 && flag != 1) return DC_ERR_INVALID_ARG;
+  if (p->m > kFp8MaxSide || p->n > kFp8MaxSide || p->k > kFp8MaxSide || p->batch > kFp8MaxBatch)
+    return DC_ERR_UNSUPPORTED;
+  return DC_OK;
+}
+
+// Sizes of a matrix to be orthogonalised.
+dc_status check_sides(int rows, int cols) {
+  if (rows < 0 || cols < 0) return DC_ERR_INVALID_ARG;
+  if ((rows < cols ? rows : cols) > 16384 || (rows < cols ? cols : rows) > (1 << 22))
+    return DC_ERR_UNSUPPORTED;
+  return DC_OK;
+}
+
+dc_status check_matrix(const dc_matrix& t) {
+  const dc_status st = check_sides(t.rows, t.cols);
+  if (st != DC_OK) return st;
+  if (!dtype_known(t.in_dtype) || !dtype_known(t.out_dtype)) return DC_ERR_INVALID_ARG;
+  if (t.rows == 0 || t.cols == 0) return DC_OK;
+  if (!t.in || !t.out) return DC_ERR_INVALID_ARG;
+  if (!aligned_to(t.in, elt_size(t.in_dtype)) || !aligned_to(t.out, elt_size(t.out_dtype)))
+    return DC_ERR_UNSUPPORTED;
+  return DC_OK;
+}
+
+dc_status check_weight(const dc_muon_tensor& t) {
+  const dc_status st = check_sides(t.rows, t.cols);
+  if (st != DC_OK) return st;
+  if (!dtype_known(t.param_dtype) || !dtype_known(t.grad_dtype)) return DC_ERR_INVALID_ARG;
+  if (t.master && t.param_dtype != DC_BF16) return DC_ERR_INVALID_ARG;
+  if (!(t.weight_decay >= 0.f) || t.weight_decay > FLT_MAX || !(fabsf(t.rate) <= FLT_MAX))
+    return DC_ERR_INVALID_ARG;
+  if (t.rows == 0 || t.cols == 0) return DC_OK;
+  if (!t.param || !t.grad || !t.m) return DC_ERR_INVALID_ARG;
+  if (!aligned_to(t.param, elt_size(t.param_dtype)) || !aligned_to(t.master, 4) ||
+      !aligned_to(t.grad, elt_size(t.grad_dtype)) || !aligned_to(t.m, 4))
+    return DC_ERR_UNSUPPORTED;
+  return DC_OK;
+}
+
+// Appends a matrix to the group, its storage at *at bytes into ws (null: only counted).
+void add_matrix(MuonGroup* g, int rows, int cols, char* ws, size_t* at) {
+  MuonMat& t = g->mat[g->count++];
+  t.rows = rows;
+  t.cols = cols;
+  t.ld = (cols + 7) / 8 * 8;
+  t.tall = rows > cols;
+  t.side = t.tall ? cols : rows;
+  t.lds = (t.side + 7) / 8 * 8;
+  auto take = [&](size_t bytes) {
+    char* p = ws ? ws + *at : nullptr;
+    *at += (bytes + 255) / 256 * 256;
+    return p;
+  };
+  for (int i = 0; i < 2; ++i) t.x[i] = reinterpret_cast<__half*>(take(4 * (size_t)muon_x_low(t)));
+  t.gram = reinterpret_cast<__half*>(take(4 * (size_t)muon_p_low(t)));
+  t.poly = reinterpret_cast<__half*>(take(4 * (size_t)muon_p_low(t)));
+  t.part = reinterpret_cast<float*>(take(kMuonParts * sizeof(float)));
+}
+
+// Workspace of `count` matrices of the sizes size(i): that of the largest group.
+template <typename F>
+size_t muon_bytes(int count, F&& size) {
+  size_t most = 0, at = 0;
+  MuonGroup g;
+  g.count = 0;
+  for (int i = 0; i < count; ++i) {
+    int rows, cols;
+    size(i, &rows, &cols);
+    if (rows == 0 || cols == 0) continue;
+    if (g.count == kMuonMats) g.count = 0, at = 0;
+    add_matrix(&g, rows, cols, nullptr, &at);
+    if (at > most) most = at;
+  }
+  return most;
+}
+
+// The group's launches.
+dc_status run_muon(MuonGroup& g, cudaStream_t s) {
+  if (g.count == 0) return DC_OK;
+  muon_plan(&g);
+  dc_status st = cuda_status(timed("muon_squares", s, [&] { return launch_muon_squares(g, s); }));
+  if (st == DC_OK) st = cuda_status(timed("muon_begin", s, [&] { return launch_muon_begin(g, s); }));
+  static const char* const names[] = {"muon_gram", "muon_poly", "muon_apply"};
+  for (int i = 0; i < 3 * g.steps && st == DC_OK; ++i)
+    st = cuda_status(timed(names[i % 3], s, [&] { return launch_muon_product(g, i % 3, i / 3 % 2, s); }));
+  if (st == DC_OK)
+    st = cuda_status(timed("muon_end", s, [&] { return launch_muon_end(g, g.steps % 2, s); }));
+  return st;
+}
+
+dc_status check_ortho(int count, const void* mats, int steps, dc_ortho_precision precision) {
+  if (count < 0 || (count && !mats) || steps < 1 || steps > 20 ||
+      (precision != DC_ORTHO_16 && precision != DC_ORTHO_32))
+    return DC_ERR_INVALID_ARG;
+  return DC_OK;
+}
+
+}  // namespace
+}  // namespace dc
+
+extern "C" {
+
+dc_status dc_fp8_sizes(const dc_fp8_problem* prob, int transposed, size_t* codes, size_t* scales) {
+  const dc_status st = check_fp8(prob);
+  if (st != DC_OK) return st;
+  if (!codes || !scales) return DC_ERR_INVALID_ARG;
+  const long long rows = transposed ? prob->cols : prob->rows, cols = transposed ? prob->rows : prob->cols;
+  const long long runs = ceil_div_ll(cols, DC_FP8_BLOCK);
+  *codes = (size_t)(prob->batch * rows * runs * DC_FP8_BLOCK);
+  *scales = (size_t)(prob->batch * ceil_div_ll(rows, 128) * ceil_div_ll(runs, 4) * 512);
+  return DC_OK;
+}
+
+dc_status dc_fp8_quantize(const dc_fp8_problem* prob, const void* x, void* codes, void* scales,
+                          void* codes_t, void* scales_t, void* stream) {
+  const dc_status st = check_fp8(prob);
+  if (st != DC_OK) return st;
+  if (prob->batch == 0) return DC_OK;
+  if (!codes != !scales || !codes_t != !scales_t || (!codes && !codes_t) || !x)
+    return DC_ERR_INVALID_ARG;
+  const void* ptrs[] = {codes, scales, codes_t, scales_t};
+  for (const void* p : ptrs)
+    if (!aligned16(p)) return DC_ERR_UNSUPPORTED;
+  if (!aligned_to(x, elt_size(prob->dtype))) return DC_ERR_UNSUPPORTED;
+  Fp8Args a{prob->batch, prob->rows, prob->cols, prob->square, prob->dtype, prob->format, x,
+            static_cast<unsigned char*>(codes), static_cast<unsigned char*>(scales),
+            static_cast<unsigned char*>(codes_t), static_cast<unsigned char*>(scales_t)};
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  return cuda_status(timed("fp8_quantize", s, [&] { return launch_fp8_quantize(a, s); }));
+}
+
+dc_status dc_fp8_values(const dc_fp8_problem* prob, int transposed, const void* codes,
+                        const void* scales, float* out, void* stream) {
+  const dc_status st = check_fp8(prob);
+  if (st != DC_OK) return st;
+  if (prob->batch == 0) return DC_OK;
+  if (!codes || !scales || !out) return DC_ERR_INVALID_ARG;
+  if (!aligned16(codes) || !aligned16(scales) || !aligned_to(out, 4)) return DC_ERR_UNSUPPORTED;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  return cuda_status(timed("fp8_values", s, [&] {
+    return launch_fp8_values(prob->batch, transposed ? prob->cols : prob->rows,
+                             transposed ? prob->rows : prob->cols, prob->format, codes, scales, out, s);
+  }));
+}
+
+dc_status dc_fp8_matmul_workspace_size(const dc_fp8_product* prob, size_t* bytes) {
+  const dc_status st = check_product(prob);
+  if (st != DC_OK) return st;
+  if (!bytes) return DC_ERR_INVALID_ARG;
+  *bytes = fp8_matmul_workspace_bytes(*prob);
+  return DC_OK;
+}
+
+dc_status dc_fp8_matmul(const dc_fp8_product* prob, const void* a, const void* a_scales,
+                        const void* b, const void* b_scales, void* d, void* ws, size_t ws_bytes,
+                        void* stream) {
+  const dc_status st = check_product(prob);
+  if (st != DC_OK) return st;
+  if (prob->batch == 0 && !prob->sum) return DC_OK;
+  const bool empty = prob->k == 0 || prob->batch == 0;
+  if (!d || (!empty && (!a || !a_scales || !b || !b_scales))) return DC_ERR_INVALID_ARG;
+  const void* ptrs[] = {a, a_scales, b, b_scales, ws};
+  for (const void* p : ptrs)
+    if (!aligned16(p)) return DC_ERR_UNSUPPORTED;
+  if (!aligned_to(d, elt_size(prob->out))) return DC_ERR_UNSUPPORTED;
+  const size_t need = fp8_matmul_workspace_bytes(*prob);
+  if (need && (!ws || ws_bytes < need)) return DC_ERR_WORKSPACE;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  const Fp8Product t{*prob, a, a_scales, b, b_scales, d, ws};
+  if (empty) {
+    const size_t count = (size_t)(prob->sum ? 1 : prob->batch) * prob->m * prob->n;
+    return cuda_status(cudaMemsetAsync(d, 0, count * elt_size(prob->out), s));
+  }
+  return cuda_status(timed("fp8_matmul", s, [&] { return launch_fp8_matmul(t, s); }));
+}
+
+dc_status dc_orthogonalize_workspace_size(const dc_matrix* mats, int count, size_t* bytes) {
+  if (count < 0 || (count && !mats) || !bytes) return DC_ERR_INVALID_ARG;
+  for (int i = 0; i < count; ++i) {
+    const dc_status st = check_sides(mats[i].rows, mats[i].cols);
+    if (st != DC_OK) return st;
+  }
+  *bytes = muon_bytes(count, [&](int i, int* r, int* c) { *r = mats[i].rows, *c = mats[i].cols; });
+  return DC_OK;
+}
+
+dc_status dc_orthogonalize(const dc_matrix* mats, int count, int steps,
+                           dc_ortho_precision precision, void* ws, size_t ws_bytes, void* stream) {
+  dc_status st = check_ortho(count, mats, steps, precision);
+  for (int i = 0; i < count && st == DC_OK; ++i) st = check_matrix(mats[i]);
+  if (st != DC_OK) return st;
+  size_t need = 0;
+  dc_orthogonalize_workspace_size(mats, count, &need);
+  if (need && (!ws || ws_bytes < need || !aligned_to(ws, 256))) return DC_ERR_WORKSPACE;
+  MuonGroup g{};
+  g.steps = steps;
+  g.precision = precision;
+  size_t at = 0;
+  for (int i = 0; i < count; ++i) {
+    const dc_matrix& m = mats[i];
+    if (m.rows == 0 || m.cols == 0) continue;
+    if (g.count == kMuonMats) {
+      if ((st = run_muon(g, static_cast<cudaStream_t>(stream))) != DC_OK) return st;
+      g.count = 0, at = 0;
+    }
+    MuonMat& t = g.mat[g.count];
+    t = MuonMat{};
+    t.in = m.in;
+    t.out = m.out;
+    t.in_dtype = m.in_dtype;
+    t.out_dtype = m.out_dtype;
+    add_matrix(&g, m.rows, m.cols, static_cast<char*>(ws), &at);
+  }
+  return run_muon(g, static_cast<cudaStream_t>(stream));
+}
+
+dc_status dc_muon_workspace_size(const dc_muon_tensor* tensors, int count, size_t* bytes) {
+  if (count < 0 || (count && !tensors) || !bytes) return DC_ERR_INVALID_ARG;
+  for (int i = 0; i < count; ++i) {
+    const dc_status st = check_sides(tensors[i].rows, tensors[i].cols);
+    if (st != DC_OK) return st;
+  }
+  *bytes = muon_bytes(count, [&](int i, int* r, int* c) { *r = tensors[i].rows, *c = tensors[i].cols; });
+  return DC_OK;
+}
+
+dc_status dc_muon_step(const dc_muon_tensor* tensors, int count, const dc_muon_hyper* hyper,
+                       const float* grad_scale, const float* lr, void* ws, size_t ws_bytes,
+                       void* stream) {
+  if (!hyper) return DC_ERR_INVALID_ARG;
+  dc_status st = check_ortho(count, tensors, hyper->steps, hyper->precision);
+  if (st != DC_OK) return st;
+  if (!(hyper->lr >= 0) || hyper->lr > FLT_MAX || !(hyper->momentum >= 0 && hyper->momentum < 1) ||
+      (hyper->nesterov != 0 && hyper->nesterov != 1))
+    return DC_ERR_INVALID_ARG;
+  if (!aligned_to(grad_scale, 4) || !aligned_to(lr, 4)) return DC_ERR_UNSUPPORTED;
+  for (int i = 0; i < count; ++i)
+    if ((st = check_weight(tensors[i])) != DC_OK) return st;
+  size_t need = 0;
+  dc_muon_workspace_size(tensors, count, &need);
+  if (need && (!ws || ws_bytes < need || !aligned_to(ws, 256))) return DC_ERR_WORKSPACE;
+  MuonGroup g{};
+  g.steps = hyper->steps;
+  g.precision = hyper->precision;
+  g.update = true;
+  g.momentum = (float)hyper->momentum;
+  g.rest = (float)(1.0 - hyper->momentum);
+  g.nesterov = hyper->nesterov;
+  g.lr = (float)hyper->lr;
+  g.grad_scale = grad_scale;
+  g.lr_device = lr;
+  size_t at = 0;
+  for (int i = 0; i < count; ++i) {
+    const dc_muon_tensor& m = tensors[i];
+    if (m.rows == 0 || m.cols == 0) continue;
+    if (g.count == kMuonMats) {
+      if ((st = run_muon(g, static_cast<cudaStream_t>(stream))) != DC_OK) return st;
+      g.count = 0, at = 0;
+    }
+    MuonMat& t = g.mat[g.count];
+    t = MuonMat{};
+    t.in = m.grad;
+    t.in_dtype = m.grad_dtype;
+    t.param = m.param;
+    t.out_dtype = m.param_dtype;
+    t.master = m.master;
+    t.m = m.m;
+    t.weight_decay = m.weight_decay;
+    t.rate = m.rate;
+    add_matrix(&g, m.rows, m.cols, static_cast<char*>(ws), &at);
+  }
+  return run_muon(g, static_cast<cudaStream_t>(stream));
 }
 
 }  // extern "C"

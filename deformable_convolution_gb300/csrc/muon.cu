@@ -1,0 +1,219 @@
+// Orthogonalisation by Newton-Schulz products and the Muon step: the passes
+// over single elements around the products.
+#include "muon.cuh"
+
+namespace dc {
+namespace {
+
+constexpr int kThreads = 256;
+
+__device__ __forceinline__ float load_in(const void* p, dc_dtype dt, long long i) {
+  return dt == DC_BF16 ? __bfloat162float(static_cast<const __nv_bfloat16*>(p)[i]) : static_cast<const float*>(p)[i];
+}
+
+// Whether the step is skipped: its scale is not finite.
+__device__ __forceinline__ bool skipped(const MuonGroup& g, float* scale) {
+  *scale = g.update && g.grad_scale ? *g.grad_scale : 1.f;
+  return !(fabsf(*scale) <= 3.402823466e38f);
+}
+
+// What is orthogonalised: u of the updated m and the gradient, or `in`.
+__device__ __forceinline__ float direction(const MuonGroup& g, const MuonMat& t, float scale, long long i) {
+  const float v = load_in(t.in, t.in_dtype, i);
+  if (!g.update) return v;
+  const float m = t.m[i];
+  return g.nesterov ? m * g.momentum + v * scale * g.rest : m;
+}
+
+__device__ __forceinline__ float block_sum(float v) {
+  __shared__ float part[kThreads / 32];
+#pragma unroll
+  for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  __syncthreads();
+  if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = v;
+  __syncthreads();
+  v = 0.f;
+#pragma unroll
+  for (int w = 0; w < kThreads / 32; ++w) v += part[w];
+  return v;
+}
+
+__global__ void __launch_bounds__(kThreads) muon_squares(const __grid_constant__ MuonGroup g) {
+  pdl_wait();
+  pdl_release();
+  const MuonMat& t = g.mat[blockIdx.y];
+  float scale;
+  if (skipped(g, &scale) || blockIdx.x >= t.parts) return;
+  const long long count = (long long)t.rows * t.cols;
+  float sum = 0.f;
+  for (long long i = (long long)blockIdx.x * kThreads + threadIdx.x; i < count; i += (long long)t.parts * kThreads) {
+    if (g.update) {
+      const float v = load_in(t.in, t.in_dtype, i) * scale;
+      t.m[i] = t.m[i] * g.momentum + v * g.rest;
+    }
+    const float u = direction(g, t, scale, i);
+    sum += u * u;
+  }
+  sum = block_sum(sum);
+  if (threadIdx.x == 0) t.part[blockIdx.x] = sum;
+}
+
+__global__ void __launch_bounds__(kThreads) muon_begin(const __grid_constant__ MuonGroup g) {
+  pdl_wait();
+  pdl_release();
+  const MuonMat& t = g.mat[blockIdx.y];
+  float scale;
+  if (skipped(g, &scale) || blockIdx.x >= t.parts) return;
+  float sum = 0.f;
+  for (int i = threadIdx.x; i < t.parts; i += kThreads) sum += t.part[i];
+  const float norm = sqrtf(block_sum(sum));
+  // a norm that is not finite makes every element NaN
+  const float f = norm <= 3.402823466e38f ? kOrthoScale / (norm + kOrthoEps) : __uint_as_float(0x7fffffffu);
+  const long long count = (long long)t.rows * t.cols;
+  for (long long i = (long long)blockIdx.x * kThreads + threadIdx.x; i < count; i += (long long)t.parts * kThreads) {
+    const long long r = i / t.cols;
+    const float v = direction(g, t, scale, i) * f;
+    const __half h = __float2half_rn(v);
+    __half* x = t.x[0] + r * t.ld + (i - r * t.cols);
+    x[0] = h;
+    x[muon_x_low(t)] = __float2half_rn(v - __half2float(h));
+  }
+}
+
+__global__ void __launch_bounds__(kThreads) muon_end(const __grid_constant__ MuonGroup g, int from) {
+  pdl_wait();
+  pdl_release();
+  const MuonMat& t = g.mat[blockIdx.y];
+  float scale;
+  if (skipped(g, &scale) || blockIdx.x >= t.parts) return;
+  const float lr = g.lr_device ? *g.lr_device : g.lr;
+  const float keep = 1.f - lr * t.weight_decay, rate = lr * t.rate;
+  const long long count = (long long)t.rows * t.cols;
+  for (long long i = (long long)blockIdx.x * kThreads + threadIdx.x; i < count; i += (long long)t.parts * kThreads) {
+    const long long r = i / t.cols;
+    const __half* x = t.x[from] + r * t.ld + (i - r * t.cols);
+    const float v = (__half2float(x[0]) + __half2float(x[muon_x_low(t)])) * (1.f / kOrthoScale);
+    if (!g.update) {
+      if (t.out_dtype == DC_BF16)
+        static_cast<__nv_bfloat16*>(t.out)[i] = __float2bfloat16_rn(v);
+      else
+        static_cast<float*>(t.out)[i] = v;
+      continue;
+    }
+    const float p = (t.master ? t.master[i] : load_in(t.param, t.out_dtype, i)) * keep - v * rate;
+    if (t.master) t.master[i] = p;
+    if (t.out_dtype == DC_BF16)
+      static_cast<__nv_bfloat16*>(t.param)[i] = __float2bfloat16_rn(p);
+    else
+      static_cast<float*>(t.param)[i] = p;
+  }
+}
+
+// The products, on CUDA cores: which 0: gram = X X^T (tall: X^T X); 1: poly = b
+// gram + c gram^2; 2: x[1 - from] = a X + poly X (tall: X poly).
+__global__ void __launch_bounds__(256) muon_product(const __grid_constant__ MuonGroup g, int which, int from) {
+  __shared__ float sa[64][17], sb[64][17];
+  pdl_wait();
+  pdl_release();
+  const MuonMat& t = g.mat[blockIdx.y];
+  const int rows = which == 2 ? t.rows : t.side, cols = which == 2 ? t.cols : t.side;
+  const int depth = which == 0 ? (t.tall ? t.rows : t.cols) : t.side;
+  const int tiles_n = (cols + 63) / 64, tiles = (rows + 63) / 64 * tiles_n;
+  const __half* x = t.x[from];
+  const long long xl = muon_x_low(t), pl = muon_p_low(t);
+  auto pair = [](const __half* p, long long low, long long i) { return __half2float(p[i]) + __half2float(p[i + low]); };
+  auto left = [&](int r, int k) {
+    if (which == 0) return t.tall ? pair(x, xl, (long long)k * t.ld + r) : pair(x, xl, (long long)r * t.ld + k);
+    if (which == 1) return pair(t.gram, pl, (long long)r * t.lds + k);
+    return t.tall ? pair(x, xl, (long long)r * t.ld + k) : pair(t.poly, pl, (long long)r * t.lds + k);
+  };
+  auto right = [&](int c, int k) {
+    if (which == 0) return t.tall ? pair(x, xl, (long long)k * t.ld + c) : pair(x, xl, (long long)c * t.ld + k);
+    if (which == 1) return pair(t.gram, pl, (long long)k * t.lds + c);
+    return t.tall ? pair(t.poly, pl, (long long)k * t.lds + c) : pair(x, xl, (long long)k * t.ld + c);
+  };
+  const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
+  for (int tile = blockIdx.x; tile < tiles; tile += gridDim.x) {
+    const int m0 = tile / tiles_n * 64, n0 = tile % tiles_n * 64;
+    float acc[4][4] = {};
+    for (int k0 = 0; k0 < depth; k0 += 16) {
+      for (int e = threadIdx.x; e < 1024; e += 256) {
+        const int r = e >> 4, k = e & 15;
+        sa[r][k] = m0 + r < rows && k0 + k < depth ? left(m0 + r, k0 + k) : 0.f;
+        sb[r][k] = n0 + r < cols && k0 + k < depth ? right(n0 + r, k0 + k) : 0.f;
+      }
+      __syncthreads();
+      for (int k = 0; k < 16; ++k)
+        for (int u = 0; u < 4; ++u)
+          for (int v = 0; v < 4; ++v) acc[u][v] += sa[ty * 4 + u][k] * sb[tx * 4 + v][k];
+      __syncthreads();
+    }
+    for (int u = 0; u < 4; ++u)
+      for (int v = 0; v < 4; ++v) {
+        const int r = m0 + ty * 4 + u, c = n0 + tx * 4 + v;
+        if (r >= rows || c >= cols) continue;
+        float d = acc[u][v] * (1.f / kOrthoScale);
+        __half* to;
+        long long low;
+        if (which == 2) {
+          const long long i = (long long)r * t.ld + c;
+          d += kOrthoA * pair(x, xl, i);
+          to = t.x[1 - from] + i;
+          low = xl;
+        } else {
+          const long long i = (long long)r * t.lds + c;
+          if (which == 1) d = kOrthoB * pair(t.gram, pl, i) + kOrthoC * d;
+          to = (which ? t.poly : t.gram) + i;
+          low = pl;
+        }
+        const __half h = __float2half_rn(d);
+        to[0] = h;
+        to[low] = __float2half_rn(d - __half2float(h));
+      }
+  }
+}
+
+template <typename K, typename... A>
+cudaError_t launch(K kern, dim3 grid, cudaStream_t s, const A&... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(kThreads);
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, kern, args...);
+  note_launches(1);
+  return e;
+}
+
+}  // namespace
+
+void muon_plan(MuonGroup* g) {
+  // a matrix's blocks go by its own size: its sums' order, and so its result's
+  // last bits, do not depend on the matrices beside it
+  g->parts = 0;
+  for (int i = 0; i < g->count; ++i) {
+    MuonMat& t = g->mat[i];
+    const long long want = ceil_div_ll((long long)t.rows * t.cols, 8 * kThreads);
+    t.parts = (int)(want < kMuonParts ? want : kMuonParts);
+    if (t.parts > g->parts) g->parts = t.parts;
+  }
+}
+
+cudaError_t launch_muon_squares(const MuonGroup& g, cudaStream_t s) {
+  return launch(muon_squares, dim3((unsigned)g.parts, (unsigned)g.count), s, g);
+}
+cudaError_t launch_muon_begin(const MuonGroup& g, cudaStream_t s) {
+  return launch(muon_begin, dim3((unsigned)g.parts, (unsigned)g.count), s, g);
+}
+cudaError_t launch_muon_product(const MuonGroup& g, int which, int from, cudaStream_t s) {
+  return launch(muon_product, dim3(608, (unsigned)g.count), s, g, which, from);
+}
+cudaError_t launch_muon_end(const MuonGroup& g, int from, cudaStream_t s) {
+  return launch(muon_end, dim3((unsigned)g.parts, (unsigned)g.count), s, g, from);
+}
+
+}  // namespace dc

@@ -1,0 +1,127 @@
+"""Pointwise (1 x 1) layers as products of matrices in 8-bit floating point.
+
+Marshalling only: the layer keeps codes, scales and workspaces between its
+calls; quantising and products run in the library's kernels.  The codes and
+their scales are defined in ``include/deform_conv.h``.
+"""
+from __future__ import annotations
+
+import torch
+
+from . import binding as B
+
+
+class Quantized:
+    """Matrices in 8 bits: codes and scales of ``p`` (an ``Fp8Problem``), and
+    of their transposes.  direct, transposed: which of the two are kept."""
+
+    def __init__(self, p: B.Fp8Problem, direct=True, transposed=False, device="cuda"):
+        self.p = p
+
+        def pair(shapes, kept):
+            return [torch.empty(s, dtype=torch.uint8, device=device) if kept else None for s in shapes]
+        self.codes, self.scales = pair(p.shapes, direct)
+        self.codes_t, self.scales_t = pair(p.shapes_t, transposed)
+
+    def load(self, x, stream=None):
+        """Quantises x (a tensor of the problem's values, any shape)."""
+        B.dc_fp8_quantize(self.p, x.view(self.p.shape), self.codes, self.scales, self.codes_t,
+                          self.scales_t, stream)
+
+    def values(self, transposed=False, stream=None):
+        """The float32 values that the codes stand for, as a new tensor."""
+        codes, scales = (self.codes_t, self.scales_t) if transposed else (self.codes, self.scales)
+        shape = (self.p.batch, self.p.cols, self.p.rows) if transposed else self.p.shape
+        out = torch.empty(shape, device=codes.device)
+        B.dc_fp8_values(self.p, codes, scales, out, transposed, stream)
+        return out
+
+
+class Pointwise:
+    """y = W x over the channels of every pixel: x [n, c_in, h, w], y
+    [n, c_out, h, w] (DC_NHWC: channels last) in ``dtype``, W [c_out, c_in].
+
+    ``load`` quantises the weight (E4M3, a scale for each 128 x 128 block),
+    ``forward`` the input (E4M3, a scale for each 128 channels of a pixel, and,
+    ``training``, each 128 pixels of a channel for the weight's gradient),
+    ``backward`` the gradient of y (``grad_format``, in ``grad_dtype``) likewise.
+    Products are exact and summed in float32.
+
+    The layer keeps the codes of its weight and of the last forward's input,
+    and workspaces: its calls belong on one stream, or on streams that wait for
+    one another."""
+
+    def __init__(self, n, c_in, c_out, h, w, dtype=B.DC_BF16, layout=B.DC_NCHW, training=True,
+                 grad_dtype=None, grad_format=B.DC_E4M3, device="cuda"):
+        grad_dtype = dtype if grad_dtype is None else grad_dtype
+        last = layout == B.DC_NHWC
+        self.training = training
+        self.x_shape, self.y_shape = ((n, h, w, c) if last else (n, c, h, w) for c in (c_in, c_out))
+        self.w_shape, self.dtype, self.grad_dtype = (c_out, c_in), B._TORCH_DTYPE[dtype], B._TORCH_DTYPE[grad_dtype]
+        pixels = max(n, 1) * h * w if last else h * w
+        batch, q = min(n, 1) if last else n, B.Fp8Product
+
+        def maps(c, kind, fmt):
+            return B.Fp8Problem(batch, pixels, c, kind, fmt) if last else B.Fp8Problem(batch, c, pixels, kind, fmt)
+        # codes by channel (runs of channels) and by pixel: direct and transposed, or the other way round
+        self.weight = Quantized(B.Fp8Problem(1, c_out, c_in, dtype, B.DC_E4M3, 1), True, training, device)
+        self.x = Quantized(maps(c_in, dtype, B.DC_E4M3), last or training, not last or training, device)
+        e, g = B.DC_E4M3, grad_format
+        # products over channels: pixels are the rows of D (channels last) or its columns
+        self._fwd = q(batch, pixels, c_out, c_in, b_shared=1, out=dtype) if last else \
+            q(batch, c_out, pixels, c_in, a_shared=1, out=dtype)
+        self._calls = [self._fwd]
+        if training:
+            self.gy = Quantized(maps(c_out, grad_dtype, g), True, True, device)
+            self._gx = q(batch, pixels, c_in, c_out, g, e, b_shared=1, out=dtype) if last else \
+                q(batch, c_in, pixels, c_out, e, g, a_shared=1, out=dtype)
+            self._gw = q(batch, c_out, c_in, pixels, g, e, sum=1, out=B.DC_F32)
+            self._calls += [self._gx, self._gw]
+        self.last = last
+        need = max(B.dc_fp8_matmul_workspace_size(p) for p in self._calls)
+        self._ws = torch.empty(max(need, 1), dtype=torch.uint8, device=device)
+
+    def load(self, w, stream=None):
+        """The weight [c_out, c_in] (or [c_out, c_in, 1, 1]), for the calls that follow."""
+        B._arg(w, "w", w.shape, self.dtype)
+        if tuple(w.shape) not in (self.w_shape, self.w_shape + (1, 1)):
+            raise ValueError(f"w: expected shape {self.w_shape}, got {tuple(w.shape)}")
+        self.weight.load(w, stream)
+
+    def forward(self, x, y=None, stream=None):
+        """y (a new tensor if not given) = W x."""
+        B._arg(x, "x", self.x_shape, self.dtype)
+        y = torch.empty(self.y_shape, dtype=self.dtype, device=x.device) if y is None else y
+        B._arg(y, "y", self.y_shape, self.dtype)
+        self.x.load(x, stream)
+        self._over_channels(self._fwd, self.weight.codes, self.weight.scales, self.x, y, stream)
+        return y
+
+    def backward(self, grad_y, grad_x=None, grad_w=None, stream=None):
+        """(grad_x, grad_w) of the last forward's input and of the weight: in
+        ``dtype`` and float32, new tensors if not given."""
+        if not self.training:
+            raise ValueError("a layer made with training=False keeps nothing for a backward pass")
+        B._arg(grad_y, "grad_y", self.y_shape, self.grad_dtype)
+        if grad_x is None:
+            grad_x = torch.empty(self.x_shape, dtype=self.dtype, device=grad_y.device)
+        if grad_w is None:
+            grad_w = torch.empty(self.w_shape, dtype=torch.float32, device=grad_y.device)
+        B._arg(grad_x, "grad_x", self.x_shape, self.dtype)
+        self.gy.load(grad_y, stream)
+        self._over_channels(self._gx, self.weight.codes_t, self.weight.scales_t, self.gy, grad_x, stream)
+        a, b = self.gy, self.x
+        if self.last:
+            B.dc_fp8_matmul(self._gw, a.codes_t, a.scales_t, b.codes_t, b.scales_t, grad_w.view(self.w_shape),
+                            self._ws, stream)
+        else:
+            B.dc_fp8_matmul(self._gw, a.codes, a.scales, b.codes, b.scales, grad_w.view(self.w_shape),
+                            self._ws, stream)
+        return grad_x, grad_w
+
+    def _over_channels(self, p, w_codes, w_scales, maps, out, stream):
+        out = out.view(p.shape)
+        if self.last:
+            B.dc_fp8_matmul(p, maps.codes, maps.scales, w_codes, w_scales, out, self._ws, stream)
+        else:
+            B.dc_fp8_matmul(p, w_codes, w_scales, maps.codes_t, maps.scales_t, out, self._ws, stream)

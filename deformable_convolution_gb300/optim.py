@@ -1,4 +1,4 @@
-"""AdamW and gradient clipping over all parameters of a network at once.
+"""AdamW, Muon and gradient clipping over all parameters of a network at once.
 
 Marshalling only: the optimiser keeps a host table of its tensors' pointers
 (``binding.adamw_tensors``) and hands it to the library, which updates every
@@ -194,3 +194,114 @@ class AdamW:
             if s.get("master") is not None:
                 q["param"].copy_(q["master"])
         self._hyper.step, self._hyper.lr = d["step"], d["lr"]
+
+
+class Orthogonalize:
+    """Writes the matrices ``ins`` (float32 or bfloat16 CUDA tensors, the first
+    dimension by all others) orthogonalised into ``outs`` (either type; a tensor
+    may be both) by ``steps`` Newton-Schulz steps.  precision: 16, where X's
+    products take its high 16 bits only (errors below a bfloat16's rounding), or 32.
+
+    Addresses are taken here.  The object keeps one workspace: its calls belong
+    on one stream, or on streams that wait for one another."""
+
+    def __init__(self, ins, outs, steps=5, precision=16):
+        self.ins, self.outs = tuple(ins), tuple(outs)
+        self._table = B.matrices(self.ins, self.outs)
+        self._how = steps, _precision(precision)
+        self._ws = _bytes(B.dc_orthogonalize_workspace_size(self._table, len(self.ins)), self.ins)
+
+    def __call__(self, stream=None):
+        B.dc_orthogonalize(self._table, len(self.ins), *self._how, self._ws, stream)
+
+
+def _precision(bits):
+    if bits not in (16, 32):
+        raise ValueError("precision must be 16 or 32")
+    return B.DC_ORTHO_16 if bits == 16 else B.DC_ORTHO_32
+
+
+def _bytes(count, like):
+    return torch.empty(max(count, 1), dtype=torch.uint8, device=like[0].device if like else "cuda")
+
+
+class Muon:
+    """Muon over ``params``, weights of two dimensions or more (a matrix: the
+    first by all others): dicts as AdamW's, with
+
+      m        optional momentum, float32, else made here (zeros)
+      rate     optional factor on lr, else rms * sqrt(the longer side): a step
+               of AdamW's usual size for rms = 0.2
+
+    and param, grad, master, weight_decay as there.  precision: of the
+    orthogonalisation (see ``Orthogonalize``).  Biases, norms' parameters and
+    other vectors belong to AdamW.  As there, ``params`` is read-only and
+    ``set_grads`` hands over gradients at other addresses."""
+
+    def __init__(self, params, lr=1e-3, momentum=0.95, nesterov=True, weight_decay=0.01, steps=5,
+                 rms=0.2, precision=16):
+        entries = []
+        for q in params:
+            q = dict(q)
+            q.setdefault("weight_decay", weight_decay)
+            if q.get("rate") is None:
+                q["rate"] = rms * max(B._matrix_shape(q["param"], "param")) ** 0.5
+            if q.get("m") is None:
+                q["m"] = torch.zeros(q["param"].shape, device=q["param"].device)
+            entries.append(q)
+        self._hyper = B.DcMuonHyper(lr, momentum, int(bool(nesterov)), steps, _precision(precision))
+        self._set(entries)
+        self._ws = _bytes(B.dc_muon_workspace_size(self._table, len(entries)),
+                          [q["param"] for q in entries])
+
+    def _set(self, entries):
+        self._table = B.muon_tensors(entries)
+        self.params = tuple(MappingProxyType(q) for q in entries)
+
+    def set_grads(self, grads):
+        """Other gradients for the next steps, one for each parameter."""
+        grads = tuple(grads)
+        if len(grads) != len(self.params):
+            raise ValueError(f"expected {len(self.params)} gradients, got {len(grads)}")
+        if any(g is None or g.shape != q["param"].shape for g, q in zip(grads, self.params)):
+            raise ValueError("a gradient is missing or of another shape than its parameter")
+        self._set([dict(q, grad=g) for q, g in zip(self.params, grads)])
+
+    @property
+    def lr(self):
+        return self._hyper.lr
+
+    @lr.setter
+    def lr(self, value):
+        self._hyper.lr = value
+
+    def step(self, grad_scale=None, lr=None, stream=None):
+        """One step with the gradients times grad_scale (a device scalar; a step
+        whose scale is not finite changes no tensor).  lr: a device scalar that
+        takes the place of ``self.lr`` (for a replayed CUDA graph)."""
+        B.dc_muon_step(self._table, len(self.params), self._hyper, grad_scale, lr, self._ws, stream)
+
+    def state_dict(self):
+        """The state as tensors (not copies), the masters among it."""
+        return dict(lr=self._hyper.lr, state=[{k: q[k] for k in ("m", "master") if q.get(k) is not None}
+                                              for q in self.params])
+
+    def load_state_dict(self, d):
+        """Copies a ``state_dict`` of the same parameters into this state.  A
+        parameter with a master becomes its rounded copy; a state that holds no
+        masters leaves both as they are."""
+        if len(d["state"]) != len(self.params):
+            raise ValueError("state of another number of tensors")
+        for q, s in zip(self.params, d["state"]):
+            for k in ("m", "master"):
+                a, b = q.get(k), s.get(k)
+                if b is None and k == "master":
+                    continue
+                if (a is None) != (b is None) or (a is not None and (a.dtype != b.dtype or a.shape != b.shape)):
+                    raise ValueError(f"state {k} of another kind or shape")
+        for q, s in zip(self.params, d["state"]):
+            for k, t in s.items():
+                q[k].copy_(t)
+            if s.get("master") is not None:
+                q["param"].copy_(q["master"])
+        self._hyper.lr = d["lr"]

@@ -458,6 +458,151 @@ dc_status dc_grad_norm_workspace_size(int count, size_t* bytes);
 dc_status dc_grad_norm(const dc_adamw_tensor* tensors, int count, float max_norm, float* norm,
                        float* scale, void* ws, size_t ws_bytes, void* stream);
 
+/* ---------------------------------------------------------------- matrices of a training step
+ * Products of matrices in 8-bit floating point (the pointwise, 1 x 1, layers
+ * that stand beside a deformable layer in a residual network), and an
+ * optimiser that takes a weight as a matrix (Muon). */
+
+/* 8-bit floating-point codes: 1 sign bit and 4 exponent bits with 3 of the
+ * mantissa (largest value 448), or 5 with 2 (largest value 57344). */
+typedef enum { DC_E4M3 = 0, DC_E5M2 = 1 } dc_fp8;
+
+/* `batch` matrices [rows][cols] of `dtype` values to be held in 8 bits.  A
+ * block of values shares a scale 2^e, kept as the byte e + 127: a run of 128
+ * columns of one row or, where `square` is 1, a block of 128 x 128 (the last
+ * ones of a matrix may be short).  e is the smallest whole number, at least
+ * -126, for which the block's largest magnitude is at most 448 * 2^e (E5M2:
+ * 57344 * 2^e); a code is value / 2^e rounded to nearest even.  A block that
+ * holds a value that is not finite has the scale byte 255 and NaN codes: all
+ * of it stands for NaN.
+ * The codes lie as [batch][rows][cols rounded up to 128], the columns past
+ * `cols` zero (NaN in a block of NaN).  The scales lie as the tensor cores take them: row r of matrix
+ * i and the run k of its columns have the byte
+ *   ((i * ceil(rows / 128) + r / 128) * ceil(runs / 4) + k / 4) * 512
+ *     + (r % 32) * 16 + (r % 128) / 32 * 4 + k % 4
+ * with runs = ceil(cols / 128); a square block's scale stands at each of its
+ * rows, bytes of no row or run are of no meaning. */
+#define DC_FP8_BLOCK 128
+typedef struct {
+  int batch, rows, cols; /* batch may be 0 */
+  dc_dtype dtype;
+  dc_fp8 format;
+  int square;
+} dc_fp8_problem;
+
+/* Bytes of the codes and scales of the matrices (transposed = 0) or of their
+ * transposes [cols][rows] (1).  Errors: DC_ERR_INVALID_ARG for NULL, rows or
+ * cols below 1, an unknown enum; DC_ERR_UNSUPPORTED for rows or cols over
+ * 2^24, a batch over 65535 or more than 2^40 values. */
+dc_status dc_fp8_sizes(const dc_fp8_problem* prob, int transposed, size_t* codes, size_t* scales);
+
+/* Quantises x [batch][rows][cols] into codes and scales and, from the same
+ * read, its transposes [cols][rows] (whose runs go along the rows of x; square
+ * blocks are the same ones) into codes_t and scales_t.  Either pair may be
+ * NULL, not both.  Pointers 16-byte aligned, x to its element's size. */
+dc_status dc_fp8_quantize(const dc_fp8_problem* prob, const void* x, void* codes, void* scales,
+                          void* codes_t, void* scales_t, void* stream);
+
+/* out [batch][rows][cols] float32 (transposed = 1: [batch][cols][rows], of
+ * codes_t and scales_t): the values that the codes stand for (infinite for
+ * 2^128, to which magnitudes close to the largest float32 round). */
+dc_status dc_fp8_values(const dc_fp8_problem* prob, int transposed, const void* codes,
+                        const void* scales, float* out, void* stream);
+
+/* D[i] = A[i] B[i]^T: A[i] [m][k] and B[i] [n][k] in codes and scales (as a
+ * dc_fp8_quantize with cols = k writes them), D[i] [m][n] in `out`, dense.
+ *   a_shared, b_shared  one matrix for all i
+ *   sum                 D [m][n] = sum over i of A[i] B[i]^T (a weight's
+ *                       gradient from the images of a batch)
+ * Products of codes are exact, sums are float32 in a fixed order (the same
+ * inputs give the same bits); a bf16 D is rounded to nearest even.  batch or k
+ * may be 0: nothing is written for batch 0 without sum, else zeros.
+ * Errors: DC_ERR_INVALID_ARG for a bad problem or a NULL required pointer,
+ * DC_ERR_UNSUPPORTED for a pointer that is not 16-byte aligned (d: not aligned
+ * to its element), m, n or k over 2^24 or a batch over 65535, DC_ERR_WORKSPACE
+ * for a short workspace. */
+typedef struct {
+  int batch, m, n, k;
+  dc_fp8 a_format, b_format;
+  int a_shared, b_shared, sum;
+  dc_dtype out;
+} dc_fp8_product;
+dc_status dc_fp8_matmul_workspace_size(const dc_fp8_product* prob, size_t* bytes);
+dc_status dc_fp8_matmul(const dc_fp8_product* prob, const void* a, const void* a_scales,
+                        const void* b, const void* b_scales, void* d, void* ws, size_t ws_bytes,
+                        void* stream);
+
+/* Orthogonalisation by Newton-Schulz products: the singular values of a matrix
+ * are driven towards 1 (into about 0.7 .. 1.2), its singular vectors kept.
+ *   X = G / (|G| + 1e-7)      |G|: Frobenius norm
+ *   `steps` times:  A = X X^T,  X = 3.4445 X + (-4.7750 A + 2.0315 A A) X
+ * (with X^T in X's place where G has more rows than columns: the same values).
+ * A G that holds a value that is not finite, or whose squares' sum overflows
+ * float32, gives NaN throughout. */
+typedef enum { DC_ORTHO_16 = 0, DC_ORTHO_32 = 1 } dc_ortho_precision;
+/* Between the products X, A and the polynomial of A are held as pairs of
+ * 16-bit floats (22 bits or more, fixed point below).  DC_ORTHO_32 multiplies
+ * both parts of every factor (the result is as good as float32 arithmetic's);
+ * DC_ORTHO_16 leaves X's low part out of its products (relative error about
+ * 1.5e-3 or less, below the rounding to bf16).  Sums are float32, in a fixed
+ * order. */
+
+/* One matrix: in, out [rows][cols] dense; out may be in where the types agree. */
+typedef struct {
+  const void* in;
+  void* out;
+  int rows, cols;
+  dc_dtype in_dtype, out_dtype;
+} dc_matrix;
+
+/* Orthogonalises `count` matrices (host array, read before the call returns);
+ * a matrix with rows or cols 0 is left out.  Pointers need only their
+ * element's alignment.  Errors: DC_ERR_INVALID_ARG for NULL, negative sizes,
+ * an unknown enum, steps outside 1 .. 20; DC_ERR_UNSUPPORTED for a shorter
+ * side over 16384, a longer one over 2^22, or a pointer without its element's
+ * alignment; DC_ERR_WORKSPACE for a workspace that is short or not 256-byte
+ * aligned.  The workspace's size depends on the matrices' sizes alone. */
+dc_status dc_orthogonalize_workspace_size(const dc_matrix* mats, int count, size_t* bytes);
+dc_status dc_orthogonalize(const dc_matrix* mats, int count, int steps,
+                           dc_ortho_precision precision, void* ws, size_t ws_bytes, void* stream);
+
+/* One weight of a Muon step, [rows][cols] dense (a convolution's [C_out]
+ * [C_in * Kh * Kw]).  Pointers need only their element's alignment; tensors
+ * must not overlap. */
+typedef struct {
+  void* param;       /* param_dtype, updated */
+  float* master;     /* NULL, or the float32 parameter a bf16 `param` is a rounded copy of */
+  const void* grad;  /* grad_dtype */
+  float* m;          /* momentum, float32 */
+  int rows, cols;
+  dc_dtype param_dtype, grad_dtype;
+  float weight_decay; /* >= 0, finite */
+  float rate;         /* this weight's factor on lr, finite */
+} dc_muon_tensor;
+typedef struct {
+  double lr, momentum; /* lr >= 0, momentum in [0, 1) */
+  int nesterov, steps; /* steps of the orthogonalisation, 1 .. 20 */
+  dc_ortho_precision precision;
+} dc_muon_hyper;
+
+/* One Muon step over `count` weights:
+ *   g = grad * *grad_scale
+ *   m = m * momentum + g * (1 - momentum)
+ *   u = nesterov ? m * momentum + g * (1 - momentum) : m
+ *   p = p * (1 - lr * weight_decay) - orthogonalised(u) * (lr * rate)
+ * in float32 but for the orthogonalisation (as above).
+ *   grad_scale  device float, NULL = 1 (dc_grad_norm's scale).  If it is not
+ *               finite the step is skipped: nothing is changed.
+ *   lr          device float that takes the place of hyper's lr, NULL = hyper's
+ *               (for steps replayed from a CUDA graph)
+ * A bf16 param without a master is updated from its rounded value and rounded
+ * to nearest even.  A gradient that is not finite makes its weight NaN.
+ * Errors as above. */
+dc_status dc_muon_workspace_size(const dc_muon_tensor* tensors, int count, size_t* bytes);
+dc_status dc_muon_step(const dc_muon_tensor* tensors, int count, const dc_muon_hyper* hyper,
+                       const float* grad_scale, const float* lr, void* ws, size_t ws_bytes,
+                       void* stream);
+
 /* Static description of a status code. */
 const char* dc_status_string(dc_status status);
 

@@ -308,6 +308,7 @@ cudaError_t launch_k3cl(const K3ClArgs& a, cudaStream_t s);
 cudaError_t launch_gx_to_nchw(const float* gx_nhwc, float* grad_x, const Geom& g, cudaStream_t s);
 unsigned int cl3_read_error(int clear);
 unsigned int tf32_read_error(int clear);
+unsigned int fp8_read_error(int clear);
 // Backward of the offset convolution on the channels-last path (one offset
 // group, K <= 9 taps): the input part adds into the NHWC grad_x buffer's
 // values and writes grad_x (NCHW) whole; the weight part writes per-chunk
@@ -334,6 +335,9 @@ cudaError_t launch_k4cl_input(const K4ClArgs& a, cudaStream_t s);
 cudaError_t launch_k4cl_weight(const K4ClArgs& a, cudaStream_t s);
 cudaError_t launch_k4cl_reduce(const K4ClArgs& a, cudaStream_t s);
 unsigned int k4cl_read_error(int clear);
+bool make_tmap(CUtensorMap* m, CUtensorMapDataType dt, const void* base, int rank,
+               const unsigned long long* dims, const unsigned long long* strides_bytes,
+               const unsigned int* box, CUtensorMapSwizzle swizzle);
 bool make_tmap_f32(CUtensorMap* m, const void* base, int rank, const unsigned long long* dims,
                    const unsigned long long* strides_bytes, const unsigned int* box);
 bool make_tmap_bf16(CUtensorMap* m, const void* base, int rank, const unsigned long long* dims,

@@ -242,7 +242,8 @@ def check_product(p, seed=0):
 
 
 SIZES = [(1, 1, 1, 1), (1, 128, 128, 128), (2, 130, 70, 200), (1, 257, 129, 513), (3, 64, 1247, 200), (1, 300, 300, 1),
-         (2, 1, 333, 1030), (2, 333, 1, 1030), (1, 512, 384, 2048), (5, 200, 49, 640)]
+         (2, 1, 333, 1030), (2, 333, 1, 1030), (1, 512, 384, 2048), (5, 200, 49, 640),
+         (40, 300, 500, 700), (90, 257, 129, 130), (3, 2500, 2100, 384)]  # enough tiles for wide ones, several to a pair
 
 
 @on_gpu

@@ -40,73 +40,192 @@ __device__ __forceinline__ uint32_t codes2(float a, float b) {
   return (uint32_t)c;
 }
 
-// Tile [128 rows][128 columns] per block, from one read to both orientations.
-template <typename T, int FMT, bool SQUARE>
-__global__ void __launch_bounds__(kThreads) fp8_quantize(Fp8Args a) {
-  __shared__ float tile[kB][kB + 1];
-  __shared__ uint32_t row_top[kB], col_top[kB];
+// A thread's eight consecutive values of a row.
+template <typename T>
+struct Eight;
+template <>
+struct Eight<float> {
+  float v[8];
+  __device__ __forceinline__ float get(int i) const { return v[i]; }
+  __device__ __forceinline__ void load(const float* p) {
+    const float4 a = *reinterpret_cast<const float4*>(p), b = *reinterpret_cast<const float4*>(p + 4);
+    v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
+  }
+  __device__ __forceinline__ void load_some(const float* p, int count) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = i < count ? p[i] : 0.f;
+  }
+  __device__ __forceinline__ uint32_t top() const {
+    uint32_t t = 0u;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) t = max(t, magnitude(v[i]));
+    return t;
+  }
+};
+template <>
+struct Eight<__nv_bfloat16> {
+  uint32_t w[4];
+  __device__ __forceinline__ float get(int i) const {
+    return __uint_as_float(i & 1 ? w[i >> 1] & 0xffff0000u : w[i >> 1] << 16);
+  }
+  __device__ __forceinline__ void load(const __nv_bfloat16* p) {
+    const uint4 a = *reinterpret_cast<const uint4*>(p);
+    w[0] = a.x, w[1] = a.y, w[2] = a.z, w[3] = a.w;
+  }
+  __device__ __forceinline__ void load_some(const __nv_bfloat16* p, int count) {
+    const unsigned short* q = reinterpret_cast<const unsigned short*>(p);
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      w[i] = (2 * i < count ? (uint32_t)q[2 * i] : 0u) | (2 * i + 1 < count ? (uint32_t)q[2 * i + 1] << 16 : 0u);
+  }
+  __device__ __forceinline__ uint32_t top() const {
+    uint32_t t = 0u;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) t = __vmaxu2(t, w[i] & 0x7fff7fffu);
+    return max(t & 0xffff0000u, t << 16);
+  }
+};
+
+// The largest magnitudes of a thread's columns over its rows.
+template <typename T>
+__device__ __forceinline__ void column_tops(const Eight<T>* x, uint32_t* top);
+template <>
+__device__ __forceinline__ void column_tops<float>(const Eight<float>* x, uint32_t* top) {
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    uint32_t t = 0u;
+#pragma unroll
+    for (int r = 0; r < 8; ++r) t = max(t, magnitude(x[r].v[i]));
+    top[i] = max(t, __shfl_xor_sync(0xffffffffu, t, 16));
+  }
+}
+template <>
+__device__ __forceinline__ void column_tops<__nv_bfloat16>(const Eight<__nv_bfloat16>* x, uint32_t* top) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    uint32_t t = 0u;
+#pragma unroll
+    for (int r = 0; r < 8; ++r) t = __vmaxu2(t, x[r].w[i] & 0x7fff7fffu);
+    t = __vmaxu2(t, __shfl_xor_sync(0xffffffffu, t, 16));
+    top[2 * i] = t << 16;
+    top[2 * i + 1] = t & 0xffff0000u;
+  }
+}
+
+// One block takes a tile of 128 rows and 128 columns, a thread 8 x 8 values of
+// it in registers: the half warp h (of 16) has rows 8 h .., its lane l columns
+// 8 l ... A row's largest magnitude is a maximum over 16 lanes (of scale bytes,
+// which order like the magnitudes, two rows in a word), a column's one over
+// half warps through shared memory.  Codes of the rows leave from registers, 16
+// lanes writing a line of 128 bytes; those of the columns go through a tile in
+// shared memory whose 8-byte units are swizzled by the column group: neither
+// its writes nor its reads meet in a bank.
+template <typename T, int FMT, bool SQUARE, bool DIRECT, bool TRANSPOSED>
+__global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 3 : 2) fp8_quantize(Fp8Args a, int vectors) {
+  __shared__ uint32_t part[TRANSPOSED && !SQUARE ? kThreads / 32 : 1][kB];
+  __shared__ uint32_t shared_top;
+  __shared__ float col_inv[kB];
+  __shared__ __align__(16) unsigned char tile[TRANSPOSED ? kB * kB : 16];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int l = lane & 15, h = 2 * warp + (lane >> 4);
+  const int tiles_c = (a.cols + kB - 1) / kB;
+  const int by = blockIdx.x / tiles_c, bx = blockIdx.x - by * tiles_c;  // the tile's row and column
+  const int r0 = by * kB, c0 = bx * kB;
+  const int row = r0 + 8 * h, col = c0 + 8 * l;
+  const T* x = static_cast<const T*>(a.x) + ((long long)blockIdx.z * a.rows + row) * a.cols + col;
+  if (SQUARE && tid == 0) shared_top = 0u;
   pdl_wait();
   pdl_release();
-  const int tid = threadIdx.x;
-  const int r0 = blockIdx.y * kB, c0 = blockIdx.x * kB;
-  const T* x = static_cast<const T*>(a.x) + (long long)blockIdx.z * a.rows * a.cols;
-  if (tid < kB) row_top[tid] = col_top[tid] = 0u;
-  __syncthreads();
-  const int lane = tid & 31, warp = tid >> 5;
-  uint32_t ct[4] = {0u, 0u, 0u, 0u};
-  for (int r = warp; r < kB; r += kThreads / 32) {
-    uint32_t top = 0u;
+  Eight<T> v[8];
+  const int left = min(8, a.cols - col);  // columns of this thread's that there are
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const int c = lane + 32 * j;
-      const bool in = r0 + r < a.rows && c0 + c < a.cols;
-      const float v = in ? ld_f(x + (long long)(r0 + r) * a.cols + c0 + c) : 0.f;
-      tile[r][c] = v;
-      const uint32_t m = magnitude(v);
-      top = max(top, m);
-      ct[j] = max(ct[j], m);
-    }
-    top = __reduce_max_sync(0xffffffffu, top);
-    if (lane == 0) row_top[r] = top;
-  }
-#pragma unroll
-  for (int j = 0; j < 4; ++j) atomicMax(&col_top[lane + 32 * j], ct[j]);
-  __syncthreads();
-  if (SQUARE) {
-    uint32_t top = 0u;
-    for (int r = lane; r < kB; r += 32) top = max(top, row_top[r]);
-    top = __reduce_max_sync(0xffffffffu, top);
-    __syncthreads();
-    if (tid < kB) row_top[tid] = col_top[tid] = top;
-    __syncthreads();
+  for (int r = 0; r < 8; ++r) {
+    const int some = row + r < a.rows ? left : 0;
+    if (vectors && some > 0)  // then `some` is eight
+      v[r].load(x + (long long)r * a.cols);
+    else
+      v[r].load_some(x + (long long)r * a.cols, some);
   }
   const long long kr = ceil_div_ll(a.rows, kB), kc = ceil_div_ll(a.cols, kB);
-  if (tid < kB) {
-    const int at = (tid & 31) * 16 + (tid >> 5) * 4;
-    const uint32_t rb = scale_byte<FMT>(row_top[tid]), cb = scale_byte<FMT>(col_top[tid]);
-    if (a.scales)
-      a.scales[((blockIdx.z * kr + blockIdx.y) * ((kc + 3) / 4) + blockIdx.x / 4) * 512 + at + blockIdx.x % 4] =
-          (unsigned char)rb;
-    if (a.scales_t)
-      a.scales_t[((blockIdx.z * kc + blockIdx.x) * ((kr + 3) / 4) + blockIdx.y / 4) * 512 + at + blockIdx.y % 4] =
-          (unsigned char)cb;
+  uint32_t byte[8];  // the rows' scales
+  if (SQUARE) {
+    uint32_t top = 0u;
+#pragma unroll
+    for (int r = 0; r < 8; ++r) top = max(top, v[r].top());
+    top = __reduce_max_sync(0xffffffffu, top);
+    __syncthreads();
+    if (lane == 0) atomicMax(&shared_top, top);
+    __syncthreads();
+    const uint32_t b = scale_byte<FMT>(shared_top);
+#pragma unroll
+    for (int r = 0; r < 8; ++r) byte[r] = b;
+  } else {
+    if (TRANSPOSED) {
+      uint32_t top[8];
+      column_tops<T>(v, top);
+      if (lane < 16) {
+        *reinterpret_cast<uint4*>(&part[warp][8 * l]) = make_uint4(top[0], top[1], top[2], top[3]);
+        *reinterpret_cast<uint4*>(&part[warp][8 * l + 4]) = make_uint4(top[4], top[5], top[6], top[7]);
+      }
+    }
+    if (DIRECT) {
+#pragma unroll
+      for (int r = 0; r < 8; r += 2) {
+        uint32_t two = scale_byte<FMT>(v[r].top()) | (scale_byte<FMT>(v[r + 1].top()) << 16);
+#pragma unroll
+        for (int o = 8; o; o >>= 1) two = __vmaxu2(two, __shfl_xor_sync(0xffffffffu, two, o));
+        byte[r] = two & 0xffffu;
+        byte[r + 1] = two >> 16;
+      }
+    }
   }
-  if (a.codes)
-    for (int r = warp; r < kB && r0 + r < a.rows; r += kThreads / 32) {
-      const float s = inverse_scale(scale_byte<FMT>(row_top[r]));
-      unsigned char* q = a.codes + ((long long)blockIdx.z * a.rows + r0 + r) * (kc * kB) + c0;
-      const uint32_t lo = codes2<FMT>(tile[r][4 * lane] * s, tile[r][4 * lane + 1] * s);
-      const uint32_t hi = codes2<FMT>(tile[r][4 * lane + 2] * s, tile[r][4 * lane + 3] * s);
-      reinterpret_cast<uint32_t*>(q)[lane] = lo | (hi << 16);
+  if (DIRECT) {
+    // the byte of row r of the tile: (r % 32) * 16 + r / 32 * 4, for the run's place among four
+    unsigned char* sc = a.scales + ((blockIdx.z * kr + by) * ((kc + 3) / 4) + bx / 4) * 512 +
+                        (8 * h & 31) * 16 + h / 4 * 4 + bx % 4;
+    unsigned char* q = a.codes + ((long long)blockIdx.z * a.rows + row) * (kc * kB) + col;
+#pragma unroll
+    for (int r = 0; r < 8; ++r) {
+      const float s = inverse_scale(byte[r]);
+      uint2 c;
+      c.x = codes2<FMT>(v[r].get(0) * s, v[r].get(1) * s) | (codes2<FMT>(v[r].get(2) * s, v[r].get(3) * s) << 16);
+      c.y = codes2<FMT>(v[r].get(4) * s, v[r].get(5) * s) | (codes2<FMT>(v[r].get(6) * s, v[r].get(7) * s) << 16);
+      if (row + r < a.rows) *reinterpret_cast<uint2*>(q + r * (kc * kB)) = c;
+      if (l == r) sc[16 * r] = (unsigned char)byte[r];
     }
-  if (a.codes_t)
-    for (int c = warp; c < kB && c0 + c < a.cols; c += kThreads / 32) {
-      const float s = inverse_scale(scale_byte<FMT>(col_top[c]));
-      unsigned char* q = a.codes_t + ((long long)blockIdx.z * a.cols + c0 + c) * (kr * kB) + r0;
-      const uint32_t lo = codes2<FMT>(tile[4 * lane][c] * s, tile[4 * lane + 1][c] * s);
-      const uint32_t hi = codes2<FMT>(tile[4 * lane + 2][c] * s, tile[4 * lane + 3][c] * s);
-      reinterpret_cast<uint32_t*>(q)[lane] = lo | (hi << 16);
+  }
+  if (!TRANSPOSED) return;
+  if (!SQUARE) __syncthreads();
+  if (tid < kB) {
+    uint32_t b = byte[0];
+    if (!SQUARE) {
+      uint32_t top = 0u;
+#pragma unroll
+      for (int w = 0; w < kThreads / 32; ++w) top = max(top, part[w][tid]);
+      b = scale_byte<FMT>(top);
     }
+    col_inv[tid] = inverse_scale(b);
+    a.scales_t[((blockIdx.z * kc + bx) * ((kr + 3) / 4) + by / 4) * 512 + (tid & 31) * 16 +
+               (tid >> 5) * 4 + by % 4] = (unsigned char)b;
+  }
+  __syncthreads();
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const float s = col_inv[8 * l + i];
+    uint2 c;
+    c.x = codes2<FMT>(v[0].get(i) * s, v[1].get(i) * s) | (codes2<FMT>(v[2].get(i) * s, v[3].get(i) * s) << 16);
+    c.y = codes2<FMT>(v[4].get(i) * s, v[5].get(i) * s) | (codes2<FMT>(v[6].get(i) * s, v[7].get(i) * s) << 16);
+    *reinterpret_cast<uint2*>(tile + (8 * l + i) * kB + ((h ^ l) << 3)) = c;
+  }
+  __syncthreads();
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    const int c = (tid >> 3) + 32 * k, u = tid & 7, g = c >> 3;  // units 2 u and 2 u + 1 of column c
+    uint4 q = *reinterpret_cast<const uint4*>(tile + c * kB + (((2 * u) ^ (g & ~1)) << 3));
+    if (g & 1) q = make_uint4(q.z, q.w, q.x, q.y);
+    if (c0 + c < a.cols)
+      *reinterpret_cast<uint4*>(a.codes_t + ((long long)blockIdx.z * a.cols + c0 + c) * (kr * kB) + r0 + 16 * u) = q;
+  }
 }
 
 // rows, cols: of the matrix that the codes are of (transposed or not).
@@ -134,7 +253,7 @@ __global__ void __launch_bounds__(kThreads)
 template <typename T, int FMT>
 cudaError_t quantize(const Fp8Args& a, cudaStream_t s) {
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)ceil_div_ll(a.cols, kB), (unsigned)ceil_div_ll(a.rows, kB), (unsigned)a.batch);
+  cfg.gridDim = dim3((unsigned)(ceil_div_ll(a.cols, kB) * ceil_div_ll(a.rows, kB)), 1, (unsigned)a.batch);
   cfg.blockDim = dim3(kThreads);
   cfg.stream = s;
   cudaLaunchAttribute attr[1];
@@ -142,8 +261,12 @@ cudaError_t quantize(const Fp8Args& a, cudaStream_t s) {
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  const cudaError_t e = a.square ? cudaLaunchKernelEx(&cfg, fp8_quantize<T, FMT, true>, a)
-                                 : cudaLaunchKernelEx(&cfg, fp8_quantize<T, FMT, false>, a);
+  const int vectors = a.cols % 8 == 0 && (uintptr_t)a.x % 16 == 0;
+  auto go = [&](auto kern) { return cudaLaunchKernelEx(&cfg, kern, a, vectors); };
+  const cudaError_t e =
+      !a.codes_t  ? (a.square ? go(fp8_quantize<T, FMT, true, true, false>) : go(fp8_quantize<T, FMT, false, true, false>))
+      : !a.codes ? (a.square ? go(fp8_quantize<T, FMT, true, false, true>) : go(fp8_quantize<T, FMT, false, false, true>))
+                 : (a.square ? go(fp8_quantize<T, FMT, true, true, true>) : go(fp8_quantize<T, FMT, false, true, true>));
   note_launches(1);
   return e;
 }

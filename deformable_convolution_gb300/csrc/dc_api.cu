@@ -1075,6 +1075,8 @@ void add_matrix(MuonGroup* g, int rows, int cols, char* ws, size_t* at) {
   t.gram = reinterpret_cast<__half*>(take(4 * (size_t)muon_p_low(t)));
   t.poly = reinterpret_cast<__half*>(take(4 * (size_t)muon_p_low(t)));
   t.part = reinterpret_cast<float*>(take(kMuonParts * sizeof(float)));
+  t.sums = reinterpret_cast<float*>(take(muon_sums_bytes(t)));
+  t.arrivals = reinterpret_cast<unsigned int*>(take(kMuonArrivals * sizeof(unsigned int)));
 }
 
 // Workspace of `count` matrices of the sizes size(i): that of the largest group.

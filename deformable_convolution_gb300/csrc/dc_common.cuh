@@ -309,6 +309,7 @@ cudaError_t launch_gx_to_nchw(const float* gx_nhwc, float* grad_x, const Geom& g
 unsigned int cl3_read_error(int clear);
 unsigned int tf32_read_error(int clear);
 unsigned int fp8_read_error(int clear);
+unsigned int muon_read_error(int clear);
 // Backward of the offset convolution on the channels-last path (one offset
 // group, K <= 9 taps): the input part adds into the NHWC grad_x buffer's
 // values and writes grad_x (NCHW) whole; the weight part writes per-chunk

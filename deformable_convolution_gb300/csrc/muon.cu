@@ -64,6 +64,8 @@ __global__ void __launch_bounds__(kThreads) muon_begin(const __grid_constant__ M
   const MuonMat& t = g.mat[blockIdx.y];
   float scale;
   if (skipped(g, &scale) || blockIdx.x >= t.parts) return;
+  if (blockIdx.x == 0)
+    for (int i = threadIdx.x; i < kMuonArrivals; i += kThreads) t.arrivals[i] = 0u;
   float sum = 0.f;
   for (int i = threadIdx.x; i < t.parts; i += kThreads) sum += t.part[i];
   const float norm = sqrtf(block_sum(sum));
@@ -109,70 +111,6 @@ __global__ void __launch_bounds__(kThreads) muon_end(const __grid_constant__ Muo
   }
 }
 
-// The products, on CUDA cores: which 0: gram = X X^T (tall: X^T X); 1: poly = b
-// gram + c gram^2; 2: x[1 - from] = a X + poly X (tall: X poly).
-__global__ void __launch_bounds__(256) muon_product(const __grid_constant__ MuonGroup g, int which, int from) {
-  __shared__ float sa[64][17], sb[64][17];
-  pdl_wait();
-  pdl_release();
-  const MuonMat& t = g.mat[blockIdx.y];
-  const int rows = which == 2 ? t.rows : t.side, cols = which == 2 ? t.cols : t.side;
-  const int depth = which == 0 ? (t.tall ? t.rows : t.cols) : t.side;
-  const int tiles_n = (cols + 63) / 64, tiles = (rows + 63) / 64 * tiles_n;
-  const __half* x = t.x[from];
-  const long long xl = muon_x_low(t), pl = muon_p_low(t);
-  auto pair = [](const __half* p, long long low, long long i) { return __half2float(p[i]) + __half2float(p[i + low]); };
-  auto left = [&](int r, int k) {
-    if (which == 0) return t.tall ? pair(x, xl, (long long)k * t.ld + r) : pair(x, xl, (long long)r * t.ld + k);
-    if (which == 1) return pair(t.gram, pl, (long long)r * t.lds + k);
-    return t.tall ? pair(x, xl, (long long)r * t.ld + k) : pair(t.poly, pl, (long long)r * t.lds + k);
-  };
-  auto right = [&](int c, int k) {
-    if (which == 0) return t.tall ? pair(x, xl, (long long)k * t.ld + c) : pair(x, xl, (long long)c * t.ld + k);
-    if (which == 1) return pair(t.gram, pl, (long long)k * t.lds + c);
-    return t.tall ? pair(t.poly, pl, (long long)k * t.lds + c) : pair(x, xl, (long long)k * t.ld + c);
-  };
-  const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
-  for (int tile = blockIdx.x; tile < tiles; tile += gridDim.x) {
-    const int m0 = tile / tiles_n * 64, n0 = tile % tiles_n * 64;
-    float acc[4][4] = {};
-    for (int k0 = 0; k0 < depth; k0 += 16) {
-      for (int e = threadIdx.x; e < 1024; e += 256) {
-        const int r = e >> 4, k = e & 15;
-        sa[r][k] = m0 + r < rows && k0 + k < depth ? left(m0 + r, k0 + k) : 0.f;
-        sb[r][k] = n0 + r < cols && k0 + k < depth ? right(n0 + r, k0 + k) : 0.f;
-      }
-      __syncthreads();
-      for (int k = 0; k < 16; ++k)
-        for (int u = 0; u < 4; ++u)
-          for (int v = 0; v < 4; ++v) acc[u][v] += sa[ty * 4 + u][k] * sb[tx * 4 + v][k];
-      __syncthreads();
-    }
-    for (int u = 0; u < 4; ++u)
-      for (int v = 0; v < 4; ++v) {
-        const int r = m0 + ty * 4 + u, c = n0 + tx * 4 + v;
-        if (r >= rows || c >= cols) continue;
-        float d = acc[u][v] * (1.f / kOrthoScale);
-        __half* to;
-        long long low;
-        if (which == 2) {
-          const long long i = (long long)r * t.ld + c;
-          d += kOrthoA * pair(x, xl, i);
-          to = t.x[1 - from] + i;
-          low = xl;
-        } else {
-          const long long i = (long long)r * t.lds + c;
-          if (which == 1) d = kOrthoB * pair(t.gram, pl, i) + kOrthoC * d;
-          to = (which ? t.poly : t.gram) + i;
-          low = pl;
-        }
-        const __half h = __float2half_rn(d);
-        to[0] = h;
-        to[low] = __float2half_rn(d - __half2float(h));
-      }
-  }
-}
-
 template <typename K, typename... A>
 cudaError_t launch(K kern, dim3 grid, cudaStream_t s, const A&... args) {
   cudaLaunchConfig_t cfg = {};
@@ -208,9 +146,6 @@ cudaError_t launch_muon_squares(const MuonGroup& g, cudaStream_t s) {
 }
 cudaError_t launch_muon_begin(const MuonGroup& g, cudaStream_t s) {
   return launch(muon_begin, dim3((unsigned)g.parts, (unsigned)g.count), s, g);
-}
-cudaError_t launch_muon_product(const MuonGroup& g, int which, int from, cudaStream_t s) {
-  return launch(muon_product, dim3(608, (unsigned)g.count), s, g, which, from);
 }
 cudaError_t launch_muon_end(const MuonGroup& g, int from, cudaStream_t s) {
   return launch(muon_end, dim3((unsigned)g.parts, (unsigned)g.count), s, g, from);

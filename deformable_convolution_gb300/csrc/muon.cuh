@@ -10,6 +10,7 @@ namespace dc {
 
 // Matrices of one group of launches.
 constexpr int kMuonMats = 48;
+constexpr int kMuonSplits = 16, kMuonArrivals = 256;
 constexpr int kMuonParts = 304;  // most blocks of the first launch for one matrix
 // Values between the products are kept times 2^12: X and A stay below 2^12 *
 // 1.5 and the polynomial of A below 2^12 * 4, inside a 16-bit float's range,
@@ -29,6 +30,8 @@ struct MuonMat {
   __half* gram;  // [2][side][lds]
   __half* poly;
   float* part;  // sums of squares of the blocks of the first launch
+  float* sums;  // a split gram's sums (muon_sums_bytes) and how many splits of each tile have arrived
+  unsigned int* arrivals;
   int rows, cols, ld, side, lds;
   int parts;    // blocks of the launches over single elements
   bool tall;  // rows > cols: A = X^T X, X = a X + X B
@@ -57,7 +60,8 @@ void muon_plan(MuonGroup* g);
 // (norm + eps) as pairs into x[0].
 cudaError_t launch_muon_squares(const MuonGroup& g, cudaStream_t s);
 cudaError_t launch_muon_begin(const MuonGroup& g, cudaStream_t s);
-// One Newton-Schulz step from x[from] to x[1 - from].
+// A product of a Newton-Schulz step from x[from] to x[1 - from]: which 0: gram, 1: poly, 2: x[1 - from].
+size_t muon_sums_bytes(const MuonMat& t);
 cudaError_t launch_muon_product(const MuonGroup& g, int which, int from, cudaStream_t s);
 // The result in x[from] to out, or to the parameters.
 cudaError_t launch_muon_end(const MuonGroup& g, int from, cudaStream_t s);

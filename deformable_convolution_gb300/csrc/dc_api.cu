@@ -1074,9 +1074,12 @@ void add_matrix(MuonGroup* g, int rows, int cols, char* ws, size_t* at) {
   for (int i = 0; i < 2; ++i) t.x[i] = reinterpret_cast<__half*>(take(4 * (size_t)muon_x_low(t)));
   t.gram = reinterpret_cast<__half*>(take(4 * (size_t)muon_p_low(t)));
   t.poly = reinterpret_cast<__half*>(take(4 * (size_t)muon_p_low(t)));
+  t.gram_diag = reinterpret_cast<float*>(take(t.lds * sizeof(float)));
+  t.poly_diag = reinterpret_cast<float*>(take(t.lds * sizeof(float)));
   t.part = reinterpret_cast<float*>(take(kMuonParts * sizeof(float)));
   t.sums = reinterpret_cast<float*>(take(muon_sums_bytes(t)));
   t.arrivals = reinterpret_cast<unsigned int*>(take(kMuonArrivals * sizeof(unsigned int)));
+  t.done = reinterpret_cast<unsigned int*>(take(3 * sizeof(unsigned int)));
 }
 
 // Workspace of `count` matrices of the sizes size(i): that of the largest group.
@@ -1102,11 +1105,7 @@ dc_status run_muon(MuonGroup& g, cudaStream_t s) {
   muon_plan(&g);
   dc_status st = cuda_status(timed("muon_squares", s, [&] { return launch_muon_squares(g, s); }));
   if (st == DC_OK) st = cuda_status(timed("muon_begin", s, [&] { return launch_muon_begin(g, s); }));
-  static const char* const names[] = {"muon_gram", "muon_poly", "muon_apply"};
-  for (int i = 0; i < 3 * g.steps && st == DC_OK; ++i)
-    st = cuda_status(timed(names[i % 3], s, [&] { return launch_muon_product(g, i % 3, i / 3 % 2, s); }));
-  if (st == DC_OK)
-    st = cuda_status(timed("muon_end", s, [&] { return launch_muon_end(g, g.steps % 2, s); }));
+  if (st == DC_OK) st = cuda_status(timed("muon_steps", s, [&] { return launch_muon_steps(g, s); }));
   return st;
 }
 

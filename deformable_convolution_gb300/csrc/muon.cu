@@ -65,7 +65,7 @@ __global__ void __launch_bounds__(kThreads) muon_begin(const __grid_constant__ M
   float scale;
   if (skipped(g, &scale) || blockIdx.x >= t.parts) return;
   if (blockIdx.x == 0)
-    for (int i = threadIdx.x; i < kMuonArrivals; i += kThreads) t.arrivals[i] = 0u;
+    for (int i = threadIdx.x; i < kMuonArrivals + 3; i += kThreads) (i < kMuonArrivals ? t.arrivals[i] : t.done[i - kMuonArrivals]) = 0u;
   float sum = 0.f;
   for (int i = threadIdx.x; i < t.parts; i += kThreads) sum += t.part[i];
   const float norm = sqrtf(block_sum(sum));
@@ -79,35 +79,6 @@ __global__ void __launch_bounds__(kThreads) muon_begin(const __grid_constant__ M
     __half* x = t.x[0] + r * t.ld + (i - r * t.cols);
     x[0] = h;
     x[muon_x_low(t)] = __float2half_rn(v - __half2float(h));
-  }
-}
-
-__global__ void __launch_bounds__(kThreads) muon_end(const __grid_constant__ MuonGroup g, int from) {
-  pdl_wait();
-  pdl_release();
-  const MuonMat& t = g.mat[blockIdx.y];
-  float scale;
-  if (skipped(g, &scale) || blockIdx.x >= t.parts) return;
-  const float lr = g.lr_device ? *g.lr_device : g.lr;
-  const float keep = 1.f - lr * t.weight_decay, rate = lr * t.rate;
-  const long long count = (long long)t.rows * t.cols;
-  for (long long i = (long long)blockIdx.x * kThreads + threadIdx.x; i < count; i += (long long)t.parts * kThreads) {
-    const long long r = i / t.cols;
-    const __half* x = t.x[from] + r * t.ld + (i - r * t.cols);
-    const float v = (__half2float(x[0]) + __half2float(x[muon_x_low(t)])) * (1.f / kOrthoScale);
-    if (!g.update) {
-      if (t.out_dtype == DC_BF16)
-        static_cast<__nv_bfloat16*>(t.out)[i] = __float2bfloat16_rn(v);
-      else
-        static_cast<float*>(t.out)[i] = v;
-      continue;
-    }
-    const float p = (t.master ? t.master[i] : load_in(t.param, t.out_dtype, i)) * keep - v * rate;
-    if (t.master) t.master[i] = p;
-    if (t.out_dtype == DC_BF16)
-      static_cast<__nv_bfloat16*>(t.param)[i] = __float2bfloat16_rn(p);
-    else
-      static_cast<float*>(t.param)[i] = p;
   }
 }
 
@@ -147,8 +118,4 @@ cudaError_t launch_muon_squares(const MuonGroup& g, cudaStream_t s) {
 cudaError_t launch_muon_begin(const MuonGroup& g, cudaStream_t s) {
   return launch(muon_begin, dim3((unsigned)g.parts, (unsigned)g.count), s, g);
 }
-cudaError_t launch_muon_end(const MuonGroup& g, int from, cudaStream_t s) {
-  return launch(muon_end, dim3((unsigned)g.parts, (unsigned)g.count), s, g, from);
-}
-
 }  // namespace dc

@@ -9,7 +9,7 @@
 namespace dc {
 
 // Matrices of one group of launches.
-constexpr int kMuonMats = 48;
+constexpr int kMuonMats = 40;
 constexpr int kMuonSplits = 16, kMuonArrivals = 256;
 constexpr int kMuonParts = 304;  // most blocks of the first launch for one matrix
 // Values between the products are kept times 2^12: X and A stay below 2^12 *
@@ -27,11 +27,14 @@ struct MuonMat {
   float* m;
   // pairs of 16-bit floats, the low parts `x_low` (p_low) values after the high ones
   __half* x[2];  // [2][rows][ld]
-  __half* gram;  // [2][side][lds]
+  __half* gram;  // [2][side][lds], the diagonals apart in float32 [lds]
   __half* poly;
+  float* gram_diag;
+  float* poly_diag;
   float* part;  // sums of squares of the blocks of the first launch
   float* sums;  // a split gram's sums (muon_sums_bytes) and how many splits of each tile have arrived
   unsigned int* arrivals;
+  unsigned int* done;  // CTAs' finished tiles: of gram, poly and X
   int rows, cols, ld, side, lds;
   int parts;    // blocks of the launches over single elements
   bool tall;  // rows > cols: A = X^T X, X = a X + X B
@@ -57,13 +60,11 @@ __host__ __device__ inline long long muon_p_low(const MuonMat& t) { return (long
 // What the launches of a group share, from its matrices.
 void muon_plan(MuonGroup* g);
 // Sums of squares of the matrix (a Muon step: m updated); then X times 2^12 /
-// (norm + eps) as pairs into x[0].
+// (norm + eps) as pairs into x[0], and the counts at 0.
 cudaError_t launch_muon_squares(const MuonGroup& g, cudaStream_t s);
 cudaError_t launch_muon_begin(const MuonGroup& g, cudaStream_t s);
-// A product of a Newton-Schulz step from x[from] to x[1 - from]: which 0: gram, 1: poly, 2: x[1 - from].
+// All steps; the result to out, or to the parameters.
+cudaError_t launch_muon_steps(const MuonGroup& g, cudaStream_t s);
 size_t muon_sums_bytes(const MuonMat& t);
-cudaError_t launch_muon_product(const MuonGroup& g, int which, int from, cudaStream_t s);
-// The result in x[from] to out, or to the parameters.
-cudaError_t launch_muon_end(const MuonGroup& g, int from, cudaStream_t s);
 
 }  // namespace dc

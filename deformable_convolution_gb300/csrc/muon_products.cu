@@ -1,24 +1,36 @@
-// The products of the Newton-Schulz steps on the 5th-generation tensor cores.
+// The Newton-Schulz steps on the 5th-generation tensor cores, all of them in
+// one launch.
 //
 // X (rows x cols, kept times 2^12 as a pair of 16-bit floats, high and low
 // part) goes through
-//   gram: A = X X^T          (tall: X^T X)
-//   poly: P = b A + c A A
-//   apply: X' = a X + P X    (tall: a X + X P)
-// with float32 accumulators.  A factor's two parts hold 22 bits or more; a
-// product of pairs is high high + high low + low high, three MMAs on tiles that
-// are loaded once (low low is below the last bit kept).  DC_ORTHO_16 takes X's
-// high part alone: one MMA for A and two for P X; A A keeps all three, it is
-// the small product of a long matrix.
+//   gram: A = X X^T                  (tall: X^T X)        A = R + diag(d)
+//   poly: P = b A + c A A                                 P = S + diag(e)
+//   apply: X' = a X + P X            (tall: a X + X P)
+// with float32 accumulators.  The diagonals d and e are kept apart in float32:
+//   R R gives A A = R R + (d_i + d_j) R + diag(d^2), and P X = S X + diag(e) X,
+// so what is rounded to 16 bits for a product is the part off the diagonal,
+// small where the rows come close to being orthogonal.  DC_ORTHO_16 multiplies
+// the high parts (11 bits): relative error 1e-3 or less for gradients and
+// random matrices from 64 x 64 to 1024 x 1024, against 2e-3 .. 4e-3 with the
+// diagonal left in.  DC_ORTHO_32 (and a side under 64) adds high low + low high on the same tiles (low low is
+// below the last bit kept), in an accumulator of their own: these terms are
+// 2^-11 of the others, and an accumulator that the tensor cores truncate after
+// every step is truncated a third as often.
 //
-// All of a group's matrices run in one launch of each kind.  CTAs work in
-// pairs on tiles of 256 x BN (tc_pair.cuh), persistent.  A and P are symmetric:
-// of their tiles only those that reach below the diagonal are computed, and
-// what lies below a diagonal block is stored at its mirrored place too.  X
-// enters as it lies, whichever side is contracted: the tensor cores read 16-bit
-// tiles in both orders.  A gram of few tiles splits its long side over several
-// pairs: each leaves its sums in the workspace, the last one to arrive adds
-// them up in order (no result depends on who that is).
+// CTAs work in pairs on tiles of 256 x bn (tc_pair.cuh).  A and P are
+// symmetric: of their tiles only those that reach below the diagonal are
+// computed, and what lies left of a diagonal block is stored at its mirrored
+// place too.  X enters as it lies, whichever side is contracted: the tensor
+// cores read 16-bit tiles in both orders.  A gram of few tiles splits its long
+// side over several pairs: each leaves its sums in the workspace, the last one
+// to arrive adds them up in order (no result depends on who that is).
+//
+// The launch is cooperative and walks one list of tiles, step by step, kind by
+// kind, matrix by matrix, dealt to the pairs in turn; a tile waits (on a count
+// in the workspace) for its own matrix's tiles of the kind before it.  Those
+// stand before it in the list, so the first unfinished tile never waits.  A
+// launch for each of the 15 kinds and steps took 6 to 7 us where the matrices
+// are small (prologue, drain and cold caches each time), a wait takes 2.
 //
 // Warps of each CTA: 0-7 results, 8 TMA loads, 9 (of the first CTA) MMAs.
 #include <cuda.h>
@@ -36,82 +48,118 @@ using namespace pair;
 
 constexpr int kBK = 64, kBox = 64 * 128;  // a box: 64 lines of 64 elements
 constexpr int kEpiWarps = 8, kWarpTma = 8, kWarpMma = 9, kThreads = 320;
+constexpr int kPart = 2 * kBox;           // one part of a factor in a stage: 128 lines
+constexpr int kStage = 2 * kPart;         // one part of both factors
+constexpr int kStages = 5, kRing = kStages * kStage;
+constexpr int kBuf = 4096;                // a warp's 32 x 32 results, and as much for their own terms
+constexpr size_t kSmem = 1024 + kRing + kEpiWarps * 2 * kBuf + 256;
+static_assert(kSmem <= 227 * 1024, "shared memory");
+enum { GRAM = 0, POLY = 1, APPLY = 2 };
 
 struct Item {
-  CUtensorMap a, b;
-  const __half* add;  // the pair that the result's own term comes from (poly, apply)
-  __half* out;
-  float* part;        // splits: sums of [split][tile][rank], else null
-  unsigned int* count;
-  long long ld, low;  // of add and out
-  int rows, cols, nkb, tiles_n, tiles, splits, per_split;
-  int start;          // first work item
-  int a_mn, b_mn;     // the contracted side is the factor's rows
-  int a_low, b_low;   // the factor's low part is used
+  CUtensorMap x[2], gram, poly;
+  MuonMat m;
+  int start[3];                // first tile in the lists of the kinds
+  int tiles[3], tiles_n[3], bn[3];
+  int splits, per_split;       // of gram, in blocks of 64
+  int vec;                     // the result's rows are whole 16-byte pieces
+  int pairs;                   // the low parts are multiplied
 };
 
 template <int CAP>
 struct Items {
-  int which, count, work;
+  int count, steps;
+  int n[3];                    // tiles of a kind (gram: of its splits) in one step
+  bool update;
+  float lr;
+  const float* grad_scale;
+  const float* lr_device;
   Item item[CAP];
 };
 
-template <int BN>
-struct Cfg {
-  static constexpr int kA = 2 * kBox, kB = BN / 128 * kBox;  // one part of a factor in a stage
-  static constexpr int kStage = 2 * (kA + kB);
-  static constexpr int kStages = BN == 256 ? 3 : 4;
-  static constexpr size_t kSmem = 1024 + (size_t)kStages * kStage + 256;
-};
+static_assert(sizeof(Items<kMuonMats>) <= 32 * 1024 - 4, "kernel arguments");
 
 // Of the tiles of a symmetric result those that reach below the diagonal, row
-// of tiles by row: row i has min(tiles_n, (i + 1) * 256 / BN) of them.
-template <int BN>
-__host__ __device__ inline int lower_tiles(int rows, int tiles_n) {
+// of tiles by row: row i has min(tiles_n, (i + 1) * 256 / bn) of them.
+int lower_tiles(int rows, int tiles_n, int bn) {
   int n = 0;
-  for (int i = 0; i * 256 < rows; ++i) n += (i + 1) * (256 / BN) < tiles_n ? (i + 1) * (256 / BN) : tiles_n;
+  for (int i = 0; i * 256 < rows; ++i) n += (i + 1) * (256 / bn) < tiles_n ? (i + 1) * (256 / bn) : tiles_n;
   return n;
 }
 
 struct Tile {
   const Item* t;
-  int index, m0, n0, split, begin, end;
+  int which, step, index, m0, n0, bn, split, begin, end;
 };
 
-template <int BN, int CAP>
+template <int CAP>
 __device__ __forceinline__ Tile tile_of(const Items<CAP>& g, int w) {
+  Tile q;
+  const int per = g.n[0] + g.n[1] + g.n[2];
+  q.step = w / per;
+  int r = w - q.step * per;
+  q.which = GRAM;
+  if (r >= g.n[0]) {
+    r -= g.n[0];
+    q.which = POLY;
+    if (r >= g.n[1]) {
+      r -= g.n[1];
+      q.which = APPLY;
+    }
+  }
   int lo = 0, hi = g.count - 1;
   while (lo < hi) {
     const int mid = (lo + hi + 1) >> 1;
-    if (g.item[mid].start <= w)
+    if (g.item[mid].start[q.which] <= r)
       lo = mid;
     else
       hi = mid - 1;
   }
-  Tile q;
   q.t = &g.item[lo];
   const Item& t = *q.t;
-  int r = w - t.start;
-  q.split = r / t.tiles;
-  r -= q.split * t.tiles;
+  r -= t.start[q.which];
+  q.bn = t.bn[q.which];
+  q.split = 0;
+  q.begin = 0;
+  q.end = (t.m.side + kBK - 1) / kBK;
+  if (q.which == GRAM) {
+    q.split = r / t.tiles[GRAM];
+    r -= q.split * t.tiles[GRAM];
+    q.begin = q.split * t.per_split;
+    q.end = min(((t.m.tall ? t.m.rows : t.m.cols) + kBK - 1) / kBK, q.begin + t.per_split);
+  }
   q.index = r;
-  if (g.which == 2) {
-    const int i = r / t.tiles_n;
-    q.m0 = i * 256;
-    q.n0 = (r - i * t.tiles_n) * BN;
+  int i = 0;
+  const int tn = t.tiles_n[q.which];
+  if (q.which == APPLY) {
+    i = r / tn;
+    r -= i * tn;
   } else {
-    int i = 0;
     for (;; ++i) {
-      const int n = min(t.tiles_n, (i + 1) * (256 / BN));
+      const int n = min(tn, (i + 1) * (256 / q.bn));
       if (r < n) break;
       r -= n;
     }
-    q.m0 = i * 256;
-    q.n0 = r * BN;
   }
-  q.begin = q.split * t.per_split;
-  q.end = min(t.nkb, q.begin + t.per_split);
+  q.m0 = i * 256;
+  q.n0 = r * q.bn;
   return q;
+}
+
+// The tiles that this one reads are done: all CTAs' of the kind before it (of
+// gram: of the step before it).
+__device__ __forceinline__ bool inputs_done(const Tile& q) {
+  const int before = q.which == GRAM ? APPLY : q.which - 1;
+  const unsigned int want = 2u * (unsigned)q.t->tiles[before] * (unsigned)(q.which == GRAM ? q.step : q.step + 1);
+  const unsigned int* count = q.t->m.done + before;
+  for (uint32_t i = 0; i < (1u << 22); ++i) {
+    unsigned int v;
+    asm volatile("ld.acquire.gpu.global.u32 %0, [%1];" : "=r"(v) : "l"(count) : "memory");
+    if (v >= want) return true;
+    __nanosleep(20);
+  }
+  atomicOr(&g_muon_error, 1u);
+  return false;
 }
 
 __device__ __forceinline__ void umma_f16(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
@@ -120,12 +168,6 @@ __device__ __forceinline__ void umma_f16(uint32_t d, uint64_t a, uint64_t b, uin
       " tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n}\n" ::"r"(d),
       "l"(a), "l"(b), "r"(idesc), "r"(accumulate)
       : "memory");
-}
-
-// A value as high and low part.
-__device__ __forceinline__ void to_pair(float v, __half* hi, __half* lo) {
-  *hi = __float2half_rn(v);
-  *lo = __float2half_rn(v - __half2float(*hi));
 }
 
 __device__ __forceinline__ void epi_barrier() { asm volatile("bar.sync 1, 256;" ::: "memory"); }
@@ -139,27 +181,121 @@ __device__ __forceinline__ bool epi_all(bool ok) {
       : "memory");
   return r != 0;
 }
+// Generic and asynchronous accesses to global memory, in order.
+__device__ __forceinline__ void fence_global_proxies() { asm volatile("fence.proxy.async.global;" ::: "memory"); }
 
-template <int BN, int CAP>
-__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
-    muon_mm(const __grid_constant__ Items<CAP> g) {
-  using C = Cfg<BN>;
+// Eight values as high and low parts.
+union Halves {
+  __half h[8];
+  uint4 q;
+};
+__device__ __forceinline__ void to_pairs(const float* v, Halves* hi, Halves* lo) {
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    hi->h[i] = __float2half_rn(v[i]);
+    lo->h[i] = __float2half_rn(v[i] - __half2float(hi->h[i]));
+  }
+}
+__device__ __forceinline__ void from_pairs(uint4 hi, uint4 lo, float* v) {
+  const __half2* h = reinterpret_cast<const __half2*>(&hi);
+  const __half2* l = reinterpret_cast<const __half2*>(&lo);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float2 a = __half22float2(h[i]), b = __half22float2(l[i]);
+    v[2 * i] = a.x + b.x;
+    v[2 * i + 1] = a.y + b.y;
+  }
+}
+
+// A warp's 32 x 32 results in shared memory: row r's 16-byte piece u stands at
+// u ^ swizzle(r), so that rows' pieces, pairs of them and columns are read and
+// written without two lanes in a bank.
+__device__ __forceinline__ int swizzle(int r) { return ((r & 7) ^ ((r >> 3) << 1)) & 7; }
+
+// The result of the last step: eight values of row r from column c on, written
+// out or subtracted from the parameters.
+template <int CAP>
+__device__ __forceinline__ void write_result(const Items<CAP>& g, const Item& t, float lr, int r, int c, const float* x) {
+  const long long at = (long long)r * t.m.cols + c;
+  float v[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) v[i] = x[i] * (1.f / kOrthoScale);
+  const bool bf16 = t.m.out_dtype == DC_BF16;
+  void* out = g.update ? t.m.param : t.m.out;
+  if (g.update) {
+    const float keep = 1.f - lr * t.m.weight_decay, rate = lr * t.m.rate;
+    float p[8];
+    if (t.vec) {
+      if (t.m.master || !bf16) {
+        const float4* f = reinterpret_cast<const float4*>((t.m.master ? t.m.master : static_cast<float*>(out)) + at);
+        const float4 a = __ldcg(f), b = __ldcg(f + 1);
+        p[0] = a.x, p[1] = a.y, p[2] = a.z, p[3] = a.w, p[4] = b.x, p[5] = b.y, p[6] = b.z, p[7] = b.w;
+      } else {
+        const uint4 a = __ldcg(reinterpret_cast<const uint4*>(static_cast<__nv_bfloat16*>(out) + at));
+        const uint32_t w[4] = {a.x, a.y, a.z, a.w};
+#pragma unroll
+        for (int i = 0; i < 8; ++i) p[i] = __uint_as_float(i & 1 ? w[i >> 1] & 0xffff0000u : w[i >> 1] << 16);
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        p[i] = c + i >= t.m.cols ? 0.f
+               : t.m.master      ? t.m.master[at + i]
+               : bf16            ? __bfloat162float(static_cast<__nv_bfloat16*>(out)[at + i])
+                                 : static_cast<float*>(out)[at + i];
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = p[i] * keep - v[i] * rate;
+  }
+  if (t.vec) {
+    if (!bf16 || (g.update && t.m.master)) {
+      float4* f = reinterpret_cast<float4*>((bf16 ? t.m.master : static_cast<float*>(out)) + at);
+      f[0] = make_float4(v[0], v[1], v[2], v[3]);
+      f[1] = make_float4(v[4], v[5], v[6], v[7]);
+    }
+    if (bf16) {
+      uint32_t w[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const __nv_bfloat162 h = __floats2bfloat162_rn(v[2 * i], v[2 * i + 1]);
+        w[i] = *reinterpret_cast<const uint32_t*>(&h);
+      }
+      *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(out) + at) = make_uint4(w[0], w[1], w[2], w[3]);
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      if (c + i < t.m.cols) {
+        if (!bf16 || (g.update && t.m.master)) (bf16 ? t.m.master : static_cast<float*>(out))[at + i] = v[i];
+        if (bf16) static_cast<__nv_bfloat16*>(out)[at + i] = __float2bfloat16_rn(v[i]);
+      }
+    }
+  }
+}
+
+template <int CAP>
+__global__ void __launch_bounds__(kThreads, 1) muon_steps(const __grid_constant__ Items<CAP> g) {
   extern __shared__ unsigned char smem_raw[];
   unsigned char* smem = px::align1024(smem_raw);
-  uint64_t* full = reinterpret_cast<uint64_t*>(smem + C::kStages * C::kStage);
-  uint64_t* empty = full + C::kStages;
-  uint64_t* tfull = empty + C::kStages;
+  unsigned char* stg = smem + kRing;
+  uint64_t* full = reinterpret_cast<uint64_t*>(stg + kEpiWarps * 2 * kBuf);
+  uint64_t* empty = full + kStages;
+  uint64_t* tfull = empty + kStages;
   uint64_t* drained = tfull + 2;
   uint32_t* holder = reinterpret_cast<uint32_t*>(drained + 2);
   uint32_t* arrived = holder + 1;
 
+  // a step whose scale is not finite is skipped, by all alike
+  if (g.update && g.grad_scale && !(fabsf(*g.grad_scale) <= 3.402823466e38f)) return;
+
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t rank = cta_rank();
   const int first = (int)blockIdx.x >> 1, stride = (int)gridDim.x >> 1;
+  const int work = (g.n[0] + g.n[1] + g.n[2]) * g.steps;
 
   if (warp == 0) tmem_alloc(holder);
   if (threadIdx.x == 32) {
-    for (int s = 0; s < C::kStages; ++s) {
+    for (int s = 0; s < kStages; ++s) {
       mbar_init(&full[s], 1);
       mbar_init(&empty[s], 1);
     }
@@ -175,119 +311,216 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   tc_after();
   const uint32_t tmem = *holder;
   bool ok = true;
-  pdl_wait();
-  pdl_release();
 
+  // A tile's accumulators: two of them by turns, or, where 256 columns hold
+  // high high and 256 the cross terms, one.  j: this pair's tiles so far; uses
+  // of the buffers are counted apart, since widths may change from tile to tile:
+  // every tile waits for the tile before last to be read, a wide one with cross
+  // terms, or one after such a tile, for the last one.
   if (warp == kWarpTma) {
     if (lane == 0) {
-      int it = 0;
-      for (int w = first; w < g.work && ok; w += stride) {
-        const Tile q = tile_of<BN>(g, w);
-        const Item& t = *q.t;
-        const int m0 = q.m0 + (int)rank * 128, n0 = q.n0 + (int)rank * (BN / 2);
-        const uint32_t bytes = 2u * (C::kA * (1 + t.a_low) + C::kB * (1 + t.b_low));
-        for (int kb = q.begin; kb < q.end; ++kb, ++it) {
-          const int s = it % C::kStages;
-          if (it >= C::kStages && !mbar_wait(&empty[s], ((it / C::kStages) - 1) & 1, &g_muon_error)) {
-            ok = false;
-            break;
+      int s = 0, round = 0;
+      for (int w = first; w < work && ok; w += stride) {
+        const Tile q = tile_of(g, w);
+        const MuonMat& m = q.t->m;
+        if (!inputs_done(q)) {
+          ok = false;
+          break;
+        }
+        fence_global_proxies();
+        // factors and whether their contracted side runs across lines
+        const CUtensorMap* x = &q.t->x[q.step & 1];
+        const CUtensorMap* ta = q.which == GRAM ? x : q.which == POLY ? &q.t->gram : m.tall ? x : &q.t->poly;
+        const CUtensorMap* tb = q.which == GRAM ? x : q.which == POLY ? &q.t->gram : m.tall ? &q.t->poly : x;
+        const bool a_mn = q.which == GRAM && m.tall, b_mn = (q.which == GRAM && m.tall) || (q.which == APPLY && !m.tall);
+        const int m0 = q.m0 + (int)rank * 128, n0 = q.n0 + (int)rank * (q.bn / 2), nb = q.bn / 128;
+        const uint32_t bytes = 2u * (uint32_t)(2 + nb) * kBox;
+        const int parts = 1 + q.t->pairs;
+        for (int kb = q.begin; kb < q.end && ok; ++kb) {
+          // the high parts in one stage, the low ones in the next
+          for (int p = 0; p < parts; ++p) {
+            if (round && !mbar_wait(&empty[s], (round - 1) & 1, &g_muon_error)) {
+              ok = false;
+              break;
+            }
+            const uint32_t bar = in_cta(smem_u32(&full[s]), 0);
+            if (rank == 0) mbar_expect_tx(&full[s], bytes);
+            const uint32_t sa = smem_u32(smem + s * kStage), sb = sa + kPart;
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              tma_load(sa + h * kBox, ta, bar, a_mn ? m0 + 64 * h : kb * kBK, a_mn ? kb * kBK : m0 + 64 * h, p);
+              if (h < nb) tma_load(sb + h * kBox, tb, bar, b_mn ? n0 + 64 * h : kb * kBK, b_mn ? kb * kBK : n0 + 64 * h, p);
+            }
+            if (++s == kStages) s = 0, ++round;
           }
-          const uint32_t bar = in_cta(smem_u32(&full[s]), 0);
-          if (rank == 0) mbar_expect_tx(&full[s], bytes);
-          const uint32_t sa = smem_u32(smem + s * C::kStage), sb = sa + 2 * C::kA;
-          for (int p = 0; p <= t.a_low; ++p)
-#pragma unroll
-            for (int h = 0; h < 2; ++h)
-              tma_load(sa + p * C::kA + h * kBox, &t.a, bar, t.a_mn ? m0 + 64 * h : kb * kBK,
-                       t.a_mn ? kb * kBK : m0 + 64 * h, p);
-          for (int p = 0; p <= t.b_low; ++p)
-#pragma unroll
-            for (int h = 0; h < BN / 128; ++h)
-              tma_load(sb + p * C::kB + h * kBox, &t.b, bar, t.b_mn ? n0 + 64 * h : kb * kBK,
-                       t.b_mn ? kb * kBK : n0 + 64 * h, p);
         }
       }
       if (!ok) let_copies_land();
     }
   } else if (warp == kWarpMma) {
     if (rank == 0 && lane == 0) {
-      int it = 0, j = 0;
-      for (int w = first; w < g.work && ok; w += stride, ++j) {
-        const Tile q = tile_of<BN>(g, w);
-        const int a_mn = q.t->a_mn, b_mn = q.t->b_mn, a_low = q.t->a_low, b_low = q.t->b_low;
-        if (j >= 2 && !mbar_wait(&drained[j & 1], ((j >> 1) - 1) & 1, &g_muon_error)) {
+      int s = 0, round = 0, j = 0;
+      bool alone = false;  // the last tile took all columns
+      for (int w = first; w < work && ok; w += stride, ++j) {
+        const Tile q = tile_of(g, w);
+        const bool a_mn = q.which == GRAM && q.t->m.tall;
+        const bool b_mn = (q.which == GRAM && q.t->m.tall) || (q.which == APPLY && !q.t->m.tall);
+        const int pairs = q.t->pairs;
+        const bool whole = pairs && q.bn == 256;
+        // (tiles are read in turn: the last one's reading follows the one's before it)
+        const int before = j - (whole || alone ? 1 : 2);
+        alone = whole;
+        if (before >= 0 && !mbar_wait(&drained[before & 1], (before >> 1) & 1, &g_muon_error)) {
           ok = false;
           break;
         }
         tc_after();
-        const uint32_t acc = tmem + (j & 1) * 256;
+        const uint32_t acc = tmem + (whole ? 0 : (j & 1) * 256), cross = acc + q.bn;
         const uint32_t idesc = (1u << 4) | ((uint32_t)a_mn << 15) | ((uint32_t)b_mn << 16) |
-                               ((uint32_t)(BN >> 3) << 17) | ((256u >> 4) << 24);
-        for (int kb = q.begin; kb < q.end; ++kb, ++it) {
-          const int s = it % C::kStages;
-          if (!mbar_wait(&full[s], (it / C::kStages) & 1, &g_muon_error)) {
+                               ((uint32_t)(q.bn >> 3) << 17) | ((256u >> 4) << 24);
+        for (int kb = q.begin; kb < q.end; ++kb) {
+          const int s0 = s, round0 = round;
+          int s1 = s0;
+          if (++s == kStages) s = 0, ++round;
+          bool here = mbar_wait(&full[s0], round0 & 1, &g_muon_error);
+          if (pairs) {
+            s1 = s;
+            here = here && mbar_wait(&full[s1], round & 1, &g_muon_error);
+            if (++s == kStages) s = 0, ++round;
+          }
+          if (!here) {
             ok = false;
             break;
           }
           tc_after();
-          const uint32_t sa = smem_u32(smem + s * C::kStage), sb = sa + 2 * C::kA;
-#pragma unroll
-          for (int p = 0; p < 3; ++p) {  // high high, high low, low high
-            if ((p == 1 && !b_low) || (p == 2 && !a_low)) continue;
-            const uint32_t pa = sa + (p == 2 ? C::kA : 0), pb = sb + (p == 1 ? C::kB : 0);
+          const uint32_t high = smem_u32(smem + s0 * kStage), low = smem_u32(smem + s1 * kStage);
+          for (int p = 0; p < (pairs ? 3 : 1); ++p) {  // high high, high low, low high
+            const uint32_t pa = p == 2 ? low : high, pb = (p == 1 ? low : high) + kPart;
 #pragma unroll
             for (int k = 0; k < kBK / 16; ++k) {
               // along lines: 32 bytes on; across them: 16 lines on
               const uint64_t da = a_mn ? sdesc(pa + k * 2048, kBox, 1024) : sdesc(pa + k * 32, 16, 1024);
               const uint64_t db = b_mn ? sdesc(pb + k * 2048, kBox, 1024) : sdesc(pb + k * 32, 16, 1024);
-              umma_f16(acc, da, db, idesc, (kb > q.begin || p > 0 || k > 0) ? 1u : 0u);
+              umma_f16(p ? cross : acc, da, db, idesc, (kb > q.begin || p > 1 || k > 0) ? 1u : 0u);
             }
           }
-          commit_both(&empty[s]);
+          commit_both(&empty[s0]);
+          if (pairs) commit_both(&empty[s1]);
         }
         commit_both(&tfull[j & 1]);
       }
     }
   } else {
     const int quad = warp & 3, half = warp >> 2;
-    constexpr int kChunks = BN / 64;  // of 32 columns, for each half of the columns
+    float* buf = reinterpret_cast<float*>(stg + warp * 2 * kBuf);
+    const unsigned char* terms = reinterpret_cast<const unsigned char*>(buf) + kBuf;
+    const float lr = g.lr_device ? *g.lr_device : g.lr;
+    const int sub = lane >> 2, piece = lane & 3;  // eight columns of a row for a lane, rows 8 i + sub
     int j = 0;
-    for (int w = first; w < g.work; w += stride, ++j) {
-      const Tile q = tile_of<BN>(g, w);
+    for (int w = first; w < work; w += stride, ++j) {
+      const Tile q = tile_of(g, w);
       const Item& t = *q.t;
+      const MuonMat& m = t.m;
+      const int rows = q.which == APPLY ? m.rows : m.side, cols = q.which == APPLY ? m.cols : m.side;
+      const long long ld = q.which == APPLY ? m.ld : m.lds;
+      const long long low = q.which == APPLY ? muon_x_low(m) : muon_p_low(m);
+      const __half* add = q.which == POLY ? m.gram : m.x[q.step & 1];
+      __half* out = q.which == GRAM ? m.gram : q.which == POLY ? m.poly : m.x[1 - (q.step & 1)];
+      const bool last_step = q.which == APPLY && q.step + 1 == g.steps;
+      const bool store_low = q.which != POLY || t.pairs;
+      const int chunks = q.bn / 64;  // of 32 columns, for each half of the columns
+      const int row0 = q.m0 + (int)rank * 128 + quad * 32;
+      const bool whole = t.pairs && q.bn == 256;
+      const uint32_t acc = tmem + (whole ? 0 : (j & 1) * 256) + ((uint32_t)(quad * 32) << 16);
+      const bool split = q.which == GRAM && t.splits > 1;
+
+      // The result is mul * sum + (c0 + cr * row's diagonal + cc * column's) *
+      // own term: X, or R.  Terms come through shared memory by asynchronous
+      // copies, a chunk ahead; a lane reads those that it copied.
+      const bool tall_apply = q.which == APPLY && m.tall;
+      const float unit = 1.f / kOrthoScale;
+      const float mul = q.which == POLY ? kOrthoC * unit : unit;
+      const float c0 = q.which == POLY ? kOrthoB : kOrthoA;
+      const float cr = q.which == POLY ? kOrthoC : tall_apply ? 0.f : 1.f;
+      const float cc = q.which == POLY ? kOrthoC : tall_apply ? 1.f : 0.f;
+      const float* diag = q.which == POLY ? m.gram_diag : m.poly_diag;
+      float row_diag = 0.f, col_diag[8], next_diag[8];  // row_diag: of row `lane`
+      auto load_terms = [&](int c) {
+        const int col = q.n0 + (half * chunks + c) * 32 + 8 * piece;
+        if (q.which != GRAM && col < cols) {
+          const __half* from = add + (row0 + sub) * ld + col;
+          const uint32_t to = smem_u32(terms) + lane * 16;
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            if (row0 + 8 * i + sub < rows) {
+              asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to + i * 512), "l"(from + 8 * i * ld) : "memory");
+              asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to + i * 512 + 2048), "l"(from + 8 * i * ld + low)
+                           : "memory");
+            }
+          }
+          if (cc != 0.f) {
+            const float4 a = __ldcg(reinterpret_cast<const float4*>(diag + col));
+            const float4 b = __ldcg(reinterpret_cast<const float4*>(diag + col) + 1);
+            next_diag[0] = a.x, next_diag[1] = a.y, next_diag[2] = a.z, next_diag[3] = a.w;
+            next_diag[4] = b.x, next_diag[5] = b.y, next_diag[6] = b.z, next_diag[7] = b.w;
+          }
+        }
+      };
+#pragma unroll
+      for (int k = 0; k < 8; ++k) next_diag[k] = 0.f;
+      bool here = true;
+      if (lane == 0) here = inputs_done(q);
+      here = __all_sync(0xffffffffu, here);
+      if (here) {
+        if (q.which != GRAM && cr != 0.f && row0 + lane < rows) row_diag = __ldcg(diag + row0 + lane);
+        load_terms(0);
+      }
       // (all warps go on or none: they meet at barriers below)
-      ok = epi_all(mbar_wait(&tfull[j & 1], (j >> 1) & 1, &g_muon_error));
+      ok = epi_all(here && mbar_wait(&tfull[j & 1], (j >> 1) & 1, &g_muon_error));
       if (!ok) break;
       tc_after();
-      const uint32_t acc = tmem + (j & 1) * 256 + ((uint32_t)(quad * 32) << 16);
-      const int row = q.m0 + (int)rank * 128 + quad * 32 + lane;
-      const bool split = t.splits > 1;
-      // this CTA's sums of a split, 16-byte pieces in the order that warps hold them
+
+      auto results = [&](int c, uint32_t* r) {
+        const uint32_t at = acc + (half * chunks + c) * 32;
+        tmem_ld32(at, r);
+        if (t.pairs) {
+          uint32_t x[32];
+          tmem_ld32(at + q.bn, x);
+          tmem_ld_wait();
+#pragma unroll
+          for (int v = 0; v < 32; ++v) r[v] = __float_as_uint(__uint_as_float(r[v]) + __uint_as_float(x[v]));
+        } else {
+          tmem_ld_wait();
+        }
+      };
+      auto release = [&] {
+        tc_before();
+        __syncwarp();
+        if (lane == 0) arrive_at(in_cta(smem_u32(&drained[j & 1]), 0));
+      };
+      // a split's sums of this CTA, 16-byte pieces in the order that warps hold them
       auto place = [&](int k, int c) {
-        return reinterpret_cast<float4*>(t.part) +
-               (((((long long)k * t.tiles + q.index) * 2 + rank) * kEpiWarps + warp) * kChunks + c) * 256 + lane;
+        return reinterpret_cast<float4*>(m.sums) +
+               (((((long long)k * t.tiles[GRAM] + q.index) * 2 + rank) * kEpiWarps + warp) * chunks + c) * 256 + lane;
       };
       if (split) {
 #pragma unroll 1
-        for (int c = 0; c < kChunks; ++c) {
+        for (int c = 0; c < chunks; ++c) {
           uint32_t r[32];
-          tmem_ld32(acc + (half * kChunks + c) * 32, r);
-          tmem_ld_wait();
+          results(c, r);
           float4* to = place(q.split, c);
 #pragma unroll
           for (int v = 0; v < 8; ++v)
             __stcg(to + 32 * v, make_float4(__uint_as_float(r[4 * v]), __uint_as_float(r[4 * v + 1]),
                                             __uint_as_float(r[4 * v + 2]), __uint_as_float(r[4 * v + 3])));
         }
-        tc_before();
-        __syncwarp();
-        if (lane == 0) arrive_at(in_cta(smem_u32(&drained[j & 1]), 0));
-        __threadfence();
+        release();
         epi_barrier();
         if (threadIdx.x == 0) {
-          unsigned int* count = t.count + q.index * 2 + rank;
+          __threadfence();
+          unsigned int* count = m.arrivals + q.index * 2 + rank;
           const unsigned int before = atomicAdd(count, 1u);
-          if (before == (unsigned)t.splits - 1) *count = 0u;  // for the next launch
+          if (before == (unsigned)t.splits - 1) *count = 0u;  // for the next step
           __threadfence();
           *arrived = before;
         }
@@ -297,76 +530,121 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         if (!last) continue;
         __threadfence();
       }
+      const bool mirror = q.which != APPLY && q.n0 + q.bn <= q.m0;
 #pragma unroll 1
-      for (int c = 0; c < kChunks; ++c) {
-        const int col0 = q.n0 + (half * kChunks + c) * 32;
-        float f[32];
+      for (int c = 0; c < chunks; ++c) {
+        const int col0 = q.n0 + (half * chunks + c) * 32, col = col0 + 8 * piece;
+        float4* line = reinterpret_cast<float4*>(buf + lane * 32);
         if (split) {
+          float4 f[8];
 #pragma unroll
-          for (int v = 0; v < 32; ++v) f[v] = 0.f;
+          for (int v = 0; v < 8; ++v) f[v] = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 2
           for (int k = 0; k < t.splits; ++k) {
             const float4* from = place(k, c);
 #pragma unroll
             for (int v = 0; v < 8; ++v) {
               const float4 u = __ldcg(from + 32 * v);
-              f[4 * v] += u.x, f[4 * v + 1] += u.y, f[4 * v + 2] += u.z, f[4 * v + 3] += u.w;
+              f[v].x += u.x, f[v].y += u.y, f[v].z += u.z, f[v].w += u.w;
             }
           }
+#pragma unroll
+          for (int v = 0; v < 8; ++v) line[v ^ swizzle(lane)] = f[v];
         } else {
           uint32_t r[32];
-          tmem_ld32(acc + (half * kChunks + c) * 32, r);
-          tmem_ld_wait();
-          if (c == kChunks - 1) {
-            tc_before();
-            __syncwarp();
-            if (lane == 0) arrive_at(in_cta(smem_u32(&drained[j & 1]), 0));
-          }
+          results(c, r);
+          if (c == chunks - 1) release();
 #pragma unroll
-          for (int v = 0; v < 32; ++v) f[v] = __uint_as_float(r[v]);
+          for (int v = 0; v < 8; ++v)
+            line[v ^ swizzle(lane)] = make_float4(__uint_as_float(r[4 * v]), __uint_as_float(r[4 * v + 1]),
+                                                  __uint_as_float(r[4 * v + 2]), __uint_as_float(r[4 * v + 3]));
         }
-        if (row < t.rows && col0 < t.cols) {
-          const float unit = 1.f / kOrthoScale;
-          const float own = g.which == 1 ? kOrthoB : kOrthoA, mul = g.which == 1 ? kOrthoC * unit : unit;
-          const long long at = (long long)row * t.ld + col0;
-          // eight columns at a time: lines are whole 16-byte pieces, what lies past the last column is of no meaning
 #pragma unroll
-          for (int v = 0; v < 4; ++v) {
-            if (col0 + 8 * v < t.cols) {
-              float e[8];
+        for (int k = 0; k < 8; ++k) col_diag[k] = next_diag[k];
+        asm volatile("cp.async.wait_all;" ::: "memory");
+        __syncwarp();
+        // (rolled: code that runs a few times costs more to fetch than to run)
+#pragma unroll 1
+        for (int i = 0; i < 4; ++i) {
+          const int rl = 8 * i + sub, r = row0 + rl;
+          const float rd = __shfl_sync(0xffffffffu, row_diag, rl);
+          if (r < rows && col < cols) {
+            float4* p0 = reinterpret_cast<float4*>(buf + rl * 32) + ((2 * piece) ^ swizzle(rl));
+            float4* p1 = reinterpret_cast<float4*>(buf + rl * 32) + ((2 * piece + 1) ^ swizzle(rl));
+            const float4 a = *p0, b = *p1;
+            float e[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+            if (q.which == GRAM) {
 #pragma unroll
-              for (int i = 0; i < 8; ++i) e[i] = f[8 * v + i] * mul;
-              if (g.which) {
-                const uint4 hi = __ldcg(reinterpret_cast<const uint4*>(t.add + at + 8 * v));
-                const uint4 lo = __ldcg(reinterpret_cast<const uint4*>(t.add + t.low + at + 8 * v));
-                const __half2* h2 = reinterpret_cast<const __half2*>(&hi);
-                const __half2* l2 = reinterpret_cast<const __half2*>(&lo);
+              for (int k = 0; k < 8; ++k) e[k] *= mul;
+            } else {
+              float x[8];
+              const uint4* own = reinterpret_cast<const uint4*>(terms + i * 512) + lane;
+              from_pairs(own[0], own[128], x);
+              const float f = c0 + cr * rd;
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                  const float2 a = __half22float2(h2[i]), b = __half22float2(l2[i]);
-                  e[2 * i] += own * (a.x + b.x);
-                  e[2 * i + 1] += own * (a.y + b.y);
+              for (int k = 0; k < 8; ++k) e[k] = mul * e[k] + (f + cc * col_diag[k]) * x[k];
+            }
+            if (q.which != APPLY && (unsigned)(r - col) < 8u) {
+              // on the diagonal (where R is 0): b d + c d^2 + the sum's; of gram d is 0 so far
+              float* to = q.which == GRAM ? m.gram_diag : m.poly_diag;
+#pragma unroll
+              for (int k = 0; k < 8; ++k)
+                if (r - col == k) {
+                  to[r] = e[k] * unit + (kOrthoB + kOrthoC * rd) * rd;
+                  e[k] = 0.f;
                 }
-              }
-              union {
-                __half h[8];
-                uint4 q;
-              } hi, lo;
-#pragma unroll
-              for (int i = 0; i < 8; ++i) to_pair(e[i], &hi.h[i], &lo.h[i]);
-              *reinterpret_cast<uint4*>(t.out + at + 8 * v) = hi.q;
-              *reinterpret_cast<uint4*>(t.out + t.low + at + 8 * v) = lo.q;
-              if (g.which != 2 && q.n0 + BN <= q.m0) {  // left of the diagonal block: the mirrored place, 32 rows side by side
-#pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                  __half* m = t.out + (long long)(col0 + 8 * v + i) * t.ld + row;
-                  m[0] = hi.h[i];
-                  m[t.low] = lo.h[i];
-                }
-              }
+            }
+            if (mirror || last_step) {
+              *p0 = make_float4(e[0], e[1], e[2], e[3]);
+              *p1 = make_float4(e[4], e[5], e[6], e[7]);
+            }
+            if (!last_step) {
+              // whole 16-byte pieces: what lies past the last column is of no meaning
+              Halves h, l;
+              to_pairs(e, &h, &l);
+              *reinterpret_cast<uint4*>(out + r * ld + col) = h.q;
+              if (store_low) *reinterpret_cast<uint4*>(out + low + r * ld + col) = l.q;
             }
           }
         }
-        __syncwarp();  // together again for the next columns' read
+        if (c + 1 < chunks) load_terms(c + 1);
+        if (mirror || last_step) {
+          __syncwarp();
+#pragma unroll 1
+          for (int i = 0; i < 4; ++i) {
+            float e[8];
+            if (mirror) {
+              // the mirrored place: eight rows of a column for a lane; columns left of a diagonal block are rows that exist
+              const int cl = 8 * i + sub;
+#pragma unroll
+              for (int k = 0; k < 8; ++k) {
+                const int rl = 8 * piece + k;
+                e[k] = buf[rl * 32 + (((cl >> 2) ^ swizzle(rl)) << 2) + (cl & 3)];
+              }
+              if (row0 + 8 * piece < rows) {
+                Halves h, l;
+                to_pairs(e, &h, &l);
+                __half* to = out + (col0 + cl) * ld + row0 + 8 * piece;
+                *reinterpret_cast<uint4*>(to) = h.q;
+                if (store_low) *reinterpret_cast<uint4*>(to + low) = l.q;
+              }
+            } else {
+              const int rl = 8 * i + sub;
+              const float4 a = reinterpret_cast<const float4*>(buf + rl * 32)[(2 * piece) ^ swizzle(rl)];
+              const float4 b = reinterpret_cast<const float4*>(buf + rl * 32)[(2 * piece + 1) ^ swizzle(rl)];
+              e[0] = a.x, e[1] = a.y, e[2] = a.z, e[3] = a.w, e[4] = b.x, e[5] = b.y, e[6] = b.z, e[7] = b.w;
+              if (row0 + rl < rows && col < cols) write_result(g, t, lr, row0 + rl, col, e);
+            }
+          }
+        }
+        __syncwarp();
+      }
+      // this CTA's part of the tile is done
+      fence_global_proxies();
+      epi_barrier();
+      if (threadIdx.x == 0) {
+        __threadfence();
+        asm volatile("red.relaxed.gpu.global.add.u32 [%0], %1;" ::"l"(m.done + q.which), "r"(1u) : "memory");
       }
     }
   }
@@ -389,18 +667,21 @@ bool pair_map(CUtensorMap* m, const void* base, int rows, int cols, int ld) {
   return make_tmap(m, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, base, 3, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B);
 }
 
-// Tiles of a product of `rows` x `cols`.
 int tiles_of(int which, int bn, int rows, int cols) {
   const int tiles_n = (cols + bn - 1) / bn;
-  if (which == 2) return (rows + 255) / 256 * tiles_n;
-  return bn == 256 ? lower_tiles<256>(rows, tiles_n) : lower_tiles<128>(rows, tiles_n);
+  return which == APPLY ? (rows + 255) / 256 * tiles_n : lower_tiles(rows, tiles_n, bn);
 }
 
-// Splits of a gram's long side: by the matrix's own size (its result does not
-// depend on the matrices beside it), over the pairs that its tiles leave idle,
-// four blocks of 64 or more each.
+// A matrix's tiles and splits go by its own size: its result does not depend on
+// the matrices beside it.  Tiles of 256 x 256 read less of shared memory for
+// each product, those of 256 x 128 fill the pairs better: wide ones where a
+// matrix has enough of them.
+int width_of(int which, int rows, int cols) { return tiles_of(which, 256, rows, cols) >= 32 ? 256 : 128; }
+
+// Splits of a gram's long side: over the pairs that its tiles leave idle, four
+// blocks of 64 or more each.
 int gram_splits(const MuonMat& t) {
-  const int tiles = tiles_of(0, 128, t.side, t.side);
+  const int tiles = tiles_of(GRAM, width_of(GRAM, t.side, t.side), t.side, t.side);
   const int nkb = (int)ceil_div_ll(t.tall ? t.rows : t.cols, kBK);
   int want = kPairs / tiles;
   if (want > nkb / 4) want = nkb / 4;
@@ -408,68 +689,70 @@ int gram_splits(const MuonMat& t) {
   return want < 1 ? 1 : want;
 }
 
-template <int BN, int CAP>
-cudaError_t launch(const MuonGroup& m, int which, int from, cudaStream_t s) {
+template <int CAP>
+cudaError_t launch(const MuonGroup& m, cudaStream_t s) {
   Items<CAP> g;
-  g.which = which;
   g.count = m.count;
-  const int x_low = m.precision == DC_ORTHO_32;  // X's low part is used
-  int work = 0;
+  g.steps = m.steps;
+  g.update = m.update;
+  g.lr = m.lr;
+  g.grad_scale = m.grad_scale;
+  g.lr_device = m.lr_device;
+  g.n[0] = g.n[1] = g.n[2] = 0;
   for (int i = 0; i < m.count; ++i) {
     const MuonMat& t = m.mat[i];
     Item& q = g.item[i];
-    q.rows = which == 2 ? t.rows : t.side;
-    q.cols = which == 2 ? t.cols : t.side;
-    q.ld = which == 2 ? t.ld : t.lds;
-    q.low = which == 2 ? muon_x_low(t) : muon_p_low(t);
-    const int depth = which == 0 ? (t.tall ? t.rows : t.cols) : t.side;
-    q.nkb = (depth + kBK - 1) / kBK;
-    q.add = which == 1 ? t.gram : which == 2 ? t.x[from] : nullptr;
-    q.out = which == 0 ? t.gram : which == 1 ? t.poly : t.x[1 - from];
-    q.tiles_n = (q.cols + BN - 1) / BN;
-    q.tiles = tiles_of(which, BN, q.rows, q.cols);
-    q.a_low = which == 0 || (which == 2 && t.tall) ? x_low : 1;
-    q.b_low = which == 0 || (which == 2 && !t.tall) ? x_low : 1;
-    q.splits = which == 0 ? gram_splits(t) : 1;
-    q.per_split = (int)ceil_div_ll(q.nkb, q.splits);
-    q.splits = (int)ceil_div_ll(q.nkb, q.per_split);
-    q.part = q.splits > 1 ? t.sums : nullptr;
-    q.count = t.arrivals;
-    q.start = work;
-    work += q.tiles * q.splits;
-    bool made = true;
-    if (which == 0) {
-      made = pair_map(&q.a, t.x[from], t.rows, t.cols, t.ld);
-      q.b = q.a;
-      q.a_mn = q.b_mn = t.tall;
-    } else if (which == 1) {
-      made = pair_map(&q.a, t.gram, t.side, t.side, t.lds);
-      q.b = q.a;
-      q.a_mn = q.b_mn = 0;
-    } else {
-      CUtensorMap x, p;
-      made = pair_map(&x, t.x[from], t.rows, t.cols, t.ld) && pair_map(&p, t.poly, t.side, t.side, t.lds);
-      q.a = t.tall ? x : p;
-      q.b = t.tall ? p : x;
-      q.a_mn = 0;
-      q.b_mn = !t.tall;
+    q.m = t;
+    const int nkb = (int)ceil_div_ll(t.tall ? t.rows : t.cols, kBK);
+    q.splits = gram_splits(t);
+    q.per_split = (int)ceil_div_ll(nkb, q.splits);
+    q.splits = (int)ceil_div_ll(nkb, q.per_split);
+    for (int k = 0; k < 3; ++k) {
+      const int rows = k == APPLY ? t.rows : t.side, cols = k == APPLY ? t.cols : t.side;
+      q.bn[k] = width_of(k, rows, cols);
+      q.tiles_n[k] = (cols + q.bn[k] - 1) / q.bn[k];
+      q.tiles[k] = tiles_of(k, q.bn[k], rows, cols);
+      q.start[k] = g.n[k];
+      g.n[k] += q.tiles[k] * (k == GRAM ? q.splits : 1);
     }
-    if (!made) return cudaErrorInvalidValue;
+    const int e = t.out_dtype == DC_BF16 ? 2 : 4;
+    const void* out = m.update ? t.param : t.out;
+    // (products of a short side under 64 cost nothing, and its matrix has few
+    // values for the roundings to average over)
+    q.pairs = m.precision == DC_ORTHO_32 || t.side < 64;
+    q.vec = t.cols % 8 == 0 && (uintptr_t)out % 16 == 0 && (uintptr_t)t.master % 16 == 0 && (t.cols * e) % 16 == 0;
+    if (!pair_map(&q.x[0], t.x[0], t.rows, t.cols, t.ld) || !pair_map(&q.x[1], t.x[1], t.rows, t.cols, t.ld) ||
+        !pair_map(&q.gram, t.gram, t.side, t.side, t.lds) || !pair_map(&q.poly, t.poly, t.side, t.side, t.lds))
+      return cudaErrorInvalidValue;
   }
-  g.work = work;
-  cudaError_t e = cudaFuncSetAttribute(muon_mm<BN, CAP>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)Cfg<BN>::kSmem);
+  cudaError_t e = cudaFuncSetAttribute(muon_steps<CAP>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmem);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(2u * (unsigned)(work < kPairs ? work : kPairs));
+  cfg.gridDim = dim3(2 * kPairs);
   cfg.blockDim = dim3(kThreads);
-  cfg.dynamicSmemBytes = Cfg<BN>::kSmem;
+  cfg.dynamicSmemBytes = kSmem;
   cfg.stream = s;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = 2;
+  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  e = cudaLaunchKernelEx(&cfg, muon_mm<BN, CAP>, g);
+  // pairs that run at once: all of them have to, for tiles wait for one another
+  int most = 0;
+  e = cudaOccupancyMaxActiveClusters(&most, muon_steps<CAP>, &cfg);
+  if (e != cudaSuccess) return e;
+  int widest = 0;  // more pairs than the widest kind of a step has tiles would only wait
+  for (int k = 0; k < 3; ++k)
+    if (g.n[k] > widest) widest = g.n[k];
+  if (most > widest) most = widest;
+  if (most > kPairs) most = kPairs;
+  if (most < 1) return cudaErrorLaunchOutOfResources;
+  cfg.gridDim = dim3(2u * (unsigned)most);
+  attr[1].id = cudaLaunchAttributeCooperative;
+  attr[1].val.cooperative = 1;
+  cfg.numAttrs = 2;
+  e = cudaLaunchKernelEx(&cfg, muon_steps<CAP>, g);
   note_launches(1);
   return e;
 }
@@ -477,24 +760,14 @@ cudaError_t launch(const MuonGroup& m, int which, int from, cudaStream_t s) {
 }  // namespace
 
 size_t muon_sums_bytes(const MuonMat& t) {
-  const int splits = gram_splits(t);
-  if (splits == 1) return 0;
-  const size_t narrow = (size_t)tiles_of(0, 128, t.side, t.side) * 128, wide = (size_t)tiles_of(0, 256, t.side, t.side) * 256;
-  return splits * (narrow > wide ? narrow : wide) * 256 * sizeof(float);
+  const int splits = gram_splits(t), bn = width_of(GRAM, t.side, t.side);
+  return splits > 1 ? (size_t)splits * tiles_of(GRAM, bn, t.side, t.side) * 256 * bn * sizeof(float) : 0;
 }
 
-cudaError_t launch_muon_product(const MuonGroup& g, int which, int from, cudaStream_t s) {
-  // tiles of 256 x 128 fill the pairs better, those of 256 x 256 read less of
-  // shared memory for each product: wide ones where they are enough for two rounds
-  long long wide = 0;
-  for (int i = 0; i < g.count; ++i) {
-    const MuonMat& t = g.mat[i];
-    wide += tiles_of(which, 256, which == 2 ? t.rows : t.side, which == 2 ? t.cols : t.side);
-  }
-  const bool bn256 = wide >= 2 * kPairs;
-  if (g.count <= 2) return bn256 ? launch<256, 2>(g, which, from, s) : launch<128, 2>(g, which, from, s);
-  if (g.count <= 12) return bn256 ? launch<256, 12>(g, which, from, s) : launch<128, 12>(g, which, from, s);
-  return bn256 ? launch<256, kMuonMats>(g, which, from, s) : launch<128, kMuonMats>(g, which, from, s);
+cudaError_t launch_muon_steps(const MuonGroup& g, cudaStream_t s) {
+  if (g.count <= 2) return launch<2>(g, s);
+  if (g.count <= 10) return launch<10>(g, s);
+  return launch<kMuonMats>(g, s);
 }
 
 // This file's share of dc_device_error (2 = unreadable).

@@ -541,11 +541,12 @@ dc_status dc_fp8_matmul(const dc_fp8_product* prob, const void* a, const void* a
  * float32, gives NaN throughout. */
 typedef enum { DC_ORTHO_16 = 0, DC_ORTHO_32 = 1 } dc_ortho_precision;
 /* Between the products X, A and the polynomial of A are held as pairs of
- * 16-bit floats (22 bits or more, fixed point below).  DC_ORTHO_32 multiplies
- * both parts of every factor (the result is as good as float32 arithmetic's);
- * DC_ORTHO_16 leaves X's low part out of its products (relative error about
- * 1.5e-3 or less, below the rounding to bf16).  Sums are float32, in a fixed
- * order. */
+ * 16-bit floats (as good as float32; fixed point below 2^-36), their diagonals
+ * in float32.  DC_ORTHO_32 multiplies both parts of every factor: the result is
+ * as good as float32 arithmetic's.  DC_ORTHO_16 multiplies the high parts alone
+ * (relative error about 1e-3, below a rounding to bf16), but both where the
+ * shorter side is under 64.  Sums are float32, in a fixed order: the same
+ * matrix gives the same bits, whatever matrices are beside it. */
 
 /* One matrix: in, out [rows][cols] dense; out may be in where the types agree. */
 typedef struct {

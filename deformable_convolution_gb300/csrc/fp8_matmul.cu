@@ -24,6 +24,7 @@
 #include <cuda.h>
 
 #include "fp8.cuh"
+#include "once.cuh"
 #include "tc_pair.cuh"
 
 namespace dc {
@@ -393,7 +394,8 @@ Plan plan_of(const dc_fp8_product& p) {
 
 template <int BN>
 cudaError_t launch(const CUtensorMap& ta, const CUtensorMap& tb, const CUtensorMap& td, const Args& a, cudaStream_t s) {
-  cudaError_t e = cudaFuncSetAttribute(fp8_mm<BN>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)Cfg<BN>::kSmem);
+  static std::atomic<bool> allowed[kOnceDevices];
+  cudaError_t e = allow_smem_once(fp8_mm<BN>, Cfg<BN>::kSmem, allowed);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(2u * (unsigned)(a.work < kPairs ? a.work : kPairs));

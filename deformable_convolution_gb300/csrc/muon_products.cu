@@ -36,6 +36,7 @@
 #include <cuda.h>
 
 #include "muon.cuh"
+#include "once.cuh"
 #include "tc_pair.cuh"
 
 namespace dc {
@@ -152,11 +153,15 @@ __device__ __forceinline__ bool inputs_done(const Tile& q) {
   const int before = q.which == GRAM ? APPLY : q.which - 1;
   const unsigned int want = 2u * (unsigned)q.t->tiles[before] * (unsigned)(q.which == GRAM ? q.step : q.step + 1);
   const unsigned int* count = q.t->m.done + before;
+  // relaxed loads, one fence at the end: an acquire empties the L1 cache each time
   for (uint32_t i = 0; i < (1u << 22); ++i) {
     unsigned int v;
-    asm volatile("ld.acquire.gpu.global.u32 %0, [%1];" : "=r"(v) : "l"(count) : "memory");
-    if (v >= want) return true;
-    __nanosleep(20);
+    asm volatile("ld.relaxed.gpu.global.u32 %0, [%1];" : "=r"(v) : "l"(count) : "memory");
+    if (v >= want) {
+      asm volatile("fence.acq_rel.gpu;" ::: "memory");
+      return true;
+    }
+    __nanosleep(64);
   }
   atomicOr(&g_muon_error, 1u);
   return false;
@@ -184,24 +189,26 @@ __device__ __forceinline__ bool epi_all(bool ok) {
 // Generic and asynchronous accesses to global memory, in order.
 __device__ __forceinline__ void fence_global_proxies() { asm volatile("fence.proxy.async.global;" ::: "memory"); }
 
-// Eight values as high and low parts.
-union Halves {
-  __half h[8];
-  uint4 q;
-};
-__device__ __forceinline__ void to_pairs(const float* v, Halves* hi, Halves* lo) {
-#pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    hi->h[i] = __float2half_rn(v[i]);
-    lo->h[i] = __float2half_rn(v[i] - __half2float(hi->h[i]));
-  }
-}
-__device__ __forceinline__ void from_pairs(uint4 hi, uint4 lo, float* v) {
-  const __half2* h = reinterpret_cast<const __half2*>(&hi);
-  const __half2* l = reinterpret_cast<const __half2*>(&lo);
+// Eight values as high and low parts, two in a word.
+__device__ __forceinline__ void to_pairs(const float* v, uint4* hi, uint4* lo) {
+  uint32_t h[4], l[4];
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    const float2 a = __half22float2(h[i]), b = __half22float2(l[i]);
+    const __half2 a = __floats2half2_rn(v[2 * i], v[2 * i + 1]);
+    const float2 b = __half22float2(a);
+    const __half2 c = __floats2half2_rn(v[2 * i] - b.x, v[2 * i + 1] - b.y);
+    h[i] = *reinterpret_cast<const uint32_t*>(&a);
+    l[i] = *reinterpret_cast<const uint32_t*>(&c);
+  }
+  *hi = make_uint4(h[0], h[1], h[2], h[3]);
+  *lo = make_uint4(l[0], l[1], l[2], l[3]);
+}
+__device__ __forceinline__ void from_pairs(uint4 hi, uint4 lo, float* v) {
+  const uint32_t h[4] = {hi.x, hi.y, hi.z, hi.w}, l[4] = {lo.x, lo.y, lo.z, lo.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float2 a = __half22float2(*reinterpret_cast<const __half2*>(&h[i]));
+    const float2 b = __half22float2(*reinterpret_cast<const __half2*>(&l[i]));
     v[2 * i] = a.x + b.x;
     v[2 * i + 1] = a.y + b.y;
   }
@@ -428,6 +435,7 @@ __global__ void __launch_bounds__(kThreads, 1) muon_steps(const __grid_constant_
       __half* out = q.which == GRAM ? m.gram : q.which == POLY ? m.poly : m.x[1 - (q.step & 1)];
       const bool last_step = q.which == APPLY && q.step + 1 == g.steps;
       const bool store_low = q.which != POLY || t.pairs;
+      float* diag_out = q.which == GRAM ? m.gram_diag : m.poly_diag;
       const int chunks = q.bn / 64;  // of 32 columns, for each half of the columns
       const int row0 = q.m0 + (int)rank * 128 + quad * 32;
       const bool whole = t.pairs && q.bn == 256;
@@ -563,36 +571,31 @@ __global__ void __launch_bounds__(kThreads, 1) muon_steps(const __grid_constant_
         for (int k = 0; k < 8; ++k) col_diag[k] = next_diag[k];
         asm volatile("cp.async.wait_all;" ::: "memory");
         __syncwarp();
-        // (rolled: code that runs a few times costs more to fetch than to run)
-#pragma unroll 1
+        if (q.which != APPLY && row0 == col0) {
+          // the diagonal, where R is 0: b d + c d^2 and the sum's (of gram d is 0 so far)
+          float* on = buf + lane * 32 + (((lane >> 2) ^ swizzle(lane)) << 2) + (lane & 3);
+          if (row0 + lane < rows)
+            diag_out[row0 + lane] = *on * (mul * unit) + (kOrthoB + kOrthoC * row_diag) * row_diag;
+          *on = 0.f;
+          __syncwarp();
+        }
+#pragma unroll
         for (int i = 0; i < 4; ++i) {
           const int rl = 8 * i + sub, r = row0 + rl;
-          const float rd = __shfl_sync(0xffffffffu, row_diag, rl);
+          const float f = c0 + cr * __shfl_sync(0xffffffffu, row_diag, rl);
           if (r < rows && col < cols) {
             float4* p0 = reinterpret_cast<float4*>(buf + rl * 32) + ((2 * piece) ^ swizzle(rl));
             float4* p1 = reinterpret_cast<float4*>(buf + rl * 32) + ((2 * piece + 1) ^ swizzle(rl));
             const float4 a = *p0, b = *p1;
             float e[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
-            if (q.which == GRAM) {
 #pragma unroll
-              for (int k = 0; k < 8; ++k) e[k] *= mul;
-            } else {
+            for (int k = 0; k < 8; ++k) e[k] *= mul;
+            if (q.which != GRAM) {
               float x[8];
               const uint4* own = reinterpret_cast<const uint4*>(terms + i * 512) + lane;
               from_pairs(own[0], own[128], x);
-              const float f = c0 + cr * rd;
 #pragma unroll
-              for (int k = 0; k < 8; ++k) e[k] = mul * e[k] + (f + cc * col_diag[k]) * x[k];
-            }
-            if (q.which != APPLY && (unsigned)(r - col) < 8u) {
-              // on the diagonal (where R is 0): b d + c d^2 + the sum's; of gram d is 0 so far
-              float* to = q.which == GRAM ? m.gram_diag : m.poly_diag;
-#pragma unroll
-              for (int k = 0; k < 8; ++k)
-                if (r - col == k) {
-                  to[r] = e[k] * unit + (kOrthoB + kOrthoC * rd) * rd;
-                  e[k] = 0.f;
-                }
+              for (int k = 0; k < 8; ++k) e[k] += (f + cc * col_diag[k]) * x[k];
             }
             if (mirror || last_step) {
               *p0 = make_float4(e[0], e[1], e[2], e[3]);
@@ -600,10 +603,10 @@ __global__ void __launch_bounds__(kThreads, 1) muon_steps(const __grid_constant_
             }
             if (!last_step) {
               // whole 16-byte pieces: what lies past the last column is of no meaning
-              Halves h, l;
+              uint4 h, l;
               to_pairs(e, &h, &l);
-              *reinterpret_cast<uint4*>(out + r * ld + col) = h.q;
-              if (store_low) *reinterpret_cast<uint4*>(out + low + r * ld + col) = l.q;
+              *reinterpret_cast<uint4*>(out + r * ld + col) = h;
+              if (store_low) *reinterpret_cast<uint4*>(out + low + r * ld + col) = l;
             }
           }
         }
@@ -622,11 +625,11 @@ __global__ void __launch_bounds__(kThreads, 1) muon_steps(const __grid_constant_
                 e[k] = buf[rl * 32 + (((cl >> 2) ^ swizzle(rl)) << 2) + (cl & 3)];
               }
               if (row0 + 8 * piece < rows) {
-                Halves h, l;
+                uint4 h, l;
                 to_pairs(e, &h, &l);
                 __half* to = out + (col0 + cl) * ld + row0 + 8 * piece;
-                *reinterpret_cast<uint4*>(to) = h.q;
-                if (store_low) *reinterpret_cast<uint4*>(to + low) = l.q;
+                *reinterpret_cast<uint4*>(to) = h;
+                if (store_low) *reinterpret_cast<uint4*>(to + low) = l;
               }
             } else {
               const int rl = 8 * i + sub;
@@ -725,7 +728,8 @@ cudaError_t launch(const MuonGroup& m, cudaStream_t s) {
         !pair_map(&q.gram, t.gram, t.side, t.side, t.lds) || !pair_map(&q.poly, t.poly, t.side, t.side, t.lds))
       return cudaErrorInvalidValue;
   }
-  cudaError_t e = cudaFuncSetAttribute(muon_steps<CAP>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmem);
+  static std::atomic<bool> allowed[kOnceDevices];
+  cudaError_t e = allow_smem_once(muon_steps<CAP>, kSmem, allowed);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(2 * kPairs);
@@ -739,9 +743,15 @@ cudaError_t launch(const MuonGroup& m, cudaStream_t s) {
   cfg.attrs = attr;
   cfg.numAttrs = 1;
   // pairs that run at once: all of them have to, for tiles wait for one another
-  int most = 0;
-  e = cudaOccupancyMaxActiveClusters(&most, muon_steps<CAP>, &cfg);
-  if (e != cudaSuccess) return e;
+  static std::atomic<int> at_once[kOnceDevices];
+  int dev = 0, most = 0;
+  if ((e = cudaGetDevice(&dev)) != cudaSuccess) return e;
+  if (dev < kOnceDevices) most = at_once[dev].load(std::memory_order_relaxed);
+  if (most == 0) {
+    e = cudaOccupancyMaxActiveClusters(&most, muon_steps<CAP>, &cfg);
+    if (e != cudaSuccess) return e;
+    if (dev < kOnceDevices) at_once[dev].store(most, std::memory_order_relaxed);
+  }
   int widest = 0;  // more pairs than the widest kind of a step has tiles would only wait
   for (int k = 0; k < 3; ++k)
     if (g.n[k] > widest) widest = g.n[k];

@@ -30,9 +30,12 @@ __device__ __forceinline__ uint32_t in_cta(uint32_t addr, uint32_t rank) {
   asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(rank));
   return r;
 }
-// Arrives on a barrier of either CTA (an address in the cluster's window).
+// Arrives on a barrier of either CTA (an address in the cluster's window).  Not
+// a release for the cluster, which would wait for this thread's stores to
+// global memory (about 1000 cycles): what it announces are reads and writes of
+// tensor memory that tcgen05.wait and a tcgen05 fence have completed.
 __device__ __forceinline__ void arrive_at(uint32_t bar) {
-  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+  asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }
 
 // TMA loads into this CTA, counted on a barrier of either CTA of the pair.

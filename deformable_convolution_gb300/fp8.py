@@ -70,31 +70,48 @@ class Pointwise:
         # products over channels: pixels are the rows of D (channels last) or its columns
         self._fwd = q(batch, pixels, c_out, c_in, b_shared=1, out=dtype) if last else \
             q(batch, c_out, pixels, c_in, a_shared=1, out=dtype)
-        self._calls = [self._fwd]
+        products = [self._fwd]
         if training:
             self.gy = Quantized(maps(c_out, grad_dtype, g), True, True, device)
             self._gx = q(batch, pixels, c_in, c_out, g, e, b_shared=1, out=dtype) if last else \
                 q(batch, c_in, pixels, c_out, e, g, a_shared=1, out=dtype)
             self._gw = q(batch, c_out, c_in, pixels, g, e, sum=1, out=B.DC_F32)
-            self._calls += [self._gx, self._gw]
-        self.last = last
-        need = max(B.dc_fp8_matmul_workspace_size(p) for p in self._calls)
+            products += [self._gx, self._gw]
+        need = max(B.dc_fp8_matmul_workspace_size(p) for p in products)
         self._ws = torch.empty(max(need, 1), dtype=torch.uint8, device=device)
+        # addresses of what the layer keeps, in the order that the calls take them
+        self._lib = B.lib()
+        w, x = self.weight, self.x
+
+        def addresses(*tensors):
+            return tuple(None if t is None else t.data_ptr() for t in tensors)
+        self._x_to = addresses(x.codes, x.scales, x.codes_t, x.scales_t)
+        self._fwd_from = addresses(x.codes, x.scales, w.codes, w.scales) if last else \
+            addresses(w.codes, w.scales, x.codes_t, x.scales_t)
+        if training:
+            g = self.gy
+            self._gy_to = addresses(g.codes, g.scales, g.codes_t, g.scales_t)
+            self._gx_from = addresses(g.codes, g.scales, w.codes_t, w.scales_t) if last else \
+                addresses(w.codes_t, w.scales_t, g.codes_t, g.scales_t)
+            self._gw_from = addresses(g.codes_t, g.scales_t, x.codes_t, x.scales_t) if last else \
+                addresses(g.codes, g.scales, x.codes, x.scales)
+        self._ws_args = self._ws.data_ptr(), self._ws.numel()
 
     def load(self, w, stream=None):
         """The weight [c_out, c_in] (or [c_out, c_in, 1, 1]), for the calls that follow."""
         B._arg(w, "w", w.shape, self.dtype)
-        if tuple(w.shape) not in (self.w_shape, self.w_shape + (1, 1)):
+        if tuple(w.shape) not in (self.w_shape, self.w_shape + (1, 1)):  # (a 1 x 1 convolution's)
             raise ValueError(f"w: expected shape {self.w_shape}, got {tuple(w.shape)}")
         self.weight.load(w, stream)
 
     def forward(self, x, y=None, stream=None):
         """y (a new tensor if not given) = W x."""
-        B._arg(x, "x", self.x_shape, self.dtype)
+        x_ptr = B._arg(x, "x", self.x_shape, self.dtype)
         y = torch.empty(self.y_shape, dtype=self.dtype, device=x.device) if y is None else y
-        B._arg(y, "y", self.y_shape, self.dtype)
-        self.x.load(x, stream)
-        self._over_channels(self._fwd, self.weight.codes, self.weight.scales, self.x, y, stream)
+        y_ptr = B._arg(y, "y", self.y_shape, self.dtype)
+        s = B._raw_stream(stream)
+        self._run(self.x.p, x_ptr, self._x_to, s)
+        self._product(self._fwd, self._fwd_from, y_ptr, s)
         return y
 
     def backward(self, grad_y, grad_x=None, grad_w=None, stream=None):
@@ -102,26 +119,25 @@ class Pointwise:
         ``dtype`` and float32, new tensors if not given."""
         if not self.training:
             raise ValueError("a layer made with training=False keeps nothing for a backward pass")
-        B._arg(grad_y, "grad_y", self.y_shape, self.grad_dtype)
+        g_ptr = B._arg(grad_y, "grad_y", self.y_shape, self.grad_dtype)
         if grad_x is None:
             grad_x = torch.empty(self.x_shape, dtype=self.dtype, device=grad_y.device)
         if grad_w is None:
             grad_w = torch.empty(self.w_shape, dtype=torch.float32, device=grad_y.device)
-        B._arg(grad_x, "grad_x", self.x_shape, self.dtype)
-        self.gy.load(grad_y, stream)
-        self._over_channels(self._gx, self.weight.codes_t, self.weight.scales_t, self.gy, grad_x, stream)
-        a, b = self.gy, self.x
-        if self.last:
-            B.dc_fp8_matmul(self._gw, a.codes_t, a.scales_t, b.codes_t, b.scales_t, grad_w.view(self.w_shape),
-                            self._ws, stream)
-        else:
-            B.dc_fp8_matmul(self._gw, a.codes, a.scales, b.codes, b.scales, grad_w.view(self.w_shape),
-                            self._ws, stream)
+        gx_ptr = B._arg(grad_x, "grad_x", self.x_shape, self.dtype)
+        gw_ptr = B._arg(grad_w, "grad_w", self.w_shape if grad_w.dim() == 2 else self.w_shape + (1, 1), torch.float32)
+        s = B._raw_stream(stream)
+        self._run(self.gy.p, g_ptr, self._gy_to, s)
+        self._product(self._gx, self._gx_from, gx_ptr, s)
+        self._product(self._gw, self._gw_from, gw_ptr, s)
         return grad_x, grad_w
 
-    def _over_channels(self, p, w_codes, w_scales, maps, out, stream):
-        out = out.view(p.shape)
-        if self.last:
-            B.dc_fp8_matmul(p, maps.codes, maps.scales, w_codes, w_scales, out, self._ws, stream)
-        else:
-            B.dc_fp8_matmul(p, w_codes, w_scales, maps.codes_t, maps.scales_t, out, self._ws, stream)
+    def _run(self, p, ptr, to, s):
+        status = self._lib.dc_fp8_quantize(p, ptr, *to, s)
+        if status:
+            raise B.DcError(status, "dc_fp8_quantize")
+
+    def _product(self, p, factors, out, s):
+        status = self._lib.dc_fp8_matmul(p, *factors, out, *self._ws_args, s)
+        if status:
+            raise B.DcError(status, "dc_fp8_matmul")

@@ -40,17 +40,17 @@ constexpr int kEpiWarps = 8, kScaleWarps = 4;
 constexpr int kWarpTma = kEpiWarps + kScaleWarps, kWarpMma = kWarpTma + 1;
 constexpr int kThreads = (kWarpMma + 1) * 32;
 constexpr int kPairs = 76;      // of 152 SMs
-constexpr int kStageBuf = 4096; // store staging of a warp: 32 rows of 128 bytes, twice
+constexpr int kStageBuf = 4096; // store staging of a warp: 32 rows of 128 bytes, or twice 32 of 64
 
 template <int BN>
 struct Cfg {
   static constexpr int kA = 128 * kBK, kB = BN / 2 * kBK, kStage = kA + kB;
-  static constexpr int kStages = BN == 256 ? 4 : 6;
+  static constexpr int kStages = BN == 256 ? 6 : 8;
   static constexpr int kAcc1 = BN == 256 ? 224 : BN;  // second accumulator's first column
   static constexpr int kShared = BN == 256 ? 32 : 0;  // columns that the two share
   static constexpr int kScaleCol = 480;               // two slots of 4 (A) + BN / 32 (B) columns
   static constexpr int kSlot = 16;
-  static constexpr size_t kSmem = 1024 + (size_t)kStages * kStage + kEpiWarps * 2 * kStageBuf + 256;
+  static constexpr size_t kSmem = 1024 + (size_t)kStages * kStage + kEpiWarps * kStageBuf + 256;
   static_assert(kSmem <= 227 * 1024, "shared memory");
 };
 
@@ -105,7 +105,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   extern __shared__ unsigned char smem_raw[];
   unsigned char* smem = px::align1024(smem_raw);
   unsigned char* stg = smem + C::kStages * C::kStage;
-  uint64_t* full = reinterpret_cast<uint64_t*>(stg + kEpiWarps * 2 * kStageBuf);
+  uint64_t* full = reinterpret_cast<uint64_t*>(stg + kEpiWarps * kStageBuf);
   uint64_t* empty = full + C::kStages;
   uint64_t* sfull = empty + C::kStages;  // scales of a slot are in tensor memory (both CTAs')
   uint64_t* sempty = sfull + 2;
@@ -248,7 +248,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   } else {
     // results: this warp's 32 rows, half of the columns
     const int quad = warp & 3, half = warp >> 2;
-    unsigned char* buf = stg + warp * 2 * kStageBuf;
+    unsigned char* buf = stg + warp * kStageBuf;
     int j = 0, used = 0;
     for (int w = first; w < a.work; w += stride, ++j) {
       const Tile t = tile_of(a, w, BN);
@@ -274,10 +274,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         }
         const int col0 = t.n0 + chunk * 32;
         if (row0 >= a.m || col0 >= a.n) continue;
-        unsigned char* b = buf + (used & 1) * kStageBuf;
-        ++used;
+        unsigned char* b = buf + (a.out_f32 || !a.tma_out ? 0 : (used++ & 1) * (kStageBuf / 2));
         if (a.tma_out) {
-          if (lane == 0) store_wait_read<1>();
+          if (lane == 0) {
+            if (a.out_f32)
+              store_wait_read<0>();
+            else
+              store_wait_read<1>();
+          }
           __syncwarp();
           if (a.out_f32) {
 #pragma unroll

@@ -141,72 +141,79 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   pdl_release();
 
   if (warp == kWarpTma) {
-    if (lane == 0) {
-      int it = 0;
-      for (int w = first; w < a.work && ok; w += stride) {
-        const Tile t = tile_of(a, w, BN);
-        for (int f = t.begin; f < t.end; ++f, ++it) {
-          const int s = it % C::kStages;
-          if (it >= C::kStages && !mbar_wait(&empty[s], ((it / C::kStages) - 1) & 1, &g_fp8_error)) {
-            ok = false;
-            break;
-          }
-          const int img = a.sum ? f / a.nkb : t.z, kb = a.sum ? f - img * a.nkb : f;
-          // both CTAs' copies count on the first one's barrier
-          const uint32_t bar = in_cta(smem_u32(&full[s]), 0);
-          if (rank == 0) mbar_expect_tx(&full[s], 2 * C::kStage);
-          const uint32_t sa = smem_u32(smem + s * C::kStage);
-          tma_load(sa, &ta, bar, kb * kBK, t.m0 + (int)rank * 128, a.a_shared ? 0 : img);
-          tma_load(sa + C::kA, &tb, bar, kb * kBK, t.n0 + (int)rank * (BN / 2), a.b_shared ? 0 : img);
+    const bool issuer = elect_one();
+    // both CTAs' copies count on the first one's barrier
+    const uint32_t bar0 = in_cta(smem_u32(full), 0), ring = smem_u32(smem);
+    int s = 0, round = 0;
+    for (int w = first; w < a.work && ok; w += stride) {
+      const Tile t = tile_of(a, w, BN);
+      const int m0 = t.m0 + (int)rank * 128, n0 = t.n0 + (int)rank * (BN / 2);
+      int img = a.sum ? t.begin / a.nkb : t.z, kb = a.sum ? t.begin - img * a.nkb : t.begin;
+      for (int f = t.begin; f < t.end; ++f) {
+        if (round && !warp_wait(&empty[s], (round - 1) & 1, &g_fp8_error)) {
+          ok = false;
+          break;
         }
+        if (issuer) {
+          if (rank == 0) mbar_expect_tx(&full[s], 2 * C::kStage);
+          const uint32_t sa = ring + s * C::kStage, bar = bar0 + s * 8;
+          tma_load(sa, &ta, bar, kb * kBK, m0, a.a_shared ? 0 : img);
+          tma_load(sa + C::kA, &tb, bar, kb * kBK, n0, a.b_shared ? 0 : img);
+        }
+        __syncwarp();
+        if (++kb == a.nkb) kb = 0, ++img;
+        if (++s == C::kStages) s = 0, ++round;
       }
-      if (!ok) let_copies_land();
     }
+    if (!ok) let_copies_land();
   } else if (warp == kWarpMma) {
-    if (rank == 0 && lane == 0) {
+    if (rank == 0) {
+      const bool issuer = elect_one();
       const uint32_t idesc0 = ((uint32_t)a.a_fmt << 7) | ((uint32_t)a.b_fmt << 10) | ((uint32_t)(BN >> 3) << 17) |
                               (1u << 23) | ((256u >> 4) << 24);
-      int it = 0, slot = 0, j = 0;  // stages, scale slots and tiles so far
+      const uint64_t desc0 = sdesc(smem_u32(smem), 16, 1024);
+      int s = 0, round = 0, slot = 0, j = 0;  // stages, scale slots and tiles so far
       for (int w = first; w < a.work && ok; w += stride, ++j) {
         const Tile t = tile_of(a, w, BN);
         // accumulators apart: the tile before last has been read; sharing
         // columns: these have been read of the last one (and the one before whole)
         const int before = j - (C::kShared ? 1 : 2);
-        if (before >= 0 && !mbar_wait(&drained[before & 1], (before >> 1) & 1, &g_fp8_error)) {
+        if (before >= 0 && !warp_wait(&drained[before & 1], (before >> 1) & 1, &g_fp8_error)) {
           ok = false;
           break;
         }
-        tc_after();
         const uint32_t acc = tmem + (j & 1) * C::kAcc1;
-        for (int f = t.begin; f < t.end; ++f, ++it) {
-          const int kb = a.sum ? f % a.nkb : f;
-          if (f == t.begin || kb % 4 == 0) {
-            if (!mbar_wait(&sfull[slot & 1], (slot >> 1) & 1, &g_fp8_error)) {
+        int kb = a.sum ? t.begin % a.nkb : t.begin;
+        for (int f = t.begin; f < t.end; ++f) {
+          if (f == t.begin || (kb & 3) == 0) {
+            if (!warp_wait(&sfull[slot & 1], (slot >> 1) & 1, &g_fp8_error)) {
               ok = false;
               break;
             }
           }
-          const int s = it % C::kStages;
-          if (!mbar_wait(&full[s], (it / C::kStages) & 1, &g_fp8_error)) {
+          if (!warp_wait(&full[s], round & 1, &g_fp8_error)) {
             ok = false;
             break;
           }
           tc_after();
-          const uint32_t sa = smem_u32(smem + s * C::kStage), sb = sa + C::kA;
+          const uint64_t da = desc0 + (uint64_t)(s * (C::kStage >> 4)), db = da + (C::kA >> 4);
           const uint32_t scale = tmem + C::kScaleCol + (slot & 1) * C::kSlot;
           // the byte of each scale word that holds this block's exponent
           const uint32_t idesc = idesc0 | ((uint32_t)(kb & 3) << 4) | ((uint32_t)(kb & 3) << 29);
+          const bool chunk_end = f + 1 == t.end || (kb & 3) == 3 || kb + 1 == a.nkb;
+          if (issuer) {
 #pragma unroll
-          for (int k = 0; k < kBK / 32; ++k)
-            umma_scaled(acc, sdesc(sa + k * 32, 16, 1024), sdesc(sb + k * 32, 16, 1024), idesc, scale, scale + 4,
-                        (f > t.begin || k > 0) ? 1u : 0u);
-          commit_both(&empty[s]);
-          if (f + 1 == t.end || kb % 4 == 3 || kb + 1 == a.nkb) {
-            commit_both(&sempty[slot & 1]);
-            ++slot;
+            for (int k = 0; k < kBK / 32; ++k)
+              umma_scaled(acc, da + 2 * k, db + 2 * k, idesc, scale, scale + 4, (f > t.begin || k > 0) ? 1u : 0u);
+            commit_both(&empty[s]);
+            if (chunk_end) commit_both(&sempty[slot & 1]);
+            if (f + 1 == t.end) commit_both(&tfull[j & 1]);
           }
+          __syncwarp();
+          slot += chunk_end;
+          if (++kb == a.nkb) kb = 0;
+          if (++s == C::kStages) s = 0, ++round;
         }
-        commit_both(&tfull[j & 1]);
       }
     }
   } else if (warp >= kEpiWarps) {
@@ -230,7 +237,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 #pragma unroll
         for (int h = 0; h < BN / 128; ++h) vb[h] = word(a.sb, a.b_shared ? 0 : img, rb, tb0 + h);
         if (slot >= 2) {
-          ok = __all_sync(0xffffffffu, mbar_wait(&sempty[slot & 1], ((slot >> 1) - 1) & 1, &g_fp8_error));
+          ok = warp_wait(&sempty[slot & 1], ((slot >> 1) - 1) & 1, &g_fp8_error);
           if (!ok) break;
           tc_after();
         }
@@ -252,7 +259,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     int j = 0, used = 0;
     for (int w = first; w < a.work; w += stride, ++j) {
       const Tile t = tile_of(a, w, BN);
-      ok = __all_sync(0xffffffffu, mbar_wait(&tfull[j & 1], (j >> 1) & 1, &g_fp8_error));
+      ok = warp_wait(&tfull[j & 1], (j >> 1) & 1, &g_fp8_error);
       if (!ok) break;
       tc_after();
       const uint32_t acc = tmem + (j & 1) * C::kAcc1 + ((uint32_t)(quad * 32) << 16);

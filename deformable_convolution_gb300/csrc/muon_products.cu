@@ -325,47 +325,55 @@ __global__ void __launch_bounds__(kThreads, 1) muon_steps(const __grid_constant_
   // every tile waits for the tile before last to be read, a wide one with cross
   // terms, or one after such a tile, for the last one.
   if (warp == kWarpTma) {
-    if (lane == 0) {
-      int s = 0, round = 0;
-      for (int w = first; w < work && ok; w += stride) {
-        const Tile q = tile_of(g, w);
-        const MuonMat& m = q.t->m;
-        if (!inputs_done(q)) {
-          ok = false;
-          break;
-        }
-        fence_global_proxies();
-        // factors and whether their contracted side runs across lines
-        const CUtensorMap* x = &q.t->x[q.step & 1];
-        const CUtensorMap* ta = q.which == GRAM ? x : q.which == POLY ? &q.t->gram : m.tall ? x : &q.t->poly;
-        const CUtensorMap* tb = q.which == GRAM ? x : q.which == POLY ? &q.t->gram : m.tall ? &q.t->poly : x;
-        const bool a_mn = q.which == GRAM && m.tall, b_mn = (q.which == GRAM && m.tall) || (q.which == APPLY && !m.tall);
-        const int m0 = q.m0 + (int)rank * 128, n0 = q.n0 + (int)rank * (q.bn / 2), nb = q.bn / 128;
-        const uint32_t bytes = 2u * (uint32_t)(2 + nb) * kBox;
-        const int parts = 1 + q.t->pairs;
-        for (int kb = q.begin; kb < q.end && ok; ++kb) {
-          // the high parts in one stage, the low ones in the next
-          for (int p = 0; p < parts; ++p) {
-            if (round && !mbar_wait(&empty[s], (round - 1) & 1, &g_muon_error)) {
-              ok = false;
-              break;
-            }
-            const uint32_t bar = in_cta(smem_u32(&full[s]), 0);
+    const bool issuer = elect_one();
+    // both CTAs' copies count on the first one's barrier
+    const uint32_t bar0 = in_cta(smem_u32(full), 0), ring = smem_u32(smem);
+    int s = 0, round = 0;
+    for (int w = first; w < work && ok; w += stride) {
+      const Tile q = tile_of(g, w);
+      const MuonMat& m = q.t->m;
+      bool here = true;
+      if (lane == 0) here = inputs_done(q);
+      if (!__all_sync(0xffffffffu, here)) {
+        ok = false;
+        break;
+      }
+      fence_global_proxies();
+      // factors and whether their contracted side runs across lines
+      const CUtensorMap* x = &q.t->x[q.step & 1];
+      const CUtensorMap* ta = q.which == GRAM ? x : q.which == POLY ? &q.t->gram : m.tall ? x : &q.t->poly;
+      const CUtensorMap* tb = q.which == GRAM ? x : q.which == POLY ? &q.t->gram : m.tall ? &q.t->poly : x;
+      const bool a_mn = q.which == GRAM && m.tall, b_mn = (q.which == GRAM && m.tall) || (q.which == APPLY && !m.tall);
+      const int m0 = q.m0 + (int)rank * 128, n0 = q.n0 + (int)rank * (q.bn / 2), nb = q.bn / 128;
+      const uint32_t bytes = 2u * (uint32_t)(2 + nb) * kBox;
+      const int parts = 1 + q.t->pairs;
+      for (int kb = q.begin; kb < q.end && ok; ++kb) {
+        // the high parts in one stage, the low ones in the next
+        for (int p = 0; p < parts; ++p) {
+          if (round && !warp_wait(&empty[s], (round - 1) & 1, &g_muon_error)) {
+            ok = false;
+            break;
+          }
+          if (issuer) {
+            const uint32_t bar = bar0 + s * 8, sa = ring + s * kStage, sb = sa + kPart;
             if (rank == 0) mbar_expect_tx(&full[s], bytes);
-            const uint32_t sa = smem_u32(smem + s * kStage), sb = sa + kPart;
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
               tma_load(sa + h * kBox, ta, bar, a_mn ? m0 + 64 * h : kb * kBK, a_mn ? kb * kBK : m0 + 64 * h, p);
               if (h < nb) tma_load(sb + h * kBox, tb, bar, b_mn ? n0 + 64 * h : kb * kBK, b_mn ? kb * kBK : n0 + 64 * h, p);
             }
-            if (++s == kStages) s = 0, ++round;
           }
+          __syncwarp();
+          if (++s == kStages) s = 0, ++round;
         }
       }
-      if (!ok) let_copies_land();
     }
+    if (!ok) let_copies_land();
   } else if (warp == kWarpMma) {
-    if (rank == 0 && lane == 0) {
+    if (rank == 0) {
+      const bool issuer = elect_one();
+      // along lines a step of 16 elements is 32 bytes on, across them 16 lines on
+      const uint64_t along = sdesc(smem_u32(smem), 16, 1024), across = sdesc(smem_u32(smem), kBox, 1024);
       int s = 0, round = 0, j = 0;
       bool alone = false;  // the last tile took all columns
       for (int w = first; w < work && ok; w += stride, ++j) {
@@ -377,22 +385,22 @@ __global__ void __launch_bounds__(kThreads, 1) muon_steps(const __grid_constant_
         // (tiles are read in turn: the last one's reading follows the one's before it)
         const int before = j - (whole || alone ? 1 : 2);
         alone = whole;
-        if (before >= 0 && !mbar_wait(&drained[before & 1], (before >> 1) & 1, &g_muon_error)) {
+        if (before >= 0 && !warp_wait(&drained[before & 1], (before >> 1) & 1, &g_muon_error)) {
           ok = false;
           break;
         }
-        tc_after();
         const uint32_t acc = tmem + (whole ? 0 : (j & 1) * 256), cross = acc + q.bn;
         const uint32_t idesc = (1u << 4) | ((uint32_t)a_mn << 15) | ((uint32_t)b_mn << 16) |
                                ((uint32_t)(q.bn >> 3) << 17) | ((256u >> 4) << 24);
+        const uint64_t a0 = a_mn ? across : along, b0 = (b_mn ? across : along) + (kPart >> 4);
+        const uint32_t ka = a_mn ? 128 : 2, kb_step = b_mn ? 128 : 2;
         for (int kb = q.begin; kb < q.end; ++kb) {
-          const int s0 = s, round0 = round;
-          int s1 = s0;
+          const int s0 = s;
+          bool here = warp_wait(&full[s0], round & 1, &g_muon_error);
           if (++s == kStages) s = 0, ++round;
-          bool here = mbar_wait(&full[s0], round0 & 1, &g_muon_error);
+          const int s1 = s;
           if (pairs) {
-            s1 = s;
-            here = here && mbar_wait(&full[s1], round & 1, &g_muon_error);
+            here = here && warp_wait(&full[s1], round & 1, &g_muon_error);
             if (++s == kStages) s = 0, ++round;
           }
           if (!here) {
@@ -400,21 +408,27 @@ __global__ void __launch_bounds__(kThreads, 1) muon_steps(const __grid_constant_
             break;
           }
           tc_after();
-          const uint32_t high = smem_u32(smem + s0 * kStage), low = smem_u32(smem + s1 * kStage);
-          for (int p = 0; p < (pairs ? 3 : 1); ++p) {  // high high, high low, low high
-            const uint32_t pa = p == 2 ? low : high, pb = (p == 1 ? low : high) + kPart;
+          const uint64_t ah = a0 + (uint64_t)(s0 * (kStage >> 4)), bh = b0 + (uint64_t)(s0 * (kStage >> 4));
+          const uint64_t al = a0 + (uint64_t)(s1 * (kStage >> 4)), bl = b0 + (uint64_t)(s1 * (kStage >> 4));
+          const uint32_t more = kb > q.begin ? 1u : 0u;
+          if (issuer) {
 #pragma unroll
-            for (int k = 0; k < kBK / 16; ++k) {
-              // along lines: 32 bytes on; across them: 16 lines on
-              const uint64_t da = a_mn ? sdesc(pa + k * 2048, kBox, 1024) : sdesc(pa + k * 32, 16, 1024);
-              const uint64_t db = b_mn ? sdesc(pb + k * 2048, kBox, 1024) : sdesc(pb + k * 32, 16, 1024);
-              umma_f16(p ? cross : acc, da, db, idesc, (kb > q.begin || p > 1 || k > 0) ? 1u : 0u);
+            for (int k = 0; k < kBK / 16; ++k)  // high high
+              umma_f16(acc, ah + k * ka, bh + k * kb_step, idesc, k ? 1u : more);
+            if (pairs) {
+#pragma unroll
+              for (int k = 0; k < kBK / 16; ++k)  // high low
+                umma_f16(cross, ah + k * ka, bl + k * kb_step, idesc, k ? 1u : more);
+#pragma unroll
+              for (int k = 0; k < kBK / 16; ++k)  // low high
+                umma_f16(cross, al + k * ka, bh + k * kb_step, idesc, 1u);
+              commit_both(&empty[s1]);
             }
+            commit_both(&empty[s0]);
+            if (kb + 1 == q.end) commit_both(&tfull[j & 1]);
           }
-          commit_both(&empty[s0]);
-          if (pairs) commit_both(&empty[s1]);
+          __syncwarp();
         }
-        commit_both(&tfull[j & 1]);
       }
     }
   } else {
@@ -484,7 +498,7 @@ __global__ void __launch_bounds__(kThreads, 1) muon_steps(const __grid_constant_
         load_terms(0);
       }
       // (all warps go on or none: they meet at barriers below)
-      ok = epi_all(here && mbar_wait(&tfull[j & 1], (j >> 1) & 1, &g_muon_error));
+      ok = epi_all(here && warp_wait(&tfull[j & 1], (j >> 1) & 1, &g_muon_error));
       if (!ok) break;
       tc_after();
 

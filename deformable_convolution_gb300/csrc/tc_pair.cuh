@@ -21,6 +21,30 @@ __device__ __forceinline__ uint32_t cta_rank() {
   asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
   return r;
 }
+// True in one lane of the (converged) warp.  Warps that issue copies or MMAs run
+// their loops with all lanes and issue from this one: what is the same in all
+// lanes then stays in uniform registers, from which those instructions take
+// their operands (a loop run by lane 0 alone took 825 cycles for the MMAs of a
+// stage that the tensor cores do in 515).
+__device__ __forceinline__ bool elect_one() {
+  uint32_t r;
+  asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.b32 %0, 1, 0, p;\n}\n" : "=r"(r));
+  return r != 0;
+}
+// A bounded wait of a converged warp; whether it ended in time.  All lanes look
+// once, which keeps the warp together where the barrier is ready; then one polls.
+__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, unsigned int* flag) {
+  uint32_t ready;
+  asm volatile(
+      "{\n .reg .pred p;\n mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n selp.u32 %0, 1, 0, p;\n}\n"
+      : "=r"(ready)
+      : "r"(smem_u32(bar)), "r"(parity)
+      : "memory");
+  if (__all_sync(0xffffffffu, ready)) return true;
+  bool done = true;
+  if ((threadIdx.x & 31) == 0) done = mbar_wait(bar, parity, flag);
+  return __all_sync(0xffffffffu, done);
+}
 __device__ __forceinline__ void cluster_sync() {
   asm volatile("barrier.cluster.arrive.release.aligned;\nbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }

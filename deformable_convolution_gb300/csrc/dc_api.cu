@@ -1078,8 +1078,7 @@ void add_matrix(MuonGroup* g, int rows, int cols, char* ws, size_t* at) {
   t.poly_diag = reinterpret_cast<float*>(take(t.lds * sizeof(float)));
   t.part = reinterpret_cast<float*>(take(kMuonParts * sizeof(float)));
   t.sums = reinterpret_cast<float*>(take(muon_sums_bytes(t)));
-  t.arrivals = reinterpret_cast<unsigned int*>(take(kMuonArrivals * sizeof(unsigned int)));
-  t.done = reinterpret_cast<unsigned int*>(take(3 * sizeof(unsigned int)));
+  t.done = reinterpret_cast<unsigned int*>(take(4 * sizeof(unsigned int)));
 }
 
 // Workspace of `count` matrices of the sizes size(i): that of the largest group.

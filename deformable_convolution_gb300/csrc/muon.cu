@@ -64,8 +64,7 @@ __global__ void __launch_bounds__(kThreads) muon_begin(const __grid_constant__ M
   const MuonMat& t = g.mat[blockIdx.y];
   float scale;
   if (skipped(g, &scale) || blockIdx.x >= t.parts) return;
-  if (blockIdx.x == 0)
-    for (int i = threadIdx.x; i < kMuonArrivals + 3; i += kThreads) (i < kMuonArrivals ? t.arrivals[i] : t.done[i - kMuonArrivals]) = 0u;
+  if (blockIdx.x == 0 && threadIdx.x < 4) t.done[threadIdx.x] = 0u;
   float sum = 0.f;
   for (int i = threadIdx.x; i < t.parts; i += kThreads) sum += t.part[i];
   const float norm = sqrtf(block_sum(sum));

@@ -10,7 +10,6 @@ namespace dc {
 
 // Matrices of one group of launches.
 constexpr int kMuonMats = 40;
-constexpr int kMuonSplits = 16, kMuonArrivals = 256;
 constexpr int kMuonParts = 304;  // most blocks of the first launch for one matrix
 // Values between the products are kept times 2^12: X and A stay below 2^12 *
 // 1.5 and the polynomial of A below 2^12 * 4, inside a 16-bit float's range,
@@ -32,9 +31,8 @@ struct MuonMat {
   float* gram_diag;
   float* poly_diag;
   float* part;  // sums of squares of the blocks of the first launch
-  float* sums;  // a split gram's sums (muon_sums_bytes) and how many splits of each tile have arrived
-  unsigned int* arrivals;
-  unsigned int* done;  // CTAs' finished tiles: of gram, poly and X
+  float* sums;         // a split gram's (muon_sums_bytes)
+  unsigned int* done;  // [4] CTAs' finished tiles of each kind
   int rows, cols, ld, side, lds;
   int parts;    // blocks of the launches over single elements
   bool tall;  // rows > cols: A = X^T X, X = a X + X B

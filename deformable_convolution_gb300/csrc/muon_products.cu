@@ -22,8 +22,8 @@
 // computed, and what lies left of a diagonal block is stored at its mirrored
 // place too.  X enters as it lies, whichever side is contracted: the tensor
 // cores read 16-bit tiles in both orders.  A gram of few tiles splits its long
-// side over several pairs: each leaves its sums in the workspace, the last one
-// to arrive adds them up in order (no result depends on who that is).
+// side over several pairs: each leaves its sums in the workspace, and tiles of a
+// kind of their own (sum: 32 columns of a tile) add them up in order.
 //
 // The launch is cooperative and walks one list of tiles, step by step, kind by
 // kind, matrix by matrix, dealt to the pairs in turn; a tile waits (on a count
@@ -55,13 +55,14 @@ constexpr int kStages = 5, kRing = kStages * kStage;
 constexpr int kBuf = 4096;                // a warp's 32 x 32 results, and as much for their own terms
 constexpr size_t kSmem = 1024 + kRing + kEpiWarps * 2 * kBuf + 256;
 static_assert(kSmem <= 227 * 1024, "shared memory");
-enum { GRAM = 0, POLY = 1, APPLY = 2 };
+enum { GRAM = 0, SUM = 1, POLY = 2, APPLY = 3, KINDS = 4 };
 
 struct Item {
   CUtensorMap x[2], gram, poly;
   MuonMat m;
-  int start[3];                // first tile in the lists of the kinds
-  int tiles[3], tiles_n[3], bn[3];
+  int start[KINDS];            // first tile in the lists of the kinds
+  int tiles[KINDS];            // in a step (gram: of its splits; sum: 0 where it has one)
+  int tiles_n[KINDS], bn[KINDS];
   int splits, per_split;       // of gram, in blocks of 64
   int vec;                     // the result's rows are whole 16-byte pieces
   int pairs;                   // the low parts are multiplied
@@ -70,7 +71,7 @@ struct Item {
 template <int CAP>
 struct Items {
   int count, steps;
-  int n[3];                    // tiles of a kind (gram: of its splits) in one step
+  int n[KINDS];                // tiles of a kind in one step
   bool update;
   float lr;
   const float* grad_scale;
@@ -91,23 +92,19 @@ int lower_tiles(int rows, int tiles_n, int bn) {
 struct Tile {
   const Item* t;
   int which, step, index, m0, n0, bn, split, begin, end;
+  bool diagonal;  // the rows of both factors are the same ones
 };
 
 template <int CAP>
 __device__ __forceinline__ Tile tile_of(const Items<CAP>& g, int w) {
   Tile q;
-  const int per = g.n[0] + g.n[1] + g.n[2];
+  const int per = g.n[0] + g.n[1] + g.n[2] + g.n[3];
   q.step = w / per;
   int r = w - q.step * per;
   q.which = GRAM;
-  if (r >= g.n[0]) {
-    r -= g.n[0];
-    q.which = POLY;
-    if (r >= g.n[1]) {
-      r -= g.n[1];
-      q.which = APPLY;
-    }
-  }
+#pragma unroll
+  for (int k = 0; k < KINDS - 1; ++k)
+    if (q.which == k && r >= g.n[k]) r -= g.n[k], q.which = k + 1;
   int lo = 0, hi = g.count - 1;
   while (lo < hi) {
     const int mid = (lo + hi + 1) >> 1;
@@ -119,15 +116,23 @@ __device__ __forceinline__ Tile tile_of(const Items<CAP>& g, int w) {
   q.t = &g.item[lo];
   const Item& t = *q.t;
   r -= t.start[q.which];
+  // (a matrix without sums shares its place in their list with the next one)
   q.bn = t.bn[q.which];
   q.split = 0;
   q.begin = 0;
   q.end = (t.m.side + kBK - 1) / kBK;
+  int chunk = 0;
   if (q.which == GRAM) {
-    q.split = r / t.tiles[GRAM];
-    r -= q.split * t.tiles[GRAM];
+    const int whole = t.tiles[GRAM] / t.splits;
+    q.split = r / whole;
+    r -= q.split * whole;
     q.begin = q.split * t.per_split;
     q.end = min(((t.m.tall ? t.m.rows : t.m.cols) + kBK - 1) / kBK, q.begin + t.per_split);
+  } else if (q.which == SUM) {
+    const int chunks = q.bn / 32;
+    chunk = r % chunks;
+    r /= chunks;
+    q.end = 0;
   }
   q.index = r;
   int i = 0;
@@ -144,15 +149,18 @@ __device__ __forceinline__ Tile tile_of(const Items<CAP>& g, int w) {
   }
   q.m0 = i * 256;
   q.n0 = r * q.bn;
+  q.diagonal = q.bn == 256 && q.m0 == q.n0 && q.which != APPLY;
+  if (q.which == SUM) q.split = chunk;  // the 32 columns of the tile that it adds up
   return q;
 }
 
 // The tiles that this one reads are done: all CTAs' of the kind before it (of
 // gram: of the step before it).
 __device__ __forceinline__ bool inputs_done(const Tile& q) {
-  const int before = q.which == GRAM ? APPLY : q.which - 1;
-  const unsigned int want = 2u * (unsigned)q.t->tiles[before] * (unsigned)(q.which == GRAM ? q.step : q.step + 1);
-  const unsigned int* count = q.t->m.done + before;
+  const Item& t = *q.t;
+  const int before = q.which == GRAM ? APPLY : q.which == POLY && t.splits == 1 ? GRAM : q.which - 1;
+  const unsigned int want = 2u * (unsigned)t.tiles[before] * (unsigned)(q.which == GRAM ? q.step : q.step + 1);
+  const unsigned int* count = t.m.done + before;
   // relaxed loads, one fence at the end: an acquire empties the L1 cache each time
   for (uint32_t i = 0; i < (1u << 22); ++i) {
     unsigned int v;
@@ -290,7 +298,6 @@ __global__ void __launch_bounds__(kThreads, 1) muon_steps(const __grid_constant_
   uint64_t* tfull = empty + kStages;
   uint64_t* drained = tfull + 2;
   uint32_t* holder = reinterpret_cast<uint32_t*>(drained + 2);
-  uint32_t* arrived = holder + 1;
 
   // a step whose scale is not finite is skipped, by all alike
   if (g.update && g.grad_scale && !(fabsf(*g.grad_scale) <= 3.402823466e38f)) return;
@@ -298,7 +305,7 @@ __global__ void __launch_bounds__(kThreads, 1) muon_steps(const __grid_constant_
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t rank = cta_rank();
   const int first = (int)blockIdx.x >> 1, stride = (int)gridDim.x >> 1;
-  const int work = (g.n[0] + g.n[1] + g.n[2]) * g.steps;
+  const int work = (g.n[0] + g.n[1] + g.n[2] + g.n[3]) * g.steps;
 
   if (warp == 0) tmem_alloc(holder);
   if (threadIdx.x == 32) {
@@ -331,6 +338,7 @@ __global__ void __launch_bounds__(kThreads, 1) muon_steps(const __grid_constant_
     int s = 0, round = 0;
     for (int w = first; w < work && ok; w += stride) {
       const Tile q = tile_of(g, w);
+      if (q.which == SUM) continue;
       const MuonMat& m = q.t->m;
       bool here = true;
       if (lane == 0) here = inputs_done(q);
@@ -344,7 +352,9 @@ __global__ void __launch_bounds__(kThreads, 1) muon_steps(const __grid_constant_
       const CUtensorMap* ta = q.which == GRAM ? x : q.which == POLY ? &q.t->gram : m.tall ? x : &q.t->poly;
       const CUtensorMap* tb = q.which == GRAM ? x : q.which == POLY ? &q.t->gram : m.tall ? &q.t->poly : x;
       const bool a_mn = q.which == GRAM && m.tall, b_mn = (q.which == GRAM && m.tall) || (q.which == APPLY && !m.tall);
-      const int m0 = q.m0 + (int)rank * 128, n0 = q.n0 + (int)rank * (q.bn / 2), nb = q.bn / 128;
+      const int m0 = q.m0 + (int)rank * 128, n0 = q.n0 + (int)rank * (q.bn / 2);
+      // boxes of B: none where its rows are A's
+      const int nb = q.diagonal ? 0 : q.bn == 256 ? 2 : 1;
       const uint32_t bytes = 2u * (uint32_t)(2 + nb) * kBox;
       const int parts = 1 + q.t->pairs;
       for (int kb = q.begin; kb < q.end && ok; ++kb) {
@@ -376,8 +386,9 @@ __global__ void __launch_bounds__(kThreads, 1) muon_steps(const __grid_constant_
       const uint64_t along = sdesc(smem_u32(smem), 16, 1024), across = sdesc(smem_u32(smem), kBox, 1024);
       int s = 0, round = 0, j = 0;
       bool alone = false;  // the last tile took all columns
-      for (int w = first; w < work && ok; w += stride, ++j) {
+      for (int w = first; w < work && ok; w += stride) {
         const Tile q = tile_of(g, w);
+        if (q.which == SUM) continue;
         const bool a_mn = q.which == GRAM && q.t->m.tall;
         const bool b_mn = (q.which == GRAM && q.t->m.tall) || (q.which == APPLY && !q.t->m.tall);
         const int pairs = q.t->pairs;
@@ -392,7 +403,8 @@ __global__ void __launch_bounds__(kThreads, 1) muon_steps(const __grid_constant_
         const uint32_t acc = tmem + (whole ? 0 : (j & 1) * 256), cross = acc + q.bn;
         const uint32_t idesc = (1u << 4) | ((uint32_t)a_mn << 15) | ((uint32_t)b_mn << 16) |
                                ((uint32_t)(q.bn >> 3) << 17) | ((256u >> 4) << 24);
-        const uint64_t a0 = a_mn ? across : along, b0 = (b_mn ? across : along) + (kPart >> 4);
+        const uint64_t a0 = a_mn ? across : along;
+        const uint64_t b0 = (b_mn ? across : along) + (q.diagonal ? 0 : kPart >> 4);
         const uint32_t ka = a_mn ? 128 : 2, kb_step = b_mn ? 128 : 2;
         for (int kb = q.begin; kb < q.end; ++kb) {
           const int s0 = s;
@@ -429,6 +441,7 @@ __global__ void __launch_bounds__(kThreads, 1) muon_steps(const __grid_constant_
           }
           __syncwarp();
         }
+        ++j;
       }
     }
   } else {
@@ -437,8 +450,8 @@ __global__ void __launch_bounds__(kThreads, 1) muon_steps(const __grid_constant_
     const unsigned char* terms = reinterpret_cast<const unsigned char*>(buf) + kBuf;
     const float lr = g.lr_device ? *g.lr_device : g.lr;
     const int sub = lane >> 2, piece = lane & 3;  // eight columns of a row for a lane, rows 8 i + sub
-    int j = 0;
-    for (int w = first; w < work; w += stride, ++j) {
+    int j = 0;  // tiles with products so far
+    for (int w = first; w < work; w += stride) {
       const Tile q = tile_of(g, w);
       const Item& t = *q.t;
       const MuonMat& m = t.m;
@@ -446,15 +459,22 @@ __global__ void __launch_bounds__(kThreads, 1) muon_steps(const __grid_constant_
       const long long ld = q.which == APPLY ? m.ld : m.lds;
       const long long low = q.which == APPLY ? muon_x_low(m) : muon_p_low(m);
       const __half* add = q.which == POLY ? m.gram : m.x[q.step & 1];
-      __half* out = q.which == GRAM ? m.gram : q.which == POLY ? m.poly : m.x[1 - (q.step & 1)];
+      const bool gram = q.which == GRAM || q.which == SUM;
+      __half* out = gram ? m.gram : q.which == POLY ? m.poly : m.x[1 - (q.step & 1)];
       const bool last_step = q.which == APPLY && q.step + 1 == g.steps;
       const bool store_low = q.which != POLY || t.pairs;
-      float* diag_out = q.which == GRAM ? m.gram_diag : m.poly_diag;
-      const int chunks = q.bn / 64;  // of 32 columns, for each half of the columns
+      float* diag_out = gram ? m.gram_diag : m.poly_diag;
+      const int chunks = q.which == SUM ? 1 : q.bn / 64;  // of 32 columns, for each half of the columns
       const int row0 = q.m0 + (int)rank * 128 + quad * 32;
       const bool whole = t.pairs && q.bn == 256;
       const uint32_t acc = tmem + (whole ? 0 : (j & 1) * 256) + ((uint32_t)(quad * 32) << 16);
-      const bool split = q.which == GRAM && t.splits > 1;
+      const bool split = q.which == GRAM && t.splits > 1;  // sums to the workspace
+      // 16-byte pieces of a split's 32 columns of a tile, in the order that warps hold them
+      auto place = [&](int k, int chunk) {
+        const int whole = t.tiles[GRAM] / t.splits;
+        return reinterpret_cast<float4*>(m.sums) +
+               ((((long long)k * whole + q.index) * 2 + rank) * (q.bn / 32) + chunk) * 1024 + quad * 256 + lane;
+      };
 
       // The result is mul * sum + (c0 + cr * row's diagonal + cc * column's) *
       // own term: X, or R.  Terms come through shared memory by asynchronous
@@ -469,7 +489,7 @@ __global__ void __launch_bounds__(kThreads, 1) muon_steps(const __grid_constant_
       float row_diag = 0.f, col_diag[8], next_diag[8];  // row_diag: of row `lane`
       auto load_terms = [&](int c) {
         const int col = q.n0 + (half * chunks + c) * 32 + 8 * piece;
-        if (q.which != GRAM && col < cols) {
+        if (!gram && col < cols) {
           const __half* from = add + (row0 + sub) * ld + col;
           const uint32_t to = smem_u32(terms) + lane * 16;
 #pragma unroll
@@ -494,11 +514,11 @@ __global__ void __launch_bounds__(kThreads, 1) muon_steps(const __grid_constant_
       if (lane == 0) here = inputs_done(q);
       here = __all_sync(0xffffffffu, here);
       if (here) {
-        if (q.which != GRAM && cr != 0.f && row0 + lane < rows) row_diag = __ldcg(diag + row0 + lane);
+        if (!gram && cr != 0.f && row0 + lane < rows) row_diag = __ldcg(diag + row0 + lane);
         load_terms(0);
       }
       // (all warps go on or none: they meet at barriers below)
-      ok = epi_all(here && warp_wait(&tfull[j & 1], (j >> 1) & 1, &g_muon_error));
+      ok = epi_all(here && (q.which == SUM || warp_wait(&tfull[j & 1], (j >> 1) & 1, &g_muon_error)));
       if (!ok) break;
       tc_after();
 
@@ -520,58 +540,57 @@ __global__ void __launch_bounds__(kThreads, 1) muon_steps(const __grid_constant_
         __syncwarp();
         if (lane == 0) arrive_at(in_cta(smem_u32(&drained[j & 1]), 0));
       };
-      // a split's sums of this CTA, 16-byte pieces in the order that warps hold them
-      auto place = [&](int k, int c) {
-        return reinterpret_cast<float4*>(m.sums) +
-               (((((long long)k * t.tiles[GRAM] + q.index) * 2 + rank) * kEpiWarps + warp) * chunks + c) * 256 + lane;
-      };
       if (split) {
 #pragma unroll 1
         for (int c = 0; c < chunks; ++c) {
+          const int chunk = half * chunks + c;
           uint32_t r[32];
           results(c, r);
-          float4* to = place(q.split, c);
+          if (row0 < rows && q.n0 + chunk * 32 < cols) {
+            float4* to = place(q.split, chunk);
 #pragma unroll
-          for (int v = 0; v < 8; ++v)
-            __stcg(to + 32 * v, make_float4(__uint_as_float(r[4 * v]), __uint_as_float(r[4 * v + 1]),
-                                            __uint_as_float(r[4 * v + 2]), __uint_as_float(r[4 * v + 3])));
+            for (int v = 0; v < 8; ++v)
+              __stcg(to + 32 * v, make_float4(__uint_as_float(r[4 * v]), __uint_as_float(r[4 * v + 1]),
+                                              __uint_as_float(r[4 * v + 2]), __uint_as_float(r[4 * v + 3])));
+          }
         }
         release();
-        epi_barrier();
-        if (threadIdx.x == 0) {
-          __threadfence();
-          unsigned int* count = m.arrivals + q.index * 2 + rank;
-          const unsigned int before = atomicAdd(count, 1u);
-          if (before == (unsigned)t.splits - 1) *count = 0u;  // for the next step
-          __threadfence();
-          *arrived = before;
-        }
-        epi_barrier();
-        const bool last = *arrived == (unsigned)t.splits - 1;
-        epi_barrier();  // (read by all before the next tile writes it)
-        if (!last) continue;
-        __threadfence();
       }
       const bool mirror = q.which != APPLY && q.n0 + q.bn <= q.m0;
 #pragma unroll 1
-      for (int c = 0; c < chunks; ++c) {
-        const int col0 = q.n0 + (half * chunks + c) * 32, col = col0 + 8 * piece;
+      for (int c = split ? chunks : 0; c < chunks; ++c) {
+        const int col0 = q.n0 + (q.which == SUM ? q.split : half * chunks + c) * 32, col = col0 + 8 * piece;
         float4* line = reinterpret_cast<float4*>(buf + lane * 32);
-        if (split) {
+        if (q.which == SUM) {
+          // each half of the warps adds up half of the splits, in order; the first adds the second's sums to its own
           float4 f[8];
 #pragma unroll
           for (int v = 0; v < 8; ++v) f[v] = make_float4(0.f, 0.f, 0.f, 0.f);
+          if (row0 < rows && col0 < cols) {
+            const int middle = (t.splits + 1) / 2;
 #pragma unroll 2
-          for (int k = 0; k < t.splits; ++k) {
-            const float4* from = place(k, c);
+            for (int k = half ? middle : 0; k < (half ? t.splits : middle); ++k) {
+              const float4* from = place(k, q.split);
 #pragma unroll
-            for (int v = 0; v < 8; ++v) {
-              const float4 u = __ldcg(from + 32 * v);
-              f[v].x += u.x, f[v].y += u.y, f[v].z += u.z, f[v].w += u.w;
+              for (int v = 0; v < 8; ++v) {
+                const float4 u = __ldcg(from + 32 * v);
+                f[v].x += u.x, f[v].y += u.y, f[v].z += u.z, f[v].w += u.w;
+              }
             }
           }
+          const float4* second = reinterpret_cast<const float4*>(stg + (warp | 4) * 2 * kBuf) + lane * 8;
+          if (half) {
 #pragma unroll
-          for (int v = 0; v < 8; ++v) line[v ^ swizzle(lane)] = f[v];
+            for (int v = 0; v < 8; ++v) line[v ^ swizzle(lane)] = f[v];
+          }
+          epi_barrier();
+          if (!half) {
+#pragma unroll
+            for (int v = 0; v < 8; ++v) {
+              const float4 u = second[v ^ swizzle(lane)];
+              line[v ^ swizzle(lane)] = make_float4(f[v].x + u.x, f[v].y + u.y, f[v].z + u.z, f[v].w + u.w);
+            }
+          }
         } else {
           uint32_t r[32];
           results(c, r);
@@ -585,6 +604,7 @@ __global__ void __launch_bounds__(kThreads, 1) muon_steps(const __grid_constant_
         for (int k = 0; k < 8; ++k) col_diag[k] = next_diag[k];
         asm volatile("cp.async.wait_all;" ::: "memory");
         __syncwarp();
+        if (q.which == SUM && half) break;  // (the warp's one chunk)
         if (q.which != APPLY && row0 == col0) {
           // the diagonal, where R is 0: b d + c d^2 and the sum's (of gram d is 0 so far)
           float* on = buf + lane * 32 + (((lane >> 2) ^ swizzle(lane)) << 2) + (lane & 3);
@@ -604,7 +624,7 @@ __global__ void __launch_bounds__(kThreads, 1) muon_steps(const __grid_constant_
             float e[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
 #pragma unroll
             for (int k = 0; k < 8; ++k) e[k] *= mul;
-            if (q.which != GRAM) {
+            if (!gram) {
               float x[8];
               const uint4* own = reinterpret_cast<const uint4*>(terms + i * 512) + lane;
               from_pairs(own[0], own[128], x);
@@ -656,6 +676,7 @@ __global__ void __launch_bounds__(kThreads, 1) muon_steps(const __grid_constant_
         }
         __syncwarp();
       }
+      if (q.which != SUM) ++j;
       // this CTA's part of the tile is done
       fence_global_proxies();
       epi_barrier();
@@ -690,20 +711,26 @@ int tiles_of(int which, int bn, int rows, int cols) {
 }
 
 // A matrix's tiles and splits go by its own size: its result does not depend on
-// the matrices beside it.  Tiles of 256 x 256 read less of shared memory for
-// each product, those of 256 x 128 fill the pairs better: wide ones where a
-// matrix has enough of them.
-int width_of(int which, int rows, int cols) { return tiles_of(which, 256, rows, cols) >= 32 ? 256 : 128; }
+// the matrices beside it.  Wide tiles read less of shared memory for each
+// product, narrow ones fill more pairs and are finished sooner: the widest of
+// which a matrix has enough.  Of gram 256 columns wherever there are as many,
+// since a diagonal tile then has one factor to load instead of two (and the
+// pairs are filled by splits).
+int width_of(int which, int rows, int cols) {
+  if (which == GRAM || which == SUM) return cols > 128 ? 256 : cols > 64 ? 128 : 64;
+  return tiles_of(which, 256, rows, cols) >= 32 ? 256 : tiles_of(which, 128, rows, cols) >= 16 ? 128 : 64;
+}
 
-// Splits of a gram's long side: over the pairs that its tiles leave idle, four
-// blocks of 64 or more each.
+// Splits of a gram's long side, three blocks of 64 or more each, so that a
+// matrix of few tiles keeps up to 16 pairs busy.
 int gram_splits(const MuonMat& t) {
   const int tiles = tiles_of(GRAM, width_of(GRAM, t.side, t.side), t.side, t.side);
   const int nkb = (int)ceil_div_ll(t.tall ? t.rows : t.cols, kBK);
-  int want = kPairs / tiles;
-  if (want > nkb / 4) want = nkb / 4;
-  if (want > kMuonSplits) want = kMuonSplits;
-  return want < 1 ? 1 : want;
+  int want = tiles == 1 ? 12 : tiles <= 16 ? 48 / tiles : 1;
+  if (want > nkb / 3) want = nkb / 3;
+  if (want < 2) return 1;
+  const int per = (nkb + want - 1) / want;
+  return (nkb + per - 1) / per;
 }
 
 template <int CAP>
@@ -715,22 +742,23 @@ cudaError_t launch(const MuonGroup& m, cudaStream_t s) {
   g.lr = m.lr;
   g.grad_scale = m.grad_scale;
   g.lr_device = m.lr_device;
-  g.n[0] = g.n[1] = g.n[2] = 0;
+  for (int k = 0; k < KINDS; ++k) g.n[k] = 0;
   for (int i = 0; i < m.count; ++i) {
     const MuonMat& t = m.mat[i];
     Item& q = g.item[i];
     q.m = t;
     const int nkb = (int)ceil_div_ll(t.tall ? t.rows : t.cols, kBK);
     q.splits = gram_splits(t);
-    q.per_split = (int)ceil_div_ll(nkb, q.splits);
-    q.splits = (int)ceil_div_ll(nkb, q.per_split);
-    for (int k = 0; k < 3; ++k) {
+    q.per_split = (nkb + q.splits - 1) / q.splits;
+    for (int k = 0; k < KINDS; ++k) {
       const int rows = k == APPLY ? t.rows : t.side, cols = k == APPLY ? t.cols : t.side;
       q.bn[k] = width_of(k, rows, cols);
       q.tiles_n[k] = (cols + q.bn[k] - 1) / q.bn[k];
       q.tiles[k] = tiles_of(k, q.bn[k], rows, cols);
+      if (k == GRAM) q.tiles[k] *= q.splits;
+      if (k == SUM) q.tiles[k] = q.splits > 1 ? q.tiles[k] * (q.bn[k] / 32) : 0;
       q.start[k] = g.n[k];
-      g.n[k] += q.tiles[k] * (k == GRAM ? q.splits : 1);
+      g.n[k] += q.tiles[k];
     }
     const int e = t.out_dtype == DC_BF16 ? 2 : 4;
     const void* out = m.update ? t.param : t.out;
@@ -767,7 +795,7 @@ cudaError_t launch(const MuonGroup& m, cudaStream_t s) {
     if (dev < kOnceDevices) at_once[dev].store(most, std::memory_order_relaxed);
   }
   int widest = 0;  // more pairs than the widest kind of a step has tiles would only wait
-  for (int k = 0; k < 3; ++k)
+  for (int k = 0; k < KINDS; ++k)
     if (g.n[k] > widest) widest = g.n[k];
   if (most > widest) most = widest;
   if (most > kPairs) most = kPairs;

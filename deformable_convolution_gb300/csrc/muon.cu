@@ -7,6 +7,19 @@ namespace {
 
 constexpr int kThreads = 256;
 
+// Eight consecutive values of either type.
+__device__ __forceinline__ void load8(const void* p, dc_dtype dt, long long i, float* v) {
+  if (dt == DC_BF16) {
+    const uint4 a = *reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p) + i);
+    const uint32_t w[4] = {a.x, a.y, a.z, a.w};
+#pragma unroll
+    for (int k = 0; k < 8; ++k) v[k] = __uint_as_float(k & 1 ? w[k >> 1] & 0xffff0000u : w[k >> 1] << 16);
+  } else {
+    const float4* f = reinterpret_cast<const float4*>(static_cast<const float*>(p) + i);
+    const float4 a = f[0], b = f[1];
+    v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
+  }
+}
 __device__ __forceinline__ float load_in(const void* p, dc_dtype dt, long long i) {
   return dt == DC_BF16 ? __bfloat162float(static_cast<const __nv_bfloat16*>(p)[i]) : static_cast<const float*>(p)[i];
 }
@@ -17,11 +30,9 @@ __device__ __forceinline__ bool skipped(const MuonGroup& g, float* scale) {
   return !(fabsf(*scale) <= 3.402823466e38f);
 }
 
-// What is orthogonalised: u of the updated m and the gradient, or `in`.
-__device__ __forceinline__ float direction(const MuonGroup& g, const MuonMat& t, float scale, long long i) {
-  const float v = load_in(t.in, t.in_dtype, i);
+// What is orthogonalised of an input value and, in a step, its updated m.
+__device__ __forceinline__ float direction(const MuonGroup& g, float scale, float v, float m) {
   if (!g.update) return v;
-  const float m = t.m[i];
   return g.nesterov ? m * g.momentum + v * scale * g.rest : m;
 }
 
@@ -44,15 +55,36 @@ __global__ void __launch_bounds__(kThreads) muon_squares(const __grid_constant__
   const MuonMat& t = g.mat[blockIdx.y];
   float scale;
   if (skipped(g, &scale) || blockIdx.x >= t.parts) return;
-  const long long count = (long long)t.rows * t.cols;
+  const long long count = (long long)t.rows * t.cols, step = (long long)t.parts * kThreads;
   float sum = 0.f;
-  for (long long i = (long long)blockIdx.x * kThreads + threadIdx.x; i < count; i += (long long)t.parts * kThreads) {
-    if (g.update) {
-      const float v = load_in(t.in, t.in_dtype, i) * scale;
-      t.m[i] = t.m[i] * g.momentum + v * g.rest;
+  // eight values a thread where the arrays allow it (the order of a matrix's sum
+  // goes by its size and the arrays' alignment)
+  if (t.vec) {
+    for (long long i = ((long long)blockIdx.x * kThreads + threadIdx.x) * 8; i < count; i += step * 8) {
+      float v[8], m[8];
+      load8(t.in, t.in_dtype, i, v);
+      if (g.update) {
+        load8(t.m, DC_F32, i, m);
+#pragma unroll
+        for (int k = 0; k < 8; ++k) m[k] = m[k] * g.momentum + v[k] * scale * g.rest;
+        float4* to = reinterpret_cast<float4*>(t.m + i);
+        to[0] = make_float4(m[0], m[1], m[2], m[3]);
+        to[1] = make_float4(m[4], m[5], m[6], m[7]);
+      }
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        const float u = direction(g, scale, v[k], m[k]);
+        sum += u * u;
+      }
     }
-    const float u = direction(g, t, scale, i);
-    sum += u * u;
+  } else {
+    for (long long i = (long long)blockIdx.x * kThreads + threadIdx.x; i < count; i += step) {
+      const float v = load_in(t.in, t.in_dtype, i);
+      float m = 0.f;
+      if (g.update) t.m[i] = m = t.m[i] * g.momentum + v * scale * g.rest;
+      const float u = direction(g, scale, v, m);
+      sum += u * u;
+    }
   }
   sum = block_sum(sum);
   if (threadIdx.x == 0) t.part[blockIdx.x] = sum;
@@ -70,14 +102,38 @@ __global__ void __launch_bounds__(kThreads) muon_begin(const __grid_constant__ M
   const float norm = sqrtf(block_sum(sum));
   // a norm that is not finite makes every element NaN
   const float f = norm <= 3.402823466e38f ? kOrthoScale / (norm + kOrthoEps) : __uint_as_float(0x7fffffffu);
-  const long long count = (long long)t.rows * t.cols;
-  for (long long i = (long long)blockIdx.x * kThreads + threadIdx.x; i < count; i += (long long)t.parts * kThreads) {
+  const long long count = (long long)t.rows * t.cols, step = (long long)t.parts * kThreads;
+  const long long low = muon_x_low(t);
+  if (t.vec && t.cols % 8 == 0) {
+    const unsigned row8 = (unsigned)t.cols / 8;
+    for (long long i = (long long)blockIdx.x * kThreads + threadIdx.x; i < count / 8; i += step) {
+      const unsigned long long r = count < (1LL << 34) ? (unsigned)i / row8 : (unsigned long long)i / row8;
+      float v[8], m[8];
+      load8(t.in, t.in_dtype, i * 8, v);
+      if (g.update) load8(t.m, DC_F32, i * 8, m);
+      uint32_t h[4], l[4];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const float a = direction(g, scale, v[2 * k], m[2 * k]) * f, b = direction(g, scale, v[2 * k + 1], m[2 * k + 1]) * f;
+        const __half2 hi = __floats2half2_rn(a, b);
+        const float2 back = __half22float2(hi);
+        const __half2 lo = __floats2half2_rn(a - back.x, b - back.y);
+        h[k] = *reinterpret_cast<const uint32_t*>(&hi);
+        l[k] = *reinterpret_cast<const uint32_t*>(&lo);
+      }
+      __half* x = t.x[0] + r * t.ld + (i - r * row8) * 8;
+      *reinterpret_cast<uint4*>(x) = make_uint4(h[0], h[1], h[2], h[3]);
+      *reinterpret_cast<uint4*>(x + low) = make_uint4(l[0], l[1], l[2], l[3]);
+    }
+    return;
+  }
+  for (long long i = (long long)blockIdx.x * kThreads + threadIdx.x; i < count; i += step) {
     const long long r = i / t.cols;
-    const float v = direction(g, t, scale, i) * f;
+    const float v = direction(g, scale, load_in(t.in, t.in_dtype, i), g.update ? t.m[i] : 0.f) * f;
     const __half h = __float2half_rn(v);
     __half* x = t.x[0] + r * t.ld + (i - r * t.cols);
     x[0] = h;
-    x[muon_x_low(t)] = __float2half_rn(v - __half2float(h));
+    x[low] = __float2half_rn(v - __half2float(h));
   }
 }
 
@@ -105,8 +161,9 @@ void muon_plan(MuonGroup* g) {
   g->parts = 0;
   for (int i = 0; i < g->count; ++i) {
     MuonMat& t = g->mat[i];
-    const long long want = ceil_div_ll((long long)t.rows * t.cols, 8 * kThreads);
+    const long long count = (long long)t.rows * t.cols, want = ceil_div_ll(count, 8 * kThreads);
     t.parts = (int)(want < kMuonParts ? want : kMuonParts);
+    t.vec = count % 8 == 0 && (uintptr_t)t.in % 16 == 0 && (uintptr_t)t.m % 16 == 0;
     if (t.parts > g->parts) g->parts = t.parts;
   }
 }

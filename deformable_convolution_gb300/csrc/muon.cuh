@@ -10,7 +10,7 @@ namespace dc {
 
 // Matrices of one group of launches.
 constexpr int kMuonMats = 40;
-constexpr int kMuonParts = 304;  // most blocks of the first launch for one matrix
+constexpr int kMuonParts = 608;  // most blocks of the first launch for one matrix
 // Values between the products are kept times 2^12: X and A stay below 2^12 *
 // 1.5 and the polynomial of A below 2^12 * 4, inside a 16-bit float's range,
 // and a pair's low part keeps its digits down to 2^-36.
@@ -35,6 +35,7 @@ struct MuonMat {
   unsigned int* done;  // [4] CTAs' finished tiles of each kind
   int rows, cols, ld, side, lds;
   int parts;    // blocks of the launches over single elements
+  int vec;      // whose arrays are whole 16-byte pieces
   bool tall;  // rows > cols: A = X^T X, X = a X + X B
   dc_dtype in_dtype, out_dtype;
   float weight_decay, rate;

@@ -568,7 +568,7 @@ __global__ void __launch_bounds__(kThreads, 1) muon_steps(const __grid_constant_
           for (int v = 0; v < 8; ++v) f[v] = make_float4(0.f, 0.f, 0.f, 0.f);
           if (row0 < rows && col0 < cols) {
             const int middle = (t.splits + 1) / 2;
-#pragma unroll 2
+#pragma unroll 3
             for (int k = half ? middle : 0; k < (half ? t.splits : middle); ++k) {
               const float4* from = place(k, q.split);
 #pragma unroll
@@ -722,11 +722,13 @@ int width_of(int which, int rows, int cols) {
 }
 
 // Splits of a gram's long side, three blocks of 64 or more each, so that a
-// matrix of few tiles keeps up to 16 pairs busy.
+// matrix of one or three tiles (a short side up to 512) keeps up to 24 pairs
+// busy.  (Eight of 1024 x 1024 split over four lost 40 us of 130 a step to
+// adding up.)
 int gram_splits(const MuonMat& t) {
   const int tiles = tiles_of(GRAM, width_of(GRAM, t.side, t.side), t.side, t.side);
   const int nkb = (int)ceil_div_ll(t.tall ? t.rows : t.cols, kBK);
-  int want = tiles == 1 ? 12 : tiles <= 16 ? 48 / tiles : 1;
+  int want = tiles == 1 ? 12 : tiles == 3 ? 8 : 1;
   if (want > nkb / 3) want = nkb / 3;
   if (want < 2) return 1;
   const int per = (nkb + want - 1) / want;

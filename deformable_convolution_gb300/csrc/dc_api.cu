@@ -1057,8 +1057,9 @@ dc_status check_weight(const dc_muon_tensor& t) {
   return DC_OK;
 }
 
-// Appends a matrix to the group, its storage at *at bytes into ws (null: only counted).
-void add_matrix(MuonGroup* g, int rows, int cols, char* ws, size_t* at) {
+// Appends a matrix to the group, its storage at *at bytes into ws (null: only
+// counted); small ones need none.
+void add_matrix(MuonGroup* g, int rows, int cols, bool small, char* ws, size_t* at) {
   MuonMat& t = g->mat[g->count++];
   t.rows = rows;
   t.cols = cols;
@@ -1066,6 +1067,7 @@ void add_matrix(MuonGroup* g, int rows, int cols, char* ws, size_t* at) {
   t.tall = rows > cols;
   t.side = t.tall ? cols : rows;
   t.lds = (t.side + 7) / 8 * 8;
+  if (small) return;
   auto take = [&](size_t bytes) {
     char* p = ws ? ws + *at : nullptr;
     *at += (bytes + 255) / 256 * 256;
@@ -1090,22 +1092,53 @@ size_t muon_bytes(int count, F&& size) {
   for (int i = 0; i < count; ++i) {
     int rows, cols;
     size(i, &rows, &cols);
-    if (rows == 0 || cols == 0) continue;
+    if (rows == 0 || cols == 0 || muon_is_small(rows, cols)) continue;
     if (g.count == kMuonMats) g.count = 0, at = 0;
-    add_matrix(&g, rows, cols, nullptr, &at);
+    add_matrix(&g, rows, cols, false, nullptr, &at);
     if (at > most) most = at;
   }
   return most;
 }
 
-// The group's launches.
-dc_status run_muon(MuonGroup& g, cudaStream_t s) {
+// A group's launches.
+dc_status run_muon(MuonGroup& g, bool small, cudaStream_t s) {
   if (g.count == 0) return DC_OK;
-  muon_plan(&g);
-  dc_status st = cuda_status(timed("muon_squares", s, [&] { return launch_muon_squares(g, s); }));
-  if (st == DC_OK) st = cuda_status(timed("muon_begin", s, [&] { return launch_muon_begin(g, s); }));
-  if (st == DC_OK) st = cuda_status(timed("muon_steps", s, [&] { return launch_muon_steps(g, s); }));
+  dc_status st;
+  if (small) {
+    st = cuda_status(timed("muon_small", s, [&] { return launch_muon_small(g, s); }));
+  } else {
+    muon_plan(&g);
+    st = cuda_status(timed("muon_squares", s, [&] { return launch_muon_squares(g, s); }));
+    if (st == DC_OK) st = cuda_status(timed("muon_begin", s, [&] { return launch_muon_begin(g, s); }));
+    if (st == DC_OK) st = cuda_status(timed("muon_steps", s, [&] { return launch_muon_steps(g, s); }));
+  }
+  g.count = 0;
   return st;
+}
+
+// All matrices of a call, those with a short side first: set(i, &t) fills in
+// what is not a size and returns the sizes.
+template <typename F>
+dc_status run_matrices(MuonGroup& g, int count, F&& set, void* ws, cudaStream_t s) {
+  for (int small = 1; small >= 0; --small) {
+    size_t at = 0;
+    for (int i = 0; i <= count; ++i) {
+      MuonMat t{};
+      int rows = 0, cols = 0;
+      if (i < count) set(i, &t, &rows, &cols);
+      if (i == count || g.count == kMuonMats) {
+        const bool any = g.count > 0;
+        const dc_status st = run_muon(g, small != 0, s);
+        if (st != DC_OK) return st;
+        g.beside = small && any;
+        at = 0;
+      }
+      if (rows == 0 || cols == 0 || muon_is_small(rows, cols) != (small != 0)) continue;
+      g.mat[g.count] = t;
+      add_matrix(&g, rows, cols, small != 0, static_cast<char*>(ws), &at);
+    }
+  }
+  return DC_OK;
 }
 
 dc_status check_ortho(int count, const void* mats, int steps, dc_ortho_precision precision) {
@@ -1215,23 +1248,17 @@ dc_status dc_orthogonalize(const dc_matrix* mats, int count, int steps,
   MuonGroup g{};
   g.steps = steps;
   g.precision = precision;
-  size_t at = 0;
-  for (int i = 0; i < count; ++i) {
-    const dc_matrix& m = mats[i];
-    if (m.rows == 0 || m.cols == 0) continue;
-    if (g.count == kMuonMats) {
-      if ((st = run_muon(g, static_cast<cudaStream_t>(stream))) != DC_OK) return st;
-      g.count = 0, at = 0;
-    }
-    MuonMat& t = g.mat[g.count];
-    t = MuonMat{};
-    t.in = m.in;
-    t.out = m.out;
-    t.in_dtype = m.in_dtype;
-    t.out_dtype = m.out_dtype;
-    add_matrix(&g, m.rows, m.cols, static_cast<char*>(ws), &at);
-  }
-  return run_muon(g, static_cast<cudaStream_t>(stream));
+  return run_matrices(
+      g, count,
+      [&](int i, MuonMat* t, int* rows, int* cols) {
+        const dc_matrix& m = mats[i];
+        t->in = m.in;
+        t->out = m.out;
+        t->in_dtype = m.in_dtype;
+        t->out_dtype = m.out_dtype;
+        *rows = m.rows, *cols = m.cols;
+      },
+      ws, static_cast<cudaStream_t>(stream));
 }
 
 dc_status dc_muon_workspace_size(const dc_muon_tensor* tensors, int count, size_t* bytes) {
@@ -1269,27 +1296,21 @@ dc_status dc_muon_step(const dc_muon_tensor* tensors, int count, const dc_muon_h
   g.lr = (float)hyper->lr;
   g.grad_scale = grad_scale;
   g.lr_device = lr;
-  size_t at = 0;
-  for (int i = 0; i < count; ++i) {
-    const dc_muon_tensor& m = tensors[i];
-    if (m.rows == 0 || m.cols == 0) continue;
-    if (g.count == kMuonMats) {
-      if ((st = run_muon(g, static_cast<cudaStream_t>(stream))) != DC_OK) return st;
-      g.count = 0, at = 0;
-    }
-    MuonMat& t = g.mat[g.count];
-    t = MuonMat{};
-    t.in = m.grad;
-    t.in_dtype = m.grad_dtype;
-    t.param = m.param;
-    t.out_dtype = m.param_dtype;
-    t.master = m.master;
-    t.m = m.m;
-    t.weight_decay = m.weight_decay;
-    t.rate = m.rate;
-    add_matrix(&g, m.rows, m.cols, static_cast<char*>(ws), &at);
-  }
-  return run_muon(g, static_cast<cudaStream_t>(stream));
+  return run_matrices(
+      g, count,
+      [&](int i, MuonMat* t, int* rows, int* cols) {
+        const dc_muon_tensor& m = tensors[i];
+        t->in = m.grad;
+        t->in_dtype = m.grad_dtype;
+        t->param = m.param;
+        t->out_dtype = m.param_dtype;
+        t->master = m.master;
+        t->m = m.m;
+        t->weight_decay = m.weight_decay;
+        t->rate = m.rate;
+        *rows = m.rows, *cols = m.cols;
+      },
+      ws, static_cast<cudaStream_t>(stream));
 }
 
 }  // extern "C"

@@ -1,40 +1,12 @@
 // Orthogonalisation by Newton-Schulz products and the Muon step: the passes
 // over single elements around the products.
 #include "muon.cuh"
+#include "muon_values.cuh"
 
 namespace dc {
 namespace {
 
 constexpr int kThreads = 256;
-
-// Eight consecutive values of either type.
-__device__ __forceinline__ void load8(const void* p, dc_dtype dt, long long i, float* v) {
-  if (dt == DC_BF16) {
-    const uint4 a = *reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p) + i);
-    const uint32_t w[4] = {a.x, a.y, a.z, a.w};
-#pragma unroll
-    for (int k = 0; k < 8; ++k) v[k] = __uint_as_float(k & 1 ? w[k >> 1] & 0xffff0000u : w[k >> 1] << 16);
-  } else {
-    const float4* f = reinterpret_cast<const float4*>(static_cast<const float*>(p) + i);
-    const float4 a = f[0], b = f[1];
-    v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
-  }
-}
-__device__ __forceinline__ float load_in(const void* p, dc_dtype dt, long long i) {
-  return dt == DC_BF16 ? __bfloat162float(static_cast<const __nv_bfloat16*>(p)[i]) : static_cast<const float*>(p)[i];
-}
-
-// Whether the step is skipped: its scale is not finite.
-__device__ __forceinline__ bool skipped(const MuonGroup& g, float* scale) {
-  *scale = g.update && g.grad_scale ? *g.grad_scale : 1.f;
-  return !(fabsf(*scale) <= 3.402823466e38f);
-}
-
-// What is orthogonalised of an input value and, in a step, its updated m.
-__device__ __forceinline__ float direction(const MuonGroup& g, float scale, float v, float m) {
-  if (!g.update) return v;
-  return g.nesterov ? m * g.momentum + v * scale * g.rest : m;
-}
 
 __device__ __forceinline__ float block_sum(float v) {
   __shared__ float part[kThreads / 32];
@@ -50,7 +22,8 @@ __device__ __forceinline__ float block_sum(float v) {
 }
 
 __global__ void __launch_bounds__(kThreads) muon_squares(const __grid_constant__ MuonGroup g) {
-  pdl_wait();
+  // beside the launch of the small matrices, which waited for what came before
+  if (!g.beside) pdl_wait();
   pdl_release();
   const MuonMat& t = g.mat[blockIdx.y];
   float scale;

@@ -45,6 +45,7 @@ struct MuonGroup {
   int count, steps, parts;  // parts: the largest of the matrices'
   dc_ortho_precision precision;
   bool update;  // a Muon step
+  bool beside;  // launched right behind the small matrices of the same call
   float momentum, rest;
   int nesterov;
   float lr;
@@ -65,5 +66,8 @@ cudaError_t launch_muon_begin(const MuonGroup& g, cudaStream_t s);
 // All steps; the result to out, or to the parameters.
 cudaError_t launch_muon_steps(const MuonGroup& g, cudaStream_t s);
 size_t muon_sums_bytes(const MuonMat& t);
+// Matrices with a short side up to 64 go through all of it in one launch.
+bool muon_is_small(int rows, int cols);
+cudaError_t launch_muon_small(const MuonGroup& g, cudaStream_t s);
 
 }  // namespace dc

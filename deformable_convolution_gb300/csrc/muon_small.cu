@@ -1,0 +1,387 @@
+// Orthogonalisation and the Muon step of matrices with a short side of at most
+// 64 (the offset convolutions' weights): everything in one launch.
+//
+// A matrix belongs to a cluster of eight CTAs, each of which keeps its share of
+// the long side in shared memory, as pairs of 16-bit floats times 2^12, from
+// the first step to the last.  A step: every CTA multiplies its share (R and X
+// as in muon_products.cu, but on mma.sync: 18 rows fill a seventh of a tcgen05
+// tile's 128), the CTAs add up their grams by rows through distributed shared
+// memory, in order, and hand every sum to all; the polynomial (64 x 64 at most)
+// is computed by each for itself, and X updated in place.  Two cluster barriers
+// a step take the place of four waits through global memory: 18 x 2304 takes
+// 25 us in place of 125.
+//
+// Products are high high + high low + low high whatever the precision: they are
+// not what a step spends its time on.
+#include "dc_tma.cuh"
+#include "muon.cuh"
+#include "muon_values.cuh"
+
+namespace dc {
+namespace {
+
+constexpr int kThreads = 256, kWarps = 8, kCtas = 8;
+
+// Layout of a CTA's shared memory, in bytes.
+struct Small {
+  int sp, nc;        // the short side up to a multiple of 16; the columns of X that the CTA keeps
+  int xs, ps;        // row strides of X and of R and P in halves (an odd number of 16-byte pieces)
+  int ks;            // splits of the CTA's columns over warps in the gram
+  int x, part, r, p, diag, bytes;
+};
+__host__ __device__ inline Small small_of(int side, int length) {
+  Small s;
+  s.sp = (side + 15) / 16 * 16;
+  s.nc = ((length + kCtas - 1) / kCtas + 15) / 16 * 16;
+  s.xs = s.nc + 8;
+  s.ps = s.sp + 8;
+  s.ks = s.sp == 16 ? 8 : s.sp == 32 ? 2 : 1;
+  s.x = 0;                                     // [2][sp][xs] halves
+  s.part = s.x + 4 * s.sp * s.xs;              // [ks][sp][sp + 4] float
+  s.r = s.part + s.ks * s.sp * (s.sp + 4) * 4; // [2][sp][ps] halves
+  s.p = s.r + 4 * s.sp * s.ps;
+  s.diag = s.p + 4 * s.sp * s.ps;              // [2][sp] float: of the gram and of the polynomial; [8] sums of squares
+  s.bytes = s.diag + 8 * s.sp + 64;
+  return s;
+}
+constexpr int kMaxBytes = 224 * 1024;
+
+__device__ __forceinline__ uint32_t cta_rank() {
+  uint32_t r;
+  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+  return r;
+}
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\nbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+__device__ __forceinline__ uint32_t in_cta(uint32_t addr, uint32_t rank) {
+  uint32_t r;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(rank));
+  return r;
+}
+__device__ __forceinline__ float ld_remote(uint32_t addr) {
+  float v;
+  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
+  return v;
+}
+__device__ __forceinline__ void st_remote(uint32_t addr, float v) {
+  asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(addr), "f"(v) : "memory");
+}
+__device__ __forceinline__ void st_remote(uint32_t addr, __half v) {
+  asm volatile("st.shared::cluster.u16 [%0], %1;" ::"r"(addr), "h"(__half_as_ushort(v)) : "memory");
+}
+
+__device__ __forceinline__ void ldm4(uint32_t* r, uint32_t addr) { px::ldmatrix_x4(r, addr); }
+__device__ __forceinline__ void ldm4t(uint32_t* r, uint32_t addr) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr));
+}
+__device__ __forceinline__ void mma(float* d, const uint32_t* a, const uint32_t* b) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};\n"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b[0]), "r"(b[1]));
+}
+
+// acc[2][4] += rows m0 .. + 15 of `a` by rows n0 .. + 15 of `b` over columns k0
+// .. + 15 (pairs: the low parts stand `alow`, `blow` bytes on).  main: high
+// high; cross: the others.
+__device__ __forceinline__ void unit16(float (*acc)[4], float (*cross)[4], uint32_t a, uint32_t alow, uint32_t b,
+                                       uint32_t blow) {
+  uint32_t ah[4], al[4], bh[4], bl[4];
+  ldm4(ah, a);
+  ldm4(al, a + alow);
+  ldm4(bh, b);
+  ldm4(bl, b + blow);
+#pragma unroll
+  for (int n = 0; n < 2; ++n) {
+    mma(acc[n], ah, bh + 2 * n);
+    mma(cross[n], ah, bl + 2 * n);
+    mma(cross[n], al, bh + 2 * n);
+  }
+}
+
+__global__ void __launch_bounds__(kThreads, 1) muon_small(const __grid_constant__ MuonGroup g) {
+  extern __shared__ __align__(16) unsigned char smem[];
+  pdl_wait();
+  pdl_release();
+  const MuonMat& t = g.mat[blockIdx.x / kCtas];
+  float scale;
+  if (skipped(g, &scale)) return;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const uint32_t rank = cta_rank();
+  const int side = t.side, length = t.tall ? t.rows : t.cols;
+  const Small L = small_of(side, length);
+  const int j0 = (int)rank * L.nc, here = max(0, min(L.nc, length - j0));  // its share of the long side
+  __half* xh = reinterpret_cast<__half*>(smem + L.x);
+  __half* xl = xh + L.sp * L.xs;
+  float* part = reinterpret_cast<float*>(smem + L.part);
+  __half* rh = reinterpret_cast<__half*>(smem + L.r);
+  __half* ph = reinterpret_cast<__half*>(smem + L.p);
+  float* gd = reinterpret_cast<float*>(smem + L.diag);
+  float* pd = gd + L.sp;
+  float* squares = pd + L.sp;
+  const uint32_t base = px::smem_u32(smem);
+  // element e of the share in the order that memory has it: short index i, long index j of the share
+  const int inner = t.tall ? side : here;
+  auto split_of = [&](int e, int* i, int* j) {
+    const int o = e / inner, n = e - o * inner;
+    *i = t.tall ? n : o;
+    *j = t.tall ? o : n;
+  };
+  auto place = [&](int i, int j) { return t.tall ? (long long)(j0 + j) * side + i : (long long)i * length + j0 + j; };
+
+  // Passes over the share's values, kBatch of them loaded before the first is
+  // used: i, j and place of each, or a place of -1.
+  constexpr int kBatch = 6;
+  const int total = side * here;
+  auto batch = [&](int e0, int* i, int* j, long long* at) {
+#pragma unroll
+    for (int k = 0; k < kBatch; ++k) {
+      const int e = e0 + k * kThreads;
+      at[k] = -1;
+      if (e < total) {
+        split_of(e, &i[k], &j[k]);
+        at[k] = place(i[k], j[k]);
+      }
+    }
+  };
+  int bi_[kBatch], bj_[kBatch];
+  long long at[kBatch];
+
+  // the momentum's update and the norm
+  float sum = 0.f;
+  for (int e0 = tid; e0 < total; e0 += kBatch * kThreads) {
+    float v[kBatch], m[kBatch];
+    batch(e0, bi_, bj_, at);
+#pragma unroll
+    for (int k = 0; k < kBatch; ++k) {
+      v[k] = at[k] < 0 ? 0.f : load_in(t.in, t.in_dtype, at[k]);
+      m[k] = at[k] < 0 || !g.update ? 0.f : t.m[at[k]];
+    }
+#pragma unroll
+    for (int k = 0; k < kBatch; ++k) {
+      if (g.update) {
+        m[k] = m[k] * g.momentum + v[k] * scale * g.rest;
+        if (at[k] >= 0) t.m[at[k]] = m[k];
+      }
+      const float u = direction(g, scale, v[k], m[k]);
+      sum += u * u;
+    }
+  }
+#pragma unroll
+  for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+  if (lane == 0) squares[warp] = sum;
+  for (int e = tid; e < 2 * L.sp * L.xs / 8; e += kThreads) reinterpret_cast<uint4*>(smem + L.x)[e] = make_uint4(0, 0, 0, 0);
+  cluster_sync();
+  // every warp adds the 64 sums in one order
+  sum = 0.f;
+  for (int k = 0; k < 2; ++k) {
+    const int w = lane + 32 * k;
+    sum += ld_remote(in_cta(base + L.diag + 8 * L.sp + 4 * (w & 7), w >> 3));
+  }
+#pragma unroll
+  for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+  const float norm = sqrtf(sum);
+  const float f = norm <= 3.402823466e38f ? kOrthoScale / (norm + kOrthoEps) : __uint_as_float(0x7fffffffu);
+  for (int e0 = tid; e0 < total; e0 += kBatch * kThreads) {
+    float v[kBatch], m[kBatch];
+    batch(e0, bi_, bj_, at);
+#pragma unroll
+    for (int k = 0; k < kBatch; ++k) {
+      v[k] = at[k] < 0 ? 0.f : load_in(t.in, t.in_dtype, at[k]);
+      m[k] = at[k] < 0 || !g.update ? 0.f : t.m[at[k]];
+    }
+#pragma unroll
+    for (int k = 0; k < kBatch; ++k)
+      if (at[k] >= 0) {
+        const float u = direction(g, scale, v[k], m[k]) * f;
+        const __half h = __float2half_rn(u);
+        xh[bi_[k] * L.xs + bj_[k]] = h;
+        xl[bi_[k] * L.xs + bj_[k]] = __float2half_rn(u - __half2float(h));
+      }
+  }
+  __syncthreads();
+
+  const float unit = 1.f / kOrthoScale;
+  const float lr = g.lr_device ? *g.lr_device : g.lr;
+  const int blocks = L.sp / 16;
+  const uint32_t xlow = 2u * L.sp * L.xs, plow = 2u * L.sp * L.ps;
+  // ldmatrix's lanes: rows of an A unit (two 8 x 8 down, two across), of a B unit
+  // (two across, two down), and of one that is transposed as it is read
+  const int a_row = lane & 15, a_col = (lane >> 4) * 8;
+  const int b_row = (lane & 7) + (lane >> 4) * 8, b_col = (lane >> 3 & 1) * 8;
+  const int t_row = (lane & 7) + (lane >> 3 & 1) * 8, t_col = (lane >> 4) * 8;
+  const int acc_row = lane >> 2, acc_col = 2 * (lane & 3);
+
+  for (int step = 0; step < g.steps; ++step) {
+    // gram: units of 16 x 16 and, where these are few, parts of the columns, over the warps
+    const int tasks = blocks * blocks * L.ks, depth = L.nc / 16;
+    for (int q = warp; q < tasks; q += kWarps) {
+      const int k = q / (blocks * blocks), un = q - k * blocks * blocks, bi = un / blocks, bj = un - bi * blocks;
+      float acc[2][4] = {}, cross[2][4] = {};
+      const uint32_t a = base + L.x + 2u * ((16 * bi + a_row) * L.xs + a_col);
+      const uint32_t b = base + L.x + 2u * ((16 * bj + b_row) * L.xs + b_col);
+      for (int c = k; c < depth; c += L.ks) unit16(acc, cross, a + 32 * c, xlow, b + 32 * c, xlow);
+#pragma unroll
+      for (int n = 0; n < 2; ++n)
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          part[(k * L.sp + 16 * bi + acc_row + 8 * (e >> 1)) * (L.sp + 4) + 16 * bj + 8 * n + acc_col + (e & 1)] =
+              acc[n][e] + cross[n][e];
+    }
+    cluster_sync();
+    // this CTA's rows of the sum, handed to all
+    for (int e = tid; e < L.sp * L.sp / kCtas; e += kThreads) {
+      const int i = (int)rank * (L.sp / kCtas) + e / L.sp, j = e % L.sp;
+      float v = 0.f;
+      for (int k = 0; k < L.ks; ++k) {
+        const uint32_t at = base + L.part + 4u * ((k * L.sp + i) * (L.sp + 4) + j);
+        float w[kCtas];
+#pragma unroll
+        for (int c = 0; c < kCtas; ++c) w[c] = ld_remote(in_cta(at, c));
+#pragma unroll
+        for (int c = 0; c < kCtas; ++c) v += w[c];
+      }
+      v *= unit;
+      const float d = v * unit;
+      if (i == j) v = 0.f;
+      const __half h = __float2half_rn(v), l = __float2half_rn(v - __half2float(h));
+#pragma unroll
+      for (int c = 0; c < kCtas; ++c) {
+        const uint32_t to = in_cta(base, c);
+        st_remote(to + L.r + 2u * (i * L.ps + j), h);
+        st_remote(to + L.r + plow + 2u * (i * L.ps + j), l);
+        if (i == j) st_remote(to + L.diag + 4u * i, d);
+      }
+    }
+    cluster_sync();
+    // P = b R + c (R R + (d_i + d_j) R), its diagonal apart
+    for (int q = warp; q < blocks * blocks; q += kWarps) {
+      const int bi = q / blocks, bj = q - bi * blocks;
+      float acc[2][4] = {}, cross[2][4] = {};
+      const uint32_t a = base + L.r + 2u * ((16 * bi + a_row) * L.ps + a_col);
+      const uint32_t b = base + L.r + 2u * ((16 * bj + b_row) * L.ps + b_col);
+      for (int c = 0; c < blocks; ++c) unit16(acc, cross, a + 32 * c, plow, b + 32 * c, plow);
+#pragma unroll
+      for (int n = 0; n < 2; ++n)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const int i = 16 * bi + acc_row + 8 * (e >> 1), j = 16 * bj + 8 * n + acc_col + (e & 1);
+          const float sq = (acc[n][e] + cross[n][e]) * unit, di = gd[i], dj = gd[j];
+          const float x = __half2float(rh[i * L.ps + j]) + __half2float(rh[L.sp * L.ps + i * L.ps + j]);
+          float v = kOrthoB * x + kOrthoC * (sq + (di + dj) * x);
+          if (i == j) {
+            pd[i] = kOrthoB * di + kOrthoC * (di * di + sq * unit);
+            v = 0.f;
+          }
+          const __half h = __float2half_rn(v);
+          ph[i * L.ps + j] = h;
+          ph[L.sp * L.ps + i * L.ps + j] = __float2half_rn(v - __half2float(h));
+        }
+    }
+    __syncthreads();
+    // X = (a + e) X + P X, 16 columns at a time: a warp has read them all before it writes
+    for (int cb = warp; cb < L.nc / 16; cb += kWarps) {
+      if (16 * cb >= here) break;
+      uint32_t bh[4][4], bl[4][4];
+#pragma unroll
+      for (int c = 0; c < 4; ++c)
+        if (c < blocks) {
+          const uint32_t at = base + L.x + 2u * ((16 * c + t_row) * L.xs + 16 * cb + t_col);
+          ldm4t(bh[c], at);
+          ldm4t(bl[c], at + xlow);
+        }
+      __syncwarp();
+      for (int bi = 0; bi < blocks; ++bi) {
+        float acc[2][4] = {}, cross[2][4] = {};
+#pragma unroll
+        for (int c = 0; c < 4; ++c)
+          if (c < blocks) {
+            uint32_t ah[4], al[4];
+            const uint32_t at = base + L.p + 2u * ((16 * bi + a_row) * L.ps + 16 * c + a_col);
+            ldm4(ah, at);
+            ldm4(al, at + plow);
+#pragma unroll
+            for (int n = 0; n < 2; ++n) {
+              mma(acc[n], ah, bh[c] + 2 * n);
+              mma(cross[n], ah, bl[c] + 2 * n);
+              mma(cross[n], al, bh[c] + 2 * n);
+            }
+          }
+#pragma unroll
+        for (int n = 0; n < 2; ++n)
+#pragma unroll
+          for (int r = 0; r < 2; ++r) {
+            const int i = 16 * bi + acc_row + 8 * r, j = 16 * cb + 8 * n + acc_col;
+            __half2* hp = reinterpret_cast<__half2*>(xh + i * L.xs + j);
+            __half2* lp = reinterpret_cast<__half2*>(xl + i * L.xs + j);
+            const float2 h = __half22float2(*hp), l = __half22float2(*lp);
+            const float e = kOrthoA + pd[i];
+            const float v0 = (acc[n][2 * r] + cross[n][2 * r]) * unit + e * (h.x + l.x);
+            const float v1 = (acc[n][2 * r + 1] + cross[n][2 * r + 1]) * unit + e * (h.y + l.y);
+            const __half2 w = __floats2half2_rn(v0, v1);
+            const float2 back = __half22float2(w);
+            *hp = w;
+            *lp = __floats2half2_rn(v0 - back.x, v1 - back.y);
+          }
+      }
+    }
+    __syncthreads();
+  }
+  // the result, in the order that memory has it
+  for (int e0 = tid; e0 < total; e0 += kBatch * kThreads) {
+    float p[kBatch];
+    batch(e0, bi_, bj_, at);
+    if (g.update) {
+#pragma unroll
+      for (int k = 0; k < kBatch; ++k)
+        p[k] = at[k] < 0 ? 0.f : t.master ? t.master[at[k]] : load_in(t.param, t.out_dtype, at[k]);
+    }
+#pragma unroll
+    for (int k = 0; k < kBatch; ++k)
+      if (at[k] >= 0) {
+        const int x = bi_[k] * L.xs + bj_[k];
+        const float v = (__half2float(xh[x]) + __half2float(xl[x])) * unit;
+        write_one(g, t, lr, at[k], p[k], v);
+      }
+  }
+  cluster_sync();  // no CTA leaves while another reads its shared memory
+}
+
+}  // namespace
+
+bool muon_is_small(int rows, int cols) {
+  const int side = rows < cols ? rows : cols, length = rows < cols ? cols : rows;
+  return side <= 64 && length <= (1 << 20) && small_of(side, length).bytes <= kMaxBytes;
+}
+
+cudaError_t launch_muon_small(const MuonGroup& g, cudaStream_t s) {
+  int most = 0;
+  for (int i = 0; i < g.count; ++i) {
+    const MuonMat& t = g.mat[i];
+    const int b = small_of(t.side, t.tall ? t.rows : t.cols).bytes;
+    if (b > most) most = b;
+  }
+  cudaError_t e = cudaFuncSetAttribute(muon_small, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxBytes);
+  if (e != cudaSuccess) return e;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)(kCtas * g.count));
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = (size_t)most;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = kCtas;
+  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  e = cudaLaunchKernelEx(&cfg, muon_small, g);
+  note_launches(1);
+  return e;
+}
+
+}  // namespace dc

@@ -23,7 +23,7 @@ INVALID, UNSUPPORTED, WORKSPACE = B.DC_ERR_INVALID_ARG, B.DC_ERR_UNSUPPORTED, B.
 # ---------------------------------------------------------------- refusals
 
 def ortho_status(count=1, steps=5, precision=0, ws=0x10000, nbytes=1 << 40, table=True, **kw):
-    d = dict(in_=0x1000, out=0x2000, rows=8, cols=8, in_dtype=B.DC_F32, out_dtype=B.DC_F32)
+    d = dict(in_=0x1000, out=0x2000, rows=80, cols=80, in_dtype=B.DC_F32, out_dtype=B.DC_F32)
     d.update(kw)
     t = (B.DcMatrix * 1)(B.DcMatrix(**d)) if table else None
     return B.lib().dc_orthogonalize(t, count, steps, precision, ws, nbytes, None)
@@ -43,7 +43,7 @@ def test_orthogonalize_checks_its_arguments(kw, status):
 
 def muon_status(count=1, scale=None, lr_device=None, ws=0x10000, nbytes=1 << 40, **kw):
     h = dict(lr=1e-3, momentum=0.95, nesterov=1, steps=5, precision=0)
-    d = dict(param=0x1000, master=None, grad=0x2000, m=0x3000, rows=8, cols=8, param_dtype=B.DC_F32,
+    d = dict(param=0x1000, master=None, grad=0x2000, m=0x3000, rows=80, cols=80, param_dtype=B.DC_F32,
              grad_dtype=B.DC_F32, weight_decay=0.0, rate=1.0)
     for k, v in kw.items():
         (h if k in h else d)[k] = v
@@ -70,7 +70,7 @@ def test_muon_checks_its_arguments(kw, status):
 def test_other_refusals():
     L = B.lib()
     out = ctypes.c_size_t(0)
-    t = (B.DcMatrix * 1)(B.DcMatrix(None, None, 8, 8, 0, 0))
+    t = (B.DcMatrix * 1)(B.DcMatrix(None, None, 80, 80, 0, 0))
     assert L.dc_orthogonalize_workspace_size(t, 1, None) == INVALID
     assert L.dc_orthogonalize_workspace_size(None, 1, ctypes.byref(out)) == INVALID
     assert L.dc_orthogonalize_workspace_size(t, 1, ctypes.byref(out)) == B.DC_OK and out.value % 256 == 0 and out.value

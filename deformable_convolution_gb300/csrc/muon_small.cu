@@ -20,7 +20,7 @@
 namespace dc {
 namespace {
 
-constexpr int kThreads = 256, kWarps = 8, kCtas = 8;
+constexpr int kThreads = 512, kWarps = 16, kCtas = 8;
 
 // Layout of a CTA's shared memory, in bytes.
 struct Small {
@@ -35,12 +35,12 @@ __host__ __device__ inline Small small_of(int side, int length) {
   s.nc = ((length + kCtas - 1) / kCtas + 15) / 16 * 16;
   s.xs = s.nc + 8;
   s.ps = s.sp + 8;
-  s.ks = s.sp == 16 ? 8 : s.sp == 32 ? 2 : 1;
+  s.ks = s.sp == 16 ? 16 : s.sp == 32 ? 4 : 1;
   s.x = 0;                                     // [2][sp][xs] halves
   s.part = s.x + 4 * s.sp * s.xs;              // [ks][sp][sp + 4] float
   s.r = s.part + s.ks * s.sp * (s.sp + 4) * 4; // [2][sp][ps] halves
   s.p = s.r + 4 * s.sp * s.ps;
-  s.diag = s.p + 4 * s.sp * s.ps;              // [2][sp] float: of the gram and of the polynomial; [8] sums of squares
+  s.diag = s.p + 4 * s.sp * s.ps;              // [2][sp] float: of the gram and of the polynomial; [16] sums of squares
   s.bytes = s.diag + 8 * s.sp + 64;
   return s;
 }
@@ -67,8 +67,13 @@ __device__ __forceinline__ float ld_remote(uint32_t addr) {
 __device__ __forceinline__ void st_remote(uint32_t addr, float v) {
   asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(addr), "f"(v) : "memory");
 }
-__device__ __forceinline__ void st_remote(uint32_t addr, __half v) {
-  asm volatile("st.shared::cluster.u16 [%0], %1;" ::"r"(addr), "h"(__half_as_ushort(v)) : "memory");
+__device__ __forceinline__ void st_remote(uint32_t addr, __half2 v) {
+  asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(addr), "r"(*reinterpret_cast<const uint32_t*>(&v)) : "memory");
+}
+__device__ __forceinline__ float2 ld_remote2(uint32_t addr) {
+  float2 v;
+  asm volatile("ld.shared::cluster.v2.f32 {%0, %1}, [%2];" : "=f"(v.x), "=f"(v.y) : "r"(addr) : "memory");
+  return v;
 }
 
 __device__ __forceinline__ void ldm4(uint32_t* r, uint32_t addr) { px::ldmatrix_x4(r, addr); }
@@ -106,7 +111,7 @@ __global__ void __launch_bounds__(kThreads, 1) muon_small(const __grid_constant_
   extern __shared__ __align__(16) unsigned char smem[];
   pdl_wait();
   pdl_release();
-  const MuonMat& t = g.mat[blockIdx.x / kCtas];
+  const MuonMat t = g.mat[blockIdx.x / kCtas];  // (a copy: registers, where the table would be read again after every store)
   float scale;
   if (skipped(g, &scale)) return;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -123,38 +128,44 @@ __global__ void __launch_bounds__(kThreads, 1) muon_small(const __grid_constant_
   float* pd = gd + L.sp;
   float* squares = pd + L.sp;
   const uint32_t base = px::smem_u32(smem);
-  // element e of the share in the order that memory has it: short index i, long index j of the share
-  const int inner = t.tall ? side : here;
-  auto split_of = [&](int e, int* i, int* j) {
-    const int o = e / inner, n = e - o * inner;
-    *i = t.tall ? n : o;
-    *j = t.tall ? o : n;
+  // Passes over the share's values in the order that memory has them, kBatch of
+  // a thread's loaded before the first is used: short index i, long index j of
+  // the share and place of each, or a place of -1.
+  constexpr int kBatch = 8;
+  const int inner = t.tall ? side : here, total = side * here;
+  const int next_o = inner ? kThreads / inner : 0, next_n = kThreads - next_o * inner;
+  struct Walk {
+    int e, o, n;
   };
-  auto place = [&](int i, int j) { return t.tall ? (long long)(j0 + j) * side + i : (long long)i * length + j0 + j; };
-
-  // Passes over the share's values, kBatch of them loaded before the first is
-  // used: i, j and place of each, or a place of -1.
-  constexpr int kBatch = 6;
-  const int total = side * here;
-  auto batch = [&](int e0, int* i, int* j, long long* at) {
+  Walk walk;
+  auto start = [&] {
+    walk.e = tid;
+    walk.o = inner ? tid / inner : 0;
+    walk.n = tid - walk.o * inner;
+  };
+  auto batch = [&](int* x, long long* at) {  // x: the value's place in shared memory
 #pragma unroll
     for (int k = 0; k < kBatch; ++k) {
-      const int e = e0 + k * kThreads;
       at[k] = -1;
-      if (e < total) {
-        split_of(e, &i[k], &j[k]);
-        at[k] = place(i[k], j[k]);
+      if (walk.e < total) {
+        const int i = t.tall ? walk.n : walk.o, j = t.tall ? walk.o : walk.n;
+        x[k] = i * L.xs + j;
+        at[k] = t.tall ? (long long)(j0 + j) * side + i : (long long)i * length + j0 + j;
       }
+      walk.e += kThreads;
+      walk.o += next_o;
+      walk.n += next_n;
+      if (walk.n >= inner) walk.n -= inner, ++walk.o;
     }
   };
-  int bi_[kBatch], bj_[kBatch];
+  int xs[kBatch];
   long long at[kBatch];
 
   // the momentum's update and the norm
   float sum = 0.f;
-  for (int e0 = tid; e0 < total; e0 += kBatch * kThreads) {
+  for (start(); walk.e < total;) {
     float v[kBatch], m[kBatch];
-    batch(e0, bi_, bj_, at);
+    batch(xs, at);
 #pragma unroll
     for (int k = 0; k < kBatch; ++k) {
       v[k] = at[k] < 0 ? 0.f : load_in(t.in, t.in_dtype, at[k]);
@@ -175,19 +186,20 @@ __global__ void __launch_bounds__(kThreads, 1) muon_small(const __grid_constant_
   if (lane == 0) squares[warp] = sum;
   for (int e = tid; e < 2 * L.sp * L.xs / 8; e += kThreads) reinterpret_cast<uint4*>(smem + L.x)[e] = make_uint4(0, 0, 0, 0);
   cluster_sync();
-  // every warp adds the 64 sums in one order
+  // every warp adds the CTAs' sums in one order
   sum = 0.f;
-  for (int k = 0; k < 2; ++k) {
+#pragma unroll
+  for (int k = 0; k < kWarps * kCtas / 32; ++k) {
     const int w = lane + 32 * k;
-    sum += ld_remote(in_cta(base + L.diag + 8 * L.sp + 4 * (w & 7), w >> 3));
+    sum += ld_remote(in_cta(base + L.diag + 8 * L.sp + 4 * (w % kWarps), w / kWarps));
   }
 #pragma unroll
   for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
   const float norm = sqrtf(sum);
   const float f = norm <= 3.402823466e38f ? kOrthoScale / (norm + kOrthoEps) : __uint_as_float(0x7fffffffu);
-  for (int e0 = tid; e0 < total; e0 += kBatch * kThreads) {
+  for (start(); walk.e < total;) {
     float v[kBatch], m[kBatch];
-    batch(e0, bi_, bj_, at);
+    batch(xs, at);
 #pragma unroll
     for (int k = 0; k < kBatch; ++k) {
       v[k] = at[k] < 0 ? 0.f : load_in(t.in, t.in_dtype, at[k]);
@@ -198,8 +210,8 @@ __global__ void __launch_bounds__(kThreads, 1) muon_small(const __grid_constant_
       if (at[k] >= 0) {
         const float u = direction(g, scale, v[k], m[k]) * f;
         const __half h = __float2half_rn(u);
-        xh[bi_[k] * L.xs + bj_[k]] = h;
-        xl[bi_[k] * L.xs + bj_[k]] = __float2half_rn(u - __half2float(h));
+        xh[xs[k]] = h;
+        xl[xs[k]] = __float2half_rn(u - __half2float(h));
       }
   }
   __syncthreads();
@@ -233,27 +245,31 @@ __global__ void __launch_bounds__(kThreads, 1) muon_small(const __grid_constant_
     }
     cluster_sync();
     // this CTA's rows of the sum, handed to all
-    for (int e = tid; e < L.sp * L.sp / kCtas; e += kThreads) {
-      const int i = (int)rank * (L.sp / kCtas) + e / L.sp, j = e % L.sp;
-      float v = 0.f;
+    for (int e = tid; e < L.sp * L.sp / kCtas / 2; e += kThreads) {
+      const int i = (int)rank * (L.sp / kCtas) + 2 * e / L.sp, j = 2 * e % L.sp;
+      float v0 = 0.f, v1 = 0.f;
       for (int k = 0; k < L.ks; ++k) {
-        const uint32_t at = base + L.part + 4u * ((k * L.sp + i) * (L.sp + 4) + j);
-        float w[kCtas];
+        const uint32_t from = base + L.part + 4u * ((k * L.sp + i) * (L.sp + 4) + j);
+        float2 w[kCtas];
 #pragma unroll
-        for (int c = 0; c < kCtas; ++c) w[c] = ld_remote(in_cta(at, c));
+        for (int c = 0; c < kCtas; ++c) w[c] = ld_remote2(in_cta(from, c));
 #pragma unroll
-        for (int c = 0; c < kCtas; ++c) v += w[c];
+        for (int c = 0; c < kCtas; ++c) v0 += w[c].x, v1 += w[c].y;
       }
-      v *= unit;
-      const float d = v * unit;
-      if (i == j) v = 0.f;
-      const __half h = __float2half_rn(v), l = __float2half_rn(v - __half2float(h));
+      v0 *= unit, v1 *= unit;
+      const float d = (i == j ? v0 : v1) * unit;
+      const bool on = i == j || i == j + 1;
+      if (i == j) v0 = 0.f;
+      if (i == j + 1) v1 = 0.f;
+      const __half2 h = __floats2half2_rn(v0, v1);
+      const float2 back = __half22float2(h);
+      const __half2 l = __floats2half2_rn(v0 - back.x, v1 - back.y);
 #pragma unroll
       for (int c = 0; c < kCtas; ++c) {
         const uint32_t to = in_cta(base, c);
         st_remote(to + L.r + 2u * (i * L.ps + j), h);
         st_remote(to + L.r + plow + 2u * (i * L.ps + j), l);
-        if (i == j) st_remote(to + L.diag + 4u * i, d);
+        if (on) st_remote(to + L.diag + 4u * i, d);
       }
     }
     cluster_sync();
@@ -267,18 +283,22 @@ __global__ void __launch_bounds__(kThreads, 1) muon_small(const __grid_constant_
 #pragma unroll
       for (int n = 0; n < 2; ++n)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const int i = 16 * bi + acc_row + 8 * (e >> 1), j = 16 * bj + 8 * n + acc_col + (e & 1);
-          const float sq = (acc[n][e] + cross[n][e]) * unit, di = gd[i], dj = gd[j];
-          const float x = __half2float(rh[i * L.ps + j]) + __half2float(rh[L.sp * L.ps + i * L.ps + j]);
-          float v = kOrthoB * x + kOrthoC * (sq + (di + dj) * x);
-          if (i == j) {
-            pd[i] = kOrthoB * di + kOrthoC * (di * di + sq * unit);
-            v = 0.f;
-          }
-          const __half h = __float2half_rn(v);
-          ph[i * L.ps + j] = h;
-          ph[L.sp * L.ps + i * L.ps + j] = __float2half_rn(v - __half2float(h));
+        for (int r = 0; r < 2; ++r) {
+          const int i = 16 * bi + acc_row + 8 * r, j = 16 * bj + 8 * n + acc_col, o = i * L.ps + j;
+          const float2 h = __half22float2(*reinterpret_cast<const __half2*>(rh + o));
+          const float2 l = __half22float2(*reinterpret_cast<const __half2*>(rh + L.sp * L.ps + o));
+          const float di = gd[i];
+          const float2 dj = *reinterpret_cast<const float2*>(gd + j);
+          const float sq0 = (acc[n][2 * r] + cross[n][2 * r]) * unit, sq1 = (acc[n][2 * r + 1] + cross[n][2 * r + 1]) * unit;
+          float v0 = kOrthoB * (h.x + l.x) + kOrthoC * (sq0 + (di + dj.x) * (h.x + l.x));
+          float v1 = kOrthoB * (h.y + l.y) + kOrthoC * (sq1 + (di + dj.y) * (h.y + l.y));
+          const float on = kOrthoB * di + kOrthoC * di * di;
+          if (i == j) pd[i] = on + kOrthoC * sq0 * unit, v0 = 0.f;
+          if (i == j + 1) pd[i] = on + kOrthoC * sq1 * unit, v1 = 0.f;
+          const __half2 w = __floats2half2_rn(v0, v1);
+          const float2 back = __half22float2(w);
+          *reinterpret_cast<__half2*>(ph + o) = w;
+          *reinterpret_cast<__half2*>(ph + L.sp * L.ps + o) = __floats2half2_rn(v0 - back.x, v1 - back.y);
         }
     }
     __syncthreads();
@@ -331,9 +351,9 @@ __global__ void __launch_bounds__(kThreads, 1) muon_small(const __grid_constant_
     __syncthreads();
   }
   // the result, in the order that memory has it
-  for (int e0 = tid; e0 < total; e0 += kBatch * kThreads) {
+  for (start(); walk.e < total;) {
     float p[kBatch];
-    batch(e0, bi_, bj_, at);
+    batch(xs, at);
     if (g.update) {
 #pragma unroll
       for (int k = 0; k < kBatch; ++k)
@@ -342,8 +362,7 @@ __global__ void __launch_bounds__(kThreads, 1) muon_small(const __grid_constant_
 #pragma unroll
     for (int k = 0; k < kBatch; ++k)
       if (at[k] >= 0) {
-        const int x = bi_[k] * L.xs + bj_[k];
-        const float v = (__half2float(xh[x]) + __half2float(xl[x])) * unit;
+        const float v = (__half2float(xh[xs[k]]) + __half2float(xl[xs[k]])) * unit;
         write_one(g, t, lr, at[k], p[k], v);
       }
   }

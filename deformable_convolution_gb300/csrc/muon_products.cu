@@ -23,7 +23,7 @@
 // place too.  X enters as it lies, whichever side is contracted: the tensor
 // cores read 16-bit tiles in both orders.  A gram of few tiles splits its long
 // side over several pairs: each leaves its sums in the workspace, and tiles of a
-// kind of their own (sum: 32 columns of a tile) add them up in order.
+// kind of their own (sum: 16 columns of a tile) add them up in order.
 //
 // The launch is cooperative and walks one list of tiles, step by step, kind by
 // kind, matrix by matrix, dealt to the pairs in turn; a tile waits (on a count
@@ -52,6 +52,7 @@ constexpr int kEpiWarps = 8, kWarpTma = 8, kWarpMma = 9, kThreads = 320;
 constexpr int kPart = 2 * kBox;           // one part of a factor in a stage: 128 lines
 constexpr int kStage = 2 * kPart;         // one part of both factors
 constexpr int kStages = 5, kRing = kStages * kStage;
+constexpr int kSumCols = 16;              // columns of a tile that a sum adds up
 constexpr int kBuf = 4096;                // a warp's 32 x 32 results, and as much for their own terms
 constexpr size_t kSmem = 1024 + kRing + kEpiWarps * 2 * kBuf + 256;
 static_assert(kSmem <= 227 * 1024, "shared memory");
@@ -129,7 +130,7 @@ __device__ __forceinline__ Tile tile_of(const Items<CAP>& g, int w) {
     q.begin = q.split * t.per_split;
     q.end = min(((t.m.tall ? t.m.rows : t.m.cols) + kBK - 1) / kBK, q.begin + t.per_split);
   } else if (q.which == SUM) {
-    const int chunks = q.bn / 32;
+    const int chunks = q.bn / kSumCols;
     chunk = r % chunks;
     r /= chunks;
     q.end = 0;
@@ -150,7 +151,7 @@ __device__ __forceinline__ Tile tile_of(const Items<CAP>& g, int w) {
   q.m0 = i * 256;
   q.n0 = r * q.bn;
   q.diagonal = q.bn == 256 && q.m0 == q.n0 && q.which != APPLY;
-  if (q.which == SUM) q.split = chunk;  // the 32 columns of the tile that it adds up
+  if (q.which == SUM) q.split = chunk;  // the columns of the tile that it adds up
   return q;
 }
 
@@ -455,7 +456,8 @@ __global__ void __launch_bounds__(kThreads, 1) muon_steps(const __grid_constant_
       const Tile q = tile_of(g, w);
       const Item& t = *q.t;
       const MuonMat& m = t.m;
-      const int rows = q.which == APPLY ? m.rows : m.side, cols = q.which == APPLY ? m.cols : m.side;
+      const int rows = q.which == APPLY ? m.rows : m.side;
+      const int cols = q.which == APPLY ? m.cols : q.which == SUM ? min(m.side, q.n0 + (q.split + 1) * kSumCols) : m.side;
       const long long ld = q.which == APPLY ? m.ld : m.lds;
       const long long low = q.which == APPLY ? muon_x_low(m) : muon_p_low(m);
       const __half* add = q.which == POLY ? m.gram : m.x[q.step & 1];
@@ -559,20 +561,22 @@ __global__ void __launch_bounds__(kThreads, 1) muon_steps(const __grid_constant_
       const bool mirror = q.which != APPLY && q.n0 + q.bn <= q.m0;
 #pragma unroll 1
       for (int c = split ? chunks : 0; c < chunks; ++c) {
-        const int col0 = q.n0 + (q.which == SUM ? q.split : half * chunks + c) * 32, col = col0 + 8 * piece;
+        const int col0 = q.n0 + (q.which == SUM ? q.split * kSumCols : (half * chunks + c) * 32), col = col0 + 8 * piece;
         float4* line = reinterpret_cast<float4*>(buf + lane * 32);
         if (q.which == SUM) {
           // each half of the warps adds up half of the splits, in order; the first adds the second's sums to its own
-          float4 f[8];
+          constexpr int kPieces = kSumCols / 4;
+          float4 f[kPieces];
 #pragma unroll
-          for (int v = 0; v < 8; ++v) f[v] = make_float4(0.f, 0.f, 0.f, 0.f);
+          for (int v = 0; v < kPieces; ++v) f[v] = make_float4(0.f, 0.f, 0.f, 0.f);
           if (row0 < rows && col0 < cols) {
-            const int middle = (t.splits + 1) / 2;
-#pragma unroll 3
-            for (int k = half ? middle : 0; k < (half ? t.splits : middle); ++k) {
-              const float4* from = place(k, q.split);
+            const int middle = (t.splits + 1) / 2, end = half ? t.splits : middle;
+            const float4* from = place(half ? middle : 0, q.split / 2) + q.split % 2 * kPieces * 32;
+            const long long next = place(1, 0) - place(0, 0);
+#pragma unroll 6
+            for (int k = half ? middle : 0; k < end; ++k, from += next) {
 #pragma unroll
-              for (int v = 0; v < 8; ++v) {
+              for (int v = 0; v < kPieces; ++v) {
                 const float4 u = __ldcg(from + 32 * v);
                 f[v].x += u.x, f[v].y += u.y, f[v].z += u.z, f[v].w += u.w;
               }
@@ -581,12 +585,12 @@ __global__ void __launch_bounds__(kThreads, 1) muon_steps(const __grid_constant_
           const float4* second = reinterpret_cast<const float4*>(stg + (warp | 4) * 2 * kBuf) + lane * 8;
           if (half) {
 #pragma unroll
-            for (int v = 0; v < 8; ++v) line[v ^ swizzle(lane)] = f[v];
+            for (int v = 0; v < kPieces; ++v) line[v ^ swizzle(lane)] = f[v];
           }
           epi_barrier();
           if (!half) {
 #pragma unroll
-            for (int v = 0; v < 8; ++v) {
+            for (int v = 0; v < kPieces; ++v) {
               const float4 u = second[v ^ swizzle(lane)];
               line[v ^ swizzle(lane)] = make_float4(f[v].x + u.x, f[v].y + u.y, f[v].z + u.z, f[v].w + u.w);
             }
@@ -605,12 +609,14 @@ __global__ void __launch_bounds__(kThreads, 1) muon_steps(const __grid_constant_
         asm volatile("cp.async.wait_all;" ::: "memory");
         __syncwarp();
         if (q.which == SUM && half) break;  // (the warp's one chunk)
-        if (q.which != APPLY && row0 == col0) {
+        if (q.which != APPLY && (unsigned)(col0 - row0) < 32u) {
           // the diagonal, where R is 0: b d + c d^2 and the sum's (of gram d is 0 so far)
-          float* on = buf + lane * 32 + (((lane >> 2) ^ swizzle(lane)) << 2) + (lane & 3);
-          if (row0 + lane < rows)
+          const int cl = lane - (col0 - row0);  // this row's column of the chunk
+          if (cl >= 0 && row0 + lane < min(rows, cols)) {
+            float* on = buf + lane * 32 + (((cl >> 2) ^ swizzle(lane)) << 2) + (cl & 3);
             diag_out[row0 + lane] = *on * (mul * unit) + (kOrthoB + kOrthoC * row_diag) * row_diag;
-          *on = 0.f;
+            *on = 0.f;
+          }
           __syncwarp();
         }
 #pragma unroll
@@ -658,7 +664,7 @@ __global__ void __launch_bounds__(kThreads, 1) muon_steps(const __grid_constant_
                 const int rl = 8 * piece + k;
                 e[k] = buf[rl * 32 + (((cl >> 2) ^ swizzle(rl)) << 2) + (cl & 3)];
               }
-              if (row0 + 8 * piece < rows) {
+              if (row0 + 8 * piece < rows && col0 + cl < cols) {
                 uint4 h, l;
                 to_pairs(e, &h, &l);
                 __half* to = out + (col0 + cl) * ld + row0 + 8 * piece;
@@ -758,7 +764,7 @@ cudaError_t launch(const MuonGroup& m, cudaStream_t s) {
       q.tiles_n[k] = (cols + q.bn[k] - 1) / q.bn[k];
       q.tiles[k] = tiles_of(k, q.bn[k], rows, cols);
       if (k == GRAM) q.tiles[k] *= q.splits;
-      if (k == SUM) q.tiles[k] = q.splits > 1 ? q.tiles[k] * (q.bn[k] / 32) : 0;
+      if (k == SUM) q.tiles[k] = q.splits > 1 ? q.tiles[k] * (q.bn[k] / kSumCols) : 0;
       q.start[k] = g.n[k];
       g.n[k] += q.tiles[k];
     }

@@ -30,7 +30,7 @@ EXPORTED_SYMBOLS = (
     "dc_group_norm_workspace_size", "dc_group_norm_fwd", "dc_group_norm_bwd",
     "dc_adamw_step", "dc_adamw_state_values", "dc_grad_norm_workspace_size", "dc_grad_norm",
     "dc_fp8_sizes", "dc_fp8_quantize", "dc_fp8_values", "dc_fp8_matmul_workspace_size",
-    "dc_fp8_matmul", "dc_orthogonalize_workspace_size", "dc_orthogonalize",
+    "dc_fp8_matmul", "dc_fp8_pointwise", "dc_orthogonalize_workspace_size", "dc_orthogonalize",
     "dc_muon_workspace_size", "dc_muon_step",
 )
 DC_NCHW, DC_NHWC = 0, 1
@@ -83,6 +83,11 @@ class DcFp8Product(ctypes.Structure):
     """Mirror of ``dc_fp8_product``."""
     _fields_ = [(name, ctypes.c_int) for name in (
         "batch", "m", "n", "k", "a_format", "b_format", "a_shared", "b_shared", "sum", "out")]
+
+
+class DcFp8Layer(ctypes.Structure):
+    """Mirror of ``dc_fp8_layer``."""
+    _fields_ = [(name, ctypes.c_int) for name in ("n", "pixels", "c_in", "c_out", "layout")]
 
 
 class DcMatrix(ctypes.Structure):
@@ -188,6 +193,7 @@ def lib() -> ctypes.CDLL:
             dc_fp8_sizes=[pq, i, ps, ps], dc_fp8_quantize=[pq, vp, vp, vp, vp, vp, vp],
             dc_fp8_values=[pq, i, vp, vp, vp, vp], dc_fp8_matmul_workspace_size=[pm, ps],
             dc_fp8_matmul=[pm, vp, vp, vp, vp, vp, vp, sz, vp],
+            dc_fp8_pointwise=[ctypes.POINTER(DcFp8Layer), vp, vp, vp, vp, vp],
             dc_orthogonalize_workspace_size=[po, i, ps],
             dc_orthogonalize=[po, i, i, i, vp, sz, vp], dc_muon_workspace_size=[pw, i, ps],
             dc_muon_step=[pw, i, ctypes.POINTER(DcMuonHyper), vp, vp, vp, sz, vp]).items():
@@ -852,6 +858,18 @@ def dc_fp8_matmul(p: Fp8Product, a, a_scales, b, b_scales, d, ws=None, stream=No
         _arg(d, "d", p.shape, p.torch_dtype), ws_ptr, ws_bytes, _raw_stream(stream))
     if status:
         raise DcError(status, "dc_fp8_matmul")
+
+
+def dc_fp8_pointwise(p: DcFp8Layer, x, w_codes, w_scales, y, stream=None):
+    """y = W x over the channels of every pixel, x quantised on the way: bf16
+    tensors [n, channels, pixels] (DC_NCHW) or [n, pixels, channels]."""
+    w = Fp8Problem(1, p.c_out, p.c_in, DC_BF16, DC_E4M3)
+    shapes = [(p.n, p.pixels, c) if p.layout == DC_NHWC else (p.n, c, p.pixels) for c in (p.c_in, p.c_out)]
+    status = lib().dc_fp8_pointwise(
+        p, _arg(x, "x", shapes[0], torch.bfloat16), *_codes(w_codes, w_scales, w.shapes, "w"),
+        _arg(y, "y", shapes[1], torch.bfloat16), _raw_stream(stream))
+    if status:
+        raise DcError(status, "dc_fp8_pointwise")
 
 
 # ---------------------------------------------------------------- Muon

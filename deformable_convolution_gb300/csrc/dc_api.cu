@@ -1227,6 +1227,22 @@ dc_status dc_fp8_matmul(const dc_fp8_product* prob, const void* a, const void* a
   return cuda_status(timed("fp8_matmul", s, [&] { return launch_fp8_matmul(t, s); }));
 }
 
+dc_status dc_fp8_pointwise(const dc_fp8_layer* prob, const void* x, const void* w_codes,
+                           const void* w_scales, void* y, void* stream) {
+  if (!prob || prob->n < 0 || prob->pixels <= 0 || prob->c_in <= 0 || prob->c_out <= 0 ||
+      (prob->layout != DC_NCHW && prob->layout != DC_NHWC))
+    return DC_ERR_INVALID_ARG;
+  if (prob->c_out > 256 || prob->c_in > (1 << 20) || (long long)prob->n * prob->pixels > (1 << 30))
+    return DC_ERR_UNSUPPORTED;
+  if (prob->n == 0) return DC_OK;
+  if (!x || !w_codes || !w_scales || !y) return DC_ERR_INVALID_ARG;
+  if (!aligned_to(x, 2) || !aligned16(w_codes) || !aligned16(w_scales) || !aligned_to(y, 2))
+    return DC_ERR_UNSUPPORTED;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  const Fp8Pointwise t{*prob, x, w_codes, w_scales, y};
+  return cuda_status(timed("fp8_pointwise", s, [&] { return launch_fp8_pointwise(t, s); }));
+}
+
 dc_status dc_orthogonalize_workspace_size(const dc_matrix* mats, int count, size_t* bytes) {
   if (count < 0 || (count && !mats) || !bytes) return DC_ERR_INVALID_ARG;
   for (int i = 0; i < count; ++i) {

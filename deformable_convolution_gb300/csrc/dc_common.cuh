@@ -310,6 +310,7 @@ unsigned int cl3_read_error(int clear);
 unsigned int tf32_read_error(int clear);
 unsigned int fp8_read_error(int clear);
 unsigned int muon_read_error(int clear);
+unsigned int pointwise_read_error(int clear);
 // Backward of the offset convolution on the channels-last path (one offset
 // group, K <= 9 taps): the input part adds into the NHWC grad_x buffer's
 // values and writes grad_x (NCHW) whole; the weight part writes per-chunk

@@ -28,6 +28,14 @@ struct Fp8Product {
   void* d;
   void* ws;
 };
+struct Fp8Pointwise {
+  dc_fp8_layer p;
+  const void* x;
+  const void* w_codes;
+  const void* w_scales;
+  void* y;
+};
+cudaError_t launch_fp8_pointwise(const Fp8Pointwise& t, cudaStream_t s);
 size_t fp8_matmul_workspace_bytes(const dc_fp8_product& p);
 cudaError_t launch_fp8_matmul(const Fp8Product& a, cudaStream_t s);
 

@@ -1343,8 +1343,8 @@ extern "C" dc_status dc_selftest_wait_timeout(unsigned int spins, void* stream) 
 // Reads (and optionally clears) the flag bounded device waits raise on expiry.
 // The channels-last kernels, the float32 tensor-core GEMMs, the 8-bit products
 // and Muon's keep their own flags (cl_read_error, cl3_read_error,
-// k4cl_read_error, tf32_read_error, fp8_read_error, muon_read_error: 2 =
-// unreadable).
+// k4cl_read_error, tf32_read_error, fp8_read_error, pointwise_read_error,
+// muon_read_error: 2 = unreadable).
 extern "C" dc_status dc_device_error(int clear) {
   unsigned int v = 0;
   if (cudaMemcpyFromSymbol(&v, dc::g_dc_device_error, sizeof(v)) != cudaSuccess) return DC_ERR_CUDA;
@@ -1359,6 +1359,7 @@ extern "C" dc_status dc_device_error(int clear) {
   const unsigned int t = dc::tf32_read_error(clear);
   const unsigned int q = dc::fp8_read_error(clear);
   const unsigned int m = dc::muon_read_error(clear);
-  if (c == 2u || c3 == 2u || c4 == 2u || t == 2u || q == 2u || m == 2u) return DC_ERR_CUDA;
-  return (v || c || c3 || c4 || t || q || m) ? DC_ERR_TIMEOUT : DC_OK;
+  const unsigned int w = dc::pointwise_read_error(clear);
+  if (c == 2u || c3 == 2u || c4 == 2u || t == 2u || q == 2u || m == 2u || w == 2u) return DC_ERR_CUDA;
+  return (v || c || c3 || c4 || t || q || m || w) ? DC_ERR_TIMEOUT : DC_OK;
 }

@@ -43,7 +43,8 @@ class Pointwise:
 
     ``load`` quantises the weight (E4M3, a scale for each 128 x 128 block),
     ``forward`` the input (E4M3, a scale for each 128 channels of a pixel, and,
-    ``training``, each 128 pixels of a channel for the weight's gradient),
+    ``training``, each 128 pixels of a channel for the weight's gradient; else,
+    in bf16 and up to 256 output channels, on its way into the product),
     ``backward`` the gradient of y (``grad_format``, in ``grad_dtype``) likewise.
     Products are exact and summed in float32.
 
@@ -65,7 +66,13 @@ class Pointwise:
             return B.Fp8Problem(batch, pixels, c, kind, fmt) if last else B.Fp8Problem(batch, c, pixels, kind, fmt)
         # codes by channel (runs of channels) and by pixel: direct and transposed, or the other way round
         self.weight = Quantized(B.Fp8Problem(1, c_out, c_in, dtype, B.DC_E4M3, 1), True, training, device)
-        self.x = Quantized(maps(c_in, dtype, B.DC_E4M3), last or training, not last or training, device)
+        # without a backward pass the input's codes need not be kept: one launch where it takes all output channels
+        self._one = None
+        if not training and dtype == B.DC_BF16 and c_out <= 256:
+            self._one = B.DcFp8Layer(n, h * w, c_in, c_out, layout)
+        kept = self._one is None
+        self.x = Quantized(maps(c_in, dtype, B.DC_E4M3), kept and (last or training), kept and (not last or training),
+                           device)
         e, g = B.DC_E4M3, grad_format
         # products over channels: pixels are the rows of D (channels last) or its columns
         self._fwd = q(batch, pixels, c_out, c_in, b_shared=1, out=dtype) if last else \
@@ -85,6 +92,7 @@ class Pointwise:
 
         def addresses(*tensors):
             return tuple(None if t is None else t.data_ptr() for t in tensors)
+        self._w = addresses(w.codes, w.scales)
         self._x_to = addresses(x.codes, x.scales, x.codes_t, x.scales_t)
         self._fwd_from = addresses(x.codes, x.scales, w.codes, w.scales) if last else \
             addresses(w.codes, w.scales, x.codes_t, x.scales_t)
@@ -110,6 +118,11 @@ class Pointwise:
         y = torch.empty(self.y_shape, dtype=self.dtype, device=x.device) if y is None else y
         y_ptr = B._arg(y, "y", self.y_shape, self.dtype)
         s = B._raw_stream(stream)
+        if self._one is not None:
+            status = self._lib.dc_fp8_pointwise(self._one, x_ptr, *self._w, y_ptr, s)
+            if status:
+                raise B.DcError(status, "dc_fp8_pointwise")
+            return y
         self._run(self.x.p, x_ptr, self._x_to, s)
         self._product(self._fwd, self._fwd_from, y_ptr, s)
         return y

@@ -532,6 +532,24 @@ dc_status dc_fp8_matmul(const dc_fp8_product* prob, const void* a, const void* a
                         const void* b, const void* b_scales, void* d, void* ws, size_t ws_bytes,
                         void* stream);
 
+/* The forward pass of a pointwise layer in one launch: y = W x over the channels
+ * of every pixel, x in E4M3 codes with a scale for each 128 channels of a pixel
+ * that are made on the way.  Bit for bit what dc_fp8_quantize and
+ * dc_fp8_matmul give.
+ *   x, y   bf16, [n][channels][pixels] (DC_NCHW) or [n][pixels][channels]
+ *   w      codes and scales of W [c_out][c_in] in E4M3 (a dc_fp8_quantize of one
+ *          matrix, square or not)
+ * Errors: DC_ERR_INVALID_ARG for NULL, a size below 1 (n: below 0) or an
+ * unknown layout; DC_ERR_UNSUPPORTED for c_out over 256 (x would be read more
+ * than once), c_in over 2^20, n * pixels over 2^30, or w not 16-byte aligned (x,
+ * y: not aligned to their elements). */
+typedef struct {
+  int n, pixels, c_in, c_out; /* n may be 0 */
+  dc_layout layout;
+} dc_fp8_layer;
+dc_status dc_fp8_pointwise(const dc_fp8_layer* prob, const void* x, const void* w_codes,
+                           const void* w_scales, void* y, void* stream);
+
 /* Orthogonalisation by Newton-Schulz products: the singular values of a matrix
  * are driven towards 1 (into about 0.7 .. 1.2), its singular vectors kept.
  *   X = G / (|G| + 1e-7)      |G|: Frobenius norm

@@ -88,6 +88,24 @@ def test_matmul_checks_its_workspace():
         assert product_status(**kw) == WORKSPACE
 
 
+def pointwise_status(x=0x1000, w=0x2000, sw=0x3000, y=0x4000, **kw):
+    d = dict(n=1, pixels=8, c_in=8, c_out=8, layout=B.DC_NCHW)
+    d.update(kw)
+    return B.lib().dc_fp8_pointwise(ctypes.byref(B.DcFp8Layer(**d)), x, w, sw, y, None)
+
+
+@pytest.mark.parametrize("kw,status", [
+    (dict(n=-1), INVALID), (dict(pixels=0), INVALID), (dict(c_in=0), INVALID), (dict(c_out=-1), INVALID),
+    (dict(layout=2), INVALID), (dict(x=None), INVALID), (dict(w=None), INVALID), (dict(sw=None), INVALID),
+    (dict(y=None), INVALID), (dict(c_out=257), UNSUPPORTED), (dict(c_in=(1 << 20) + 1), UNSUPPORTED),
+    (dict(n=1 << 20, pixels=2048), UNSUPPORTED), (dict(x=0x1001), UNSUPPORTED), (dict(w=0x2008), UNSUPPORTED),
+    (dict(sw=0x3004), UNSUPPORTED), (dict(y=0x4001), UNSUPPORTED), (dict(n=0, x=None), B.DC_OK),
+])
+def test_pointwise_checks_its_arguments(kw, status):
+    assert pointwise_status(**kw) == status
+    assert B.lib().dc_fp8_pointwise(None, 0x1000, 0x2000, 0x3000, 0x4000, None) == INVALID
+
+
 def test_layer_checks_its_arguments():
     with pytest.raises(B.DcError):
         fp8.Pointwise(1, 0, 4, 4, 4, device="cpu")
@@ -354,6 +372,57 @@ def check_layer(n, ci, co, h, w, dtype, layout, grad_dtype, fmt, seed=0):
 @pytest.mark.parametrize("size", [(1, 16, 16, 1, 1), (2, 200, 72, 5, 31), (3, 64, 256, 12, 12), (1, 130, 8, 40, 40)])
 def test_layer(size, kinds, layout, fmt):
     check_layer(*size, kinds[0], layout, kinds[1], fmt)
+
+
+@on_gpu
+@pytest.mark.parametrize("layout", (B.DC_NCHW, B.DC_NHWC))
+@pytest.mark.parametrize("size", [(1, 8, 1, 1), (3, 24, 24, 130), (2, 700, 200, 257), (1, 129, 193, 4000), (8, 256, 256, 3136),
+                                  (40, 64, 256, 1000), (5, 72, 40, 1247), (2, 1024, 31, 128), (1, 300, 225, 40000)])
+def test_one_launch_gives_what_two_give(size, layout):
+    """The forward that quantises on the way against codes and product apart, bit
+    for bit, with guards around y and a block that is not finite."""
+    n, ci, co, pixels = size
+    last = layout == B.DC_NHWC
+    x = values((n, pixels, ci) if last else (n, ci, pixels), B.DC_BF16, 7, spread=1.0)
+    if pixels > 100:
+        x[0, 70 if last else 5, 5 if last else 70] = float("nan")
+    x = x.cuda()
+    gen = torch.Generator().manual_seed(2)
+    w = fp8.Quantized(B.Fp8Problem(1, co, ci, B.DC_F32, B.DC_E4M3, 1))
+    w.load((torch.randn(co, ci, generator=gen) * ci ** -0.5).cuda())
+    q = fp8.Quantized(B.Fp8Problem(n, *x.shape[1:], B.DC_BF16), last, not last)
+    q.load(x)
+    if last:
+        p = B.Fp8Product(n, pixels, co, ci, b_shared=1)
+        args = q.codes, q.scales, w.codes, w.scales
+    else:
+        p = B.Fp8Product(n, co, pixels, ci, a_shared=1)
+        args = w.codes, w.scales, q.codes_t, q.scales_t
+    want = torch.empty(p.shape, dtype=BF16, device="cuda")
+    ws = torch.empty(max(1, B.dc_fp8_matmul_workspace_size(p)), dtype=torch.uint8, device="cuda")
+    B.dc_fp8_matmul(p, *args, want, ws)
+    for skip in (16, 1):  # y on a vector's boundary, and off it
+        room = torch.full((want.numel() + 64,), 7.0, dtype=BF16, device="cuda")
+        y = room[skip:skip + want.numel()].view(p.shape)
+        B.dc_fp8_pointwise(B.DcFp8Layer(n, pixels, ci, co, layout), x, w.codes, w.scales, y)
+        assert torch.equal(torch.nan_to_num(y, nan=-1e30), torch.nan_to_num(want, nan=-1e30))
+        assert torch.isnan(want).any() or pixels <= 100
+        assert (room[:skip] == 7).all() and (room[skip + want.numel():] == 7).all()
+
+
+@on_gpu
+def test_one_launch_reads_x_off_a_vector():
+    flat = values((1, 1, 72 * 131 + 8), B.DC_BF16, 4, spread=1.0).flatten().cuda()
+    w = fp8.Quantized(B.Fp8Problem(1, 40, 72, B.DC_F32, B.DC_E4M3, 1))
+    w.load(torch.ones(40, 72, device="cuda"))
+    for layout in (B.DC_NCHW, B.DC_NHWC):
+        shape = (1, 131, 72) if layout == B.DC_NHWC else (1, 72, 131)
+        got = []
+        for x in (flat[1:1 + 72 * 131].view(shape), flat[1:1 + 72 * 131].clone().view(shape)):
+            y = torch.empty((1, 131, 40) if layout == B.DC_NHWC else (1, 40, 131), dtype=BF16, device="cuda")
+            B.dc_fp8_pointwise(B.DcFp8Layer(1, 131, 72, 40, layout), x, w.codes, w.scales, y)
+            got.append(y)
+        assert torch.equal(*got)
 
 
 @on_gpu

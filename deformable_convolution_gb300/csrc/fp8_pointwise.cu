@@ -5,8 +5,10 @@
 // for bit, without the codes' way to memory and back: 1 + 1 of 2 + 1 + 1 + 2
 // bytes a value of x and y at c_in = c_out.  A tile is 128 pixels by all output
 // channels (at most 256, so that x is read once).  What bounds it is memory:
-// 16 x 100 x 168 pixels of 256 -> 256 channels, 275 MB, in place of a quantiser
-// (35 us) and a product (35 us).
+// channels last, 16 x 100 x 168 pixels of 256 -> 256 channels, 275 MB, take 57 us
+// (71 % of the copy bandwidth) in place of a quantiser's and a product's 75.
+// Channels first the codes are transposed on the way and y leaves in lines of 64
+// bytes: 92 us (the two launches: 80).
 //
 // Warps: 0-7 and 8-15 take every other block of 128 channels of the tile's x
 // into registers and write its codes where the tensor cores read them (the
@@ -92,6 +94,17 @@ __device__ __forceinline__ bool group_all(int group, bool ok) {
       : "r"((int)ok), "r"(1 + group)
       : "memory");
   return r != 0;
+}
+
+// A thread's eight values turned so that the k-th comes first.
+__device__ __forceinline__ void turn(Eight<__nv_bfloat16>& x, int k) {
+  uint32_t a[4], b[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) a[i] = k & 2 ? x.w[(i + 1) & 3] : x.w[i];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) b[i] = k & 4 ? a[(i + 2) & 3] : a[i];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) x.w[i] = k & 1 ? __funnelshift_r(b[i], b[(i + 1) & 3], 16) : b[i];
 }
 
 // LAST: x [pixel][channel], else [channel][pixel] of each image.
@@ -221,14 +234,17 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (free) sb[gt] = (unsigned char)byte;
           }
           group_meets(group);
+          // lanes start at pixels of their own, so that two of them and not 16 write to a bank
+#pragma unroll
+          for (int r = 0; r < 8; ++r) turn(v[r], l & 7);
 #pragma unroll
           for (int i = 0; i < 8; ++i) {
-            const int row = 8 * l + i;  // the pixel; its channels 8 h ..
+            const int in = (i + l) & 7, row = 8 * l + in;  // the pixel; its channels 8 h ..
             const float f = inverse[row];
             uint2 c;
             c.x = codes2<DC_E4M3>(v[0].get(i) * f, v[1].get(i) * f) | (codes2<DC_E4M3>(v[2].get(i) * f, v[3].get(i) * f) << 16);
             c.y = codes2<DC_E4M3>(v[4].get(i) * f, v[5].get(i) * f) | (codes2<DC_E4M3>(v[6].get(i) * f, v[7].get(i) * f) << 16);
-            if (free) *reinterpret_cast<uint2*>(codes + row * 128 + (((h >> 1) ^ i) << 4) + (h & 1) * 8) = c;
+            if (free) *reinterpret_cast<uint2*>(codes + row * 128 + (((h >> 1) ^ in) << 4) + (h & 1) * 8) = c;
           }
         }
         advance(2);

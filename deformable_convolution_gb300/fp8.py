@@ -44,7 +44,7 @@ class Pointwise:
     ``load`` quantises the weight (E4M3, a scale for each 128 x 128 block),
     ``forward`` the input (E4M3, a scale for each 128 channels of a pixel, and,
     ``training``, each 128 pixels of a channel for the weight's gradient; else,
-    in bf16 and up to 256 output channels, on its way into the product),
+    where one launch is faster, on its way into the product),
     ``backward`` the gradient of y (``grad_format``, in ``grad_dtype``) likewise.
     Products are exact and summed in float32.
 
@@ -66,9 +66,12 @@ class Pointwise:
             return B.Fp8Problem(batch, pixels, c, kind, fmt) if last else B.Fp8Problem(batch, c, pixels, kind, fmt)
         # codes by channel (runs of channels) and by pixel: direct and transposed, or the other way round
         self.weight = Quantized(B.Fp8Problem(1, c_out, c_in, dtype, B.DC_E4M3, 1), True, training, device)
-        # without a backward pass the input's codes need not be kept: one launch where it takes all output channels
+        # Without a backward pass the input's codes need not be kept, and one launch is faster (in us, one against
+        # two): channels last 16 x 100 x 168, 256 -> 256: 57, 75; 4 x 112 x 112, 128 -> 64: 7.8, 10.1; channels first
+        # the latter 10.0, 13.0.  Not where rows of y are no whole 16-byte pieces (9 x 22 x 4, 144 -> 71: 13.7, 7.1),
+        # and channels first not for many output channels (8 x 56 x 56, 256 -> 256: 16.4, 11.3).
         self._one = None
-        if not training and dtype == B.DC_BF16 and c_out <= 256:
+        if not training and dtype == B.DC_BF16 and (c_out <= 256 and c_out % 8 == 0 if last else c_out <= 128):
             self._one = B.DcFp8Layer(n, h * w, c_in, c_out, layout)
         kept = self._one is None
         self.x = Quantized(maps(c_in, dtype, B.DC_E4M3), kept and (last or training), kept and (not last or training),

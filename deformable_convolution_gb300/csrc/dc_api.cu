@@ -1020,6 +1020,12 @@ dc_status check_product(const dc_fp8_product* p) {
     if (flag != 0 && flag != 1) return DC_ERR_INVALID_ARG;
   if (p->m > kFp8MaxSide || p->n > kFp8MaxSide || p->k > kFp8MaxSide || p->batch > kFp8MaxBatch)
     return DC_ERR_UNSUPPORTED;
+  // strides and counts of tiles and of blocks of k that the product's kernel holds
+  const long long most = 1LL << 38, batch = p->batch ? p->batch : 1;
+  if ((long long)p->m * p->k > most || (long long)p->n * p->k > most || (long long)p->m * p->n > (1LL << 37) ||
+      batch * ceil_div_ll(p->m, 256) * ceil_div_ll(p->n, 128) > INT_MAX ||
+      batch * ceil_div_ll(p->k, DC_FP8_BLOCK) > INT_MAX)
+    return DC_ERR_UNSUPPORTED;
   return DC_OK;
 }
 

@@ -22,12 +22,16 @@ __device__ __forceinline__ float block_sum(float v) {
 }
 
 __global__ void __launch_bounds__(kThreads) muon_squares(const __grid_constant__ MuonGroup g) {
-  // beside the launch of the small matrices, which waited for what came before
+  // Beside the launch of the small matrices, which waited for what came before:
+  // it is waited for only before this grid ends, so that what follows finds both done.
   if (!g.beside) pdl_wait();
   pdl_release();
   const MuonMat& t = g.mat[blockIdx.y];
   float scale;
-  if (skipped(g, &scale) || blockIdx.x >= t.parts) return;
+  if (skipped(g, &scale) || blockIdx.x >= t.parts) {
+    if (g.beside) pdl_wait();
+    return;
+  }
   const long long count = (long long)t.rows * t.cols, step = (long long)t.parts * kThreads;
   float sum = 0.f;
   // eight values a thread where the arrays allow it (the order of a matrix's sum
@@ -61,6 +65,7 @@ __global__ void __launch_bounds__(kThreads) muon_squares(const __grid_constant__
   }
   sum = block_sum(sum);
   if (threadIdx.x == 0) t.part[blockIdx.x] = sum;
+  if (g.beside) pdl_wait();
 }
 
 __global__ void __launch_bounds__(kThreads) muon_begin(const __grid_constant__ MuonGroup g) {

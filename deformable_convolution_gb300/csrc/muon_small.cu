@@ -232,16 +232,25 @@ __global__ void __launch_bounds__(kThreads, 1) muon_small(const __grid_constant_
     const int tasks = blocks * blocks * L.ks, depth = L.nc / 16;
     for (int q = warp; q < tasks; q += kWarps) {
       const int k = q / (blocks * blocks), un = q - k * blocks * blocks, bi = un / blocks, bj = un - bi * blocks;
-      float acc[2][4] = {}, cross[2][4] = {};
+      // every 16 columns' sums added up by float32 additions: an accumulator that is
+      // truncated after each product loses half a unit in the last place each time
+      float total[2][4] = {};
       const uint32_t a = base + L.x + 2u * ((16 * bi + a_row) * L.xs + a_col);
       const uint32_t b = base + L.x + 2u * ((16 * bj + b_row) * L.xs + b_col);
-      for (int c = k; c < depth; c += L.ks) unit16(acc, cross, a + 32 * c, xlow, b + 32 * c, xlow);
+      for (int c = k; c < depth; c += L.ks) {
+        float acc[2][4] = {}, cross[2][4] = {};
+        unit16(acc, cross, a + 32 * c, xlow, b + 32 * c, xlow);
+#pragma unroll
+        for (int n = 0; n < 2; ++n)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) total[n][e] += acc[n][e] + cross[n][e];
+      }
 #pragma unroll
       for (int n = 0; n < 2; ++n)
 #pragma unroll
         for (int e = 0; e < 4; ++e)
           part[(k * L.sp + 16 * bi + acc_row + 8 * (e >> 1)) * (L.sp + 4) + 16 * bj + 8 * n + acc_col + (e & 1)] =
-              acc[n][e] + cross[n][e];
+              total[n][e];
     }
     cluster_sync();
     // this CTA's rows of the sum, handed to all

@@ -107,6 +107,7 @@ class Pointwise:
             self._gw_from = addresses(g.codes_t, g.scales_t, x.codes_t, x.scales_t) if last else \
                 addresses(g.codes, g.scales, x.codes, x.scales)
         self._ws_args = self._ws.data_ptr(), self._ws.numel()
+        self._loaded = self._kept = False
 
     def load(self, w, stream=None):
         """The weight [c_out, c_in] (or [c_out, c_in, 1, 1]), for the calls that follow."""
@@ -114,9 +115,12 @@ class Pointwise:
         if tuple(w.shape) not in (self.w_shape, self.w_shape + (1, 1)):  # (a 1 x 1 convolution's)
             raise ValueError(f"w: expected shape {self.w_shape}, got {tuple(w.shape)}")
         self.weight.load(w, stream)
+        self._loaded = True
 
     def forward(self, x, y=None, stream=None):
         """y (a new tensor if not given) = W x."""
+        if not self._loaded:
+            raise ValueError("the layer has no weight yet (load)")
         x_ptr = B._arg(x, "x", self.x_shape, self.dtype)
         y = torch.empty(self.y_shape, dtype=self.dtype, device=x.device) if y is None else y
         y_ptr = B._arg(y, "y", self.y_shape, self.dtype)
@@ -128,6 +132,7 @@ class Pointwise:
             return y
         self._run(self.x.p, x_ptr, self._x_to, s)
         self._product(self._fwd, self._fwd_from, y_ptr, s)
+        self._kept = True
         return y
 
     def backward(self, grad_y, grad_x=None, grad_w=None, stream=None):
@@ -135,6 +140,8 @@ class Pointwise:
         ``dtype`` and float32, new tensors if not given."""
         if not self.training:
             raise ValueError("a layer made with training=False keeps nothing for a backward pass")
+        if not self._kept:
+            raise ValueError("no forward pass before the backward pass")
         g_ptr = B._arg(grad_y, "grad_y", self.y_shape, self.grad_dtype)
         if grad_x is None:
             grad_x = torch.empty(self.x_shape, dtype=self.dtype, device=grad_y.device)

@@ -88,8 +88,10 @@ class Trainer:
                     e["master"] = q[k].float()
                 (matrices if optimizer == "muon" and k in weights else entries).append(e)
         self.opt = optim.AdamW(entries, lr=lr, betas=betas, state_bits=state_bits, min_8bit=4096)
-        self.muon = optim.Muon(matrices, lr=lr) if matrices else None
-        self._norm = optim.GradNorm([e["grad"] for e in entries + matrices])
+        self.muon, self._norm = None, self.opt.grad_norm
+        if matrices:  # one norm over both optimisers' gradients
+            self.muon = optim.Muon(matrices, lr=lr)
+            self._norm = optim.GradNorm([e["grad"] for e in entries + matrices])
         self.grad_norm, self.clip = empty(1), empty(1)
 
     def forward(self, x0):

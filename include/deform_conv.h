@@ -519,8 +519,9 @@ dc_status dc_fp8_values(const dc_fp8_problem* prob, int transposed, const void* 
  * may be 0: nothing is written for batch 0 without sum, else zeros.
  * Errors: DC_ERR_INVALID_ARG for a bad problem or a NULL required pointer,
  * DC_ERR_UNSUPPORTED for a pointer that is not 16-byte aligned (d: not aligned
- * to its element), m, n or k over 2^24 or a batch over 65535, DC_ERR_WORKSPACE
- * for a short workspace. */
+ * to its element), m, n or k over 2^24, a batch over 65535, a factor over 2^38
+ * values, D over 2^37 or more than 2^31 - 1 tiles of 256 x 128 or blocks of k in
+ * all, DC_ERR_WORKSPACE for a short workspace. */
 typedef struct {
   int batch, m, n, k;
   dc_fp8 a_format, b_format;
@@ -561,12 +562,15 @@ typedef enum { DC_ORTHO_16 = 0, DC_ORTHO_32 = 1 } dc_ortho_precision;
 /* Between the products X, A and the polynomial of A are held as pairs of
  * 16-bit floats (as good as float32; fixed point below 2^-36), their diagonals
  * in float32.  DC_ORTHO_32 multiplies both parts of every factor: the result is
- * as good as float32 arithmetic's.  DC_ORTHO_16 multiplies the high parts alone
+ * about as good as float32 arithmetic's (the tensor cores truncate their sums
+ * after 16 products each, which a long side of many thousands adds up).
+ * DC_ORTHO_16 multiplies the high parts alone
  * (relative error about 1e-3, below a rounding to bf16), but both where the
  * shorter side is under 64.  Sums are float32, in a fixed order: the same
  * matrix gives the same bits, whatever matrices are beside it. */
 
-/* One matrix: in, out [rows][cols] dense; out may be in where the types agree. */
+/* One matrix: in, out [rows][cols] dense; out may be in where the types agree,
+ * else no matrix may overlap another. */
 typedef struct {
   const void* in;
   void* out;

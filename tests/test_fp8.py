@@ -72,6 +72,9 @@ def product_status(a=0x1000, sa=0x2000, b=0x3000, sb=0x4000, d=0x5000, ws=None, 
     (dict(a_format=2), INVALID), (dict(b_format=-1), INVALID), (dict(a_shared=2), INVALID), (dict(sum=-1), INVALID),
     (dict(out=2), INVALID), (dict(a=None), INVALID), (dict(sb=None), INVALID), (dict(d=None), INVALID),
     (dict(m=(1 << 24) + 1), UNSUPPORTED), (dict(batch=65536), UNSUPPORTED), (dict(a=0x1008), UNSUPPORTED),
+    (dict(m=1 << 20, k=1 << 19), UNSUPPORTED), (dict(n=1 << 24, k=1 << 15), UNSUPPORTED),
+    (dict(m=1 << 20, n=1 << 18), UNSUPPORTED), (dict(batch=60000, m=1 << 18, n=8192), UNSUPPORTED),
+    (dict(batch=60000, k=1 << 23, sum=1), UNSUPPORTED),
     (dict(sa=0x2004), UNSUPPORTED), (dict(d=0x5002), UNSUPPORTED), (dict(d=0x5001, out=B.DC_BF16), UNSUPPORTED),
     (dict(ws=0x6008), UNSUPPORTED), (dict(batch=0), B.DC_OK),
 ])
@@ -113,7 +116,12 @@ def test_layer_checks_its_arguments():
     with pytest.raises(ValueError):
         layer.backward(torch.zeros(1, 4, 4, 4))
     with pytest.raises(ValueError):
-        layer.forward(torch.zeros(1, 8, 4, 4))
+        layer.forward(torch.zeros(1, 8, 4, 4))  # no weight yet
+    layer = fp8.Pointwise(1, 8, 4, 4, 4, device="cpu")
+    with pytest.raises(ValueError):
+        layer.backward(torch.zeros(1, 4, 4, 4))  # no forward yet
+    with pytest.raises(ValueError):
+        layer.load(torch.zeros(8, 4))
 
 
 # ---------------------------------------------------------------- codes

@@ -134,6 +134,42 @@ def test_orthogonalize(size, kind):
 
 
 @on_gpu
+@pytest.mark.parametrize("size", [(8, 40000), (40000, 5), (64, 5000), (33, 9000), (65, 64), (64, 65), (1100, 1030), (1030, 1100),
+                                  (2048, 2304), (2100, 2049)])
+def test_orthogonalize_at_the_paths_borders(size):
+    """Short sides whose long ones fit a cluster or not, several rows of tiles,
+    tiles of every width: as above, the 64-bit form computed on the GPU."""
+    g = matrix(*size, "full", sum(size))
+
+    def plain(dtype):
+        a, b, c = P.NS
+        x = g.cuda().to(dtype)
+        x = x / (x.square().sum().sqrt() + 1e-7)
+        x = x.T if size[0] > size[1] else x
+        for _ in range(5):
+            p = x @ x.T
+            x = a * x + (b * p + c * (p @ p)) @ x
+        return (x.T if size[0] > size[1] else x).cpu()
+    want = plain(torch.float64)
+    e32 = off(plain(F32), want)
+    x = g.cuda()
+    outs = {b: torch.full_like(x, 5.0) for b in (16, 32)}
+    for b in (16, 32):
+        optim.Orthogonalize([x], [outs[b]], precision=b)()
+    # an accumulator of A is truncated after every 16 products, after a split's 64 at most (or, with 1024 values a side
+    # and more, after all): half a unit in the last place of the sum each time on the diagonal, twice that of X
+    # by the steps' slopes
+    long = max(size) / 16
+    truncated = 2 * (long if min(size) > 512 else min(long, 64 * max(1, long / 64 / 48))) * 2.0 ** -25
+    assert off(outs[32], want) <= 4 * e32 + 2e-6 + truncated
+    assert off(outs[16], want) <= 4.2e-3
+    # beside others of its kind and of the small ones' the same bits
+    y, more = torch.empty_like(x), [torch.randn(s, device="cuda") for s in ((18, 200), (300, 300), (130, 700))]
+    optim.Orthogonalize(more + [x], [torch.empty_like(t) for t in more] + [y], precision=32)()
+    assert torch.equal(y, outs[32])
+
+
+@on_gpu
 @pytest.mark.parametrize("kinds", [(F32, BF16), (BF16, F32), (BF16, BF16)])
 def test_types_and_in_place(kinds):
     g = matrix(96, 200, "full", 1).to(kinds[0])
@@ -218,7 +254,7 @@ def weights(kind, grad, shapes, seed):
     return params
 
 
-SHAPES = [(16, 8, 3, 3), (18, 72), (130, 40), (1, 5), (64, 64, 1, 1)]
+SHAPES = [(16, 8, 3, 3), (18, 72), (130, 40), (1, 5), (64, 64, 1, 1), (80, 70), (72, 16, 3, 3), (200, 131)]
 
 
 @on_gpu

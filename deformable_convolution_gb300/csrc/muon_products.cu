@@ -12,12 +12,14 @@
 // small where the rows come close to being orthogonal.  DC_ORTHO_16 multiplies
 // the high parts (11 bits): relative error 1e-3 or less for gradients and
 // random matrices from 64 x 64 to 1024 x 1024, against 2e-3 .. 4e-3 with the
-// diagonal left in.  DC_ORTHO_32 (and a side under 64) adds high low + low high on the same tiles (low low is
-// below the last bit kept), in an accumulator of their own: these terms are
-// 2^-11 of the others, and an accumulator that the tensor cores truncate after
-// every product is truncated a third as often (relative error against 64 bits:
-// 256 x 2304 9e-7, 600 x 1000 4e-6, 2048 x 2304 9e-6; float32 arithmetic's 2e-6,
-// 3e-6, 4e-6).
+// diagonal left in.  DC_ORTHO_32 (and a side under 64) adds high low + low high
+// (low low is below the last bit kept).  The tensor cores truncate their sums
+// after each product of 16, so these small terms of a block come first, and an
+// accumulator runs over kRun blocks, whose sums are added up in registers:
+// relative error against 64 bits 2.6e-6 for 600 x 1000 and 2048 x 2048, 3.3e-6
+// for 700 x 70000, 1e-6 for 256 x 2304 (float32 arithmetic: 3.1e-6, 3.6e-6,
+// 1.4e-5, 2e-6).  Four of 2048 x 2048 take 1538 us so; runs of 16 blocks 1394 us
+// and 5.4e-6, a tile in one run 1289 us and 1.1e-5.
 //
 // CTAs work in pairs on tiles of 256 x bn (tc_pair.cuh).  A and P are
 // symmetric: of their tiles only those that reach below the diagonal are
@@ -55,6 +57,7 @@ constexpr int kPart = 2 * kBox;           // one part of a factor in a stage: 12
 constexpr int kStage = 2 * kPart;         // one part of both factors
 constexpr int kStages = 5, kRing = kStages * kStage;
 constexpr int kSumCols = 16;              // columns of a tile that a sum adds up
+constexpr int kRun = 8;                   // blocks of 64 that an accumulator with low parts' terms runs over
 constexpr int kBuf = 4096;                // a warp's 32 x 32 results, and as much for their own terms
 constexpr size_t kSmem = 1024 + kRing + kEpiWarps * 2 * kBuf + 256;
 static_assert(kSmem <= 227 * 1024, "shared memory");
@@ -291,7 +294,43 @@ __device__ __forceinline__ void write_result(const Items<CAP>& g, const Item& t,
   }
 }
 
-template <int CAP>
+// A result warp's columns (32 each of `chunks`) of a tile of several runs, added
+// up in registers and put back in place of the last run's.  j: as in the kernel,
+// of the first run (whose sums are there); returns the last one's, or -1 where a
+// wait expired.  (Not inline: its registers would be taken from the rest.)
+__device__ __noinline__ int add_runs(uint32_t acc, int chunks, int runs, int j, uint64_t* tfull, uint32_t drained) {
+  float total[4][32];
+#pragma unroll 1
+  for (int u = 0;; ++u, ++j) {
+    if (u) {
+      if (!epi_all(warp_wait(&tfull[j & 1], (j >> 1) & 1, &g_muon_error))) return -1;
+      tc_after();
+    }
+    const uint32_t from = acc + (j & 1) * 256;
+    const bool last = u + 1 == runs;
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {
+      if (c < chunks) {
+        uint32_t r[32];
+        tmem_ld32(from + c * 32, r);
+        tmem_ld_wait();
+#pragma unroll
+        for (int v = 0; v < 32; ++v) total[c][v] = (u ? total[c][v] : 0.f) + __uint_as_float(r[v]);
+        if (last) tmem_st32(from + c * 32, total[c]);
+      }
+    }
+    if (last) break;
+    tc_before();
+    __syncwarp();
+    if ((threadIdx.x & 31) == 0) arrive_at(drained + 8 * (j & 1));
+  }
+  tmem_st_wait();
+  return j;
+}
+
+// PAIRS: some of the matrices have their low parts multiplied, RUNS: some of
+// their tiles have more than one run.
+template <int CAP, bool PAIRS, bool RUNS>
 __global__ void __launch_bounds__(kThreads, 1) muon_steps(const __grid_constant__ Items<CAP> g) {
   extern __shared__ unsigned char smem_raw[];
   unsigned char* smem = px::align1024(smem_raw);
@@ -329,11 +368,9 @@ __global__ void __launch_bounds__(kThreads, 1) muon_steps(const __grid_constant_
   const uint32_t tmem = *holder;
   bool ok = true;
 
-  // A tile's accumulators: two of them by turns, or, where 256 columns hold
-  // high high and 256 the cross terms, one.  j: this pair's tiles so far; uses
-  // of the buffers are counted apart, since widths may change from tile to tile:
-  // every tile waits for the tile before last to be read, a wide one with cross
-  // terms, or one after such a tile, for the last one.
+  // Accumulators are two, by turns, one for a run: a tile or, where low parts are
+  // multiplied, kRun blocks of it, added up in the result warps' registers.  j:
+  // this pair's runs so far; each waits for the run before last to be read.
   if (warp == kWarpTma) {
     const bool issuer = elect_one();
     // both CTAs' copies count on the first one's barrier
@@ -359,7 +396,7 @@ __global__ void __launch_bounds__(kThreads, 1) muon_steps(const __grid_constant_
       // boxes of B: none where its rows are A's
       const int nb = q.diagonal ? 0 : q.bn == 256 ? 2 : 1;
       const uint32_t bytes = 2u * (uint32_t)(2 + nb) * kBox;
-      const int parts = 1 + q.t->pairs;
+      const int parts = PAIRS ? 1 + q.t->pairs : 1;
       for (int kb = q.begin; kb < q.end && ok; ++kb) {
         // the high parts in one stage, the low ones in the next
         for (int p = 0; p < parts; ++p) {
@@ -388,28 +425,28 @@ __global__ void __launch_bounds__(kThreads, 1) muon_steps(const __grid_constant_
       // along lines a step of 16 elements is 32 bytes on, across them 16 lines on
       const uint64_t along = sdesc(smem_u32(smem), 16, 1024), across = sdesc(smem_u32(smem), kBox, 1024);
       int s = 0, round = 0, j = 0;
-      bool alone = false;  // the last tile took all columns
       for (int w = first; w < work && ok; w += stride) {
         const Tile q = tile_of(g, w);
         if (q.which == SUM) continue;
         const bool a_mn = q.which == GRAM && q.t->m.tall;
         const bool b_mn = (q.which == GRAM && q.t->m.tall) || (q.which == APPLY && !q.t->m.tall);
-        const int pairs = q.t->pairs;
-        const bool whole = pairs && q.bn == 256;
-        // (tiles are read in turn: the last one's reading follows the one's before it)
-        const int before = j - (whole || alone ? 1 : 2);
-        alone = whole;
-        if (before >= 0 && !warp_wait(&drained[before & 1], (before >> 1) & 1, &g_muon_error)) {
-          ok = false;
-          break;
-        }
-        const uint32_t acc = tmem + (whole ? 0 : (j & 1) * 256), cross = acc + q.bn;
+        const bool pairs = PAIRS && q.t->pairs;
+        const int run = RUNS && pairs ? kRun - 1 : INT_MAX;
+        uint32_t acc = tmem;
         const uint32_t idesc = (1u << 4) | ((uint32_t)a_mn << 15) | ((uint32_t)b_mn << 16) |
                                ((uint32_t)(q.bn >> 3) << 17) | ((256u >> 4) << 24);
         const uint64_t a0 = a_mn ? across : along;
         const uint64_t b0 = (b_mn ? across : along) + (q.diagonal ? 0 : kPart >> 4);
         const uint32_t ka = a_mn ? 128 : 2, kb_step = b_mn ? 128 : 2;
         for (int kb = q.begin; kb < q.end; ++kb) {
+          const bool begins = ((kb - q.begin) & run) == 0, ends = kb + 1 == q.end || ((kb + 1 - q.begin) & run) == 0;
+          if (begins) {
+            if (j >= 2 && !warp_wait(&drained[j & 1], ((j >> 1) - 1) & 1, &g_muon_error)) {
+              ok = false;
+              break;
+            }
+            acc = tmem + (j & 1) * 256;
+          }
           const int s0 = s;
           bool here = warp_wait(&full[s0], round & 1, &g_muon_error);
           if (++s == kStages) s = 0, ++round;
@@ -425,26 +462,26 @@ __global__ void __launch_bounds__(kThreads, 1) muon_steps(const __grid_constant_
           tc_after();
           const uint64_t ah = a0 + (uint64_t)(s0 * (kStage >> 4)), bh = b0 + (uint64_t)(s0 * (kStage >> 4));
           const uint64_t al = a0 + (uint64_t)(s1 * (kStage >> 4)), bl = b0 + (uint64_t)(s1 * (kStage >> 4));
-          const uint32_t more = kb > q.begin ? 1u : 0u;
+          const uint32_t more = begins ? 0u : 1u;
           if (issuer) {
-#pragma unroll
-            for (int k = 0; k < kBK / 16; ++k)  // high high
-              umma_f16(acc, ah + k * ka, bh + k * kb_step, idesc, k ? 1u : more);
-            if (pairs) {
+            if (pairs) {  // small terms first, while the sums are
 #pragma unroll
               for (int k = 0; k < kBK / 16; ++k)  // high low
-                umma_f16(cross, ah + k * ka, bl + k * kb_step, idesc, k ? 1u : more);
+                umma_f16(acc, ah + k * ka, bl + k * kb_step, idesc, k ? 1u : more);
 #pragma unroll
               for (int k = 0; k < kBK / 16; ++k)  // low high
-                umma_f16(cross, al + k * ka, bh + k * kb_step, idesc, 1u);
+                umma_f16(acc, al + k * ka, bh + k * kb_step, idesc, 1u);
               commit_both(&empty[s1]);
             }
+#pragma unroll
+            for (int k = 0; k < kBK / 16; ++k)  // high high
+              umma_f16(acc, ah + k * ka, bh + k * kb_step, idesc, k || pairs ? 1u : more);
             commit_both(&empty[s0]);
-            if (kb + 1 == q.end) commit_both(&tfull[j & 1]);
+            if (ends) commit_both(&tfull[j & 1]);
           }
           __syncwarp();
+          j += ends;
         }
-        ++j;
       }
     }
   } else {
@@ -453,7 +490,7 @@ __global__ void __launch_bounds__(kThreads, 1) muon_steps(const __grid_constant_
     const unsigned char* terms = reinterpret_cast<const unsigned char*>(buf) + kBuf;
     const float lr = g.lr_device ? *g.lr_device : g.lr;
     const int sub = lane >> 2, piece = lane & 3;  // eight columns of a row for a lane, rows 8 i + sub
-    int j = 0;  // tiles with products so far
+    int j = 0;  // runs so far
     for (int w = first; w < work; w += stride) {
       const Tile q = tile_of(g, w);
       const Item& t = *q.t;
@@ -466,12 +503,12 @@ __global__ void __launch_bounds__(kThreads, 1) muon_steps(const __grid_constant_
       const bool gram = q.which == GRAM || q.which == SUM;
       __half* out = gram ? m.gram : q.which == POLY ? m.poly : m.x[1 - (q.step & 1)];
       const bool last_step = q.which == APPLY && q.step + 1 == g.steps;
-      const bool store_low = q.which != POLY || t.pairs;
+      const bool pairs = PAIRS && t.pairs;
+      const bool store_low = q.which != POLY || pairs;
       float* diag_out = gram ? m.gram_diag : m.poly_diag;
       const int chunks = q.which == SUM ? 1 : q.bn / 64;  // of 32 columns, for each half of the columns
       const int row0 = q.m0 + (int)rank * 128 + quad * 32;
-      const bool whole = t.pairs && q.bn == 256;
-      const uint32_t acc = tmem + (whole ? 0 : (j & 1) * 256) + ((uint32_t)(quad * 32) << 16);
+      const uint32_t lanes = tmem + ((uint32_t)(quad * 32) << 16);
       const bool split = q.which == GRAM && t.splits > 1;  // sums to the workspace
       // 16-byte pieces of a split's 32 columns of a tile, in the order that warps hold them
       auto place = [&](int k, int chunk) {
@@ -526,23 +563,22 @@ __global__ void __launch_bounds__(kThreads, 1) muon_steps(const __grid_constant_
       if (!ok) break;
       tc_after();
 
-      auto results = [&](int c, uint32_t* r) {
-        const uint32_t at = acc + (half * chunks + c) * 32;
-        tmem_ld32(at, r);
-        if (t.pairs) {
-          uint32_t x[32];
-          tmem_ld32(at + q.bn, x);
-          tmem_ld_wait();
-#pragma unroll
-          for (int v = 0; v < 32; ++v) r[v] = __float_as_uint(__uint_as_float(r[v]) + __uint_as_float(x[v]));
-        } else {
-          tmem_ld_wait();
-        }
-      };
       auto release = [&] {
         tc_before();
         __syncwarp();
         if (lane == 0) arrive_at(in_cta(smem_u32(&drained[j & 1]), 0));
+      };
+      if (RUNS && pairs && q.end - q.begin > kRun) {
+        j = add_runs(lanes + half * chunks * 32, chunks, (q.end - q.begin + kRun - 1) / kRun, j, tfull,
+                     in_cta(smem_u32(drained), 0));
+        ok = j >= 0;
+        if (!ok) break;
+      }
+      const uint32_t acc = lanes + (j & 1) * 256;
+      auto results = [&](int c, uint32_t* r) {
+        const uint32_t at = acc + (half * chunks + c) * 32;
+        tmem_ld32(at, r);
+        tmem_ld_wait();
       };
       if (split) {
 #pragma unroll 1
@@ -738,16 +774,23 @@ int gram_splits(const MuonMat& t) {
   const int nkb = (int)ceil_div_ll(t.tall ? t.rows : t.cols, kBK);
   int want = tiles == 1 ? 12 : tiles == 3 ? 8 : 1;
   if (want > nkb / 3) want = nkb / 3;
-  // (and no accumulator runs over more than 16 blocks, up to 48 splits: the
-  // tensor cores truncate it after each of 4 products a block)
-  if (tiles <= 3 && want < nkb / 16) want = nkb / 16 < 48 ? nkb / 16 : 48;
+  // And no accumulator of few tiles runs over more than 16 blocks (up to 48
+  // splits), none over more than 256: the tensor cores truncate it after each of
+  // 4 products a block (cross terms' tiles add up shorter runs).
+  const int runs = (nkb + 15) / 16, least = (nkb + 255) / 256;
+  if (tiles <= 3 && want < runs) want = runs < 48 ? runs : 48;
+  if (want < least) want = least;
   if (want < 2) return 1;
   const int per = (nkb + want - 1) / want;
   return (nkb + per - 1) / per;
 }
 
-template <int CAP>
-cudaError_t launch(const MuonGroup& m, cudaStream_t s) {
+// (products of a short side under 64 cost nothing, and its matrix has few values
+// for the roundings to average over)
+bool takes_pairs(const MuonGroup& g, const MuonMat& t) { return g.precision == DC_ORTHO_32 || t.side < 64; }
+
+template <int CAP, bool PAIRS, bool RUNS>
+cudaError_t launch_as(const MuonGroup& m, cudaStream_t s) {
   Items<CAP> g;
   g.count = m.count;
   g.steps = m.steps;
@@ -775,16 +818,14 @@ cudaError_t launch(const MuonGroup& m, cudaStream_t s) {
     }
     const int e = t.out_dtype == DC_BF16 ? 2 : 4;
     const void* out = m.update ? t.param : t.out;
-    // (products of a short side under 64 cost nothing, and its matrix has few
-    // values for the roundings to average over)
-    q.pairs = m.precision == DC_ORTHO_32 || t.side < 64;
+    q.pairs = takes_pairs(m, t);
     q.vec = t.cols % 8 == 0 && (uintptr_t)out % 16 == 0 && (uintptr_t)t.master % 16 == 0 && (t.cols * e) % 16 == 0;
     if (!pair_map(&q.x[0], t.x[0], t.rows, t.cols, t.ld) || !pair_map(&q.x[1], t.x[1], t.rows, t.cols, t.ld) ||
         !pair_map(&q.gram, t.gram, t.side, t.side, t.lds) || !pair_map(&q.poly, t.poly, t.side, t.side, t.lds))
       return cudaErrorInvalidValue;
   }
   static std::atomic<bool> allowed[kOnceDevices];
-  cudaError_t e = allow_smem_once(muon_steps<CAP>, kSmem, allowed);
+  cudaError_t e = allow_smem_once(muon_steps<CAP, PAIRS, RUNS>, kSmem, allowed);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(2 * kPairs);
@@ -803,7 +844,7 @@ cudaError_t launch(const MuonGroup& m, cudaStream_t s) {
   if ((e = cudaGetDevice(&dev)) != cudaSuccess) return e;
   if (dev < kOnceDevices) most = at_once[dev].load(std::memory_order_relaxed);
   if (most == 0) {
-    e = cudaOccupancyMaxActiveClusters(&most, muon_steps<CAP>, &cfg);
+    e = cudaOccupancyMaxActiveClusters(&most, muon_steps<CAP, PAIRS, RUNS>, &cfg);
     if (e != cudaSuccess) return e;
     if (dev < kOnceDevices) at_once[dev].store(most, std::memory_order_relaxed);
   }
@@ -817,9 +858,26 @@ cudaError_t launch(const MuonGroup& m, cudaStream_t s) {
   attr[1].id = cudaLaunchAttributeCooperative;
   attr[1].val.cooperative = 1;
   cfg.numAttrs = 2;
-  e = cudaLaunchKernelEx(&cfg, muon_steps<CAP>, g);
+  e = cudaLaunchKernelEx(&cfg, muon_steps<CAP, PAIRS, RUNS>, g);
   note_launches(1);
   return e;
+}
+
+// (one kernel for all took 630 us in place of 545 for four of 2048 x 2048, high
+// parts only, and 237 in place of 200 for four pairs of 256 x 2304 and 18 x 2304
+// with the low ones: the sums of runs take registers from all the rest)
+template <int CAP>
+cudaError_t launch(const MuonGroup& g, cudaStream_t s) {
+  bool pairs = false, runs = false;
+  for (int i = 0; i < g.count; ++i) {
+    const MuonMat& t = g.mat[i];
+    if (!takes_pairs(g, t)) continue;
+    const int nkb = (int)ceil_div_ll(t.tall ? t.rows : t.cols, kBK), splits = gram_splits(t);
+    pairs = true;
+    runs = runs || t.side > kRun * kBK || (nkb + splits - 1) / splits > kRun;
+  }
+  return runs ? launch_as<CAP, true, true>(g, s)
+         : pairs ? launch_as<CAP, true, false>(g, s) : launch_as<CAP, false, false>(g, s);
 }
 
 }  // namespace

@@ -562,8 +562,7 @@ typedef enum { DC_ORTHO_16 = 0, DC_ORTHO_32 = 1 } dc_ortho_precision;
 /* Between the products X, A and the polynomial of A are held as pairs of
  * 16-bit floats (as good as float32; fixed point below 2^-36), their diagonals
  * in float32.  DC_ORTHO_32 multiplies both parts of every factor: the result is
- * about as good as float32 arithmetic's (the tensor cores truncate their sums
- * after 16 products each, which a long side of many thousands adds up).
+ * as good as float32 arithmetic's.
  * DC_ORTHO_16 multiplies the high parts alone
  * (relative error about 1e-3, below a rounding to bf16), but both where the
  * shorter side is under 64.  Sums are float32, in a fixed order: the same

@@ -152,7 +152,7 @@ def test_layers_beyond_32_bits(layout, training):
 
 def polynomial(x, steps=5):
     """M (64 bits) with M X0 = X after `steps`, for a wide x, and X0's factor."""
-    gram, squares = torch.zeros(x.shape[0], x.shape[0], dtype=torch.float64, device="cuda"), 0.0
+    gram = torch.zeros(x.shape[0], x.shape[0], dtype=torch.float64, device="cuda")
     for part in x.split(200_000, 1):
         part = part.double()
         gram += part @ part.T
@@ -174,7 +174,7 @@ def test_orthogonalize_long_sides(size):
     96 products of 16, each truncated by less than 2^-23 of the sum so far, half
     the run's on average: 96 * 2^-24 = 5.7e-6 of the gram.  A gram that is off by
     d moves these sizes' results by 1.1 d and 1.4 d (the steps evaluated at their
-    singular values, all within 2 %, 10 % of one another): 8e-6, and 2e-6 for the
+    singular values, within 10 % and 1.3 % of their mean): 8e-6, and 2e-6 for the
     other roundings."""
     x = normal(*size, dtype=F32)
     m, f = polynomial(x)

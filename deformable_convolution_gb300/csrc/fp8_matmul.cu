@@ -55,7 +55,7 @@ struct Cfg {
 };
 
 struct Args {
-  int batch, m, n, sum, a_shared, b_shared;
+  int m, n, sum, a_shared, b_shared;
   int nkb;                  // scale blocks along k
   int a_fmt, b_fmt;
   int tiles_m, tiles_n, splits, per_split;  // per_split: blocks of the reduction for one split
@@ -441,7 +441,6 @@ cudaError_t launch_fp8_matmul(const Fp8Product& t, cudaStream_t s) {
   const dc_fp8_product& p = t.p;
   const Plan q = plan_of(p);
   Args a{};
-  a.batch = p.batch;
   a.m = p.m;
   a.n = p.n;
   a.sum = p.sum;

@@ -11,6 +11,12 @@ import torch
 from . import binding as B
 
 
+def _empty(shape, dtype, device, stream):
+    """A new tensor for a kernel on ``stream``, whose memory no other stream still writes to."""
+    with torch.cuda.stream(stream):  # (None: the current one)
+        return torch.empty(shape, dtype=dtype, device=device)
+
+
 class Quantized:
     """Matrices in 8 bits: codes and scales of ``p`` (an ``Fp8Problem``), and
     of their transposes.  direct, transposed: which of the two are kept."""
@@ -32,7 +38,7 @@ class Quantized:
         """The float32 values that the codes stand for, as a new tensor."""
         codes, scales = (self.codes_t, self.scales_t) if transposed else (self.codes, self.scales)
         shape = (self.p.batch, self.p.cols, self.p.rows) if transposed else self.p.shape
-        out = torch.empty(shape, device=codes.device)
+        out = _empty(shape, torch.float32, codes.device, stream)
         B.dc_fp8_values(self.p, codes, scales, out, transposed, stream)
         return out
 
@@ -118,11 +124,11 @@ class Pointwise:
         self._loaded = True
 
     def forward(self, x, y=None, stream=None):
-        """y (a new tensor if not given) = W x."""
+        """y (a new tensor of ``stream``'s if not given) = W x."""
         if not self._loaded:
             raise ValueError("the layer has no weight yet (load)")
         x_ptr = B._arg(x, "x", self.x_shape, self.dtype)
-        y = torch.empty(self.y_shape, dtype=self.dtype, device=x.device) if y is None else y
+        y = _empty(self.y_shape, self.dtype, x.device, stream) if y is None else y
         y_ptr = B._arg(y, "y", self.y_shape, self.dtype)
         s = B._raw_stream(stream)
         if self._one is not None:
@@ -144,9 +150,9 @@ class Pointwise:
             raise ValueError("no forward pass before the backward pass")
         g_ptr = B._arg(grad_y, "grad_y", self.y_shape, self.grad_dtype)
         if grad_x is None:
-            grad_x = torch.empty(self.x_shape, dtype=self.dtype, device=grad_y.device)
+            grad_x = _empty(self.x_shape, self.dtype, grad_y.device, stream)
         if grad_w is None:
-            grad_w = torch.empty(self.w_shape, dtype=torch.float32, device=grad_y.device)
+            grad_w = _empty(self.w_shape, torch.float32, grad_y.device, stream)
         gx_ptr = B._arg(grad_x, "grad_x", self.x_shape, self.dtype)
         gw_ptr = B._arg(grad_w, "grad_w", self.w_shape if grad_w.dim() == 2 else self.w_shape + (1, 1), torch.float32)
         s = B._raw_stream(stream)

@@ -86,6 +86,28 @@ def test_graphs_that_share_a_workspace():
         assert torch.equal(got[0], y) and torch.equal(got[1], z) and y.any()
 
 
+def test_new_results_on_another_stream():
+    """A result made for a call on another stream does not take memory that the
+    current stream, which has just given it up, has still to write."""
+    layer = fp8.Pointwise(2, 64, 64, 64, 64, B.DC_BF16, B.DC_NHWC)
+    layer.load(normal(64, 64))
+    x, gy = normal(*layer.x_shape, seed=1), normal(*layer.y_shape, seed=2)
+    want = [layer.forward(x), *layer.backward(gy)]
+    values = layer.x.values()
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    for k in range(4):
+        late = [torch.empty_like(t) for t in want + [values]]
+        torch.cuda._sleep(20_000_000)  # about 10 ms
+        for t in late:
+            t.fill_(7.0)
+        del late, t
+        got = [layer.forward(x, stream=side), *layer.backward(gy, stream=side)]
+        again = layer.x.values(stream=side)
+        torch.cuda.synchronize()
+        assert all(in_bits(a, b) for a, b in zip(got, want)) and in_bits(again, values)
+
+
 # ---------------------------------------------------------------- beyond 32 bits
 
 def test_codes_beyond_32_bits():

@@ -82,7 +82,7 @@ class DcFp8Problem(ctypes.Structure):
 class DcFp8Product(ctypes.Structure):
     """Mirror of ``dc_fp8_product``."""
     _fields_ = [(name, ctypes.c_int) for name in (
-        "batch", "m", "n", "k", "a_format", "b_format", "a_shared", "b_shared", "sum", "out")]
+        "batch", "m", "n", "k", "a_format", "b_format", "a_shared", "b_shared", "sum", "out", "beside")]
 
 
 class DcFp8Layer(ctypes.Structure):
@@ -768,7 +768,8 @@ class Fp8Problem:
 class Fp8Product:
     """D[i] = A[i] B[i]^T for matrices in 8 bits, A[i] [m, k], B[i] [n, k]
     (``Fp8Problem``s with cols = k); a_shared, b_shared: one matrix for all i;
-    sum: D is the sum over i.  out: D's type."""
+    sum: D is the sum over i.  out: D's type.  beside: the stream's last launch
+    was another product that has nothing to do with what this one reads or writes."""
     batch: int
     m: int
     n: int
@@ -779,12 +780,13 @@ class Fp8Product:
     b_shared: int = 0
     sum: int = 0
     out: int = DC_BF16
+    beside: int = 0
 
     @cached_property
     def _as_parameter_(self):
         return ctypes.byref(DcFp8Product(self.batch, self.m, self.n, self.k, self.a_format,
                                          self.b_format, self.a_shared, self.b_shared, self.sum,
-                                         self.out))
+                                         self.out, self.beside))
 
     @cached_property
     def torch_dtype(self):

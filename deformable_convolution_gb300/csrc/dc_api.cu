@@ -1016,7 +1016,7 @@ dc_status check_product(const dc_fp8_product* p) {
   if (!p || p->batch < 0 || p->m <= 0 || p->n <= 0 || p->k < 0 || !fp8_known(p->a_format) ||
       !fp8_known(p->b_format) || !dtype_known(p->out))
     return DC_ERR_INVALID_ARG;
-  for (int flag : {p->a_shared, p->b_shared, p->sum})
+  for (int flag : {p->a_shared, p->b_shared, p->sum, p->beside})
     if (flag != 0 && flag != 1) return DC_ERR_INVALID_ARG;
   if (p->m > kFp8MaxSide || p->n > kFp8MaxSide || p->k > kFp8MaxSide || p->batch > kFp8MaxBatch)
     return DC_ERR_UNSUPPORTED;

@@ -64,6 +64,7 @@ struct Args {
   int m_first;              // tiles run down m first
   int tma_out;              // D by TMA, else element by element
   int out_f32;
+  int beside;               // what it reads was there before the product launched ahead of it
   const unsigned char* sa;
   const unsigned char* sb;
   void* d;                  // [batch or splits][m][ldd]
@@ -137,7 +138,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   tc_after();
   const uint32_t tmem = *holder;
   bool ok = true;
-  pdl_wait();
+  if (!a.beside) pdl_wait();
   pdl_release();
 
   if (warp == kWarpTma) {
@@ -344,6 +345,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   cluster_sync();  // the pair's barriers and tensor memory are no longer used
   tc_after();
   if (warp == 0) tmem_free(tmem);
+  if (a.beside) pdl_wait();  // what follows this launch also follows the one before it
 }
 
 // D = the splits' sums, in order.
@@ -458,6 +460,7 @@ cudaError_t launch_fp8_matmul(const Fp8Product& t, cudaStream_t s) {
   const long long work = (long long)q.tiles_m * q.tiles_n * z;
   if (work > INT_MAX) return cudaErrorInvalidValue;
   a.work = (int)work;
+  a.beside = p.beside;
   a.m_first = q.tiles_m <= q.tiles_n;
   a.sa = static_cast<const unsigned char*>(t.a_scales);
   a.sb = static_cast<const unsigned char*>(t.b_scales);

@@ -91,7 +91,9 @@ class Pointwise:
             self.gy = Quantized(maps(c_out, grad_dtype, g), True, True, device)
             self._gx = q(batch, pixels, c_in, c_out, g, e, b_shared=1, out=dtype) if last else \
                 q(batch, c_in, pixels, c_out, e, g, a_shared=1, out=dtype)
-            self._gw = q(batch, c_out, c_in, pixels, g, e, sum=1, out=B.DC_F32)
+            # (beside the product ahead of it: 3 x 29 x 43, 200 -> 328: 17.8 us in place of 21.8; none where that one
+            # fills the GPU)
+            self._gw = q(batch, c_out, c_in, pixels, g, e, sum=1, out=B.DC_F32, beside=1)
             products += [self._gx, self._gw]
         need = max(B.dc_fp8_matmul_workspace_size(p) for p in products)
         self._ws = torch.empty(max(need, 1), dtype=torch.uint8, device=device)

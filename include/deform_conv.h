@@ -514,6 +514,10 @@ dc_status dc_fp8_values(const dc_fp8_problem* prob, int transposed, const void* 
  *   a_shared, b_shared  one matrix for all i
  *   sum                 D [m][n] = sum over i of A[i] B[i]^T (a weight's
  *                       gradient from the images of a batch)
+ *   beside              the stream's last launch was another dc_fp8_matmul that
+ *                       neither writes what this one reads nor reads or writes
+ *                       what this one writes (d, ws): it may start before that
+ *                       one has ended
  * Products of codes are exact, sums are float32 in a fixed order (the same
  * inputs give the same bits); a bf16 D is rounded to nearest even.  batch or k
  * may be 0: nothing is written for batch 0 without sum, else zeros.
@@ -527,6 +531,7 @@ typedef struct {
   dc_fp8 a_format, b_format;
   int a_shared, b_shared, sum;
   dc_dtype out;
+  int beside;
 } dc_fp8_product;
 dc_status dc_fp8_matmul_workspace_size(const dc_fp8_product* prob, size_t* bytes);
 dc_status dc_fp8_matmul(const dc_fp8_product* prob, const void* a, const void* a_scales,

@@ -82,6 +82,12 @@ def test_matmul_checks_its_arguments(kw, status):
     assert product_status(**kw) == status
 
 
+def test_matmul_beside_is_a_flag():
+    for beside, status in ((2, INVALID), (-1, INVALID), (0, B.DC_OK), (1, B.DC_OK)):
+        q, out = B.DcFp8Product(1, 64, 64, 128, 0, 0, 0, 0, 0, B.DC_F32, beside), ctypes.c_size_t(0)
+        assert B.lib().dc_fp8_matmul_workspace_size(ctypes.byref(q), ctypes.byref(out)) == status
+
+
 def test_matmul_checks_its_workspace():
     p = B.Fp8Product(64, 64, 64, 1 << 16, sum=1)
     need = B.dc_fp8_matmul_workspace_size(p)

@@ -1,6 +1,8 @@
 """Matrices in 8 bits, orthogonalisation and Muon where their calls meet others
 (two streams at once, graphs that share a workspace) and where an element's
 place passes 32 bits."""
+import dataclasses
+
 import pytest
 import torch
 
@@ -84,6 +86,48 @@ def test_graphs_that_share_a_workspace():
         y.zero_(), z.zero_()
         call()
         assert torch.equal(got[0], y) and torch.equal(got[1], z) and y.any()
+
+
+@pytest.mark.parametrize("size", [(1, 512, 32, 64, 64), (3, 40, 72, 9, 11), (2, 64, 300, 40, 33), (8, 256, 256, 56, 56)])
+@pytest.mark.parametrize("layout", (B.DC_NCHW, B.DC_NHWC))
+def test_backward_products_side_by_side(size, layout):
+    """The weight's gradient may start before the product ahead of it has ended:
+    what comes after both (the next pass's codes of other inputs, in the same
+    place) waits for both, eagerly and in a graph."""
+    n, c_in, c_out, h, w = size
+    layer = fp8.Pointwise(n, c_in, c_out, h, w, B.DC_BF16, layout)
+    layer.load(normal(c_out, c_in))
+    sets = [(normal(*layer.x_shape, seed=k), normal(*layer.y_shape, seed=k + 9)) for k in range(3)]
+    want = []
+    for x, gy in sets:
+        layer.forward(x)
+        torch.cuda.synchronize()
+        want.append([t.clone() for t in layer.backward(gy)])
+        torch.cuda.synchronize()
+    # the same with the weight's gradient behind the other product
+    apart = fp8.Pointwise(n, c_in, c_out, h, w, B.DC_BF16, layout)
+    apart._gw = dataclasses.replace(apart._gw, beside=0)
+    apart.load(normal(c_out, c_in))
+    for (x, gy), r in zip(sets, want):
+        apart.forward(x)
+        assert all(in_bits(a, b) for a, b in zip(apart.backward(gy), r))
+
+    def passes(times):
+        got = []
+        for _ in range(times):
+            for x, gy in sets:
+                layer.forward(x)
+                got.append(layer.backward(gy))
+        return got
+    got = passes(10)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        captured = passes(2)
+    for _ in range(3):
+        graph.replay()
+    torch.cuda.synchronize()
+    for k, r in enumerate(got + captured):
+        assert all(in_bits(a, b) for a, b in zip(r, want[k % len(sets)]))
 
 
 def test_new_results_on_another_stream():

@@ -39,6 +39,7 @@ DC_STATE_F32, DC_STATE_Q8 = 0, 1
 DC_E4M3, DC_E5M2 = 0, 1
 DC_ORTHO_16, DC_ORTHO_32 = 0, 1
 FP8_BLOCK = 128    # values that share a scale
+FP8_RUN = 8192     # most values of k that a product sums in one accumulator
 STATE_BLOCK = 256  # elements of an 8-bit state that share a scale
 DC_COL_PLANE_MAJOR, DC_COL_PIXEL_MAJOR = 0, 1
 MARGIN_BINS = 64

@@ -1238,7 +1238,7 @@ dc_status dc_fp8_pointwise(const dc_fp8_layer* prob, const void* x, const void* 
   if (!prob || prob->n < 0 || prob->pixels <= 0 || prob->c_in <= 0 || prob->c_out <= 0 ||
       (prob->layout != DC_NCHW && prob->layout != DC_NHWC))
     return DC_ERR_INVALID_ARG;
-  if (prob->c_out > 256 || prob->c_in > (1 << 20) || (long long)prob->n * prob->pixels > (1 << 30))
+  if (prob->c_out > 256 || prob->c_in > DC_FP8_RUN || (long long)prob->n * prob->pixels > (1 << 30))
     return DC_ERR_UNSUPPORTED;
   if (prob->n == 0) return DC_OK;
   if (!x || !w_codes || !w_scales || !y) return DC_ERR_INVALID_ARG;

@@ -9,6 +9,15 @@
 // would have to be multiplied in by CUDA cores every 128 of k, reading the
 // accumulator out of tensor memory each time.
 //
+// The tensor cores cut the sum off after each product of 32, always towards zero:
+// a sum of one sign over 2^20 of k came out 3e-3 too small in one accumulator.  So
+// an accumulator runs over at most kRun blocks (256 products; 8192 of k: 5e-6 too
+// small at most), and the runs of a longer reduction are added up in float32 in
+// the workspace or D, by TMA reductions of one thread, one behind the other: their
+// order, and so the result's bits, stay the same.  2048 x 2048 over 2^20: 4.8e-6 at
+// most.  A run's end costs 2.5 us (2048 x 2048 over 33600: 90 us against 80 in one
+// accumulator, which is 2.8e-5 too small; over 2^18: 626 against 556).
+//
 // CTAs work in pairs on tiles of 256 x BN (tc_pair.cuh).  The tensor cores read
 // 128 rows of A and BN / 2 of B per SM from shared memory for 128 x BN results,
 // at 256 x 256 as many bytes as shared memory gives in the time of the MMAs;
@@ -40,6 +49,7 @@ constexpr int kEpiWarps = 8, kScaleWarps = 4;
 constexpr int kWarpTma = kEpiWarps + kScaleWarps, kWarpMma = kWarpTma + 1;
 constexpr int kThreads = (kWarpMma + 1) * 32;
 constexpr int kPairs = 76;      // of 152 SMs
+constexpr int kRun = DC_FP8_RUN / kBK;  // most blocks of an accumulator
 constexpr int kStageBuf = 4096; // store staging of a warp: 32 rows of 128 bytes, or twice 32 of 64
 
 template <int BN>
@@ -62,6 +72,7 @@ struct Args {
   int total;                // blocks of a tile's whole reduction
   int work;                 // tiles * splits (or batch)
   int m_first;              // tiles run down m first
+  int add_runs;             // reductions have more than kRun blocks: the later runs are added to D
   int tma_out;              // D by TMA, else element by element
   int out_f32;
   int beside;               // what it reads was there before the product launched ahead of it
@@ -173,19 +184,25 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       const uint32_t idesc0 = ((uint32_t)a.a_fmt << 7) | ((uint32_t)a.b_fmt << 10) | ((uint32_t)(BN >> 3) << 17) |
                               (1u << 23) | ((256u >> 4) << 24);
       const uint64_t desc0 = sdesc(smem_u32(smem), 16, 1024);
-      int s = 0, round = 0, slot = 0, j = 0;  // stages, scale slots and tiles so far
-      for (int w = first; w < a.work && ok; w += stride, ++j) {
+      int s = 0, round = 0, slot = 0, j = 0;  // stages, scale slots and runs so far
+      uint32_t acc = tmem;
+      for (int w = first; w < a.work && ok; w += stride) {
         const Tile t = tile_of(a, w, BN);
-        // accumulators apart: the tile before last has been read; sharing
-        // columns: these have been read of the last one (and the one before whole)
-        const int before = j - (C::kShared ? 1 : 2);
-        if (before >= 0 && !warp_wait(&drained[before & 1], (before >> 1) & 1, &g_fp8_error)) {
-          ok = false;
-          break;
-        }
-        const uint32_t acc = tmem + (j & 1) * C::kAcc1;
         int kb = a.sum ? t.begin % a.nkb : t.begin;
-        for (int f = t.begin; f < t.end; ++f) {
+        int left = 0;  // blocks of the run
+        for (int f = t.begin; f < t.end; ++f, --left) {
+          const bool begins = left == 0;
+          if (begins) {
+            left = min(kRun, t.end - f);
+            // accumulators apart: the run before last has been read; sharing
+            // columns: these have been read of the last one (and the one before whole)
+            const int before = j - (C::kShared ? 1 : 2);
+            if (before >= 0 && !warp_wait(&drained[before & 1], (before >> 1) & 1, &g_fp8_error)) {
+              ok = false;
+              break;
+            }
+            acc = tmem + (j & 1) * C::kAcc1;
+          }
           if (f == t.begin || (kb & 3) == 0) {
             if (!warp_wait(&sfull[slot & 1], (slot >> 1) & 1, &g_fp8_error)) {
               ok = false;
@@ -205,12 +222,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           if (issuer) {
 #pragma unroll
             for (int k = 0; k < kBK / 32; ++k)
-              umma_scaled(acc, da + 2 * k, db + 2 * k, idesc, scale, scale + 4, (f > t.begin || k > 0) ? 1u : 0u);
+              umma_scaled(acc, da + 2 * k, db + 2 * k, idesc, scale, scale + 4, (!begins || k > 0) ? 1u : 0u);
             commit_both(&empty[s]);
             if (chunk_end) commit_both(&sempty[slot & 1]);
-            if (f + 1 == t.end) commit_both(&tfull[j & 1]);
+            if (left == 1) commit_both(&tfull[j & 1]);
           }
           __syncwarp();
+          j += left == 1;
           slot += chunk_end;
           if (++kb == a.nkb) kb = 0;
           if (++s == C::kStages) s = 0, ++round;
@@ -258,11 +276,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     const int quad = warp & 3, half = warp >> 2;
     unsigned char* buf = stg + warp * kStageBuf;
     int j = 0, used = 0;
-    for (int w = first; w < a.work; w += stride, ++j) {
+    for (int w = first, from = 0; w < a.work; ++j) {
       const Tile t = tile_of(a, w, BN);
+      const bool adds = a.add_runs && from > 0;  // to what this warp's runs before have left
       ok = warp_wait(&tfull[j & 1], (j >> 1) & 1, &g_fp8_error);
       if (!ok) break;
       tc_after();
+      if (adds && lane == 0) store_wait_all();
       const uint32_t acc = tmem + (j & 1) * C::kAcc1 + ((uint32_t)(quad * 32) << 16);
       const int row0 = t.m0 + (int)rank * 128 + quad * 32;
       constexpr int kChunks = BN / 64;  // of 32 columns, for each half
@@ -314,7 +334,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           fence_proxy_async();
           __syncwarp();
           if (lane == 0) {
-            tma_store(&td, smem_u32(b), col0, row0, t.z);
+            if (adds)
+              tma_add(&td, smem_u32(b), col0, row0, t.z);
+            else
+              tma_store(&td, smem_u32(b), col0, row0, t.z);
             store_commit();
           }
         } else {
@@ -336,6 +359,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           __syncwarp();
         }
       }
+      // the tile's next run, or the next tile
+      from = t.end - t.begin - from > kRun ? from + kRun : 0;
+      if (from == 0) w += stride;
     }
     if (lane == 0) store_wait_all();
   }
@@ -348,29 +374,29 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   if (a.beside) pdl_wait();  // what follows this launch also follows the one before it
 }
 
-// D = the splits' sums, in order.
+// D = the splits' sums, in order (rows: those of all matrices).
 __global__ void __launch_bounds__(256)
-    fp8_mm_sum(const float* __restrict__ part, int splits, long long stride, int m, int n, long long ldd, void* d,
-               int out_f32) {
+    fp8_mm_sum(const float* __restrict__ part, int splits, long long rows, int n, long long ldd, void* d, int out_f32) {
   pdl_wait();
   pdl_release();
-  const long long total = (long long)m * ldd / 4;
+  const long long total = rows * ldd / 4, stride = rows * ldd;
   for (long long i = (long long)blockIdx.x * 256 + threadIdx.x; i < total; i += (long long)gridDim.x * 256) {
-    float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
+    float4 s = __ldcg(reinterpret_cast<const float4*>(part) + i);
 #pragma unroll 8
-    for (int k = 0; k < splits; ++k) {
+    for (int k = 1; k < splits; ++k) {
       const float4 v = __ldcg(reinterpret_cast<const float4*>(part + k * stride) + i);
       s.x += v.x, s.y += v.y, s.z += v.z, s.w += v.w;
     }
-    const int r = (int)(4 * i / ldd), c = (int)(4 * i - r * ldd);
+    const long long r = 4 * i / ldd;
+    const int c = (int)(4 * i - r * ldd);
     const float e[4] = {s.x, s.y, s.z, s.w};
 #pragma unroll
     for (int q = 0; q < 4; ++q)
       if (c + q < n) {
         if (out_f32)
-          static_cast<float*>(d)[(long long)r * n + c + q] = e[q];
+          static_cast<float*>(d)[r * n + c + q] = e[q];
         else
-          static_cast<__nv_bfloat16*>(d)[(long long)r * n + c + q] = __float2bfloat16_rn(e[q]);
+          static_cast<__nv_bfloat16*>(d)[r * n + c + q] = __float2bfloat16_rn(e[q]);
       }
   }
 }
@@ -379,7 +405,9 @@ __global__ void __launch_bounds__(256)
 
 struct Plan {
   int bn, tiles_m, tiles_n, splits, per_split, total;
-  long long ldd;  // of a split's sums
+  bool add_runs;  // a tile's (or split's) reduction has more than kRun blocks
+  bool sums;      // float32 sums in the workspace, by splits or runs
+  long long ldd;  // theirs, or D's
 };
 
 Plan plan_of(const dc_fp8_product& p) {
@@ -407,7 +435,9 @@ Plan plan_of(const dc_fp8_product& p) {
     q.per_split = (int)ceil_div_ll(q.total, want);
     q.splits = (int)ceil_div_ll(q.total, q.per_split);
   }
-  q.ldd = q.splits > 1 ? (p.n + 3) / 4 * 4 : p.n;
+  q.add_runs = q.per_split > kRun;
+  q.sums = q.splits > 1 || q.add_runs;
+  q.ldd = q.sums ? (p.n + 3) / 4 * 4 : p.n;
   return q;
 }
 
@@ -436,7 +466,7 @@ cudaError_t launch(const CUtensorMap& ta, const CUtensorMap& tb, const CUtensorM
 size_t fp8_matmul_workspace_bytes(const dc_fp8_product& p) {
   if (p.k == 0 || p.batch == 0) return 0;
   const Plan q = plan_of(p);
-  return q.splits > 1 ? (size_t)q.splits * p.m * q.ldd * sizeof(float) : 0;
+  return q.sums ? (size_t)(p.sum ? q.splits : p.batch) * p.m * q.ldd * sizeof(float) : 0;
 }
 
 cudaError_t launch_fp8_matmul(const Fp8Product& t, cudaStream_t s) {
@@ -464,8 +494,12 @@ cudaError_t launch_fp8_matmul(const Fp8Product& t, cudaStream_t s) {
   a.m_first = q.tiles_m <= q.tiles_n;
   a.sa = static_cast<const unsigned char*>(t.a_scales);
   a.sb = static_cast<const unsigned char*>(t.b_scales);
-  a.out_f32 = p.out == DC_F32 || q.splits > 1;
-  a.d = q.splits > 1 ? t.ws : t.d;
+  a.add_runs = q.add_runs;
+  // runs of one split are added up in D itself where TMA can write it (2048 x 2048
+  // over 33600: 90 us in place of 97; ldd is n then)
+  const bool sums = q.sums && !(q.splits == 1 && p.out == DC_F32 && q.ldd == p.n && (uintptr_t)t.d % 16 == 0);
+  a.out_f32 = p.out == DC_F32 || sums;
+  a.d = sums ? t.ws : t.d;
   a.ldd = q.ldd;
   const int size = a.out_f32 ? 4 : 2;
   a.tma_out = a.ldd * size % 16 == 0 && (uintptr_t)a.d % 16 == 0;
@@ -490,8 +524,8 @@ cudaError_t launch_fp8_matmul(const Fp8Product& t, cudaStream_t s) {
   }
   if (!made) return cudaErrorInvalidValue;
   cudaError_t e = q.bn == 256 ? launch<256>(ta, tb, td, a, s) : launch<128>(ta, tb, td, a, s);
-  if (e != cudaSuccess || q.splits == 1) return e;
-  const long long blocks = ceil_div_ll((long long)p.m * q.ldd / 4, 256);
+  if (e != cudaSuccess || !sums) return e;
+  const long long rows = (long long)(p.sum ? 1 : p.batch) * p.m, blocks = ceil_div_ll(rows * q.ldd / 4, 256);
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(blocks < 152 * 8 ? blocks : 152 * 8));
   cfg.blockDim = dim3(256);
@@ -501,8 +535,8 @@ cudaError_t launch_fp8_matmul(const Fp8Product& t, cudaStream_t s) {
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  e = cudaLaunchKernelEx(&cfg, fp8_mm_sum, static_cast<const float*>(t.ws), q.splits, (long long)p.m * q.ldd, p.m, p.n,
-                         q.ldd, t.d, (int)(p.out == DC_F32));
+  e = cudaLaunchKernelEx(&cfg, fp8_mm_sum, static_cast<const float*>(t.ws), q.splits, rows, p.n, q.ldd, t.d,
+                         (int)(p.out == DC_F32));
   note_launches(1);
   return e;
 }

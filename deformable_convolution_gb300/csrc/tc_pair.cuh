@@ -77,6 +77,13 @@ __device__ __forceinline__ void tma_store(const CUtensorMap* map, uint32_t src, 
       "r"(c0), "r"(c1), "r"(c2)
       : "memory");
 }
+// As that, float32 values added to what stands there (numbers below 2^-126 count as zero).
+__device__ __forceinline__ void tma_add(const CUtensorMap* map, uint32_t src, int c0, int c1, int c2) {
+  asm volatile(
+      "cp.reduce.async.bulk.tensor.3d.global.shared::cta.add.tile.bulk_group [%0, {%2, %3, %4}], [%1];" ::"l"(map),
+      "r"(src), "r"(c0), "r"(c1), "r"(c2)
+      : "memory");
+}
 __device__ __forceinline__ void store_commit() { asm volatile("cp.async.bulk.commit_group;" ::: "memory"); }
 // All but the last N stores of this thread have read their source.
 template <int N>

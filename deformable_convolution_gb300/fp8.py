@@ -52,7 +52,7 @@ class Pointwise:
     ``training``, each 128 pixels of a channel for the weight's gradient; else,
     where one launch is faster, on its way into the product),
     ``backward`` the gradient of y (``grad_format``, in ``grad_dtype``) likewise.
-    Products are exact and summed in float32.
+    Products are exact and summed in float32 (``dc_fp8_matmul``).
 
     The layer keeps the codes of its weight and of the last forward's input,
     and workspaces: its calls belong on one stream, or on streams that wait for
@@ -77,7 +77,8 @@ class Pointwise:
         # the latter 10.0, 13.0.  Not where rows of y are no whole 16-byte pieces (9 x 22 x 4, 144 -> 71: 13.7, 7.1),
         # and channels first not for many output channels (8 x 56 x 56, 256 -> 256: 16.4, 11.3).
         self._one = None
-        if not training and dtype == B.DC_BF16 and (c_out <= 256 and c_out % 8 == 0 if last else c_out <= 128):
+        if not training and dtype == B.DC_BF16 and c_in <= B.FP8_RUN and \
+                (c_out <= 256 and c_out % 8 == 0 if last else c_out <= 128):
             self._one = B.DcFp8Layer(n, h * w, c_in, c_out, layout)
         kept = self._one is None
         self.x = Quantized(maps(c_in, dtype, B.DC_E4M3), kept and (last or training), kept and (not last or training),
@@ -92,8 +93,9 @@ class Pointwise:
             self._gx = q(batch, pixels, c_in, c_out, g, e, b_shared=1, out=dtype) if last else \
                 q(batch, c_in, pixels, c_out, e, g, a_shared=1, out=dtype)
             # (beside the product ahead of it: 3 x 29 x 43, 200 -> 328: 17.8 us in place of 21.8; none where that one
-            # fills the GPU)
-            self._gw = q(batch, c_out, c_in, pixels, g, e, sum=1, out=B.DC_F32, beside=1)
+            # fills the GPU; not where that one's sums stand in the workspace that both share)
+            alone = B.dc_fp8_matmul_workspace_size(self._gx) == 0
+            self._gw = q(batch, c_out, c_in, pixels, g, e, sum=1, out=B.DC_F32, beside=int(alone))
             products += [self._gx, self._gw]
         need = max(B.dc_fp8_matmul_workspace_size(p) for p in products)
         self._ws = torch.empty(max(need, 1), dtype=torch.uint8, device=device)

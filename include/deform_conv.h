@@ -483,6 +483,8 @@ typedef enum { DC_E4M3 = 0, DC_E5M2 = 1 } dc_fp8;
  * with runs = ceil(cols / 128); a square block's scale stands at each of its
  * rows, bytes of no row or run are of no meaning. */
 #define DC_FP8_BLOCK 128
+/* The most values of k that a product sums in one accumulator (dc_fp8_matmul). */
+#define DC_FP8_RUN 8192
 typedef struct {
   int batch, rows, cols; /* batch may be 0 */
   dc_dtype dtype;
@@ -519,8 +521,13 @@ dc_status dc_fp8_values(const dc_fp8_problem* prob, int transposed, const void* 
  *                       what this one writes (d, ws): it may start before that
  *                       one has ended
  * Products of codes are exact, sums are float32 in a fixed order (the same
- * inputs give the same bits); a bf16 D is rounded to nearest even.  batch or k
- * may be 0: nothing is written for batch 0 without sum, else zeros.
+ * inputs give the same bits); a bf16 D is rounded to nearest even.  The tensor
+ * cores cut a sum off towards zero after each 32 of k, so no accumulator runs
+ * over more than DC_FP8_RUN of k (of all matrices where `sum`): it is off by less
+ * than 128 * 2^-23 of the sum of its products' magnitudes (5e-6 as a rule for
+ * products of one sign, far less for mixed ones).  The runs of a longer reduction
+ * are added up in float32, which takes workspace.  batch or k may be 0: nothing is
+ * written for batch 0 without sum, else zeros.
  * Errors: DC_ERR_INVALID_ARG for a bad problem or a NULL required pointer,
  * DC_ERR_UNSUPPORTED for a pointer that is not 16-byte aligned (d: not aligned
  * to its element), m, n or k over 2^24, a batch over 65535, a factor over 2^38
@@ -547,8 +554,8 @@ dc_status dc_fp8_matmul(const dc_fp8_product* prob, const void* a, const void* a
  *          matrix, square or not)
  * Errors: DC_ERR_INVALID_ARG for NULL, a size below 1 (n: below 0) or an
  * unknown layout; DC_ERR_UNSUPPORTED for c_out over 256 (x would be read more
- * than once), c_in over 2^20, n * pixels over 2^30, or w not 16-byte aligned (x,
- * y: not aligned to their elements). */
+ * than once), c_in over DC_FP8_RUN (more than one accumulator's run), n * pixels
+ * over 2^30, or w not 16-byte aligned (x, y: not aligned to their elements). */
 typedef struct {
   int n, pixels, c_in, c_out; /* n may be 0 */
   dc_layout layout;

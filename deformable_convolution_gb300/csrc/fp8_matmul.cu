@@ -149,8 +149,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   tc_after();
   const uint32_t tmem = *holder;
   bool ok = true;
-  if (!a.beside) pdl_wait();
-  pdl_release();
+  if (!a.beside) {
+    pdl_wait();
+    pdl_release();
+  }
 
   if (warp == kWarpTma) {
     const bool issuer = elect_one();
@@ -371,7 +373,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   cluster_sync();  // the pair's barriers and tensor memory are no longer used
   tc_after();
   if (warp == 0) tmem_free(tmem);
-  if (a.beside) pdl_wait();  // what follows this launch also follows the one before it
+  // what follows this launch also follows the one before it, and starts no earlier
+  // than this one's wait (it is released by this one's end)
+  if (a.beside) pdl_wait();
 }
 
 // D = the splits' sums, in order (rows: those of all matrices).

@@ -23,9 +23,12 @@ __device__ __forceinline__ float block_sum(float v) {
 
 __global__ void __launch_bounds__(kThreads) muon_squares(const __grid_constant__ MuonGroup g) {
   // Beside the launch of the small matrices, which waited for what came before:
-  // it is waited for only before this grid ends, so that what follows finds both done.
-  if (!g.beside) pdl_wait();
-  pdl_release();
+  // it is waited for only before this grid ends, so that what follows finds both done
+  // (and starts no earlier than that wait).
+  if (!g.beside) {
+    pdl_wait();
+    pdl_release();
+  }
   const MuonMat& t = g.mat[blockIdx.y];
   float scale;
   if (skipped(g, &scale) || blockIdx.x >= t.parts) {

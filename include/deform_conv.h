@@ -519,7 +519,7 @@ dc_status dc_fp8_values(const dc_fp8_problem* prob, int transposed, const void* 
  *   beside              the stream's last launch was another dc_fp8_matmul that
  *                       neither writes what this one reads nor reads or writes
  *                       what this one writes (d, ws): it may start before that
- *                       one has ended
+ *                       one has ended.  What follows it starts after both.
  * Products of codes are exact, sums are float32 in a fixed order (the same
  * inputs give the same bits); a bf16 D is rounded to nearest even.  The tensor
  * cores cut a sum off towards zero after each 32 of k, so no accumulator runs

@@ -382,7 +382,9 @@ __global__ void __launch_bounds__(kThreads, 1) muon_steps(const __grid_constant_
       const MuonMat& m = q.t->m;
       bool here = true;
       if (lane == 0) here = inputs_done(q);
-      if (!__all_sync(0xffffffffu, here)) {
+      here = __all_sync(0xffffffffu, here);
+      __syncwarp();  // (a vote does not order memory: the other lanes read what lane 0 has waited for)
+      if (!here) {
         ok = false;
         break;
       }
@@ -554,6 +556,7 @@ __global__ void __launch_bounds__(kThreads, 1) muon_steps(const __grid_constant_
       bool here = true;
       if (lane == 0) here = inputs_done(q);
       here = __all_sync(0xffffffffu, here);
+      __syncwarp();
       if (here) {
         if (!gram && cr != 0.f && row0 + lane < rows) row_diag = __ldcg(diag + row0 + lane);
         load_terms(0);

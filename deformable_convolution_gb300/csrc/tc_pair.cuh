@@ -43,7 +43,9 @@ __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, unsign
   if (__all_sync(0xffffffffu, ready)) return true;
   bool done = true;
   if ((threadIdx.x & 31) == 0) done = mbar_wait(bar, parity, flag);
-  return __all_sync(0xffffffffu, done);
+  done = __all_sync(0xffffffffu, done);
+  __syncwarp();  // a vote does not order memory: the other lanes read what lane 0 has waited for
+  return done;
 }
 __device__ __forceinline__ void cluster_sync() {
   asm volatile("barrier.cluster.arrive.release.aligned;\nbarrier.cluster.wait.acquire.aligned;" ::: "memory");

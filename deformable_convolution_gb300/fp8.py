@@ -24,10 +24,10 @@ class Quantized:
     def __init__(self, p: B.Fp8Problem, direct=True, transposed=False, device="cuda"):
         self.p = p
 
-        def pair(shapes, kept):
-            return [torch.empty(s, dtype=torch.uint8, device=device) if kept else None for s in shapes]
-        self.codes, self.scales = pair(p.shapes, direct)
-        self.codes_t, self.scales_t = pair(p.shapes_t, transposed)
+        def pair(shapes):
+            return [torch.empty(s, dtype=torch.uint8, device=device) for s in shapes]
+        self.codes, self.scales = pair(p.shapes) if direct else (None, None)
+        self.codes_t, self.scales_t = pair(p.shapes_t) if transposed else (None, None)
 
     def load(self, x, stream=None):
         """Quantises x (a tensor of the problem's values, any shape)."""
@@ -52,7 +52,9 @@ class Pointwise:
     ``training``, each 128 pixels of a channel for the weight's gradient; else,
     where one launch is faster, on its way into the product),
     ``backward`` the gradient of y (``grad_format``, in ``grad_dtype``) likewise.
-    Products are exact and summed in float32 (``dc_fp8_matmul``).
+    Products are exact and summed in float32 (``dc_fp8_matmul``).  Codes that are
+    kept have at most 2^24 rows: channels last that many pixels of all images,
+    channels first of one; a forward in one launch takes 2^30 of all.
 
     The layer keeps the codes of its weight and of the last forward's input,
     and workspaces: its calls belong on one stream, or on streams that wait for
@@ -77,7 +79,8 @@ class Pointwise:
         # the latter 10.0, 13.0.  Not where rows of y are no whole 16-byte pieces (9 x 22 x 4, 144 -> 71: 13.7, 7.1),
         # and channels first not for many output channels (8 x 56 x 56, 256 -> 256: 16.4, 11.3).
         self._one = None
-        if not training and dtype == B.DC_BF16 and c_in <= B.FP8_RUN and \
+        takes = n >= 0 and h * w > 0 and n * h * w <= 1 << 30 and c_in <= B.FP8_RUN  # (dc_fp8_pointwise)
+        if not training and dtype == B.DC_BF16 and takes and \
                 (c_out <= 256 and c_out % 8 == 0 if last else c_out <= 128):
             self._one = B.DcFp8Layer(n, h * w, c_in, c_out, layout)
         kept = self._one is None
@@ -87,7 +90,7 @@ class Pointwise:
         # products over channels: pixels are the rows of D (channels last) or its columns
         self._fwd = q(batch, pixels, c_out, c_in, b_shared=1, out=dtype) if last else \
             q(batch, c_out, pixels, c_in, a_shared=1, out=dtype)
-        products = [self._fwd]
+        products = [self._fwd] if kept else []
         if training:
             self.gy = Quantized(maps(c_out, grad_dtype, g), True, True, device)
             self._gx = q(batch, pixels, c_in, c_out, g, e, b_shared=1, out=dtype) if last else \
@@ -97,7 +100,7 @@ class Pointwise:
             alone = B.dc_fp8_matmul_workspace_size(self._gx) == 0
             self._gw = q(batch, c_out, c_in, pixels, g, e, sum=1, out=B.DC_F32, beside=int(alone))
             products += [self._gx, self._gw]
-        need = max(B.dc_fp8_matmul_workspace_size(p) for p in products)
+        need = max((B.dc_fp8_matmul_workspace_size(p) for p in products), default=0)
         self._ws = torch.empty(max(need, 1), dtype=torch.uint8, device=device)
         # addresses of what the layer keeps, in the order that the calls take them
         self._lib = B.lib()

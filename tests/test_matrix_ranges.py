@@ -1,7 +1,56 @@
 """Pointwise layers at the ends of their ranges: sizes that a layer takes, and
 which of its two forward passes it takes them with."""
+import pytest
+import torch
+
 from deformable_convolution_gb300 import binding as B
 from deformable_convolution_gb300 import fp8
+
+
+def on_gpu(f):
+    f = pytest.mark.gpu(f)
+    return pytest.mark.skipif(not torch.cuda.is_available(), reason="needs a CUDA GPU")(f)
+
+
+MANY = (17, 8, 8, 1024, 1024)  # 17.8 million pixels: more than the 2^24 rows of a matrix of codes
+
+
+@pytest.mark.parametrize("layout", (B.DC_NCHW, B.DC_NHWC))
+def test_a_layer_that_keeps_no_codes_takes_more_pixels_than_codes_have_rows(layout):
+    layer = fp8.Pointwise(*MANY, B.DC_BF16, layout, training=False, device="cpu")
+    assert layer.x.codes is None and layer.x.codes_t is None and layer._ws.numel() <= 1
+
+
+def test_more_pixels_than_codes_have_rows_are_refused_where_codes_are_kept():
+    with pytest.raises(B.DcError):
+        fp8.Pointwise(*MANY, B.DC_BF16, B.DC_NHWC, training=True, device="cpu")
+    with pytest.raises(B.DcError):
+        fp8.Pointwise(*MANY, B.DC_F32, B.DC_NHWC, training=False, device="cpu")
+    # channels first every image has codes of its own
+    fp8.Pointwise(2, 8, 8, 64, 64, B.DC_BF16, B.DC_NCHW, training=True, device="cpu")
+
+
+@pytest.mark.parametrize("training", (True, False))
+@pytest.mark.parametrize("layout", (B.DC_NCHW, B.DC_NHWC))
+@pytest.mark.parametrize("size", [(-1, 8, 8, 4, 4), (1, 0, 8, 4, 4), (1, 8, 0, 4, 4), (1, 8, 8, 0, 4), (1, 8, 8, 4, -1)])
+def test_sizes_that_are_none_are_refused_where_the_layer_is_made(size, layout, training):
+    with pytest.raises(B.DcError):
+        fp8.Pointwise(*size, B.DC_BF16, layout, training, device="cpu")
+
+
+@on_gpu
+@pytest.mark.parametrize("layout", (B.DC_NCHW, B.DC_NHWC))
+def test_more_pixels_than_codes_have_rows(layout):
+    """The last image as a layer of its own gives it."""
+    n = MANY[0]
+    gen = torch.Generator(device="cuda").manual_seed(0)
+    layer, one = (fp8.Pointwise(k, *MANY[1:], B.DC_BF16, layout, training=False) for k in (n, 1))
+    w = torch.empty(8, 8, dtype=torch.bfloat16, device="cuda").normal_(generator=gen)
+    layer.load(w), one.load(w)
+    x = torch.empty(layer.x_shape, dtype=torch.bfloat16, device="cuda").normal_(generator=gen)
+    y = layer.forward(x)
+    for i in (0, n // 2, n - 1):
+        assert torch.equal(y[i:i + 1], one.forward(x[i:i + 1])) and y[i].any()
 
 
 def test_reductions_of_more_than_a_run():

@@ -77,10 +77,14 @@ class Pointwise:
         # Without a backward pass the input's codes need not be kept, and one launch is faster (in us, one against
         # two): channels last 16 x 100 x 168, 256 -> 256: 57, 75; 4 x 112 x 112, 128 -> 64: 7.8, 10.1; channels first
         # the latter 10.0, 13.0.  Not where rows of y are no whole 16-byte pieces (9 x 22 x 4, 144 -> 71: 13.7, 7.1),
-        # and channels first not for many output channels (8 x 56 x 56, 256 -> 256: 16.4, 11.3).
+        # and channels first not for many output channels (8 x 56 x 56, 256 -> 256: 16.4, 11.3).  A tile of 128 pixels
+        # runs through all of c_in by itself: deep inputs take two launches unless there are tiles for more than one
+        # and a half rounds of the 152 SMs (channels last, -> 128: 8 x 14 x 14, 512: 8.9, 6.8, 2048: 26.8, 10.2;
+        # 8 x 56 x 56, 1024: 25.4, 20.7; 2 x 100 x 168, 1024: 26.5, 30.7; 8 x 14 x 14, 256: 5.8, 6.3).
         self._one = None
+        few = batch * -(-pixels // 128) <= 228
         takes = n >= 0 and h * w > 0 and n * h * w <= 1 << 30 and c_in <= B.FP8_RUN  # (dc_fp8_pointwise)
-        if not training and dtype == B.DC_BF16 and takes and \
+        if not training and dtype == B.DC_BF16 and takes and not (few and c_in > 256) and \
                 (c_out <= 256 and c_out % 8 == 0 if last else c_out <= 128):
             self._one = B.DcFp8Layer(n, h * w, c_in, c_out, layout)
         kept = self._one is None

@@ -30,6 +30,35 @@ def test_more_pixels_than_codes_have_rows_are_refused_where_codes_are_kept():
     fp8.Pointwise(2, 8, 8, 64, 64, B.DC_BF16, B.DC_NCHW, training=True, device="cpu")
 
 
+@pytest.mark.parametrize("layout", (B.DC_NCHW, B.DC_NHWC))
+def test_deep_inputs_of_small_maps_take_two_launches(layout):
+    """One launch gives a tile of 128 pixels its whole reduction: 8 x 14 x 14 pixels
+    of 2048 channels took 27 to 46 us so, 10 to 15 us in two."""
+    def one(n, c_in, h, w):
+        return fp8.Pointwise(n, c_in, 64, h, w, B.DC_BF16, layout, training=False, device="cpu")._one is not None
+    assert not one(8, 2048, 14, 14) and not one(1, 1024, 7, 7) and not one(8, 512, 28, 28)
+    assert one(8, 256, 14, 14) and one(1, 64, 7, 7) and one(16, 256, 100, 168) and one(16, 1024, 100, 168)
+
+
+@on_gpu
+@pytest.mark.parametrize("layout", (B.DC_NCHW, B.DC_NHWC))
+@pytest.mark.parametrize("size", [(3, 520, 64, 14, 14), (1, 1030, 128, 7, 7), (2, 264, 8, 120, 130)])
+def test_either_way_gives_the_same(size, layout):
+    n, c_in, c_out, h, w = size
+    gen = torch.Generator(device="cuda").manual_seed(0)
+    layer = fp8.Pointwise(*size, B.DC_BF16, layout, training=False)
+    wt, x = (torch.empty(s, dtype=torch.bfloat16, device="cuda").normal_(generator=gen)
+             for s in ((c_out, c_in), layer.x_shape))
+    layer.load(wt)
+    y = torch.empty(layer.y_shape, dtype=torch.bfloat16, device="cuda")
+    p = B.DcFp8Layer(n, h * w, c_in, c_out, layout)
+    assert B.lib().dc_fp8_pointwise(p, x.data_ptr(), layer.weight.codes.data_ptr(), layer.weight.scales.data_ptr(),
+                                    y.data_ptr(), torch.cuda.current_stream().cuda_stream) == B.DC_OK
+    kept = fp8.Pointwise(*size, B.DC_BF16, layout, training=True)
+    kept.load(wt)
+    assert torch.equal(layer.forward(x), y) and torch.equal(kept.forward(x), y) and y.any()
+
+
 @pytest.mark.parametrize("training", (True, False))
 @pytest.mark.parametrize("layout", (B.DC_NCHW, B.DC_NHWC))
 @pytest.mark.parametrize("size", [(-1, 8, 8, 4, 4), (1, 0, 8, 4, 4), (1, 8, 0, 4, 4), (1, 8, 8, 0, 4), (1, 8, 8, 4, -1)])

@@ -88,10 +88,10 @@ class Trainer:
                     e["master"] = q[k].float()
                 (matrices if optimizer == "muon" and k in weights else entries).append(e)
         self.opt = optim.AdamW(entries, lr=lr, betas=betas, state_bits=state_bits, min_8bit=4096)
-        self.muon, self._norm = None, self.opt.grad_norm
-        if matrices:  # one norm over both optimisers' gradients
-            self.muon = optim.Muon(matrices, lr=lr)
-            self._norm = optim.GradNorm([e["grad"] for e in entries + matrices])
+        self.muon = optim.Muon(matrices, lr=lr) if matrices else None
+        if matrices:
+            self._tables = self.opt.params, self.muon.params
+            self._both = optim.GradNorm(self._both_grads())
         self.grad_norm, self.clip = empty(1), empty(1)
 
     def forward(self, x0):
@@ -121,6 +121,19 @@ class Trainer:
                               g["w_off"], g["b_off"], g["w"], None, self.ws[l], after_fwd=True)
             grad = self.gx
         return self.gx
+
+    def _norm(self, max_norm, norm, scale):
+        """One norm over both optimisers' gradients, those that their next steps take."""
+        if self.muon is None:
+            return self.opt.grad_norm(max_norm, norm, scale)
+        tables = self.opt.params, self.muon.params  # (new ones after a set_grads)
+        if any(a is not b for a, b in zip(self._tables, tables)):
+            self._tables = tables
+            self._both.set_grads(self._both_grads())
+        return self._both(max_norm, norm, scale)
+
+    def _both_grads(self):
+        return [q["grad"] for table in self._tables for q in table]
 
     def update(self):
         """The clipped step; the norm stays in ``self.grad_norm``.  A norm that is

@@ -200,10 +200,12 @@ class Orthogonalize:
     """Writes the matrices ``ins`` (float32 or bfloat16 CUDA tensors, the first
     dimension by all others) orthogonalised into ``outs`` (either type; a tensor
     may be both) by ``steps`` Newton-Schulz steps.  precision: 16, where X's
-    products take its high 16 bits only (errors below a bfloat16's rounding), or 32.
+    products take its high 16 bits only (errors below a bfloat16's rounding, also
+    for float32 results), or 32.
 
-    Addresses are taken here.  The object keeps one workspace: its calls belong
-    on one stream, or on streams that wait for one another."""
+    Addresses are taken here.  The object keeps one workspace, about 8 to 16
+    bytes a value of up to 40 matrices: its calls belong on one stream, or on streams that
+    wait for one another."""
 
     def __init__(self, ins, outs, steps=5, precision=16):
         self.ins, self.outs = tuple(ins), tuple(outs)
@@ -236,7 +238,8 @@ class Muon:
     and param, grad, master, weight_decay as there.  precision: of the
     orthogonalisation (see ``Orthogonalize``).  Biases, norms' parameters and
     other vectors belong to AdamW.  As there, ``params`` is read-only and
-    ``set_grads`` hands over gradients at other addresses."""
+    ``set_grads`` hands over gradients at other addresses.  The workspace is
+    ``Orthogonalize``'s (40 weights of 2048 x 2048: 2.7 GB, as long as the object)."""
 
     def __init__(self, params, lr=1e-3, momentum=0.95, nesterov=True, weight_decay=0.01, steps=5,
                  rms=0.2, precision=16):

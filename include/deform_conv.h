@@ -595,7 +595,8 @@ typedef struct {
  * an unknown enum, steps outside 1 .. 20; DC_ERR_UNSUPPORTED for a shorter
  * side over 16384, a longer one over 2^22, or a pointer without its element's
  * alignment; DC_ERR_WORKSPACE for a workspace that is short or not 256-byte
- * aligned.  The workspace's size depends on the matrices' sizes alone. */
+ * aligned.  The workspace's size depends on the matrices' sizes alone: up to 40
+ * of them go through it at once, which takes about 8 to 16 bytes a value of each. */
 dc_status dc_orthogonalize_workspace_size(const dc_matrix* mats, int count, size_t* bytes);
 dc_status dc_orthogonalize(const dc_matrix* mats, int count, int steps,
                            dc_ortho_precision precision, void* ws, size_t ws_bytes, void* stream);

@@ -79,7 +79,7 @@ __device__ __forceinline__ void tma_store(const CUtensorMap* map, uint32_t src, 
       "r"(c0), "r"(c1), "r"(c2)
       : "memory");
 }
-// As that, float32 values added to what stands there (numbers below 2^-126 count as zero).
+// As that, float32 values added to what stands there (2^-127 and less are kept).
 __device__ __forceinline__ void tma_add(const CUtensorMap* map, uint32_t src, int c0, int c1, int c2) {
   asm volatile(
       "cp.reduce.async.bulk.tensor.3d.global.shared::cta.add.tile.bulk_group [%0, {%2, %3, %4}], [%1];" ::"l"(map),
